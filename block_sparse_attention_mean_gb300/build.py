@@ -15,8 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbsa.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "mask_kernels.cu", "fwd_tc.cu", "fwd_simt.cu", "noalloc.cu", "residual.cu",
-           "exact_select.cu", "fwd_tokens.cu", "query_groups.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "walk.cuh", "sync.cuh"]
+           "exact_select.cu", "fwd_tokens.cu", "query_groups.cu", "block_api.cu", "rotary.cu", "gated_norm.cu"]
+HEADERS = ["internal.h", "ptx.cuh", "walk.cuh", "sync.cuh", "block_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -36,7 +36,7 @@ def _stale(target, deps):
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     header_deps = [os.path.join(CSRC, h) for h in HEADERS] + [
-        os.path.join(HERE, "..", "include", "bsa.h")]
+        os.path.join(HERE, "..", "include", h) for h in ("bsa.h", "bsa_block.h")]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)
