@@ -1,5 +1,6 @@
 """GB300 block-sparse attention forward: mean-pooled top-k / static block masks
-and a tcgen05 block-sparse FlashAttention kernel behind a C ABI (libbsa.so).
+and a tcgen05 block-sparse FlashAttention kernel behind a C ABI (libbsa.so), and
+the operators around the attention (multi-axis rotary positions, gated norm).
 
 The compute path is the CUDA library only; this package marshals arguments.
 The binding (and with it torch) is imported on first use of one of its names, so
@@ -10,11 +11,18 @@ _BINDING_NAMES = (
     "bsa_debug_config", "bsa_forward", "bsa_mask_nnz", "bsa_status_string", "bsa_validate_index",
     "bsa_workspace_size", "build_mask", "cuboid_spec", "explicit_spec", "forward", "load", "workspace")
 
-__all__ = list(_BINDING_NAMES)
+_BLOCK_NAMES = (
+    "GatedNormGrads", "NormSpec", "RotaryPlan", "gated_norm", "gated_norm_backward", "gated_norm_workspace",
+    "grid_positions", "rotary", "rotary_backward", "rotary_plan", "rotary_workspace")
+
+__all__ = list(_BINDING_NAMES + _BLOCK_NAMES)
 
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
         return getattr(binding, name)
+    if name in _BLOCK_NAMES:
+        from . import block_binding
+        return getattr(block_binding, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,542 @@
+"""ctypes binding of the operators around the attention (include/bsa_block.h): one Python function
+per entry point with the same name (argument marshalling only), plus helpers that take tensors,
+check that they go together and allocate outputs and workspaces with torch.
+
+As in ``binding`` there is no fallback: if libbsa.so cannot be loaded every call raises. The helpers
+run on the tensors' device and on ``stream`` (that device's current stream by default).
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
+
+import torch
+
+from . import binding
+from .binding import BF16, ERR_DTYPE, ERR_INVALID_ARG, ERR_SHAPE, FP32, BsaError, _check, _ptr, _stream
+
+ROTARY_MAX_AXES = 4
+ROTARY_INTERLEAVED = 0
+ROTARY_HALVES = 1
+NORM_NONE = 0
+NORM_RMS = 1
+NORM_LAYER = 2
+
+# every symbol declared in include/bsa_block.h
+EXPORTS = ("bsa_rotary_plan_init", "bsa_rotary", "bsa_rotary_backward", "bsa_rotary_workspace_size",
+           "bsa_gated_norm", "bsa_gated_norm_backward", "bsa_gated_norm_workspace_size")
+
+
+class RotarySpec(ctypes.Structure):
+    """Mirror of bsa_rotary_spec."""
+    _fields_ = [("n_axes", ctypes.c_int), ("axis_dim", ctypes.c_int * ROTARY_MAX_AXES),
+                ("theta", ctypes.c_double * ROTARY_MAX_AXES), ("scale", ctypes.c_double * ROTARY_MAX_AXES),
+                ("pairing", ctypes.c_int), ("inv_freq", ctypes.c_void_p)]
+
+
+class RotaryPlan(ctypes.Structure):
+    """Mirror of bsa_rotary_plan."""
+    _fields_ = [("magic", ctypes.c_uint32), ("d", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("pairing", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64),
+                ("axis", ctypes.c_uint8 * 64)]
+
+
+_I64 = ctypes.c_int64
+
+
+class Heads(ctypes.Structure):
+    """Mirror of bsa_heads."""
+    _fields_ = [("src", ctypes.c_void_p), ("src_batch", _I64), ("src_token", _I64), ("src_head", _I64),
+                ("dst", ctypes.c_void_p), ("dst_batch", _I64), ("dst_token", _I64), ("dst_head", _I64),
+                ("weight", ctypes.c_void_p), ("heads", ctypes.c_int)]
+
+
+class HeadsGrad(ctypes.Structure):
+    """Mirror of bsa_heads_grad."""
+    _fields_ = [("dy", ctypes.c_void_p), ("dy_batch", _I64), ("dy_token", _I64), ("dy_head", _I64),
+                ("x", ctypes.c_void_p), ("x_batch", _I64), ("x_token", _I64), ("x_head", _I64),
+                ("dx", ctypes.c_void_p), ("dx_batch", _I64), ("dx_token", _I64), ("dx_head", _I64),
+                ("weight", ctypes.c_void_p), ("dweight", ctypes.c_void_p), ("heads", ctypes.c_int)]
+
+
+class Norm(ctypes.Structure):
+    """Mirror of bsa_norm."""
+    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
+class Rows(ctypes.Structure):
+    """Mirror of bsa_rows."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch", _I64), ("token", _I64)]
+
+
+class Modulation(ctypes.Structure):
+    """Mirror of bsa_modulation."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch", _I64), ("frame", _I64)]
+
+
+class GatedNormDesc(ctypes.Structure):
+    """Mirror of bsa_gated_norm_desc."""
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("C", ctypes.c_int), ("F", ctypes.c_int),
+                ("stream_dt", ctypes.c_int), ("branch_dt", ctypes.c_int), ("mod_dt", ctypes.c_int),
+                ("alpha", ctypes.c_float), ("post", Norm), ("pre", Norm), ("gate", Modulation),
+                ("scale", Modulation), ("shift", Modulation)]
+
+
+class GatedNormGradArgs(ctypes.Structure):
+    """Mirror of bsa_gated_norm_grads."""
+    _fields_ = [("dh", Rows), ("dz", Rows), ("h", Rows), ("y", Rows), ("dx", Rows), ("dy", Rows),
+                ("dgate", ctypes.c_void_p), ("dscale", ctypes.c_void_p), ("dshift", ctypes.c_void_p),
+                ("dpost_weight", ctypes.c_void_p), ("dpost_bias", ctypes.c_void_p),
+                ("dpre_weight", ctypes.c_void_p), ("dpre_bias", ctypes.c_void_p)]
+
+
+_lib = None
+
+
+def load():
+    """Load libbsa.so (raises OSError if it was not built) with this header's signatures."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    lib = binding.load()
+    P, I, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    lib.bsa_rotary_plan_init.argtypes = [P, I, P]
+    lib.bsa_rotary.argtypes = [P, P, P, P, I, I, I, P, _I64, I, F, P]
+    lib.bsa_rotary_backward.argtypes = [P, P, P, P, I, I, I, P, _I64, I, F, P, SZ, P]
+    lib.bsa_rotary_workspace_size.argtypes = [I, I, I, ctypes.POINTER(SZ)]
+    lib.bsa_gated_norm.argtypes = [P, P, P, P, P, P]
+    lib.bsa_gated_norm_backward.argtypes = [P, P, P, SZ, P]
+    lib.bsa_gated_norm_workspace_size.argtypes = [I, I, I, ctypes.POINTER(SZ)]
+    for name in EXPORTS:
+        getattr(lib, name).restype = I
+    _lib = lib
+    return lib
+
+
+def _ref(s):
+    return ctypes.byref(s) if s is not None else None
+
+
+# ------------------------------------------------------------------ C ABI mirror
+
+
+def bsa_rotary_plan_init(spec: Optional[RotarySpec], d: int, plan: Optional[RotaryPlan]) -> None:
+    _check(load().bsa_rotary_plan_init(_ref(spec), int(d), _ref(plan)), "bsa_rotary_plan_init")
+
+
+def bsa_rotary(plan: Optional[RotaryPlan], q: Optional[Heads], k: Optional[Heads], v: Optional[Heads], dt: int, B: int,
+               N: int, positions, pos_batch: int, norm: int, eps: float, stream=None) -> None:
+    _check(load().bsa_rotary(_ref(plan), _ref(q), _ref(k), _ref(v), dt, B, N, _ptr(positions), pos_batch, norm, eps,
+                             _stream(stream)), "bsa_rotary")
+
+
+def bsa_rotary_backward(plan: Optional[RotaryPlan], q: Optional[HeadsGrad], k: Optional[HeadsGrad],
+                        v: Optional[HeadsGrad], dt: int, B: int, N: int, positions, pos_batch: int, norm: int,
+                        eps: float, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(load().bsa_rotary_backward(_ref(plan), _ref(q), _ref(k), _ref(v), dt, B, N, _ptr(positions), pos_batch,
+                                      norm, eps, _ptr(workspace), workspace_bytes, _stream(stream)),
+           "bsa_rotary_backward")
+
+
+def bsa_rotary_workspace_size(B: int, N: int, d: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().bsa_rotary_workspace_size(B, N, d, ctypes.byref(out)), "bsa_rotary_workspace_size")
+    return out.value
+
+
+def bsa_gated_norm(desc: Optional[GatedNormDesc], x: Optional[Rows], y: Optional[Rows], h: Optional[Rows],
+                   z: Optional[Rows], stream=None) -> None:
+    _check(load().bsa_gated_norm(_ref(desc), _ref(x), _ref(y), _ref(h), _ref(z), _stream(stream)), "bsa_gated_norm")
+
+
+def bsa_gated_norm_backward(desc: Optional[GatedNormDesc], grads: Optional[GatedNormGradArgs], workspace,
+                            workspace_bytes: int, stream=None) -> None:
+    _check(load().bsa_gated_norm_backward(_ref(desc), _ref(grads), _ptr(workspace), workspace_bytes,
+                                          _stream(stream)), "bsa_gated_norm_backward")
+
+
+def bsa_gated_norm_workspace_size(B: int, N: int, C: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().bsa_gated_norm_workspace_size(B, N, C, ctypes.byref(out)), "bsa_gated_norm_workspace_size")
+    return out.value
+
+
+# ------------------------------------------------------------------ helpers
+
+_CODES = {torch.bfloat16: BF16, torch.float32: FP32}
+
+
+def _code(t: torch.Tensor, what: str) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise BsaError(ERR_DTYPE, f"{what}: tensor dtype {t.dtype}")
+    return code
+
+
+def _expect(t: torch.Tensor, shape, dtype: torch.dtype, device, what: str) -> None:
+    """Shape, dtype, device and contiguous channels of a tensor that a kernel will index by them."""
+    if t.shape != shape:
+        raise BsaError(ERR_SHAPE, f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise BsaError(ERR_DTYPE, f"{what}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise BsaError(ERR_INVALID_ARG, f"{what}: on {t.device}, expected {device}")
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise BsaError(ERR_INVALID_ARG, f"{what}: channels must be contiguous")
+
+
+def _cuda_device(t: torch.Tensor, what: str) -> torch.device:
+    if not t.is_cuda:
+        raise BsaError(ERR_INVALID_ARG, f"{what}: not a CUDA tensor")
+    return t.device
+
+
+def _on(device: torch.device, fn, *args, stream=None) -> None:
+    """fn(*args, stream) with `device` current: the library launches on the current device."""
+    if device.index == torch.cuda.current_device():
+        fn(*args, stream)
+        return
+    with torch.cuda.device(device):
+        fn(*args, stream)
+
+
+def _workspace_bytes(ws: Optional[torch.Tensor], device: torch.device, what: str) -> int:
+    if ws is None:
+        return 0
+    if ws.device != device or not ws.is_contiguous():
+        raise BsaError(ERR_INVALID_ARG, f"{what}: the workspace must be contiguous and on {device}")
+    return ws.numel() * ws.element_size()
+
+
+def rotary_plan(d: int, axis_dims: Sequence[int], theta: Union[float, Sequence[float]] = 10000.0,
+                scale: Union[float, Sequence[float]] = 1.0, interleaved: bool = True,
+                inv_freq: Optional[Sequence[float]] = None) -> RotaryPlan:
+    """Frequencies of a head of d channels whose axes take `axis_dims` channels each, one after another
+    (bsa_rotary_plan_init). `theta` and `scale` per axis or for all; `inv_freq` (radians per position of
+    every pair) in their place. interleaved: channels (2p, 2p + 1) are a pair; else (p, p + rot / 2)."""
+    dims = [int(x) for x in axis_dims]
+    if not 1 <= len(dims) <= ROTARY_MAX_AXES:
+        raise BsaError(ERR_INVALID_ARG, f"rotary_plan: {len(dims)} axes")
+
+    def each(v, what):
+        v = [float(v)] * len(dims) if isinstance(v, (int, float)) else [float(x) for x in v]
+        if len(v) != len(dims):
+            raise BsaError(ERR_INVALID_ARG, f"rotary_plan: {len(v)} values of {what} for {len(dims)} axes")
+        return v
+
+    spec = RotarySpec()
+    spec.n_axes = len(dims)
+    for a, (dim, th, sc) in enumerate(zip(dims, each(theta, "theta"), each(scale, "scale"))):
+        spec.axis_dim[a], spec.theta[a], spec.scale[a] = dim, th, sc
+    spec.pairing = ROTARY_INTERLEAVED if interleaved else ROTARY_HALVES
+    keep = None
+    if inv_freq is not None:
+        freq = [float(x) for x in inv_freq]
+        if len(freq) != sum(dims) // 2:
+            raise BsaError(ERR_INVALID_ARG, f"rotary_plan: {len(freq)} frequencies for {sum(dims) // 2} pairs")
+        keep = (ctypes.c_double * len(freq))(*freq)
+        spec.inv_freq = ctypes.cast(keep, ctypes.c_void_p)
+    plan = RotaryPlan()
+    bsa_rotary_plan_init(spec, d, plan)
+    return plan
+
+
+def grid_positions(grid: Sequence[int], n_text: int = 0, cuboid: Optional[Sequence[int]] = None,
+                   device="cuda") -> torch.Tensor:
+    """int32 [n_text + prod(grid), len(grid)]: `n_text` tokens at the origin, then the grid's coordinates in
+    raster order (last axis fastest). With `cuboid` (its extent per axis, dividing the grid's) in the token
+    order of cuboid_spec: cuboid after cuboid in raster order, each cuboid's tokens in raster order."""
+    grid = [int(g) for g in grid]
+    c = torch.stack(torch.meshgrid(*[torch.arange(g, dtype=torch.int32, device=device) for g in grid],
+                                   indexing="ij"), dim=-1)
+    if cuboid is not None:
+        cub = [int(x) for x in cuboid]
+        if len(cub) != len(grid) or any(x < 1 or g % x for g, x in zip(grid, cub)):
+            raise BsaError(ERR_SHAPE, f"grid_positions: cuboid {tuple(cub)} does not divide the grid {tuple(grid)}")
+        n = len(grid)
+        c = c.reshape(*[v for g, x in zip(grid, cub) for v in (g // x, x)], n)
+        c = c.permute(*range(0, 2 * n, 2), *range(1, 2 * n, 2), 2 * n)
+    c = c.reshape(-1, len(grid))
+    return torch.cat((torch.zeros((n_text, len(grid)), dtype=torch.int32, device=device), c)).contiguous()
+
+
+def _rotary_args(plan, tensors, names, positions, weights, layout, what):
+    """Common checks of rotary and rotary_backward: (device, dtype code, B, N, heads of each, pos_batch).
+    layout: "nh" for [B, N, heads, d] tensors, "hn" for [B, heads, N, d]."""
+    first = next((t for t in tensors if t is not None), None)
+    if first is None:
+        raise BsaError(ERR_INVALID_ARG, f"{what}: none of q, k, v")
+    device = _cuda_device(first, what)
+    if first.dim() != 4:
+        raise BsaError(ERR_SHAPE, f"{what}: {first.dim()} dimensions, expected 4")
+    B, N = first.shape[0], first.shape[1 if layout == "nh" else 2]
+    h_at = 2 if layout == "nh" else 1
+    heads = []
+    for t, name in zip(tensors, names):
+        if t is None:
+            heads.append(0)
+            continue
+        h = t.shape[h_at] if t.dim() == 4 else 0
+        _expect(t, (B, N, h, plan.d) if layout == "nh" else (B, h, N, plan.d), first.dtype, device, f"{what}: {name}")
+        heads.append(h)
+    pos_batch = 0
+    if tensors[0] is not None or tensors[1] is not None:
+        if positions is None:
+            raise BsaError(ERR_INVALID_ARG, f"{what}: no positions")
+        shape = (N, plan.n_axes) if positions.dim() == 2 else (B, N, plan.n_axes)
+        _expect(positions, shape, torch.int32, device, f"{what}: positions")
+        if N > 1 and positions.stride(-2) != plan.n_axes:
+            raise BsaError(ERR_INVALID_ARG, f"{what}: a token's positions must follow the last token's")
+        pos_batch = positions.stride(0) if positions.dim() == 3 else 0
+    for w, name in zip(weights, ("q_weight", "k_weight")):
+        if w is not None:
+            _expect(w, (plan.d,), torch.float32, device, f"{what}: {name}")
+    return device, _code(first, what), B, N, heads, pos_batch
+
+
+def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None,
+           v: Optional[torch.Tensor] = None, *, positions: Optional[torch.Tensor] = None,
+           norm_eps: Optional[float] = None, q_weight: Optional[torch.Tensor] = None,
+           k_weight: Optional[torch.Tensor] = None,
+           out: Optional[Tuple[Optional[torch.Tensor], ...]] = None, stream=None):
+    """Run bsa_rotary: q, k, v [B, N, heads, d] (views of a fused projection do) to [B, heads, N, d], Q and K
+    normalised per head (norm_eps not None; fp32 weights [d] optional) and turned by `positions`
+    (int32 [N, axes] or [B, N, axes]). `out`: the three results' tensors, any strides with contiguous
+    channels. Returns (q, k, v), None where none was given."""
+    device, dt, B, N, heads, pos_batch = _rotary_args(plan, (q, k, v), "qkv", positions, (q_weight, k_weight), "nh",
+                                                      "rotary")
+    if out is None:
+        out = (None, None, None)
+    res, desc = [], []
+    for t, o, w, h in zip((q, k, v), out, (q_weight, k_weight, None), heads):
+        if t is None:
+            res.append(None)
+            desc.append(None)
+            continue
+        if o is None:
+            o = torch.empty((B, h, N, plan.d), dtype=t.dtype, device=device)
+        else:
+            _expect(o, (B, h, N, plan.d), t.dtype, device, "rotary: out")
+        s0, s1, s2, _ = t.stride()
+        o0, o1, o2, _ = o.stride()
+        desc.append(Heads(t.data_ptr(), s0, s1, s2, o.data_ptr(), o0, o2, o1, w.data_ptr() if w is not None else None, h))
+        res.append(o)
+    norm = norm_eps is not None
+    _on(device, bsa_rotary, plan, *desc, dt, B, N, positions, pos_batch, int(norm), norm_eps if norm else 0.0,
+        stream=stream)
+    return tuple(res)
+
+
+def rotary_workspace(B: int, N: int, d: int, device="cuda") -> torch.Tensor:
+    """Device workspace of rotary_backward."""
+    return torch.empty(bsa_rotary_workspace_size(B, N, d), dtype=torch.uint8, device=device)
+
+
+def rotary_backward(plan: RotaryPlan, dq: Optional[torch.Tensor], dk: Optional[torch.Tensor] = None,
+                    dv: Optional[torch.Tensor] = None, *, positions: Optional[torch.Tensor] = None,
+                    q: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
+                    norm_eps: Optional[float] = None, q_weight: Optional[torch.Tensor] = None,
+                    k_weight: Optional[torch.Tensor] = None,
+                    out: Optional[Tuple[Optional[torch.Tensor], ...]] = None, ws: Optional[torch.Tensor] = None,
+                    stream=None):
+    """Run bsa_rotary_backward: the gradients dq, dk, dv [B, heads, N, d] that arrive at rotary's results, to
+    the gradients [B, N, heads, d] of its inputs. With norm_eps, q and k are rotary's inputs. Returns
+    (gq, gk, gv, gq_weight, gk_weight); a weight's gradient (fp32 [d]) where that weight is given."""
+    device, dt, B, N, heads, pos_batch = _rotary_args(plan, (dq, dk, dv), ("dq", "dk", "dv"), positions,
+                                                      (q_weight, k_weight), "hn", "rotary_backward")
+    norm = norm_eps is not None
+    if out is None:
+        out = (None, None, None)
+    res, desc, dweights = [], [], [None, None, None]
+    if norm and (q_weight is not None or k_weight is not None):
+        both = torch.empty((2, plan.d), dtype=torch.float32, device=device)
+        dweights = [both[0] if dq is not None and q_weight is not None else None,
+                    both[1] if dk is not None and k_weight is not None else None, None]
+    for t, x, o, w, dw, h in zip((dq, dk, dv), (q, k, None), out, (q_weight, k_weight, None), dweights, heads):
+        if t is None:
+            res.append(None)
+            desc.append(None)
+            continue
+        if o is None:
+            o = torch.empty((B, N, h, plan.d), dtype=t.dtype, device=device)
+        else:
+            _expect(o, (B, N, h, plan.d), t.dtype, device, "rotary_backward: out")
+        x_args = (None, 0, 0, 0)
+        if norm and len(res) < 2:
+            if x is None:
+                raise BsaError(ERR_INVALID_ARG, "rotary_backward: the norm needs q and k")
+            _expect(x, (B, N, h, plan.d), t.dtype, device, "rotary_backward: q, k")
+            x_args = (x.data_ptr(), *x.stride()[:3])
+        s0, s1, s2, _ = t.stride()
+        desc.append(HeadsGrad(t.data_ptr(), s0, s2, s1, *x_args, o.data_ptr(), *o.stride()[:3],
+                              w.data_ptr() if w is not None else None, dw.data_ptr() if dw is not None else None, h))
+        res.append(o)
+    if ws is None and (dweights[0] is not None or dweights[1] is not None):
+        ws = rotary_workspace(B, N, plan.d, device)
+    _on(device, bsa_rotary_backward, plan, *desc, dt, B, N, positions, pos_batch, int(norm), norm_eps if norm else 0.0,
+        ws, _workspace_bytes(ws, device, "rotary_backward"), stream=stream)
+    return (*res, dweights[0], dweights[1])
+
+
+_KINDS = {"rms": NORM_RMS, "layer": NORM_LAYER}
+
+
+class NormSpec:
+    """A norm over the channels: kind "rms" or "layer", fp32 weight and bias [C] (None: ones, zeros), eps."""
+
+    def __init__(self, kind: str, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6):
+        if kind not in _KINDS:
+            raise BsaError(ERR_INVALID_ARG, f"NormSpec: kind {kind!r}")
+        self.kind, self.weight, self.bias, self.eps = kind, weight, bias, float(eps)
+
+
+class GatedNormGrads(NamedTuple):
+    """What gated_norm_backward returns; None for what the forward did not have."""
+    dx: Optional[torch.Tensor]
+    dy: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dscale: Optional[torch.Tensor]
+    dshift: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dpost_bias: Optional[torch.Tensor]
+    dpre_weight: Optional[torch.Tensor]
+    dpre_bias: Optional[torch.Tensor]
+
+
+def _rows(t: Optional[torch.Tensor]) -> Rows:
+    return Rows(None, 0, 0) if t is None else Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _gated_desc(shape, device, stream_t, branch_t, alpha, post, pre, gate, scale, shift, what) -> GatedNormDesc:
+    B, N, C = shape
+    F, mod = 1, None
+    mods = []
+    for m, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+        if m is None:
+            mods.append(Modulation(None, 0, 0))
+            continue
+        if mod is None:
+            F, mod = (m.shape[1] if m.dim() == 3 else 1), m.dtype
+        _expect(m, (B, F, C) if m.dim() == 3 else (B, C), mod, device, f"{what}: {name}")
+        if m.dim() == 2 and F != 1:
+            raise BsaError(ERR_SHAPE, f"{what}: {name}: {tuple(m.shape)} beside {F} frames")
+        mods.append(Modulation(m.data_ptr(), m.stride(0), m.stride(1) if m.dim() == 3 else 0))
+    if mod is not None and mod not in _CODES:
+        raise BsaError(ERR_DTYPE, f"{what}: modulation dtype {mod}")
+    norms = []
+    for n, name in ((post, "post"), (pre, "pre")):
+        if n is None:
+            norms.append(Norm(NORM_NONE, 0.0, None, None))
+            continue
+        for w in (n.weight, n.bias):
+            if w is not None:
+                _expect(w, (C,), torch.float32, device, f"{what}: {name} weight or bias")
+        norms.append(Norm(_KINDS[n.kind], n.eps, _ptr(n.weight), _ptr(n.bias)))
+    return GatedNormDesc(B, N, C, F, _code(stream_t, what), _code(branch_t, what), _CODES[mod] if mod else BF16, alpha,
+                         norms[0], norms[1], mods[0], mods[1], mods[2])
+
+
+def gated_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, gate: Optional[torch.Tensor] = None,
+               alpha: float = 1.0, post: Optional[NormSpec] = None, pre: Optional[NormSpec] = None,
+               scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None,
+               out: Optional[Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]] = None,
+               branch_dtype: Optional[torch.dtype] = None, stream=None):
+    """Run bsa_gated_norm: h = x + alpha * gate * post(y), z = pre(h) * (1 + scale) + shift, for x, y [B, N, C] and
+    modulations [B, C] or [B, F, C] (F frames of N / F tokens). Without y, h is x and is not written; without
+    pre there is no z, whose dtype is y's (without y: that of out's z, branch_dtype or x's). Returns (h, z)."""
+    device = _cuda_device(x, "gated_norm")
+    if x.dim() != 3:
+        raise BsaError(ERR_SHAPE, f"gated_norm: x has {x.dim()} dimensions, expected 3")
+    shape = x.shape
+    _expect(x, shape, x.dtype, device, "gated_norm: x")
+    h, z = out if out is not None else (None, None)
+    branch = y if y is not None else z
+    dtype = branch.dtype if branch is not None else branch_dtype or x.dtype
+    if y is not None:
+        _expect(y, shape, dtype, device, "gated_norm: y")
+        if h is None:
+            h = torch.empty(shape, dtype=x.dtype, device=device)
+        else:
+            _expect(h, shape, x.dtype, device, "gated_norm: out h")
+    if pre is not None:
+        if z is None:
+            z = torch.empty(shape, dtype=dtype, device=device)
+        else:
+            _expect(z, shape, dtype, device, "gated_norm: out z")
+    desc = _gated_desc(shape, device, x, z if z is not None else y if y is not None else x, alpha, post, pre, gate,
+                       scale, shift, "gated_norm")
+    _on(device, bsa_gated_norm, desc, _rows(x), _rows(y), _rows(h), _rows(z), stream=stream)
+    return h, z
+
+
+def gated_norm_workspace(B: int, N: int, C: int, device="cuda") -> torch.Tensor:
+    """Device workspace of gated_norm_backward."""
+    return torch.empty(bsa_gated_norm_workspace_size(B, N, C), dtype=torch.uint8, device=device)
+
+
+def gated_norm_backward(dh: Optional[torch.Tensor], dz: Optional[torch.Tensor], h: Optional[torch.Tensor],
+                        y: Optional[torch.Tensor] = None, *, gate: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                        post: Optional[NormSpec] = None, pre: Optional[NormSpec] = None,
+                        scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None,
+                        out: Optional[Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]] = None,
+                        ws: Optional[torch.Tensor] = None, stream=None) -> GatedNormGrads:
+    """Run bsa_gated_norm_backward. dh [B, N, C] is the gradient that arrives at h from where h goes on (None:
+    zero), dz the one at z (with pre only), h gated_norm's h (its x without y) and y its y. Without pre, dx is dh
+    itself and nothing is written for it. `out`: (dx, dy). Gradients of the modulations have their dtype and
+    shape, those of weights and biases are fp32 [C]."""
+    what = "gated_norm_backward"
+    first = dh if dh is not None else dz
+    if first is None:
+        raise BsaError(ERR_INVALID_ARG, f"{what}: neither dh nor dz")
+    device = _cuda_device(first, what)
+    if first.dim() != 3:
+        raise BsaError(ERR_SHAPE, f"{what}: {first.dim()} dimensions, expected 3")
+    shape = first.shape
+    B, N, C = shape
+    stream_t = dh if dh is not None else h
+    branch_t = dz if dz is not None else y if y is not None else dh
+    if stream_t is None:
+        raise BsaError(ERR_INVALID_ARG, f"{what}: no h")
+    for t, like, name in ((dh, stream_t, "dh"), (h if pre is not None else None, stream_t, "h"), (dz, branch_t, "dz"),
+                          (y, branch_t, "y")):
+        if t is not None:
+            _expect(t, shape, like.dtype, device, f"{what}: {name}")
+    dx, dy = out if out is not None else (None, None)
+    g = GatedNormGradArgs()
+    g.dh, g.dz, g.y = _rows(dh), _rows(dz), _rows(y)
+    if pre is not None:
+        g.h = _rows(h)
+        if dx is None:
+            dx = torch.empty(shape, dtype=stream_t.dtype, device=device)
+        else:
+            _expect(dx, shape, stream_t.dtype, device, f"{what}: out dx")
+        g.dx = _rows(dx)
+    else:
+        dx = dh
+    if y is not None:
+        if dy is None:
+            dy = torch.empty(shape, dtype=y.dtype, device=device)
+        else:
+            _expect(dy, shape, y.dtype, device, f"{what}: out dy")
+        g.dy = _rows(dy)
+    else:
+        dy = None
+    desc = _gated_desc(shape, device, stream_t, branch_t, alpha, post, pre, gate, scale, shift, what)
+    dmods = [None, None, None]
+    if gate is not None or scale is not None or shift is not None:
+        some = next(m for m in (gate, scale, shift) if m is not None)
+        rows = torch.empty((3, B, desc.F, C), dtype=some.dtype, device=device)
+        dmods = [None if m is None else r.view(m.shape) for m, r in zip((gate, scale, shift), rows.unbind(0))]
+        g.dgate, g.dscale, g.dshift = (_ptr(m) for m in dmods)
+    params = [p for n in (post, pre) for p in ((n.weight, n.bias) if n is not None else (None, None))]
+    dparams = [None, None, None, None]
+    if any(p is not None for p in params):
+        rows = torch.empty((4, C), dtype=torch.float32, device=device).unbind(0)
+        dparams = [None if p is None else r for p, r in zip(params, rows)]
+        g.dpost_weight, g.dpost_bias, g.dpre_weight, g.dpre_bias = (_ptr(p) for p in dparams)
+    if ws is None and (any(m is not None for m in dmods) or any(p is not None for p in dparams)):
+        ws = gated_norm_workspace(B, N, C, device)
+    _on(device, bsa_gated_norm_backward, desc, g, ws, _workspace_bytes(ws, device, what), stream=stream)
+    return GatedNormGrads(dx, dy, *dmods, *dparams)
