@@ -1,0 +1,126 @@
+"""The attention step of a block as a model runs it: fused projection -> rotary -> mask -> sparse forward ->
+gated norm, and the operators' backward passes around it, each stage against its own reference."""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_mean_gb300 as pkg
+import oracle
+from block_sparse_attention_mean_gb300 import binding as bb
+from block_sparse_attention_mean_gb300 import block_binding as ob
+from block_sparse_attention_mean_gb300 import build as bbuild
+from tests import block_ref as ref
+from tests import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    bbuild.build()
+    oracle.build()
+    ob.load()
+
+
+@pytest.mark.parametrize("static,d,grid,n_text", [(True, 64, (8, 8, 8), 128), (False, 128, (4, 8, 9), 40)])
+def test_attention_step(static, d, grid, n_text):
+    B, H = 2, 4
+    N, C = n_text + grid[0] * grid[1] * grid[2], H * d
+    g = torch.Generator(DEV).manual_seed(1)
+
+    def draw(*shape, dt=torch.bfloat16, scale=1.0, mean=0.0):
+        return (torch.randn(*shape, generator=g, device=DEV) * scale + mean).to(dt)
+
+    qkv, x = draw(B, N, 3 * H, d), draw(B, N, C)
+    src = qkv.split(H, dim=2)
+    weights = [draw(d, dt=torch.float32, scale=0.2, mean=1.0) for _ in range(2)]
+    axes = (16, 24, 24) if d == 64 else (44, 42, 42)
+    plan = pkg.rotary_plan(d, axes)
+    pos = pkg.grid_positions(grid, n_text, cuboid=(4, 4, 4) if static else None)
+    spec = bb.cuboid_spec(n_text // 64, tuple(s // 4 for s in grid)) if static else None
+    post, pre = pkg.NormSpec("rms", draw(C, dt=torch.float32, mean=1.0)), pkg.NormSpec("layer")
+    rows = draw(B, 3, C, scale=0.3)
+    mods = dict(gate=rows[:, 0], scale=rows[:, 1], shift=rows[:, 2])
+    proj = draw(C, C, scale=C ** -0.5)
+
+    # the step, without a wait between its calls
+    q, k, v = pkg.rotary(plan, *src, positions=pos, norm_eps=1e-6, q_weight=weights[0], k_weight=weights[1])
+    idx = bb.build_mask(None if static else q, None if static else k, 64, density=0.25, spec=spec, shape=(B, H, N, d),
+                        check=False)
+    o, lse = bb.forward(q, k, v, idx, check=False)
+    y = o.transpose(1, 2).reshape(B, N, C) @ proj
+    h, z = pkg.gated_norm(x, y, post=post, pre=pre, **mods)
+    torch.cuda.synchronize()
+
+    ang = ref.angles(pos, axes, 10000.0)
+    for got, t, w, name in ((q, src[0], weights[0], "q"), (k, src[1], weights[1], "k")):
+        ref.within(got, *ref.rotary(t, ang, True, 1e-6, w), name)
+    assert torch.equal(v, src[2].transpose(1, 2))
+
+    host = [t.float().cpu().numpy() for t in (q, k, v)]
+    nB = -(-N // 64)
+    if static:
+        mask = np.broadcast_to(oracle.cuboid_mask(n_text // 64, tuple(s // 4 for s in grid)), (B, H, nB, nB)).copy()
+    else:
+        mask = oracle.select_mask(host[0], host[1], 64, 0.25)
+    gu.assert_index_equal(idx, mask)
+    o_ref, l_ref = oracle.attention(*host, mask, 64)
+    err = np.abs(o.float().cpu().numpy().reshape(-1, d) - o_ref)
+    assert err.max() <= gu.O_MAX_ABS and err.mean() <= gu.O_MEAN_ABS
+    assert np.abs(lse.cpu().numpy().reshape(-1) - l_ref).max() <= gu.LSE_MAX_ABS
+
+    kw = dict(mods, post=("rms", post.weight, None, 1e-6), pre=("layer", None, None, 1e-6))
+    (rh, dh), (rz, dz) = ref.gated_norm(x, y, **kw)
+    ref.within(h, rh, dh, "h")
+    ref.within(z, rz, dz, "z")
+
+    # the way back through the two operators, the arriving gradients in the layouts the attention has
+    gh, gz = draw(B, N, C), draw(B, N, C)
+    back = pkg.gated_norm_backward(gh, gz, h, y, post=post, pre=pre, **mods)
+    want = ref.gated_norm_backward(gh, gz, h, y, **kw)
+    for name in ("dx", "dy", "dpost_weight"):
+        ref.within(getattr(back, name), *want[name], name)
+    dqkv = torch.empty_like(qkv)
+    do = [draw(B, H, N, d) for _ in range(3)]
+    dw = pkg.rotary_backward(plan, *do, positions=pos, q=src[0], k=src[1], norm_eps=1e-6, q_weight=weights[0],
+                             k_weight=weights[1], out=dqkv.split(H, dim=2))[3:]
+    for i, w in enumerate(weights):
+        dx, bound, rdw, dw_bound = ref.rotary_backward(do[i], ang, True, src[i], 1e-6, w)
+        ref.within(dqkv[:, :, i * H:(i + 1) * H], dx, bound, f"d{'qk'[i]}")
+        ref.within(dw[i], rdw, dw_bound, "weight")
+    assert torch.equal(dqkv[:, :, 2 * H:], do[2].transpose(1, 2))
+
+
+def test_two_steps_on_two_streams():
+    """the operators on two streams at once, each with its own buffers, as two halves of a batch would run"""
+    g = torch.Generator(DEV).manual_seed(2)
+    B, N, H, d = 1, 2000, 8, 128
+    plan = pkg.rotary_plan(d, (44, 42, 42))
+    pos = pkg.grid_positions((8, 10, 25))
+    w = torch.ones(d, device=DEV)
+    post = pkg.NormSpec("rms", torch.ones(H * d, device=DEV))
+    pre = pkg.NormSpec("layer")
+    inputs = [[torch.randn(*s, generator=g, device=DEV).bfloat16() for s in ((B, N, 3 * H, d), (B, N, H * d), (B, N, H * d))]
+              for _ in range(2)]
+
+    def half(qkv, x, y):
+        out = pkg.rotary(plan, *qkv.split(H, dim=2), positions=pos, norm_eps=1e-6, q_weight=w, k_weight=w)
+        back = pkg.rotary_backward(plan, *out, positions=pos, q=qkv[:, :, :H], k=qkv[:, :, H:2 * H], norm_eps=1e-6,
+                                   q_weight=w, k_weight=w)
+        h, z = pkg.gated_norm(x, y, post=post, pre=pre)
+        return (*out, *back, h, z, *(t for t in pkg.gated_norm_backward(h, z, h, y, post=post, pre=pre) if t is not None))
+
+    alone = [half(*i) for i in inputs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s, i in zip(streams, inputs):
+            with torch.cuda.stream(s):
+                got.append(half(*i))
+        torch.cuda.synchronize()
+        for a, b in zip(got, alone):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
