@@ -1,0 +1,473 @@
+// gated_norm.cuh -- what the forward (gated_norm.cu) and backward (gated_norm_backward.cu) kernels of the gated norm
+// share: pairs of fp32, a thread's part of a row, the sums over a row, and how the rows are dealt out.
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "block_internal.h"
+#include "ptx.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kMaxWarps = 16;  // CTAs of up to 512 threads
+
+// Rows in flight per worker: three, fewer where a CTA of 512 threads would not find room for them (rows of more
+// than 4096 channels). `bytes`: what a thread copies per row; `kept`: what it holds in shared memory besides.
+__host__ __device__ constexpr int stages_for(int bytes, int kept = 0)
+{
+    const int fit = (221184 - 512 * kept) / (512 * bytes);
+    return fit > 3 ? 3 : fit < 1 ? 1 : fit;
+}
+
+__host__ __device__ constexpr int pow2_ceil(int v)
+{
+    int p = 1;
+    while (p < v) p *= 2;
+    return p;
+}
+
+// Threads that hold a row of `groups` groups of 8 channels, v of them per thread
+__host__ __device__ inline int row_threads(int groups, int v)
+{
+    return groups <= 32 ? pow2_ceil(groups) : (groups + 32 * v - 1) / (32 * v) * 32;
+}
+
+// ------------------------------------------------------------ pairs of fp32
+// Two channels per instruction: fp32 add, multiply and fused multiply-add on register pairs.
+using f2 = unsigned long long;
+
+__device__ __forceinline__ f2 pair(float a, float b)
+{
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 twice(float a) { return pair(a, a); }
+__device__ __forceinline__ void split(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ float two(f2 v)
+{
+    float a, b;
+    split(v, a, b);
+    return a + b;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
+{
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// ------------------------------------------------------------ E channels of a row: a thread's unit
+// E / 2 pairs from and to memory. Stores to bf16 round to nearest even: half a step per element.
+__device__ __forceinline__ f2 widen(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t narrow(f2 v)
+{
+    float a, b;
+    split(v, a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <typename T, int P>  // P pairs
+struct Unit;
+
+template <>
+struct Unit<__nv_bfloat16, 4> {
+    static __device__ __forceinline__ void get(const void *p, f2 (&v)[4])
+    {
+        const uint4 r = *static_cast<const uint4 *>(p);
+        v[0] = widen(r.x), v[1] = widen(r.y), v[2] = widen(r.z), v[3] = widen(r.w);
+    }
+    static __device__ __forceinline__ void put(void *p, const f2 (&v)[4])
+    {
+        *static_cast<uint4 *>(p) = make_uint4(narrow(v[0]), narrow(v[1]), narrow(v[2]), narrow(v[3]));
+    }
+};
+
+template <>
+struct Unit<__nv_bfloat16, 2> {
+    static __device__ __forceinline__ void get(const void *p, f2 (&v)[2])
+    {
+        const uint2 r = *static_cast<const uint2 *>(p);
+        v[0] = widen(r.x), v[1] = widen(r.y);
+    }
+    static __device__ __forceinline__ void put(void *p, const f2 (&v)[2])
+    {
+        *static_cast<uint2 *>(p) = make_uint2(narrow(v[0]), narrow(v[1]));
+    }
+};
+
+template <int P>
+struct Unit<float, P> {
+    static __device__ __forceinline__ void get(const void *p, f2 (&v)[P])
+    {
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            const float4 r = static_cast<const float4 *>(p)[i / 2];
+            v[i] = pair(r.x, r.y), v[i + 1] = pair(r.z, r.w);
+        }
+    }
+    static __device__ __forceinline__ void put(void *p, const f2 (&v)[P])
+    {
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            float4 r;
+            split(v[i], r.x, r.y);
+            split(v[i + 1], r.z, r.w);
+            static_cast<float4 *>(p)[i / 2] = r;
+        }
+    }
+};
+
+// channels of a modulation or of a weight (fp32)
+template <int P>
+__device__ __forceinline__ void load_mod(const void *p, int dt, int64_t at, f2 (&v)[P])
+{
+    if (dt == BSA_BF16)
+        Unit<__nv_bfloat16, P>::get(static_cast<const char *>(p) + at * 2, v);
+    else
+        Unit<float, P>::get(static_cast<const char *>(p) + at * 4, v);
+}
+
+template <int P>
+__device__ __forceinline__ void store_mod(char *p, int dt, int64_t at, const f2 (&v)[P])
+{
+    if (dt == BSA_BF16)
+        Unit<__nv_bfloat16, P>::put(p + at * 2, v);
+    else
+        Unit<float, P>::put(p + at * 4, v);
+}
+
+// v *= m, v *= 1 + m, v += m, for a modulation's (or weight's) channels
+template <int P>
+__device__ __forceinline__ void times(const void *p, int dt, int64_t at, f2 (&v)[P])
+{
+    f2 m[P];
+    load_mod(p, dt, at, m);
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = mul2(v[i], m[i]);
+}
+template <int P>
+__device__ __forceinline__ void times_one_plus(const void *p, int dt, int64_t at, f2 (&v)[P])
+{
+    f2 m[P];
+    load_mod(p, dt, at, m);
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = mul2(v[i], add2(twice(1.0f), m[i]));
+}
+template <int P>
+__device__ __forceinline__ void plus(const void *p, int dt, int64_t at, f2 (&v)[P])
+{
+    f2 m[P];
+    load_mod(p, dt, at, m);
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = add2(v[i], m[i]);
+}
+template <int P>
+__device__ __forceinline__ void fill(float x, f2 (&v)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = twice(x);
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// ------------------------------------------------------------ rows and workers
+
+// The rows, B * N in order, cut into `workers` ranges that differ by at most one row.
+struct Ranges {
+    int rows, workers, most;  // most: the longest range
+    int per_group;            // rows that share a modulation
+
+    __host__ __device__ int first(int64_t w) const { return static_cast<int>(w * rows / workers); }
+    __host__ __device__ int worker_of(int64_t row) const
+    {
+        return static_cast<int>(((row + 1) * workers - 1) / rows);
+    }
+};
+
+// A thread's place in a [B][N][C] tensor, walked one row at a time
+struct Walk {
+    char *p;
+
+    __device__ __forceinline__ Walk(const RowsView &v, int b, int n, int size) : p(v.p + (b * v.b + n * v.n) * size) {}
+    __device__ __forceinline__ void next(const RowsView &v, int size) { p += v.n * size; }
+    // after the last token's next(): to the next batch's first
+    __device__ __forceinline__ void wrap(const RowsView &v, int N, int size) { p += (v.b - N * v.n) * size; }
+};
+
+// What a thread knows of its row: its channels, and the CTA's exchange of the warps' sums. SUB: the row is held
+// by `lanes` < 32 lanes of a warp; else by whole warps.
+template <int K, int P, bool SUB>
+struct Row {
+    static constexpr int E = 2 * P;
+    int C, lanes, warps, turn;
+    float inv_c, inv_held;  // 1 / channels of the row, of this warp's part of it
+    bool on[K];
+    int c[K];
+    float *buf;   // [2][4][kMaxWarps]
+    float *held;  // channels that each warp holds
+
+    __device__ __forceinline__ Row(int C_, int tpr, float *buf_)
+    {
+        C = C_;
+        lanes = SUB ? tpr : 32;
+        warps = SUB ? 1 : tpr / 32;
+        buf = buf_;
+        held = buf + 8 * kMaxWarps;
+        turn = 0;
+        inv_c = inv_held = 1.0f / static_cast<float>(C);
+        const int t = threadIdx.x % tpr;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int at = E * (t + k * tpr);
+            on[k] = at < C;
+            c[k] = on[k] ? at : 0;
+        }
+        if (warps > 1) {
+            for (int i = threadIdx.x; i < 9 * kMaxWarps; i += blockDim.x) {
+                float n = 0.0f;  // the sums of warps that are not there stay zero, and they hold nothing
+                const int w = i - 8 * kMaxWarps;
+                if (w >= 0 && w < warps)
+                    for (int k = 0; k < K; ++k) n += E * min(32, max(0, C / E - k * tpr - 32 * w));
+                buf[i] = n;
+            }
+            __syncthreads();
+            inv_held = 1.0f / held[threadIdx.x / 32];
+        }
+    }
+
+    template <int M>
+    __device__ __forceinline__ void lanes_sum(float (&v)[M]) const
+    {
+        if (SUB) {
+            for (int o = lanes / 2; o > 0; o >>= 1) {
+#pragma unroll
+                for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+            }
+        } else {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+                for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+            }
+        }
+    }
+
+    // Puts each warp's M values where every thread can read them: one barrier. Two buffers in turn, so that a
+    // warp that is ahead does not overwrite what others still read.
+    template <int M>
+    __device__ __forceinline__ const float *exchange(const float (&v)[M])
+    {
+        float *b = buf + turn * 4 * kMaxWarps;
+        turn ^= 1;
+        if (threadIdx.x % 32 == 0) {
+#pragma unroll
+            for (int m = 0; m < M; ++m) b[m * kMaxWarps + threadIdx.x / 32] = v[m];
+        }
+        __syncthreads();
+        return b;
+    }
+
+    __device__ __forceinline__ float total(const float *b) const
+    {
+        float s = 0.0f;
+#pragma unroll 1
+        for (int w = 0; w < warps; w += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(b + w);
+            s += (q.x + q.y) + (q.z + q.w);
+        }
+        return s;
+    }
+
+    // sums over the row, the same in every thread
+    template <int M>
+    __device__ __forceinline__ void sums(float (&v)[M])
+    {
+        lanes_sum(v);
+        if (warps == 1) return;
+        const float *b = exchange(v);
+#pragma unroll
+        for (int m = 0; m < M; ++m) v[m] = total(b + m * kMaxWarps);
+    }
+
+    // -mean where a unit is on, 0 where it is off: adding it leaves units that are off at zero
+    __device__ __forceinline__ f2 minus(float mean, int k) const { return twice(on[k] ? -mean : 0.0f); }
+
+    // Mean (0 but for LAYER) and mean square about it of M rows at once, one exchange. The spread is taken about
+    // each warp's own mean and joined exactly: sum_w (spread_w + n_w (mean_w - mean)^2), no cancellation for rows
+    // far from zero. Units that are off hold zeros.
+    template <int M>
+    __device__ __forceinline__ void stats(const f2 (&v)[M][K][P], const int (&kind)[M], float (&mean)[M], float (&square)[M])
+    {
+        bool layer = false;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            layer = layer || kind[m] == BSA_NORM_LAYER;
+            mean[m] = 0.0f;
+        }
+        if (layer) {
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                f2 q = v[m][0][0];
+#pragma unroll
+                for (int i = 1; i < K * P; ++i) q = add2(q, v[m][i / P][i % P]);
+                mean[m] = two(q);
+            }
+            lanes_sum(mean);
+#pragma unroll
+            for (int m = 0; m < M; ++m) mean[m] = kind[m] == BSA_NORM_LAYER ? mean[m] * inv_held : 0.0f;
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            f2 q = 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const f2 off = minus(mean[m], k);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const f2 x = add2(v[m][k][i], off);
+                    q = fma2(x, x, q);
+                }
+            }
+            square[m] = two(q);
+        }
+        lanes_sum(square);
+        if (warps > 1) {
+            float s[2 * M];
+#pragma unroll
+            for (int m = 0; m < M; ++m) s[m] = square[m], s[M + m] = mean[m];
+            const float *b = exchange(s);
+#pragma unroll
+            for (int m = 0; m < M; ++m) square[m] = total(b + m * kMaxWarps);
+            if (layer) {
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const float4 *means = reinterpret_cast<const float4 *>(b + (M + m) * kMaxWarps);
+                    const float4 *n = reinterpret_cast<const float4 *>(held);
+                    float all = 0.0f;
+#pragma unroll 1
+                    for (int w = 0; w < warps; w += 4) {
+                        const float4 a = means[w / 4], h = n[w / 4];
+                        all += (a.x * h.x + a.y * h.y) + (a.z * h.z + a.w * h.w);
+                    }
+                    mean[m] = all * inv_c;
+#pragma unroll 1
+                    for (int w = 0; w < warps; w += 4) {
+                        float4 a = means[w / 4];
+                        const float4 h = n[w / 4];
+                        a.x -= mean[m], a.y -= mean[m], a.z -= mean[m], a.w -= mean[m];
+                        square[m] += (a.x * a.x * h.x + a.y * a.y * h.y) + (a.z * a.z * h.z + a.w * a.w * h.w);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) square[m] *= inv_c;
+    }
+};
+
+constexpr int kExchangeFloats = 9 * kMaxWarps;
+
+// ------------------------------------------------------------ host
+
+// Vectors of 8 channels per thread, V: two from 512 channels on. What a row costs a thread apart from its channels
+// (the sums over the row, addresses, the loop) is about as much as eight channels cost, and half as many warps pay
+// it: at 2048 channels bf16 223 -> 179 us forward (65536 rows), 147 -> 119 us backward (16384 rows).
+inline int vectors(int C) { return C >= 512 ? 2 : 1; }
+
+// What a launch needs to know of a kernel, looked up once: registers, and (once per device) leave to use all of
+// the shared memory.
+template <typename Kernel>
+bsa_status ready(Kernel kern, int smem, std::atomic<uint64_t> &done, std::atomic<int> &regs)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return BSA_OK;
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, kern) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+            cudaSuccess)
+        return BSA_ERR_CUDA;
+    regs.store(at.numRegs, std::memory_order_relaxed);
+    done.fetch_or(bit, std::memory_order_release);
+    return BSA_OK;
+}
+
+struct Shape {
+    int tpr, threads, ctas;
+    size_t smem;
+    Ranges rg;
+};
+
+// Workers: as many as fit on the device at once, each with an equal share of the rows; at most one per row.
+inline Shape shape_of(const bsa_gated_norm_desc &d, int v, int regs, int sms, int stages, int thread_bytes,
+                      int kept_bytes = 0)
+{
+    Shape s;
+    s.tpr = row_threads(d.C / 8, v);
+    s.threads = s.tpr <= 32 ? 128 : s.tpr;
+    s.smem = static_cast<size_t>(s.threads) * (stages * thread_bytes + kept_bytes);
+    const int by_regs = 65536 / ((regs + 7) / 8 * 8 * s.threads);
+    const int by_smem = static_cast<int>((228 * 1024) / (s.smem + 4096));
+    int resident = by_regs < by_smem ? by_regs : by_smem;
+    if (resident > 2048 / s.threads) resident = 2048 / s.threads;
+    if (resident < 1) resident = 1;
+    const int per_cta = s.threads / s.tpr;
+    s.rg.rows = d.B * d.N;
+    s.rg.per_group = d.N / d.F;
+    const int64_t fill = static_cast<int64_t>(sms) * resident * per_cta, most = gated_norm_max_workers(s.rg.rows, d.C);
+    s.rg.workers = static_cast<int>(fill < most ? fill : most);
+    s.rg.most = (s.rg.rows + s.rg.workers - 1) / s.rg.workers;
+    s.ctas = (s.rg.workers + per_cta - 1) / per_cta;
+    return s;
+}
+
+// run(stream dtype, branch dtype, V, registers per thread, whether lanes of one warp hold several rows, whether there
+// is a post norm) for the kernel that a desc needs
+template <typename F>
+bsa_status by_kernel(const bsa_gated_norm_desc &d, F &&run)
+{
+    auto by_width = [&](auto ts, auto tb, auto post) {
+        const auto no = std::false_type();
+        const std::integral_constant<int, 1> one;
+        const std::integral_constant<int, 2> two;
+        // up to 256 threads per row: three CTAs of 128 threads per SM find 168 registers each; beyond, 512 threads
+        if (d.C > 4096) return run(ts, tb, two, std::integral_constant<int, 128>(), no, post);
+        if (vectors(d.C) == 2) return run(ts, tb, two, std::integral_constant<int, 168>(), no, post);
+        const std::integral_constant<int, 128> regs;
+        return row_threads(d.C / 8, 1) < 32 ? run(ts, tb, one, regs, std::true_type(), post) : run(ts, tb, one, regs, no, post);
+    };
+    auto by_post = [&](auto ts, auto tb) {
+        return d.post.kind != BSA_NORM_NONE ? by_width(ts, tb, std::true_type()) : by_width(ts, tb, std::false_type());
+    };
+    if (d.stream_dt == BSA_BF16) return by_post(__nv_bfloat16(), __nv_bfloat16());
+    if (d.branch_dt == BSA_BF16) return by_post(float(), __nv_bfloat16());
+    return by_post(float(), float());
+}
+
+}  // namespace
+}  // namespace bsa

@@ -1,0 +1,481 @@
+// gated_norm_backward.cu -- the backward pass of the gated norm (gated_norm.cu), in one pass over the rows.
+// A worker keeps four sums per channel in registers while it walks its rows,
+//   A = sum dz,  S = sum dz n,  P = sum dx,  Q = sum dx m      (m = y without a post norm),
+// from which every parameter's gradient follows by factors that are constant over the rows that share a
+// modulation (a group):
+//   dshift = A,  dscale = w S + b A,  dgate = alpha (w2 Q + b2 P),
+//   dpre_weight = sum_g (1 + scale_g) S_g,  dpre_bias = sum_g (1 + scale_g) A_g,
+//   dpost_weight = alpha sum_g gate_g Q_g,  dpost_bias = alpha sum_g gate_g P_g.
+// At the end of a group the worker writes the group's gradients itself if it held the whole group, else the
+// four sums into one of its two slots (groups that its range's ends cut); the weights' sums go on in its
+// third. A second kernel adds the slots in the order of the workers, so that results do not depend on timing.
+#include "gated_norm.cuh"
+
+namespace bsa {
+namespace {
+
+struct Wants {
+    bool pre_sums, post_sums, weights;
+};
+
+__device__ __forceinline__ Wants wants_of(const NormArgs &a)
+{
+    Wants w;
+    w.pre_sums = a.dscale || a.dshift || a.dpre_w || a.dpre_b;
+    w.post_sums = a.dgate || a.dpost_w || a.dpost_b;
+    w.weights = a.dpre_w || a.dpre_b || a.dpost_w || a.dpost_b;
+    return w;
+}
+
+// o = one * w + zero * b for a norm's weight and bias at channels c ..
+template <int P>
+__device__ __forceinline__ void join(const bsa_norm &n, int c, const f2 (&one)[P], const f2 (&zero)[P], f2 (&o)[P])
+{
+#pragma unroll
+    for (int i = 0; i < P; ++i) o[i] = one[i];
+    if (n.weight) times(n.weight, BSA_FP32, c, o);
+    if (n.bias) {
+        f2 b[P];
+        load_mod(n.bias, BSA_FP32, c, b);
+#pragma unroll
+        for (int i = 0; i < P; ++i) o[i] = fma2(zero[i], b[i], o[i]);
+    }
+}
+
+// the gradients of a group's modulations from its four sums, at channels c ..
+template <int P>
+__device__ __forceinline__ void write_group(const NormArgs &a, int64_t g, int c, const f2 (&sA)[P], const f2 (&sS)[P],
+                                            const f2 (&sP)[P], const f2 (&sQ)[P])
+{
+    const bsa_gated_norm_desc &d = a.d;
+    const int64_t at = g * d.C + c;
+    f2 o[P];
+    if (a.dshift) store_mod(a.dshift, d.mod_dt, at, sA);
+    if (a.dscale) {
+        join(d.pre, c, sS, sA, o);
+        store_mod(a.dscale, d.mod_dt, at, o);
+    }
+    if (a.dgate) {
+        join(d.post, c, sQ, sP, o);
+#pragma unroll
+        for (int i = 0; i < P; ++i) o[i] = mul2(o[i], twice(d.alpha));
+        store_mod(a.dgate, d.mod_dt, at, o);
+    }
+}
+
+template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST>
+__global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_constant__ NormArgs a, Ranges rg, int tpr)
+{
+    constexpr int E = 16 / sizeof(TS), P = E / 2, K = 8 * V / E, SB = E * sizeof(TS), BB = E * sizeof(TB);
+    constexpr int STAGES = stages_for(16 * V * (sizeof(TS) + sizeof(TB)), 64 * V);
+    __shared__ __align__(16) float buf[kExchangeFloats];
+    extern __shared__ __align__(16) char ring[];  // [stage][h, dh, dz, y: K units of every thread each]
+    const bsa_gated_norm_desc &d = a.d;
+    const bool pre = d.pre.kind != BSA_NORM_NONE, has_y = a.y.p != nullptr,
+               has_dh = a.dh.p != nullptr;
+    const int threads = blockDim.x, C = d.C;
+    // where each tensor's units lie within a stage
+    const int at_dh = pre ? K * threads * SB : 0, at_dz = at_dh + (has_dh ? K * threads * SB : 0),
+              at_y = at_dz + (pre ? K * threads * BB : 0), stage_bytes = at_y + (has_y ? K * threads * BB : 0);
+    Row<K, P, SUB> rw(C, tpr, buf);
+    const Wants want = wants_of(a);
+
+    const int64_t worker = static_cast<int64_t>(blockIdx.x) * (threads / tpr) + threadIdx.x / tpr;
+    const bool some = worker < rg.workers;
+    const int first = some ? rg.first(worker) : 0, count = some ? rg.first(worker + 1) - first : 0;
+    const int b0 = first / d.N, n0 = first % d.N;
+    Walk ph(a.h, b0, n0, sizeof(TS)), pdh(a.dh, b0, n0, sizeof(TS)), pdx(a.dx, b0, n0, sizeof(TS));
+    Walk pdz(a.dz, b0, n0, sizeof(TB)), py(a.y, b0, n0, sizeof(TB)), pdy(a.dy, b0, n0, sizeof(TB));
+    int n_ahead = n0, n_here = n0;
+    const int first_group = first / rg.per_group;
+    int left = rg.per_group - first % rg.per_group, group = first_group;
+    float *const slots = a.partial + worker * gated_norm_worker_floats(C);
+    bool weighed = false;  // the worker's third slot holds sums
+
+    char *const mine_s = ring + threadIdx.x * SB, *const mine_b = ring + threadIdx.x * BB;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {  // units that are off stay zero: they add nothing to a sum
+        if (rw.on[k]) continue;
+        const f2 zero[P] = {};
+        for (int st = 0; st < STAGES; ++st) {
+            const int s_at = st * stage_bytes + k * threads * SB, b_at = st * stage_bytes + k * threads * BB;
+            if (pre) Unit<TS, P>::put(mine_s + s_at, zero), Unit<TB, P>::put(mine_b + at_dz + b_at, zero);
+            if (has_dh) Unit<TS, P>::put(mine_s + at_dh + s_at, zero);
+            if (has_y) Unit<TB, P>::put(mine_b + at_y + b_at, zero);
+        }
+    }
+    int to = 0, from = 0;  // stages
+    auto fetch = [&](bool any) {
+        if (any) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!rw.on[k]) continue;
+                const uint32_t s_at = smem_u32(mine_s + to * stage_bytes + k * threads * SB);
+                const uint32_t b_at = smem_u32(mine_b + to * stage_bytes + k * threads * BB);
+                if (pre) {
+                    copy_async<SB>(s_at, ph.p + rw.c[k] * sizeof(TS));
+                    copy_async<BB>(b_at + at_dz, pdz.p + rw.c[k] * sizeof(TB));
+                }
+                if (has_dh) copy_async<SB>(s_at + at_dh, pdh.p + rw.c[k] * sizeof(TS));
+                if (has_y) copy_async<BB>(b_at + at_y, py.p + rw.c[k] * sizeof(TB));
+            }
+            ph.next(a.h, sizeof(TS));
+            pdh.next(a.dh, sizeof(TS));
+            pdz.next(a.dz, sizeof(TB));
+            py.next(a.y, sizeof(TB));
+            if (++n_ahead == d.N) {
+                n_ahead = 0;
+                ph.wrap(a.h, d.N, sizeof(TS));
+                pdh.wrap(a.dh, d.N, sizeof(TS));
+                pdz.wrap(a.dz, d.N, sizeof(TB));
+                py.wrap(a.y, d.N, sizeof(TB));
+            }
+        }
+        cp_async_commit();
+        if (++to == STAGES) to = 0;
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i < count);
+
+    f2 sA[K][P] = {}, sS[K][P] = {}, sP[K][P] = {}, sQ[K][P] = {};
+    // what dz and dx are multiplied by on their way to n and m: the thread's own 16-byte pieces of shared memory
+    float4 *const kept = reinterpret_cast<float4 *>(ring + STAGES * stage_bytes) + threadIdx.x;
+    auto keep = [&](int which, int k, const f2(&v)[P]) {
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+            f2 two_pairs[2] = {v[j], v[j + 1]};
+            Unit<float, 2>::put(kept + ((which * K + k) * (P / 2) + j / 2) * threads, two_pairs);
+        }
+    };
+    auto kept_times = [&](int which, int k, f2(&v)[P]) {
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+            f2 m[2];
+            Unit<float, 2>::get(kept + ((which * K + k) * (P / 2) + j / 2) * threads, m);
+            v[j] = mul2(v[j], m[0]);
+            v[j + 1] = mul2(v[j + 1], m[1]);
+        }
+    };
+    auto factors = [&](int g) {
+        const int b = g / d.F, f = g % d.F;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = rw.c[k];
+            f2 m[P];
+            fill(1.0f, m);
+            if (d.pre.weight) load_mod(d.pre.weight, BSA_FP32, c, m);
+            if (d.scale.ptr) times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, m);
+            keep(0, k, m);
+            fill(d.alpha, m);
+            if (d.post.weight) times(d.post.weight, BSA_FP32, c, m);
+            if (d.gate.ptr) times(d.gate.ptr, d.mod_dt, b * d.gate.batch + f * d.gate.frame + c, m);
+            keep(1, k, m);
+        }
+    };
+    if (count > 0) factors(group);
+
+    const int rounds = SUB ? rg.most : count;
+    for (int i = 0; i < rounds; ++i) {
+        fetch(i + STAGES - 1 < count);
+        cp_async_wait_group<STAGES - 1>();
+        const bool live = !SUB || i < count;
+        const char *const here_s = mine_s + from * stage_bytes, *const here_b = mine_b + from * stage_bytes;
+        if (++from == STAGES) from = 0;
+        constexpr int M = POST ? 2 : 1;
+        f2 v[K][P];  // h, then n; later y, then m (read from the ring a second time: registers are what is scarce)
+        float mean[M], r[M];
+        if (pre || POST) {
+            f2 both_rows[M][K][P];
+            int kind[M];
+            kind[0] = d.pre.kind;
+            if (POST) kind[M - 1] = d.post.kind;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                fill(0.0f, both_rows[0][k]);
+                if (pre) Unit<TS, P>::get(here_s + k * threads * SB, both_rows[0][k]);
+                if (POST) Unit<TB, P>::get(here_b + at_y + k * threads * BB, both_rows[M - 1][k]);
+            }
+            rw.stats(both_rows, kind, mean, r);
+            r[0] = rsqrtf(r[0] + d.pre.eps);
+            if (POST) r[M - 1] = rsqrtf(r[M - 1] + d.post.eps);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const f2 off = rw.minus(mean[0], k), rr = twice(r[0]);
+#pragma unroll
+                for (int j = 0; j < P; ++j) v[k][j] = mul2(add2(both_rows[0][k][j], off), rr);
+            }
+        }
+        f2 g[K][P];  // the gradient at h, then at u
+        if (pre) {
+            f2 q[K][P], s0 = 0, s1 = 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                Unit<TB, P>::get(here_b + at_dz + k * threads * BB, q[k]);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (live) {
+                        sA[k][j] = add2(sA[k][j], q[k][j]);
+                        sS[k][j] = fma2(q[k][j], v[k][j], sS[k][j]);
+                    }
+                }
+                kept_times(0, k, q[k]);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    s0 = fma2(q[k][j], v[k][j], s0);
+                    s1 = add2(s1, q[k][j]);
+                }
+            }
+            float s[2] = {two(s0), two(s1)};
+            rw.sums(s);
+            const f2 along = twice(-s[0] * rw.inv_c), rr = twice(r[0]);
+            const float m = d.pre.kind == BSA_NORM_LAYER ? s[1] * rw.inv_c : 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const f2 off = rw.minus(m, k);
+                fill(0.0f, g[k]);
+                if (has_dh) Unit<TS, P>::get(here_s + at_dh + k * threads * SB, g[k]);
+#pragma unroll
+                for (int j = 0; j < P; ++j) g[k][j] = fma2(rr, fma2(v[k][j], along, add2(q[k][j], off)), g[k][j]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k) Unit<TS, P>::get(here_s + at_dh + k * threads * SB, g[k]);
+        }
+        if (a.dx.p && live) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (rw.on[k]) Unit<TS, P>::put(pdx.p + rw.c[k] * sizeof(TS), g[k]);
+        }
+        if (has_y) {
+            f2 s0 = 0, s1 = 0;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                Unit<TB, P>::get(here_b + at_y + k * threads * BB, v[k]);
+                if (POST) {
+                    const f2 off = rw.minus(mean[M - 1], k), rr = twice(r[M - 1]);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) v[k][j] = mul2(add2(v[k][j], off), rr);
+                }
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (live) {
+                        sP[k][j] = add2(sP[k][j], g[k][j]);
+                        sQ[k][j] = fma2(g[k][j], v[k][j], sQ[k][j]);
+                    }
+                }
+                kept_times(1, k, g[k]);
+                if (POST) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        s0 = fma2(g[k][j], v[k][j], s0);
+                        s1 = add2(s1, g[k][j]);
+                    }
+                }
+            }
+            if (POST) {
+                float s[2] = {two(s0), two(s1)};
+                rw.sums(s);
+                const f2 along = twice(-s[0] * rw.inv_c), rr = twice(r[M - 1]);
+                const float m = d.post.kind == BSA_NORM_LAYER ? s[1] * rw.inv_c : 0.0f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const f2 off = rw.minus(m, k);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) g[k][j] = mul2(rr, fma2(v[k][j], along, add2(g[k][j], off)));
+                }
+            }
+            if (a.dy.p && live) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (rw.on[k]) Unit<TB, P>::put(pdy.p + rw.c[k] * sizeof(TB), g[k]);
+            }
+        }
+        if (!live) continue;
+        pdx.next(a.dx, sizeof(TS));
+        pdy.next(a.dy, sizeof(TB));
+        if (++n_here == d.N) {
+            n_here = 0;
+            pdx.wrap(a.dx, d.N, sizeof(TS));
+            pdy.wrap(a.dy, d.N, sizeof(TB));
+        }
+        if (--left > 0 && i + 1 < count) continue;
+        // the end of a group, or of the range
+        if (want.pre_sums || want.post_sums) {
+            const int64_t begin = static_cast<int64_t>(group) * rg.per_group;
+            const bool whole = begin >= first && begin + rg.per_group <= static_cast<int64_t>(first) + count;
+            float *const slot = slots + (group == first_group ? 0 : 4 * C);
+            const int b = group / d.F, f = group % d.F;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!rw.on[k]) continue;
+                const int c = rw.c[k];
+                if (whole) {
+                    write_group(a, group, c, sA[k], sS[k], sP[k], sQ[k]);
+                } else {
+                    Unit<float, P>::put(slot + c, sA[k]);
+                    Unit<float, P>::put(slot + C + c, sS[k]);
+                    Unit<float, P>::put(slot + 2 * C + c, sP[k]);
+                    Unit<float, P>::put(slot + 3 * C + c, sQ[k]);
+                }
+                if (want.weights) {  // weighted for the parameters that all groups share, and added up
+                    if (d.scale.ptr) {
+                        times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sA[k]);
+                        times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sS[k]);
+                    }
+                    if (d.gate.ptr) {
+                        times(d.gate.ptr, d.mod_dt, b * d.gate.batch + f * d.gate.frame + c, sP[k]);
+                        times(d.gate.ptr, d.mod_dt, b * d.gate.batch + f * d.gate.frame + c, sQ[k]);
+                    }
+                    float *const sum = slots + 8 * C + c;
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        sP[k][j] = mul2(sP[k][j], twice(d.alpha));
+                        sQ[k][j] = mul2(sQ[k][j], twice(d.alpha));
+                    }
+                    if (weighed) {
+                        plus(sum, BSA_FP32, 0, sA[k]);
+                        plus(sum + C, BSA_FP32, 0, sS[k]);
+                        plus(sum + 2 * C, BSA_FP32, 0, sP[k]);
+                        plus(sum + 3 * C, BSA_FP32, 0, sQ[k]);
+                    }
+                    Unit<float, P>::put(sum, sA[k]);
+                    Unit<float, P>::put(sum + C, sS[k]);
+                    Unit<float, P>::put(sum + 2 * C, sP[k]);
+                    Unit<float, P>::put(sum + 3 * C, sQ[k]);
+                }
+                fill(0.0f, sA[k]);
+                fill(0.0f, sS[k]);
+                fill(0.0f, sP[k]);
+                fill(0.0f, sQ[k]);
+            }
+            weighed = true;
+        }
+        if (i + 1 < count) {
+            left = rg.per_group;
+            factors(++group);
+        }
+    }
+}
+
+// Adds the workers' slots: 64 channels per CTA (four per thread), kSumSlices slices of the workers. blockIdx.y == 0:
+// the weights' sums over all workers; blockIdx.y > 0: one group that several workers share.
+constexpr int kSumSlices = 32;
+
+__global__ void __launch_bounds__(16 * kSumSlices) gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg,
+                                                                          int64_t n_groups)
+{
+    __shared__ __align__(16) float part[kSumSlices / 2][4][64];
+    grid_dependency_wait();
+    const bsa_gated_norm_desc &d = a.d;
+    const int C = d.C;
+    const int64_t stride = gated_norm_worker_floats(C);
+    const Wants want = wants_of(a);
+    int w0 = 0, w1 = rg.workers - 1;
+    int64_t group = -1;
+    if (blockIdx.y == 0) {
+        if (!want.weights) return;
+    } else {
+        // the group itself where there are at most as many groups as workers; else the one that worker y - 1's
+        // range begins inside
+        const int i = blockIdx.y - 1;
+        group = n_groups <= rg.workers ? i : rg.first(i) / rg.per_group;
+        w0 = rg.worker_of(group * rg.per_group);
+        w1 = rg.worker_of((group + 1) * rg.per_group - 1);
+        if (w0 == w1) return;                              // written by its worker
+        if (n_groups > rg.workers && i != w0 + 1) return;  // one CTA per group
+    }
+    const int lane = threadIdx.x % 16, c = blockIdx.x * 64 + 4 * lane;
+    float4 v[4] = {};
+    if (c < C) {
+#pragma unroll 2
+        for (int w = w0 + threadIdx.x / 16; w <= w1; w += kSumSlices) {
+            // a group begins in its first worker's range, in slot 0 if it is the first there; it is the first in the others'
+            const int slot = group < 0 ? 8 : w == w0 && rg.first(w) / rg.per_group != group ? 4 : 0;
+            const float *p = a.partial + w * stride + slot * C + c;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 q = *reinterpret_cast<const float4 *>(p + k * C);
+                v[k].x += q.x, v[k].y += q.y, v[k].z += q.z, v[k].w += q.w;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[k].x += __shfl_xor_sync(0xffffffffu, v[k].x, 16);
+        v[k].y += __shfl_xor_sync(0xffffffffu, v[k].y, 16);
+        v[k].z += __shfl_xor_sync(0xffffffffu, v[k].z, 16);
+        v[k].w += __shfl_xor_sync(0xffffffffu, v[k].w, 16);
+        if (threadIdx.x % 32 < 16) *reinterpret_cast<float4 *>(&part[threadIdx.x / 32][k][4 * lane]) = v[k];
+    }
+    __syncthreads();
+    if (threadIdx.x < 256) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSumSlices / 2; ++i) s += part[i][threadIdx.x / 64][threadIdx.x % 64];
+        part[0][threadIdx.x / 64][threadIdx.x % 64] = s;
+    }
+    __syncthreads();
+    const int at = threadIdx.x, ch = blockIdx.x * 64 + at;
+    if (at >= 64 || ch >= C) return;
+    const float sA = part[0][0][at], sS = part[0][1][at], sP = part[0][2][at], sQ = part[0][3][at];
+    if (group < 0) {
+        if (a.dpre_b) a.dpre_b[ch] = sA;
+        if (a.dpre_w) a.dpre_w[ch] = sS;
+        if (a.dpost_b) a.dpost_b[ch] = sP;
+        if (a.dpost_w) a.dpost_w[ch] = sQ;
+        return;
+    }
+    auto put = [&](char *p, float x) {
+        const int64_t i = group * C + ch;
+        if (d.mod_dt == BSA_BF16)
+            reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
+        else
+            reinterpret_cast<float *>(p)[i] = x;
+    };
+    auto by = [&](const float *w, float one, float x) { return (w ? w[ch] : one) * x; };
+    if (a.dshift) put(a.dshift, sA);
+    if (a.dscale) put(a.dscale, by(d.pre.weight, 1.0f, sS) + by(d.pre.bias, 0.0f, sA));
+    if (a.dgate) put(a.dgate, d.alpha * (by(d.post.weight, 1.0f, sQ) + by(d.post.bias, 0.0f, sP)));
+}
+
+template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST>
+bsa_status backward(const NormArgs &a, int sms, cudaStream_t st)
+{
+    auto kern = gated_norm_backward_kernel<TS, TB, V, REGS, SUB, POST>;
+    static std::atomic<uint64_t> done{0};
+    static std::atomic<int> regs{0};
+    constexpr int BYTES = 16 * V * (sizeof(TS) + sizeof(TB)), STAGES = stages_for(BYTES, 64 * V);
+    const bsa_status ok = ready(kern, 512 * (STAGES * BYTES + 64 * V), done, regs);
+    if (ok != BSA_OK) return ok;
+    const int pre = a.d.pre.kind != BSA_NORM_NONE;
+    const Shape s = shape_of(a.d, V, regs.load(std::memory_order_relaxed), sms, STAGES,
+                             8 * V * static_cast<int>(sizeof(TS) * (pre + (a.dh.p ? 1 : 0)) + sizeof(TB) * (pre + (a.y.p ? 1 : 0))), 64 * V);
+    kern<<<s.ctas, s.threads, s.smem, st>>>(a, s.rg, s.tpr);
+    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+    if (a.partial == nullptr) return BSA_OK;
+    const int64_t n_groups = static_cast<int64_t>(a.d.B) * a.d.F;
+    const int64_t items = n_groups < s.rg.workers ? n_groups : s.rg.workers;
+    const dim3 grid((a.d.C + 63) / 64, static_cast<unsigned>(items + 1));
+    return pdl_launch(gated_norm_sums_kernel, grid, 16 * kSumSlices, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // namespace
+
+int64_t gated_norm_max_workers(int64_t rows, int C)
+{
+    const int64_t w = kNormMaxThreads / row_threads(C / 8, vectors(C));
+    return rows < w ? rows : w;
+}
+
+bsa_status launch_gated_norm_backward(const NormArgs &a, cudaStream_t st)
+{
+    int sms = 0;
+    const bsa_status s = current_sm_count(&sms);
+    if (s != BSA_OK) return s;
+    return by_kernel(a.d, [&](auto ts, auto tb, auto v, auto regs, auto sub, auto post) {
+        return backward<decltype(ts), decltype(tb), decltype(v)::value, decltype(regs)::value,
+                        decltype(sub)::value, decltype(post)::value>(a, sms, st);
+    });
+}
+
+}  // namespace bsa
