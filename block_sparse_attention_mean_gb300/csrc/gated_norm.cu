@@ -33,8 +33,9 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
     const int threads = blockDim.x, at_y = K * threads * XB, stage_bytes = at_y + (branch ? K * threads * YB : 0);
     Row<K, P, SUB> rw(d.C, tpr, buf);
 
-    const int64_t worker = static_cast<int64_t>(blockIdx.x) * (threads / tpr) + threadIdx.x / tpr;
-    const bool some = worker < rg.workers;
+    // a CTA is one worker, unless lanes of a warp hold several rows: all that depends on the row alone is uniform
+    const int worker = SUB ? blockIdx.x * (threads / tpr) + threadIdx.x / tpr : blockIdx.x;
+    const bool some = !SUB || worker < rg.workers;
     const int first = some ? rg.first(worker) : 0, count = some ? rg.first(worker + 1) - first : 0;
     const int b0 = first / d.N, n0 = first % d.N;
     Walk x(a.x, b0, n0, sizeof(TS)), y(a.y, b0, n0, sizeof(TB)), h(a.h, b0, n0, sizeof(TS)), z(a.z, b0, n0, sizeof(TB));
@@ -57,8 +58,8 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (!rw.on[k]) continue;
-                copy_async<XB>(smem_u32(mine_x + to * stage_bytes + k * threads * XB), x.p + rw.c[k] * sizeof(TS));
-                if (branch) copy_async<YB>(smem_u32(mine_y + to * stage_bytes + k * threads * YB), y.p + rw.c[k] * sizeof(TB));
+                copy_async<XB>(smem_u32(mine_x + to * stage_bytes + k * threads * XB), x.p + rw.c[k] * unsigned(sizeof(TS)));
+                if (branch) copy_async<YB>(smem_u32(mine_y + to * stage_bytes + k * threads * YB), y.p + rw.c[k] * unsigned(sizeof(TB)));
             }
             x.next(a.x, sizeof(TS));
             y.next(a.y, sizeof(TB));
@@ -148,7 +149,7 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
             }
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (live && rw.on[k]) Unit<TS, P>::put(h.p + rw.c[k] * sizeof(TS), t[0][k]);
+                if (live && rw.on[k]) Unit<TS, P>::put(h.p + rw.c[k] * unsigned(sizeof(TS)), t[0][k]);
         }
         if (pre) {  // of h before its rounding: the norm sees the exact sum
             float mean[1], square[1];
@@ -160,7 +161,7 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
                 const f2 off = rw.minus(mean[0], k);
 #pragma unroll
                 for (int j = 0; j < P; ++j) t[0][k][j] = fma2(add2(t[0][k][j], off), mul2(r, z1[k][j]), z0[k][j]);
-                if (live && rw.on[k]) Unit<TB, P>::put(z.p + rw.c[k] * sizeof(TB), t[0][k]);
+                if (live && rw.on[k]) Unit<TB, P>::put(z.p + rw.c[k] * unsigned(sizeof(TB)), t[0][k]);
             }
         }
         if (live) {

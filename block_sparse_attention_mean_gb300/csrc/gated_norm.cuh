@@ -199,6 +199,7 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
 struct Ranges {
     int rows, workers, most;  // most: the longest range
     int per_group;            // rows that share a modulation
+    int long_groups;          // no range is longer than a group: it touches two groups at most
 
     __host__ __device__ int first(int64_t w) const { return static_cast<int>(w * rows / workers); }
     __host__ __device__ int worker_of(int64_t row) const
@@ -225,7 +226,7 @@ struct Row {
     int C, lanes, warps, turn;
     float inv_c, inv_held;  // 1 / channels of the row, of this warp's part of it
     bool on[K];
-    int c[K];
+    unsigned c[K];
     float *buf;   // [2][4][kMaxWarps]
     float *held;  // channels that each warp holds
 
@@ -238,12 +239,12 @@ struct Row {
         held = buf + 8 * kMaxWarps;
         turn = 0;
         inv_c = inv_held = 1.0f / static_cast<float>(C);
-        const int t = threadIdx.x % tpr;
+        const int t = SUB ? threadIdx.x % tpr : threadIdx.x;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int at = E * (t + k * tpr);
             on[k] = at < C;
-            c[k] = on[k] ? at : 0;
+            c[k] = at;  // not looked at where the unit is off
         }
         if (warps > 1) {
             for (int i = threadIdx.x; i < 9 * kMaxWarps; i += blockDim.x) {
@@ -341,7 +342,7 @@ struct Row {
         }
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            f2 q = 0;
+            f2 q = twice(0.0f);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const f2 off = minus(mean[m], k);
@@ -429,12 +430,13 @@ inline Shape shape_of(const bsa_gated_norm_desc &d, int v, int regs, int sms, in
 {
     Shape s;
     s.tpr = row_threads(d.C / 8, v);
-    s.threads = s.tpr <= 32 ? 128 : s.tpr;
+    s.threads = s.tpr < 32 ? 128 : s.tpr;
     s.smem = static_cast<size_t>(s.threads) * (stages * thread_bytes + kept_bytes);
     const int by_regs = 65536 / ((regs + 7) / 8 * 8 * s.threads);
     const int by_smem = static_cast<int>((228 * 1024) / (s.smem + 4096));
     int resident = by_regs < by_smem ? by_regs : by_smem;
     if (resident > 2048 / s.threads) resident = 2048 / s.threads;
+    if (resident > 32) resident = 32;
     if (resident < 1) resident = 1;
     const int per_cta = s.threads / s.tpr;
     s.rg.rows = d.B * d.N;
@@ -442,6 +444,7 @@ inline Shape shape_of(const bsa_gated_norm_desc &d, int v, int regs, int sms, in
     const int64_t fill = static_cast<int64_t>(sms) * resident * per_cta, most = gated_norm_max_workers(s.rg.rows, d.C);
     s.rg.workers = static_cast<int>(fill < most ? fill : most);
     s.rg.most = (s.rg.rows + s.rg.workers - 1) / s.rg.workers;
+    s.rg.long_groups = s.rg.per_group >= s.rg.most;
     s.ctas = (s.rg.workers + per_cta - 1) / per_cta;
     return s;
 }

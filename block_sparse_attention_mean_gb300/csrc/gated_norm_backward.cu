@@ -6,9 +6,10 @@
 //   dshift = A,  dscale = w S + b A,  dgate = alpha (w2 Q + b2 P),
 //   dpre_weight = sum_g (1 + scale_g) S_g,  dpre_bias = sum_g (1 + scale_g) A_g,
 //   dpost_weight = alpha sum_g gate_g Q_g,  dpost_bias = alpha sum_g gate_g P_g.
-// At the end of a group the worker writes the group's gradients itself if it held the whole group, else the
-// four sums into one of its two slots (groups that its range's ends cut); the weights' sums go on in its
-// third. A second kernel adds the slots in the order of the workers, so that results do not depend on timing.
+// At the end of a group the worker writes the four sums into one of its two slots; a second kernel adds the slots
+// in the order of the workers, so that results do not depend on timing. Where groups are shorter than the longest
+// range (long_groups == 0), a worker that held a whole group writes its modulations' gradients itself, and adds up
+// the sums for the weights in a third slot.
 #include "gated_norm.cuh"
 
 namespace bsa {
@@ -80,8 +81,9 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     Row<K, P, SUB> rw(C, tpr, buf);
     const Wants want = wants_of(a);
 
-    const int64_t worker = static_cast<int64_t>(blockIdx.x) * (threads / tpr) + threadIdx.x / tpr;
-    const bool some = worker < rg.workers;
+    // a CTA is one worker, unless lanes of a warp hold several rows: all that depends on the row alone is uniform
+    const int worker = SUB ? blockIdx.x * (threads / tpr) + threadIdx.x / tpr : blockIdx.x;
+    const bool some = !SUB || worker < rg.workers;
     const int first = some ? rg.first(worker) : 0, count = some ? rg.first(worker + 1) - first : 0;
     const int b0 = first / d.N, n0 = first % d.N;
     Walk ph(a.h, b0, n0, sizeof(TS)), pdh(a.dh, b0, n0, sizeof(TS)), pdx(a.dx, b0, n0, sizeof(TS));
@@ -89,7 +91,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     int n_ahead = n0, n_here = n0;
     const int first_group = first / rg.per_group;
     int left = rg.per_group - first % rg.per_group, group = first_group;
-    float *const slots = a.partial + worker * gated_norm_worker_floats(C);
+    float *const slots = a.partial + int64_t(worker) * gated_norm_worker_floats(C);
     bool weighed = false;  // the worker's third slot holds sums
 
     char *const mine_s = ring + threadIdx.x * SB, *const mine_b = ring + threadIdx.x * BB;
@@ -113,11 +115,11 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
                 const uint32_t s_at = smem_u32(mine_s + to * stage_bytes + k * threads * SB);
                 const uint32_t b_at = smem_u32(mine_b + to * stage_bytes + k * threads * BB);
                 if (pre) {
-                    copy_async<SB>(s_at, ph.p + rw.c[k] * sizeof(TS));
-                    copy_async<BB>(b_at + at_dz, pdz.p + rw.c[k] * sizeof(TB));
+                    copy_async<SB>(s_at, ph.p + rw.c[k] * unsigned(sizeof(TS)));
+                    copy_async<BB>(b_at + at_dz, pdz.p + rw.c[k] * unsigned(sizeof(TB)));
                 }
-                if (has_dh) copy_async<SB>(s_at + at_dh, pdh.p + rw.c[k] * sizeof(TS));
-                if (has_y) copy_async<BB>(b_at + at_y, py.p + rw.c[k] * sizeof(TB));
+                if (has_dh) copy_async<SB>(s_at + at_dh, pdh.p + rw.c[k] * unsigned(sizeof(TS)));
+                if (has_y) copy_async<BB>(b_at + at_y, py.p + rw.c[k] * unsigned(sizeof(TB)));
             }
             ph.next(a.h, sizeof(TS));
             pdh.next(a.dh, sizeof(TS));
@@ -207,7 +209,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
         }
         f2 g[K][P];  // the gradient at h, then at u
         if (pre) {
-            f2 q[K][P], s0 = 0, s1 = 0;
+            f2 q[K][P], s0 = twice(0.0f), s1 = twice(0.0f);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 Unit<TB, P>::get(here_b + at_dz + k * threads * BB, q[k]);
@@ -244,10 +246,10 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
         if (a.dx.p && live) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (rw.on[k]) Unit<TS, P>::put(pdx.p + rw.c[k] * sizeof(TS), g[k]);
+                if (rw.on[k]) Unit<TS, P>::put(pdx.p + rw.c[k] * unsigned(sizeof(TS)), g[k]);
         }
         if (has_y) {
-            f2 s0 = 0, s1 = 0;
+            f2 s0 = twice(0.0f), s1 = twice(0.0f);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 Unit<TB, P>::get(here_b + at_y + k * threads * BB, v[k]);
@@ -287,7 +289,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
             if (a.dy.p && live) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (rw.on[k]) Unit<TB, P>::put(pdy.p + rw.c[k] * sizeof(TB), g[k]);
+                    if (rw.on[k]) Unit<TB, P>::put(pdy.p + rw.c[k] * unsigned(sizeof(TB)), g[k]);
             }
         }
         if (!live) continue;
@@ -302,7 +304,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
         // the end of a group, or of the range
         if (want.pre_sums || want.post_sums) {
             const int64_t begin = static_cast<int64_t>(group) * rg.per_group;
-            const bool whole = begin >= first && begin + rg.per_group <= static_cast<int64_t>(first) + count;
+            const bool whole = !rg.long_groups && begin >= first && begin + rg.per_group <= static_cast<int64_t>(first) + count;
             float *const slot = slots + (group == first_group ? 0 : 4 * C);
             const int b = group / d.F, f = group % d.F;
 #pragma unroll
@@ -317,7 +319,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
                     Unit<float, P>::put(slot + 2 * C + c, sP[k]);
                     Unit<float, P>::put(slot + 3 * C + c, sQ[k]);
                 }
-                if (want.weights) {  // weighted for the parameters that all groups share, and added up
+                if (want.weights && !rg.long_groups) {  // weighted for the parameters that all groups share, and added up
                     if (d.scale.ptr) {
                         times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sA[k]);
                         times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sS[k]);
@@ -357,23 +359,50 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     }
 }
 
-// Adds the workers' slots: 64 channels per CTA (four per thread), kSumSlices slices of the workers. blockIdx.y == 0:
-// the weights' sums over all workers; blockIdx.y > 0: one group that several workers share.
-constexpr int kSumSlices = 32;
+// Adds the workers' slots: 32 channels per CTA (four per thread), kSumSlices slices of the workers. blockIdx.y == 0:
+// the weights' sums over all workers; blockIdx.y > 0: one group.
+constexpr int kSumSlices = 64;
 
-__global__ void __launch_bounds__(16 * kSumSlices) gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg,
-                                                                          int64_t n_groups)
+__device__ __forceinline__ void add_slot(const float *p, int C, float4 (&v)[4])
 {
-    __shared__ __align__(16) float part[kSumSlices / 2][4][64];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float4 q = *reinterpret_cast<const float4 *>(p + k * C);
+        v[k].x += q.x, v[k].y += q.y, v[k].z += q.z, v[k].w += q.w;
+    }
+}
+
+// the same, with A and S times 1 + scale and P and Q times gate of group g
+__device__ __forceinline__ void add_slot_weighted(const NormArgs &a, int g, int c, const float *p, float4 (&v)[4])
+{
+    const bsa_gated_norm_desc &d = a.d;
+    const int b = g / d.F, f = g % d.F;
+    f2 m[2][2], q[2];
+    fill(1.0f, m[0]);
+    fill(1.0f, m[1]);
+    if (d.scale.ptr) times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, m[0]);
+    if (d.gate.ptr) load_mod(d.gate.ptr, d.mod_dt, b * d.gate.batch + f * d.gate.frame + c, m[1]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        Unit<float, 2>::get(p + k * d.C, q);
+        f2 x = fma2(q[0], m[k / 2][0], pair(v[k].x, v[k].y)), y = fma2(q[1], m[k / 2][1], pair(v[k].z, v[k].w));
+        split(x, v[k].x, v[k].y);
+        split(y, v[k].z, v[k].w);
+    }
+}
+
+__global__ void __launch_bounds__(8 * kSumSlices) gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg,
+                                                                         int64_t n_groups)
+{
+    __shared__ __align__(16) float part[kSumSlices / 4][4][32];
     grid_dependency_wait();
     const bsa_gated_norm_desc &d = a.d;
     const int C = d.C;
     const int64_t stride = gated_norm_worker_floats(C);
-    const Wants want = wants_of(a);
     int w0 = 0, w1 = rg.workers - 1;
     int64_t group = -1;
     if (blockIdx.y == 0) {
-        if (!want.weights) return;
+        if (!wants_of(a).weights) return;
     } else {
         // the group itself where there are at most as many groups as workers; else the one that worker y - 1's
         // range begins inside
@@ -381,48 +410,59 @@ __global__ void __launch_bounds__(16 * kSumSlices) gated_norm_sums_kernel(const 
         group = n_groups <= rg.workers ? i : rg.first(i) / rg.per_group;
         w0 = rg.worker_of(group * rg.per_group);
         w1 = rg.worker_of((group + 1) * rg.per_group - 1);
-        if (w0 == w1) return;                              // written by its worker
-        if (n_groups > rg.workers && i != w0 + 1) return;  // one CTA per group
+        if (!rg.long_groups) {
+            if (w0 == w1) return;                              // written by its worker
+            if (n_groups > rg.workers && i != w0 + 1) return;  // one CTA per group
+        }
     }
-    const int lane = threadIdx.x % 16, c = blockIdx.x * 64 + 4 * lane;
+    const int lane = threadIdx.x % 8, c = blockIdx.x * 32 + 4 * lane;
     float4 v[4] = {};
     if (c < C) {
+        const float *const slots = a.partial + c;
+        if (group < 0 && rg.long_groups) {
 #pragma unroll 2
-        for (int w = w0 + threadIdx.x / 16; w <= w1; w += kSumSlices) {
-            // a group begins in its first worker's range, in slot 0 if it is the first there; it is the first in the others'
-            const int slot = group < 0 ? 8 : w == w0 && rg.first(w) / rg.per_group != group ? 4 : 0;
-            const float *p = a.partial + w * stride + slot * C + c;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 q = *reinterpret_cast<const float4 *>(p + k * C);
-                v[k].x += q.x, v[k].y += q.y, v[k].z += q.z, v[k].w += q.w;
+            for (int w = w0 + threadIdx.x / 8; w <= w1; w += kSumSlices) {
+                const int g0 = rg.first(w) / rg.per_group, g1 = (rg.first(w + 1) - 1) / rg.per_group;
+                add_slot_weighted(a, g0, c, slots + w * stride, v);
+                if (g1 != g0) add_slot_weighted(a, g1, c, slots + w * stride + 4 * C, v);
+            }
+        } else {
+#pragma unroll 2
+            for (int w = w0 + threadIdx.x / 8; w <= w1; w += kSumSlices) {
+                // a group is the first in the ranges of its workers but, perhaps, that of the first of them
+                const int slot = group < 0 ? 8 : w == w0 && rg.first(w) / rg.per_group != group ? 4 : 0;
+                add_slot(slots + w * stride + slot * C, C, v);
             }
         }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        v[k].x += __shfl_xor_sync(0xffffffffu, v[k].x, 16);
-        v[k].y += __shfl_xor_sync(0xffffffffu, v[k].y, 16);
-        v[k].z += __shfl_xor_sync(0xffffffffu, v[k].z, 16);
-        v[k].w += __shfl_xor_sync(0xffffffffu, v[k].w, 16);
-        if (threadIdx.x % 32 < 16) *reinterpret_cast<float4 *>(&part[threadIdx.x / 32][k][4 * lane]) = v[k];
+#pragma unroll
+        for (int o = 8; o < 32; o <<= 1) {
+            v[k].x += __shfl_xor_sync(0xffffffffu, v[k].x, o);
+            v[k].y += __shfl_xor_sync(0xffffffffu, v[k].y, o);
+            v[k].z += __shfl_xor_sync(0xffffffffu, v[k].z, o);
+            v[k].w += __shfl_xor_sync(0xffffffffu, v[k].w, o);
+        }
+        if (threadIdx.x % 32 < 8) *reinterpret_cast<float4 *>(&part[threadIdx.x / 32][k][4 * lane]) = v[k];
     }
     __syncthreads();
-    if (threadIdx.x < 256) {
+    const int at = threadIdx.x % 32, ch = blockIdx.x * 32 + at;
+    if (threadIdx.x < 128) {
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kSumSlices / 2; ++i) s += part[i][threadIdx.x / 64][threadIdx.x % 64];
-        part[0][threadIdx.x / 64][threadIdx.x % 64] = s;
+        for (int i = 0; i < kSumSlices / 4; ++i) s += part[i][threadIdx.x / 32][at];
+        part[0][threadIdx.x / 32][at] = s;
     }
     __syncthreads();
-    const int at = threadIdx.x, ch = blockIdx.x * 64 + at;
-    if (at >= 64 || ch >= C) return;
+    if (threadIdx.x >= 32 || ch >= C) return;
     const float sA = part[0][0][at], sS = part[0][1][at], sP = part[0][2][at], sQ = part[0][3][at];
     if (group < 0) {
+        const float alpha = rg.long_groups ? d.alpha : 1.0f;  // the third slots have it already
         if (a.dpre_b) a.dpre_b[ch] = sA;
         if (a.dpre_w) a.dpre_w[ch] = sS;
-        if (a.dpost_b) a.dpost_b[ch] = sP;
-        if (a.dpost_w) a.dpost_w[ch] = sQ;
+        if (a.dpost_b) a.dpost_b[ch] = alpha * sP;
+        if (a.dpost_w) a.dpost_w[ch] = alpha * sQ;
         return;
     }
     auto put = [&](char *p, float x) {
@@ -455,8 +495,8 @@ bsa_status backward(const NormArgs &a, int sms, cudaStream_t st)
     if (a.partial == nullptr) return BSA_OK;
     const int64_t n_groups = static_cast<int64_t>(a.d.B) * a.d.F;
     const int64_t items = n_groups < s.rg.workers ? n_groups : s.rg.workers;
-    const dim3 grid((a.d.C + 63) / 64, static_cast<unsigned>(items + 1));
-    return pdl_launch(gated_norm_sums_kernel, grid, 16 * kSumSlices, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
+    const dim3 grid((a.d.C + 31) / 32, static_cast<unsigned>(items + 1));
+    return pdl_launch(gated_norm_sums_kernel, grid, 8 * kSumSlices, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
 }
 
 }  // namespace
