@@ -21,7 +21,7 @@
 namespace bsa {
 namespace {
 
-template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST>
+template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST, bool LN>
 __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ NormArgs a, Ranges rg, int tpr)
 {
     constexpr int E = 16 / sizeof(TS), P = E / 2, K = 8 * V / E, XB = E * sizeof(TS), YB = E * sizeof(TB);
@@ -31,7 +31,7 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
     const bsa_gated_norm_desc &d = a.d;
     const bool branch = a.y.p != nullptr, pre = d.pre.kind != BSA_NORM_NONE;
     const int threads = blockDim.x, at_y = K * threads * XB, stage_bytes = at_y + (branch ? K * threads * YB : 0);
-    Row<K, P, SUB> rw(d.C, tpr, buf);
+    Row<K, P, SUB, LN> rw(d.C, tpr, buf);
 
     // a CTA is one worker, unless lanes of a warp hold several rows: all that depends on the row alone is uniform
     const int worker = SUB ? blockIdx.x * (threads / tpr) + threadIdx.x / tpr : blockIdx.x;
@@ -109,7 +109,7 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
     if (count > 0) factors(group);
 
     // workers of whole warps end on their own; lanes that share a warp go on with it, writing nothing
-    const int rounds = SUB ? rg.most : count;
+    const int rounds = SUB ? rg.most() : count;
     for (int i = 0; i < rounds; ++i) {
         fetch(i + STAGES - 1 < count);
         cp_async_wait_group<STAGES - 1>();  // row i is here
@@ -137,7 +137,7 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
 #pragma unroll
                     for (int j = 0; j < P; ++j) {
                         t[0][k][j] = add2(t[0][k][j], h0[k][j]);
-                        t[0][k][j] = fma2(add2(m[0][k][j], off), mul2(r, h1[k][j]), t[0][k][j]);
+                        t[0][k][j] = fma2(rw.centred(m[0][k][j], off), mul2(r, h1[k][j]), t[0][k][j]);
                     }
                 }
             } else {
@@ -160,7 +160,7 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
             for (int k = 0; k < K; ++k) {
                 const f2 off = rw.minus(mean[0], k);
 #pragma unroll
-                for (int j = 0; j < P; ++j) t[0][k][j] = fma2(add2(t[0][k][j], off), mul2(r, z1[k][j]), z0[k][j]);
+                for (int j = 0; j < P; ++j) t[0][k][j] = fma2(rw.centred(t[0][k][j], off), mul2(r, z1[k][j]), z0[k][j]);
                 if (live && rw.on[k]) Unit<TB, P>::put(z.p + rw.c[k] * unsigned(sizeof(TB)), t[0][k]);
             }
         }
@@ -177,10 +177,10 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
     }
 }
 
-template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST>
+template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST, bool LN>
 bsa_status forward(const NormArgs &a, int sms, cudaStream_t st)
 {
-    auto kern = gated_norm_kernel<TS, TB, V, REGS, SUB, POST>;
+    auto kern = gated_norm_kernel<TS, TB, V, REGS, SUB, POST, LN>;
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> regs{0};
     constexpr int BYTES = 8 * V * (sizeof(TS) + sizeof(TB)), STAGES = stages_for(BYTES);
@@ -199,9 +199,9 @@ bsa_status launch_gated_norm(const NormArgs &a, cudaStream_t st)
     int sms = 0;
     const bsa_status s = current_sm_count(&sms);
     if (s != BSA_OK) return s;
-    return by_kernel(a.d, [&](auto ts, auto tb, auto v, auto regs, auto sub, auto post) {
+    return by_kernel(a.d, [&](auto ts, auto tb, auto v, auto regs, auto sub, auto post, auto ln) {
         return forward<decltype(ts), decltype(tb), decltype(v)::value, decltype(regs)::value,
-                        decltype(sub)::value, decltype(post)::value>(a, sms, st);
+                        decltype(sub)::value, decltype(post)::value, decltype(ln)::value>(a, sms, st);
     });
 }
 

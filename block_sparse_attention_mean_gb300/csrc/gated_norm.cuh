@@ -13,7 +13,8 @@ namespace {
 
 constexpr int kMaxWarps = 16;  // CTAs of up to 512 threads
 
-// Rows in flight per worker: three, fewer where a CTA of 512 threads would not find room for them (rows of more
+// Rows in flight per worker: three (more of them are slower: 65536 rows of 2048 channels 181 us, with four 196 us),
+// fewer where a CTA of 512 threads would not find room for them (rows of more
 // than 4096 channels). `bytes`: what a thread copies per row; `kept`: what it holds in shared memory besides.
 __host__ __device__ constexpr int stages_for(int bytes, int kept = 0)
 {
@@ -195,16 +196,21 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
 
 // ------------------------------------------------------------ rows and workers
 
-// The rows, B * N in order, cut into `workers` ranges that differ by at most one row.
+// The rows, B * N in order, cut into `workers` ranges of nearly equal length: range w begins at row
+// floor(w * step / 2^32), step = ceil(rows * 2^32 / workers). Longer and shorter ranges alternate on purpose: with
+// the longer ones first, all workers stood a whole number of rows (a multiple of a large power of two in bytes)
+// apart and met in the same memory channels (65536 rows of 2048 channels: 184 against 174 us).
 struct Ranges {
-    int rows, workers, most;  // most: the longest range
-    int per_group;            // rows that share a modulation
-    int long_groups;          // no range is longer than a group: it touches two groups at most
+    int rows, workers;
+    uint64_t step;
+    int per_group;    // rows that share a modulation
+    int long_groups;  // no range is longer than a group: it touches two groups at most
 
-    __host__ __device__ int first(int64_t w) const { return static_cast<int>(w * rows / workers); }
-    __host__ __device__ int worker_of(int64_t row) const
+    __host__ __device__ int first(int w) const { return static_cast<int>(static_cast<uint64_t>(w) * step >> 32); }
+    __host__ __device__ int most() const { return static_cast<int>(step >> 32) + 1; }  // no range is longer
+    __device__ int worker_of(int row) const
     {
-        return static_cast<int>(((row + 1) * workers - 1) / rows);
+        return static_cast<int>(((static_cast<uint64_t>(row) + 1 << 32) - 1) / step);
     }
 };
 
@@ -219,8 +225,8 @@ struct Walk {
 };
 
 // What a thread knows of its row: its channels, and the CTA's exchange of the warps' sums. SUB: the row is held
-// by `lanes` < 32 lanes of a warp; else by whole warps.
-template <int K, int P, bool SUB>
+// by `lanes` < 32 lanes of a warp; else by whole warps. LN: a layer norm is among the norms (RMS alone needs no means).
+template <int K, int P, bool SUB, bool LN>
 struct Row {
     static constexpr int E = 2 * P;
     int C, lanes, warps, turn;
@@ -315,6 +321,8 @@ struct Row {
 
     // -mean where a unit is on, 0 where it is off: adding it leaves units that are off at zero
     __device__ __forceinline__ f2 minus(float mean, int k) const { return twice(on[k] ? -mean : 0.0f); }
+    // v - mean, for a mean's minus(); nothing to do without a layer norm
+    static __device__ __forceinline__ f2 centred(f2 v, f2 off) { return LN ? add2(v, off) : v; }
 
     // Mean (0 but for LAYER) and mean square about it of M rows at once, one exchange. The spread is taken about
     // each warp's own mean and joined exactly: sum_w (spread_w + n_w (mean_w - mean)^2), no cancellation for rows
@@ -322,13 +330,9 @@ struct Row {
     template <int M>
     __device__ __forceinline__ void stats(const f2 (&v)[M][K][P], const int (&kind)[M], float (&mean)[M], float (&square)[M])
     {
-        bool layer = false;
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-            layer = layer || kind[m] == BSA_NORM_LAYER;
-            mean[m] = 0.0f;
-        }
-        if (layer) {
+        for (int m = 0; m < M; ++m) mean[m] = 0.0f;
+        if (LN) {
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 f2 q = v[m][0][0];
@@ -348,7 +352,7 @@ struct Row {
                 const f2 off = minus(mean[m], k);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    const f2 x = add2(v[m][k][i], off);
+                    const f2 x = centred(v[m][k][i], off);
                     q = fma2(x, x, q);
                 }
             }
@@ -356,13 +360,16 @@ struct Row {
         }
         lanes_sum(square);
         if (warps > 1) {
-            float s[2 * M];
+            float s[LN ? 2 * M : M];
 #pragma unroll
-            for (int m = 0; m < M; ++m) s[m] = square[m], s[M + m] = mean[m];
+            for (int m = 0; m < M; ++m) {
+                s[m] = square[m];
+                if (LN) s[(LN ? M : 0) + m] = mean[m];
+            }
             const float *b = exchange(s);
 #pragma unroll
             for (int m = 0; m < M; ++m) square[m] = total(b + m * kMaxWarps);
-            if (layer) {
+            if (LN) {
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
                     const float4 *means = reinterpret_cast<const float4 *>(b + (M + m) * kMaxWarps);
@@ -443,33 +450,37 @@ inline Shape shape_of(const bsa_gated_norm_desc &d, int v, int regs, int sms, in
     s.rg.per_group = d.N / d.F;
     const int64_t fill = static_cast<int64_t>(sms) * resident * per_cta, most = gated_norm_max_workers(s.rg.rows, d.C);
     s.rg.workers = static_cast<int>(fill < most ? fill : most);
-    s.rg.most = (s.rg.rows + s.rg.workers - 1) / s.rg.workers;
-    s.rg.long_groups = s.rg.per_group >= s.rg.most;
+    s.rg.step = ((static_cast<uint64_t>(s.rg.rows) << 32) + s.rg.workers - 1) / s.rg.workers;
+    s.rg.long_groups = s.rg.per_group >= s.rg.most();
     s.ctas = (s.rg.workers + per_cta - 1) / per_cta;
     return s;
 }
 
 // run(stream dtype, branch dtype, V, registers per thread, whether lanes of one warp hold several rows, whether there
-// is a post norm) for the kernel that a desc needs
+// is a post norm, whether a layer norm is among the norms) for the kernel that a desc needs
 template <typename F>
 bsa_status by_kernel(const bsa_gated_norm_desc &d, F &&run)
 {
-    auto by_width = [&](auto ts, auto tb, auto post) {
+    auto by_width = [&](auto ts, auto tb, auto post, auto ln) {
         const auto no = std::false_type();
         const std::integral_constant<int, 1> one;
         const std::integral_constant<int, 2> two;
         // up to 256 threads per row: three CTAs of 128 threads per SM find 168 registers each; beyond, 512 threads
-        if (d.C > 4096) return run(ts, tb, two, std::integral_constant<int, 128>(), no, post);
-        if (vectors(d.C) == 2) return run(ts, tb, two, std::integral_constant<int, 168>(), no, post);
+        if (d.C > 4096) return run(ts, tb, two, std::integral_constant<int, 128>(), no, post, ln);
+        if (vectors(d.C) == 2) return run(ts, tb, two, std::integral_constant<int, 168>(), no, post, ln);
         const std::integral_constant<int, 128> regs;
-        return row_threads(d.C / 8, 1) < 32 ? run(ts, tb, one, regs, std::true_type(), post) : run(ts, tb, one, regs, no, post);
+        return row_threads(d.C / 8, 1) < 32 ? run(ts, tb, one, regs, std::true_type(), post, ln)
+                                            : run(ts, tb, one, regs, no, post, ln);
     };
-    auto by_post = [&](auto ts, auto tb) {
-        return d.post.kind != BSA_NORM_NONE ? by_width(ts, tb, std::true_type()) : by_width(ts, tb, std::false_type());
+    auto by_norms = [&](auto ts, auto tb) {
+        const bool ln = d.post.kind == BSA_NORM_LAYER || d.pre.kind == BSA_NORM_LAYER;
+        if (d.post.kind != BSA_NORM_NONE)
+            return ln ? by_width(ts, tb, std::true_type(), std::true_type()) : by_width(ts, tb, std::true_type(), std::false_type());
+        return ln ? by_width(ts, tb, std::false_type(), std::true_type()) : by_width(ts, tb, std::false_type(), std::false_type());
     };
-    if (d.stream_dt == BSA_BF16) return by_post(__nv_bfloat16(), __nv_bfloat16());
-    if (d.branch_dt == BSA_BF16) return by_post(float(), __nv_bfloat16());
-    return by_post(float(), float());
+    if (d.stream_dt == BSA_BF16) return by_norms(__nv_bfloat16(), __nv_bfloat16());
+    if (d.branch_dt == BSA_BF16) return by_norms(float(), __nv_bfloat16());
+    return by_norms(float(), float());
 }
 
 }  // namespace

@@ -64,7 +64,7 @@ __device__ __forceinline__ void write_group(const NormArgs &a, int64_t g, int c,
     }
 }
 
-template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST>
+template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST, bool LN>
 __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_constant__ NormArgs a, Ranges rg, int tpr)
 {
     constexpr int E = 16 / sizeof(TS), P = E / 2, K = 8 * V / E, SB = E * sizeof(TS), BB = E * sizeof(TB);
@@ -78,7 +78,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     // where each tensor's units lie within a stage
     const int at_dh = pre ? K * threads * SB : 0, at_dz = at_dh + (has_dh ? K * threads * SB : 0),
               at_y = at_dz + (pre ? K * threads * BB : 0), stage_bytes = at_y + (has_y ? K * threads * BB : 0);
-    Row<K, P, SUB> rw(C, tpr, buf);
+    Row<K, P, SUB, LN> rw(C, tpr, buf);
     const Wants want = wants_of(a);
 
     // a CTA is one worker, unless lanes of a warp hold several rows: all that depends on the row alone is uniform
@@ -176,7 +176,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     };
     if (count > 0) factors(group);
 
-    const int rounds = SUB ? rg.most : count;
+    const int rounds = SUB ? rg.most() : count;
     for (int i = 0; i < rounds; ++i) {
         fetch(i + STAGES - 1 < count);
         cp_async_wait_group<STAGES - 1>();
@@ -187,24 +187,59 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
         f2 v[K][P];  // h, then n; later y, then m (read from the ring a second time: registers are what is scarce)
         float mean[M], r[M];
         if (pre || POST) {
-            f2 both_rows[M][K][P];
-            int kind[M];
-            kind[0] = d.pre.kind;
-            if (POST) kind[M - 1] = d.post.kind;
+            if (LN) {
+                f2 both_rows[M][K][P];
+                int kind[M];
+                kind[0] = d.pre.kind;
+                if (POST) kind[M - 1] = d.post.kind;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                fill(0.0f, both_rows[0][k]);
-                if (pre) Unit<TS, P>::get(here_s + k * threads * SB, both_rows[0][k]);
-                if (POST) Unit<TB, P>::get(here_b + at_y + k * threads * BB, both_rows[M - 1][k]);
-            }
-            rw.stats(both_rows, kind, mean, r);
-            r[0] = rsqrtf(r[0] + d.pre.eps);
-            if (POST) r[M - 1] = rsqrtf(r[M - 1] + d.post.eps);
+                for (int k = 0; k < K; ++k) {
+                    fill(0.0f, both_rows[0][k]);
+                    if (pre) Unit<TS, P>::get(here_s + k * threads * SB, both_rows[0][k]);
+                    if (POST) Unit<TB, P>::get(here_b + at_y + k * threads * BB, both_rows[M - 1][k]);
+                }
+                rw.stats(both_rows, kind, mean, r);
+                r[0] = rsqrtf(r[0] + d.pre.eps);
+                if (POST) r[M - 1] = rsqrtf(r[M - 1] + d.post.eps);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const f2 off = rw.minus(mean[0], k), rr = twice(r[0]);
+                for (int k = 0; k < K; ++k) {
+                    const f2 off = rw.minus(mean[0], k), rr = twice(r[0]);
 #pragma unroll
-                for (int j = 0; j < P; ++j) v[k][j] = mul2(add2(both_rows[0][k][j], off), rr);
+                    for (int j = 0; j < P; ++j) v[k][j] = mul2(rw.centred(both_rows[0][k][j], off), rr);
+                }
+            } else {
+                // one row after the other, to hold only one of them
+                float square[M];
+                if (POST) {
+                    f2 s = twice(0.0f);
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        Unit<TB, P>::get(here_b + at_y + k * threads * BB, v[k]);
+#pragma unroll
+                        for (int j = 0; j < P; ++j) s = fma2(v[k][j], v[k][j], s);
+                    }
+                    square[M - 1] = two(s);
+                    asm volatile("" ::: "memory");
+                }
+                f2 s = twice(0.0f);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    fill(0.0f, v[k]);
+                    if (pre) Unit<TS, P>::get(here_s + k * threads * SB, v[k]);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) s = fma2(v[k][j], v[k][j], s);
+                }
+                square[0] = two(s);
+                rw.sums(square);
+                r[0] = rsqrtf(square[0] * rw.inv_c + d.pre.eps);
+                mean[0] = mean[M - 1] = 0.0f;
+                if (POST) r[M - 1] = rsqrtf(square[M - 1] * rw.inv_c + d.post.eps);
+                const f2 rr = twice(r[0]);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) v[k][j] = mul2(v[k][j], rr);
+                }
             }
         }
         f2 g[K][P];  // the gradient at h, then at u
@@ -224,20 +259,21 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     s0 = fma2(q[k][j], v[k][j], s0);
-                    s1 = add2(s1, q[k][j]);
+                    if (LN) s1 = add2(s1, q[k][j]);
                 }
             }
-            float s[2] = {two(s0), two(s1)};
+            float s[LN ? 2 : 1] = {two(s0)};
+            if (LN) s[LN ? 1 : 0] = two(s1);
             rw.sums(s);
             const f2 along = twice(-s[0] * rw.inv_c), rr = twice(r[0]);
-            const float m = d.pre.kind == BSA_NORM_LAYER ? s[1] * rw.inv_c : 0.0f;
+            const float m = LN && d.pre.kind == BSA_NORM_LAYER ? s[LN ? 1 : 0] * rw.inv_c : 0.0f;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const f2 off = rw.minus(m, k);
                 fill(0.0f, g[k]);
                 if (has_dh) Unit<TS, P>::get(here_s + at_dh + k * threads * SB, g[k]);
 #pragma unroll
-                for (int j = 0; j < P; ++j) g[k][j] = fma2(rr, fma2(v[k][j], along, add2(q[k][j], off)), g[k][j]);
+                for (int j = 0; j < P; ++j) g[k][j] = fma2(rr, fma2(v[k][j], along, rw.centred(q[k][j], off)), g[k][j]);
             }
         } else {
 #pragma unroll
@@ -256,7 +292,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
                 if (POST) {
                     const f2 off = rw.minus(mean[M - 1], k), rr = twice(r[M - 1]);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) v[k][j] = mul2(add2(v[k][j], off), rr);
+                    for (int j = 0; j < P; ++j) v[k][j] = mul2(rw.centred(v[k][j], off), rr);
                 }
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
@@ -270,20 +306,21 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
 #pragma unroll
                     for (int j = 0; j < P; ++j) {
                         s0 = fma2(g[k][j], v[k][j], s0);
-                        s1 = add2(s1, g[k][j]);
+                        if (LN) s1 = add2(s1, g[k][j]);
                     }
                 }
             }
             if (POST) {
-                float s[2] = {two(s0), two(s1)};
+                float s[LN ? 2 : 1] = {two(s0)};
+            if (LN) s[LN ? 1 : 0] = two(s1);
                 rw.sums(s);
                 const f2 along = twice(-s[0] * rw.inv_c), rr = twice(r[M - 1]);
-                const float m = d.post.kind == BSA_NORM_LAYER ? s[1] * rw.inv_c : 0.0f;
+                const float m = LN && d.post.kind == BSA_NORM_LAYER ? s[LN ? 1 : 0] * rw.inv_c : 0.0f;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const f2 off = rw.minus(m, k);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) g[k][j] = mul2(rr, fma2(v[k][j], along, add2(g[k][j], off)));
+                    for (int j = 0; j < P; ++j) g[k][j] = mul2(rr, fma2(v[k][j], along, rw.centred(g[k][j], off)));
                 }
             }
             if (a.dy.p && live) {
@@ -478,10 +515,10 @@ __global__ void __launch_bounds__(8 * kSumSlices) gated_norm_sums_kernel(const _
     if (a.dgate) put(a.dgate, d.alpha * (by(d.post.weight, 1.0f, sQ) + by(d.post.bias, 0.0f, sP)));
 }
 
-template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST>
+template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST, bool LN>
 bsa_status backward(const NormArgs &a, int sms, cudaStream_t st)
 {
-    auto kern = gated_norm_backward_kernel<TS, TB, V, REGS, SUB, POST>;
+    auto kern = gated_norm_backward_kernel<TS, TB, V, REGS, SUB, POST, LN>;
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> regs{0};
     constexpr int BYTES = 16 * V * (sizeof(TS) + sizeof(TB)), STAGES = stages_for(BYTES, 64 * V);
@@ -512,9 +549,9 @@ bsa_status launch_gated_norm_backward(const NormArgs &a, cudaStream_t st)
     int sms = 0;
     const bsa_status s = current_sm_count(&sms);
     if (s != BSA_OK) return s;
-    return by_kernel(a.d, [&](auto ts, auto tb, auto v, auto regs, auto sub, auto post) {
+    return by_kernel(a.d, [&](auto ts, auto tb, auto v, auto regs, auto sub, auto post, auto ln) {
         return backward<decltype(ts), decltype(tb), decltype(v)::value, decltype(regs)::value,
-                        decltype(sub)::value, decltype(post)::value>(a, sms, st);
+                        decltype(sub)::value, decltype(post)::value, decltype(ln)::value>(a, sms, st);
     });
 }
 
