@@ -8,12 +8,13 @@ run on the tensors' device and on ``stream`` (that device's current stream by de
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import binding
-from .binding import BF16, ERR_DTYPE, ERR_INVALID_ARG, ERR_SHAPE, FP32, BsaError, _check, _ptr, _stream
+from .binding import BF16, ERR_DTYPE, ERR_INVALID_ARG, ERR_SHAPE, FP32, OK, BsaError, _check, _ptr, _stream
 
 ROTARY_MAX_AXES = 4
 ROTARY_INTERLEAVED = 0
@@ -163,8 +164,17 @@ def bsa_gated_norm_workspace_size(B: int, N: int, C: int) -> int:
 
 
 # ------------------------------------------------------------------ helpers
+#
+# The helpers pass descriptors as bytes in the structures' layout (struct.pack: a tenth of the time of a ctypes
+# structure), and put off every message until a check fails: what they cost counts in calls on small tensors.
 
 _CODES = {torch.bfloat16: BF16, torch.float32: FP32}
+_HEADS = struct.Struct("PqqqPqqqPi4x")
+_HEADS_GRAD = struct.Struct("PqqqPqqqPqqqPPi4x")
+_ROWS = struct.Struct("Pqq")
+_DESC = struct.Struct("7if" + "ifPP" * 2 + "Pqq" * 3)
+_GRADS = struct.Struct("Pqq" * 6 + "7P")
+_NO_ROWS = (0, 0, 0)
 
 
 def _code(t: torch.Tensor, what: str) -> int:
@@ -174,16 +184,17 @@ def _code(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _expect(t: torch.Tensor, shape, dtype: torch.dtype, device, what: str) -> None:
+def _expect(t: torch.Tensor, shape, dtype: torch.dtype, device, what: str, name: str) -> None:
     """Shape, dtype, device and contiguous channels of a tensor that a kernel will index by them."""
+    if t.shape == shape and t.dtype == dtype and t.device == device and (t.stride(-1) == 1 or shape[-1] <= 1):
+        return
     if t.shape != shape:
-        raise BsaError(ERR_SHAPE, f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise BsaError(ERR_SHAPE, f"{what}: {name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
-        raise BsaError(ERR_DTYPE, f"{what}: dtype {t.dtype}, expected {dtype}")
+        raise BsaError(ERR_DTYPE, f"{what}: {name}: dtype {t.dtype}, expected {dtype}")
     if t.device != device:
-        raise BsaError(ERR_INVALID_ARG, f"{what}: on {t.device}, expected {device}")
-    if t.stride(-1) != 1 and shape[-1] > 1:
-        raise BsaError(ERR_INVALID_ARG, f"{what}: channels must be contiguous")
+        raise BsaError(ERR_INVALID_ARG, f"{what}: {name}: on {t.device}, expected {device}")
+    raise BsaError(ERR_INVALID_ARG, f"{what}: {name}: channels must be contiguous")
 
 
 def _cuda_device(t: torch.Tensor, what: str) -> torch.device:
@@ -192,13 +203,26 @@ def _cuda_device(t: torch.Tensor, what: str) -> torch.device:
     return t.device
 
 
-def _on(device: torch.device, fn, *args, stream=None) -> None:
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)  # the same without an object
+
+
+def _run(what: str, fn, device: torch.device, stream, *args) -> None:
     """fn(*args, stream) with `device` current: the library launches on the current device."""
+    if stream is None:
+        stream = _current_stream(device.index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        fn(*args, stream)
-        return
-    with torch.cuda.device(device):
-        fn(*args, stream)
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, stream)
+    if code != OK:
+        raise BsaError(code, what)
 
 
 def _workspace_bytes(ws: Optional[torch.Tensor], device: torch.device, what: str) -> int:
@@ -261,38 +285,36 @@ def grid_positions(grid: Sequence[int], n_text: int = 0, cuboid: Optional[Sequen
     return torch.cat((torch.zeros((n_text, len(grid)), dtype=torch.int32, device=device), c)).contiguous()
 
 
-def _rotary_args(plan, tensors, names, positions, weights, layout, what):
-    """Common checks of rotary and rotary_backward: (device, dtype code, B, N, heads of each, pos_batch).
-    layout: "nh" for [B, N, heads, d] tensors, "hn" for [B, heads, N, d]."""
-    first = next((t for t in tensors if t is not None), None)
+def _rotary_args(plan, tensors, positions, q_weight, k_weight, h_at, what):
+    """Common checks of rotary and rotary_backward: (device, dtype code, B, N, positions, pos_batch). h_at: where the
+    heads are, 2 in [B, N, heads, d] tensors and 1 in [B, heads, N, d] ones."""
+    first = tensors[0] if tensors[0] is not None else tensors[1] if tensors[1] is not None else tensors[2]
     if first is None:
         raise BsaError(ERR_INVALID_ARG, f"{what}: none of q, k, v")
     device = _cuda_device(first, what)
     if first.dim() != 4:
         raise BsaError(ERR_SHAPE, f"{what}: {first.dim()} dimensions, expected 4")
-    B, N = first.shape[0], first.shape[1 if layout == "nh" else 2]
-    h_at = 2 if layout == "nh" else 1
-    heads = []
-    for t, name in zip(tensors, names):
-        if t is None:
-            heads.append(0)
-            continue
-        h = t.shape[h_at] if t.dim() == 4 else 0
-        _expect(t, (B, N, h, plan.d) if layout == "nh" else (B, h, N, plan.d), first.dtype, device, f"{what}: {name}")
-        heads.append(h)
+    B, N, d = first.shape[0], first.shape[3 - h_at], plan.d
+    for t, name in zip(tensors, "qkv"):
+        if t is not None:
+            h = t.shape[h_at] if t.dim() == 4 else 0
+            _expect(t, (B, N, h, d) if h_at == 2 else (B, h, N, d), first.dtype, device, what, name)
     pos_batch = 0
     if tensors[0] is not None or tensors[1] is not None:
         if positions is None:
             raise BsaError(ERR_INVALID_ARG, f"{what}: no positions")
-        shape = (N, plan.n_axes) if positions.dim() == 2 else (B, N, plan.n_axes)
-        _expect(positions, shape, torch.int32, device, f"{what}: positions")
+        flat = positions.dim() == 2
+        _expect(positions, (N, plan.n_axes) if flat else (B, N, plan.n_axes), torch.int32, device, what, "positions")
         if N > 1 and positions.stride(-2) != plan.n_axes:
             raise BsaError(ERR_INVALID_ARG, f"{what}: a token's positions must follow the last token's")
-        pos_batch = positions.stride(0) if positions.dim() == 3 else 0
-    for w, name in zip(weights, ("q_weight", "k_weight")):
+        pos_batch = 0 if flat else positions.stride(0)
+        positions = positions.data_ptr()
+    else:
+        positions = None
+    for w in (q_weight, k_weight):
         if w is not None:
-            _expect(w, (plan.d,), torch.float32, device, f"{what}: {name}")
-    return device, _code(first, what), B, N, heads, pos_batch
+            _expect(w, (d,), torch.float32, device, what, "weight")
+    return device, _code(first, what), B, N, positions, pos_batch
 
 
 def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None,
@@ -304,27 +326,25 @@ def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor
     normalised per head (norm_eps not None; fp32 weights [d] optional) and turned by `positions`
     (int32 [N, axes] or [B, N, axes]). `out`: the three results' tensors, any strides with contiguous
     channels. Returns (q, k, v), None where none was given."""
-    device, dt, B, N, heads, pos_batch = _rotary_args(plan, (q, k, v), "qkv", positions, (q_weight, k_weight), "nh",
-                                                      "rotary")
-    if out is None:
-        out = (None, None, None)
+    device, dt, B, N, pos, pos_batch = _rotary_args(plan, (q, k, v), positions, q_weight, k_weight, 2, "rotary")
     res, desc = [], []
-    for t, o, w, h in zip((q, k, v), out, (q_weight, k_weight, None), heads):
+    for t, o, w in zip((q, k, v), out if out is not None else (None, None, None), (q_weight, k_weight, None)):
         if t is None:
             res.append(None)
             desc.append(None)
             continue
+        h = t.shape[2]
         if o is None:
             o = torch.empty((B, h, N, plan.d), dtype=t.dtype, device=device)
         else:
-            _expect(o, (B, h, N, plan.d), t.dtype, device, "rotary: out")
+            _expect(o, (B, h, N, plan.d), t.dtype, device, "rotary", "out")
         s0, s1, s2, _ = t.stride()
         o0, o1, o2, _ = o.stride()
-        desc.append(Heads(t.data_ptr(), s0, s1, s2, o.data_ptr(), o0, o2, o1, w.data_ptr() if w is not None else None, h))
+        desc.append(_HEADS.pack(t.data_ptr(), s0, s1, s2, o.data_ptr(), o0, o2, o1, 0 if w is None else w.data_ptr(), h))
         res.append(o)
     norm = norm_eps is not None
-    _on(device, bsa_rotary, plan, *desc, dt, B, N, positions, pos_batch, int(norm), norm_eps if norm else 0.0,
-        stream=stream)
+    _run("bsa_rotary", load().bsa_rotary, device, stream, ctypes.byref(plan), *desc, dt, B, N, pos, pos_batch, norm,
+         norm_eps if norm else 0.0)
     return tuple(res)
 
 
@@ -343,39 +363,40 @@ def rotary_backward(plan: RotaryPlan, dq: Optional[torch.Tensor], dk: Optional[t
     """Run bsa_rotary_backward: the gradients dq, dk, dv [B, heads, N, d] that arrive at rotary's results, to
     the gradients [B, N, heads, d] of its inputs. With norm_eps, q and k are rotary's inputs. Returns
     (gq, gk, gv, gq_weight, gk_weight); a weight's gradient (fp32 [d]) where that weight is given."""
-    device, dt, B, N, heads, pos_batch = _rotary_args(plan, (dq, dk, dv), ("dq", "dk", "dv"), positions,
-                                                      (q_weight, k_weight), "hn", "rotary_backward")
+    what = "rotary_backward"
+    device, dt, B, N, pos, pos_batch = _rotary_args(plan, (dq, dk, dv), positions, q_weight, k_weight, 1, what)
     norm = norm_eps is not None
-    if out is None:
-        out = (None, None, None)
-    res, desc, dweights = [], [], [None, None, None]
-    if norm and (q_weight is not None or k_weight is not None):
-        both = torch.empty((2, plan.d), dtype=torch.float32, device=device)
-        dweights = [both[0] if dq is not None and q_weight is not None else None,
-                    both[1] if dk is not None and k_weight is not None else None, None]
-    for t, x, o, w, dw, h in zip((dq, dk, dv), (q, k, None), out, (q_weight, k_weight, None), dweights, heads):
+    res, desc, dweights = [], [], []
+    for i, (t, x, o, w) in enumerate(zip((dq, dk, dv), (q, k, None), out if out is not None else (None, None, None),
+                                         (q_weight, k_weight, None))):
+        dw = torch.empty_like(w) if norm and w is not None and t is not None else None
+        dweights.append(dw)
         if t is None:
             res.append(None)
             desc.append(None)
             continue
+        h = t.shape[1]
+        shape = (B, N, h, plan.d)
         if o is None:
-            o = torch.empty((B, N, h, plan.d), dtype=t.dtype, device=device)
+            o = torch.empty(shape, dtype=t.dtype, device=device)
         else:
-            _expect(o, (B, N, h, plan.d), t.dtype, device, "rotary_backward: out")
-        x_args = (None, 0, 0, 0)
-        if norm and len(res) < 2:
+            _expect(o, shape, t.dtype, device, what, "out")
+        x0 = x1 = x2 = x_at = 0
+        if norm and i < 2:
             if x is None:
                 raise BsaError(ERR_INVALID_ARG, "rotary_backward: the norm needs q and k")
-            _expect(x, (B, N, h, plan.d), t.dtype, device, "rotary_backward: q, k")
-            x_args = (x.data_ptr(), *x.stride()[:3])
+            _expect(x, shape, t.dtype, device, what, "q, k")
+            x_at = x.data_ptr()
+            x0, x1, x2, _ = x.stride()
         s0, s1, s2, _ = t.stride()
-        desc.append(HeadsGrad(t.data_ptr(), s0, s2, s1, *x_args, o.data_ptr(), *o.stride()[:3],
-                              w.data_ptr() if w is not None else None, dw.data_ptr() if dw is not None else None, h))
+        o0, o1, o2, _ = o.stride()
+        desc.append(_HEADS_GRAD.pack(t.data_ptr(), s0, s2, s1, x_at, x0, x1, x2, o.data_ptr(), o0, o1, o2,
+                                     0 if w is None else w.data_ptr(), 0 if dw is None else dw.data_ptr(), h))
         res.append(o)
     if ws is None and (dweights[0] is not None or dweights[1] is not None):
         ws = rotary_workspace(B, N, plan.d, device)
-    _on(device, bsa_rotary_backward, plan, *desc, dt, B, N, positions, pos_batch, int(norm), norm_eps if norm else 0.0,
-        ws, _workspace_bytes(ws, device, "rotary_backward"), stream=stream)
+    _run("bsa_rotary_backward", load().bsa_rotary_backward, device, stream, ctypes.byref(plan), *desc, dt, B, N, pos,
+         pos_batch, norm, norm_eps if norm else 0.0, _ptr(ws), _workspace_bytes(ws, device, what))
     return (*res, dweights[0], dweights[1])
 
 
@@ -405,37 +426,48 @@ class GatedNormGrads(NamedTuple):
     dpre_bias: Optional[torch.Tensor]
 
 
-def _rows(t: Optional[torch.Tensor]) -> Rows:
-    return Rows(None, 0, 0) if t is None else Rows(t.data_ptr(), t.stride(0), t.stride(1))
+def _rows(t: Optional[torch.Tensor]):
+    if t is None:
+        return _NO_ROWS
+    s0, s1, _ = t.stride()
+    return t.data_ptr(), s0, s1
 
 
-def _gated_desc(shape, device, stream_t, branch_t, alpha, post, pre, gate, scale, shift, what) -> GatedNormDesc:
+def _norm_args(n: Optional[NormSpec], C: int, device, what: str):
+    if n is None:
+        return NORM_NONE, 0.0, 0, 0
+    w, b = n.weight, n.bias
+    if w is not None:
+        _expect(w, (C,), torch.float32, device, what, "weight")
+    if b is not None:
+        _expect(b, (C,), torch.float32, device, what, "bias")
+    return _KINDS[n.kind], n.eps, 0 if w is None else w.data_ptr(), 0 if b is None else b.data_ptr()
+
+
+def _gated_desc(shape, device, stream_dt: int, branch_dt: int, alpha, post, pre, gate, scale, shift, what: str):
+    """(bsa_gated_norm_desc as bytes, F)"""
     B, N, C = shape
     F, mod = 1, None
     mods = []
-    for m, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+    for m in (gate, scale, shift):
         if m is None:
-            mods.append(Modulation(None, 0, 0))
+            mods += _NO_ROWS
             continue
+        frames = m.dim() == 3
         if mod is None:
-            F, mod = (m.shape[1] if m.dim() == 3 else 1), m.dtype
-        _expect(m, (B, F, C) if m.dim() == 3 else (B, C), mod, device, f"{what}: {name}")
-        if m.dim() == 2 and F != 1:
-            raise BsaError(ERR_SHAPE, f"{what}: {name}: {tuple(m.shape)} beside {F} frames")
-        mods.append(Modulation(m.data_ptr(), m.stride(0), m.stride(1) if m.dim() == 3 else 0))
+            F, mod = m.shape[1] if frames else 1, m.dtype
+        _expect(m, (B, F, C) if frames else (B, C), mod, device, what, "gate, scale, shift")
+        if frames:
+            s0, s1, _ = m.stride()
+        elif F == 1:
+            s0, s1 = m.stride(0), 0
+        else:
+            raise BsaError(ERR_SHAPE, f"{what}: modulations of shape {tuple(m.shape)} and of {F} frames")
+        mods += (m.data_ptr(), s0, s1)
     if mod is not None and mod not in _CODES:
         raise BsaError(ERR_DTYPE, f"{what}: modulation dtype {mod}")
-    norms = []
-    for n, name in ((post, "post"), (pre, "pre")):
-        if n is None:
-            norms.append(Norm(NORM_NONE, 0.0, None, None))
-            continue
-        for w in (n.weight, n.bias):
-            if w is not None:
-                _expect(w, (C,), torch.float32, device, f"{what}: {name} weight or bias")
-        norms.append(Norm(_KINDS[n.kind], n.eps, _ptr(n.weight), _ptr(n.bias)))
-    return GatedNormDesc(B, N, C, F, _code(stream_t, what), _code(branch_t, what), _CODES[mod] if mod else BF16, alpha,
-                         norms[0], norms[1], mods[0], mods[1], mods[2])
+    return _DESC.pack(B, N, C, F, stream_dt, branch_dt, _CODES[mod] if mod is not None else BF16, alpha,
+                      *_norm_args(post, C, device, what), *_norm_args(pre, C, device, what), *mods), F
 
 
 def gated_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, gate: Optional[torch.Tensor] = None,
@@ -446,28 +478,31 @@ def gated_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, gate: Optio
     """Run bsa_gated_norm: h = x + alpha * gate * post(y), z = pre(h) * (1 + scale) + shift, for x, y [B, N, C] and
     modulations [B, C] or [B, F, C] (F frames of N / F tokens). Without y, h is x and is not written; without
     pre there is no z, whose dtype is y's (without y: that of out's z, branch_dtype or x's). Returns (h, z)."""
-    device = _cuda_device(x, "gated_norm")
+    what = "gated_norm"
+    device = _cuda_device(x, what)
     if x.dim() != 3:
         raise BsaError(ERR_SHAPE, f"gated_norm: x has {x.dim()} dimensions, expected 3")
-    shape = x.shape
-    _expect(x, shape, x.dtype, device, "gated_norm: x")
+    shape, dtype = x.shape, x.dtype
+    _expect(x, shape, dtype, device, what, "x")
     h, z = out if out is not None else (None, None)
     branch = y if y is not None else z
-    dtype = branch.dtype if branch is not None else branch_dtype or x.dtype
+    branch_dtype = branch.dtype if branch is not None else branch_dtype or dtype
     if y is not None:
-        _expect(y, shape, dtype, device, "gated_norm: y")
+        _expect(y, shape, branch_dtype, device, what, "y")
         if h is None:
-            h = torch.empty(shape, dtype=x.dtype, device=device)
+            h = torch.empty(shape, dtype=dtype, device=device)
         else:
-            _expect(h, shape, x.dtype, device, "gated_norm: out h")
+            _expect(h, shape, dtype, device, what, "out h")
     if pre is not None:
         if z is None:
-            z = torch.empty(shape, dtype=dtype, device=device)
+            z = torch.empty(shape, dtype=branch_dtype, device=device)
         else:
-            _expect(z, shape, dtype, device, "gated_norm: out z")
-    desc = _gated_desc(shape, device, x, z if z is not None else y if y is not None else x, alpha, post, pre, gate,
-                       scale, shift, "gated_norm")
-    _on(device, bsa_gated_norm, desc, _rows(x), _rows(y), _rows(h), _rows(z), stream=stream)
+            _expect(z, shape, branch_dtype, device, what, "out z")
+    desc, _ = _gated_desc(shape, device, _code(x, what), _CODES.get(branch_dtype, -1), alpha, post, pre, gate, scale,
+                          shift, what)
+    pack = _ROWS.pack
+    _run("bsa_gated_norm", load().bsa_gated_norm, device, stream, desc, pack(*_rows(x)), pack(*_rows(y)),
+         pack(*_rows(h)), pack(*_rows(z)))
     return h, z
 
 
@@ -494,49 +529,47 @@ def gated_norm_backward(dh: Optional[torch.Tensor], dz: Optional[torch.Tensor], 
     if first.dim() != 3:
         raise BsaError(ERR_SHAPE, f"{what}: {first.dim()} dimensions, expected 3")
     shape = first.shape
-    B, N, C = shape
-    stream_t = dh if dh is not None else h
-    branch_t = dz if dz is not None else y if y is not None else dh
-    if stream_t is None:
+    like = dh if dh is not None else h
+    if like is None:
         raise BsaError(ERR_INVALID_ARG, f"{what}: no h")
-    for t, like, name in ((dh, stream_t, "dh"), (h if pre is not None else None, stream_t, "h"), (dz, branch_t, "dz"),
-                          (y, branch_t, "y")):
-        if t is not None:
-            _expect(t, shape, like.dtype, device, f"{what}: {name}")
+    stream_dtype = like.dtype
+    branch_dtype = dz.dtype if dz is not None else y.dtype if y is not None else stream_dtype
+    if dh is not None:
+        _expect(dh, shape, stream_dtype, device, what, "dh")
+    if dz is not None:
+        _expect(dz, shape, branch_dtype, device, what, "dz")
     dx, dy = out if out is not None else (None, None)
-    g = GatedNormGradArgs()
-    g.dh, g.dz, g.y = _rows(dh), _rows(dz), _rows(y)
     if pre is not None:
-        g.h = _rows(h)
+        if h is not None:
+            _expect(h, shape, stream_dtype, device, what, "h")
         if dx is None:
-            dx = torch.empty(shape, dtype=stream_t.dtype, device=device)
+            dx = torch.empty(shape, dtype=stream_dtype, device=device)
         else:
-            _expect(dx, shape, stream_t.dtype, device, f"{what}: out dx")
-        g.dx = _rows(dx)
-    else:
-        dx = dh
+            _expect(dx, shape, stream_dtype, device, what, "out dx")
     if y is not None:
+        _expect(y, shape, branch_dtype, device, what, "y")
         if dy is None:
-            dy = torch.empty(shape, dtype=y.dtype, device=device)
+            dy = torch.empty(shape, dtype=branch_dtype, device=device)
         else:
-            _expect(dy, shape, y.dtype, device, f"{what}: out dy")
-        g.dy = _rows(dy)
+            _expect(dy, shape, branch_dtype, device, what, "out dy")
     else:
         dy = None
-    desc = _gated_desc(shape, device, stream_t, branch_t, alpha, post, pre, gate, scale, shift, what)
-    dmods = [None, None, None]
-    if gate is not None or scale is not None or shift is not None:
-        some = next(m for m in (gate, scale, shift) if m is not None)
-        rows = torch.empty((3, B, desc.F, C), dtype=some.dtype, device=device)
-        dmods = [None if m is None else r.view(m.shape) for m, r in zip((gate, scale, shift), rows.unbind(0))]
-        g.dgate, g.dscale, g.dshift = (_ptr(m) for m in dmods)
-    params = [p for n in (post, pre) for p in ((n.weight, n.bias) if n is not None else (None, None))]
-    dparams = [None, None, None, None]
-    if any(p is not None for p in params):
-        rows = torch.empty((4, C), dtype=torch.float32, device=device).unbind(0)
-        dparams = [None if p is None else r for p, r in zip(params, rows)]
-        g.dpost_weight, g.dpost_bias, g.dpre_weight, g.dpre_bias = (_ptr(p) for p in dparams)
-    if ws is None and (any(m is not None for m in dmods) or any(p is not None for p in dparams)):
-        ws = gated_norm_workspace(B, N, C, device)
-    _on(device, bsa_gated_norm_backward, desc, g, ws, _workspace_bytes(ws, device, what), stream=stream)
-    return GatedNormGrads(dx, dy, *dmods, *dparams)
+    desc, F = _gated_desc(shape, device, _code(like, what), _CODES.get(branch_dtype, -1), alpha, post, pre, gate, scale,
+                          shift, what)
+    dmods, dparams, at = [], [], []
+    for m in (gate, scale, shift):
+        d = None if m is None else torch.empty(m.shape, dtype=m.dtype, device=device)
+        dmods.append(d)
+        at.append(0 if d is None else d.data_ptr())
+    for n in (post, pre):
+        for p in (n.weight, n.bias) if n is not None else (None, None):
+            d = None if p is None else torch.empty_like(p)
+            dparams.append(d)
+            at.append(0 if d is None else d.data_ptr())
+    if ws is None and any(at):
+        ws = gated_norm_workspace(*shape, device)
+    args = _GRADS.pack(*_rows(dh), *_rows(dz), *(_rows(h) if pre is not None else _NO_ROWS), *_rows(y),
+                       *(_rows(dx) if pre is not None else _NO_ROWS), *_rows(dy), *at)
+    _run("bsa_gated_norm_backward", load().bsa_gated_norm_backward, device, stream, desc, args, _ptr(ws),
+         _workspace_bytes(ws, device, what))
+    return GatedNormGrads(dx if pre is not None else dh, dy, *dmods, *dparams)

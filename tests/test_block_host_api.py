@@ -71,6 +71,20 @@ def test_struct_layouts_match_the_header(tmp_path):
     assert [int(x) for x in got] == expected
 
 
+def test_packed_descriptors_match_the_structures():
+    """the helpers' byte layouts: every field of a mirror holds what was packed at its place"""
+    for fmt, mirror in ((ob._HEADS, ob.Heads), (ob._HEADS_GRAD, ob.HeadsGrad), (ob._ROWS, ob.Rows),
+                        (ob._DESC, ob.GatedNormDesc), (ob._GRADS, ob.GatedNormGradArgs)):
+        assert fmt.size == ctypes.sizeof(mirror)
+        n = len(fmt.unpack(bytes(fmt.size)))
+        got = mirror.from_buffer_copy(fmt.pack(*range(1, n + 1)))
+
+        def flat(v):
+            return [x for f, _ in v._fields_ for x in flat(getattr(v, f))] if isinstance(v, ctypes.Structure) else [v]
+
+        assert flat(got) == list(range(1, n + 1))
+
+
 def test_package_offers_the_helpers():
     for name in ("rotary", "rotary_backward", "rotary_plan", "gated_norm", "gated_norm_backward", "NormSpec",
                  "grid_positions"):

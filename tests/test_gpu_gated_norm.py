@@ -316,16 +316,19 @@ def test_some_gradients_alone():
     dh, dz = draw(gen(112), B, N, C, dt=BF16), draw(gen(113), B, N, C, dt=BF16)
     h = pkg.gated_norm(x, y, **kw)[0]
     full = pkg.gated_norm_backward(dh, dz, h, y, **kw)
-    desc = ob._gated_desc((B, N, C), h.device, h, y, kw["alpha"], kw["post"], kw["pre"], kw["gate"], kw["scale"],
-                          kw["shift"], "test")
+    mod = lambda m: ob.Modulation(m.data_ptr(), m.stride(0), 0)  # noqa: E731
+    norm = lambda n: ob.Norm(ob.NORM_RMS, n.eps, n.weight.data_ptr(), None)  # noqa: E731
+    rows = lambda t: ob.Rows(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+    desc = ob.GatedNormDesc(B, N, C, 1, bb.BF16, bb.BF16, bb.BF16, 1.0, norm(kw["post"]), norm(kw["pre"]), mod(kw["gate"]),
+                            mod(kw["scale"]), mod(kw["shift"]))
     ws = pkg.gated_norm_workspace(B, N, C)
     for name in NAMES:
         out = torch.zeros_like(getattr(full, name)) if getattr(full, name) is not None else None
         if out is None:
             continue
         g = ob.GatedNormGradArgs()
-        g.dh, g.dz, g.h, g.y = (ob._rows(t) for t in (dh, dz, h, y))
-        setattr(g, name, ob._rows(out) if name in ("dx", "dy") else out.data_ptr())
+        g.dh, g.dz, g.h, g.y = (rows(t) for t in (dh, dz, h, y))
+        setattr(g, name, rows(out) if name in ("dx", "dy") else out.data_ptr())
         ob.bsa_gated_norm_backward(desc, g, ws, ws.numel())
         torch.cuda.synchronize()
         assert torch.equal(out, getattr(full, name)), name
