@@ -17,7 +17,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "mask_kernels.cu", "fwd_tc.cu", "fwd_simt.cu", "noalloc.cu", "residual.cu",
            "exact_select.cu", "fwd_tokens.cu", "query_groups.cu", "block_api.cu", "rotary.cu", "gated_norm.cu",
            "gated_norm_backward.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "walk.cuh", "sync.cuh", "block_internal.h", "gated_norm.cuh"]
+HEADERS = ["internal.h", "ptx.cuh", "walk.cuh", "sync.cuh", "block_internal.h", "gated_norm.cuh", "pairs.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 

@@ -6,18 +6,21 @@
 //   y_a = u_a cos t - u_b sin t,  y_b = u_b cos t + u_a sin t.
 // Each element is read once and written once and takes about ten operations: HBM bounds it.
 //
-// Split: a CTA of 256 threads takes a tile of tokens, d / 16 threads to a token, 16 channels (8 pairs) each, and
-// walks over the heads of Q, then K, then V, so that a thread's eight angles, the one costly part, are computed once
-// for all heads of its token. The work, (tiles) x (heads) in that order, is cut into equal ranges, one per CTA that
-// fits on the device at once: no last wave that is only partly full.
+// Split: d / 16 threads hold one head of one token, 16 channels (8 pairs) each. A CTA of 256 threads takes a tile of
+// tokens and `together` heads at a time, and walks over the heads of Q, then K, then V, so that a thread's eight
+// angles, the one costly part, are computed once for all its heads of a token. Heads are taken together so that both
+// layouts are met in long runs: per token `together` heads side by side, per head the tile's tokens side by side.
+// The work, (tiles) x (groups of heads) in that order, is cut into equal ranges, one per CTA that fits on the device
+// at once: no last wave that is only partly full.
 //
-// Loads: each thread copies its own 16 channels of the next heads to shared memory with cp.async, kStages heads
+// Loads: each thread copies its own 16 channels of the next heads to shared memory with cp.async, some steps
 // ahead, and reads them back itself: loads stay in flight across heads and tiles, and no barrier guards the buffers.
 //
 // Angles: frequencies are 64-bit fixed point in turns, so pos * f modulo one turn is the low 64 bits of an integer
 // product. Its top 32 bits, as a signed fraction of half turns, go to sincospif in fp32: the angle is off by at most
 // 2^-25 half turns whatever the position, without fp64 or a slow argument reduction.
 #include "block_internal.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 #include <atomic>
@@ -27,7 +30,17 @@ namespace bsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStages = 4;  // heads in flight per thread (a power of two)
+// CTAs per SM, and steps in flight per thread, forward and backward. More of either is slower although the kernels
+// wait for memory: what is asked for at once then comes from more places than the memory keeps open (16640 tokens of 24
+// heads of 128 bf16, us: forward two CTAs of three, four, five stages 105.3, 101.9, 104.6, three CTAs of four 117.0,
+// one of eight 139.6; backward two CTAs of three and four stages 133.8 and 139.7, one of six 166.5).
+constexpr int kResident = 2, kForwardStages = 4, kBackwardStages = 3;
+
+// Heads side by side in a step: the largest power of two up to this that divides all the head counts. With one, a
+// token's row is read 256 bytes at a time, with eight, a head's rows are written 1 KB at a time, and either way the
+// memory's pages are opened more often (d = 128 bf16, 16640 tokens of 24 heads, us forward and backward: one 115.7
+// and 154.7, two 111.8 and 153.2, four 108.0 and 134.8, eight 117.9 and 155.8).
+constexpr int kTogether = 4;
 
 // What a thread holds of a head: two groups of 8 channels from c0 and c1 on, in which its pairs are
 //   INTERLEAVED: channels (2j, 2j + 1) of the groups (j < 4 of the first);  HALVES: channel j of the first and of the second
@@ -61,7 +74,7 @@ __device__ __forceinline__ Lane lane_of(int t, int rot)
 }
 
 template <int D, bool HALVES>
-__device__ __forceinline__ void angles(const bsa_rotary_plan &plan, const int32_t *pos, int t, unsigned turns,
+__device__ __forceinline__ void angles(const bsa_rotary_plan &plan, const int *pos, int t, unsigned turns,
                                        float (&cs)[8], float (&sn)[8])
 {
 #pragma unroll
@@ -70,30 +83,61 @@ __device__ __forceinline__ void angles(const bsa_rotary_plan &plan, const int32_
         sn[j] = 0.0f;
         if (turns >> j & 1u) {
             const int p = pair_of<D, HALVES>(t, j);
-            const uint64_t ph = plan.turns[p] * static_cast<uint64_t>(static_cast<int64_t>(pos[plan.axis[p]]));
+            const uint64_t ph = plan.turns[p] * static_cast<uint64_t>(static_cast<int64_t>(pos[plan.axis[p] * (kThreads * 16 / D)]));
             const float half_turns = static_cast<float>(static_cast<int32_t>(ph >> 32)) * 4.656612873077393e-10f;  // 2^-31
             sincospif(half_turns, &sn[j], &cs[j]);
         }
     }
 }
 
-// Turns the 16 channels of a thread by its angles (DIR = 1) or back (DIR = -1). Channels that do not
-// turn pass through as they are (no product with zero: an infinity stays one).
-template <bool HALVES, int DIR>
-__device__ __forceinline__ void turn(float (&u0)[8], float (&u1)[8], const float (&cs)[8], const float (&sn)[8],
-                                     unsigned turns)
+// A thread's 16 channels are held as pairs of neighbours, u[0..3] the first group, u[4..7] the second; channel() is
+// one of them as a float. Pair j's channels a and b:
+template <bool HALVES>
+__host__ __device__ constexpr int a_of(int j)
+{
+    return HALVES ? j : 2 * j;
+}
+template <bool HALVES>
+__host__ __device__ constexpr int b_of(int j)
+{
+    return HALVES ? 8 + j : 2 * j + 1;
+}
+
+__device__ __forceinline__ void channels_of(const f2 (&u)[8], float (&x)[16])
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float &a = HALVES ? u0[j] : (j < 4 ? u0[2 * j] : u1[2 * j - 8]);
-        float &b = HALVES ? u1[j] : (j < 4 ? u0[2 * j + 1] : u1[2 * j - 7]);
-        const float s = DIR * sn[j];
-        const float ya = a * cs[j] - b * s, yb = b * cs[j] + a * s;
-        if (turns >> j & 1u) {
-            a = ya;
-            b = yb;
+    for (int i = 0; i < 8; ++i) split(u[i], x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ void pairs_of(const float (&x)[16], f2 (&u)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = pair(x[2 * i], x[2 * i + 1]);
+}
+
+// Turns the thread's eight pairs by their angles (DIR = 1) or back (DIR = -1). Channels that do not turn pass through
+// as they are (no product with zero: an infinity stays one).
+template <bool HALVES, int DIR>
+__device__ __forceinline__ void turn(f2 (&u)[8], const float (&cs)[8], const float (&sn)[8], unsigned turns)
+{
+    float x[16], y[16];
+    channels_of(u, x);
+    if (turns == 0xffu) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int a = a_of<HALVES>(j), b = b_of<HALVES>(j);
+            y[a] = x[a] * cs[j] - x[b] * (DIR * sn[j]);
+            y[b] = x[b] * cs[j] + x[a] * (DIR * sn[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int a = a_of<HALVES>(j), b = b_of<HALVES>(j);
+            const bool on = turns >> j & 1u;
+            y[a] = on ? x[a] * cs[j] - x[b] * (DIR * sn[j]) : x[a];
+            y[b] = on ? x[b] * cs[j] + x[a] * (DIR * sn[j]) : x[b];
         }
     }
+    pairs_of(y, u);
 }
 
 template <int LANES>
@@ -104,60 +148,99 @@ __device__ __forceinline__ float lanes_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ void load_weight(const float *w, int c, float (&f)[8])
+__device__ __forceinline__ f2 sum_squares(const f2 (&u)[8])
 {
-    if (w) {
-        Vec8<float> v;
-        v.load(w, c);
-        v.unpack(f);
-    } else {
+    f2 q = mul2(u[0], u[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = 1.0f;
-    }
+    for (int i = 1; i < 8; ++i) q = fma2(u[i], u[i], q);
+    return q;
 }
 
-// A CTA's range of the work: units of one head of one tile of tokens, heads of Q, K, V in order within a tile.
-struct Work {
-    int64_t units;
-    int heads;  // of Q, K and V together
+// What a CTA keeps in shared memory besides the stages: the weights of Q and K (ones where there is none), and the
+// positions of the tokens of the tiles in flight, copied ahead like the heads by the threads that share the token.
+template <int D, int STAGES>
+struct Side {
+    float weight[2][D];
+    int pos[STAGES][BSA_ROTARY_MAX_AXES][kThreads * 16 / D];
+
+    __device__ __forceinline__ void weights(const RotaryArgs &a)
+    {
+        for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+            const float *w = a.norm ? a.t[i / D].weight : nullptr;
+            weight[i / D][i % D] = w ? w[i % D] : 1.0f;
+        }
+    }
+    __device__ __forceinline__ void positions(const RotaryArgs &a, int tile, int b, int n)
+    {
+        const int axis = threadIdx.x % (D / 16);  // at least four threads to a token
+        if (axis >= a.plan.n_axes) return;
+        const int32_t *from = a.positions + b * a.pos_batch + static_cast<int64_t>(n) * a.plan.n_axes + axis;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                         smem_u32(&pos[tile % STAGES][axis][threadIdx.x / (D / 16)])),
+                     "l"(from)
+                     : "memory");
+    }
+    // the positions of the thread's token, one axis every kThreads * 16 / D entries
+    __device__ __forceinline__ const int *at(int tile) const { return &pos[tile % STAGES][0][threadIdx.x / (D / 16)]; }
+    // 16 channels of a tensor's weight
+    __device__ __forceinline__ void read(int s, const Lane &l, f2 (&f)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(&weight[s][(i < 4 ? l.c0 : l.c1 - 8) + 2 * i]);
+            f[i] = pair(v.x, v.y);
+            f[i + 1] = pair(v.z, v.w);
+        }
+    }
 };
 
-// A thread's place in the work: the tile's token (clamped: shuffles take whole warps), the tensor and the head.
-struct Place {
-    int64_t tile;
-    int s, h;  // tensor, head
-    int b, n;
-    bool live;
+// The work: units of `together` heads of one tile of `tokens` tokens, heads of Q, K, V in order within a tile.
+struct Work {
+    int64_t units;
+    int groups;  // of heads, of Q, K and V
+    int together, tokens;
+};
 
-    __device__ __forceinline__ void tile_at(int64_t t, const RotaryArgs &a, int tokens, int mine)
+// A place in the work, the same for the whole CTA: tile, tensor, first head of the group.
+struct Place {
+    int tile, s, h;
+
+    __device__ __forceinline__ Place(int64_t unit, const Work &w, const RotaryArgs &a)
     {
-        tile = t;
-        const int64_t all = static_cast<int64_t>(a.B) * a.N;
-        int64_t token = t * tokens + mine;
-        live = token < all;
-        if (!live) token = all - 1;
-        b = static_cast<int>(token) / a.N;
-        n = static_cast<int>(token) % a.N;
-    }
-    __device__ __forceinline__ void start(int64_t unit, const Work &w, const RotaryArgs &a, int tokens, int mine)
-    {
-        tile_at(unit / w.heads, a, tokens, mine);
-        h = static_cast<int>(unit % w.heads);
+        tile = static_cast<int>(unit / w.groups);
+        h = static_cast<int>(unit % w.groups) * w.together;
         s = 0;
         while (h >= a.t[s].heads) h -= a.t[s++].heads;
     }
-    // to the next head; true where the tensor or the tile changed
-    __device__ __forceinline__ bool next(const RotaryArgs &a, int tokens, int mine)
+    // to the next group; true where the tensor or the tile changed
+    __device__ __forceinline__ bool next(const Work &w, const RotaryArgs &a)
     {
-        if (++h < a.t[s].heads) return false;
+        h += w.together;
+        if (h < a.t[s].heads) return false;
         h = 0;
         do {
             if (++s == 3) {
                 s = 0;
-                tile_at(tile + 1, a, tokens, mine);
+                ++tile;
             }
         } while (a.t[s].heads == 0);
         return true;
+    }
+};
+
+// A thread's token of a tile: (b, n), the last one for threads past it (shuffles take whole warps; they are not live)
+struct Token {
+    int b, n;
+    bool live;
+
+    __device__ __forceinline__ Token(int tile, int tokens, int mine, const RotaryArgs &a)
+    {
+        const int64_t at = static_cast<int64_t>(tile) * tokens + mine;
+        const int all = a.B * a.N;
+        live = at < all;
+        const int token = live ? static_cast<int>(at) : all - 1;
+        b = token / a.N;
+        n = token % a.N;
     }
 };
 
@@ -174,225 +257,242 @@ __device__ __forceinline__ void copy_groups(uint32_t to, const char *from, const
     }
 }
 
-// one group of 8 channels from the thread's place in a stage
+// 16 channels from the thread's place in a stage
 template <typename T>
-__device__ __forceinline__ void read_group(const char *at, int g, float (&f)[8])
+__device__ __forceinline__ void read_groups(const char *at, f2 (&u)[8])
 {
-    constexpr int PIECES = sizeof(T) / 2;
-    Vec8<T> v;
-    if constexpr (PIECES == 1) {
-        v.r = *reinterpret_cast<const uint4 *>(at + g * kThreads * 16);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const uint4 r = *reinterpret_cast<const uint4 *>(at + g * kThreads * 16);
+            u[4 * g] = widen(r.x), u[4 * g + 1] = widen(r.y), u[4 * g + 2] = widen(r.z), u[4 * g + 3] = widen(r.w);
+        }
     } else {
-        v.a = *reinterpret_cast<const float4 *>(at + 2 * g * kThreads * 16);
-        v.b = *reinterpret_cast<const float4 *>(at + (2 * g + 1) * kThreads * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 r = *reinterpret_cast<const float4 *>(at + i * kThreads * 16);
+            u[2 * i] = pair(r.x, r.y), u[2 * i + 1] = pair(r.z, r.w);
+        }
     }
-    v.unpack(f);
 }
 
+// and to global memory; rounded to nearest even where T is bf16
 template <typename T>
-__device__ __forceinline__ void write_group(char *to, int c, const float (&f)[8])
+__device__ __forceinline__ void write_groups(char *to, const Lane &l, const f2 (&u)[8])
 {
-    Vec8<T> v;
-    v.pack(f);
-    v.store(to, c);
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4 *>(to + l.c0 * 2) = make_uint4(narrow(u[0]), narrow(u[1]), narrow(u[2]), narrow(u[3]));
+        *reinterpret_cast<uint4 *>(to + l.c1 * 2) = make_uint4(narrow(u[4]), narrow(u[5]), narrow(u[6]), narrow(u[7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float4 r;
+            split(u[2 * i], r.x, r.y);
+            split(u[2 * i + 1], r.z, r.w);
+            *reinterpret_cast<float4 *>(to + (i < 2 ? l.c0 : l.c1 - 8) * 4 + 16 * i) = r;
+        }
+    }
 }
 
 template <typename T, int D, bool HALVES>
-__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const __grid_constant__ RotaryArgs a, Work w)
+__global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const __grid_constant__ RotaryArgs a, Work work)
 {
-    constexpr int LANES = D / 16, TOKENS = kThreads / LANES, STAGE = kThreads * 16 * sizeof(T);
+    constexpr int STAGES = kForwardStages, LANES = D / 16, STAGE = kThreads * 16 * sizeof(T);
     extern __shared__ __align__(16) char ring[];
-    const int t = threadIdx.x % LANES, mine = threadIdx.x / LANES;
+    const int t = threadIdx.x % LANES, mine = threadIdx.x / LANES % work.tokens, head = threadIdx.x / LANES / work.tokens;
     const Lane l = lane_of<D, HALVES>(t, a.plan.rot);
-    const int64_t u0 = w.units * blockIdx.x / gridDim.x, u1 = w.units * (blockIdx.x + 1) / gridDim.x;
+    const int64_t u0 = work.units * blockIdx.x / gridDim.x, u1 = work.units * (blockIdx.x + 1) / gridDim.x;
     const int count = static_cast<int>(u1 - u0);
     char *const own = ring + threadIdx.x * 16;
+    __shared__ __align__(16) Side<D, STAGES> side;
 
-    Place ahead;
-    ahead.start(u0, w, a, TOKENS, mine);
+    Place ahead(u0, work, a);
     const char *src = nullptr;
+    int tile_ahead = -1;
     auto enter_src = [&] {
         const HeadsView &v = a.t[ahead.s];
-        src = v.src + (ahead.b * v.src_b + ahead.n * v.src_n + ahead.h * v.src_h) * sizeof(T);
+        const Token k(ahead.tile, work.tokens, mine, a);
+        if (ahead.s < 2 && ahead.tile != tile_ahead) {
+            __syncwarp();  // every thread of the token has read the positions that are overwritten
+            side.positions(a, tile_ahead = ahead.tile, k.b, k.n);
+        }
+        src = v.src + (k.b * v.src_b + k.n * v.src_n + (ahead.h + head) * v.src_h) * sizeof(T);
     };
-    enter_src();
-    auto fetch = [&](int i) {  // a group of copies per head, empty past the end
+    bool fresh = true;  // src is to be found anew
+    auto fetch = [&](int i) {  // a group of copies per step, empty past the end; a tile's positions come with its first
         if (i < count) {
-            copy_groups<T>(smem_u32(own + (i % kStages) * STAGE), src, l);
-            src += a.t[ahead.s].src_h * sizeof(T);
-            if (ahead.next(a, TOKENS, mine)) enter_src();
+            if (fresh) enter_src();
+            copy_groups<T>(smem_u32(own + (i % STAGES) * STAGE), src, l);
+            src += work.together * a.t[ahead.s].src_h * sizeof(T);
+            fresh = ahead.next(work, a);
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 
-    Place here;
-    here.start(u0, w, a, TOKENS, mine);
-    float cs[8], sn[8], w0[8], w1[8];
+    Place here(u0, work, a);
+    bool live = false;
+    float cs[8], sn[8];
     char *dst = nullptr;
-    int64_t tile = -1;  // the one whose angles are here
+    int tile = -1;  // the one whose angles are here
     auto enter = [&] {
         const HeadsView &v = a.t[here.s];
-        dst = v.dst + (here.b * v.dst_b + here.n * v.dst_n + here.h * v.dst_h) * sizeof(T);
-        if (here.s == 2) return;
-        if (tile != here.tile) {
-            tile = here.tile;
-            angles<D, HALVES>(a.plan, a.positions + here.b * a.pos_batch + static_cast<int64_t>(here.n) * a.plan.n_axes, t,
-                              l.turns, cs, sn);
-        }
-        if (a.norm) {
-            load_weight(v.weight, l.c0, w0);
-            load_weight(v.weight, l.c1, w1);
-        }
+        const Token k(here.tile, work.tokens, mine, a);
+        live = k.live;
+        dst = v.dst + (k.b * v.dst_b + k.n * v.dst_n + (here.h + head) * v.dst_h) * sizeof(T);
+        if (here.s == 2 || tile == here.tile) return;
+        tile = here.tile;
+        __syncwarp();  // the token's positions were copied by its other threads
+        angles<D, HALVES>(a.plan, side.at(tile), t, l.turns, cs, sn);
     };
-    enter();
+    side.weights(a);
+    __syncthreads();
+    bool entered = false;
     for (int i = 0; i < count; ++i) {
-        fetch(i + kStages - 1);
-        cp_async_wait_group<kStages - 1>();
-        const char *at = own + (i % kStages) * STAGE;
-        float x0[8], x1[8];
-        read_group<T>(at, 0, x0);
-        read_group<T>(at, 1, x1);
+        fetch(i + STAGES - 1);
+        cp_async_wait_group<STAGES - 1>();
+        if (!entered) enter();
+        entered = true;
+        f2 u[8];
+        read_groups<T>(own + (i % STAGES) * STAGE, u);
         if (here.s < 2) {
             if (a.norm) {
-                float ss = 0.0f;
+                const f2 r = twice(rsqrtf(lanes_sum<LANES>(two(sum_squares(u))) * (1.0f / D) + a.eps));
+                f2 w[8];
+                side.read(here.s, l, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) ss += x0[j] * x0[j] + x1[j] * x1[j];
-                const float r = rsqrtf(lanes_sum<LANES>(ss) * (1.0f / D) + a.eps);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x0[j] *= r * w0[j];
-                    x1[j] *= r * w1[j];
-                }
+                for (int j = 0; j < 8; ++j) u[j] = mul2(u[j], mul2(r, w[j]));
             }
-            turn<HALVES, 1>(x0, x1, cs, sn, l.turns);
+            turn<HALVES, 1>(u, cs, sn, l.turns);
         }
-        if (here.live) {
-            write_group<T>(dst, l.c0, x0);
-            write_group<T>(dst, l.c1, x1);
-        }
-        dst += a.t[here.s].dst_h * sizeof(T);
-        if (i + 1 < count && here.next(a, TOKENS, mine)) enter();
+        if (live) write_groups<T>(dst, l, u);
+        dst += work.together * a.t[here.s].dst_h * sizeof(T);
+        entered = !here.next(work, a);
     }
 }
 
 // Backward. Two copies per head under the norm, dy and x. A thread sums the weight gradients of its 16 channels in
 // registers over a run of heads, then in its own place in shared memory over its CTA's work.
 template <typename T, int D, bool HALVES>
-__global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __grid_constant__ RotaryArgs a, Work w)
+__global__ void __launch_bounds__(kThreads, kResident) rotary_backward_kernel(const __grid_constant__ RotaryArgs a, Work work)
 {
-    constexpr int LANES = D / 16, TOKENS = kThreads / LANES, STAGE = kThreads * 16 * sizeof(T);
+    constexpr int STAGES = kBackwardStages, LANES = D / 16, STAGE = kThreads * 16 * sizeof(T);
     extern __shared__ __align__(16) char ring[];  // [stage][dy, then x with norm], then the weight gradients' sums
     __shared__ float sums[kThreads / 32][D];
-    const int t = threadIdx.x % LANES, mine = threadIdx.x / LANES;
+    const int t = threadIdx.x % LANES, mine = threadIdx.x / LANES % work.tokens, head = threadIdx.x / LANES / work.tokens;
     const Lane l = lane_of<D, HALVES>(t, a.plan.rot);
-    const int64_t u0 = w.units * blockIdx.x / gridDim.x, u1 = w.units * (blockIdx.x + 1) / gridDim.x;
+    const int64_t u0 = work.units * blockIdx.x / gridDim.x, u1 = work.units * (blockIdx.x + 1) / gridDim.x;
     const int count = static_cast<int>(u1 - u0), stage_bytes = a.norm ? 2 * STAGE : STAGE;
     char *const own = ring + threadIdx.x * 16;
-    float4 *const dw_at = reinterpret_cast<float4 *>(ring + kStages * stage_bytes) + threadIdx.x;  // [2][4] pieces
+    float4 *const dw_at = reinterpret_cast<float4 *>(ring + STAGES * stage_bytes) + threadIdx.x;  // [2][4] pieces
     if (a.partial) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw_at[i * kThreads] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
+    __shared__ __align__(16) Side<D, STAGES> side;
 
-    Place ahead;
-    ahead.start(u0, w, a, TOKENS, mine);
+    Place ahead(u0, work, a);
     const char *src = nullptr, *xsrc = nullptr;
+    int tile_ahead = -1;
     auto enter_src = [&] {
         const HeadsView &v = a.t[ahead.s];
-        src = v.src + (ahead.b * v.src_b + ahead.n * v.src_n + ahead.h * v.src_h) * sizeof(T);
-        xsrc = v.x + (ahead.b * v.x_b + ahead.n * v.x_n + ahead.h * v.x_h) * sizeof(T);
+        const Token k(ahead.tile, work.tokens, mine, a);
+        if (ahead.s < 2 && ahead.tile != tile_ahead) {
+            __syncwarp();  // every thread of the token has read the positions that are overwritten
+            side.positions(a, tile_ahead = ahead.tile, k.b, k.n);
+        }
+        src = v.src + (k.b * v.src_b + k.n * v.src_n + (ahead.h + head) * v.src_h) * sizeof(T);
+        xsrc = v.x + (k.b * v.x_b + k.n * v.x_n + (ahead.h + head) * v.x_h) * sizeof(T);
     };
-    enter_src();
+    bool fresh = true;  // src is to be found anew
     auto fetch = [&](int i) {
         if (i < count) {
+            if (fresh) enter_src();
             const HeadsView &v = a.t[ahead.s];
-            const uint32_t to = smem_u32(own + (i % kStages) * stage_bytes);
+            const uint32_t to = smem_u32(own + (i % STAGES) * stage_bytes);
             copy_groups<T>(to, src, l);
             if (a.norm && ahead.s < 2) copy_groups<T>(to + STAGE, xsrc, l);
-            src += v.src_h * sizeof(T);
-            xsrc += v.x_h * sizeof(T);
-            if (ahead.next(a, TOKENS, mine)) enter_src();
+            src += work.together * v.src_h * sizeof(T);
+            xsrc += work.together * v.x_h * sizeof(T);
+            fresh = ahead.next(work, a);
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 
-    Place here;
-    here.start(u0, w, a, TOKENS, mine);
-    float cs[8], sn[8], w0[8], w1[8], dw[16] = {};
+    Place here(u0, work, a);
+    bool live = false;
+    float cs[8], sn[8];
+    f2 w[8], dw[8] = {};
     char *dst = nullptr;
-    int64_t tile = -1;
+    int tile = -1;
     auto enter = [&] {
         const HeadsView &v = a.t[here.s];
-        dst = v.dst + (here.b * v.dst_b + here.n * v.dst_n + here.h * v.dst_h) * sizeof(T);
+        const Token k(here.tile, work.tokens, mine, a);
+        live = k.live;
+        dst = v.dst + (k.b * v.dst_b + k.n * v.dst_n + (here.h + head) * v.dst_h) * sizeof(T);
         if (here.s == 2) return;
         if (tile != here.tile) {
             tile = here.tile;
-            angles<D, HALVES>(a.plan, a.positions + here.b * a.pos_batch + static_cast<int64_t>(here.n) * a.plan.n_axes, t,
-                              l.turns, cs, sn);
+            __syncwarp();  // the token's positions were copied by its other threads
+            angles<D, HALVES>(a.plan, side.at(tile), t, l.turns, cs, sn);
         }
-        if (a.norm) {
-            load_weight(v.weight, l.c0, w0);
-            load_weight(v.weight, l.c1, w1);
-        }
+        side.read(here.s, l, w);
     };
     auto leave = [&](int s) {  // the end of a run of heads of one tensor
         if (!a.partial || s == 2) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float4 v = dw_at[(4 * s + i) * kThreads];
-            v.x += dw[4 * i], v.y += dw[4 * i + 1], v.z += dw[4 * i + 2], v.w += dw[4 * i + 3];
+            float d[4];
+            split(dw[2 * i], d[0], d[1]);
+            split(dw[2 * i + 1], d[2], d[3]);
+            v.x += d[0], v.y += d[1], v.z += d[2], v.w += d[3];
             dw_at[(4 * s + i) * kThreads] = v;
-            dw[4 * i] = dw[4 * i + 1] = dw[4 * i + 2] = dw[4 * i + 3] = 0.0f;
+            dw[2 * i] = dw[2 * i + 1] = twice(0.0f);
         }
     };
-    enter();
+    side.weights(a);
+    __syncthreads();
+    bool entered = false;
     for (int i = 0; i < count; ++i) {
-        fetch(i + kStages - 1);
-        cp_async_wait_group<kStages - 1>();
-        const char *at = own + (i % kStages) * stage_bytes;
-        float g0[8], g1[8];
-        read_group<T>(at, 0, g0);
-        read_group<T>(at, 1, g1);
+        fetch(i + STAGES - 1);
+        cp_async_wait_group<STAGES - 1>();
+        if (!entered) enter();
+        entered = true;
+        const char *at = own + (i % STAGES) * stage_bytes;
+        f2 g[8];
+        read_groups<T>(at, g);
         if (here.s < 2) {
-            turn<HALVES, -1>(g0, g1, cs, sn, l.turns);
+            turn<HALVES, -1>(g, cs, sn, l.turns);
             if (a.norm) {
-                float x0[8], x1[8];
-                read_group<T>(at + STAGE, 0, x0);
-                read_group<T>(at + STAGE, 1, x1);
-                float ss = 0.0f, sv = 0.0f;
+                f2 x[8], sv = twice(0.0f);
+                read_groups<T>(at + STAGE, x);
+                const float ss = two(sum_squares(x));
+                f2 p[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    ss += x0[j] * x0[j] + x1[j] * x1[j];
-                    sv += g0[j] * w0[j] * x0[j] + g1[j] * w1[j] * x1[j];
+                    p[j] = mul2(g[j], x[j]);
+                    sv = fma2(p[j], w[j], sv);
                 }
                 const float r = rsqrtf(lanes_sum<LANES>(ss) * (1.0f / D) + a.eps);
-                const float m = lanes_sum<LANES>(sv) * (1.0f / D) * r * r;
-                const float rl = here.live ? r : 0.0f;  // the clamped token is not counted again
+                const float m = lanes_sum<LANES>(two(sv)) * (1.0f / D) * r * r;
+                const f2 rr = twice(r), mr = twice(-m * r);
+                if (live) {  // the clamped token is not counted again
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (here.live) {
-                        dw[j] += g0[j] * (x0[j] * rl);
-                        dw[8 + j] += g1[j] * (x1[j] * rl);
-                    }
-                    g0[j] = r * (g0[j] * w0[j] - x0[j] * m);
-                    g1[j] = r * (g1[j] * w1[j] - x1[j] * m);
+                    for (int j = 0; j < 8; ++j) dw[j] = fma2(p[j], rr, dw[j]);
                 }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = fma2(mul2(g[j], w[j]), rr, mul2(x[j], mr));
             }
         }
-        if (here.live) {
-            write_group<T>(dst, l.c0, g0);
-            write_group<T>(dst, l.c1, g1);
-        }
-        dst += a.t[here.s].dst_h * sizeof(T);
+        if (live) write_groups<T>(dst, l, g);
+        dst += work.together * a.t[here.s].dst_h * sizeof(T);
         const int s = here.s;
-        if (i + 1 == count || here.next(a, TOKENS, mine)) {
-            leave(s);
-            if (i + 1 < count) enter();
-        }
+        entered = !here.next(work, a);
+        if (i + 1 == count || !entered) leave(s);
     }
 
     if (a.partial == nullptr) return;
@@ -444,10 +544,13 @@ __global__ void __launch_bounds__(1024) rotary_dweight_kernel(const float *parti
 template <int D>
 int work_of(const RotaryArgs &a, int sms, int resident, Work *w)
 {
-    constexpr int TOKENS = kThreads / (D / 16);
-    const int64_t tiles = (static_cast<int64_t>(a.B) * a.N + TOKENS - 1) / TOKENS;
-    w->heads = a.t[0].heads + a.t[1].heads + a.t[2].heads;
-    w->units = tiles * w->heads;
+    w->together = kTogether;
+    for (const HeadsView &t : a.t)
+        while (t.heads % w->together != 0) w->together /= 2;
+    w->tokens = kThreads / (D / 16) / w->together;
+    const int64_t tiles = (static_cast<int64_t>(a.B) * a.N + w->tokens - 1) / w->tokens;
+    w->groups = (a.t[0].heads + a.t[1].heads + a.t[2].heads) / w->together;
+    w->units = tiles * w->groups;
     const int64_t ctas = static_cast<int64_t>(sms) * resident;
     return static_cast<int>(w->units < ctas ? w->units : ctas);
 }
@@ -472,12 +575,12 @@ template <typename T, int D, bool HALVES>
 bsa_status forward(const RotaryArgs &a, int sms, cudaStream_t st)
 {
     auto kern = rotary_kernel<T, D, HALVES>;
-    constexpr int SMEM = kStages * kThreads * 16 * sizeof(T);
+    constexpr int SMEM = kThreads * kForwardStages * 16 * sizeof(T);
     static std::atomic<uint64_t> done{0};
     const bsa_status ok = allow_smem(kern, SMEM, done);
     if (ok != BSA_OK) return ok;
     Work w;
-    const int ctas = work_of<D>(a, sms, 3, &w);
+    const int ctas = work_of<D>(a, sms, kResident, &w);
     kern<<<ctas, kThreads, SMEM, st>>>(a, w);
     return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
@@ -488,13 +591,13 @@ bsa_status backward(const RotaryArgs &a, int sms, cudaStream_t st)
     auto kern = rotary_backward_kernel<T, D, HALVES>;
     constexpr int STAGE = kThreads * 16 * sizeof(T), SUMS = kThreads * 128;
     static std::atomic<uint64_t> done{0};
-    const bsa_status ok = allow_smem(kern, kStages * 2 * STAGE + SUMS, done);
+    constexpr int RESIDENT = sizeof(T) == 2 ? kResident : 1;  // fp32: 160 KB of shared memory per CTA
+    const bsa_status ok = allow_smem(kern, kBackwardStages * 2 * STAGE + SUMS, done);
     if (ok != BSA_OK) return ok;
     Work w;
-    const int resident = sizeof(T) == 2 ? 2 : 1;  // fp32: 160 KB of shared memory per CTA
-    int ctas = work_of<D>(a, sms, resident, &w);
+    int ctas = work_of<D>(a, sms, RESIDENT, &w);
     if (ctas > kRotaryMaxCtas) ctas = kRotaryMaxCtas;
-    kern<<<ctas, kThreads, kStages * (a.norm ? 2 : 1) * STAGE + (a.partial ? SUMS : 0), st>>>(a, w);
+    kern<<<ctas, kThreads, kBackwardStages * (a.norm ? 2 : 1) * STAGE + (a.partial ? SUMS : 0), st>>>(a, w);
     if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     if (a.partial && !pdl_launch(rotary_dweight_kernel, dim3(2 * D / 32), 1024, 0, st, a.partial, ctas, D, a.t[0].dweight,
                                  a.t[1].dweight))
