@@ -80,6 +80,8 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
               at_y = at_dz + (pre ? K * threads * BB : 0), stage_bytes = at_y + (has_y ? K * threads * BB : 0);
     Row<K, P, SUB, LN> rw(C, tpr, buf);
     const Wants want = wants_of(a);
+    if (a.partial && blockIdx.x == 0)
+        for (int i = threadIdx.x; i < kNormTickets; i += threads) a.tickets[i] = 0;
 
     // a CTA is one worker, unless lanes of a warp hold several rows: all that depends on the row alone is uniform
     const int worker = SUB ? blockIdx.x * (threads / tpr) + threadIdx.x / tpr : blockIdx.x;
@@ -396,123 +398,158 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     }
 }
 
-// Adds the workers' slots: 32 channels per CTA (four per thread), kSumSlices slices of the workers. blockIdx.y == 0:
-// the weights' sums over all workers; blockIdx.y > 0: one group.
-constexpr int kSumSlices = 64;
+// Adds the workers' slots, 32 channels per CTA (four per thread), slices of 8 threads each taking every so many-th
+// worker. Items, blockIdx.y:
+//   long groups     group y: its modulations' gradients; its sums, weighted for the parameters that all groups share, go
+//                   into the third slot of worker y, and the last CTA of the channels adds those of all groups
+//   short groups    0: the weights' third slots over all workers; y > 0: a group that several workers share
+constexpr int kMaxSlices = 64;
 
-__device__ __forceinline__ void add_slot(const float *p, int C, float4 (&v)[4])
+struct Quad {
+    float4 v[4];  // A, S, P, Q of four channels
+};
+
+// the sums of slots[w * stride] over w = w0 .. w1, this thread's share
+__device__ __forceinline__ void add_slots(const float *slots, int64_t stride, int C, int w0, int w1, Quad &q)
 {
+    const int slices = blockDim.x / 8;
+#pragma unroll 2
+    for (int w = w0 + static_cast<int>(threadIdx.x) / 8; w <= w1; w += slices) {
+        const float *p = slots + w * stride;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float4 q = *reinterpret_cast<const float4 *>(p + k * C);
-        v[k].x += q.x, v[k].y += q.y, v[k].z += q.z, v[k].w += q.w;
+        for (int k = 0; k < 4; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(p + k * C);
+            q.v[k].x += x.x, q.v[k].y += x.y, q.v[k].z += x.z, q.v[k].w += x.w;
+        }
     }
 }
 
-// the same, with A and S times 1 + scale and P and Q times gate of group g
-__device__ __forceinline__ void add_slot_weighted(const NormArgs &a, int g, int c, const float *p, float4 (&v)[4])
+// the CTA's sums of all slices, in the order of the slices: s[k] of channel threadIdx.x, for threads below 32
+__device__ __forceinline__ void join_slices(Quad &q, float (*part)[4][32], float (&s)[4])
 {
-    const bsa_gated_norm_desc &d = a.d;
-    const int b = g / d.F, f = g % d.F;
-    f2 m[2][2], q[2];
-    fill(1.0f, m[0]);
-    fill(1.0f, m[1]);
-    if (d.scale.ptr) times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, m[0]);
-    if (d.gate.ptr) load_mod(d.gate.ptr, d.mod_dt, b * d.gate.batch + f * d.gate.frame + c, m[1]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        Unit<float, 2>::get(p + k * d.C, q);
-        f2 x = fma2(q[0], m[k / 2][0], pair(v[k].x, v[k].y)), y = fma2(q[1], m[k / 2][1], pair(v[k].z, v[k].w));
-        split(x, v[k].x, v[k].y);
-        split(y, v[k].z, v[k].w);
-    }
-}
-
-__global__ void __launch_bounds__(8 * kSumSlices) gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg,
-                                                                         int64_t n_groups)
-{
-    __shared__ __align__(16) float part[kSumSlices / 4][4][32];
-    grid_dependency_wait();
-    const bsa_gated_norm_desc &d = a.d;
-    const int C = d.C;
-    const int64_t stride = gated_norm_worker_floats(C);
-    int w0 = 0, w1 = rg.workers - 1;
-    int64_t group = -1;
-    if (blockIdx.y == 0) {
-        if (!wants_of(a).weights) return;
-    } else {
-        // the group itself where there are at most as many groups as workers; else the one that worker y - 1's
-        // range begins inside
-        const int i = blockIdx.y - 1;
-        group = n_groups <= rg.workers ? i : rg.first(i) / rg.per_group;
-        w0 = rg.worker_of(group * rg.per_group);
-        w1 = rg.worker_of((group + 1) * rg.per_group - 1);
-        if (!rg.long_groups) {
-            if (w0 == w1) return;                              // written by its worker
-            if (n_groups > rg.workers && i != w0 + 1) return;  // one CTA per group
-        }
-    }
-    const int lane = threadIdx.x % 8, c = blockIdx.x * 32 + 4 * lane;
-    float4 v[4] = {};
-    if (c < C) {
-        const float *const slots = a.partial + c;
-        if (group < 0 && rg.long_groups) {
-#pragma unroll 2
-            for (int w = w0 + threadIdx.x / 8; w <= w1; w += kSumSlices) {
-                const int g0 = rg.first(w) / rg.per_group, g1 = (rg.first(w + 1) - 1) / rg.per_group;
-                add_slot_weighted(a, g0, c, slots + w * stride, v);
-                if (g1 != g0) add_slot_weighted(a, g1, c, slots + w * stride + 4 * C, v);
-            }
-        } else {
-#pragma unroll 2
-            for (int w = w0 + threadIdx.x / 8; w <= w1; w += kSumSlices) {
-                // a group is the first in the ranges of its workers but, perhaps, that of the first of them
-                const int slot = group < 0 ? 8 : w == w0 && rg.first(w) / rg.per_group != group ? 4 : 0;
-                add_slot(slots + w * stride + slot * C, C, v);
-            }
-        }
-    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
         for (int o = 8; o < 32; o <<= 1) {
-            v[k].x += __shfl_xor_sync(0xffffffffu, v[k].x, o);
-            v[k].y += __shfl_xor_sync(0xffffffffu, v[k].y, o);
-            v[k].z += __shfl_xor_sync(0xffffffffu, v[k].z, o);
-            v[k].w += __shfl_xor_sync(0xffffffffu, v[k].w, o);
+            q.v[k].x += __shfl_xor_sync(0xffffffffu, q.v[k].x, o);
+            q.v[k].y += __shfl_xor_sync(0xffffffffu, q.v[k].y, o);
+            q.v[k].z += __shfl_xor_sync(0xffffffffu, q.v[k].z, o);
+            q.v[k].w += __shfl_xor_sync(0xffffffffu, q.v[k].w, o);
         }
-        if (threadIdx.x % 32 < 8) *reinterpret_cast<float4 *>(&part[threadIdx.x / 32][k][4 * lane]) = v[k];
+        if (threadIdx.x % 32 < 8) *reinterpret_cast<float4 *>(&part[threadIdx.x / 32][k][4 * (threadIdx.x % 8)]) = q.v[k];
     }
     __syncthreads();
-    const int at = threadIdx.x % 32, ch = blockIdx.x * 32 + at;
-    if (threadIdx.x < 128) {
-        float s = 0.0f;
+    if (threadIdx.x < 32) {
 #pragma unroll
-        for (int i = 0; i < kSumSlices / 4; ++i) s += part[i][threadIdx.x / 32][at];
-        part[0][threadIdx.x / 32][at] = s;
+        for (int k = 0; k < 4; ++k) {
+            s[k] = 0.0f;
+            for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s[k] += part[i][k][threadIdx.x];
+        }
     }
     __syncthreads();
-    if (threadIdx.x >= 32 || ch >= C) return;
-    const float sA = part[0][0][at], sS = part[0][1][at], sP = part[0][2][at], sQ = part[0][3][at];
-    if (group < 0) {
-        const float alpha = rg.long_groups ? d.alpha : 1.0f;  // the third slots have it already
-        if (a.dpre_b) a.dpre_b[ch] = sA;
-        if (a.dpre_w) a.dpre_w[ch] = sS;
-        if (a.dpost_b) a.dpost_b[ch] = alpha * sP;
-        if (a.dpost_w) a.dpost_w[ch] = alpha * sQ;
+}
+
+__device__ __forceinline__ float modulation(const bsa_modulation &m, int dt, int b, int f, int c)
+{
+    const int64_t at = b * m.batch + f * m.frame + c;
+    return dt == BSA_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(m.ptr)[at])
+                          : static_cast<const float *>(m.ptr)[at];
+}
+
+__global__ void __launch_bounds__(8 * kMaxSlices, 2) gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg,
+                                                                            int64_t n_groups)
+{
+    __shared__ __align__(16) float part[kMaxSlices / 4][4][32];
+    __shared__ int last;
+    grid_dependency_wait();
+    const bsa_gated_norm_desc &d = a.d;
+    const int C = d.C;
+    const int64_t stride = gated_norm_worker_floats(C);
+    const Wants want = wants_of(a);
+    int w0 = 0, w1 = rg.workers - 1;
+    int64_t group = -1;
+    if (rg.long_groups) {
+        group = blockIdx.y;
+    } else if (blockIdx.y > 0) {
+        // the group itself where there are at most as many groups as workers; else the one that worker y - 1's
+        // range begins inside
+        const int i = blockIdx.y - 1;
+        group = n_groups <= rg.workers ? i : rg.first(i) / rg.per_group;
+    } else if (!want.weights) {
         return;
     }
-    auto put = [&](char *p, float x) {
-        const int64_t i = group * C + ch;
-        if (d.mod_dt == BSA_BF16)
-            reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
-        else
-            reinterpret_cast<float *>(p)[i] = x;
+    if (group >= 0) {
+        w0 = rg.worker_of(group * rg.per_group);
+        w1 = rg.worker_of((group + 1) * rg.per_group - 1);
+        if (!rg.long_groups) {
+            if (w0 == w1) return;                                                         // written by its worker
+            if (n_groups > rg.workers && static_cast<int>(blockIdx.y) - 1 != w0 + 1) return;  // one CTA per group
+        }
+    }
+    const int c = blockIdx.x * 32 + 4 * (threadIdx.x % 8), ch = blockIdx.x * 32 + threadIdx.x;
+    const bool mine = threadIdx.x < 32 && ch < C;
+    float *const slots = a.partial + (c < C ? c : 0);
+    Quad q = {};
+    float s[4];
+    if (group < 0) {
+        add_slots(slots + 8 * C, stride, C, w0, w1, q);
+    } else {
+        // a group is the first in the ranges of its workers but, perhaps, that of the first of them
+        if (rg.first(w0) / rg.per_group != group) {
+            if (threadIdx.x < 8) add_slots(slots + 4 * C, stride, C, w0, w0, q);
+            ++w0;
+        }
+        add_slots(slots, stride, C, w0, w1, q);
+    }
+    join_slices(q, part, s);
+    auto put_weights = [&] {
+        if (a.dpre_b) a.dpre_b[ch] = s[0];
+        if (a.dpre_w) a.dpre_w[ch] = s[1];
+        if (a.dpost_b) a.dpost_b[ch] = s[2];
+        if (a.dpost_w) a.dpost_w[ch] = s[3];
     };
-    auto by = [&](const float *w, float one, float x) { return (w ? w[ch] : one) * x; };
-    if (a.dshift) put(a.dshift, sA);
-    if (a.dscale) put(a.dscale, by(d.pre.weight, 1.0f, sS) + by(d.pre.bias, 0.0f, sA));
-    if (a.dgate) put(a.dgate, d.alpha * (by(d.post.weight, 1.0f, sQ) + by(d.post.bias, 0.0f, sP)));
+    if (group < 0) {
+        if (mine) put_weights();
+        return;
+    }
+    if (mine) {
+        auto put = [&](char *p, float x) {
+            const int64_t i = group * C + ch;
+            if (d.mod_dt == BSA_BF16)
+                reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
+            else
+                reinterpret_cast<float *>(p)[i] = x;
+        };
+        auto by = [&](const float *w, float one, float x) { return (w ? w[ch] : one) * x; };
+        if (a.dshift) put(a.dshift, s[0]);
+        if (a.dscale) put(a.dscale, by(d.pre.weight, 1.0f, s[1]) + by(d.pre.bias, 0.0f, s[0]));
+        if (a.dgate) put(a.dgate, d.alpha * (by(d.post.weight, 1.0f, s[3]) + by(d.post.bias, 0.0f, s[2])));
+    }
+    if (!want.weights || !rg.long_groups) return;
+    const int b = static_cast<int>(group) / d.F, f = static_cast<int>(group) % d.F;
+    if (mine) {
+        const float m = d.scale.ptr ? 1.0f + modulation(d.scale, d.mod_dt, b, f, ch) : 1.0f;
+        const float g = d.alpha * (d.gate.ptr ? modulation(d.gate, d.mod_dt, b, f, ch) : 1.0f);
+        s[0] *= m, s[1] *= m, s[2] *= g, s[3] *= g;
+        if (n_groups == 1) {
+            put_weights();
+            return;
+        }
+        float *const to = a.partial + group * stride + 8 * C + ch;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to[k * C] = s[k];
+    }
+    if (n_groups == 1) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(a.tickets + blockIdx.x, 1u) == gridDim.y - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    q = Quad{};
+    add_slots(slots + 8 * C, stride, C, 0, static_cast<int>(n_groups) - 1, q);
+    join_slices(q, part, s);
+    if (mine) put_weights();
 }
 
 template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST, bool LN>
@@ -531,9 +568,13 @@ bsa_status backward(const NormArgs &a, int sms, cudaStream_t st)
     if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     if (a.partial == nullptr) return BSA_OK;
     const int64_t n_groups = static_cast<int64_t>(a.d.B) * a.d.F;
-    const int64_t items = n_groups < s.rg.workers ? n_groups : s.rg.workers;
-    const dim3 grid((a.d.C + 31) / 32, static_cast<unsigned>(items + 1));
-    return pdl_launch(gated_norm_sums_kernel, grid, 8 * kSumSlices, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
+    const int64_t items = s.rg.long_groups ? n_groups : (n_groups < s.rg.workers ? n_groups : s.rg.workers) + 1;
+    // as many slices as a group has workers
+    int slices = kMaxSlices;
+    if (s.rg.long_groups)
+        while (slices > 8 && slices / 2 >= s.rg.workers / n_groups + 2) slices /= 2;
+    const dim3 grid((a.d.C + 31) / 32, static_cast<unsigned>(items));
+    return pdl_launch(gated_norm_sums_kernel, grid, 8 * slices, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
 }
 
 }  // namespace
