@@ -157,15 +157,17 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
 // apart and met in the same memory channels (65536 rows of 2048 channels: 184 against 174 us).
 struct Ranges {
     int rows, workers;
-    uint64_t step;
+    uint64_t step, per_step;
     int per_group;    // rows that share a modulation
     int long_groups;  // no range is longer than a group: it touches two groups at most
 
     __host__ __device__ int first(int w) const { return static_cast<int>(static_cast<uint64_t>(w) * step >> 32); }
     __host__ __device__ int most() const { return static_cast<int>(step >> 32) + 1; }  // no range is longer
+    // floor(x / step) for x = (row + 1) 2^32 - 1, by the reciprocal floor(2^64 / step): at most one too small
     __device__ int worker_of(int row) const
     {
-        return static_cast<int>(((static_cast<uint64_t>(row) + 1 << 32) - 1) / step);
+        const int w = static_cast<int>(__umul64hi((static_cast<uint64_t>(row) + 1 << 32) - 1, per_step));
+        return w + (first(w + 1) <= row);
     }
 };
 
@@ -406,6 +408,7 @@ inline Shape shape_of(const bsa_gated_norm_desc &d, int v, int regs, int sms, in
     const int64_t fill = static_cast<int64_t>(sms) * resident * per_cta, most = gated_norm_max_workers(s.rg.rows, d.C);
     s.rg.workers = static_cast<int>(fill < most ? fill : most);
     s.rg.step = ((static_cast<uint64_t>(s.rg.rows) << 32) + s.rg.workers - 1) / s.rg.workers;
+    s.rg.per_step = UINT64_MAX / s.rg.step;
     s.rg.long_groups = s.rg.per_group >= s.rg.most();
     s.ctas = (s.rg.workers + per_cta - 1) / per_cta;
     return s;

@@ -533,15 +533,17 @@ __global__ void __launch_bounds__(8 * kMaxSlices, 2) gated_norm_sums_kernel(cons
         s[0] *= m, s[1] *= m, s[2] *= g, s[3] *= g;
         if (n_groups == 1) {
             put_weights();
-            return;
-        }
-        float *const to = a.partial + group * stride + 8 * C + ch;
+        } else {
+            float *const to = a.partial + group * stride + 8 * C + ch;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) to[k * C] = s[k];
+            for (int k = 0; k < 4; ++k) to[k * C] = s[k];
+        }
     }
     if (n_groups == 1) return;
-    __threadfence();
-    __syncthreads();
+    if (threadIdx.x < 32) {  // the writers above
+        __threadfence();
+        __syncwarp();
+    }
     if (threadIdx.x == 0) last = atomicAdd(a.tickets + blockIdx.x, 1u) == gridDim.y - 1;
     __syncthreads();
     if (!last) return;
