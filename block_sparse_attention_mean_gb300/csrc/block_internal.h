@@ -54,9 +54,9 @@ struct NormArgs {
     uint32_t *tickets;  // behind them: how many CTAs are done with 32 channels (zeroed by the first kernel)
 };
 
-// Backward: the rows are cut into contiguous ranges, one per worker (the threads that hold a row).
-// kNormMaxThreads bounds the workers, and with them the workspace, whatever the device.
-constexpr int64_t kNormMaxThreads = 152 * 1024;
+// Backward: the rows are cut into contiguous ranges, one per worker (a CTA). kNormMaxThreads bounds the
+// workers, and with them the workspace, whatever the device.
+constexpr int64_t kNormMaxThreads = 152 * 512;
 int64_t gated_norm_max_workers(int64_t rows, int C);
 // floats of partial sums per worker: two unfinished groups of 4 sums, and 4 sums for weights
 __host__ __device__ inline int64_t gated_norm_worker_floats(int C) { return int64_t(12) * C; }

@@ -21,7 +21,7 @@
 namespace bsa {
 namespace {
 
-template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST, bool LN>
+template <typename TS, typename TB, int REGS, bool MULTI, bool POST, bool LN>
 __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ NormArgs a, Ranges rg, int tpr)
 {
     constexpr int E = 16 / sizeof(TS), P = E / 2, K = 8 * V / E, XB = E * sizeof(TS), YB = E * sizeof(TB);
@@ -31,11 +31,11 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
     const bsa_gated_norm_desc &d = a.d;
     const bool branch = a.y.p != nullptr, pre = d.pre.kind != BSA_NORM_NONE;
     const int threads = blockDim.x, at_y = K * threads * XB, stage_bytes = at_y + (branch ? K * threads * YB : 0);
-    Row<K, P, SUB, LN> rw(d.C, tpr, buf);
+    Row<K, P, MULTI, LN> rw(d.C, tpr, buf);
 
     // a CTA is one worker, unless lanes of a warp hold several rows: all that depends on the row alone is uniform
-    const int worker = SUB ? blockIdx.x * (threads / tpr) + threadIdx.x / tpr : blockIdx.x;
-    const bool some = !SUB || worker < rg.workers;
+    const int worker = MULTI ? blockIdx.x * (threads / tpr) + threadIdx.x / tpr : blockIdx.x;
+    const bool some = !MULTI || worker < rg.workers;
     const int first = some ? rg.first(worker) : 0, count = some ? rg.first(worker + 1) - first : 0;
     const int b0 = first / d.N, n0 = first % d.N;
     Walk x(a.x, b0, n0, sizeof(TS)), y(a.y, b0, n0, sizeof(TB)), h(a.h, b0, n0, sizeof(TS)), z(a.z, b0, n0, sizeof(TB));
@@ -109,59 +109,69 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
     if (count > 0) factors(group);
 
     // workers of whole warps end on their own; lanes that share a warp go on with it, writing nothing
-    const int rounds = SUB ? rg.most() : count;
+    const int rounds = MULTI ? rg.most() : count;
     for (int i = 0; i < rounds; ++i) {
         fetch(i + STAGES - 1 < count);
         cp_async_wait_group<STAGES - 1>();  // row i is here
-        const bool live = !SUB || i < count;
+        const bool live = !MULTI || i < count;
         if (live && left == 0) {
             left = rg.per_group;
             factors(++group);
         }
         --left;
-        f2 t[1][K][P];
+        f2 t[K][P];
 #pragma unroll
-        for (int k = 0; k < K; ++k) Unit<TS, P>::get(mine_x + from * stage_bytes + k * threads * XB, t[0][k]);
+        for (int k = 0; k < K; ++k) Unit<TS, P>::get(mine_x + from * stage_bytes + k * threads * XB, t[k]);
         if (branch) {
-            f2 m[1][K][P], r = twice(1.0f);
+            f2 m[K][P], r = twice(1.0f);
 #pragma unroll
-            for (int k = 0; k < K; ++k) Unit<TB, P>::get(mine_y + from * stage_bytes + k * threads * YB, m[0][k]);
+            for (int k = 0; k < K; ++k) Unit<TB, P>::get(mine_y + from * stage_bytes + k * threads * YB, m[k]);
             if (POST) {
                 float mean[1], square[1];
                 const int kind[1] = {d.post.kind};
-                rw.stats(m, kind, mean, square);
+                rw.stats(
+                    [&](int, int k, f2(&v)[P]) {
+#pragma unroll
+                        for (int j = 0; j < P; ++j) v[j] = m[k][j];
+                    },
+                    kind, mean, square);
                 r = twice(rsqrtf(square[0] + d.post.eps));
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     const f2 off = rw.minus(mean[0], k);
 #pragma unroll
                     for (int j = 0; j < P; ++j) {
-                        t[0][k][j] = add2(t[0][k][j], h0[k][j]);
-                        t[0][k][j] = fma2(rw.centred(m[0][k][j], off), mul2(r, h1[k][j]), t[0][k][j]);
+                        t[k][j] = add2(t[k][j], h0[k][j]);
+                        t[k][j] = fma2(rw.centred(m[k][j], off), mul2(r, h1[k][j]), t[k][j]);
                     }
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
 #pragma unroll
-                    for (int j = 0; j < P; ++j) t[0][k][j] = fma2(m[0][k][j], h1[k][j], t[0][k][j]);
+                    for (int j = 0; j < P; ++j) t[k][j] = fma2(m[k][j], h1[k][j], t[k][j]);
                 }
             }
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (live && rw.on[k]) Unit<TS, P>::put(h.p + rw.c[k] * unsigned(sizeof(TS)), t[0][k]);
+                if (live && rw.on[k]) Unit<TS, P>::put(h.p + rw.c[k] * unsigned(sizeof(TS)), t[k]);
         }
         if (pre) {  // of h before its rounding: the norm sees the exact sum
             float mean[1], square[1];
             const int kind[1] = {d.pre.kind};
-            rw.stats(t, kind, mean, square);
+            rw.stats(
+                [&](int, int k, f2(&v)[P]) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) v[j] = t[k][j];
+                },
+                kind, mean, square);
             const f2 r = twice(rsqrtf(square[0] + d.pre.eps));
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const f2 off = rw.minus(mean[0], k);
 #pragma unroll
-                for (int j = 0; j < P; ++j) t[0][k][j] = fma2(rw.centred(t[0][k][j], off), mul2(r, z1[k][j]), z0[k][j]);
-                if (live && rw.on[k]) Unit<TB, P>::put(z.p + rw.c[k] * unsigned(sizeof(TB)), t[0][k]);
+                for (int j = 0; j < P; ++j) t[k][j] = fma2(rw.centred(t[k][j], off), mul2(r, z1[k][j]), z0[k][j]);
+                if (live && rw.on[k]) Unit<TB, P>::put(z.p + rw.c[k] * unsigned(sizeof(TB)), t[k]);
             }
         }
         if (live) {
@@ -177,16 +187,16 @@ __global__ void __maxnreg__(REGS) gated_norm_kernel(const __grid_constant__ Norm
     }
 }
 
-template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST, bool LN>
+template <typename TS, typename TB, int REGS, bool MULTI, bool POST, bool LN>
 bsa_status forward(const NormArgs &a, int sms, cudaStream_t st)
 {
-    auto kern = gated_norm_kernel<TS, TB, V, REGS, SUB, POST, LN>;
+    auto kern = gated_norm_kernel<TS, TB, REGS, MULTI, POST, LN>;
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> regs{0};
     constexpr int BYTES = 8 * V * (sizeof(TS) + sizeof(TB)), STAGES = stages_for(BYTES);
     const bsa_status ok = ready(kern, STAGES * 512 * BYTES, done, regs);
     if (ok != BSA_OK) return ok;
-    const Shape s = shape_of(a.d, V, regs.load(std::memory_order_relaxed), sms, STAGES,
+    const Shape s = shape_of(a.d, regs.load(std::memory_order_relaxed), sms, STAGES,
                              8 * V * static_cast<int>(sizeof(TS) + (a.y.p ? sizeof(TB) : 0)));
     kern<<<s.ctas, s.threads, s.smem, st>>>(a, s.rg, s.tpr);
     return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
@@ -199,9 +209,9 @@ bsa_status launch_gated_norm(const NormArgs &a, cudaStream_t st)
     int sms = 0;
     const bsa_status s = current_sm_count(&sms);
     if (s != BSA_OK) return s;
-    return by_kernel(a.d, [&](auto ts, auto tb, auto v, auto regs, auto sub, auto post, auto ln) {
-        return forward<decltype(ts), decltype(tb), decltype(v)::value, decltype(regs)::value,
-                        decltype(sub)::value, decltype(post)::value, decltype(ln)::value>(a, sms, st);
+    return by_kernel<16>(a.d, [&](auto ts, auto tb, auto regs, auto multi, auto post, auto ln) {
+        return forward<decltype(ts), decltype(tb), decltype(regs)::value, decltype(multi)::value, decltype(post)::value,
+                       decltype(ln)::value>(a, sms, st);
     });
 }
 

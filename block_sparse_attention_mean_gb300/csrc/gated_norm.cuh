@@ -33,7 +33,7 @@ __host__ __device__ constexpr int pow2_ceil(int v)
 // Threads that hold a row of `groups` groups of 8 channels, v of them per thread
 __host__ __device__ inline int row_threads(int groups, int v)
 {
-    return groups <= 32 ? pow2_ceil(groups) : (groups + 32 * v - 1) / (32 * v) * 32;
+    return groups <= 32 * v ? pow2_ceil((groups + v - 1) / v) : (groups + 32 * v - 1) / (32 * v) * 32;
 }
 
 // ------------------------------------------------------------ E channels of a row: a thread's unit
@@ -89,14 +89,31 @@ struct Unit<float, P> {
     }
 };
 
-// channels of a modulation or of a weight (fp32)
+// channels of a modulation or of a weight (fp32): nothing writes them while the kernel runs, so that their loads need not
+// wait for one another's uses
 template <int P>
 __device__ __forceinline__ void load_mod(const void *p, int dt, int64_t at, f2 (&v)[P])
 {
-    if (dt == BSA_BF16)
-        Unit<__nv_bfloat16, P>::get(static_cast<const char *>(p) + at * 2, v);
-    else
-        Unit<float, P>::get(static_cast<const char *>(p) + at * 4, v);
+    if (dt == BSA_BF16) {
+        const char *from = static_cast<const char *>(p) + at * 2;
+        uint32_t r[P];
+        if constexpr (P == 4) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(from));
+            r[0] = q.x, r[1] = q.y, r[2] = q.z, r[3] = q.w;
+        } else {
+            const uint2 q = __ldg(reinterpret_cast<const uint2 *>(from));
+            r[0] = q.x, r[1] = q.y;
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = widen(r[i]);
+    } else {
+        const float4 *from = reinterpret_cast<const float4 *>(static_cast<const char *>(p) + at * 4);
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            const float4 r = __ldg(from + i / 2);
+            v[i] = pair(r.x, r.y), v[i + 1] = pair(r.z, r.w);
+        }
+    }
 }
 
 template <int P>
@@ -149,6 +166,12 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Vectors of 8 channels per thread. What a row costs a thread apart from its channels (the sums over the row, addresses,
+// the loop) is about as much as eight channels cost: with one vector, twice as many warps pay it (2048 channels bf16:
+// 223 against 179 us forward, 65536 rows; 147 against 119 us backward, 16384 rows). With more there are too few
+// registers for the sums of the backward pass.
+constexpr int V = 2;
+
 // ------------------------------------------------------------ rows and workers
 
 // The rows, B * N in order, cut into `workers` ranges of nearly equal length: range w begins at row
@@ -176,33 +199,36 @@ struct Walk {
     char *p;
 
     __device__ __forceinline__ Walk(const RowsView &v, int b, int n, int size) : p(v.p + (b * v.b + n * v.n) * size) {}
-    __device__ __forceinline__ void next(const RowsView &v, int size) { p += v.n * size; }
+    __device__ __forceinline__ void next(const RowsView &v, int size, int rows = 1) { p += rows * v.n * size; }
     // after the last token's next(): to the next batch's first
     __device__ __forceinline__ void wrap(const RowsView &v, int N, int size) { p += (v.b - N * v.n) * size; }
 };
 
-// What a thread knows of its row: its channels, and the CTA's exchange of the warps' sums. SUB: the row is held
-// by `lanes` < 32 lanes of a warp; else by whole warps. LN: a layer norm is among the norms (RMS alone needs no means).
-template <int K, int P, bool SUB, bool LN>
+// What a thread knows of its row: its channels, and the CTA's exchange of the warps' sums. MULTI: the CTA may hold
+// several rows, each in `lanes` lanes of a warp or in up to two warps; else one. LN: a layer norm is among the norms (RMS alone needs no means).
+template <int K, int P, bool MULTI, bool LN>
 struct Row {
     static constexpr int E = 2 * P;
     int C, lanes, warps, turn;
     float inv_c, inv_held;  // 1 / channels of the row, of this warp's part of it
     bool on[K];
     unsigned c[K];
-    float *buf;   // [2][4][kMaxWarps]
+    float *buf;   // [2][4][kMaxWarps]: the warps' sums
     float *held;  // channels that each warp holds
+    int base, warp;  // where the row's warps are in these (rows of up to two warps: four places each), this warp there
 
     __device__ __forceinline__ Row(int C_, int tpr, float *buf_)
     {
         C = C_;
-        lanes = SUB ? tpr : 32;
-        warps = SUB ? 1 : tpr / 32;
-        buf = buf_;
-        held = buf + 8 * kMaxWarps;
+        lanes = MULTI ? min(tpr, 32) : 32;
+        warps = MULTI ? max(1, tpr / 32) : tpr / 32;
+        const int t = MULTI ? threadIdx.x % tpr : threadIdx.x, rows = MULTI ? blockDim.x / tpr : 1;
+        base = MULTI && rows > 1 && warps > 1 ? 4 * (threadIdx.x / tpr) : 0;
+        warp = t / 32;
+        buf = buf_ + base;
+        held = buf_ + 8 * kMaxWarps + base;
         turn = 0;
         inv_c = inv_held = 1.0f / static_cast<float>(C);
-        const int t = SUB ? threadIdx.x % tpr : threadIdx.x;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int at = E * (t + k * tpr);
@@ -212,20 +238,20 @@ struct Row {
         if (warps > 1) {
             for (int i = threadIdx.x; i < 9 * kMaxWarps; i += blockDim.x) {
                 float n = 0.0f;  // the sums of warps that are not there stay zero, and they hold nothing
-                const int w = i - 8 * kMaxWarps;
-                if (w >= 0 && w < warps)
+                const int w = rows > 1 ? (i - 8 * kMaxWarps) % 4 : i - 8 * kMaxWarps;
+                if (i >= 8 * kMaxWarps && w < warps)
                     for (int k = 0; k < K; ++k) n += E * min(32, max(0, C / E - k * tpr - 32 * w));
-                buf[i] = n;
+                buf_[i] = n;
             }
             __syncthreads();
-            inv_held = 1.0f / held[threadIdx.x / 32];
+            inv_held = 1.0f / held[warp];
         }
     }
 
     template <int M>
     __device__ __forceinline__ void lanes_sum(float (&v)[M]) const
     {
-        if (SUB) {
+        if (MULTI) {
             for (int o = lanes / 2; o > 0; o >>= 1) {
 #pragma unroll
                 for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
@@ -248,7 +274,7 @@ struct Row {
         turn ^= 1;
         if (threadIdx.x % 32 == 0) {
 #pragma unroll
-            for (int m = 0; m < M; ++m) b[m * kMaxWarps + threadIdx.x / 32] = v[m];
+            for (int m = 0; m < M; ++m) b[m * kMaxWarps + warp] = v[m];
         }
         __syncthreads();
         return b;
@@ -281,20 +307,25 @@ struct Row {
     // v - mean, for a mean's minus(); nothing to do without a layer norm
     static __device__ __forceinline__ f2 centred(f2 v, f2 off) { return LN ? add2(v, off) : v; }
 
-    // Mean (0 but for LAYER) and mean square about it of M rows at once, one exchange. The spread is taken about
-    // each warp's own mean and joined exactly: sum_w (spread_w + n_w (mean_w - mean)^2), no cancellation for rows
-    // far from zero. Units that are off hold zeros.
-    template <int M>
-    __device__ __forceinline__ void stats(const f2 (&v)[M][K][P], const int (&kind)[M], float (&mean)[M], float (&square)[M])
+    // Mean (0 but for LAYER) and mean square about it of M rows at once, one exchange; read(m, k, v) gives unit k of row
+    // m, zeros where it is off. The spread is taken about each warp's own mean and joined exactly:
+    // sum_w (spread_w + n_w (mean_w - mean)^2), no cancellation for rows far from zero.
+    template <int M, typename Read>
+    __device__ __forceinline__ void stats(const Read &read, const int (&kind)[M], float (&mean)[M], float (&square)[M])
     {
 #pragma unroll
         for (int m = 0; m < M; ++m) mean[m] = 0.0f;
         if (LN) {
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                f2 q = v[m][0][0];
+                f2 q = twice(0.0f);
 #pragma unroll
-                for (int i = 1; i < K * P; ++i) q = add2(q, v[m][i / P][i % P]);
+                for (int k = 0; k < K; ++k) {
+                    f2 v[P];
+                    read(m, k, v);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) q = add2(q, v[i]);
+                }
                 mean[m] = two(q);
             }
             lanes_sum(mean);
@@ -307,9 +338,11 @@ struct Row {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const f2 off = minus(mean[m], k);
+                f2 v[P];
+                read(m, k, v);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    const f2 x = centred(v[m][k][i], off);
+                    const f2 x = centred(v[i], off);
                     q = fma2(x, x, q);
                 }
             }
@@ -357,11 +390,6 @@ constexpr int kExchangeFloats = 9 * kMaxWarps;
 
 // ------------------------------------------------------------ host
 
-// Vectors of 8 channels per thread, V: two from 512 channels on. What a row costs a thread apart from its channels
-// (the sums over the row, addresses, the loop) is about as much as eight channels cost, and half as many warps pay
-// it: at 2048 channels bf16 223 -> 179 us forward (65536 rows), 147 -> 119 us backward (16384 rows).
-inline int vectors(int C) { return C >= 512 ? 2 : 1; }
-
 // What a launch needs to know of a kernel, looked up once: registers, and (once per device) leave to use all of
 // the shared memory.
 template <typename Kernel>
@@ -388,13 +416,21 @@ struct Shape {
     Ranges rg;
 };
 
-// Workers: as many as fit on the device at once, each with an equal share of the rows; at most one per row.
-inline Shape shape_of(const bsa_gated_norm_desc &d, int v, int regs, int sms, int stages, int thread_bytes,
-                      int kept_bytes = 0)
+// Workers: as many as fit on the device at once, each with an equal share of the rows; at most one per row. A worker is
+// a row's threads, or (teams) a CTA: several rows of up to 512 channels side by side in 128 threads, no more of them than
+// a group has rows.
+inline Shape shape_of(const bsa_gated_norm_desc &d, int regs, int sms, int stages, int thread_bytes, int kept_bytes = 0,
+                      bool teams = false)
 {
     Shape s;
-    s.tpr = row_threads(d.C / 8, v);
-    s.threads = s.tpr < 32 ? 128 : s.tpr;
+    s.rg.rows = d.B * d.N;
+    s.rg.per_group = d.N / d.F;
+    s.tpr = row_threads(d.C / 8, V);
+    s.threads = s.tpr < (teams ? 128 : 32) ? 128 / s.tpr * s.tpr : s.tpr;
+    if (teams) {
+        while (s.threads / s.tpr > s.rg.per_group && s.threads > 32) s.threads /= 2;
+        if (s.threads > s.tpr) kept_bytes += 32 * V;  // where the teams' sums meet
+    }
     s.smem = static_cast<size_t>(s.threads) * (stages * thread_bytes + kept_bytes);
     const int by_regs = 65536 / ((regs + 7) / 8 * 8 * s.threads);
     const int by_smem = static_cast<int>((228 * 1024) / (s.smem + 4096));
@@ -402,10 +438,9 @@ inline Shape shape_of(const bsa_gated_norm_desc &d, int v, int regs, int sms, in
     if (resident > 2048 / s.threads) resident = 2048 / s.threads;
     if (resident > 32) resident = 32;
     if (resident < 1) resident = 1;
-    const int per_cta = s.threads / s.tpr;
-    s.rg.rows = d.B * d.N;
-    s.rg.per_group = d.N / d.F;
-    const int64_t fill = static_cast<int64_t>(sms) * resident * per_cta, most = gated_norm_max_workers(s.rg.rows, d.C);
+    const int per_cta = teams ? 1 : s.threads / s.tpr;
+    const int64_t fill = static_cast<int64_t>(sms) * resident * per_cta,
+                  most = teams ? gated_norm_max_workers(s.rg.rows, d.C) : s.rg.rows;
     s.rg.workers = static_cast<int>(fill < most ? fill : most);
     s.rg.step = ((static_cast<uint64_t>(s.rg.rows) << 32) + s.rg.workers - 1) / s.rg.workers;
     s.rg.per_step = UINT64_MAX / s.rg.step;
@@ -414,21 +449,19 @@ inline Shape shape_of(const bsa_gated_norm_desc &d, int v, int regs, int sms, in
     return s;
 }
 
-// run(stream dtype, branch dtype, V, registers per thread, whether lanes of one warp hold several rows, whether there
-// is a post norm, whether a layer norm is among the norms) for the kernel that a desc needs
-template <typename F>
+// run(stream dtype, branch dtype, registers per thread, whether the CTA holds several rows, whether there is a post norm,
+// whether a layer norm is among the norms) for the kernel that a desc needs. Rows of up to MULTI threads share a CTA.
+// Registers: 168, or 128 where 168 do not fit (more than 384 threads) or leave room for only half as many CTAs. Backward,
+// bf16, both norms, us with 168 and with 128: 4096 channels (256 threads) 154 and 143, 5016 channels (320 threads) 94 and 119.
+template <int MULTI, typename F>
 bsa_status by_kernel(const bsa_gated_norm_desc &d, F &&run)
 {
     auto by_width = [&](auto ts, auto tb, auto post, auto ln) {
-        const auto no = std::false_type();
-        const std::integral_constant<int, 1> one;
-        const std::integral_constant<int, 2> two;
-        // up to 256 threads per row: three CTAs of 128 threads per SM find 168 registers each; beyond, 512 threads
-        if (d.C > 4096) return run(ts, tb, two, std::integral_constant<int, 128>(), no, post, ln);
-        if (vectors(d.C) == 2) return run(ts, tb, two, std::integral_constant<int, 168>(), no, post, ln);
-        const std::integral_constant<int, 128> regs;
-        return row_threads(d.C / 8, 1) < 32 ? run(ts, tb, one, regs, std::true_type(), post, ln)
-                                            : run(ts, tb, one, regs, no, post, ln);
+        const int threads = row_threads(d.C / 8, V), fit = 65536 / (168 * threads);
+        const std::integral_constant<int, 168> regs;
+        if (fit == 0 || 65536 / (128 * threads) >= 2 * fit)
+            if (threads > 128) return run(ts, tb, std::integral_constant<int, 128>(), std::false_type(), post, ln);
+        return threads <= MULTI ? run(ts, tb, regs, std::true_type(), post, ln) : run(ts, tb, regs, std::false_type(), post, ln);
     };
     auto by_norms = [&](auto ts, auto tb) {
         const bool ln = d.post.kind == BSA_NORM_LAYER || d.pre.kind == BSA_NORM_LAYER;

@@ -1,15 +1,16 @@
 // gated_norm_backward.cu -- the backward pass of the gated norm (gated_norm.cu), in one pass over the rows.
-// A worker keeps four sums per channel in registers while it walks its rows,
+// A CTA walks a contiguous range of the rows, its teams (the threads that hold a row; one team for rows of more than
+// 1024 channels) side by side, never past the end of a group (the rows that share a modulation) in one step. A thread keeps
+// four sums per channel in registers,
 //   A = sum dz,  S = sum dz n,  P = sum dx,  Q = sum dx m      (m = y without a post norm),
-// from which every parameter's gradient follows by factors that are constant over the rows that share a
-// modulation (a group):
+// from which every parameter's gradient follows by factors that are constant over the group:
 //   dshift = A,  dscale = w S + b A,  dgate = alpha (w2 Q + b2 P),
 //   dpre_weight = sum_g (1 + scale_g) S_g,  dpre_bias = sum_g (1 + scale_g) A_g,
 //   dpost_weight = alpha sum_g gate_g Q_g,  dpost_bias = alpha sum_g gate_g P_g.
-// At the end of a group the worker writes the four sums into one of its two slots; a second kernel adds the slots
-// in the order of the workers, so that results do not depend on timing. Where groups are shorter than the longest
-// range (long_groups == 0), a worker that held a whole group writes its modulations' gradients itself, and adds up
-// the sums for the weights in a third slot.
+// At the end of a group the CTA adds its teams' sums and writes them into one of its two slots; a second kernel adds the
+// slots in the order of the CTAs, so that results do not depend on timing. Where groups are shorter than the longest
+// range (long_groups == 0), a CTA that held a whole group writes its modulations' gradients itself, and adds up the sums
+// for the weights in a third slot.
 #include "gated_norm.cuh"
 
 namespace bsa {
@@ -64,7 +65,30 @@ __device__ __forceinline__ void write_group(const NormArgs &a, int64_t g, int c,
     }
 }
 
-template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST, bool LN>
+// Adds one of the sums over the teams, in their order, into the first team's registers. shared: C floats per team.
+template <int K, int P, typename R>
+__device__ __forceinline__ void join_teams(f2 (&v)[K][P], const R &rw, int team, int teams, float *shared)
+{
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (rw.on[k]) Unit<float, P>::put(shared + team * rw.C + rw.c[k], v[k]);
+    __syncthreads();
+    for (int c = 4 * threadIdx.x; c < rw.C; c += 4 * blockDim.x) {
+        float4 s = *reinterpret_cast<const float4 *>(shared + c);
+        for (int t = 1; t < teams; ++t) {
+            const float4 q = *reinterpret_cast<const float4 *>(shared + t * rw.C + c);
+            s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+        }
+        *reinterpret_cast<float4 *>(shared + c) = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (rw.on[k] && team == 0) Unit<float, P>::get(shared + rw.c[k], v[k]);
+    __syncthreads();
+}
+
+template <typename TS, typename TB, int REGS, bool MULTI, bool POST, bool LN>
 __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_constant__ NormArgs a, Ranges rg, int tpr)
 {
     constexpr int E = 16 / sizeof(TS), P = E / 2, K = 8 * V / E, SB = E * sizeof(TS), BB = E * sizeof(TB);
@@ -78,21 +102,25 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     // where each tensor's units lie within a stage
     const int at_dh = pre ? K * threads * SB : 0, at_dz = at_dh + (has_dh ? K * threads * SB : 0),
               at_y = at_dz + (pre ? K * threads * BB : 0), stage_bytes = at_y + (has_y ? K * threads * BB : 0);
-    Row<K, P, SUB, LN> rw(C, tpr, buf);
+    Row<K, P, MULTI, LN> rw(C, tpr, buf);
     const Wants want = wants_of(a);
     if (a.partial && blockIdx.x == 0)
         for (int i = threadIdx.x; i < kNormTickets; i += threads) a.tickets[i] = 0;
 
-    // a CTA is one worker, unless lanes of a warp hold several rows: all that depends on the row alone is uniform
-    const int worker = SUB ? blockIdx.x * (threads / tpr) + threadIdx.x / tpr : blockIdx.x;
-    const bool some = !SUB || worker < rg.workers;
-    const int first = some ? rg.first(worker) : 0, count = some ? rg.first(worker + 1) - first : 0;
+    // all that depends on the CTA's rows alone is uniform
+    const int worker = blockIdx.x, teams = MULTI ? threads / tpr : 1, team = MULTI ? threadIdx.x / tpr : 0;
+    const int first = rg.first(worker), end = rg.first(worker + 1);
     const int b0 = first / d.N, n0 = first % d.N;
     Walk ph(a.h, b0, n0, sizeof(TS)), pdh(a.dh, b0, n0, sizeof(TS)), pdx(a.dx, b0, n0, sizeof(TS));
     Walk pdz(a.dz, b0, n0, sizeof(TB)), py(a.y, b0, n0, sizeof(TB)), pdy(a.dy, b0, n0, sizeof(TB));
-    int n_ahead = n0, n_here = n0;
+    // a step: `teams` rows of one group, fewer at its end and at the end of the range
+    struct Steps {
+        int row, n, stop;  // first row of the step, its token; the end of its group within the range
+    };
     const int first_group = first / rg.per_group;
-    int left = rg.per_group - first % rg.per_group, group = first_group;
+    Steps ahead{first, n0, min(end, (first_group + 1) * rg.per_group)}, here = ahead;
+    auto next_stop = [&](int stop) { return end - stop < rg.per_group ? end : stop + rg.per_group; };
+    int group = first_group;
     float *const slots = a.partial + int64_t(worker) * gated_norm_worker_floats(C);
     bool weighed = false;  // the worker's third slot holds sums
 
@@ -109,41 +137,47 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
         }
     }
     int to = 0, from = 0;  // stages
-    auto fetch = [&](bool any) {
-        if (any) {
+    auto fetch = [&] {  // copies the rows of the next step; a group of copies per step, empty past the end
+        if (ahead.row < end) {
+            const int rows = min(teams, ahead.stop - ahead.row);
+            if (team < rows) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!rw.on[k]) continue;
-                const uint32_t s_at = smem_u32(mine_s + to * stage_bytes + k * threads * SB);
-                const uint32_t b_at = smem_u32(mine_b + to * stage_bytes + k * threads * BB);
-                if (pre) {
-                    copy_async<SB>(s_at, ph.p + rw.c[k] * unsigned(sizeof(TS)));
-                    copy_async<BB>(b_at + at_dz, pdz.p + rw.c[k] * unsigned(sizeof(TB)));
+                for (int k = 0; k < K; ++k) {
+                    if (!rw.on[k]) continue;
+                    const uint32_t s_at = smem_u32(mine_s + to * stage_bytes + k * threads * SB);
+                    const uint32_t b_at = smem_u32(mine_b + to * stage_bytes + k * threads * BB);
+                    if (pre) {
+                        copy_async<SB>(s_at, ph.p + team * a.h.n * sizeof(TS) + rw.c[k] * unsigned(sizeof(TS)));
+                        copy_async<BB>(b_at + at_dz, pdz.p + team * a.dz.n * sizeof(TB) + rw.c[k] * unsigned(sizeof(TB)));
+                    }
+                    if (has_dh) copy_async<SB>(s_at + at_dh, pdh.p + team * a.dh.n * sizeof(TS) + rw.c[k] * unsigned(sizeof(TS)));
+                    if (has_y) copy_async<BB>(b_at + at_y, py.p + team * a.y.n * sizeof(TB) + rw.c[k] * unsigned(sizeof(TB)));
                 }
-                if (has_dh) copy_async<SB>(s_at + at_dh, pdh.p + rw.c[k] * unsigned(sizeof(TS)));
-                if (has_y) copy_async<BB>(b_at + at_y, py.p + rw.c[k] * unsigned(sizeof(TB)));
             }
-            ph.next(a.h, sizeof(TS));
-            pdh.next(a.dh, sizeof(TS));
-            pdz.next(a.dz, sizeof(TB));
-            py.next(a.y, sizeof(TB));
-            if (++n_ahead == d.N) {
-                n_ahead = 0;
+            ph.next(a.h, sizeof(TS), rows);
+            pdh.next(a.dh, sizeof(TS), rows);
+            pdz.next(a.dz, sizeof(TB), rows);
+            py.next(a.y, sizeof(TB), rows);
+            ahead.row += rows;
+            if ((ahead.n += rows) == d.N) {
+                ahead.n = 0;
                 ph.wrap(a.h, d.N, sizeof(TS));
                 pdh.wrap(a.dh, d.N, sizeof(TS));
                 pdz.wrap(a.dz, d.N, sizeof(TB));
                 py.wrap(a.y, d.N, sizeof(TB));
             }
+            if (ahead.row == ahead.stop) ahead.stop = next_stop(ahead.stop);
         }
         cp_async_commit();
         if (++to == STAGES) to = 0;
     };
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) fetch(i < count);
+    for (int i = 0; i < STAGES - 1; ++i) fetch();
 
     f2 sA[K][P] = {}, sS[K][P] = {}, sP[K][P] = {}, sQ[K][P] = {};
     // what dz and dx are multiplied by on their way to n and m: the thread's own 16-byte pieces of shared memory
     float4 *const kept = reinterpret_cast<float4 *>(ring + STAGES * stage_bytes) + threadIdx.x;
+    float *const shared = reinterpret_cast<float *>(ring + STAGES * stage_bytes + threads * 64 * V);  // for several teams
     auto keep = [&](int which, int k, const f2(&v)[P]) {
 #pragma unroll
         for (int j = 0; j < P; j += 2) {
@@ -176,13 +210,13 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
             keep(1, k, m);
         }
     };
-    if (count > 0) factors(group);
+    factors(group);
 
-    const int rounds = SUB ? rg.most() : count;
-    for (int i = 0; i < rounds; ++i) {
-        fetch(i + STAGES - 1 < count);
+    while (here.row < end) {
+        fetch();
         cp_async_wait_group<STAGES - 1>();
-        const bool live = !SUB || i < count;
+        const int rows = min(teams, here.stop - here.row);
+        const bool live = team < rows;
         const char *const here_s = mine_s + from * stage_bytes, *const here_b = mine_b + from * stage_bytes;
         if (++from == STAGES) from = 0;
         constexpr int M = POST ? 2 : 1;
@@ -200,7 +234,12 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
                     if (pre) Unit<TS, P>::get(here_s + k * threads * SB, both_rows[0][k]);
                     if (POST) Unit<TB, P>::get(here_b + at_y + k * threads * BB, both_rows[M - 1][k]);
                 }
-                rw.stats(both_rows, kind, mean, r);
+                rw.stats(
+                    [&](int m, int k, f2(&x)[P]) {
+#pragma unroll
+                        for (int j = 0; j < P; ++j) x[j] = both_rows[m][k][j];
+                    },
+                    kind, mean, r);
                 r[0] = rsqrtf(r[0] + d.pre.eps);
                 if (POST) r[M - 1] = rsqrtf(r[M - 1] + d.post.eps);
 #pragma unroll
@@ -284,7 +323,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
         if (a.dx.p && live) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (rw.on[k]) Unit<TS, P>::put(pdx.p + rw.c[k] * unsigned(sizeof(TS)), g[k]);
+                if (rw.on[k]) Unit<TS, P>::put(pdx.p + team * a.dx.n * sizeof(TS) + rw.c[k] * unsigned(sizeof(TS)), g[k]);
         }
         if (has_y) {
             f2 s0 = twice(0.0f), s1 = twice(0.0f);
@@ -328,29 +367,37 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
             if (a.dy.p && live) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (rw.on[k]) Unit<TB, P>::put(pdy.p + rw.c[k] * unsigned(sizeof(TB)), g[k]);
+                    if (rw.on[k]) Unit<TB, P>::put(pdy.p + team * a.dy.n * sizeof(TB) + rw.c[k] * unsigned(sizeof(TB)), g[k]);
             }
         }
-        if (!live) continue;
-        pdx.next(a.dx, sizeof(TS));
-        pdy.next(a.dy, sizeof(TB));
-        if (++n_here == d.N) {
-            n_here = 0;
+        pdx.next(a.dx, sizeof(TS), rows);
+        pdy.next(a.dy, sizeof(TB), rows);
+        here.row += rows;
+        if ((here.n += rows) == d.N) {
+            here.n = 0;
             pdx.wrap(a.dx, d.N, sizeof(TS));
             pdy.wrap(a.dy, d.N, sizeof(TB));
         }
-        if (--left > 0 && i + 1 < count) continue;
+        if (here.row < here.stop) continue;
         // the end of a group, or of the range
         if (want.pre_sums || want.post_sums) {
+            if (teams > 1) {
+                join_teams<K, P>(sA, rw, team, teams, shared);
+                join_teams<K, P>(sS, rw, team, teams, shared);
+                join_teams<K, P>(sP, rw, team, teams, shared);
+                join_teams<K, P>(sQ, rw, team, teams, shared);
+            }
             const int64_t begin = static_cast<int64_t>(group) * rg.per_group;
-            const bool whole = !rg.long_groups && begin >= first && begin + rg.per_group <= static_cast<int64_t>(first) + count;
+            const bool whole = !rg.long_groups && begin >= first && begin + rg.per_group <= end;
             float *const slot = slots + (group == first_group ? 0 : 4 * C);
             const int b = group / d.F, f = group % d.F;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (!rw.on[k]) continue;
                 const int c = rw.c[k];
-                if (whole) {
+                if (team > 0) {
+                    // the first team has their sums
+                } else if (whole) {
                     write_group(a, group, c, sA[k], sS[k], sP[k], sQ[k]);
                 } else {
                     Unit<float, P>::put(slot + c, sA[k]);
@@ -358,7 +405,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
                     Unit<float, P>::put(slot + 2 * C + c, sP[k]);
                     Unit<float, P>::put(slot + 3 * C + c, sQ[k]);
                 }
-                if (want.weights && !rg.long_groups) {  // weighted for the parameters that all groups share, and added up
+                if (want.weights && !rg.long_groups && team == 0) {  // weighted for the parameters that all groups share, and added up
                     if (d.scale.ptr) {
                         times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sA[k]);
                         times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sS[k]);
@@ -374,10 +421,16 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
                         sQ[k][j] = mul2(sQ[k][j], twice(d.alpha));
                     }
                     if (weighed) {
-                        plus(sum, BSA_FP32, 0, sA[k]);
-                        plus(sum + C, BSA_FP32, 0, sS[k]);
-                        plus(sum + 2 * C, BSA_FP32, 0, sP[k]);
-                        plus(sum + 3 * C, BSA_FP32, 0, sQ[k]);
+                        f2 before[4][P];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) Unit<float, P>::get(sum + m * C, before[m]);
+#pragma unroll
+                        for (int j = 0; j < P; ++j) {
+                            sA[k][j] = add2(sA[k][j], before[0][j]);
+                            sS[k][j] = add2(sS[k][j], before[1][j]);
+                            sP[k][j] = add2(sP[k][j], before[2][j]);
+                            sQ[k][j] = add2(sQ[k][j], before[3][j]);
+                        }
                     }
                     Unit<float, P>::put(sum, sA[k]);
                     Unit<float, P>::put(sum + C, sS[k]);
@@ -391,18 +444,16 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
             }
             weighed = true;
         }
-        if (i + 1 < count) {
-            left = rg.per_group;
-            factors(++group);
-        }
+        here.stop = next_stop(here.stop);
+        if (here.row < end) factors(++group);
     }
 }
 
 // Adds the workers' slots, 32 channels per CTA (four per thread), slices of 8 threads each taking every so many-th
-// worker. Items, blockIdx.y:
+// worker:
 //   long groups     group y: its modulations' gradients; its sums, weighted for the parameters that all groups share, go
 //                   into the third slot of worker y, and the last CTA of the channels adds those of all groups
-//   short groups    0: the weights' third slots over all workers; y > 0: a group that several workers share
+//   short groups    (x alone) first the weights' third slots over all workers, then the groups that several workers share
 constexpr int kMaxSlices = 64;
 
 struct Quad {
@@ -456,6 +507,28 @@ __device__ __forceinline__ float modulation(const bsa_modulation &m, int dt, int
                           : static_cast<const float *>(m.ptr)[at];
 }
 
+// short groups: the gradients of a group that two or more workers share
+__device__ __forceinline__ void write_cut_group(const NormArgs &a, const Ranges &rg, int group, int w0, int w1)
+{
+    const int C = a.d.C;
+    const int64_t stride = gated_norm_worker_floats(C);
+    for (int c = 4 * threadIdx.x; c < C; c += 4 * blockDim.x) {
+        f2 s[4][2] = {};
+        for (int w = w0; w <= w1; ++w) {
+            // it is the first in the ranges of its workers but, perhaps, that of the first of them
+            const float *p = a.partial + w * stride + (w == w0 && rg.first(w) / rg.per_group != group ? 4 * C : 0) + c;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f2 q[2];
+                Unit<float, 2>::get(p + k * C, q);
+                s[k][0] = add2(s[k][0], q[0]);
+                s[k][1] = add2(s[k][1], q[1]);
+            }
+        }
+        write_group<2>(a, group, c, s[0], s[1], s[2], s[3]);
+    }
+}
+
 __global__ void __launch_bounds__(8 * kMaxSlices, 2) gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg,
                                                                             int64_t n_groups)
 {
@@ -468,23 +541,22 @@ __global__ void __launch_bounds__(8 * kMaxSlices, 2) gated_norm_sums_kernel(cons
     const Wants want = wants_of(a);
     int w0 = 0, w1 = rg.workers - 1;
     int64_t group = -1;
+    const int strips = (C + 31) / 32;
     if (rg.long_groups) {
         group = blockIdx.y;
-    } else if (blockIdx.y > 0) {
-        // the group itself where there are at most as many groups as workers; else the one that worker y - 1's
-        // range begins inside
-        const int i = blockIdx.y - 1;
-        group = n_groups <= rg.workers ? i : rg.first(i) / rg.per_group;
-    } else if (!want.weights) {
-        return;
-    }
-    if (group >= 0) {
         w0 = rg.worker_of(group * rg.per_group);
         w1 = rg.worker_of((group + 1) * rg.per_group - 1);
-        if (!rg.long_groups) {
-            if (w0 == w1) return;                                                         // written by its worker
-            if (n_groups > rg.workers && static_cast<int>(blockIdx.y) - 1 != w0 + 1) return;  // one CTA per group
-        }
+    } else if (static_cast<int>(blockIdx.x) >= strips) {
+        // the group itself where there are at most as many groups as workers; else the one that the range begins inside
+        const int i = blockIdx.x - strips;
+        group = n_groups <= rg.workers ? i : rg.first(i) / rg.per_group;
+        w0 = rg.worker_of(group * rg.per_group);
+        w1 = rg.worker_of((group + 1) * rg.per_group - 1);
+        if (w0 == w1 || (n_groups > rg.workers && i != w0 + 1)) return;  // written by its worker, or by another CTA
+        write_cut_group(a, rg, static_cast<int>(group), w0, w1);
+        return;
+    } else if (!want.weights) {
+        return;
     }
     const int c = blockIdx.x * 32 + 4 * (threadIdx.x % 8), ch = blockIdx.x * 32 + threadIdx.x;
     const bool mine = threadIdx.x < 32 && ch < C;
@@ -554,28 +626,29 @@ __global__ void __launch_bounds__(8 * kMaxSlices, 2) gated_norm_sums_kernel(cons
     if (mine) put_weights();
 }
 
-template <typename TS, typename TB, int V, int REGS, bool SUB, bool POST, bool LN>
+template <typename TS, typename TB, int REGS, bool MULTI, bool POST, bool LN>
 bsa_status backward(const NormArgs &a, int sms, cudaStream_t st)
 {
-    auto kern = gated_norm_backward_kernel<TS, TB, V, REGS, SUB, POST, LN>;
+    auto kern = gated_norm_backward_kernel<TS, TB, REGS, MULTI, POST, LN>;
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> regs{0};
     constexpr int BYTES = 16 * V * (sizeof(TS) + sizeof(TB)), STAGES = stages_for(BYTES, 64 * V);
     const bsa_status ok = ready(kern, 512 * (STAGES * BYTES + 64 * V), done, regs);
     if (ok != BSA_OK) return ok;
     const int pre = a.d.pre.kind != BSA_NORM_NONE;
-    const Shape s = shape_of(a.d, V, regs.load(std::memory_order_relaxed), sms, STAGES,
-                             8 * V * static_cast<int>(sizeof(TS) * (pre + (a.dh.p ? 1 : 0)) + sizeof(TB) * (pre + (a.y.p ? 1 : 0))), 64 * V);
-    kern<<<s.ctas, s.threads, s.smem, st>>>(a, s.rg, s.tpr);
+    const Shape s = shape_of(a.d, regs.load(std::memory_order_relaxed), sms, STAGES,
+                             8 * V * static_cast<int>(sizeof(TS) * (pre + (a.dh.p ? 1 : 0)) + sizeof(TB) * (pre + (a.y.p ? 1 : 0))), 64 * V, true);
+    kern<<<s.rg.workers, s.threads, s.smem, st>>>(a, s.rg, s.tpr);
     if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     if (a.partial == nullptr) return BSA_OK;
     const int64_t n_groups = static_cast<int64_t>(a.d.B) * a.d.F;
-    const int64_t items = s.rg.long_groups ? n_groups : (n_groups < s.rg.workers ? n_groups : s.rg.workers) + 1;
     // as many slices as a group has workers
     int slices = kMaxSlices;
     if (s.rg.long_groups)
         while (slices > 8 && slices / 2 >= s.rg.workers / n_groups + 2) slices /= 2;
-    const dim3 grid((a.d.C + 31) / 32, static_cast<unsigned>(items));
+    const unsigned strips = (a.d.C + 31) / 32;
+    const dim3 grid = s.rg.long_groups ? dim3(strips, static_cast<unsigned>(n_groups))
+                                       : dim3(strips + static_cast<unsigned>(n_groups < s.rg.workers ? n_groups : s.rg.workers));
     return pdl_launch(gated_norm_sums_kernel, grid, 8 * slices, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
 }
 
@@ -583,7 +656,8 @@ bsa_status backward(const NormArgs &a, int sms, cudaStream_t st)
 
 int64_t gated_norm_max_workers(int64_t rows, int C)
 {
-    const int64_t w = kNormMaxThreads / row_threads(C / 8, vectors(C));
+    const int tpr = row_threads(C / 8, V);
+    const int64_t w = kNormMaxThreads / (tpr < 128 ? 128 / tpr * tpr : tpr);
     return rows < w ? rows : w;
 }
 
@@ -592,9 +666,9 @@ bsa_status launch_gated_norm_backward(const NormArgs &a, cudaStream_t st)
     int sms = 0;
     const bsa_status s = current_sm_count(&sms);
     if (s != BSA_OK) return s;
-    return by_kernel(a.d, [&](auto ts, auto tb, auto v, auto regs, auto sub, auto post, auto ln) {
-        return backward<decltype(ts), decltype(tb), decltype(v)::value, decltype(regs)::value,
-                        decltype(sub)::value, decltype(post)::value, decltype(ln)::value>(a, sms, st);
+    return by_kernel<64>(a.d, [&](auto ts, auto tb, auto regs, auto multi, auto post, auto ln) {
+        return backward<decltype(ts), decltype(tb), decltype(regs)::value, decltype(multi)::value, decltype(post)::value,
+                        decltype(ln)::value>(a, sms, st);
     });
 }
 

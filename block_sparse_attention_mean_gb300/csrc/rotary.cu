@@ -42,47 +42,57 @@ constexpr int kResident = 2, kForwardStages = 4, kBackwardStages = 3;
 // and 154.7, two 111.8 and 153.2, four 108.0 and 134.8, eight 117.9 and 155.8).
 constexpr int kTogether = 4;
 
-// What a thread holds of a head: two groups of 8 channels from c0 and c1 on, in which its pairs are
-//   INTERLEAVED: channels (2j, 2j + 1) of the groups (j < 4 of the first);  HALVES: channel j of the first and of the second
-// and which of the 8 pairs turn (bits). Groups are dealt out so that a warp's 16-byte accesses are contiguous.
+// What a thread holds of a head: 16 channels in groups of 16 bytes (GROUP channels), from c[g] on, dealt out so that a
+// warp's accesses are contiguous; and which of its 8 pairs turn (bits). Pair j is
+//   INTERLEAVED: channels 2i and 2i + 1 of a group;  HALVES: channel i of a group of the first half, and of its partner
+template <typename T>
 struct Lane {
-    int c0, c1;
+    static constexpr int GROUP = 16 / sizeof(T), GROUPS = 16 / GROUP;
+    int c[GROUPS];
     unsigned turns;
 };
 
-template <int D, bool HALVES>
-__device__ __forceinline__ int pair_of(int t, int j)
+// the index of pair j
+template <typename T, bool HALVES>
+__device__ __forceinline__ int pair_of(const Lane<T> &l, int j)
 {
-    return HALVES ? 8 * t + j : j < 4 ? 4 * t + j : D / 4 + 4 * t + j - 4;
+    constexpr int G = Lane<T>::GROUP;
+    return HALVES ? l.c[j / G] + j % G : l.c[j / (G / 2)] / 2 + j % (G / 2);
 }
 
-template <int D, bool HALVES>
-__device__ __forceinline__ Lane lane_of(int t, int rot)
+template <typename T, int D, bool HALVES>
+__device__ __forceinline__ Lane<T> lane_of(int t, int rot)
 {
-    Lane l;
+    constexpr int G = Lane<T>::GROUP, N = Lane<T>::GROUPS;
+    Lane<T> l;
+    // HALVES: rot is a multiple of 16, so that all pairs of a thread turn, or none
+    const int turning = HALVES ? rot / 16 : D / 16;
+    const bool first = t < turning;
+#pragma unroll
+    for (int g = 0; g < N; ++g) {
+        if (!HALVES)
+            l.c[g] = G * t + g * (D / N);
+        else if (first)
+            l.c[g] = G * t + g % (N / 2) * G * turning + g / (N / 2) * (rot / 2);
+        else
+            l.c[g] = rot + G * (t - turning) + g * G * (D / 16 - turning);
+    }
     l.turns = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) l.turns |= (pair_of<D, HALVES>(t, j) < rot / 2 ? 1u : 0u) << j;
-    if (HALVES) {  // rot / 2 is a multiple of 8: all eight pairs turn, or none (then 16 channels past the turning ones)
-        l.c0 = l.turns ? 8 * t : 16 * t;
-        l.c1 = l.turns ? rot / 2 + 8 * t : 16 * t + 8;
-    } else {
-        l.c0 = 8 * t;
-        l.c1 = D / 2 + 8 * t;
-    }
+    for (int j = 0; j < 8; ++j) l.turns |= (first && pair_of<T, HALVES>(l, j) < rot / 2 ? 1u : 0u) << j;
     return l;
 }
 
-template <int D, bool HALVES>
-__device__ __forceinline__ void angles(const bsa_rotary_plan &plan, const int *pos, int t, unsigned turns,
-                                       float (&cs)[8], float (&sn)[8])
+template <typename T, int D, bool HALVES>
+__device__ __forceinline__ void angles(const bsa_rotary_plan &plan, const int *pos, const Lane<T> &l, float (&cs)[8],
+                                       float (&sn)[8])
 {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         cs[j] = 1.0f;
         sn[j] = 0.0f;
-        if (turns >> j & 1u) {
-            const int p = pair_of<D, HALVES>(t, j);
+        if (l.turns >> j & 1u) {
+            const int p = pair_of<T, HALVES>(l, j);
             const uint64_t ph = plan.turns[p] * static_cast<uint64_t>(static_cast<int64_t>(pos[plan.axis[p] * (kThreads * 16 / D)]));
             const float half_turns = static_cast<float>(static_cast<int32_t>(ph >> 32)) * 4.656612873077393e-10f;  // 2^-31
             sincospif(half_turns, &sn[j], &cs[j]);
@@ -90,8 +100,7 @@ __device__ __forceinline__ void angles(const bsa_rotary_plan &plan, const int *p
     }
 }
 
-// A thread's 16 channels are held as pairs of neighbours, u[0..3] the first group, u[4..7] the second; channel() is
-// one of them as a float. Pair j's channels a and b:
+// A thread's 16 channels are held as pairs of neighbours, group after group. The channels of its pair j among them:
 template <bool HALVES>
 __host__ __device__ constexpr int a_of(int j)
 {
@@ -183,11 +192,13 @@ struct Side {
     // the positions of the thread's token, one axis every kThreads * 16 / D entries
     __device__ __forceinline__ const int *at(int tile) const { return &pos[tile % STAGES][0][threadIdx.x / (D / 16)]; }
     // 16 channels of a tensor's weight
-    __device__ __forceinline__ void read(int s, const Lane &l, f2 (&f)[8]) const
+    template <typename T>
+    __device__ __forceinline__ void read(int s, const Lane<T> &l, f2 (&f)[8]) const
     {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float4 v = *reinterpret_cast<const float4 *>(&weight[s][(i < 4 ? l.c0 : l.c1 - 8) + 2 * i]);
+            constexpr int G = Lane<T>::GROUP;
+            const float4 v = *reinterpret_cast<const float4 *>(&weight[s][l.c[2 * i / G] + 2 * i % G]);
             f[i] = pair(v.x, v.y);
             f[i + 1] = pair(v.z, v.w);
         }
@@ -246,18 +257,13 @@ struct Token {
 
 // 16 channels of a thread, from global memory to its own place in a stage
 template <typename T>
-__device__ __forceinline__ void copy_groups(uint32_t to, const char *from, const Lane &l)
+__device__ __forceinline__ void copy_groups(uint32_t to, const char *from, const Lane<T> &l)
 {
-    constexpr int PIECES = sizeof(T) / 2;  // of 16 bytes, per group
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i)
-            cp_async16(to + (g * PIECES + i) * kThreads * 16, from + (g ? l.c1 : l.c0) * sizeof(T) + 16 * i);
-    }
+    for (int g = 0; g < Lane<T>::GROUPS; ++g) cp_async16(to + g * kThreads * 16, from + l.c[g] * sizeof(T));
 }
 
-// 16 channels from the thread's place in a stage
+// from there
 template <typename T>
 __device__ __forceinline__ void read_groups(const char *at, f2 (&u)[8])
 {
@@ -269,27 +275,27 @@ __device__ __forceinline__ void read_groups(const char *at, f2 (&u)[8])
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 r = *reinterpret_cast<const float4 *>(at + i * kThreads * 16);
-            u[2 * i] = pair(r.x, r.y), u[2 * i + 1] = pair(r.z, r.w);
+        for (int g = 0; g < 4; ++g) {
+            const float4 r = *reinterpret_cast<const float4 *>(at + g * kThreads * 16);
+            u[2 * g] = pair(r.x, r.y), u[2 * g + 1] = pair(r.z, r.w);
         }
     }
 }
 
 // and to global memory; rounded to nearest even where T is bf16
 template <typename T>
-__device__ __forceinline__ void write_groups(char *to, const Lane &l, const f2 (&u)[8])
+__device__ __forceinline__ void write_groups(char *to, const Lane<T> &l, const f2 (&u)[8])
 {
-    if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4 *>(to + l.c0 * 2) = make_uint4(narrow(u[0]), narrow(u[1]), narrow(u[2]), narrow(u[3]));
-        *reinterpret_cast<uint4 *>(to + l.c1 * 2) = make_uint4(narrow(u[4]), narrow(u[5]), narrow(u[6]), narrow(u[7]));
-    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int g = 0; g < Lane<T>::GROUPS; ++g) {
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4 *>(to + l.c[g] * 2) =
+                make_uint4(narrow(u[4 * g]), narrow(u[4 * g + 1]), narrow(u[4 * g + 2]), narrow(u[4 * g + 3]));
+        } else {
             float4 r;
-            split(u[2 * i], r.x, r.y);
-            split(u[2 * i + 1], r.z, r.w);
-            *reinterpret_cast<float4 *>(to + (i < 2 ? l.c0 : l.c1 - 8) * 4 + 16 * i) = r;
+            split(u[2 * g], r.x, r.y);
+            split(u[2 * g + 1], r.z, r.w);
+            *reinterpret_cast<float4 *>(to + l.c[g] * 4) = r;
         }
     }
 }
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const __gri
     constexpr int STAGES = kForwardStages, LANES = D / 16, STAGE = kThreads * 16 * sizeof(T);
     extern __shared__ __align__(16) char ring[];
     const int t = threadIdx.x % LANES, mine = threadIdx.x / LANES % work.tokens, head = threadIdx.x / LANES / work.tokens;
-    const Lane l = lane_of<D, HALVES>(t, a.plan.rot);
+    const Lane<T> l = lane_of<T, D, HALVES>(t, a.plan.rot);
     const int64_t u0 = work.units * blockIdx.x / gridDim.x, u1 = work.units * (blockIdx.x + 1) / gridDim.x;
     const int count = static_cast<int>(u1 - u0);
     char *const own = ring + threadIdx.x * 16;
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const __gri
         if (here.s == 2 || tile == here.tile) return;
         tile = here.tile;
         __syncwarp();  // the token's positions were copied by its other threads
-        angles<D, HALVES>(a.plan, side.at(tile), t, l.turns, cs, sn);
+        angles<T, D, HALVES>(a.plan, side.at(tile), l, cs, sn);
     };
     side.weights(a);
     __syncthreads();
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_backward_kernel(co
     extern __shared__ __align__(16) char ring[];  // [stage][dy, then x with norm], then the weight gradients' sums
     __shared__ float sums[kThreads / 32][D];
     const int t = threadIdx.x % LANES, mine = threadIdx.x / LANES % work.tokens, head = threadIdx.x / LANES / work.tokens;
-    const Lane l = lane_of<D, HALVES>(t, a.plan.rot);
+    const Lane<T> l = lane_of<T, D, HALVES>(t, a.plan.rot);
     const int64_t u0 = work.units * blockIdx.x / gridDim.x, u1 = work.units * (blockIdx.x + 1) / gridDim.x;
     const int count = static_cast<int>(u1 - u0), stage_bytes = a.norm ? 2 * STAGE : STAGE;
     char *const own = ring + threadIdx.x * 16;
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_backward_kernel(co
         if (tile != here.tile) {
             tile = here.tile;
             __syncwarp();  // the token's positions were copied by its other threads
-            angles<D, HALVES>(a.plan, side.at(tile), t, l.turns, cs, sn);
+            angles<T, D, HALVES>(a.plan, side.at(tile), l, cs, sn);
         }
         side.read(here.s, l, w);
     };
@@ -508,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, kResident) rotary_backward_kernel(co
 #pragma unroll
                 for (int o = LANES; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
                 const int j = 4 * i + e;
-                if (threadIdx.x % 32 < LANES) sums[threadIdx.x / 32][(j < 8 ? l.c0 : l.c1 - 8) + j] = v[e];
+                if (threadIdx.x % 32 < LANES) sums[threadIdx.x / 32][l.c[j / Lane<T>::GROUP] + j % Lane<T>::GROUP] = v[e];
             }
         }
         __syncthreads();
