@@ -139,7 +139,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     int to = 0, from = 0;  // stages
     auto fetch = [&] {  // copies the rows of the next step; a group of copies per step, empty past the end
         if (ahead.row < end) {
-            const int rows = min(teams, ahead.stop - ahead.row);
+            const int rows = MULTI ? min(teams, ahead.stop - ahead.row) : 1;
             if (team < rows) {
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
@@ -215,7 +215,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     while (here.row < end) {
         fetch();
         cp_async_wait_group<STAGES - 1>();
-        const int rows = min(teams, here.stop - here.row);
+        const int rows = MULTI ? min(teams, here.stop - here.row) : 1;
         const bool live = team < rows;
         const char *const here_s = mine_s + from * stage_bytes, *const here_b = mine_b + from * stage_bytes;
         if (++from == STAGES) from = 0;
