@@ -198,6 +198,12 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
         const int b = g / d.F, f = g % d.F;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+            if (!rw.on[k]) {  // nothing is there to be read; the sums stay as they are
+                const f2 none[P] = {};
+                keep(0, k, none);
+                keep(1, k, none);
+                continue;
+            }
             const int c = rw.c[k];
             f2 m[P];
             fill(1.0f, m);

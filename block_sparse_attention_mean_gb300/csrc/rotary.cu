@@ -36,11 +36,13 @@ constexpr int kThreads = 256;
 // one of eight 139.6; backward two CTAs of three and four stages 133.8 and 139.7, one of six 166.5).
 constexpr int kResident = 2, kForwardStages = 4, kBackwardStages = 3;
 
-// Heads side by side in a step: the largest power of two up to this that divides all the head counts. With one, a
-// token's row is read 256 bytes at a time, with eight, a head's rows are written 1 KB at a time, and either way the
-// memory's pages are opened more often (d = 128 bf16, 16640 tokens of 24 heads, us forward and backward: one 115.7
-// and 154.7, two 111.8 and 153.2, four 108.0 and 134.8, eight 117.9 and 155.8).
-constexpr int kTogether = 4;
+// Heads side by side in a step: the largest power of two up to kTogether that divides all the head counts, as long as
+// there are kSteps steps of Q and K to a tile. With one, a token's row is read 256 bytes at a time, with eight, a head's
+// rows are written 1 KB at a time, and either way the memory's pages are opened more often (d = 128 bf16, 16640 tokens of
+// 24 heads, us forward and backward: one 115.7 and 154.7, two 111.8 and 153.2, four 108.0 and 134.8, eight 117.9 and
+// 155.8). But each of the threads that share a token computes its angles, and few steps do not make up for that (three
+// batches of 57314 tokens, two heads: two together 174, one 125; 65536 tokens of 16 heads: four together 267, two 257).
+constexpr int kTogether = 4, kSteps = 12;
 
 // What a thread holds of a head: 16 channels in groups of 16 bytes (GROUP channels), from c[g] on, dealt out so that a
 // warp's accesses are contiguous; and which of its 8 pairs turn (bits). Pair j is
@@ -553,6 +555,7 @@ int work_of(const RotaryArgs &a, int sms, int resident, Work *w)
     w->together = kTogether;
     for (const HeadsView &t : a.t)
         while (t.heads % w->together != 0) w->together /= 2;
+    while (w->together > 1 && a.t[0].heads + a.t[1].heads < kSteps * w->together) w->together /= 2;
     w->tokens = kThreads / (D / 16) / w->together;
     const int64_t tiles = (static_cast<int64_t>(a.B) * a.N + w->tokens - 1) / w->tokens;
     w->groups = (a.t[0].heads + a.t[1].heads + a.t[2].heads) / w->together;

@@ -102,7 +102,7 @@ TYPES = [(BF16, BF16, BF16), (FP32, BF16, FP32), (FP32, FP32, BF16), (BF16, BF16
 
 
 @pytest.mark.parametrize("types", TYPES)
-@pytest.mark.parametrize("C", [8, 24, 64, 72, 256, 264, 1000, 2048, 4096, 4104, 8192])
+@pytest.mark.parametrize("C", [8, 24, 64, 72, 256, 264, 504, 520, 1000, 1032, 2048, 3080, 4096, 4104, 6152, 8192])
 def test_widths_and_types(C, types):
     both(C, 2, 37, C, types=types, post=("rms", "w"), pre=("layer", "wb"))
 
@@ -123,14 +123,15 @@ def test_first_norm_without_a_branch(pre, types):
 
 @pytest.mark.parametrize("B,N,F", [(1, 1, 1), (5, 1, 1), (1, 2, 2), (2, 6, 3), (3, 64, 64), (1, 1000, 1), (2, 700, 7),
                                    (1, 999, 333), (4, 500, 2)])
-@pytest.mark.parametrize("C", [48, 1160])
+@pytest.mark.parametrize("C", [16, 48, 400, 800, 1160])
 def test_groups(B, N, F, C):
     """groups shorter than, as long as and longer than a worker's rows, one row each among them"""
     both(B + N + F, B, N, C, F=F, types=(FP32, FP32, FP32), post=("layer", "wb"), pre=("rms", "wb"))
 
 
 @pytest.mark.parametrize("N,F,C", [(9000, 1, 1024), (9000, 9000, 1024), (9000, 18, 1024), (6000, 2000, 2048),
-                                   (20000, 10, 64), (20000, 20000, 16), (30011, 1, 136)])
+                                   (20000, 10, 64), (20000, 20000, 16), (30011, 1, 136), (7000, 1000, 264),
+                                   (9001, 1, 920), (6006, 858, 700 * 8), (40000, 20000, 40)])
 def test_many_rows(N, F, C):
     """several rows per worker: groups that lie within, cross and span the workers' ranges"""
     both(N + F, 1, N, C, F=F, post=("rms", "w"), pre=("layer", "wb"))
@@ -179,6 +180,30 @@ def test_slices_of_larger_buffers():
     pair = torch.stack((x, x), 2)
     pkg.gated_norm(pair[:, :, 0], y, **kw, out=(pair[:, :, 1], None))
     assert torch.equal(pair[:, :, 1], h) and torch.equal(pair[:, :, 0], x)
+
+
+@pytest.mark.parametrize("C", [8, 24, 72, 136, 264, 520, 1032, 2056, 4104, 5600, 8184])
+def test_nothing_past_the_channels_is_read(C):
+    """rows, modulations and weights with NaN right behind their channels: none of it reaches a result"""
+    B, N, F = 2, 45, 3
+
+    def fenced(t):
+        room = torch.full((*t.shape[:-1], C + 512), float("nan"), dtype=t.dtype, device=DEV)
+        room[..., :C] = t
+        return room[..., :C]
+
+    for types in TYPES[:3]:
+        x, y, kw, rkw = make(C, B, N, C, F=F, types=types, post=("layer", "wb"), pre=("layer", "wb"))
+        for n in ("gate", "scale", "shift"):
+            kw[n] = rkw[n] = fenced(kw[n])
+        for n in ("post", "pre"):
+            kind, w, b, eps = rkw[n]
+            w, b = fenced(w), fenced(b)
+            kw[n], rkw[n] = pkg.NormSpec(kind, w, b, eps), (kind, w, b, eps)
+        x, y = fenced(x), fenced(y)
+        h, _ = check_forward(x, y, kw, rkw)
+        dh, dz = fenced(draw(gen(1), B, N, C, dt=types[0])), fenced(draw(gen(2), B, N, C, dt=types[1]))
+        check_backward(fenced(h), y, kw, rkw, dh, dz)
 
 
 def test_broadcast_inputs():

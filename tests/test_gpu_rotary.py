@@ -68,6 +68,11 @@ CASES = [
     (BF16, 1, 64, 2, 2, 64, (62,), True, None, False),            # the last pair does not turn
     (BF16, 1, 300, 17, 17, 64, (16, 24, 24), False, 0.0, True),
     (BF16, 1, 12, 64, 8, 128, (128,), False, 1e-6, True),
+    (FP32, 2, 70, 48, 24, 64, (16, 16), False, 1e-6, True),       # halves, half of the channels turn, heads by fours
+    (FP32, 1, 41, 32, 8, 128, (32, 16, 48), False, 1e-6, True),
+    (BF16, 2, 39, 26, 26, 64, (20, 6, 4), True, 1e-6, True),      # heads by twos
+    (FP32, 1, 1000, 24, 24, 128, (44, 42, 42), True, 1e-6, True),  # many tiles per CTA
+    (BF16, 3, 2000, 1, 1, 64, (16, 24, 24), True, 1e-6, True),
 ]
 
 
