@@ -184,10 +184,11 @@ def _code(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _expect(t: torch.Tensor, shape, dtype: torch.dtype, device, what: str, name: str) -> None:
-    """Shape, dtype, device and contiguous channels of a tensor that a kernel will index by them."""
-    if t.shape == shape and t.dtype == dtype and t.device == device and (t.stride(-1) == 1 or shape[-1] <= 1):
-        return
+def _view(t: torch.Tensor, shape, dtype: torch.dtype, device, what: str, name: str):
+    """(address, strides) of a tensor that a kernel will index by this shape, dtype and device, channels contiguous."""
+    s = t.stride()
+    if t.shape == shape and t.dtype == dtype and t.device == device and (s[-1] == 1 or shape[-1] <= 1):
+        return t.data_ptr(), s
     if t.shape != shape:
         raise BsaError(ERR_SHAPE, f"{what}: {name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
@@ -285,36 +286,34 @@ def grid_positions(grid: Sequence[int], n_text: int = 0, cuboid: Optional[Sequen
     return torch.cat((torch.zeros((n_text, len(grid)), dtype=torch.int32, device=device), c)).contiguous()
 
 
-def _rotary_args(plan, tensors, positions, q_weight, k_weight, h_at, what):
-    """Common checks of rotary and rotary_backward: (device, dtype code, B, N, positions, pos_batch). h_at: where the
-    heads are, 2 in [B, N, heads, d] tensors and 1 in [B, heads, N, d] ones."""
-    first = tensors[0] if tensors[0] is not None else tensors[1] if tensors[1] is not None else tensors[2]
+def _rotary_args(plan, first, positions, needed: bool, q_weight, k_weight, n_at: int, what: str):
+    """What rotary and rotary_backward have in common, from the first of their tensors (tokens at dimension n_at):
+    (device, dtype, dtype code, B, N, positions, pos_batch, weights)."""
     if first is None:
         raise BsaError(ERR_INVALID_ARG, f"{what}: none of q, k, v")
-    device = _cuda_device(first, what)
+    device, dtype = _cuda_device(first, what), first.dtype
     if first.dim() != 4:
         raise BsaError(ERR_SHAPE, f"{what}: {first.dim()} dimensions, expected 4")
-    B, N, d = first.shape[0], first.shape[3 - h_at], plan.d
-    for t, name in zip(tensors, "qkv"):
-        if t is not None:
-            h = t.shape[h_at] if t.dim() == 4 else 0
-            _expect(t, (B, N, h, d) if h_at == 2 else (B, h, N, d), first.dtype, device, what, name)
-    pos_batch = 0
-    if tensors[0] is not None or tensors[1] is not None:
+    B, N = first.shape[0], first.shape[n_at]
+    pos, pos_batch = None, 0
+    if needed:
         if positions is None:
             raise BsaError(ERR_INVALID_ARG, f"{what}: no positions")
-        flat = positions.dim() == 2
-        _expect(positions, (N, plan.n_axes) if flat else (B, N, plan.n_axes), torch.int32, device, what, "positions")
-        if N > 1 and positions.stride(-2) != plan.n_axes:
+        axes = plan.n_axes
+        if positions.dim() == 2:
+            pos, s = _view(positions, (N, axes), torch.int32, device, what, "positions")
+        else:
+            pos, s = _view(positions, (B, N, axes), torch.int32, device, what, "positions")
+            pos_batch = s[0]
+        if N > 1 and s[-2] != axes:
             raise BsaError(ERR_INVALID_ARG, f"{what}: a token's positions must follow the last token's")
-        pos_batch = 0 if flat else positions.stride(0)
-        positions = positions.data_ptr()
-    else:
-        positions = None
-    for w in (q_weight, k_weight):
-        if w is not None:
-            _expect(w, (d,), torch.float32, device, what, "weight")
-    return device, _code(first, what), B, N, positions, pos_batch
+    d = plan.d
+    weights = (0 if q_weight is None else _view(q_weight, (d,), torch.float32, device, what, "q_weight")[0],
+               0 if k_weight is None else _view(k_weight, (d,), torch.float32, device, what, "k_weight")[0], 0)
+    code = _CODES.get(dtype)
+    if code is None:
+        raise BsaError(ERR_DTYPE, f"{what}: tensor dtype {dtype}")
+    return device, dtype, code, B, N, pos, pos_batch, weights
 
 
 def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None,
@@ -326,24 +325,25 @@ def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor
     normalised per head (norm_eps not None; fp32 weights [d] optional) and turned by `positions`
     (int32 [N, axes] or [B, N, axes]). `out`: the three results' tensors, any strides with contiguous
     channels. Returns (q, k, v), None where none was given."""
-    device, dt, B, N, pos, pos_batch = _rotary_args(plan, (q, k, v), positions, q_weight, k_weight, 2, "rotary")
-    res, desc = [], []
-    for t, o, w in zip((q, k, v), out if out is not None else (None, None, None), (q_weight, k_weight, None)):
+    what = "rotary"
+    first = q if q is not None else k if k is not None else v
+    device, dtype, code, B, N, pos, pos_batch, weights = _rotary_args(
+        plan, first, positions, q is not None or k is not None, q_weight, k_weight, 1, what)
+    d = plan.d
+    res, desc = [None, None, None], [None, None, None]
+    for i, t in enumerate((q, k, v)):
         if t is None:
-            res.append(None)
-            desc.append(None)
             continue
-        h = t.shape[2]
+        h = t.shape[2] if t.dim() == 4 else 0
+        at, s = _view(t, (B, N, h, d), dtype, device, what, "q, k, v")
+        o = out[i] if out is not None else None
         if o is None:
-            o = torch.empty((B, h, N, plan.d), dtype=t.dtype, device=device)
-        else:
-            _expect(o, (B, h, N, plan.d), t.dtype, device, "rotary", "out")
-        s0, s1, s2, _ = t.stride()
-        o0, o1, o2, _ = o.stride()
-        desc.append(_HEADS.pack(t.data_ptr(), s0, s1, s2, o.data_ptr(), o0, o2, o1, 0 if w is None else w.data_ptr(), h))
-        res.append(o)
+            o = torch.empty((B, h, N, d), dtype=dtype, device=device)
+        o_at, r = _view(o, (B, h, N, d), dtype, device, what, "out")
+        desc[i] = _HEADS.pack(at, s[0], s[1], s[2], o_at, r[0], r[2], r[1], weights[i], h)
+        res[i] = o
     norm = norm_eps is not None
-    _run("bsa_rotary", load().bsa_rotary, device, stream, ctypes.byref(plan), *desc, dt, B, N, pos, pos_batch, norm,
+    _run("bsa_rotary", load().bsa_rotary, device, stream, ctypes.byref(plan), *desc, code, B, N, pos, pos_batch, norm,
          norm_eps if norm else 0.0)
     return tuple(res)
 
@@ -364,38 +364,35 @@ def rotary_backward(plan: RotaryPlan, dq: Optional[torch.Tensor], dk: Optional[t
     the gradients [B, N, heads, d] of its inputs. With norm_eps, q and k are rotary's inputs. Returns
     (gq, gk, gv, gq_weight, gk_weight); a weight's gradient (fp32 [d]) where that weight is given."""
     what = "rotary_backward"
-    device, dt, B, N, pos, pos_batch = _rotary_args(plan, (dq, dk, dv), positions, q_weight, k_weight, 1, what)
-    norm = norm_eps is not None
-    res, desc, dweights = [], [], []
-    for i, (t, x, o, w) in enumerate(zip((dq, dk, dv), (q, k, None), out if out is not None else (None, None, None),
-                                         (q_weight, k_weight, None))):
-        dw = torch.empty_like(w) if norm and w is not None and t is not None else None
-        dweights.append(dw)
+    first = dq if dq is not None else dk if dk is not None else dv
+    device, dtype, code, B, N, pos, pos_batch, weights = _rotary_args(
+        plan, first, positions, dq is not None or dk is not None, q_weight, k_weight, 2, what)
+    norm, d = norm_eps is not None, plan.d
+    res, desc, dweights = [None, None, None], [None, None, None], [None, None]
+    for i, t in enumerate((dq, dk, dv)):
         if t is None:
-            res.append(None)
-            desc.append(None)
             continue
-        h = t.shape[1]
-        shape = (B, N, h, plan.d)
+        h = t.shape[1] if t.dim() == 4 else 0
+        shape = (B, N, h, d)
+        at, s = _view(t, (B, h, N, d), dtype, device, what, "dq, dk, dv")
+        o = out[i] if out is not None else None
         if o is None:
-            o = torch.empty(shape, dtype=t.dtype, device=device)
-        else:
-            _expect(o, shape, t.dtype, device, what, "out")
-        x0 = x1 = x2 = x_at = 0
+            o = torch.empty(shape, dtype=dtype, device=device)
+        o_at, r = _view(o, shape, dtype, device, what, "out")
+        x_at, x, dw = 0, (0, 0, 0), 0
         if norm and i < 2:
-            if x is None:
+            side = q if i == 0 else k
+            if side is None:
                 raise BsaError(ERR_INVALID_ARG, "rotary_backward: the norm needs q and k")
-            _expect(x, shape, t.dtype, device, what, "q, k")
-            x_at = x.data_ptr()
-            x0, x1, x2, _ = x.stride()
-        s0, s1, s2, _ = t.stride()
-        o0, o1, o2, _ = o.stride()
-        desc.append(_HEADS_GRAD.pack(t.data_ptr(), s0, s2, s1, x_at, x0, x1, x2, o.data_ptr(), o0, o1, o2,
-                                     0 if w is None else w.data_ptr(), 0 if dw is None else dw.data_ptr(), h))
-        res.append(o)
+            x_at, x = _view(side, shape, dtype, device, what, "q, k")
+            if weights[i]:
+                dweights[i] = torch.empty(d, dtype=torch.float32, device=device)
+                dw = dweights[i].data_ptr()
+        desc[i] = _HEADS_GRAD.pack(at, s[0], s[2], s[1], x_at, x[0], x[1], x[2], o_at, r[0], r[1], r[2], weights[i], dw, h)
+        res[i] = o
     if ws is None and (dweights[0] is not None or dweights[1] is not None):
         ws = rotary_workspace(B, N, plan.d, device)
-    _run("bsa_rotary_backward", load().bsa_rotary_backward, device, stream, ctypes.byref(plan), *desc, dt, B, N, pos,
+    _run("bsa_rotary_backward", load().bsa_rotary_backward, device, stream, ctypes.byref(plan), *desc, code, B, N, pos,
          pos_batch, norm, norm_eps if norm else 0.0, _ptr(ws), _workspace_bytes(ws, device, what))
     return (*res, dweights[0], dweights[1])
 
@@ -426,22 +423,12 @@ class GatedNormGrads(NamedTuple):
     dpre_bias: Optional[torch.Tensor]
 
 
-def _rows(t: Optional[torch.Tensor]):
-    if t is None:
-        return _NO_ROWS
-    s0, s1, _ = t.stride()
-    return t.data_ptr(), s0, s1
-
-
 def _norm_args(n: Optional[NormSpec], C: int, device, what: str):
     if n is None:
         return NORM_NONE, 0.0, 0, 0
     w, b = n.weight, n.bias
-    if w is not None:
-        _expect(w, (C,), torch.float32, device, what, "weight")
-    if b is not None:
-        _expect(b, (C,), torch.float32, device, what, "bias")
-    return _KINDS[n.kind], n.eps, 0 if w is None else w.data_ptr(), 0 if b is None else b.data_ptr()
+    return (_KINDS[n.kind], n.eps, 0 if w is None else _view(w, (C,), torch.float32, device, what, "weight")[0],
+            0 if b is None else _view(b, (C,), torch.float32, device, what, "bias")[0])
 
 
 def _gated_desc(shape, device, stream_dt: int, branch_dt: int, alpha, post, pre, gate, scale, shift, what: str):
@@ -456,14 +443,10 @@ def _gated_desc(shape, device, stream_dt: int, branch_dt: int, alpha, post, pre,
         frames = m.dim() == 3
         if mod is None:
             F, mod = m.shape[1] if frames else 1, m.dtype
-        _expect(m, (B, F, C) if frames else (B, C), mod, device, what, "gate, scale, shift")
-        if frames:
-            s0, s1, _ = m.stride()
-        elif F == 1:
-            s0, s1 = m.stride(0), 0
-        else:
+        at, s = _view(m, (B, F, C) if frames else (B, C), mod, device, what, "gate, scale, shift")
+        if not frames and F != 1:
             raise BsaError(ERR_SHAPE, f"{what}: modulations of shape {tuple(m.shape)} and of {F} frames")
-        mods += (m.data_ptr(), s0, s1)
+        mods += (at, s[0], s[1] if frames else 0)
     if mod is not None and mod not in _CODES:
         raise BsaError(ERR_DTYPE, f"{what}: modulation dtype {mod}")
     return _DESC.pack(B, N, C, F, stream_dt, branch_dt, _CODES[mod] if mod is not None else BF16, alpha,
@@ -483,26 +466,28 @@ def gated_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, gate: Optio
     if x.dim() != 3:
         raise BsaError(ERR_SHAPE, f"gated_norm: x has {x.dim()} dimensions, expected 3")
     shape, dtype = x.shape, x.dtype
-    _expect(x, shape, dtype, device, what, "x")
+    pack = _ROWS.pack
+    at, s = _view(x, shape, dtype, device, what, "x")
+    rows = [pack(at, s[0], s[1]), None, None, None]
     h, z = out if out is not None else (None, None)
     branch = y if y is not None else z
     branch_dtype = branch.dtype if branch is not None else branch_dtype or dtype
     if y is not None:
-        _expect(y, shape, branch_dtype, device, what, "y")
+        at, s = _view(y, shape, branch_dtype, device, what, "y")
+        rows[1] = pack(at, s[0], s[1])
         if h is None:
             h = torch.empty(shape, dtype=dtype, device=device)
-        else:
-            _expect(h, shape, dtype, device, what, "out h")
-    if pre is not None:
-        if z is None:
-            z = torch.empty(shape, dtype=branch_dtype, device=device)
-        else:
-            _expect(z, shape, branch_dtype, device, what, "out z")
+    if pre is not None and z is None:
+        z = torch.empty(shape, dtype=branch_dtype, device=device)
+    if h is not None:
+        at, s = _view(h, shape, dtype, device, what, "out h")
+        rows[2] = pack(at, s[0], s[1])
+    if z is not None:
+        at, s = _view(z, shape, branch_dtype, device, what, "out z")
+        rows[3] = pack(at, s[0], s[1])
     desc, _ = _gated_desc(shape, device, _code(x, what), _CODES.get(branch_dtype, -1), alpha, post, pre, gate, scale,
                           shift, what)
-    pack = _ROWS.pack
-    _run("bsa_gated_norm", load().bsa_gated_norm, device, stream, desc, pack(*_rows(x)), pack(*_rows(y)),
-         pack(*_rows(h)), pack(*_rows(z)))
+    _run("bsa_gated_norm", load().bsa_gated_norm, device, stream, desc, *rows)
     return h, z
 
 
@@ -534,27 +519,25 @@ def gated_norm_backward(dh: Optional[torch.Tensor], dz: Optional[torch.Tensor], 
         raise BsaError(ERR_INVALID_ARG, f"{what}: no h")
     stream_dtype = like.dtype
     branch_dtype = dz.dtype if dz is not None else y.dtype if y is not None else stream_dtype
-    if dh is not None:
-        _expect(dh, shape, stream_dtype, device, what, "dh")
-    if dz is not None:
-        _expect(dz, shape, branch_dtype, device, what, "dz")
+
+    def rows(t, dtype, name):
+        if t is None:
+            return _NO_ROWS
+        at, s = _view(t, shape, dtype, device, what, name)
+        return at, s[0], s[1]
+
     dx, dy = out if out is not None else (None, None)
-    if pre is not None:
-        if h is not None:
-            _expect(h, shape, stream_dtype, device, what, "h")
-        if dx is None:
-            dx = torch.empty(shape, dtype=stream_dtype, device=device)
-        else:
-            _expect(dx, shape, stream_dtype, device, what, "out dx")
-    if y is not None:
-        _expect(y, shape, branch_dtype, device, what, "y")
-        if dy is None:
-            dy = torch.empty(shape, dtype=branch_dtype, device=device)
-        else:
-            _expect(dy, shape, branch_dtype, device, what, "out dy")
-    else:
+    if pre is None:
+        dx = h = None
+    elif dx is None:
+        dx = torch.empty(shape, dtype=stream_dtype, device=device)
+    if y is None:
         dy = None
-    desc, F = _gated_desc(shape, device, _code(like, what), _CODES.get(branch_dtype, -1), alpha, post, pre, gate, scale,
+    elif dy is None:
+        dy = torch.empty(shape, dtype=branch_dtype, device=device)
+    views = (*rows(dh, stream_dtype, "dh"), *rows(dz, branch_dtype, "dz"), *rows(h, stream_dtype, "h"),
+             *rows(y, branch_dtype, "y"), *rows(dx, stream_dtype, "out dx"), *rows(dy, branch_dtype, "out dy"))
+    desc, _ = _gated_desc(shape, device, _code(like, what), _CODES.get(branch_dtype, -1), alpha, post, pre, gate, scale,
                           shift, what)
     dmods, dparams, at = [], [], []
     for m in (gate, scale, shift):
@@ -568,8 +551,7 @@ def gated_norm_backward(dh: Optional[torch.Tensor], dz: Optional[torch.Tensor], 
             at.append(0 if d is None else d.data_ptr())
     if ws is None and any(at):
         ws = gated_norm_workspace(*shape, device)
-    args = _GRADS.pack(*_rows(dh), *_rows(dz), *(_rows(h) if pre is not None else _NO_ROWS), *_rows(y),
-                       *(_rows(dx) if pre is not None else _NO_ROWS), *_rows(dy), *at)
+    args = _GRADS.pack(*views, *at)
     _run("bsa_gated_norm_backward", load().bsa_gated_norm_backward, device, stream, desc, args, _ptr(ws),
          _workspace_bytes(ws, device, what))
     return GatedNormGrads(dx if pre is not None else dh, dy, *dmods, *dparams)
