@@ -437,6 +437,7 @@ bsa_status bsa_gated_norm_backward(const bsa_gated_norm_desc *desc, const bsa_ga
         if (!rows_of(g.dy, d, d.branch_dt, &all.out[all.n_out], &a.dy)) return BSA_ERR_INVALID_ARG;
         all.may_be[all.n_out++] = y_bit | dz_bit;
     }
+    if (!a.y.p) a.d.post = bsa_norm{};  // nothing is asked for behind the post norm
     if (!all.check()) return BSA_ERR_INVALID_ARG;
     a.dgate = static_cast<char *>(g.dgate);
     a.dscale = static_cast<char *>(g.dscale);

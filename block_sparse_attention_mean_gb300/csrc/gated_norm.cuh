@@ -1,5 +1,5 @@
 // gated_norm.cuh -- what the forward (gated_norm.cu) and backward (gated_norm_backward.cu) kernels of the gated norm
-// share: pairs of fp32, a thread's part of a row, the sums over a row, and how the rows are dealt out.
+// share: a thread's part of a row, the sums over a row, and how the rows are dealt out.
 #pragma once
 
 #include <atomic>
@@ -14,13 +14,20 @@ namespace {
 
 constexpr int kMaxWarps = 16;  // CTAs of up to 512 threads
 
-// Rows in flight per worker: three (more of them are slower: 65536 rows of 2048 channels 181 us, with four 196 us),
-// fewer where a CTA of 512 threads would not find room for them (rows of more
-// than 4096 channels). `bytes`: what a thread copies per row; `kept`: what it holds in shared memory besides.
-__host__ __device__ constexpr int stages_for(int bytes, int kept = 0)
+// Threads of a CTA at most: of several rows, of a row in that many registers (by_kernel)
+__host__ __device__ constexpr int most_threads(int regs, bool multi, int branch_size)
 {
-    const int fit = (221184 - 512 * kept) / (512 * bytes);
-    return fit > 3 ? 3 : fit < 1 ? 1 : fit;
+    return multi ? 128 : regs == 128 ? 512 : branch_size == 4 ? 320 : 384;
+}
+
+// Rows in flight per worker, forward: more of them are slower (65536 rows of 2048 channels: three 181 us, four 196 us).
+// Backward two, which have more tensors each (three: 94.8 against 93.2 us for 16384 rows of 2048 channels bf16), or one
+// where the largest CTA has no room for two of `bytes` a thread beside the `kept` bytes (one in place of two: 172 against
+// 143 us, 2048 channels of fp32).
+constexpr int kStages = 3;
+__host__ __device__ constexpr int stages_for(int threads, int bytes, int kept)
+{
+    return threads * (2 * bytes + kept) <= 221184 ? 2 : 1;
 }
 
 __host__ __device__ constexpr int pow2_ceil(int v)
@@ -36,9 +43,9 @@ __host__ __device__ inline int row_threads(int groups, int v)
     return groups <= 32 * v ? pow2_ceil((groups + v - 1) / v) : (groups + 32 * v - 1) / (32 * v) * 32;
 }
 
-// ------------------------------------------------------------ E channels of a row: a thread's unit
-// E / 2 pairs from and to memory. Stores to bf16 round to nearest even: half a step per element.
-template <typename T, int P>  // P pairs
+// ------------------------------------------------------------ a thread's unit of a row
+// P pairs of channels from and to memory. Stores to bf16 round to nearest even: half a step per element.
+template <typename T, int P>
 struct Unit;
 
 template <>
@@ -205,7 +212,8 @@ struct Walk {
 };
 
 // What a thread knows of its row: its channels, and the CTA's exchange of the warps' sums. MULTI: the CTA may hold
-// several rows, each in `lanes` lanes of a warp or in up to two warps; else one. LN: a layer norm is among the norms (RMS alone needs no means).
+// several rows, each in `lanes` lanes of a warp or in up to two warps; else one. LN: a layer norm is among the norms (RMS
+// alone needs no means).
 template <int K, int P, bool MULTI, bool LN>
 struct Row {
     static constexpr int E = 2 * P;
@@ -451,7 +459,8 @@ inline Shape shape_of(const bsa_gated_norm_desc &d, int regs, int sms, int stage
 
 // run(stream dtype, branch dtype, registers per thread, whether the CTA holds several rows, whether there is a post norm,
 // whether a layer norm is among the norms) for the kernel that a desc needs. Rows of up to MULTI threads share a CTA.
-// Registers: 168, or 128 where 168 do not fit (more than 384 threads) or leave room for only half as many CTAs. Backward,
+// Registers: 168, or 128 where 168 do not fit (more than 384 threads; 320 with an fp32 branch, so that the backward pass
+// has room for two rows in flight) or leave room for only half as many CTAs. Backward,
 // bf16, both norms, us with 168 and with 128: 4096 channels (256 threads) 154 and 143, 5016 channels (320 threads) 94 and 119.
 template <int MULTI, typename F>
 bsa_status by_kernel(const bsa_gated_norm_desc &d, F &&run)
@@ -459,7 +468,7 @@ bsa_status by_kernel(const bsa_gated_norm_desc &d, F &&run)
     auto by_width = [&](auto ts, auto tb, auto post, auto ln) {
         const int threads = row_threads(d.C / 8, V), fit = 65536 / (168 * threads);
         const std::integral_constant<int, 168> regs;
-        if (fit == 0 || 65536 / (128 * threads) >= 2 * fit)
+        if (threads > most_threads(168, false, sizeof(tb)) || 65536 / (128 * threads) >= 2 * fit)
             if (threads > 128) return run(ts, tb, std::integral_constant<int, 128>(), std::false_type(), post, ln);
         return threads <= MULTI ? run(ts, tb, regs, std::true_type(), post, ln) : run(ts, tb, regs, std::false_type(), post, ln);
     };
