@@ -209,7 +209,7 @@ bsa_status launch_gated_norm(const NormArgs &a, cudaStream_t st)
     int sms = 0;
     const bsa_status s = current_sm_count(&sms);
     if (s != BSA_OK) return s;
-    return by_kernel<16>(a.d, [&](auto ts, auto tb, auto regs, auto multi, auto post, auto ln) {
+    return by_kernel<16, false>(a.d, [&](auto ts, auto tb, auto regs, auto multi, auto post, auto ln) {
         return forward<decltype(ts), decltype(tb), decltype(regs)::value, decltype(multi)::value, decltype(post)::value,
                        decltype(ln)::value>(a, sms, st);
     });

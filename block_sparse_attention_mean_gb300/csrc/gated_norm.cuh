@@ -175,7 +175,7 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
 
 // Vectors of 8 channels per thread. What a row costs a thread apart from its channels (the sums over the row, addresses,
 // the loop) is about as much as eight channels cost: with one vector, twice as many warps pay it (2048 channels bf16:
-// 223 against 179 us forward, 65536 rows; 147 against 119 us backward, 16384 rows). With more there are too few
+// 193 against 182 us forward, 65536 rows; 109 against 93 us backward, 16384 rows). With more there are too few
 // registers for the sums of the backward pass.
 constexpr int V = 2;
 
@@ -460,16 +460,21 @@ inline Shape shape_of(const bsa_gated_norm_desc &d, int regs, int sms, int stage
 // run(stream dtype, branch dtype, registers per thread, whether the CTA holds several rows, whether there is a post norm,
 // whether a layer norm is among the norms) for the kernel that a desc needs. Rows of up to MULTI threads share a CTA.
 // Registers: 168, or 128 where 168 do not fit (more than 384 threads; 320 with an fp32 branch, so that the backward pass
-// has room for two rows in flight) or leave room for only half as many CTAs. Backward,
-// bf16, both norms, us with 168 and with 128: 4096 channels (256 threads) 154 and 143, 5016 channels (320 threads) 94 and 119.
-template <int MULTI, typename F>
+// has room for two rows in flight) or, mostly, where they leave room for only half as many CTAs (224 and 256 threads, that
+// is 3080 to 4096 channels). The backward pass has the fewest registers to spare with a post norm or in fp32, and takes
+// fewer CTAs there. us with 168 and with 128, 4096 channels bf16: forward 32768 rows 206 and 195, layer norms 328 and 225;
+// backward 8192 rows 123 and 133, layer norms 158 and 162, no post norm 99 and 91; fp32 stream 137 and 162, no post norm
+// 121 and 133, layer norm alone 177 and 140. 320 threads, backward, 4096 rows: 93 and 123.
+template <int MULTI, bool BACKWARD, typename F>
 bsa_status by_kernel(const bsa_gated_norm_desc &d, F &&run)
 {
     auto by_width = [&](auto ts, auto tb, auto post, auto ln) {
-        const int threads = row_threads(d.C / 8, V), fit = 65536 / (168 * threads);
+        const int threads = row_threads(d.C / 8, V);
         const std::integral_constant<int, 168> regs;
-        if (threads > most_threads(168, false, sizeof(tb)) || 65536 / (128 * threads) >= 2 * fit)
-            if (threads > 128) return run(ts, tb, std::integral_constant<int, 128>(), std::false_type(), post, ln);
+        const bool halved = 65536 / (128 * threads) >= 2 * (65536 / (168 * threads)),
+                   rather = BACKWARD && (post.value || (sizeof(ts) == 4 && !ln.value));
+        if (threads > most_threads(168, false, sizeof(tb)) || (threads > 128 && halved && !rather))
+            return run(ts, tb, std::integral_constant<int, 128>(), std::false_type(), post, ln);
         return threads <= MULTI ? run(ts, tb, regs, std::true_type(), post, ln) : run(ts, tb, regs, std::false_type(), post, ln);
     };
     auto by_norms = [&](auto ts, auto tb) {

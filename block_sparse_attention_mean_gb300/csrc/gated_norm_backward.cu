@@ -676,7 +676,7 @@ bsa_status launch_gated_norm_backward(const NormArgs &a, cudaStream_t st)
     int sms = 0;
     const bsa_status s = current_sm_count(&sms);
     if (s != BSA_OK) return s;
-    return by_kernel<64>(a.d, [&](auto ts, auto tb, auto regs, auto multi, auto post, auto ln) {
+    return by_kernel<64, true>(a.d, [&](auto ts, auto tb, auto regs, auto multi, auto post, auto ln) {
         return backward<decltype(ts), decltype(tb), decltype(regs)::value, decltype(multi)::value, decltype(post)::value,
                         decltype(ln)::value>(a, sms, st);
     });
