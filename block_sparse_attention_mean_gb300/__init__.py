@@ -24,5 +24,6 @@ def __getattr__(name):
         return getattr(binding, name)
     if name in _BLOCK_NAMES:
         from . import block_binding
-        return getattr(block_binding, name)
+        value = globals()[name] = getattr(block_binding, name)  # found at once from now on: small calls are bound by the host
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -338,7 +338,7 @@ def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor
         at, s = _view(t, (B, N, h, d), dtype, device, what, "q, k, v")
         o = out[i] if out is not None else None
         if o is None:
-            o = torch.empty((B, h, N, d), dtype=dtype, device=device)
+            o = t.new_empty((B, h, N, d))
         o_at, r = _view(o, (B, h, N, d), dtype, device, what, "out")
         desc[i] = _HEADS.pack(at, s[0], s[1], s[2], o_at, r[0], r[2], r[1], weights[i], h)
         res[i] = o
@@ -377,7 +377,7 @@ def rotary_backward(plan: RotaryPlan, dq: Optional[torch.Tensor], dk: Optional[t
         at, s = _view(t, (B, h, N, d), dtype, device, what, "dq, dk, dv")
         o = out[i] if out is not None else None
         if o is None:
-            o = torch.empty(shape, dtype=dtype, device=device)
+            o = t.new_empty(shape)
         o_at, r = _view(o, shape, dtype, device, what, "out")
         x_at, x, dw = 0, (0, 0, 0), 0
         if norm and i < 2:
@@ -386,7 +386,7 @@ def rotary_backward(plan: RotaryPlan, dq: Optional[torch.Tensor], dk: Optional[t
                 raise BsaError(ERR_INVALID_ARG, "rotary_backward: the norm needs q and k")
             x_at, x = _view(side, shape, dtype, device, what, "q, k")
             if weights[i]:
-                dweights[i] = torch.empty(d, dtype=torch.float32, device=device)
+                dweights[i] = torch.empty_like(q_weight if i == 0 else k_weight)
                 dw = dweights[i].data_ptr()
         desc[i] = _HEADS_GRAD.pack(at, s[0], s[2], s[1], x_at, x[0], x[1], x[2], o_at, r[0], r[1], r[2], weights[i], dw, h)
         res[i] = o
@@ -476,7 +476,7 @@ def gated_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, gate: Optio
         at, s = _view(y, shape, branch_dtype, device, what, "y")
         rows[1] = pack(at, s[0], s[1])
         if h is None:
-            h = torch.empty(shape, dtype=dtype, device=device)
+            h = x.new_empty(shape)
     if pre is not None and z is None:
         z = torch.empty(shape, dtype=branch_dtype, device=device)
     if h is not None:
@@ -541,7 +541,7 @@ def gated_norm_backward(dh: Optional[torch.Tensor], dz: Optional[torch.Tensor], 
                           shift, what)
     dmods, dparams, at = [], [], []
     for m in (gate, scale, shift):
-        d = None if m is None else torch.empty(m.shape, dtype=m.dtype, device=device)
+        d = None if m is None else m.new_empty(m.shape)
         dmods.append(d)
         at.append(0 if d is None else d.data_ptr())
     for n in (post, pre):
