@@ -452,7 +452,6 @@ bsa_status bsa_gated_norm_backward(const bsa_gated_norm_desc *desc, const bsa_ga
         if (s != BSA_OK) return s;
         if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return BSA_ERR_WORKSPACE;
         a.partial = static_cast<float *>(workspace);
-        a.tickets = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + need) - bsa::kNormTickets;
     }
     return bsa::launch_gated_norm_backward(a, static_cast<cudaStream_t>(stream));
 }
@@ -463,8 +462,7 @@ bsa_status bsa_gated_norm_workspace_size(int B, int N, int C, size_t *bytes)
     if (B < 1 || N < 1 || static_cast<int64_t>(B) * N > INT32_MAX || C < 8 || C > 8192 || C % 8 != 0) return BSA_ERR_SHAPE;
     const int64_t rows = static_cast<int64_t>(B) * N;
     *bytes = sizeof(float) * static_cast<size_t>(bsa::gated_norm_max_workers(rows, C)) *
-                 static_cast<size_t>(bsa::gated_norm_worker_floats(C)) +
-             sizeof(uint32_t) * bsa::kNormTickets;
+             static_cast<size_t>(bsa::gated_norm_worker_floats(C));
     return BSA_OK;
 }
 

@@ -50,7 +50,6 @@ struct NormArgs {
     char *dgate, *dscale, *dshift;
     float *dpost_w, *dpost_b, *dpre_w, *dpre_b;
     float *partial;  // backward: partial column sums
-    uint32_t *tickets;  // behind them: how many CTAs are done with 32 channels (zeroed by the first kernel)
 };
 
 // Backward: the rows are cut into contiguous ranges, one per worker (a CTA). kNormMaxThreads bounds the
@@ -60,7 +59,6 @@ constexpr int64_t kNormMaxThreads = 152 * 512;
 int64_t gated_norm_max_workers(int64_t rows, int C);
 // floats of partial sums per worker: 4 sums of the first group that it shares with others, of the last, and for weights
 __host__ __device__ inline int64_t gated_norm_worker_floats(int C) { return int64_t(12) * C; }
-constexpr int kNormTickets = 256;  // 8192 channels
 bsa_status launch_gated_norm(const NormArgs &a, cudaStream_t st);
 bsa_status launch_gated_norm_backward(const NormArgs &a, cudaStream_t st);
 

@@ -69,6 +69,24 @@ __device__ __forceinline__ void write_group(const NormArgs &a, int64_t g, int c,
     }
 }
 
+// a group's sums, weighted for the parameters that all groups share
+template <int P>
+__device__ __forceinline__ void weight(const bsa_gated_norm_desc &d, int g, int c, f2 (&sA)[P], f2 (&sS)[P], f2 (&sP)[P],
+                                       f2 (&sQ)[P])
+{
+    const int b = g / d.F, f = g % d.F;
+    if (d.scale.ptr) {
+        times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sA);
+        times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sS);
+    }
+    if (d.gate.ptr) {
+        times(d.gate.ptr, d.mod_dt, b * d.gate.batch + f * d.gate.frame + c, sP);
+        times(d.gate.ptr, d.mod_dt, b * d.gate.batch + f * d.gate.frame + c, sQ);
+    }
+#pragma unroll
+    for (int j = 0; j < P; ++j) sP[j] = mul2(sP[j], twice(d.alpha)), sQ[j] = mul2(sQ[j], twice(d.alpha));
+}
+
 // Adds one of the sums over the teams, in their order, into the first team's registers. shared: C floats per team.
 template <int K, int P, typename R>
 __device__ __forceinline__ void join_teams(f2 (&v)[K][P], const R &rw, int team, int teams, float *shared)
@@ -107,8 +125,6 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
               at_y = at_dz + (pre ? K * threads * BB : 0), stage_bytes = at_y + (has_y ? K * threads * BB : 0);
     Row<K, P, MULTI, LN> rw(C, tpr, buf);
     const Wants want = wants_of(a);
-    if (a.partial && blockIdx.x == 0)
-        for (int i = threadIdx.x; i < kNormTickets; i += threads) a.tickets[i] = 0;
 
     // all that depends on the CTA's rows alone is uniform
     const int worker = blockIdx.x, teams = MULTI ? threads / tpr : 1, team = MULTI ? threadIdx.x / tpr : 0;
@@ -398,7 +414,6 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
             const int64_t begin = static_cast<int64_t>(group) * rg.per_group;
             const bool whole = !rg.long_groups && begin >= first && begin + rg.per_group <= end;
             float *const slot = slots + (group == first_group ? 0 : 4 * C);
-            const int b = group / d.F, f = group % d.F;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (!rw.on[k]) continue;
@@ -415,20 +430,8 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
                 }
                 // weighted for the parameters that all groups share, and added up
                 if (want.weights && !rg.long_groups && team == 0) {
-                    if (d.scale.ptr) {
-                        times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sA[k]);
-                        times_one_plus(d.scale.ptr, d.mod_dt, b * d.scale.batch + f * d.scale.frame + c, sS[k]);
-                    }
-                    if (d.gate.ptr) {
-                        times(d.gate.ptr, d.mod_dt, b * d.gate.batch + f * d.gate.frame + c, sP[k]);
-                        times(d.gate.ptr, d.mod_dt, b * d.gate.batch + f * d.gate.frame + c, sQ[k]);
-                    }
+                    weight(d, group, c, sA[k], sS[k], sP[k], sQ[k]);
                     float *const sum = slots + 8 * C + c;
-#pragma unroll
-                    for (int j = 0; j < P; ++j) {
-                        sP[k][j] = mul2(sP[k][j], twice(d.alpha));
-                        sQ[k][j] = mul2(sQ[k][j], twice(d.alpha));
-                    }
                     if (weighed) {
                         f2 before[4][P];
 #pragma unroll
@@ -458,62 +461,43 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     }
 }
 
-// Adds the workers' slots, 32 channels per CTA (four per thread), slices of 8 threads each taking every so many-th
-// worker:
-//   long groups     group y: its modulations' gradients; its sums, weighted for the parameters that all groups share, go
-//                   into the third slot of worker y, and the last CTA of the channels adds those of all groups
-//   short groups    (x alone) first the weights' third slots over all workers, then the groups that several workers share
-constexpr int kMaxSlices = 64;
+// Adds the workers' slots, kStrip channels per CTA: a warp takes four quads of channels from eight slots at a time.
+//   long groups     the warps are split into as many teams as there are groups (a power of two), each adding up every
+//                   so many-th group, writing its modulations' gradients and weighting its sums for the parameters that
+//                   all groups share; those of all teams are added in the end
+//   short groups    the weights' third slots of all workers; further CTAs, one each for the groups that workers share
+constexpr int kStrip = 16, kSumsWarps = 16;
 
 struct Quad {
     float4 v[4];  // A, S, P, Q of four channels
 };
 
-// the sums of slots[w * stride] over w = w0 .. w1, this thread's share
-__device__ __forceinline__ void add_slots(const float *slots, int64_t stride, int C, int w0, int w1, Quad &q)
+__device__ __forceinline__ void add(float4 &a, const float4 &b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
+
+// the sums of slots[w * stride] over w = w0, w0 + step ... w1
+__device__ __forceinline__ void add_slots(const float *slots, int64_t stride, int C, int w0, int w1, int step, Quad &q)
 {
-    const int slices = blockDim.x / 8;
 #pragma unroll 2
-    for (int w = w0 + static_cast<int>(threadIdx.x) / 8; w <= w1; w += slices) {
+    for (int w = w0; w <= w1; w += step) {
         const float *p = slots + w * stride;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 x = *reinterpret_cast<const float4 *>(p + k * C);
-            q.v[k].x += x.x, q.v[k].y += x.y, q.v[k].z += x.z, q.v[k].w += x.w;
-        }
+        for (int k = 0; k < 4; ++k) add(q.v[k], *reinterpret_cast<const float4 *>(p + k * C));
     }
 }
 
-// the CTA's sums of all slices, in the order of the slices: s[k] of channel threadIdx.x, for threads below 32
-__device__ __forceinline__ void join_slices(Quad &q, float (*part)[4][32], float (&s)[4])
+// over the eight slots of a warp, in every lane
+__device__ __forceinline__ void join_lanes(Quad &q)
 {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int o = 8; o < 32; o <<= 1) {
+        for (int o = 4; o < 32; o <<= 1) {
             q.v[k].x += __shfl_xor_sync(0xffffffffu, q.v[k].x, o);
             q.v[k].y += __shfl_xor_sync(0xffffffffu, q.v[k].y, o);
             q.v[k].z += __shfl_xor_sync(0xffffffffu, q.v[k].z, o);
             q.v[k].w += __shfl_xor_sync(0xffffffffu, q.v[k].w, o);
         }
-        if (threadIdx.x % 32 < 8) *reinterpret_cast<float4 *>(&part[threadIdx.x / 32][k][4 * (threadIdx.x % 8)]) = q.v[k];
     }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            s[k] = 0.0f;
-            for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) s[k] += part[i][k][threadIdx.x];
-        }
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ float modulation(const bsa_modulation &m, int dt, int b, int f, int c)
-{
-    const int64_t at = b * m.batch + f * m.frame + c;
-    return dt == BSA_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(m.ptr)[at])
-                          : static_cast<const float *>(m.ptr)[at];
 }
 
 // short groups: the gradients of a group that two or more workers share
@@ -538,101 +522,98 @@ __device__ __forceinline__ void write_cut_group(const NormArgs &a, const Ranges 
     }
 }
 
-__global__ void __launch_bounds__(8 * kMaxSlices, 2) gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg,
-                                                                            int64_t n_groups)
+__global__ void __launch_bounds__(32 * kSumsWarps, 2) gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg,
+                                                                             int64_t n_groups)
 {
-    __shared__ __align__(16) float part[kMaxSlices / 4][4][32];
-    __shared__ int last;
-    grid_dependency_wait();
+    __shared__ float4 part[kSumsWarps][4][4];  // [warp][sum][quad]
     const bsa_gated_norm_desc &d = a.d;
-    const int C = d.C;
+    const int C = d.C, strips = (C + kStrip - 1) / kStrip;
     const int64_t stride = gated_norm_worker_floats(C);
     const Wants want = wants_of(a);
-    int w0 = 0, w1 = rg.workers - 1;
-    int64_t group = -1;
-    const int strips = (C + 31) / 32;
-    if (rg.long_groups) {
-        group = blockIdx.y;
-        w0 = rg.worker_of(group * rg.per_group);
-        w1 = rg.worker_of((group + 1) * rg.per_group - 1);
-    } else if (static_cast<int>(blockIdx.x) >= strips) {
+    grid_dependency_wait();
+    if (static_cast<int>(blockIdx.x) >= strips) {
         // the group itself where there are at most as many groups as workers; else the one that the range begins inside
         const int i = blockIdx.x - strips;
-        group = n_groups <= rg.workers ? i : rg.first(i) / rg.per_group;
-        w0 = rg.worker_of(group * rg.per_group);
-        w1 = rg.worker_of((group + 1) * rg.per_group - 1);
+        const int64_t group = n_groups <= rg.workers ? i : rg.first(i) / rg.per_group;
+        const int w0 = rg.worker_of(group * rg.per_group), w1 = rg.worker_of((group + 1) * rg.per_group - 1);
         if (w0 == w1 || (n_groups > rg.workers && i != w0 + 1)) return;  // written by its worker, or by another CTA
         write_cut_group(a, rg, static_cast<int>(group), w0, w1);
         return;
-    } else if (!want.weights) {
-        return;
     }
-    const int c = blockIdx.x * 32 + 4 * (threadIdx.x % 8), ch = blockIdx.x * 32 + threadIdx.x;
-    const bool mine = threadIdx.x < 32 && ch < C;
-    float *const slots = a.partial + (c < C ? c : 0);
-    Quad q = {};
-    float s[4];
-    if (group < 0) {
-        add_slots(slots + 8 * C, stride, C, w0, w1, q);
-    } else {
-        // a group is the first in the ranges of its workers but, perhaps, that of the first of them
-        if (rg.first(w0) / rg.per_group != group) {
-            if (threadIdx.x < 8) add_slots(slots + 4 * C, stride, C, w0, w0, q);
-            ++w0;
+    if (!rg.long_groups && !want.weights) return;
+
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, quad = lane % 4, c = blockIdx.x * kStrip + 4 * quad;
+    const float *const slots = a.partial + (c < C ? c : 0);
+    int teams = 1;
+    if (rg.long_groups)
+        while (2 * teams <= kSumsWarps && 2 * teams <= n_groups) teams *= 2;
+    const int size = kSumsWarps / teams, team = warp / size, in = warp % size;  // warps of a team
+    const bool writes = in == 0 && lane < 4 && c < C;
+    Quad all = {};  // for the weights
+    for (int64_t g0 = 0; g0 < (rg.long_groups ? n_groups : 1); g0 += teams) {
+        const int group = static_cast<int>(g0) + team;
+        const bool some = !rg.long_groups || group < n_groups;
+        Quad q = {};
+        if (!rg.long_groups) {
+            add_slots(slots + 8 * C, stride, C, in * 8 + lane / 4, rg.workers - 1, 8 * size, q);
+        } else if (some) {
+            // a group is the first in the ranges of its workers but, perhaps, that of the first of them
+            int w0 = rg.worker_of(group * rg.per_group);
+            const int w1 = rg.worker_of((group + 1) * rg.per_group - 1);
+            if (rg.first(w0) / rg.per_group != group) {
+                if (in == 0 && lane < 4) add_slots(slots + 4 * C, stride, C, w0, w0, 1, q);
+                ++w0;
+            }
+            add_slots(slots, stride, C, w0 + in * 8 + lane / 4, w1, 8 * size, q);
         }
-        add_slots(slots, stride, C, w0, w1, q);
-    }
-    join_slices(q, part, s);
-    auto put_weights = [&] {
-        if (a.dpre_b) a.dpre_b[ch] = s[0];
-        if (a.dpre_w) a.dpre_w[ch] = s[1];
-        if (a.dpost_b) a.dpost_b[ch] = s[2];
-        if (a.dpost_w) a.dpost_w[ch] = s[3];
-    };
-    if (group < 0) {
-        if (mine) put_weights();
-        return;
-    }
-    if (mine) {
-        auto put = [&](char *p, float x) {
-            const int64_t i = group * C + ch;
-            if (d.mod_dt == BSA_BF16)
-                reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
-            else
-                reinterpret_cast<float *>(p)[i] = x;
-        };
-        auto by = [&](const float *w, float one, float x) { return (w ? w[ch] : one) * x; };
-        if (a.dshift) put(a.dshift, s[0]);
-        if (a.dscale) put(a.dscale, by(d.pre.weight, 1.0f, s[1]) + by(d.pre.bias, 0.0f, s[0]));
-        if (a.dgate) put(a.dgate, d.alpha * (by(d.post.weight, 1.0f, s[3]) + by(d.post.bias, 0.0f, s[2])));
-    }
-    if (!want.weights || !rg.long_groups) return;
-    const int b = static_cast<int>(group) / d.F, f = static_cast<int>(group) % d.F;
-    if (mine) {
-        const float m = d.scale.ptr ? 1.0f + modulation(d.scale, d.mod_dt, b, f, ch) : 1.0f;
-        const float g = d.alpha * (d.gate.ptr ? modulation(d.gate, d.mod_dt, b, f, ch) : 1.0f);
-        s[0] *= m, s[1] *= m, s[2] *= g, s[3] *= g;
-        if (n_groups == 1) {
-            put_weights();
-        } else {
-            float *const to = a.partial + group * stride + 8 * C + ch;
+        join_lanes(q);
+        if (size > 1) {
+            if (lane < 4) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) to[k * C] = s[k];
+                for (int k = 0; k < 4; ++k) part[warp][k][quad] = q.v[k];
+            }
+            __syncthreads();
+            if (writes) {
+                for (int i = 1; i < size; ++i) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) add(q.v[k], part[warp + i][k][quad]);
+                }
+            }
+            __syncthreads();
+        }
+        if (!writes || !some) continue;
+        f2 s[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k][0] = pair(q.v[k].x, q.v[k].y), s[k][1] = pair(q.v[k].z, q.v[k].w);
+        if (rg.long_groups) {
+            write_group<2>(a, group, c, s[0], s[1], s[2], s[3]);
+            if (want.weights) weight<2>(d, group, c, s[0], s[1], s[2], s[3]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            split(s[k][0], q.v[k].x, q.v[k].y);
+            split(s[k][1], q.v[k].z, q.v[k].w);
+            add(all.v[k], q.v[k]);
         }
     }
-    if (n_groups == 1) return;
-    if (threadIdx.x < 32) {  // the writers above
-        __threadfence();
-        __syncwarp();
+    if (!want.weights) return;
+    if (teams > 1) {
+        if (in == 0 && lane < 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) part[team][k][quad] = all.v[k];
+        }
+        __syncthreads();
+        if (warp > 0) return;
+        for (int i = 1; i < teams; ++i) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) add(all.v[k], part[i][k][quad]);
+        }
     }
-    if (threadIdx.x == 0) last = atomicAdd(a.tickets + blockIdx.x, 1u) == gridDim.y - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    q = Quad{};
-    add_slots(slots + 8 * C, stride, C, 0, static_cast<int>(n_groups) - 1, q);
-    join_slices(q, part, s);
-    if (mine) put_weights();
+    if (warp > 0 || !writes) return;
+    if (a.dpre_b) *reinterpret_cast<float4 *>(a.dpre_b + c) = all.v[0];
+    if (a.dpre_w) *reinterpret_cast<float4 *>(a.dpre_w + c) = all.v[1];
+    if (a.dpost_b) *reinterpret_cast<float4 *>(a.dpost_b + c) = all.v[2];
+    if (a.dpost_w) *reinterpret_cast<float4 *>(a.dpost_w + c) = all.v[3];
 }
 
 template <typename TS, typename TB, int REGS, bool MULTI, bool POST, bool LN>
@@ -652,14 +633,9 @@ bsa_status backward(const NormArgs &a, int sms, cudaStream_t st)
     if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     if (a.partial == nullptr) return BSA_OK;
     const int64_t n_groups = static_cast<int64_t>(a.d.B) * a.d.F;
-    // as many slices as a group has workers
-    int slices = kMaxSlices;
-    if (s.rg.long_groups)
-        while (slices > 8 && slices / 2 >= s.rg.workers / n_groups + 2) slices /= 2;
-    const unsigned strips = (a.d.C + 31) / 32;
-    const dim3 grid = s.rg.long_groups ? dim3(strips, static_cast<unsigned>(n_groups))
-                                       : dim3(strips + static_cast<unsigned>(n_groups < s.rg.workers ? n_groups : s.rg.workers));
-    return pdl_launch(gated_norm_sums_kernel, grid, 8 * slices, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
+    const unsigned strips = (a.d.C + kStrip - 1) / kStrip;
+    const unsigned cut = s.rg.long_groups ? 0 : static_cast<unsigned>(n_groups < s.rg.workers ? n_groups : s.rg.workers);
+    return pdl_launch(gated_norm_sums_kernel, dim3(strips + cut), 32 * kSumsWarps, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
 }
 
 }  // namespace
