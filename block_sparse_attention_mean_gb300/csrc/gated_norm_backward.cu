@@ -462,10 +462,12 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
 }
 
 // Adds the workers' slots, kStrip channels per CTA: a warp takes four quads of channels from eight slots at a time.
-//   long groups     the warps are split into as many teams as there are groups (a power of two), each adding up every
-//                   so many-th group, writing its modulations' gradients and weighting its sums for the parameters that
-//                   all groups share; those of all teams are added in the end
-//   short groups    the weights' third slots of all workers; further CTAs, one each for the groups that workers share
+//   few long groups   the warps are split into as many teams as there are groups (a power of two), each adding up one
+//                     group or two, writing its modulations' gradients and weighting its sums for the parameters that all
+//                     groups share; those of all teams are added in the end
+//   more long groups  all workers' slots, weighted, for those parameters; further CTAs, one for each group, write its
+//                     modulations' gradients (256 groups, 16384 rows of 2048 channels: 118 us with a row of CTAs per 16)
+//   short groups      the weights' third slots of all workers; further CTAs, one each for the groups that workers share
 constexpr int kStrip = 16, kSumsWarps = 16;
 
 struct Quad {
@@ -500,13 +502,14 @@ __device__ __forceinline__ void join_lanes(Quad &q)
     }
 }
 
-// short groups: the gradients of a group that two or more workers share
+// the gradients of a group that several workers share (short groups), or any number
 __device__ __forceinline__ void write_cut_group(const NormArgs &a, const Ranges &rg, int group, int w0, int w1)
 {
     const int C = a.d.C;
     const int64_t stride = gated_norm_worker_floats(C);
     for (int c = 4 * threadIdx.x; c < C; c += 4 * blockDim.x) {
         f2 s[4][2] = {};
+#pragma unroll 2
         for (int w = w0; w <= w1; ++w) {
             // it is the first in the ranges of its workers but, perhaps, that of the first of them
             const float *p = a.partial + w * stride + (w == w0 && rg.first(w) / rg.per_group != group ? 4 * C : 0) + c;
@@ -536,27 +539,77 @@ __global__ void __launch_bounds__(32 * kSumsWarps, 2) gated_norm_sums_kernel(con
         const int i = blockIdx.x - strips;
         const int64_t group = n_groups <= rg.workers ? i : rg.first(i) / rg.per_group;
         const int w0 = rg.worker_of(group * rg.per_group), w1 = rg.worker_of((group + 1) * rg.per_group - 1);
-        if (w0 == w1 || (n_groups > rg.workers && i != w0 + 1)) return;  // written by its worker, or by another CTA
+        // written by its worker, or by another CTA
+        if (!rg.long_groups && (w0 == w1 || (n_groups > rg.workers && i != w0 + 1))) return;
         write_cut_group(a, rg, static_cast<int>(group), w0, w1);
         return;
     }
-    if (!rg.long_groups && !want.weights) return;
+    // the groups that this CTA looks at one by one; with none of them it adds up the weights' gradients alone
+    const int groups = rg.long_groups && n_groups <= kSumsWarps ? static_cast<int>(n_groups) : 0;
+    if (groups == 0 && !want.weights) return;
 
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, quad = lane % 4, c = blockIdx.x * kStrip + 4 * quad;
-    const float *const slots = a.partial + (c < C ? c : 0);
+    const int at = c < C ? c : 0;
+    const float *const slots = a.partial + at;
     int teams = 1;
-    if (rg.long_groups)
-        while (2 * teams <= kSumsWarps && 2 * teams <= n_groups) teams *= 2;
+    while (2 * teams <= groups) teams *= 2;
     const int size = kSumsWarps / teams, team = warp / size, in = warp % size;  // warps of a team
+    const int slice = in * 8 + lane / 4, slices = 8 * size;
     const bool writes = in == 0 && lane < 4 && c < C;
     Quad all = {};  // for the weights
-    for (int64_t g0 = 0; g0 < (rg.long_groups ? n_groups : 1); g0 += teams) {
-        const int group = static_cast<int>(g0) + team;
-        const bool some = !rg.long_groups || group < n_groups;
-        Quad q = {};
+    auto weighted = [&](int group, const Quad &q) {
+        f2 s[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k][0] = pair(q.v[k].x, q.v[k].y), s[k][1] = pair(q.v[k].z, q.v[k].w);
+        weight<2>(d, group, at, s[0], s[1], s[2], s[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float4 x;
+            split(s[k][0], x.x, x.y);
+            split(s[k][1], x.z, x.w);
+            add(all.v[k], x);
+        }
+    };
+    // a team's sums, in its first lanes
+    auto join = [&](Quad &q) {
+        join_lanes(q);
+        if (size == 1) return;
+        if (lane < 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) part[warp][k][quad] = q.v[k];
+        }
+        __syncthreads();
+        if (writes) {
+            for (int i = 1; i < size; ++i) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) add(q.v[k], part[warp + i][k][quad]);
+            }
+        }
+        __syncthreads();
+    };
+    if (groups == 0) {
         if (!rg.long_groups) {
-            add_slots(slots + 8 * C, stride, C, in * 8 + lane / 4, rg.workers - 1, 8 * size, q);
-        } else if (some) {
+            add_slots(slots + 8 * C, stride, C, slice, rg.workers - 1, slices, all);
+        } else {
+            for (int w = slice; w < rg.workers; w += slices) {
+                const int group = rg.first(w) / rg.per_group;
+                Quad q = {};
+                add_slots(slots, stride, C, w, w, 1, q);
+                weighted(group, q);
+                if ((rg.first(w + 1) - 1) / rg.per_group != group) {
+                    q = Quad{};
+                    add_slots(slots + 4 * C, stride, C, w, w, 1, q);
+                    weighted(group + 1, q);
+                }
+            }
+        }
+        join(all);
+    }
+    for (int g0 = 0; g0 < groups; g0 += teams) {
+        const int group = g0 + team;
+        const bool some = group < groups;
+        Quad q = {};
+        if (some) {
             // a group is the first in the ranges of its workers but, perhaps, that of the first of them
             int w0 = rg.worker_of(group * rg.per_group);
             const int w1 = rg.worker_of((group + 1) * rg.per_group - 1);
@@ -564,37 +617,15 @@ __global__ void __launch_bounds__(32 * kSumsWarps, 2) gated_norm_sums_kernel(con
                 if (in == 0 && lane < 4) add_slots(slots + 4 * C, stride, C, w0, w0, 1, q);
                 ++w0;
             }
-            add_slots(slots, stride, C, w0 + in * 8 + lane / 4, w1, 8 * size, q);
+            add_slots(slots, stride, C, w0 + slice, w1, slices, q);
         }
-        join_lanes(q);
-        if (size > 1) {
-            if (lane < 4) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) part[warp][k][quad] = q.v[k];
-            }
-            __syncthreads();
-            if (writes) {
-                for (int i = 1; i < size; ++i) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) add(q.v[k], part[warp + i][k][quad]);
-                }
-            }
-            __syncthreads();
-        }
+        join(q);
         if (!writes || !some) continue;
         f2 s[4][2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[k][0] = pair(q.v[k].x, q.v[k].y), s[k][1] = pair(q.v[k].z, q.v[k].w);
-        if (rg.long_groups) {
-            write_group<2>(a, group, c, s[0], s[1], s[2], s[3]);
-            if (want.weights) weight<2>(d, group, c, s[0], s[1], s[2], s[3]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            split(s[k][0], q.v[k].x, q.v[k].y);
-            split(s[k][1], q.v[k].z, q.v[k].w);
-            add(all.v[k], q.v[k]);
-        }
+        write_group<2>(a, group, c, s[0], s[1], s[2], s[3]);
+        if (want.weights) weighted(group, q);
     }
     if (!want.weights) return;
     if (teams > 1) {
@@ -634,7 +665,7 @@ bsa_status backward(const NormArgs &a, int sms, cudaStream_t st)
     if (a.partial == nullptr) return BSA_OK;
     const int64_t n_groups = static_cast<int64_t>(a.d.B) * a.d.F;
     const unsigned strips = (a.d.C + kStrip - 1) / kStrip;
-    const unsigned cut = s.rg.long_groups ? 0 : static_cast<unsigned>(n_groups < s.rg.workers ? n_groups : s.rg.workers);
+    const unsigned cut = s.rg.long_groups && n_groups <= kSumsWarps ? 0 : static_cast<unsigned>(n_groups < s.rg.workers ? n_groups : s.rg.workers);
     return pdl_launch(gated_norm_sums_kernel, dim3(strips + cut), 32 * kSumsWarps, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
 }
 
