@@ -20,18 +20,21 @@
 namespace bsa {
 namespace {
 
+// Which of the sums A, S, P, Q (bits 0 to 3) the gradients that are asked for need, and whether those of weights are among
+// them. The others are neither written nor read: most blocks have no norm with a bias behind the branch, and need no P.
 struct Wants {
-    bool pre_sums, post_sums, weights;
-};
+    unsigned sums;
+    bool weights;
 
-__device__ __forceinline__ Wants wants_of(const NormArgs &a)
-{
-    Wants w;
-    w.pre_sums = a.dscale || a.dshift || a.dpre_w || a.dpre_b;
-    w.post_sums = a.dgate || a.dpost_w || a.dpost_b;
-    w.weights = a.dpre_w || a.dpre_b || a.dpost_w || a.dpost_b;
-    return w;
-}
+    __device__ __forceinline__ explicit Wants(const NormArgs &a)
+    {
+        const bool A = a.dshift || a.dpre_b || (a.dscale && a.d.pre.bias), S = a.dscale || a.dpre_w,
+                   P = a.dpost_b || (a.dgate && a.d.post.bias), Q = a.dgate || a.dpost_w;
+        sums = A | S << 1 | P << 2 | Q << 3;
+        weights = a.dpre_w || a.dpre_b || a.dpost_w || a.dpost_b;
+    }
+    __device__ __forceinline__ bool has(int k) const { return sums >> k & 1u; }
+};
 
 // o = one * w + zero * b for a norm's weight and bias at channels c ..
 template <int P>
@@ -124,7 +127,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
     const int at_dh = pre ? K * threads * SB : 0, at_dz = at_dh + (has_dh ? K * threads * SB : 0),
               at_y = at_dz + (pre ? K * threads * BB : 0), stage_bytes = at_y + (has_y ? K * threads * BB : 0);
     Row<K, P, MULTI, LN> rw(C, tpr, buf);
-    const Wants want = wants_of(a);
+    const Wants want(a);
 
     // all that depends on the CTA's rows alone is uniform
     const int worker = blockIdx.x, teams = MULTI ? threads / tpr : 1, team = MULTI ? threadIdx.x / tpr : 0;
@@ -404,7 +407,7 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
         }
         if (here.row < here.stop) continue;
         // the end of a group, or of the range
-        if (want.pre_sums || want.post_sums) {
+        if (want.sums) {
             if (teams > 1) {
                 join_teams<K, P>(sA, rw, team, teams, shared);
                 join_teams<K, P>(sS, rw, team, teams, shared);
@@ -423,10 +426,10 @@ __global__ void __maxnreg__(REGS) gated_norm_backward_kernel(const __grid_consta
                 } else if (whole) {
                     write_group(a, group, c, sA[k], sS[k], sP[k], sQ[k]);
                 } else {
-                    Unit<float, P>::put(slot + c, sA[k]);
-                    Unit<float, P>::put(slot + C + c, sS[k]);
-                    Unit<float, P>::put(slot + 2 * C + c, sP[k]);
-                    Unit<float, P>::put(slot + 3 * C + c, sQ[k]);
+                    if (want.has(0)) Unit<float, P>::put(slot + c, sA[k]);
+                    if (want.has(1)) Unit<float, P>::put(slot + C + c, sS[k]);
+                    if (want.has(2)) Unit<float, P>::put(slot + 2 * C + c, sP[k]);
+                    if (want.has(3)) Unit<float, P>::put(slot + 3 * C + c, sQ[k]);
                 }
                 // weighted for the parameters that all groups share, and added up
                 if (want.weights && !rg.long_groups && team == 0) {
@@ -477,13 +480,14 @@ struct Quad {
 __device__ __forceinline__ void add(float4 &a, const float4 &b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
 
 // the sums of slots[w * stride] over w = w0, w0 + step ... w1
-__device__ __forceinline__ void add_slots(const float *slots, int64_t stride, int C, int w0, int w1, int step, Quad &q)
+__device__ __forceinline__ void add_slots(const float *slots, int64_t stride, int C, int w0, int w1, int step, const Wants &want, Quad &q)
 {
 #pragma unroll 2
     for (int w = w0; w <= w1; w += step) {
         const float *p = slots + w * stride;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) add(q.v[k], *reinterpret_cast<const float4 *>(p + k * C));
+        for (int k = 0; k < 4; ++k)
+            if (want.has(k)) add(q.v[k], *reinterpret_cast<const float4 *>(p + k * C));
     }
 }
 
@@ -503,7 +507,7 @@ __device__ __forceinline__ void join_lanes(Quad &q)
 }
 
 // the gradients of a group that several workers share (short groups), or any number
-__device__ __forceinline__ void write_cut_group(const NormArgs &a, const Ranges &rg, int group, int w0, int w1)
+__device__ __forceinline__ void write_cut_group(const NormArgs &a, const Ranges &rg, const Wants &want, int group, int w0, int w1)
 {
     const int C = a.d.C;
     const int64_t stride = gated_norm_worker_floats(C);
@@ -515,6 +519,7 @@ __device__ __forceinline__ void write_cut_group(const NormArgs &a, const Ranges 
             const float *p = a.partial + w * stride + (w == w0 && rg.first(w) / rg.per_group != group ? 4 * C : 0) + c;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+                if (!want.has(k)) continue;
                 f2 q[2];
                 Unit<float, 2>::get(p + k * C, q);
                 s[k][0] = add2(s[k][0], q[0]);
@@ -525,14 +530,15 @@ __device__ __forceinline__ void write_cut_group(const NormArgs &a, const Ranges 
     }
 }
 
-__global__ void __launch_bounds__(32 * kSumsWarps, 2) gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg,
-                                                                             int64_t n_groups)
+template <int PER_SM>
+__global__ void __launch_bounds__(32 * kSumsWarps, PER_SM)
+    gated_norm_sums_kernel(const __grid_constant__ NormArgs a, Ranges rg, int64_t n_groups)
 {
     __shared__ float4 part[kSumsWarps][4][4];  // [warp][sum][quad]
     const bsa_gated_norm_desc &d = a.d;
     const int C = d.C, strips = (C + kStrip - 1) / kStrip;
     const int64_t stride = gated_norm_worker_floats(C);
-    const Wants want = wants_of(a);
+    const Wants want(a);
     grid_dependency_wait();
     if (static_cast<int>(blockIdx.x) >= strips) {
         // the group itself where there are at most as many groups as workers; else the one that the range begins inside
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(32 * kSumsWarps, 2) gated_norm_sums_kernel(con
         const int w0 = rg.worker_of(group * rg.per_group), w1 = rg.worker_of((group + 1) * rg.per_group - 1);
         // written by its worker, or by another CTA
         if (!rg.long_groups && (w0 == w1 || (n_groups > rg.workers && i != w0 + 1))) return;
-        write_cut_group(a, rg, static_cast<int>(group), w0, w1);
+        write_cut_group(a, rg, want, static_cast<int>(group), w0, w1);
         return;
     }
     // the groups that this CTA looks at one by one; with none of them it adds up the weights' gradients alone
@@ -589,16 +595,16 @@ __global__ void __launch_bounds__(32 * kSumsWarps, 2) gated_norm_sums_kernel(con
     };
     if (groups == 0) {
         if (!rg.long_groups) {
-            add_slots(slots + 8 * C, stride, C, slice, rg.workers - 1, slices, all);
+            add_slots(slots + 8 * C, stride, C, slice, rg.workers - 1, slices, want, all);
         } else {
             for (int w = slice; w < rg.workers; w += slices) {
                 const int group = rg.first(w) / rg.per_group;
                 Quad q = {};
-                add_slots(slots, stride, C, w, w, 1, q);
+                add_slots(slots, stride, C, w, w, 1, want, q);
                 weighted(group, q);
                 if ((rg.first(w + 1) - 1) / rg.per_group != group) {
                     q = Quad{};
-                    add_slots(slots + 4 * C, stride, C, w, w, 1, q);
+                    add_slots(slots + 4 * C, stride, C, w, w, 1, want, q);
                     weighted(group + 1, q);
                 }
             }
@@ -614,10 +620,10 @@ __global__ void __launch_bounds__(32 * kSumsWarps, 2) gated_norm_sums_kernel(con
             int w0 = rg.worker_of(group * rg.per_group);
             const int w1 = rg.worker_of((group + 1) * rg.per_group - 1);
             if (rg.first(w0) / rg.per_group != group) {
-                if (in == 0 && lane < 4) add_slots(slots + 4 * C, stride, C, w0, w0, 1, q);
+                if (in == 0 && lane < 4) add_slots(slots + 4 * C, stride, C, w0, w0, 1, want, q);
                 ++w0;
             }
-            add_slots(slots, stride, C, w0 + slice, w1, slices, q);
+            add_slots(slots, stride, C, w0 + slice, w1, slices, want, q);
         }
         join(q);
         if (!writes || !some) continue;
@@ -666,7 +672,11 @@ bsa_status backward(const NormArgs &a, int sms, cudaStream_t st)
     const int64_t n_groups = static_cast<int64_t>(a.d.B) * a.d.F;
     const unsigned strips = (a.d.C + kStrip - 1) / kStrip;
     const unsigned cut = s.rg.long_groups && n_groups <= kSumsWarps ? 0 : static_cast<unsigned>(n_groups < s.rg.workers ? n_groups : s.rg.workers);
-    return pdl_launch(gated_norm_sums_kernel, dim3(strips + cut), 32 * kSumsWarps, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
+    const unsigned ctas = strips + cut;
+    // one CTA per SM, which spills no registers, unless there are more of them than SMs (us with one and with two: 16384 rows
+    // of 2048 channels, 128 CTAs, 88.4 and 90.4; 8192 rows of 4096 channels, 256 CTAs, 122.3 and 119.2)
+    auto sums = ctas <= static_cast<unsigned>(sms) ? gated_norm_sums_kernel<1> : gated_norm_sums_kernel<2>;
+    return pdl_launch(sums, dim3(ctas), 32 * kSumsWarps, 0, st, a, s.rg, n_groups) ? BSA_OK : BSA_ERR_CUDA;
 }
 
 }  // namespace
