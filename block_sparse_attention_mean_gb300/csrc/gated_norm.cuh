@@ -21,9 +21,8 @@ __host__ __device__ constexpr int most_threads(int regs, bool multi, int branch_
 }
 
 // Rows in flight per worker, forward: more of them are slower (65536 rows of 2048 channels: three 181 us, four 196 us).
-// Backward two, which have more tensors each (three: 94.8 against 93.2 us for 16384 rows of 2048 channels bf16), or one
-// where the largest CTA has no room for two of `bytes` a thread beside the `kept` bytes (one in place of two: 172 against
-// 143 us, 2048 channels of fp32).
+// Backward two, which have more tensors each (16384 rows of 2048 channels bf16: one 110.8 us, two 87.4, three 87.9), or one
+// where the largest CTA has no room for two of `bytes` a thread beside the `kept` bytes.
 constexpr int kStages = 3;
 __host__ __device__ constexpr int stages_for(int threads, int bytes, int kept)
 {
@@ -175,7 +174,7 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
 
 // Vectors of 8 channels per thread. What a row costs a thread apart from its channels (the sums over the row, addresses,
 // the loop) is about as much as eight channels cost: with one vector, twice as many warps pay it (2048 channels bf16:
-// 193 against 182 us forward, 65536 rows; 109 against 93 us backward, 16384 rows). With more there are too few
+// 193 against 182 us forward, 65536 rows; 153 against 87 us backward, 16384 rows). With more there are too few
 // registers for the sums of the backward pass.
 constexpr int V = 2;
 
@@ -461,10 +460,10 @@ inline Shape shape_of(const bsa_gated_norm_desc &d, int regs, int sms, int stage
 // whether a layer norm is among the norms) for the kernel that a desc needs. Rows of up to MULTI threads share a CTA.
 // Registers: 168, or 128 where 168 do not fit (more than 384 threads; 320 with an fp32 branch, so that the backward pass
 // has room for two rows in flight) or, mostly, where they leave room for only half as many CTAs (224 and 256 threads, that
-// is 3080 to 4096 channels). The backward pass has the fewest registers to spare with a post norm or in fp32, and takes
-// fewer CTAs there. us with 168 and with 128, 4096 channels bf16: forward 32768 rows 206 and 195, layer norms 328 and 225;
-// backward 8192 rows 123 and 133, layer norms 158 and 162, no post norm 99 and 91; fp32 stream 137 and 162, no post norm
-// 121 and 133, layer norm alone 177 and 140. 320 threads, backward, 4096 rows: 93 and 123.
+// is 3080 to 4096 channels). The backward pass of an fp32 stream with a post norm has the fewest registers to spare, and
+// takes fewer CTAs there. us with 168 and with 128, 4096 channels: forward, 32768 rows bf16, 206 and 195, layer norms 328
+// and 225; backward, 8192 rows, bf16 119 and 121, layer norms 154 and 150, no post norm 94 and 79; fp32 stream 132 and 147,
+// no post norm 119 and 120. 320 threads, backward, 4096 rows: 89 and 117.
 template <int MULTI, bool BACKWARD, typename F>
 bsa_status by_kernel(const bsa_gated_norm_desc &d, F &&run)
 {
@@ -472,7 +471,7 @@ bsa_status by_kernel(const bsa_gated_norm_desc &d, F &&run)
         const int threads = row_threads(d.C / 8, V);
         const std::integral_constant<int, 168> regs;
         const bool halved = 65536 / (128 * threads) >= 2 * (65536 / (168 * threads)),
-                   rather = BACKWARD && (post.value || (sizeof(ts) == 4 && !ln.value));
+                   rather = BACKWARD && post.value && sizeof(ts) == 4;
         if (threads > most_threads(168, false, sizeof(tb)) || (threads > 128 && halved && !rather))
             return run(ts, tb, std::integral_constant<int, 128>(), std::false_type(), post, ln);
         return threads <= MULTI ? run(ts, tb, regs, std::true_type(), post, ln) : run(ts, tb, regs, std::false_type(), post, ln);
