@@ -359,6 +359,37 @@ def test_some_gradients_alone():
         assert torch.equal(out, getattr(full, name)), name
 
 
+@pytest.mark.parametrize("B,F,per_group,C", [(1, 2, 900, 520), (3, 1, 900, 264), (1, 5, 900, 1032), (2, 8, 900, 40),
+                                             (1, 17, 640, 264), (3, 7, 640, 1544), (1, 200, 64, 136), (8, 40, 32, 24)])
+def test_groups_of_many_rows(B, F, per_group, C):
+    both(131, B, F * per_group, C, F=F, post=("layer", "wb"), pre=("rms", "wb"))
+
+
+@pytest.mark.parametrize("F,N", [(1, 130), (4, 2400), (20, 4000), (1000, 2000)])
+def test_gradients_alone_with_biases(F, N):
+    """each gradient alone is the one that comes with the others: the sums that only others need may be missing"""
+    B, C = 1, 264
+    x, y, kw, rkw = make(121, B, N, C, F=F, post=("layer", "wb"), pre=("rms", "wb"))
+    dh, dz = draw(gen(122), B, N, C, dt=BF16), draw(gen(123), B, N, C, dt=BF16)
+    h = pkg.gated_norm(x, y, **kw)[0]
+    full = pkg.gated_norm_backward(dh, dz, h, y, **kw)
+    mod = lambda m: ob.Modulation(m.data_ptr(), m.stride(0), m.stride(1) if F > 1 else 0)  # noqa: E731
+    norm = lambda kind, n: ob.Norm(kind, n.eps, n.weight.data_ptr(), n.bias.data_ptr())  # noqa: E731
+    rows = lambda t: ob.Rows(t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+    desc = ob.GatedNormDesc(B, N, C, F, bb.BF16, bb.BF16, bb.BF16, 1.0, norm(ob.NORM_LAYER, kw["post"]),
+                            norm(ob.NORM_RMS, kw["pre"]), mod(kw["gate"]), mod(kw["scale"]), mod(kw["shift"]))
+    ws = pkg.gated_norm_workspace(B, N, C)
+    for name in NAMES:
+        out = torch.zeros_like(getattr(full, name))
+        ws.fill_(0xff)  # NaN, whichever sums are not written
+        g = ob.GatedNormGradArgs()
+        g.dh, g.dz, g.h, g.y = (rows(t) for t in (dh, dz, h, y))
+        setattr(g, name, rows(out) if name in ("dx", "dy") else out.data_ptr())
+        ob.bsa_gated_norm_backward(desc, g, ws, ws.numel())
+        torch.cuda.synchronize()
+        assert torch.equal(out, getattr(full, name)), name
+
+
 def test_helper_refusals():
     x, y, kw, _ = make(121, 2, 8, 64)
 
