@@ -3,7 +3,8 @@ per entry point with the same name (argument marshalling only), plus helpers tha
 check that they go together and allocate outputs and workspaces with torch.
 
 As in ``binding`` there is no fallback: if libbsa.so cannot be loaded every call raises. The helpers
-run on the tensors' device and on ``stream`` (that device's current stream by default).
+run on the tensors' device and on ``stream`` (that device's current stream by default), as under
+torch.cuda.stream(stream): what they allocate, results and workspace, belongs to that stream.
 """
 from __future__ import annotations
 
@@ -211,12 +212,28 @@ def _current_stream(index: int) -> int:
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)  # the same without an object
 
 
-def _run(what: str, fn, device: torch.device, stream, *args) -> None:
-    """fn(*args, stream) with `device` current: the library launches on the current device."""
-    if stream is None:
-        stream = _current_stream(device.index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
+def _elsewhere(stream, t: Optional[torch.Tensor], what: str):
+    """A context in which `stream` is current, or None where it is already. The helpers allocate on the current
+    stream, and the allocator hands a block on as soon as the work of the stream it was taken on allows: a workspace
+    taken on another stream than the kernels' would go to the next tensor while they still use it."""
+    if t is None:
+        return None  # refused by the helper
+    device = _cuda_device(t, what)
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise BsaError(ERR_INVALID_ARG, f"{what}: a stream of {stream.device}, the tensors are on {device}")
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if handle in (0, 1):  # the default stream, by either of its handles
+        handle, stream = 0, torch.cuda.default_stream(device)
+    if handle == _current_stream(device.index):
+        return None
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _run(what: str, fn, device: torch.device, *args) -> None:
+    """fn(*args, the device's current stream) with `device` current: the library launches on the current device."""
+    stream = _current_stream(device.index)
     if device.index == torch.cuda.current_device():
         code = fn(*args, stream)
     else:
@@ -327,6 +344,10 @@ def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor
     channels. Returns (q, k, v), None where none was given."""
     what = "rotary"
     first = q if q is not None else k if k is not None else v
+    if stream is not None and (there := _elsewhere(stream, first, what)):
+        with there:
+            return rotary(plan, q, k, v, positions=positions, norm_eps=norm_eps, q_weight=q_weight, k_weight=k_weight,
+                          out=out)
     device, dtype, code, B, N, pos, pos_batch, weights = _rotary_args(
         plan, first, positions, q is not None or k is not None, q_weight, k_weight, 1, what)
     d = plan.d
@@ -343,7 +364,7 @@ def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor
         desc[i] = _HEADS.pack(at, s[0], s[1], s[2], o_at, r[0], r[2], r[1], weights[i], h)
         res[i] = o
     norm = norm_eps is not None
-    _run("bsa_rotary", load().bsa_rotary, device, stream, ctypes.byref(plan), *desc, code, B, N, pos, pos_batch, norm,
+    _run("bsa_rotary", load().bsa_rotary, device, ctypes.byref(plan), *desc, code, B, N, pos, pos_batch, norm,
          norm_eps if norm else 0.0)
     return tuple(res)
 
@@ -365,6 +386,10 @@ def rotary_backward(plan: RotaryPlan, dq: Optional[torch.Tensor], dk: Optional[t
     (gq, gk, gv, gq_weight, gk_weight); a weight's gradient (fp32 [d]) where that weight is given."""
     what = "rotary_backward"
     first = dq if dq is not None else dk if dk is not None else dv
+    if stream is not None and (there := _elsewhere(stream, first, what)):
+        with there:
+            return rotary_backward(plan, dq, dk, dv, positions=positions, q=q, k=k, norm_eps=norm_eps,
+                                   q_weight=q_weight, k_weight=k_weight, out=out, ws=ws)
     device, dtype, code, B, N, pos, pos_batch, weights = _rotary_args(
         plan, first, positions, dq is not None or dk is not None, q_weight, k_weight, 2, what)
     norm, d = norm_eps is not None, plan.d
@@ -392,7 +417,7 @@ def rotary_backward(plan: RotaryPlan, dq: Optional[torch.Tensor], dk: Optional[t
         res[i] = o
     if ws is None and (dweights[0] is not None or dweights[1] is not None):
         ws = rotary_workspace(B, N, plan.d, device)
-    _run("bsa_rotary_backward", load().bsa_rotary_backward, device, stream, ctypes.byref(plan), *desc, code, B, N, pos,
+    _run("bsa_rotary_backward", load().bsa_rotary_backward, device, ctypes.byref(plan), *desc, code, B, N, pos,
          pos_batch, norm, norm_eps if norm else 0.0, _ptr(ws), _workspace_bytes(ws, device, what))
     return (*res, dweights[0], dweights[1])
 
@@ -462,6 +487,10 @@ def gated_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, gate: Optio
     modulations [B, C] or [B, F, C] (F frames of N / F tokens). Without y, h is x and is not written; without
     pre there is no z, whose dtype is y's (without y: that of out's z, branch_dtype or x's). Returns (h, z)."""
     what = "gated_norm"
+    if stream is not None and (there := _elsewhere(stream, x, what)):
+        with there:
+            return gated_norm(x, y, gate=gate, alpha=alpha, post=post, pre=pre, scale=scale, shift=shift, out=out,
+                              branch_dtype=branch_dtype)
     device = _cuda_device(x, what)
     if x.dim() != 3:
         raise BsaError(ERR_SHAPE, f"gated_norm: x has {x.dim()} dimensions, expected 3")
@@ -487,7 +516,7 @@ def gated_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, gate: Optio
         rows[3] = pack(at, s[0], s[1])
     desc, _ = _gated_desc(shape, device, _code(x, what), _CODES.get(branch_dtype, -1), alpha, post, pre, gate, scale,
                           shift, what)
-    _run("bsa_gated_norm", load().bsa_gated_norm, device, stream, desc, *rows)
+    _run("bsa_gated_norm", load().bsa_gated_norm, device, desc, *rows)
     return h, z
 
 
@@ -510,6 +539,10 @@ def gated_norm_backward(dh: Optional[torch.Tensor], dz: Optional[torch.Tensor], 
     first = dh if dh is not None else dz
     if first is None:
         raise BsaError(ERR_INVALID_ARG, f"{what}: neither dh nor dz")
+    if stream is not None and (there := _elsewhere(stream, first, what)):
+        with there:
+            return gated_norm_backward(dh, dz, h, y, gate=gate, alpha=alpha, post=post, pre=pre, scale=scale,
+                                       shift=shift, out=out, ws=ws)
     device = _cuda_device(first, what)
     if first.dim() != 3:
         raise BsaError(ERR_SHAPE, f"{what}: {first.dim()} dimensions, expected 3")
@@ -552,6 +585,6 @@ def gated_norm_backward(dh: Optional[torch.Tensor], dz: Optional[torch.Tensor], 
     if ws is None and any(at):
         ws = gated_norm_workspace(*shape, device)
     args = _GRADS.pack(*views, *at)
-    _run("bsa_gated_norm_backward", load().bsa_gated_norm_backward, device, stream, desc, args, _ptr(ws),
+    _run("bsa_gated_norm_backward", load().bsa_gated_norm_backward, device, desc, args, _ptr(ws),
          _workspace_bytes(ws, device, what))
     return GatedNormGrads(dx if pre is not None else dh, dy, *dmods, *dparams)

@@ -1,5 +1,6 @@
 """Checks of the operators around the attention that need no GPU: the header and the binding agree,
 the rotary plan's frequencies, and the refusals, which all happen before any launch."""
+import contextlib
 import ctypes
 import math
 import os
@@ -374,3 +375,54 @@ def test_helpers_refuse_host_tensors():
     refused(bb.ERR_INVALID_ARG, pkg.gated_norm, torch.zeros(1, 4, 64), pre=pkg.NormSpec("rms"))
     refused(bb.ERR_INVALID_ARG, pkg.gated_norm_backward, None, None, None)
     refused(bb.ERR_INVALID_ARG, pkg.NormSpec, "batch")
+
+
+@pytest.mark.parametrize("call", ["rotary_backward", "gated_norm_backward"])
+def test_workspace_is_allocated_on_the_calls_stream(monkeypatch, call):
+    """with the CUDA calls faked: what a helper allocates for a call on another stream is allocated while that stream
+    is current, and the launch goes to it"""
+    now, allocated, launched, plan = [7], [], [], _plan()
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.cuda_stream, self.device = handle, device
+
+    @contextlib.contextmanager
+    def current(stream):
+        now.append(stream.cuda_stream)
+        yield
+        now.pop()
+
+    real = ob.load()
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_size"):
+                return getattr(real, name)
+            return lambda *args: launched.append(args[-1]) or bb.OK
+
+    monkeypatch.setattr(ob, "load", Lib)
+    monkeypatch.setattr(ob, "_cuda_device", lambda t, what: t.device)
+    monkeypatch.setattr(ob, "_current_stream", lambda index: now[-1])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: Stream(0, device))
+    monkeypatch.setattr(torch.cuda, "stream", current)
+    for name in ("rotary_workspace", "gated_norm_workspace"):
+        made = getattr(ob, name)
+        monkeypatch.setattr(ob, name, lambda *args, made=made: allocated.append(now[-1]) or made(*args))
+
+    def run(stream):
+        if call == "rotary_backward":
+            x = torch.zeros(1, 4, 2, 64)
+            ob.rotary_backward(plan, x.transpose(1, 2).contiguous(), positions=torch.zeros(4, 2, dtype=torch.int32),
+                               q=x, norm_eps=1e-6, q_weight=torch.ones(64), stream=stream)
+        else:
+            x = torch.zeros(1, 4, 64)
+            ob.gated_norm_backward(x, x, x, x, gate=torch.zeros(1, 64), pre=ob.NormSpec("rms"), stream=stream)
+
+    for stream, handle in ((None, 7), (7, 7), (40, 40), (Stream(48, torch.device("cpu")), 48), (0, 0), (1, 0)):
+        run(stream)
+        assert (allocated.pop(), launched.pop(), now) == (handle, handle, [7])
+    refused(bb.ERR_INVALID_ARG, run, Stream(48, torch.device("meta")))

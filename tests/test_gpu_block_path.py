@@ -124,3 +124,75 @@ def test_two_steps_on_two_streams():
         torch.cuda.synchronize()
         for a, b in zip(got, alone):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def side_stream_case():
+    """(plan, call): call(stream) runs the two operators and their backward passes, all results and workspaces
+    left to the helpers"""
+    g = torch.Generator(DEV).manual_seed(3)
+    B, N, H, d = 1, 1500, 4, 128
+    C = H * d
+    pos = pkg.grid_positions((6, 10, 25))
+    plan = pkg.rotary_plan(d, (44, 42, 42))
+    w = torch.randn(d, generator=g, device=DEV)
+    qkv = torch.randn(B, N, 3, H, d, generator=g, device=DEV).bfloat16().unbind(2)
+    x, y, dh, dz = (torch.randn(B, N, C, generator=g, device=DEV).bfloat16() for _ in range(4))
+    kw = dict(gate=torch.randn(B, C, generator=g, device=DEV),
+              post=pkg.NormSpec("rms", torch.randn(C, generator=g, device=DEV)), pre=pkg.NormSpec("layer"))
+    grads = [torch.randn(B, H, N, d, generator=g, device=DEV).bfloat16() for _ in range(3)]
+    turn = dict(positions=pos, norm_eps=1e-6, q_weight=w, k_weight=w)
+
+    def call(stream):
+        out = [*pkg.rotary(plan, *qkv, **turn, stream=stream)]
+        out += pkg.rotary_backward(plan, *grads, q=qkv[0], k=qkv[1], **turn, stream=stream)
+        out += pkg.gated_norm(x, y, **kw, stream=stream)
+        out += pkg.gated_norm_backward(dh, dz, x, y, **kw, stream=stream)
+        return [t for t in out if t is not None]
+
+    sizes = sorted({t.numel() * t.element_size() for t in call(None)} |
+                   {pkg.rotary_workspace(B, N, d).numel(), pkg.gated_norm_workspace(B, N, C).numel()})
+    return call, sizes
+
+
+@pytest.mark.parametrize("given", ["stream", "handle"])
+@pytest.mark.parametrize("late", ["side", "current"])
+def test_what_a_call_allocates_belongs_to_its_stream(given, late):
+    """Around a call on a side stream the current stream frees, allocates and fills tensors of the sizes of its
+    workspaces and results. Whichever of the two streams runs late, neither may touch the other's tensors: a workspace
+    that goes back to the current stream's pool would be written behind the fill of the tensor that took its place,
+    and a result from that pool would be written before the fill of the tensor that had its place."""
+    call, sizes = side_stream_case()
+    expected = call(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        if late == "current":
+            torch.cuda._sleep(20_000_000)
+        else:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+        for n in sizes:
+            torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0x55)
+        got = call(side if given == "stream" else side.cuda_stream)
+        mine = [torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0xAA) for n in sizes for _ in range(2)]
+        torch.cuda.synchronize()
+        assert len(got) == len(expected)
+        for a, b in zip(got, expected):
+            assert torch.equal(a, b)
+        for t in mine:
+            assert t.eq(0xAA).all()
+
+
+def test_the_default_stream_from_another():
+    """handles 0 and 1 both name the default stream, and a stream object of it does"""
+    call, _ = side_stream_case()
+    expected = call(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (0, 1, torch.cuda.default_stream()):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+            got = call(stream)
+            assert torch.cuda.current_stream() == side
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, expected))
