@@ -20,7 +20,7 @@ int size_of(int dt) { return dt == BSA_BF16 ? 2 : 4; }
 
 // The bytes that a strided tensor covers: three dimensions (sizes, byte strides) of `inner` bytes each.
 struct Footprint {
-    uintptr_t at;
+    uintptr_t at, end;  // end: one past the last
     int64_t size[3], stride[3], inner;
 
     // bytes from the first to one past the last, over dimensions whose stride is below `under`
@@ -51,7 +51,21 @@ bool make_footprint(const void *p, int64_t n0, int64_t s0, int64_t n1, int64_t s
         end += static_cast<double>(n[i] - 1) * static_cast<double>(f->stride[i]);
     }
     f->inner = inner * elem;
-    return end < 4.0e18;
+    if (end >= 4.0e18) return false;
+    f->end = f->at + f->span(INT64_MAX);
+    return true;
+}
+
+// `count` of `bytes` each, `step` bytes apart, at any address
+Footprint block_of(const void *p, int64_t bytes, int64_t count = 1, int64_t step = 0)
+{
+    Footprint f{};
+    f.at = reinterpret_cast<uintptr_t>(p);
+    f.size[0] = count, f.size[1] = f.size[2] = 1;
+    f.stride[0] = count > 1 ? step : 0;
+    f.inner = bytes;
+    f.end = f.at + f.span(INT64_MAX);
+    return f;
 }
 
 // Whether no two elements of an output share an address: each stride steps over what lies below it.
@@ -70,7 +84,7 @@ bool steps_clear(const Footprint &f)
 // strides, because they lie beside each other within one step of some dimension.
 bool disjoint(const Footprint &a, const Footprint &b)
 {
-    if (a.at + a.span(INT64_MAX) <= b.at || b.at + b.span(INT64_MAX) <= a.at) return true;
+    if (a.end <= b.at || b.end <= a.at) return true;
     const Footprint &lo = a.at <= b.at ? a : b, &hi = a.at <= b.at ? b : a;
     int64_t step[3];
     for (int i = 0; i < 3; ++i) {
@@ -97,13 +111,25 @@ bool same(const Footprint &a, const Footprint &b)
            std::memcmp(a.stride, b.stride, sizeof(a.stride)) == 0;
 }
 
-// The tensors of a call: outputs must be clear of themselves, of each other and of every input but those
-// they may replace.
+// What a call reads and writes, weights, modulations, positions and the workspace among it: outputs must be clear of
+// themselves, of each other and of every input but those they may replace.
 struct Tensors {
     static constexpr int kMax = 12;
     Footprint in[kMax], out[kMax];
     int n_in = 0, n_out = 0;
     unsigned may_be[kMax];  // out[i] may be in[k] for the bits k
+
+    // a contiguous operand, where there is one
+    void reads(const void *p, int64_t bytes)
+    {
+        if (p) in[n_in++] = block_of(p, bytes);
+    }
+    void writes(const void *p, int64_t bytes)
+    {
+        if (!p) return;
+        may_be[n_out] = 0;
+        out[n_out++] = block_of(p, bytes);
+    }
 
     bool check() const
     {
@@ -134,7 +160,8 @@ bsa_status check_rotary(const bsa_rotary_plan *plan, int dt, int B, int N, const
         return BSA_ERR_INVALID_ARG;
     for (int p = 0; p < plan->rot / 2; ++p)
         if (plan->axis[p] >= plan->n_axes) return BSA_ERR_INVALID_ARG;
-    if (turns && (!positions || !aligned(positions, 4) || pos_batch < 0 || pos_batch > (INT64_MAX >> 32)))
+    if (turns && (!positions || !aligned(positions, 4) || pos_batch < 0 || pos_batch > (INT64_MAX >> 32) ||
+                  4.0 * (B - 1) * static_cast<double>(pos_batch) > 4.0e18))
         return BSA_ERR_INVALID_ARG;
     if (norm && !(std::isfinite(eps) && eps >= 0.0f)) return BSA_ERR_INVALID_ARG;
     return BSA_OK;
@@ -150,11 +177,15 @@ bool valid_norm(const bsa_norm &n)
     return (!n.weight || aligned(n.weight, 16)) && (!n.bias || aligned(n.bias, 16));
 }
 
+bool modulation_of(const bsa_modulation &m, const bsa_gated_norm_desc &d, Footprint *f)
+{
+    return make_footprint(m.ptr, d.B, m.batch, d.F, m.frame, 1, 0, d.C, size_of(d.mod_dt), f);
+}
+
 bool valid_modulation(const bsa_modulation &m, const bsa_gated_norm_desc &d)
 {
-    if (!m.ptr) return true;
     Footprint f;
-    return make_footprint(m.ptr, d.B, m.batch, d.F, m.frame, 1, 0, d.C, size_of(d.mod_dt), &f);
+    return !m.ptr || modulation_of(m, d, &f);
 }
 
 bool broadcast(const bsa_modulation &m, const bsa_gated_norm_desc &d)
@@ -198,6 +229,17 @@ bsa_gated_norm_desc tidy(const bsa_gated_norm_desc &in)
         if (d.F == 1) m->frame = 0;
     }
     return d;
+}
+
+// the weights and modulations that a (tidy) desc names
+void reads_parameters(const bsa_gated_norm_desc &d, Tensors *all)
+{
+    for (const bsa_norm *n : {&d.post, &d.pre}) {
+        all->reads(n->weight, int64_t(4) * d.C);
+        all->reads(n->bias, int64_t(4) * d.C);
+    }
+    for (const bsa_modulation *m : {&d.gate, &d.scale, &d.shift})
+        if (m->ptr) modulation_of(*m, d, &all->in[all->n_in++]);
 }
 
 }  // namespace
@@ -274,9 +316,11 @@ bsa_status bsa_rotary(const bsa_rotary_plan *plan, const bsa_heads *q, const bsa
         if (norm && i < 2) {
             if (t[i]->weight && !aligned(t[i]->weight, 16)) return BSA_ERR_INVALID_ARG;
             h.weight = t[i]->weight;
+            all.reads(h.weight, int64_t(4) * d);
         }
         h.heads = heads;
     }
+    if (q || k) all.in[all.n_in++] = block_of(positions, int64_t(4) * N * plan->n_axes, B, 4 * pos_batch);
     if (!all.check()) return BSA_ERR_INVALID_ARG;
     a.positions = positions;
     a.pos_batch = B > 1 ? pos_batch : 0;
@@ -329,21 +373,25 @@ bsa_status bsa_rotary_backward(const bsa_rotary_plan *plan, const bsa_heads_grad
                 return BSA_ERR_INVALID_ARG;
             h.weight = t[i]->weight;
             h.dweight = t[i]->dweight;
+            all.reads(h.weight, int64_t(4) * d);
             sums = sums || h.dweight;
         } else if (t[i]->dweight) {
             return BSA_ERR_INVALID_ARG;  // no norm, no weight
         }
         all.may_be[all.n_out++] = may_be;
+        all.writes(h.dweight, int64_t(4) * d);
         h.heads = heads;
     }
-    if (!all.check()) return BSA_ERR_INVALID_ARG;
+    if (q || k) all.in[all.n_in++] = block_of(positions, int64_t(4) * N * plan->n_axes, B, 4 * pos_batch);
     if (sums) {
         size_t need = 0;
         s = bsa_rotary_workspace_size(B, N, d, &need);
         if (s != BSA_OK) return s;
         if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return BSA_ERR_WORKSPACE;
         a.partial = static_cast<float *>(workspace);
+        all.writes(workspace, static_cast<int64_t>(need));
     }
+    if (!all.check()) return BSA_ERR_INVALID_ARG;
     a.positions = positions;
     a.pos_batch = B > 1 ? pos_batch : 0;
     a.dt = dt;
@@ -388,6 +436,7 @@ bsa_status bsa_gated_norm(const bsa_gated_norm_desc *desc, const bsa_rows *x, co
         if (!rows_of(*z, d, d.branch_dt, &all.out[all.n_out], &a.z)) return BSA_ERR_INVALID_ARG;
         all.may_be[all.n_out++] = 2u;
     }
+    reads_parameters(a.d, &all);
     if (!all.check()) return BSA_ERR_INVALID_ARG;
     return bsa::launch_gated_norm(a, static_cast<cudaStream_t>(stream));
 }
@@ -438,7 +487,9 @@ bsa_status bsa_gated_norm_backward(const bsa_gated_norm_desc *desc, const bsa_ga
         all.may_be[all.n_out++] = y_bit | dz_bit;
     }
     if (!a.y.p) a.d.post = bsa_norm{};  // nothing is asked for behind the post norm
-    if (!all.check()) return BSA_ERR_INVALID_ARG;
+    reads_parameters(a.d, &all);
+    for (const void *p : {g.dgate, g.dscale, g.dshift}) all.writes(p, int64_t(d.B) * d.F * d.C * size_of(d.mod_dt));
+    for (const float *p : {g.dpost_weight, g.dpost_bias, g.dpre_weight, g.dpre_bias}) all.writes(p, int64_t(4) * d.C);
     a.dgate = static_cast<char *>(g.dgate);
     a.dscale = static_cast<char *>(g.dscale);
     a.dshift = static_cast<char *>(g.dshift);
@@ -452,7 +503,9 @@ bsa_status bsa_gated_norm_backward(const bsa_gated_norm_desc *desc, const bsa_ga
         if (s != BSA_OK) return s;
         if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return BSA_ERR_WORKSPACE;
         a.partial = static_cast<float *>(workspace);
+        all.writes(workspace, static_cast<int64_t>(need));
     }
+    if (!all.check()) return BSA_ERR_INVALID_ARG;
     return bsa::launch_gated_norm_backward(a, static_cast<cudaStream_t>(stream));
 }
 

@@ -18,8 +18,9 @@
  * Tensors are given by a pointer and element strides; channels are contiguous. Pointers are
  * 16-byte aligned and strides non-negative multiples of 16 bytes (the stride of a dimension of
  * length one is not looked at). An input may have a stride of zero (a broadcast input). An
- * output must not overlap itself, another output or an input, except that an output may be
- * the input that its own comment names (the same pointer, strides and dtype). Views of the
+ * output (gradients and the workspace count) must not overlap itself, another output or an
+ * input that the call reads (weights, modulations and positions count), except that an output may
+ * be the input that its own comment names (the same pointer, strides and dtype). Views of the
  * same strides that interleave in one buffer (Q, K and V of a fused projection, a slice of the
  * channels or tokens) are told apart; otherwise the address ranges must be disjoint.
  */

@@ -426,3 +426,122 @@ def test_workspace_is_allocated_on_the_calls_stream(monkeypatch, call):
         run(stream)
         assert (allocated.pop(), launched.pop(), now) == (handle, handle, [7])
     refused(bb.ERR_INVALID_ARG, run, Stream(48, torch.device("meta")))
+
+
+# ------------------------------------------------------------------ overlaps of every operand
+
+
+def _passes(fn, *args):
+    """not refused: without a device the call fails at its first CUDA call, behind all checks"""
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real")
+    refused(bb.ERR_CUDA, fn, *args)
+
+
+def test_rotary_outputs_over_weights_and_positions():
+    inv, B, N, H, d = bb.ERR_INVALID_ARG, 2, 16, 2, 64
+    dst, size = FAKE + 8 * FAR, B * N * H * d * 2
+
+    def call(q=None, k=None, pos=FAKE + 30 * FAR, pos_batch=0):
+        return _plan(), q or _heads(0, weight=FAKE + 31 * FAR), k, None, bb.BF16, B, N, pos, pos_batch, 1, 1e-6, 0
+
+    _passes(ob.bsa_rotary, *call())
+    for at in (dst - 4 * d + 16, dst, dst + size - 16):  # a weight whose end, whole or start lies in q's result
+        refused(inv, ob.bsa_rotary, *call(_heads(0, weight=at)))
+        refused(inv, ob.bsa_rotary, *call(k=_heads(1, weight=at)))
+    for at in (dst - 4 * d, dst + size):
+        _passes(ob.bsa_rotary, *call(_heads(0, weight=at)))
+    for at in (dst - N * 2 * 4 + 4, dst + 64, dst + size - 4):
+        refused(inv, ob.bsa_rotary, *call(pos=at))
+    refused(inv, ob.bsa_rotary, *call(pos=dst - 4096, pos_batch=1024))  # the second batch's positions
+    for at in (dst - N * 2 * 4, dst + size):
+        _passes(ob.bsa_rotary, *call(pos=at))
+    _passes(ob.bsa_rotary, *call(pos=dst - 4096, pos_batch=992))
+    refused(inv, ob.bsa_rotary, *call(pos_batch=(1 << 31) + 1))
+    # a weight and positions that the call does not read
+    _passes(ob.bsa_rotary, _plan(), _heads(0, weight=dst), None, None, bb.BF16, B, N, FAKE + 30 * FAR, 0, 0, 0.0, 0)
+    _passes(ob.bsa_rotary, _plan(), None, None, _heads(0, weight=dst), bb.BF16, B, N, dst, 0, 1, 1e-6, 0)
+
+
+def test_rotary_backward_overlaps():
+    inv, B, N, d = bb.ERR_INVALID_ARG, 2, 16, 64
+    need = ob.bsa_rotary_workspace_size(B, N, d)
+    pos, ws, dx = FAKE + 40 * FAR, FAKE + 41 * FAR, FAKE + 16 * FAR
+    w = [FAKE + (42 + i) * FAR for i in range(4)]
+
+    def call(ws=ws, k=None, **q):
+        q = _grad(0, **{**dict(weight=w[0], dweight=w[1]), **q})
+        k = _grad(1, **{**dict(weight=w[2], dweight=w[3]), **(k or {})})
+        return _plan(), q, k, None, bb.BF16, B, N, pos, 0, 1, 1e-6, ws, need, 0
+
+    _passes(ob.bsa_rotary_backward, *call())
+    _passes(ob.bsa_rotary_backward, *call(weight=w[2]))                     # one weight for both
+    _passes(ob.bsa_rotary_backward, *call(dx=FAKE + 8 * FAR))               # dx over x
+    for bad in (w[0], w[2], w[3], dx, FAKE, FAKE + 8 * FAR, pos, ws, ws + need - 4):
+        refused(inv, ob.bsa_rotary_backward, *call(dweight=bad))            # over a weight, the other's gradient, dx ...
+    for bad in (w[1], dx, pos & ~255, FAKE, dx - need + 256):
+        refused(inv, ob.bsa_rotary_backward, *call(ws=bad))
+    refused(inv, ob.bsa_rotary_backward, *call(dx=w[2]))
+    refused(inv, ob.bsa_rotary_backward, *call(k=dict(dweight=w[1])))
+    _passes(ob.bsa_rotary_backward, *call(dweight=ws + need))               # behind what the workspace needs
+
+
+def test_gated_norm_outputs_over_parameters():
+    inv, B, N, C = bb.ERR_INVALID_ARG, 2, 16, 64
+    p = [FAKE + (20 + i) * FAR for i in range(8)]
+    h, z, size = FAKE + 2 * FAR, FAKE + 3 * FAR, B * N * C * 2
+
+    def call(**kw):
+        d = dict(post=_norm(ob.NORM_RMS, weight=p[0], bias=p[1]), pre=_norm(weight=p[2], bias=p[3]), gate=_mod(p[4]),
+                 scale=_mod(p[5]), shift=_mod(p[6]))
+        return _desc(**{**d, **kw}), _rows(0), _rows(1), _rows(2), _rows(3), 0
+
+    _passes(ob.bsa_gated_norm, *call())
+    for out in (h, z):
+        for at in (out - 16, out, out + size - 16):
+            for name in ("gate", "scale", "shift"):
+                refused(inv, ob.bsa_gated_norm, *call(**{name: _mod(at)}))
+            refused(inv, ob.bsa_gated_norm, *call(post=_norm(ob.NORM_RMS, weight=at)))
+            refused(inv, ob.bsa_gated_norm, *call(post=_norm(ob.NORM_RMS, bias=at)))
+            refused(inv, ob.bsa_gated_norm, *call(pre=_norm(weight=at)))
+            refused(inv, ob.bsa_gated_norm, *call(pre=_norm(bias=at)))
+        refused(inv, ob.bsa_gated_norm, *call(gate=_mod(out - 4096, batch=2048)))  # its second batch
+        _passes(ob.bsa_gated_norm, *call(gate=_mod(out - 4096, batch=0)))
+        _passes(ob.bsa_gated_norm, *call(gate=_mod(out + size)))
+    # modulations between the rows of an output: one buffer [B][N][C + 3 * C]
+    wide = dict(token=4 * C, batch=N * 4 * C)
+    args = list(call(gate=_mod(h + 2 * C, batch=N * 4 * C)))
+    args[3] = _rows(2, **wide)
+    _passes(ob.bsa_gated_norm, *args)
+
+
+def test_gated_norm_backward_overlaps():
+    inv, none = bb.ERR_INVALID_ARG, ob.Rows(None, 0, 0)
+    need = ob.bsa_gated_norm_workspace_size(2, 16, 64)
+    p = [FAKE + (30 + i) * FAR for i in range(7)]
+    ws = FAKE + 40 * FAR
+    grads = {n: FAKE + (50 + i) * FAR for i, n in enumerate(("dgate", "dscale", "dshift", "dpost_weight", "dpost_bias",
+                                                             "dpre_weight", "dpre_bias"))}
+    desc = _desc(post=_norm(ob.NORM_RMS, weight=p[0], bias=p[1]), pre=_norm(weight=p[2], bias=p[3]), gate=_mod(p[4]),
+                 scale=_mod(p[5]), shift=_mod(p[6]))
+
+    def call(ws=ws, **kw):
+        return desc, _norm_grads(**{**grads, **kw}), ws, need, 0
+
+    _passes(ob.bsa_gated_norm_backward, *call())
+    _passes(ob.bsa_gated_norm_backward, *call(dx=_rows(0), dy=_rows(1)))
+    rows = [FAKE + i * FAR for i in range(6)]
+    for name, own in grads.items():
+        others = [g for n, g in grads.items() if n != name]
+        for at in p + rows + others + [ws, ws + need - 16]:
+            refused(inv, ob.bsa_gated_norm_backward, *call(**{name: at}))
+        _passes(ob.bsa_gated_norm_backward, *call(**{name: ws + need}))
+    for at in p + rows + list(grads.values()):
+        refused(inv, ob.bsa_gated_norm_backward, *call(ws=at))
+    for at in p:
+        refused(inv, ob.bsa_gated_norm_backward, *call(dx=_rows(0, ptr=at)))
+        refused(inv, ob.bsa_gated_norm_backward, *call(dy=_rows(0, ptr=at)))
+    # without a gradient that needs it the workspace is not looked at
+    alone = {n: None for n in grads}
+    _passes(ob.bsa_gated_norm_backward, *call(ws=rows[4], **alone))
+    _passes(ob.bsa_gated_norm_backward, *call(ws=rows[4], dx=none, **alone))
