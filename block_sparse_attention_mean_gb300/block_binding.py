@@ -303,7 +303,7 @@ def grid_positions(grid: Sequence[int], n_text: int = 0, cuboid: Optional[Sequen
     return torch.cat((torch.zeros((n_text, len(grid)), dtype=torch.int32, device=device), c)).contiguous()
 
 
-def _rotary_args(plan, first, positions, needed: bool, q_weight, k_weight, n_at: int, what: str):
+def _rotary_args(plan, first, positions, needed: bool, norm: bool, q_weight, k_weight, n_at: int, what: str):
     """What rotary and rotary_backward have in common, from the first of their tensors (tokens at dimension n_at):
     (device, dtype, dtype code, B, N, positions, pos_batch, weights)."""
     if first is None:
@@ -324,6 +324,8 @@ def _rotary_args(plan, first, positions, needed: bool, q_weight, k_weight, n_at:
             pos_batch = s[0]
         if N > 1 and s[-2] != axes:
             raise BsaError(ERR_INVALID_ARG, f"{what}: a token's positions must follow the last token's")
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise BsaError(ERR_INVALID_ARG, f"{what}: a weight without norm_eps, which selects the norm")
     d = plan.d
     weights = (0 if q_weight is None else _view(q_weight, (d,), torch.float32, device, what, "q_weight")[0],
                0 if k_weight is None else _view(k_weight, (d,), torch.float32, device, what, "k_weight")[0], 0)
@@ -339,7 +341,7 @@ def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor
            k_weight: Optional[torch.Tensor] = None,
            out: Optional[Tuple[Optional[torch.Tensor], ...]] = None, stream=None):
     """Run bsa_rotary: q, k, v [B, N, heads, d] (views of a fused projection do) to [B, heads, N, d], Q and K
-    normalised per head (norm_eps not None; fp32 weights [d] optional) and turned by `positions`
+    normalised per head (norm_eps not None; fp32 weights [d] optional, refused without it) and turned by `positions`
     (int32 [N, axes] or [B, N, axes]). `out`: the three results' tensors, any strides with contiguous
     channels. Returns (q, k, v), None where none was given."""
     what = "rotary"
@@ -349,7 +351,7 @@ def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor
             return rotary(plan, q, k, v, positions=positions, norm_eps=norm_eps, q_weight=q_weight, k_weight=k_weight,
                           out=out)
     device, dtype, code, B, N, pos, pos_batch, weights = _rotary_args(
-        plan, first, positions, q is not None or k is not None, q_weight, k_weight, 1, what)
+        plan, first, positions, q is not None or k is not None, norm_eps is not None, q_weight, k_weight, 1, what)
     d = plan.d
     res, desc = [None, None, None], [None, None, None]
     for i, t in enumerate((q, k, v)):
@@ -391,7 +393,7 @@ def rotary_backward(plan: RotaryPlan, dq: Optional[torch.Tensor], dk: Optional[t
             return rotary_backward(plan, dq, dk, dv, positions=positions, q=q, k=k, norm_eps=norm_eps,
                                    q_weight=q_weight, k_weight=k_weight, out=out, ws=ws)
     device, dtype, code, B, N, pos, pos_batch, weights = _rotary_args(
-        plan, first, positions, dq is not None or dk is not None, q_weight, k_weight, 2, what)
+        plan, first, positions, dq is not None or dk is not None, norm_eps is not None, q_weight, k_weight, 2, what)
     norm, d = norm_eps is not None, plan.d
     res, desc, dweights = [None, None, None], [None, None, None], [None, None]
     for i, t in enumerate((dq, dk, dv)):

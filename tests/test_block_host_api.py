@@ -545,3 +545,13 @@ def test_gated_norm_backward_overlaps():
     alone = {n: None for n in grads}
     _passes(ob.bsa_gated_norm_backward, *call(ws=rows[4], **alone))
     _passes(ob.bsa_gated_norm_backward, *call(ws=rows[4], dx=none, **alone))
+
+
+def test_weight_without_the_norm_is_refused(monkeypatch):
+    monkeypatch.setattr(ob, "_cuda_device", lambda t, what: t.device)
+    x, pos, w = torch.zeros(1, 4, 2, 64), torch.zeros(4, 2, dtype=torch.int32), torch.ones(64)
+    for fn, t in ((pkg.rotary, x), (pkg.rotary_backward, x.transpose(1, 2))):
+        for weights in (dict(q_weight=w), dict(k_weight=w)):
+            with pytest.raises(bb.BsaError, match="norm_eps") as e:
+                fn(_plan(), t, positions=pos, **weights)
+            assert e.value.code == bb.ERR_INVALID_ARG

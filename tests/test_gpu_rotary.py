@@ -321,3 +321,17 @@ def test_helper_refusals():
     small = torch.empty(256, device=DEV, dtype=torch.uint8)
     bad(bb.ERR_WORKSPACE, pkg.rotary_backward, plan, dq, positions=pos, norm_eps=1e-6, q=q,
         q_weight=torch.ones(64, device=DEV), ws=small)
+
+
+def test_weight_without_the_norm_is_refused():
+    """it would change nothing, and its gradient would be missing"""
+    g = gen(14)
+    q, k, _ = fused(g, 1, 8, 2, 2, 64, BF16)
+    plan, pos, w = pkg.rotary_plan(64, (64,)), pkg.grid_positions((8,)), torch.ones(64, device=DEV)
+    dq, dk = (t.transpose(1, 2).contiguous() for t in (q, k))
+    for fn, args, more in ((pkg.rotary, (q, k), {}), (pkg.rotary_backward, (dq, dk), dict(q=q, k=k))):
+        for weights in (dict(q_weight=w), dict(k_weight=w), dict(q_weight=w, k_weight=w)):
+            with pytest.raises(bb.BsaError) as e:
+                fn(plan, *args, positions=pos, **more, **weights)
+            assert e.value.code == bb.ERR_INVALID_ARG
+        fn(plan, *args, positions=pos, **more)
