@@ -4,7 +4,9 @@ check that they go together and allocate outputs and workspaces with torch.
 
 As in ``binding`` there is no fallback: if libbsa.so cannot be loaded every call raises. The helpers
 run on the tensors' device and on ``stream`` (that device's current stream by default), as under
-torch.cuda.stream(stream): what they allocate, results and workspace, belongs to that stream.
+torch.cuda.stream(stream): what they allocate, results and workspace, belongs to that stream. They record
+nothing for autograd, and refuse a tensor that requires a gradient while gradients are recorded: call them
+under torch.no_grad() or inside a torch.autograd.Function, whose backward calls the backward helper.
 """
 from __future__ import annotations
 
@@ -188,7 +190,8 @@ def _code(t: torch.Tensor, what: str) -> int:
 def _view(t: torch.Tensor, shape, dtype: torch.dtype, device, what: str, name: str):
     """(address, strides) of a tensor that a kernel will index by this shape, dtype and device, channels contiguous."""
     s = t.stride()
-    if t.shape == shape and t.dtype == dtype and t.device == device and (s[-1] == 1 or shape[-1] <= 1):
+    if (t.shape == shape and t.dtype == dtype and t.device == device and (s[-1] == 1 or shape[-1] <= 1) and
+            not (t.requires_grad and torch.is_grad_enabled())):
         return t.data_ptr(), s
     if t.shape != shape:
         raise BsaError(ERR_SHAPE, f"{what}: {name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -196,7 +199,10 @@ def _view(t: torch.Tensor, shape, dtype: torch.dtype, device, what: str, name: s
         raise BsaError(ERR_DTYPE, f"{what}: {name}: dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise BsaError(ERR_INVALID_ARG, f"{what}: {name}: on {t.device}, expected {device}")
-    raise BsaError(ERR_INVALID_ARG, f"{what}: {name}: channels must be contiguous")
+    if s[-1] != 1 and shape[-1] > 1:
+        raise BsaError(ERR_INVALID_ARG, f"{what}: {name}: channels must be contiguous")
+    raise BsaError(ERR_INVALID_ARG, f"{what}: {name}: requires a gradient, which this call does not record: call it under "
+                                    "torch.no_grad() or in a torch.autograd.Function")
 
 
 def _cuda_device(t: torch.Tensor, what: str) -> torch.device:

@@ -555,3 +555,48 @@ def test_weight_without_the_norm_is_refused(monkeypatch):
             with pytest.raises(bb.BsaError, match="norm_eps") as e:
                 fn(_plan(), t, positions=pos, **weights)
             assert e.value.code == bb.ERR_INVALID_ARG
+
+
+def test_gradients_that_would_vanish_are_refused(monkeypatch):
+    """a tensor that requires a gradient, each operand in turn, while gradients are recorded"""
+    monkeypatch.setattr(ob, "_cuda_device", lambda t, what: t.device)
+    heads, rows, plan = torch.zeros(1, 4, 2, 64), torch.zeros(1, 4, 64), _plan()
+
+    def back(**t):
+        return pkg.rotary_backward(plan, t.pop("dq"), t.pop("dk"), t.pop("dv"), **t)
+
+    def norms(t):
+        w = {n: t.pop(n) for n in ("post_w", "post_b", "pre_w", "pre_b")}
+        return dict(post=ob.NormSpec("rms", w["post_w"], w["post_b"]), pre=ob.NormSpec("layer", w["pre_w"], w["pre_b"]))
+
+    pos, w64 = torch.zeros(4, 2, dtype=torch.int32), torch.ones(64)
+    turn = dict(positions=pos, q_weight=w64, k_weight=w64)
+    dy = heads.transpose(1, 2).contiguous()
+    mods = {n: torch.zeros(1, 64) for n in ("gate", "scale", "shift")}
+    params = {n: w64 for n in ("post_w", "post_b", "pre_w", "pre_b")}
+    calls = [(lambda **t: pkg.rotary(plan, t.pop("q"), t.pop("k"), t.pop("v"), norm_eps=1e-6, **t),
+              dict(q=heads, k=heads, v=heads, **turn)),
+             (lambda **t: back(norm_eps=1e-6, **t), dict(dq=dy, dk=dy, dv=dy, q=heads, k=heads, **turn)),
+             (lambda **t: pkg.gated_norm(t.pop("x"), t.pop("y"), **norms(t), **t), dict(x=rows, y=rows, **mods, **params)),
+             (lambda **t: pkg.gated_norm_backward(t.pop("dh"), t.pop("dz"), t.pop("h"), t.pop("y"), **norms(t), **t),
+              dict(dh=rows, dz=rows, h=rows, y=rows, **mods, **params))]
+
+    class Reached(Exception):
+        pass
+
+    def launch(*args):
+        raise Reached
+
+    monkeypatch.setattr(ob, "_run", launch)
+    for fn, tensors in calls:
+        with pytest.raises(Reached):
+            fn(**tensors)
+        for name, t in tensors.items():
+            if name == "positions":
+                continue
+            wanted = dict(tensors, **{name: t.clone().requires_grad_()})
+            with pytest.raises(bb.BsaError, match="gradient") as e:
+                fn(**wanted)
+            assert e.value.code == bb.ERR_INVALID_ARG, name
+            with torch.no_grad(), pytest.raises(Reached):
+                fn(**wanted)

@@ -196,3 +196,59 @@ def test_the_default_stream_from_another():
             assert torch.cuda.current_stream() == side
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, expected))
+
+
+def test_inside_an_autograd_function():
+    """as a training step uses the two pairs: parameters that require gradients, which arrive from the backward
+    helpers"""
+    g = torch.Generator(DEV).manual_seed(4)
+    B, N, H, d = 2, 70, 4, 64
+    C = H * d
+    plan, pos = pkg.rotary_plan(d, (16, 24, 24)), pkg.grid_positions((2, 5, 7))
+
+    def draw(*shape):
+        return torch.randn(*shape, generator=g, device=DEV)
+
+    class Turn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, w):
+            ctx.save_for_backward(q, w)
+            return pkg.rotary(plan, q, positions=pos, norm_eps=1e-6, q_weight=w)[0]
+
+        @staticmethod
+        def backward(ctx, dy):
+            q, w = ctx.saved_tensors
+            got = pkg.rotary_backward(plan, dy.contiguous(), positions=pos, q=q, norm_eps=1e-6, q_weight=w)
+            return got[0], got[3]
+
+    class Step(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, y, gate, w):
+            h, z = pkg.gated_norm(x, y, gate=gate, pre=pkg.NormSpec("rms", w))
+            ctx.save_for_backward(h, y, gate, w)
+            return h, z
+
+        @staticmethod
+        def backward(ctx, dh, dz):
+            h, y, gate, w = ctx.saved_tensors
+            got = pkg.gated_norm_backward(dh.contiguous(), dz.contiguous(), h, y, gate=gate, pre=pkg.NormSpec("rms", w))
+            return got.dx, got.dy, got.dgate, got.dpre_weight
+
+    q, wq, x, gate, w = draw(B, N, H, d), draw(d), draw(B, N, C), draw(B, C), draw(C)
+    leaves = [t.requires_grad_() for t in (q, wq, x, gate, w)]
+    o = Turn.apply(q, wq)
+    h, z = Step.apply(x, o.transpose(1, 2).reshape(B, N, C), gate, w)
+    ch, cz = draw(B, N, C), draw(B, N, C)
+    got = torch.autograd.grad((h * ch + z * cz).sum(), leaves)
+
+    # the calls one by one (each is compared with its 64-bit form elsewhere): the same bits
+    with torch.no_grad():
+        y = pkg.rotary(plan, q, positions=pos, norm_eps=1e-6, q_weight=wq)[0].transpose(1, 2).reshape(B, N, C)
+        pre = pkg.NormSpec("rms", w)
+        h2, z2 = pkg.gated_norm(x, y, gate=gate, pre=pre)
+        back = pkg.gated_norm_backward(ch, cz, h2, y, gate=gate, pre=pre)
+        dy = back.dy.view(B, N, H, d).transpose(1, 2).contiguous()
+        turned = pkg.rotary_backward(plan, dy, positions=pos, q=q, norm_eps=1e-6, q_weight=wq)
+    assert torch.equal(h, h2) and torch.equal(z, z2)
+    for a, b, name in zip(got, (turned[0], turned[3], back.dx, back.dgate, back.dpre_weight), ("q", "wq", "x", "gate", "w")):
+        assert torch.equal(a, b), name
