@@ -167,6 +167,30 @@ bsa_status check_rotary(const bsa_rotary_plan *plan, int dt, int B, int N, const
     return BSA_OK;
 }
 
+// scale * theta^(-2 j / dim) as f + rest. The exponent is a double and what it lacks, e + e_rest, of which the second
+// comes in by theta^e_rest = 1 + e_rest log(theta); the product's rounding is kept too. What remains is the rounding of
+// pow, one unit in the last place at most: 2^-52 of the value.
+void frequency(double scale, double theta, int j, int dim, double *f, double *rest)
+{
+    const double e = -2.0 * j / dim, e_rest = std::fma(-e, static_cast<double>(dim), -2.0 * j) / dim;
+    const double power = std::pow(theta, e);
+    *f = scale * power;
+    *rest = std::fma(scale, power, -*f) + scale * (power * (e_rest * std::log(theta)));
+}
+
+// x, at most 0.5 in magnitude, as 2^64 x modulo 2^64
+uint64_t fixed(double x) { return x >= 0.5 ? uint64_t(1) << 63 : static_cast<uint64_t>(static_cast<int64_t>(std::rint(std::ldexp(x, 64)))); }
+
+// (f + rest) / 2 pi turns in 2^-64 turns, modulo one turn: positions are whole numbers, so whole turns drop out. 1 / 2 pi
+// and the product are kept in two doubles each; the remainder of a double is exact, and so is its product with 2^64.
+uint64_t turns_of(double f, double rest)
+{
+    constexpr double kInvTwoPi = 0.15915494309189533577, kInvTwoPiRest = -9.839338337591243e-18;
+    const double turns = f * kInvTwoPi, more = std::fma(f, kInvTwoPi, -turns) + f * kInvTwoPiRest + rest * kInvTwoPi;
+    const double whole = std::remainder(turns, 1.0), below = std::ldexp(whole, 64) - std::rint(std::ldexp(whole, 64));
+    return fixed(whole) + fixed(std::remainder(more + std::ldexp(below, -64), 1.0));
+}
+
 bsa_status check_heads(int heads) { return heads >= 1 && heads <= 65535 ? BSA_OK : BSA_ERR_SHAPE; }
 
 bool valid_norm(const bsa_norm &n)
@@ -272,15 +296,13 @@ bsa_status bsa_rotary_plan_init(const bsa_rotary_spec *spec, int d, bsa_rotary_p
     int p = 0;
     for (int a = 0; a < spec->n_axes; ++a) {
         for (int j = 0; j < spec->axis_dim[a] / 2; ++j, ++p) {
-            const double f = spec->inv_freq
-                                 ? spec->inv_freq[p]
-                                 : spec->scale[a] * std::pow(spec->theta[a], -2.0 * j / spec->axis_dim[a]);
+            double f = 0.0, rest = 0.0;  // their sum
+            if (spec->inv_freq)
+                f = spec->inv_freq[p];
+            else
+                frequency(spec->scale[a], spec->theta[a], j, spec->axis_dim[a], &f, &rest);
             if (!std::isfinite(f)) return BSA_ERR_INVALID_ARG;
-            // Turns per position, modulo one turn: positions are whole numbers, so whole turns drop out. The
-            // remainder of a double is exact, and so is its product with 2^64 (at most 2^63 in magnitude).
-            const double turns = std::remainder(f * 0.15915494309189533577, 1.0);
-            out.turns[p] = turns >= 0.5 ? uint64_t(1) << 63
-                                        : static_cast<uint64_t>(static_cast<int64_t>(std::rint(std::ldexp(turns, 64))));
+            out.turns[p] = turns_of(f, rest);
             out.axis[p] = static_cast<uint8_t>(a);
         }
     }

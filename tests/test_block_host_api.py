@@ -2,6 +2,7 @@
 the rotary plan's frequencies, and the refusals, which all happen before any launch."""
 import contextlib
 import ctypes
+import decimal
 import math
 import os
 import re
@@ -121,6 +122,37 @@ def test_plan_angles(dims, theta, scale, pos):
             assert plan.axis[p] == a
             p += 1
     assert (plan.rot, plan.n_axes, plan.d) == (sum(dims), len(dims), 128)
+
+
+# 2 pi to 60 places
+TWO_PI = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+
+
+def check_turns(plan, p, f):
+    """turns[p] against the frequency f (60 digits): within 2^-51 of its value and half a unit, 2^-65 turns"""
+    with decimal.localcontext(prec=60):
+        turns = f / TWO_PI
+        off = (decimal.Decimal(plan.turns[p]) / 2 ** 64 - turns) % 1
+        off = min(abs(off), abs(off - 1), abs(off + 1))
+        assert off <= abs(turns) / 2 ** 51 + decimal.Decimal(2) ** -65, (p, float(off / (abs(turns) + decimal.Decimal(10) ** -40)))
+
+
+@pytest.mark.parametrize("theta", [10000.0, 500000.0, 256.0, 3.7, 1e8, 0.25, 1.0])
+@pytest.mark.parametrize("dim", [2, 6, 16, 42, 44, 48, 56, 62, 112, 128])
+def test_plan_frequencies(theta, dim):
+    for scale in (1.0, -0.3, 40.0):
+        plan = ob.rotary_plan(128, [dim], theta=theta, scale=scale)
+        with decimal.localcontext(prec=60):
+            for j in range(dim // 2):
+                f = decimal.Decimal(scale) * decimal.Decimal(theta) ** (decimal.Decimal(-2 * j) / dim)
+                check_turns(plan, j, f)
+
+
+def test_plan_given_frequencies_are_exact():
+    freq = [1.0, math.pi, -0.1, 3e-7, 1e-19, 12345.678, 2.0 ** 40 + 0.5, 0.0]
+    plan = ob.rotary_plan(64, [16], inv_freq=freq)
+    for p, f in enumerate(freq):
+        check_turns(plan, p, decimal.Decimal(f))
 
 
 def test_plan_given_frequencies():
