@@ -422,3 +422,26 @@ def test_helper_refusals():
     small = torch.empty(256, device=DEV, dtype=torch.uint8)
     bad(bb.ERR_WORKSPACE, pkg.gated_norm_backward, x, y, x, y, **kw, ws=small)
     bad(bb.ERR_INVALID_ARG, pkg.gated_norm_backward, x, y, x, y, **kw, ws=small.cpu())
+
+
+# the kernels differ by types, by width (several rows in a CTA, one row, one row of few registers), by whether there is a
+# post norm and whether a layer norm is among the norms: every one of them, forward and backward
+FORMS = [(None, ("layer", "")), (None, ("rms", "w")), (("rms", "w"), ("rms", "w")), (("layer", "wb"), ("rms", "")),
+         (("rms", ""), None), (("layer", "w"), None), (None, None)]
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("C", [136, 520, 1536, 4096, 6144])
+@pytest.mark.parametrize("form", range(len(FORMS)))
+def test_forms_over_widths(form, C, types):
+    post, pre = FORMS[form]
+    both(C + form, 2, 19, C, types=types, post=post, pre=pre, alpha=0.7)
+
+
+@pytest.mark.parametrize("types", TYPES[:3])
+@pytest.mark.parametrize("C", [264, 1536, 6144])
+@pytest.mark.parametrize("post", [None, ("rms", "")])
+def test_forms_with_many_rows(post, C, types):
+    """several rows per worker, two groups, of a branch, a gate and a layer norm"""
+    both(C, 1, 1402, C, F=2, types=types, post=post, pre=("layer", ""))
+    both(C + 1, 1, 1402, C, F=2, types=types, post=post, pre=("rms", ""), arriving=False)
