@@ -1,5 +1,10 @@
 """The attention step of a block as a model runs it: fused projection -> rotary -> mask -> sparse forward ->
 gated norm, and the operators' backward passes around it, each stage against its own reference."""
+import concurrent.futures
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -252,3 +257,102 @@ def test_inside_an_autograd_function():
     assert torch.equal(h, h2) and torch.equal(z, z2)
     for a, b, name in zip(got, (turned[0], turned[3], back.dx, back.dgate, back.dpre_weight), ("q", "wq", "x", "gate", "w")):
         assert torch.equal(a, b), name
+
+
+def test_two_graphs_with_one_workspace():
+    """captured one after the other with the same workspaces and replayed in turn on one stream: neither needs what
+    the other left there"""
+    g = torch.Generator(DEV).manual_seed(5)
+    N, H, d = 700, 4, 64
+    C = H * d
+    plan, pos, w = pkg.rotary_plan(d, (64,)), torch.arange(N, device=DEV, dtype=torch.int32)[:, None], torch.ones(d, device=DEV)
+    ws = pkg.rotary_workspace(1, N, d), pkg.gated_norm_workspace(1, N, C)
+    post = pkg.NormSpec("rms", torch.ones(C, device=DEV))
+
+    def draw(*s):
+        return torch.randn(*s, generator=g, device=DEV).bfloat16()
+
+    def back(q, dy, x, y, ws):
+        got = pkg.rotary_backward(plan, dy, positions=pos, q=q, norm_eps=1e-6, q_weight=w, ws=ws[0])
+        more = pkg.gated_norm_backward(x, y, x, y, post=post, pre=pkg.NormSpec("layer"), ws=ws[1])
+        return [t for t in (*got, *more) if t is not None]
+
+    inputs = [(draw(1, N, H, d), draw(1, H, N, d), draw(1, N, C), draw(1, N, C)) for _ in range(2)]
+    expected = [back(*i, (None, None)) for i in inputs]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for i in inputs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(back(*i, ws))
+        graphs.append(graph)
+    for k in (0, 1, 1, 0, 1):
+        for t in got[k]:
+            t.zero_()
+        graphs[k].replay()
+        graphs[1 - k].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, expected):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_threads_at_once():
+    """two host threads, a stream each: every call has the bits that it has alone"""
+    g = torch.Generator(DEV).manual_seed(6)
+    N, d = 300, 128
+    plan, pos, w = pkg.rotary_plan(d, (44, 42, 42)), pkg.grid_positions((3, 10, 10)), torch.ones(d, device=DEV)
+
+    def draw(*s):
+        return torch.randn(*s, generator=g, device=DEV).bfloat16()
+
+    def step(q, x, y):
+        turned = pkg.rotary(plan, q, positions=pos, norm_eps=1e-6, q_weight=w)[0]
+        back = pkg.rotary_backward(plan, turned, positions=pos, q=q, norm_eps=1e-6, q_weight=w)
+        h, z = pkg.gated_norm(x, y, pre=pkg.NormSpec("layer"))
+        more = pkg.gated_norm_backward(h, z, h, y, post=pkg.NormSpec("rms", eps=1e-3), pre=pkg.NormSpec("layer"))
+        return [t for t in (turned, *back, h, z, *more) if t is not None]
+
+    inputs = [(draw(1, N, 4, d), draw(1, N, 512 + 520 * i), draw(1, N, 512 + 520 * i)) for i in range(2)]
+    expected = [step(*i) for i in inputs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            runs = [step(*inputs[i]) for _ in range(20)]
+        side.synchronize()
+        return all(torch.equal(a, b) for run in runs for a, b in zip(run, expected[i]))
+
+    with concurrent.futures.ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(work, range(2)))
+
+
+FIRST_CALL = """
+import torch
+import block_sparse_attention_mean_gb300 as pkg
+g = torch.Generator("cuda").manual_seed(1)
+def draw(*s): return torch.randn(*s, generator=g, device="cuda").bfloat16()
+q, x, y = draw(1, 40, 2, 64), draw(1, 40, 1032), draw(1, 40, 1032)
+pos, w = torch.arange(40, device="cuda", dtype=torch.int32)[:, None], torch.ones(64, device="cuda")
+plan, post, pre = pkg.rotary_plan(64, (64,)), pkg.NormSpec("rms", torch.ones(1032, device="cuda")), pkg.NormSpec("layer")
+def step():
+    a = pkg.rotary(plan, q, positions=pos, norm_eps=1e-6, q_weight=w)[0]
+    b = pkg.rotary_backward(plan, a, positions=pos, q=q, norm_eps=1e-6, q_weight=w)
+    h, z = pkg.gated_norm(x, y, post=post, pre=pre)
+    return [t for t in (a, *b, h, z, *pkg.gated_norm_backward(h, z, h, y, post=post, pre=pre)) if t is not None]
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("same")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    """what the library looks up once per kernel it may look up while a graph is captured"""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.split() == ["same"], r.stdout + r.stderr

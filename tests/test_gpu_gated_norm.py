@@ -445,3 +445,19 @@ def test_forms_with_many_rows(post, C, types):
     """several rows per worker, two groups, of a branch, a gate and a layer norm"""
     both(C, 1, 1402, C, F=2, types=types, post=post, pre=("layer", ""))
     both(C + 1, 1, 1402, C, F=2, types=types, post=post, pre=("rms", ""), arriving=False)
+
+
+@pytest.mark.parametrize("C", [136, 1536, 6144])
+@pytest.mark.parametrize("pre", [("layer", "wb"), ("rms", "w")])
+def test_first_norm_of_an_fp32_stream_for_a_bf16_branch(C, pre):
+    """without a branch the result's dtype is asked for, or that of the tensor that is given"""
+    x, _, kw, rkw = make(141, 2, 33, C, types=(FP32, BF16, FP32), pre=pre, branch=False)
+    h, z = pkg.gated_norm(x, None, **kw, branch_dtype=BF16)
+    assert h is None and z.dtype == BF16
+    (_, _), (rz, dz) = ref.gated_norm(x, None, **rkw)
+    ref.within(z, rz, dz, "z")
+    given = torch.empty_like(z)
+    assert pkg.gated_norm(x, None, **kw, out=(None, given))[1] is given and torch.equal(given, z)
+    plain = pkg.gated_norm(x, None, **kw)[1]
+    assert plain.dtype == FP32
+    ref.within(plain, rz, dz, "z")
