@@ -542,7 +542,8 @@ def gated_norm_backward(dh: Optional[torch.Tensor], dz: Optional[torch.Tensor], 
     """Run bsa_gated_norm_backward. dh [B, N, C] is the gradient that arrives at h from where h goes on (None:
     zero), dz the one at z (with pre only), h gated_norm's h (its x without y) and y its y. Without pre, dx is dh
     itself and nothing is written for it. `out`: (dx, dy). Gradients of the modulations have their dtype and
-    shape, those of weights and biases are fp32 [C]."""
+    shape, those of weights and biases are fp32 [C]. A broadcast modulation (an expanded one) is refused: its
+    gradient would be a sum over what it is broadcast to."""
     what = "gated_norm_backward"
     first = dh if dh is not None else dz
     if first is None:

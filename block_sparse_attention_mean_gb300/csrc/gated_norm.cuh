@@ -20,7 +20,7 @@ __host__ __device__ constexpr int most_threads(int regs, bool multi, int branch_
     return multi ? 128 : regs == 128 ? 512 : branch_size == 4 ? 320 : 384;
 }
 
-// Rows in flight per worker, forward: more of them are slower (65536 rows of 2048 channels: three 181 us, four 196 us).
+// Rows in flight per worker, forward: more of them are slower (65536 rows of 2048 channels: three 182 us, four 197 us).
 // Backward two, which have more tensors each (16384 rows of 2048 channels bf16: one 110.8 us, two 87.4, three 87.9), or one
 // where the largest CTA has no room for two of `bytes` a thread beside the `kept` bytes.
 constexpr int kStages = 3;
@@ -181,9 +181,9 @@ constexpr int V = 2;
 // ------------------------------------------------------------ rows and workers
 
 // The rows, B * N in order, cut into `workers` ranges of nearly equal length: range w begins at row
-// floor(w * step / 2^32), step = ceil(rows * 2^32 / workers). Longer and shorter ranges alternate on purpose: with
-// the longer ones first, all workers stood a whole number of rows (a multiple of a large power of two in bytes)
-// apart and met in the same memory channels (65536 rows of 2048 channels: 184 against 174 us).
+// floor(w * step / 2^32), step = ceil(rows * 2^32 / workers). Longer and shorter ranges alternate: with the longer ones
+// first, most workers stand the same number of rows apart, and meet a little more often in the same memory channels
+// (65536 rows of 2048 channels: 183.3 against 181.9 us).
 struct Ranges {
     int rows, workers;
     uint64_t step, per_step;
@@ -424,8 +424,8 @@ struct Shape {
 };
 
 // Workers: as many as fit on the device at once, each with an equal share of the rows; at most one per row. A worker is
-// a row's threads, or (teams) a CTA: several rows of up to 512 channels side by side in 128 threads, no more of them than
-// a group has rows.
+// a row's threads, or (teams) a CTA: several rows of up to 1024 channels side by side in up to 128 threads, no more of them
+// than a group has rows.
 inline Shape shape_of(const bsa_gated_norm_desc &d, int regs, int sms, int stages, int thread_bytes, int kept_bytes = 0,
                       bool teams = false)
 {

@@ -12,7 +12,7 @@
 // range (long_groups == 0), a CTA that held a whole group writes its modulations' gradients itself, and adds up the sums
 // for the weights in a third slot.
 //
-// 16384 rows of 2048 channels bf16, RMS norms before and after, all gradients, 16 groups: 87 us, 4.6 TB/s (68% of a plain
+// 16384 rows of 2048 channels bf16, RMS norms before and after, all gradients, 16 groups: 88 us, 4.6 TB/s (68% of a plain
 // copy's rate). Each further row costs 4.1 ns, 89% of that rate; the rest is the start, the slots (8 KB a CTA and sum) and the
 // second kernel, 20 us together. The four sums take 64 registers per thread, which leaves 12 warps per SM; kept in tensor
 // memory they leave 16, but each row then waits for them four times (111 against 93 us).

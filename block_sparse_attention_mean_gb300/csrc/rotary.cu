@@ -43,9 +43,9 @@ constexpr int kResident = 2, kForwardStages = 4, kBackwardStages = 3;
 // Heads side by side in a step: the largest power of two up to kTogether that divides all the head counts, as long as
 // there are kSteps steps of Q and K to a tile. With one, a token's row is read 256 bytes at a time, with eight, a head's
 // rows are written 1 KB at a time, and either way the memory's pages are opened more often (d = 128 bf16, 16640 tokens of
-// 24 heads, us forward and backward: one 115.7 and 154.7, two 111.8 and 153.2, four 108.0 and 134.8, eight 117.9 and
-// 155.8). But each of the threads that share a token computes its angles, and few steps do not make up for that (three
-// batches of 57314 tokens, two heads: two together 174, one 125; 65536 tokens of 16 heads: four together 267, two 257).
+// 24 heads, us forward and backward: one 115.6 and 152.5, two 111.8 and 145.8, four 101.9 and 133.2, eight 113.1 and
+// 149.7). But each of the threads that share a token computes its angles, and few steps do not make up for that (three
+// batches of 57314 tokens, two heads: two together 169, one 117; 65536 tokens of 16 heads: four together 264, two 254).
 constexpr int kTogether = 4, kSteps = 12;
 
 // What a thread holds of a head: 16 channels in groups of 16 bytes (GROUP channels), from c[g] on, dealt out so that a
@@ -622,7 +622,9 @@ bsa_status backward(const RotaryArgs &a, int sms, cudaStream_t st)
     auto kern = rotary_backward_kernel<T, D, HALVES>;
     constexpr int STAGE = kThreads * 16 * sizeof(T), SUMS = kThreads * 128;
     static std::atomic<uint64_t> done{0};
-    constexpr int RESIDENT = sizeof(T) == 2 ? kResident : 1;  // fp32: 128 KB of shared memory per CTA
+    // fp32 with the norm and a dweight takes 128 KB of shared memory, which leaves one CTA per SM (16640 tokens of 24
+    // heads of 128: 272 us, 6.0 TB/s). The forms that take less, 48 KB without the norm, go by the same rule (190 us, 6.5).
+    constexpr int RESIDENT = sizeof(T) == 2 ? kResident : 1;
     const bsa_status ok = allow_smem(kern, kBackwardStages * 2 * STAGE + SUMS, done);
     if (ok != BSA_OK) return ok;
     Work w;
