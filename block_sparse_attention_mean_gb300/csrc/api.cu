@@ -124,6 +124,12 @@ bsa_status check_spec(const bsa_static_spec *s, int nB, int64_t *count)
 
 namespace bsa {
 
+void current_debug_config(uint32_t *flags, uint64_t *wait_limit_ns)
+{
+    *flags = g_dbg_flags;
+    *wait_limit_ns = g_wait_limit_ns;
+}
+
 bsa_status current_sm_count(int *sm_count)
 {
     int dev = 0;

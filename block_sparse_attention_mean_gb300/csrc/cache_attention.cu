@@ -1,0 +1,711 @@
+// cache_attention.cu -- attention of one new token per sequence over a paged cache (bsa_cache_attention).
+//
+// Every key and value is used by the H / Hk query heads of its head and by nothing else: one pass over the cache
+// bounds the call (2 * d multiplications per byte-pair and head are far below the tensor cores' rate), so the
+// kernel is built around keeping loads in flight everywhere at once.
+//
+//   * The tokens of all sequences and key heads form one row of units of 64 tokens, which is cut evenly over the
+//     resident CTAs, whatever the lengths. Where a cut falls inside a (sequence, key head), its pieces leave partial
+//     results (O, max, sums) in the workspace and the CTA that finishes last joins them in the order of the tokens:
+//     in groups of kGroup, then over the groups, so that no CTA reads many.
+//   * Each of a CTA's four warps takes 16 tokens of a unit through a ring of its own in shared memory, filled with
+//     16-byte cp.async far ahead and across the ends of sequences. Warps meet only at the end of a (sequence, head).
+//   * The products run on mma.sync.m16n8k16 with the 16 tokens (then 16 channels) as rows and 8 query heads as
+//     columns, S^T = K Q^T and O^T = V^T P^T: 8 heads fill the narrow side, as many as share a key head in practice, and the
+//     softmax's result moves from one product to the next by transposing 8 x 8 blocks in registers. tcgen05 wants 64 or
+//     more rows and operands in shared memory; at one query the tensor cores are a quarter busy at most either way.
+//   * The running maximum is raised, and O rescaled, only when a score passes it by 2^8 (fp32 sums, P at most 2^8).
+//   * 8-bit rows become fp16 (exact: e4m3 has 4 bits and fp16 its range). Q is scaled by a power of two to below 2
+//     and rounded to fp16 (exact for all of its 8 bits down to 2^-17 of the largest); the key's exponent multiplies
+//     the fp32 score, the value's is added to it in log2, so that P 2^e is what is rounded, to 11 bits, with a maximum
+//     of its own near one; the softmax's sum takes 2^-e out again.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "cache_internal.h"
+#include "ptx.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 16;              // tokens of a warp at a time
+constexpr int kUnit = kWarps * kTile;  // tokens of a unit
+constexpr int kGroup = 16;             // partial results that one CTA joins at a time
+constexpr int kSlotHeads = 16;         // query heads of a partial result
+constexpr float kRaise = 8.0f;         // log2 of how far a score may pass the running maximum
+
+struct Params {
+    CacheView cache;
+    TableView table;
+    PackedView q, o;
+    const int32_t *kv_lens;
+    float *lse;
+    int H, g, chunks, HH;  // query heads per key head; chunks of them; chunks of all key heads
+    float scale;
+    uint32_t *err;
+    uint32_t *tickets;  // [3][kCacheMaxCtas]
+    float *part_o;      // [slot][kSlotHeads][D]
+    float4 *part_s;     // [slot][kSlotHeads] (max in log2, sum, sum of the rounded weights, 0)
+};
+
+template <int D, bool E4M3>
+struct Ring {
+    static constexpr int kRow = E4M3 ? D : 2 * D;  // bytes of a row
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kData = kTile * kRow;     // K of a tile, or V
+    static constexpr int kStage = 2 * kData + (E4M3 ? 32 : 0);
+    static constexpr int kStages = 24576 / (2 * kData) > 8 ? 8 : 24576 / (2 * kData);
+    static constexpr int kWarpBytes = kStages * kStage;
+    static constexpr int kPad = D + 4;             // floats between heads where warps join
+    static constexpr int kJoin = kWarps * kWarpBytes;
+    static constexpr int kBytes = kJoin + 8 * kPad * 4;
+    // 16-byte chunk ch of row r lies at chunk swizzle(ch, r): without it the readers' rows share banks
+    static __device__ __forceinline__ int k_swizzle(int ch, int r) { return E4M3 ? (D == 128 ? ch ^ ((r & 1) << 2) : ch) : ch ^ (r & 7); }
+    static __device__ __forceinline__ int v_swizzle(int ch, int r)
+    {
+        return E4M3 ? (D == 128 ? ch ^ (((r >> 1) & 3) << 1) : ch ^ ((r >> 1) & 3)) : ch ^ (r & 7);
+    }
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// c += a b: rows x 16 times 16 x 8, 16-bit operands of one type
+template <bool HALF>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (HALF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the two e4m3 values of a 16-bit half of w, as f16x2
+__device__ __forceinline__ uint32_t half2_lo(uint32_t w)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+    return h;
+}
+__device__ __forceinline__ uint32_t half2_hi(uint32_t w) { return half2_lo(w >> 16); }
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// tokens of sequence b in the cache; a malformed length (reported) counts as none
+__device__ __forceinline__ int valid_len(const Params &p, int b)
+{
+    const int n = __ldg(p.kv_lens + b);
+    if (n < 0 || n > (static_cast<int64_t>(p.table.width) << p.cache.page_shift)) {
+        raise_error(p.err, BSA_ERR_INVALID_ARG);
+        return 0;
+    }
+    return n;
+}
+
+// A place among the units: unit `tile` of (sequence b, chunk of heads hu)
+struct Place {
+    int b, hu, tile, len;
+    __device__ __forceinline__ int tiles() const { return (len + kUnit - 1) / kUnit; }
+    // the next unit; only called where there is one
+    __device__ __forceinline__ void next(const Params &p)
+    {
+        if (++tile < tiles()) return;
+        tile = 0;
+        if (++hu < p.HH) return;
+        hu = 0;
+        do {
+            ++b;
+            len = b < p.table.B ? valid_len(p, b) : 1;
+        } while (len == 0);
+    }
+};
+
+// CTA that has unit u when `units` are cut over `ctas`: CTA c has [c * units / ctas, (c + 1) * units / ctas)
+__device__ __forceinline__ int cta_of(int64_t u, int64_t units, int ctas)
+{
+    return static_cast<int>(((u + 1) * ctas + units - 1) / units) - 1;
+}
+
+__device__ __forceinline__ size_t slot_of(int c0, int part) { return part == 0 ? 2 * c0 + 1 : 2 * (c0 + part); }
+
+// One thread's share of a joined result: 8 channels of a head
+struct Joined {
+    float o[8];
+    float m, l, lp;
+};
+
+// The partial results 0, step, 2 step, ... (count of them) of the parts that begin at CTA c0, for one head and 8 channels
+template <int D>
+__device__ __forceinline__ Joined join_parts(const Params &p, int c0, int first, int step, int count, int head, int ch)
+{
+    Joined r;
+    r.m = -CUDART_INF_F;
+    for (int i = 0; i < count; ++i)
+        r.m = fmaxf(r.m, __ldcg(p.part_s + slot_of(c0, first + i * step) * kSlotHeads + head).x);
+    r.l = r.lp = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r.o[k] = 0.0f;
+    const float base = r.m == -CUDART_INF_F ? 0.0f : r.m;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+        const size_t row = slot_of(c0, first + i * step) * kSlotHeads + head;
+        const float4 s = __ldcg(p.part_s + row);
+        const float4 *src = reinterpret_cast<const float4 *>(p.part_o + row * D + ch);
+        const float4 a = __ldcg(src), b = __ldcg(src + 1);
+        const float w = ex2_approx(s.x - base);
+        r.l += w * s.y;
+        r.lp += w * s.z;
+        r.o[0] += w * a.x, r.o[1] += w * a.y, r.o[2] += w * a.z, r.o[3] += w * a.w;
+        r.o[4] += w * b.x, r.o[5] += w * b.y, r.o[6] += w * b.z, r.o[7] += w * b.w;
+    }
+    return r;
+}
+
+__device__ __forceinline__ void write_result(const Params &p, int b, int h, int ch, const Joined &r)
+{
+    const float inv = r.lp != 0.0f ? 1.0f / r.lp : 0.0f;
+    uint4 v;
+    v.x = pack_bf16x2(r.o[0] * inv, r.o[1] * inv);
+    v.y = pack_bf16x2(r.o[2] * inv, r.o[3] * inv);
+    v.z = pack_bf16x2(r.o[4] * inv, r.o[5] * inv);
+    v.w = pack_bf16x2(r.o[6] * inv, r.o[7] * inv);
+    *reinterpret_cast<uint4 *>(p.o.p + b * p.o.token + h * p.o.head + ch * 2) = v;
+    if (ch == 0 && p.lse)
+        p.lse[static_cast<int64_t>(b) * p.H + h] = (r.m + log2f(r.l)) * 0.69314718055994530942f;
+}
+
+template <int D, bool E4M3, int NH>
+__global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Params p)
+{
+    using R = Ring<D, E4M3>;
+    constexpr int KS = D / 16;  // steps of 16 channels
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t scan[kWarps];
+    __shared__ int64_t found_rel;
+    __shared__ int found_b;
+    __shared__ float st_m[kWarps][8 * NH], st_l[kWarps][8 * NH], st_lp[kWarps][8 * NH];
+    __shared__ uint32_t arrived;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r = lane >> 2, j = lane & 3;
+    const int cta = blockIdx.x;
+
+    // sequences without tokens
+    for (int b = cta; b < p.table.B; b += gridDim.x) {
+        if (valid_len(p, b) != 0) continue;
+        for (int i = tid; i < p.H * (D / 8); i += kThreads)
+            *reinterpret_cast<uint4 *>(p.o.p + b * p.o.token + (i / (D / 8)) * p.o.head + (i % (D / 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse)
+            for (int h = tid; h < p.H; h += kThreads) p.lse[static_cast<int64_t>(b) * p.H + h] = -CUDART_INF_F;
+    }
+
+    // units in front of each thread's run of sequences, and of all
+    const int run = (p.table.B + kThreads - 1) / kThreads;
+    const int b_lo = min(p.table.B, tid * run), b_hi = min(p.table.B, b_lo + run);
+    int64_t mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += (valid_len(p, b) + kUnit - 1) / kUnit;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t units = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += scan[w];
+        units += scan[w];
+    }
+    units *= p.HH;
+    before *= p.HH;
+    // every CTA that takes part has a unit, so that the parts of a (sequence, head) belong to consecutive ones
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), units));
+    if (cta >= ctas) return;
+    const int64_t u_lo = cta * units / ctas, u_hi = (cta + 1) * units / ctas;
+    if (u_lo >= before && u_lo < before + mine * p.HH) {
+        int64_t at = before;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const int64_t n = static_cast<int64_t>((valid_len(p, b) + kUnit - 1) / kUnit) * p.HH;
+            if (u_lo < at + n) {
+                found_b = b;
+                found_rel = u_lo - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    Place here;
+    here.b = found_b;
+    here.len = valid_len(p, here.b);
+    here.hu = static_cast<int>(found_rel / here.tiles());
+    here.tile = static_cast<int>(found_rel - static_cast<int64_t>(here.hu) * here.tiles());
+
+    // ---- the warp's ring: `ahead` runs kStages - 1 units in front of `here`
+    const uint32_t ring = smem_u32(smem) + warp * R::kWarpBytes;
+    Place ahead = here;
+    int64_t issued = u_lo;  // next unit to load
+    const int page_mask = (1 << p.cache.page_shift) - 1;
+    auto page_of = [&](const Place &w) -> int {
+        const int tok = w.tile * kUnit + warp * kTile;
+        if (tok >= w.len) return 0;
+        return __ldg(p.table.pages + w.b * p.table.stride + (tok >> p.cache.page_shift));
+    };
+    int page = page_of(ahead);
+    auto load = [&](int stage) {
+        if (issued < u_hi) {
+            const int tok = ahead.tile * kUnit + warp * kTile;
+            const int left = ahead.len - tok;  // tokens of the tile that exist
+            if (left > 0) {
+                bool ok = page >= 0 && page < p.cache.n_pages;
+                if (!ok) raise_error(p.err, BSA_ERR_INVALID_ARG);
+                const int kh = ahead.hu / p.chunks;
+                const int64_t row = ok ? ((static_cast<int64_t>(page) * p.cache.heads + kh) << p.cache.page_shift) + (tok & page_mask) : 0;
+                const char *ks = p.cache.k + row * R::kRow, *vs = p.cache.v + row * R::kRow;
+                const uint32_t at = ring + stage * R::kStage;
+#pragma unroll
+                for (int i = 0; i < R::kChunks / 2; ++i) {
+                    const int idx = i * 32 + lane, rr = idx / R::kChunks, ch = idx % R::kChunks;
+                    const uint32_t bytes = ok && rr < left ? 16u : 0u;  // rows that do not exist become zeros
+                    cp_async16(at + rr * R::kRow + R::k_swizzle(ch, rr) * 16, ks + idx * 16, bytes);
+                    cp_async16(at + R::kData + rr * R::kRow + R::v_swizzle(ch, rr) * 16, vs + idx * 16, bytes);
+                }
+                if constexpr (E4M3)
+                    if (lane < 2) cp_async16(at + 2 * R::kData + lane * 16, (lane ? p.cache.v_exp : p.cache.k_exp) + row, ok ? 16u : 0u);
+            }
+            if (++issued < u_hi) {
+                ahead.next(p);
+                page = page_of(ahead);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < R::kStages - 1; ++s) load(s);
+
+    uint32_t qf[NH][KS][2];
+    float qs[NH][2];           // scale of the scores of heads 2j and 2j + 1
+    float m[NH][2], l[NH][2], lp[NH][2];
+    float o[KS][NH][4];        // O^T: rows are channels, columns heads 2j and 2j + 1
+    int stage = 0;
+    int64_t u = u_lo;
+    while (u < u_hi) {
+        // ---- a (sequence, chunk of heads): its units in this CTA are [here.tile, end)
+        const int tiles = here.tiles(), first = here.tile;
+        const int64_t whole = u - first;  // its first unit
+        const int end = static_cast<int>(min(static_cast<int64_t>(tiles), u_hi - whole));
+        const int kh = here.hu / p.chunks, head0 = (here.hu % p.chunks) * 8 * NH;  // of the group
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const int head = head0 + n * 8 + r;
+            const bool real = head < p.g;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                p.q.p + here.b * p.q.token + static_cast<int64_t>(kh * p.g + (real ? head : 0)) * p.q.head);
+            uint32_t big = 0u;
+#pragma unroll
+            for (int t = 0; t < KS; ++t) {
+                if constexpr (E4M3) {  // channels c .. c + 3, as the thread reads them from K's rows
+                    const int c = D == 128 ? (j + 4 * (t >> 2)) * 16 + 4 * (t & 3) : j * 16 + 4 * t;
+                    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src + c / 2));
+                    qf[n][t][0] = real ? w.x : 0u;
+                    qf[n][t][1] = real ? w.y : 0u;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        big = max(big, (qf[n][t][k] << 16) & 0x7FFFFFFFu);
+                        big = max(big, qf[n][t][k] & 0x7FFF0000u);
+                    }
+                } else {
+                    const uint32_t lo = __ldg(src + t * 8 + j), hi = __ldg(src + t * 8 + j + 4);
+                    qf[n][t][0] = real ? lo : 0u;
+                    qf[n][t][1] = real ? hi : 0u;
+                }
+            }
+            if constexpr (E4M3) {
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+                // |q| < 2 after division by 2^E; a row below 2^-126 keeps its values (they are zero in fp16)
+                const int E = max(-126, min(126, static_cast<int>(big >> 23) - 127));
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
+                const float up = p.scale * __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
+#pragma unroll
+                for (int t = 0; t < KS; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        qf[n][t][k] = pack_half2(__uint_as_float(qf[n][t][k] << 16) * down,
+                                                 __uint_as_float(qf[n][t][k] & 0xFFFF0000u) * down);
+                qs[n][0] = __shfl_sync(0xFFFFFFFFu, up, 8 * j);
+                qs[n][1] = __shfl_sync(0xFFFFFFFFu, up, 8 * j + 4);
+            } else {
+                qs[n][0] = qs[n][1] = p.scale;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) m[n][k] = -CUDART_INF_F, l[n][k] = lp[n][k] = 0.0f;
+#pragma unroll
+            for (int t = 0; t < KS; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[t][n][k] = 0.0f;
+        }
+
+        for (int tile = first; tile < end; ++tile, ++u) {
+            load((stage + R::kStages - 1) % R::kStages);
+            cp_async_wait_group<R::kStages - 1>();
+            __syncwarp();
+            const int left = here.len - tile * kUnit - warp * kTile;
+            if (left > 0) {
+                const uint32_t ka = ring + stage * R::kStage, va = ka + R::kData;
+                float s[NH][2][4];  // S^T, two sums of every other step: rows are tokens, columns heads
+#pragma unroll
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s[n][0][k] = s[n][1][k] = 0.0f;
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint4 lo = lds128(ka + r * R::kRow + R::k_swizzle(j + 4 * c, r) * 16);
+                        const uint4 hi = lds128(ka + (r + 8) * R::kRow + R::k_swizzle(j + 4 * c, r + 8) * 16);
+                        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t a[4] = {half2_lo(wl[t]), half2_lo(wh[t]), half2_hi(wl[t]), half2_hi(wh[t])};
+#pragma unroll
+                            for (int n = 0; n < NH; ++n) mma16816<true>(s[n][t & 1], a, qf[n][4 * c + t][0], qf[n][4 * c + t][1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < KS; ++t) {
+                        uint32_t a[4];
+                        ldmatrix4(a, ka + (lane & 15) * R::kRow + R::k_swizzle(2 * t + (lane >> 4), lane & 15) * 16);
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) mma16816<false>(s[n][t & 1], a, qf[n][t][0], qf[n][t][1]);
+                    }
+                }
+                // weights: log2 of them in x, of tokens r and r + 8
+                const bool in0 = r < left, in1 = r + 8 < left;
+                float k0 = 1.0f, k1 = 1.0f, e0 = 0.0f, e1 = 0.0f, d0 = 1.0f, d1 = 1.0f;
+                if constexpr (E4M3) {
+                    const uint32_t ea = ka + 2 * R::kData;
+                    const uint32_t b0 = lds8(ea + r), b1 = lds8(ea + r + 8), c0 = lds8(ea + 16 + r), c1 = lds8(ea + 24 + r);
+                    k0 = __uint_as_float(b0 << 23), k1 = __uint_as_float(b1 << 23);
+                    e0 = static_cast<float>(static_cast<int>(c0) - 127), e1 = static_cast<float>(static_cast<int>(c1) - 127);
+                    d0 = __uint_as_float((254u - min(c0, 253u)) << 23), d1 = __uint_as_float((254u - min(c1, 253u)) << 23);
+                }
+                bool pass = false;
+#pragma unroll
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float x = s[n][0][k] + s[n][1][k];
+                        if constexpr (E4M3) x = fmaf(x, qs[n][k & 1] * (k < 2 ? k0 : k1), k < 2 ? e0 : e1);
+                        else x *= qs[n][k & 1];
+                        x = (k < 2 ? in0 : in1) ? x : -CUDART_INF_F;
+                        s[n][0][k] = x;
+                        pass |= x > m[n][k & 1] + kRaise;
+                    }
+                if (__any_sync(0xFFFFFFFFu, pass)) {
+#pragma unroll
+                    for (int n = 0; n < NH; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float x = fmaxf(s[n][0][h], s[n][0][2 + h]);
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
+                            x = fmaxf(x, m[n][h]);
+                            const float a = x == -CUDART_INF_F ? 1.0f : ex2_approx(m[n][h] - x);
+                            m[n][h] = x;
+                            l[n][h] *= a;
+                            lp[n][h] *= a;
+#pragma unroll
+                            for (int t = 0; t < KS; ++t) o[t][n][h] *= a, o[t][n][2 + h] *= a;
+                        }
+                }
+                uint32_t pf[NH][2];
+#pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    float w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float base = m[n][k & 1] == -CUDART_INF_F ? 0.0f : m[n][k & 1];
+                        w[k] = ex2_approx(s[n][0][k] - base);
+                        if constexpr (E4M3) l[n][k & 1] = fmaf(w[k], k < 2 ? d0 : d1, l[n][k & 1]);
+                        else l[n][k & 1] += w[k];
+                    }
+                    if constexpr (E4M3) {
+                        pf[n][0] = pack_half2(w[0], w[1]);
+                        pf[n][1] = pack_half2(w[2], w[3]);
+                    } else {
+                        pf[n][0] = pack_bf16x2(w[0], w[1]);
+                        pf[n][1] = pack_bf16x2(w[2], w[3]);
+                        add_bf16x2_to_f32(lp[n][0], lp[n][1], pf[n][0]);
+                        add_bf16x2_to_f32(lp[n][0], lp[n][1], pf[n][1]);
+                    }
+                    pf[n][0] = transpose8x8(pf[n][0]);
+                    pf[n][1] = transpose8x8(pf[n][1]);
+                }
+                if constexpr (E4M3) {
+                    // thread r has channels [r * D / 8, (r + 1) * D / 8) of tokens 2j, 2j + 1, 2j + 8, 2j + 9
+                    uint32_t w[4][D / 32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = 2 * j + (k & 1) + 8 * (k >> 1);
+                        if constexpr (D == 128) {
+                            const uint4 v = lds128(va + row * R::kRow + R::v_swizzle(r, row) * 16);
+                            w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
+                        } else {
+                            const uint2 v = lds64(va + row * R::kRow + R::v_swizzle(r >> 1, row) * 16 + (r & 1) * 8);
+                            w[k][0] = v.x, w[k][1] = v.y;
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) {
+                        const uint32_t a01 = __byte_perm(w[0][q], w[1][q], 0x5140), a23 = __byte_perm(w[0][q], w[1][q], 0x7362);
+                        const uint32_t b01 = __byte_perm(w[2][q], w[3][q], 0x5140), b23 = __byte_perm(w[2][q], w[3][q], 0x7362);
+                        const uint32_t t0[4] = {half2_lo(a01), half2_hi(a01), half2_lo(b01), half2_hi(b01)};
+                        const uint32_t t1[4] = {half2_lo(a23), half2_hi(a23), half2_lo(b23), half2_hi(b23)};
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) {
+                            mma16816<true>(o[2 * q][n], t0, pf[n][0], pf[n][1]);
+                            mma16816<true>(o[2 * q + 1][n], t1, pf[n][0], pf[n][1]);
+                        }
+                    }
+                } else {
+                    const int row = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+                    for (int t = 0; t < KS; ++t) {
+                        uint32_t a[4];
+                        ldmatrix4_trans(a, va + row * R::kRow + R::v_swizzle(2 * t + ((lane >> 3) & 1), row) * 16);
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) mma16816<false>(o[t][n], a, pf[n][0], pf[n][1]);
+                    }
+                }
+            }
+            __syncwarp();  // the stage is read: the next load may overwrite it
+            stage = stage + 1 == R::kStages ? 0 : stage + 1;
+        }
+
+        // ---- the four warps' results become one
+#pragma unroll
+        for (int n = 0; n < NH; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) {
+                    l[n][h] += __shfl_xor_sync(0xFFFFFFFFu, l[n][h], w);
+                    lp[n][h] += __shfl_xor_sync(0xFFFFFFFFu, lp[n][h], w);
+                }
+                if (r == 0) {
+                    st_m[warp][n * 8 + 2 * j + h] = m[n][h];
+                    st_l[warp][n * 8 + 2 * j + h] = l[n][h];
+                    st_lp[warp][n * 8 + 2 * j + h] = E4M3 ? l[n][h] : lp[n][h];
+                }
+            }
+        __syncthreads();
+        const bool is_whole = first == 0 && end == tiles;
+        const int c0 = cta_of(whole, units, ctas), c1 = cta_of(whole + tiles - 1, units, ctas);
+        const int parts = c1 - c0 + 1, part = cta - c0;
+        float *join = reinterpret_cast<float *>(smem + R::kJoin);
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            if (head0 + n * 8 >= p.g) break;
+            float wt[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = n * 8 + 2 * j + h;
+                const float M = fmaxf(fmaxf(st_m[0][c], st_m[1][c]), fmaxf(st_m[2][c], st_m[3][c]));
+                wt[h] = M == -CUDART_INF_F ? 0.0f : ex2_approx(m[n][h] - M);
+            }
+            for (int w = 0; w < kWarps; ++w) {  // in turn, so that the sum has one order
+                if (w == warp) {
+#pragma unroll
+                    for (int t = 0; t < KS; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int ch = E4M3 ? r * (D / 8) + 2 * t + (k >> 1) : 16 * t + r + 8 * (k >> 1);
+                            float *at = join + (2 * j + (k & 1)) * R::kPad + ch;
+                            const float x = o[t][n][k] * wt[k & 1];
+                            *at = w == 0 ? x : *at + x;
+                        }
+                }
+                __syncthreads();
+            }
+            for (int i = tid; i < D; i += kThreads) {  // 8 heads, D / 8 lanes of 8 channels
+                const int hd = i / (D / 8), ch = (i % (D / 8)) * 8, c = n * 8 + hd;
+                if (head0 + c >= p.g) continue;
+                Joined res;
+                res.m = fmaxf(fmaxf(st_m[0][c], st_m[1][c]), fmaxf(st_m[2][c], st_m[3][c]));
+                res.l = res.lp = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float a = res.m == -CUDART_INF_F ? 0.0f : ex2_approx(st_m[w][c] - res.m);
+                    res.l += a * st_l[w][c];
+                    res.lp += a * st_lp[w][c];
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) res.o[k] = join[hd * R::kPad + ch + k];
+                if (is_whole) {
+                    write_result(p, here.b, kh * p.g + head0 + c, ch, res);
+                } else {
+                    const size_t row = slot_of(c0, part) * kSlotHeads + c;
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + row * D + ch);
+                    dst[0] = make_float4(res.o[0], res.o[1], res.o[2], res.o[3]);
+                    dst[1] = make_float4(res.o[4], res.o[5], res.o[6], res.o[7]);
+                    if (ch == 0) p.part_s[row] = make_float4(res.m, res.l, res.lp, 0.0f);
+                }
+            }
+            __syncthreads();
+        }
+        if (!is_whole) {
+            // The last of a group of kGroup parts joins them, the last group joins the groups. A ticket is indexed by the
+            // CTA of the group's first part; the first group's and the final ones have rows of their own, since a CTA
+            // can be in the middle of one (sequence, head) and begin another.
+            const int group = part / kGroup, groups = (parts + kGroup - 1) / kGroup;
+            const int members = min(kGroup, parts - group * kGroup);
+            auto last_of = [&](uint32_t *ticket, int count) -> bool {
+                __threadfence();
+                __syncthreads();
+                if (tid == 0) {
+                    const uint32_t before_me = atomicAdd(ticket, 1u);
+                    if (before_me == static_cast<uint32_t>(count - 1)) *ticket = 0u;  // for the next call
+                    arrived = before_me;
+                }
+                __syncthreads();
+                const bool last = arrived == static_cast<uint32_t>(count - 1);
+                __threadfence();
+                __syncthreads();  // `arrived` may be written again
+                return last;
+            };
+            const int heads = min(8 * NH, p.g - head0);
+            if (last_of(p.tickets + (group == 0 ? 0 : kCacheMaxCtas) + c0 + group * kGroup, members)) {
+                bool final_join = groups == 1;
+                for (int i0 = 0; i0 < heads * (D / 8); i0 += kThreads) {
+                    const int i = i0 + tid, hd = i / (D / 8), ch = (i % (D / 8)) * 8;
+                    const bool on = hd < heads;
+                    Joined res;
+                    if (on) res = join_parts<D>(p, c0, group * kGroup, 1, members, hd, ch);
+                    if (final_join) {
+                        if (on) write_result(p, here.b, kh * p.g + head0 + hd, ch, res);
+                        continue;
+                    }
+                    __syncthreads();  // this round's heads are read: their first part's slot takes the group's result
+                    if (on) {
+                        const size_t row = slot_of(c0, group * kGroup) * kSlotHeads + hd;
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + row * D + ch);
+                        dst[0] = make_float4(res.o[0], res.o[1], res.o[2], res.o[3]);
+                        dst[1] = make_float4(res.o[4], res.o[5], res.o[6], res.o[7]);
+                        if (ch == 0) p.part_s[row] = make_float4(res.m, res.l, res.lp, 0.0f);
+                    }
+                }
+                if (!final_join && last_of(p.tickets + 2 * kCacheMaxCtas + c0, groups)) {
+                    for (int i = tid; i < heads * (D / 8); i += kThreads) {
+                        const int hd = i / (D / 8), ch = (i % (D / 8)) * 8;
+                        write_result(p, here.b, kh * p.g + head0 + hd, ch, join_parts<D>(p, c0, 0, kGroup, groups, hd, ch));
+                    }
+                }
+            }
+        }
+        if (u < u_hi) {
+            here.tile = tiles - 1;
+            here.next(p);
+        }
+    }
+    cp_async_wait_group<0>();
+}
+
+template <int D, bool E4M3, int NH>
+bsa_status launch(const CacheAttentionArgs &a, cudaStream_t st)
+{
+    using R = Ring<D, E4M3>;
+    auto kern = cache_attention_kernel<D, E4M3, NH>;
+    static_assert(2 * (R::kBytes + 2048) <= 233472, "two CTAs per SM");
+    static std::atomic<uint64_t> ready{0};
+    if (!allow_shared_memory(kern, R::kBytes, ready)) return BSA_ERR_CUDA;
+    int sms = 0;
+    const bsa_status s = current_sm_count(&sms);
+    if (s != BSA_OK) return s;
+    Params p;
+    p.cache = a.cache;
+    p.table = a.table;
+    p.q = a.q;
+    p.o = a.o;
+    p.kv_lens = a.kv_lens;
+    p.lse = a.lse;
+    p.H = a.H;
+    p.g = a.H / a.cache.heads;
+    p.chunks = (p.g + 8 * NH - 1) / (8 * NH);
+    p.HH = p.chunks * a.cache.heads;
+    p.scale = a.scale * 1.44269504088896340736f;
+    p.err = reinterpret_cast<uint32_t *>(a.ws);
+    p.tickets = reinterpret_cast<uint32_t *>(a.ws + kCacheTickets);
+    p.part_s = reinterpret_cast<float4 *>(a.ws + kCacheScratch);
+    p.part_o = reinterpret_cast<float *>(a.ws + kCacheScratch + sizeof(float4) * 2 * kCacheMaxCtas * kSlotHeads);
+    const int ctas = 2 * sms < kCacheMaxCtas ? 2 * sms : kCacheMaxCtas;
+    kern<<<ctas, kThreads, R::kBytes, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+template <int D, bool E4M3>
+bsa_status launch_heads(const CacheAttentionArgs &a, cudaStream_t st)
+{
+    return a.H / a.cache.heads <= 8 ? launch<D, E4M3, 1>(a, st) : launch<D, E4M3, 2>(a, st);
+}
+
+}  // namespace
+
+size_t cache_attention_workspace(int d)
+{
+    return sizeof(float4) * 2 * kCacheMaxCtas * kSlotHeads + sizeof(float) * 2 * kCacheMaxCtas * kSlotHeads * d;
+}
+
+bsa_status launch_cache_attention(const CacheAttentionArgs &a, cudaStream_t st)
+{
+    if (a.d == 128) return a.cache.e4m3 ? launch_heads<128, true>(a, st) : launch_heads<128, false>(a, st);
+    return a.cache.e4m3 ? launch_heads<64, true>(a, st) : launch_heads<64, false>(a, st);
+}
+
+}  // namespace bsa

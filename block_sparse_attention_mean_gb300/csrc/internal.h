@@ -87,6 +87,8 @@ bsa_status prepare_build_mask(const void *Q, const void *K, int dt, int B, int H
                               int64_t col_capacity, uint32_t *bitmap, MaskArgs *a);
 // streaming multiprocessors of the current device (a host query; enqueues nothing)
 bsa_status current_sm_count(int *sm_count);
+// what bsa_debug_config set
+void current_debug_config(uint32_t *flags, uint64_t *wait_limit_ns);
 bsa_status launch_build_mask(const MaskArgs &a, cudaStream_t st);
 bsa_status launch_validate_index(int R, int nKB, const int32_t *row_ptr, const int32_t *col_idx,
                                  const uint32_t *bitmap, char *ws, cudaStream_t st);

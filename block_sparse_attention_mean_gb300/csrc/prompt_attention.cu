@@ -1,0 +1,1099 @@
+// prompt_attention.cu -- attention over packed sequences, causal or not, with grouped heads (bsa_prompt_attention).
+//
+// 4 d multiplications and additions per visible (query, key) pair and head bound it: the tensor cores' rate, at which a
+// 128 x 128 block of one head takes 2 x 512 cycles of an SM (d = 128) and its 16384 exponentials about 550.
+//
+//   * A tile is 128 rows of S = Q K^T: floor(128 / g) tokens of a sequence with the g query heads of one key head, loaded
+//     by one TMA box, so that grouped heads share each K and V block that is fetched. A CTA holds two tiles of
+//     consecutive tokens (one CTA per SM) and both use each block: half the shared-memory fills per product.
+//   * 8 softmax warps, 4 per tile, a thread per row; a warp that issues each tile's products, a warp that loads, and one
+//     that looks after V where a mask ends in a block. The two tiles take turns on the tensor cores: while one's
+//     softmax runs, the other's P V and next Q K^T do. P (bf16) overwrites S in TMEM: 2 x (128 + d) columns.
+//   * The order of one tile's products is PV(i), QK(i + 1), from one thread: they execute in that order, so a
+//     QK(i + 1) may overwrite the P that PV(i) reads, and a full S(i + 1) says that O holds PV(i).
+//   * Online softmax in log2: the running maximum is raised only when a row's step sum passes 2^8 (then the step is
+//     done again and O rescaled). fp32 sums; O is divided by the sum of the weights as rounded to bf16.
+//   * A plan in one CTA cuts the work: items are (sequence, key head, two tiles), a sequence's heads one after another
+//     so that its K and V stay in L2, longest sequences and longest ranges first; an item well above the average of a
+//     CTA is split by key range, and a second launch joins the parts in order.
+//   * 0 * NaN: a masked weight of zero still multiplies V. In blocks where a mask ends, rows of V behind the sequence
+//     are zeroed in shared memory, and other values that are not finite too; these are then added in the epilogue to
+//     the rows that see them. Blocks that every row sees whole are not looked at.
+//   * Every wait is bounded (BSA_ERR_TIMEOUT in the workspace, clean exit).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "cache_internal.h"
+#include "ptx.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kTileM = 128;
+constexpr int kStep = 128;  // keys of a step
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadWarp = 8, kIssueWarp = 9, kFixWarp = 11;  // issuers: one per tile
+constexpr int kThreads = 12 * 32;
+// registers a thread after the split: 256 * 216 + 128 * 72 = 384 * 168, what the block is launched with
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr float kRescaleSum = 256.0f;
+constexpr uint32_t kDbgStall = 1u;  // of bsa_debug_config
+constexpr unsigned long long kDrainNs = 1000000000ull;  // copies and products in flight are waited for this long
+
+// Parts: an item of more than 1.5 shares (a CTA's average of steps, rounded up) becomes ceil(steps / share) parts, so
+// all split items together at most 1.67 per CTA.
+constexpr int kMaxSlots = 320;   // partial results (two tiles each): 1.67 * 152 and some
+constexpr int kMaxParts = 1088;  // entries that parts add: 1.67 * 640
+constexpr int kMaxChunks = 32;   // parts of one item
+constexpr int kPlanThreads = 1024;
+
+// Work of one CTA at a time; expanded by the key heads
+struct __align__(16) Entry {
+    int b, t0;       // sequence, first token of the first tile
+    int lo, hi;      // steps of 128 keys
+    int slot, seq0;  // first partial slot (of key head 0) or -1; first entry of the sequence
+    int seq_n, pad;  // entries of the sequence
+};
+struct __align__(16) Split {
+    int b, t0, chunks, slot;
+};
+
+struct PlanHeader {  // in the workspace, behind the tickets
+    uint32_t next, n_items, n_splits, n_slots;
+};
+
+struct Seqs {
+    const int32_t *cu_q, *cu_k;
+    int Tq, Tk, B, Hk, g, tpt, causal;
+};
+
+struct Seq {
+    int q0, n_q, k0, n_k;
+};
+
+// Sequence b, or one without queries where it is malformed (reported)
+__device__ __forceinline__ Seq seq_of(const Seqs &s, int b, uint32_t *err)
+{
+    Seq r;
+    r.q0 = __ldg(s.cu_q + b);
+    r.k0 = __ldg(s.cu_k + b);
+    const int q1 = __ldg(s.cu_q + b + 1), k1 = __ldg(s.cu_k + b + 1);
+    r.n_q = q1 - r.q0;
+    r.n_k = k1 - r.k0;
+    if (r.q0 < 0 || q1 < r.q0 || q1 > s.Tq || r.k0 < 0 || k1 < r.k0 || k1 > s.Tk) {
+        raise_error(err, BSA_ERR_INVALID_ARG);
+        r = Seq{0, 0, 0, 0};
+    }
+    return r;
+}
+
+// keys that query t of the sequence sees
+__device__ __forceinline__ int visible(int causal, int n_q, int n_k, int t)
+{
+    return causal ? max(0, min(n_k, t + 1 + n_k - n_q)) : n_k;
+}
+// steps of 128 keys of tokens [t0, t0 + n) (those of them that exist)
+__device__ __forceinline__ int steps_of(int causal, int n_q, int n_k, int t0, int n)
+{
+    if (t0 >= n_q) return 0;
+    return (visible(causal, n_q, n_k, min(t0 + n, n_q) - 1) + kStep - 1) / kStep;
+}
+__device__ __forceinline__ int item_steps(const Seqs &s, const Seq &q, int t0)
+{
+    return max(steps_of(s.causal, q.n_q, q.n_k, t0, s.tpt), steps_of(s.causal, q.n_q, q.n_k, t0 + s.tpt, s.tpt));
+}
+
+// ---------------------------------------------------------------- plan
+
+struct PlanArgs {
+    Seqs s;
+    int ctas, max_slots;
+    long long max_entries;
+    PlanHeader *hdr;
+    Entry *entries;
+    Split *splits;
+    int32_t *rank;    // [B] sequences, longest first
+    int32_t *at;      // [B] scratch: entries of the sequence of that rank
+    uint32_t *err;
+};
+
+// Exclusive prefix over the block's threads, and the total
+__device__ __forceinline__ long long block_prefix(long long v, long long &total, long long *warp_sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        long long w = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            if (lane >= o) w += y;
+        }
+        warp_sums[lane] = w;
+    }
+    __syncthreads();
+    total = warp_sums[31];
+    const long long excl = x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+    __syncthreads();
+    return excl;
+}
+
+__device__ __forceinline__ int chunks_of(int steps, int share)
+{
+    if (steps <= share + share / 2) return 1;
+    const int n = (steps + share - 1) / share;
+    return n < kMaxChunks ? n : kMaxChunks;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
+{
+    grid_launch_dependents();
+    __shared__ long long warp_sums[32];
+    __shared__ int bucket[kPlanThreads];
+    __shared__ int longest;
+    __shared__ uint32_t n_splits, n_slots;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Seqs &s = a.s;
+    bucket[tid] = 0;
+    if (tid == 0) longest = 0, n_splits = 0u, n_slots = 0u;
+    __syncthreads();
+    // sequences by their last item's steps, longest first (counting sort; 1023 steps and more count as equal)
+    auto key = [&](const Seq &q) -> int {
+        if (q.n_q == 0) return kPlanThreads - 1;
+        const int n = (visible(s.causal, q.n_q, q.n_k, q.n_q - 1) + kStep - 1) / kStep;
+        return kPlanThreads - 1 - min(n, kPlanThreads - 1);
+    };
+    for (int b = tid; b < s.B; b += kPlanThreads) atomicAdd(&bucket[key(seq_of(s, b, a.err))], 1);
+    __syncthreads();
+    long long total;
+    const int start = static_cast<int>(block_prefix(bucket[tid], total, warp_sums));
+    bucket[tid] = start;
+    __syncthreads();
+    for (int b = tid; b < s.B; b += kPlanThreads) a.rank[atomicAdd(&bucket[key(seq_of(s, b, a.err))], 1)] = b;
+    // steps of all items, and of the longest
+    long long mine = 0;
+    int most = 0;
+    for (int b = warp; b < s.B; b += 32) {
+        const Seq q = seq_of(s, b, a.err);
+        const int items = (q.n_q + 2 * s.tpt - 1) / (2 * s.tpt);
+        for (int i = lane; i < items; i += 32) {
+            const int n = item_steps(s, q, i * 2 * s.tpt);
+            mine += n;
+            most = max(most, n);
+        }
+    }
+    atomicMax(&longest, most);
+    block_prefix(mine, total, warp_sums);
+    const int share = static_cast<int>(max(1ll, min(1ll << 29, (total * s.Hk + a.ctas - 1) / a.ctas)));
+    const bool split = chunks_of(longest, share) > 1;
+    // entries of each sequence, in order of rank, and their places
+    for (int r = warp; r < s.B; r += 32) {
+        const Seq q = seq_of(s, a.rank[r], a.err);
+        const int items = (q.n_q + 2 * s.tpt - 1) / (2 * s.tpt);
+        int n = items;
+        if (split) {
+            n = 0;
+            for (int i = lane; i < items; i += 32) n += chunks_of(item_steps(s, q, i * 2 * s.tpt), share);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+        }
+        if (lane == 0) a.at[r] = n;
+    }
+    __syncthreads();
+    const int run = (s.B + kPlanThreads - 1) / kPlanThreads;
+    const int lo = min(s.B, tid * run), hi = min(s.B, lo + run);
+    long long n = 0;
+    for (int r = lo; r < hi; ++r) n += a.at[r];
+    long long before = block_prefix(n, total, warp_sums);
+    if (total > a.max_entries) {  // sequences that overlap: more tokens than there are
+        if (tid == 0) {
+            raise_error(a.err, BSA_ERR_INVALID_ARG);
+            a.hdr->next = a.hdr->n_items = a.hdr->n_splits = 0u;
+        }
+        return;
+    }
+    for (int r = lo; r < hi; ++r) {
+        const int c = a.at[r];
+        a.at[r] = static_cast<int>(before);
+        before += c;
+    }
+    __syncthreads();
+    const int entries = static_cast<int>(total);
+    for (int r = warp; r < s.B; r += 32) {
+        const int b = a.rank[r];
+        const Seq q = seq_of(s, b, a.err);
+        const int items = (q.n_q + 2 * s.tpt - 1) / (2 * s.tpt);
+        const int seq0 = a.at[r], seq_n = (r + 1 < s.B ? a.at[r + 1] : entries) - seq0;
+        int base = seq0;
+        for (int i0 = 0; i0 < items; i0 += 32) {
+            const int i = items - 1 - (i0 + lane);  // longest first
+            const int t0 = i * 2 * s.tpt;
+            const int steps = i >= 0 ? item_steps(s, q, t0) : 0;
+            const int c = i >= 0 ? (split ? chunks_of(steps, share) : 1) : 0;
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const int at = base + incl - c;
+            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            if (c == 0) continue;
+            // parts where there is room for their results; else the first entry takes the whole range
+            int slot = -1;
+            if (c > 1) {
+                slot = static_cast<int>(atomicAdd(&n_slots, static_cast<uint32_t>(c * s.Hk)));
+                if (slot + c * s.Hk > a.max_slots) slot = -1;
+                else a.splits[atomicAdd(&n_splits, 1u)] = Split{b, t0, c, slot};
+            }
+            for (int k = 0; k < c; ++k) {
+                Entry e;
+                e.b = b;
+                e.t0 = slot < 0 && k > 0 ? -1 : t0;  // -1: nothing to do
+                e.lo = slot < 0 ? 0 : static_cast<int>(static_cast<long long>(k) * steps / c);
+                e.hi = slot < 0 ? steps : static_cast<int>(static_cast<long long>(k + 1) * steps / c);
+                e.slot = slot < 0 ? -1 : slot + k * s.Hk;
+                e.seq0 = seq0;
+                e.seq_n = seq_n;
+                e.pad = 0;
+                a.entries[at + k] = e;
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        a.hdr->next = 0u;
+        a.hdr->n_items = static_cast<uint32_t>(entries) * static_cast<uint32_t>(s.Hk);
+        a.hdr->n_splits = n_splits;
+    }
+}
+
+// ---------------------------------------------------------------- the attention
+
+struct Params {
+    Seqs s;
+    float scale_log2;
+    PackedView o, v;
+    float *lse;
+    PlanHeader *hdr;
+    const Entry *entries;
+    float *part_o;       // [slot][2][128][D]
+    float4 *part_stats;  // [slot][2][128] (max in log2, sum, sum of the rounded weights, 0)
+    uint32_t *err;
+    unsigned long long wait_limit_ns;
+    int stall;  // load and multiply nothing: the first waits run out
+};
+
+struct Item {
+    int b, t0, n_q, n_k, q0, k0, kh, lo, hi, slot;
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int NK = D == 128 ? 2 : 4, NV = D == 128 ? 3 : 4;
+    static constexpr int kQBytes = kTileM * D * 2, kKVBytes = kStep * D * 2;
+    static constexpr int kSlab = 128 * 128;  // bytes of 64 columns of 128 rows
+    static constexpr int Q_OFF = 0, K_OFF = 2 * kQBytes, V_OFF = K_OFF + NK * kKVBytes, BAR_OFF = V_OFF + NV * kKVBytes;
+    static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_KEMPTY = B_KFULL + NK, B_VFULL = B_KEMPTY + NK,
+                         B_VEMPTY = B_VFULL + NV, B_VFIXED = B_VEMPTY + NV, B_SFULL = B_VFIXED + NV, B_PFULL = B_SFULL + 2,
+                         B_OFULL = B_PFULL + 2, B_OEMPTY = B_OFULL + 2, B_TFULL = B_OEMPTY + 2, B_TEMPTY = B_TFULL + 2,
+                         B_DRAIN = B_TEMPTY + 2, NBAR = B_DRAIN + 2;
+    static constexpr int MISC_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;
+    static constexpr int kItemWords = 12;
+    static constexpr int MISC_WORDS = 4 + 2 * kItemWords;  // TMEM base, abort flag, V flags of the two items, the items
+    static constexpr int SMEM = MISC_OFF + 4 * MISC_WORDS;
+    static constexpr int SMEM_ALLOC = SMEM + 1024;
+    static constexpr uint32_t IDESC_QK = idesc_bf16_f32(kTileM, kStep, 0, 0);
+    static constexpr uint32_t IDESC_PV = idesc_bf16_f32(kTileM, D, 0, 1);
+    static constexpr int T_S = 0, T_O = 2 * kStep;  // TMEM columns: S / P of both tiles, then O of both
+};
+
+// ---- bounded waits, inlined: a kernel that moves registers between its warps calls no functions
+struct Ctl {
+    volatile uint32_t *abort_flag;
+    uint32_t *err;
+    unsigned long long limit;
+};
+
+// Waits for a barrier's phase with all lanes of a warp. False (the abort flag raised, and BSA_ERR_TIMEOUT) after `limit`
+// ns, or when another warp gave up.
+__device__ __forceinline__ bool warp_wait_all(uint32_t bar, uint32_t parity, const Ctl &c)
+{
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!(ok = mbar_try_wait_sleep(bar, parity, 50000u))) {
+            if (*c.abort_flag) break;
+            if (globaltimer_ns() - t0 > c.limit) {
+                *c.abort_flag = 1u;
+                raise_error(c.err, BSA_ERR_TIMEOUT);
+                break;
+            }
+        }
+    }
+    return __all_sync(0xFFFFFFFFu, ok ? 1 : 0) != 0;
+}
+
+// For copies and products in flight on the way out: whatever the abort flag says
+__device__ __forceinline__ void wait_bar_drain(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 50000u))
+        if (globaltimer_ns() - t0 > kDrainNs) return;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// steps of tile x among the item's
+__device__ __forceinline__ int tile_steps(const Params &p, const Item &it, int x)
+{
+    const int n = steps_of(p.s.causal, it.n_q, it.n_k, it.t0 + x * p.s.tpt, p.s.tpt);
+    return max(0, min(n, it.hi) - it.lo);
+}
+
+// The next item from the ring of two; false at the end or when a wait gave up
+template <class C>
+__device__ __forceinline__ bool fetch(uint32_t sbase, const volatile int *items, const Ctl &ctl, int lane, int &count, Item &it)
+{
+    const int slot = count & 1;
+    if (!warp_wait_all(sbase + C::BAR_OFF + 8u * (C::B_TFULL + slot), (count >> 1) & 1, ctl)) return false;
+    const volatile int *w = items + slot * C::kItemWords;
+    it.b = w[0], it.t0 = w[1], it.n_q = w[2], it.n_k = w[3], it.q0 = w[4], it.k0 = w[5], it.kh = w[6], it.lo = w[7], it.hi = w[8],
+    it.slot = w[9];
+    ++count;
+    return it.b >= 0;
+}
+// ... and the slot may be written again
+template <class C>
+__device__ __forceinline__ void done_with(uint32_t sbase, int lane, int count)
+{
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sbase + C::BAR_OFF + 8u * (C::B_TEMPTY + ((count - 1) & 1)));
+}
+
+// Adds what is not finite among the rows [j_lo, j_hi) of V to a row of D results (fp32 or bf16) in global memory
+template <int D>
+__device__ __forceinline__ void add_not_finite(const char *v, int64_t stride, int j_lo, int j_hi, char *row, bool fp32)
+{
+    for (int j = j_lo; j < j_hi; ++j)
+        for (int c = 0; c < D; ++c) {
+            const float x = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(v + j * stride)[c]);
+            if ((__float_as_uint(x) & 0x7F800000u) != 0x7F800000u) continue;
+            float *f = reinterpret_cast<float *>(row) + c;
+            __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(row) + c;
+            if (fp32) *f += x;
+            else *h = __float2bfloat16(__bfloat162float(*h) + x);
+        }
+}
+
+template <int D, class C>
+__device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, uint32_t tmem, const volatile int *items,
+                                             const volatile uint32_t *vflags, const Ctl &ctl, int warp, int lane)
+{
+    auto bar = [&](int idx) -> uint32_t { return sbase + C::BAR_OFF + 8u * idx; };
+    constexpr int NC = kStep / 32;
+    const int x = warp >> 2;  // tile
+    const int trow = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + C::T_S + x * kStep;
+    const uint32_t tO = tmem + lanes + C::T_O + x * D;
+    const int rt = trow / p.s.g, rh = trow % p.s.g;  // token and head of the row within the tile
+    int G = 0, e = 0, count = 0;
+    Item it;
+    while (fetch<C>(sbase, items, ctl, lane, count, it)) {
+        const int n = tile_steps(p, it, x);
+        const int tok = it.t0 + x * p.s.tpt + rt;
+        const bool real = rt < p.s.tpt && tok < it.n_q;
+        const int nvis = real ? visible(p.s.causal, it.n_q, it.n_k, tok) : 0;
+        float m_run = -CUDART_INF_F;
+        uint64_t acc[2] = {0ull, 0ull};
+        float accp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < n; ++i, ++G) {
+            if (!warp_wait_all(bar(C::B_SFULL + x), G & 1, ctl)) return;
+            tc_fence_after();
+            const int nv = nvis - (it.lo + i) * kStep;  // columns that the row sees
+            const bool masked = __any_sync(0xFFFFFFFFu, nv < kStep);
+            // chunk c of S, columns that the row does not see as -inf; the loads that are under way complete here
+            auto ready = [&](int c, uint32_t (&sv)[32]) {
+                tmem_wait_ld();
+                reg_fence32(sv);
+                if (masked) {
+#pragma unroll
+                    for (int t = 0; t < 32; ++t)
+                        if (c * 32 + t >= nv) sv[t] = 0xFF800000u;
+                }
+            };
+            auto step_max = [&]() -> float {
+                float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll 1
+                for (int c = 0; c < NC; ++c) {
+                    uint32_t sv[32];
+                    tmem_ld32(tS + c * 32, sv);
+                    ready(c, sv);
+#pragma unroll
+                    for (int t = 0; t < 32; t += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mx[k] = fmax3(mx[k], __uint_as_float(sv[t + 2 * k]), __uint_as_float(sv[t + 2 * k + 1]));
+                }
+                return fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.scale_log2;
+            };
+            const uint64_t c2x = f2_pack(p.scale_log2, p.scale_log2);
+            uint64_t sacc[2];
+            float sap[4];
+            uint32_t pk[NC][16];  // P, stored over S when the step's sum has passed
+            auto exps = [&](float m) {
+                const float base = m == -CUDART_INF_F ? 0.0f : m;  // a row that has seen no key yet: every weight 0
+                const uint64_t nm2 = f2_pack(-base, -base);
+                sacc[0] = sacc[1] = 0ull;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sap[k] = 0.0f;
+                uint32_t sv[2][32];
+                tmem_ld32(tS, sv[0]);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    ready(c, sv[c & 1]);
+                    if (c + 1 < NC) tmem_ld32(tS + (c + 1) * 32, sv[(c + 1) & 1]);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c & 1][2 * q]), __uint_as_float(sv[c & 1][2 * q + 1])), c2x, nm2),
+                                  x0, x1);
+                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                        sacc[q & 1] = f2_add(sacc[q & 1], f2_pack(p0, p1));
+                        pk[c][q] = pack_bf16x2(p0, p1);
+                        add_bf16x2_to_f32(sap[2 * (q & 1)], sap[2 * (q & 1) + 1], pk[c][q]);
+                    }
+                }
+            };
+            if (__any_sync(0xFFFFFFFFu, m_run == -CUDART_INF_F)) {
+                const float m_step = step_max();
+                if (m_run == -CUDART_INF_F) m_run = m_step;
+            }
+            // a step sum of at most 2^8 bounds every weight: only a larger one (or NaN) raises the running maximum
+            float alpha = 1.0f;
+            bool again = false;
+            for (;;) {
+                exps(m_run);
+                if (again) break;
+                float s0, s1;
+                f2_unpack(f2_add(sacc[0], sacc[1]), s0, s1);
+                const bool raise = !(s0 + s1 <= kRescaleSum);
+                if (!__any_sync(0xFFFFFFFFu, raise)) break;
+                again = true;  // the whole warp: TMEM accesses are the warp's
+                const float m_step = fmaxf(m_run, step_max());
+                if (raise) {
+                    alpha = ex2_approx(m_run - m_step);
+                    m_run = m_step;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) tmem_st16(tS + c * 16, pk[c]);
+            if (again) {
+                const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) acc[k] = f2_fma(acc[k], a2, 0ull);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) accp[k] *= alpha;
+                if (i > 0) {  // O holds the steps before this one (see the order of the products)
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO + c * 32, ov);
+                        tmem_wait_ld();
+                        reg_fence32(ov);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alpha);
+                        tmem_st32(tO + c * 32, ov);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) acc[k] = f2_add(acc[k], sacc[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) accp[k] += sap[k];
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_PFULL + x));
+        }
+        float e0, e1;
+        f2_unpack(f2_add(acc[0], acc[1]), e0, e1);
+        const float l = e0 + e1, lp = (accp[0] + accp[1]) + (accp[2] + accp[3]);
+        const bool part = it.slot >= 0;
+        const int head = it.kh * p.s.g + rh;
+        char *orow = p.o.p + static_cast<int64_t>(it.q0 + tok) * p.o.token + head * p.o.head;
+        const size_t prow = part ? static_cast<size_t>(it.slot * 2 + x) * kTileM + trow : 0;
+        bool dirty = false;
+        if (n > 0) {
+            if (!warp_wait_all(bar(C::B_OFULL + x), e & 1, ctl)) return;
+            tc_fence_after();
+            ++e;
+            dirty = vflags[(count - 1) & 1] != 0u;
+        }
+        const float inv = part ? 1.0f : lp != 0.0f ? 1.0f / lp : 0.0f;
+#pragma unroll
+        for (int c0 = 0; c0 < D / 32; c0 += 2) {
+            uint32_t ov[2][32];
+            if (n > 0) {
+                tmem_ld32(tO + c0 * 32, ov[0]);
+                tmem_ld32(tO + (c0 + 1) * 32, ov[1]);
+                tmem_wait_ld();
+                reg_fence32(ov[0]);
+                reg_fence32(ov[1]);
+                if (c0 + 2 == D / 32) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + x));
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = c0 + h;
+#pragma unroll
+                for (int q = 0; q < 32; ++q) ov[h][q] = n > 0 ? __float_as_uint(__uint_as_float(ov[h][q]) * inv) : 0u;
+                if (part) {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + c * 32);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        dst[q] = make_float4(__uint_as_float(ov[h][4 * q]), __uint_as_float(ov[h][4 * q + 1]),
+                                             __uint_as_float(ov[h][4 * q + 2]), __uint_as_float(ov[h][4 * q + 3]));
+                } else if (real) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 64);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint4 w;
+                        w.x = pack_bf16x2(__uint_as_float(ov[h][8 * q]), __uint_as_float(ov[h][8 * q + 1]));
+                        w.y = pack_bf16x2(__uint_as_float(ov[h][8 * q + 2]), __uint_as_float(ov[h][8 * q + 3]));
+                        w.z = pack_bf16x2(__uint_as_float(ov[h][8 * q + 4]), __uint_as_float(ov[h][8 * q + 5]));
+                        w.w = pack_bf16x2(__uint_as_float(ov[h][8 * q + 6]), __uint_as_float(ov[h][8 * q + 7]));
+                        dst[q] = w;
+                    }
+                }
+            }
+        }
+        if (dirty && real) {
+            const int from = max(it.lo, visible(p.s.causal, it.n_q, it.n_k, it.t0) / kStep) * kStep;
+            add_not_finite<D>(p.v.p + static_cast<int64_t>(it.k0) * p.v.token + it.kh * p.v.head, p.v.token, from,
+                              min(nvis, it.hi * kStep), part ? reinterpret_cast<char *>(p.part_o + prow * D) : orow, part);
+        }
+        if (part) p.part_stats[prow] = make_float4(m_run, l, lp, 0.0f);
+        else if (real && p.lse)
+            p.lse[static_cast<int64_t>(head) * p.s.Tq + it.q0 + tok] = (m_run + log2f(l)) * 0.69314718055994530942f;
+        done_with<C>(sbase, lane, count);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const Params p)
+{
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int idx) -> uint32_t { return sbase + C::BAR_OFF + 8u * idx; };
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile uint32_t *vflags = misc + 2;
+    volatile int *items = reinterpret_cast<volatile int *>(misc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar(C::B_QFULL + x), 1);
+            mbar_init(bar(C::B_QEMPTY + x), 1);
+            mbar_init(bar(C::B_SFULL + x), 1);
+            mbar_init(bar(C::B_PFULL + x), 4);
+            mbar_init(bar(C::B_OFULL + x), 1);
+            mbar_init(bar(C::B_OEMPTY + x), 4);
+            mbar_init(bar(C::B_TFULL + x), 1);
+            mbar_init(bar(C::B_TEMPTY + x), kSoftmaxWarps + 3);
+            mbar_init(bar(C::B_DRAIN + x), 1);
+        }
+        for (int s = 0; s < C::NK; ++s) {
+            mbar_init(bar(C::B_KFULL + s), 1);
+            mbar_init(bar(C::B_KEMPTY + s), 2);  // both tiles' issuers
+        }
+        for (int s = 0; s < C::NV; ++s) {
+            mbar_init(bar(C::B_VFULL + s), 1);
+            mbar_init(bar(C::B_VEMPTY + s), 2);
+            mbar_init(bar(C::B_VFIXED + s), 1);
+        }
+        misc[1] = 0u;
+        misc[2] = misc[3] = 0u;
+        fence_mbar_init();
+    }
+    if (warp == kIssueWarp) {
+        tmem_alloc(smem_u32(misc), 512);
+        tmem_relinquish();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        tma_prefetch_map(&tmQ);
+        tma_prefetch_map(&tmK);
+        tma_prefetch_map(&tmV);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    grid_dependency_wait();  // the plan's results are read from here on
+    const uint32_t tmem = misc[0];
+    const Ctl ctl{reinterpret_cast<volatile uint32_t *>(misc + 1), p.err, p.wait_limit_ns};
+
+    if (warp < kSoftmaxWarps) {
+        regs_up<kSoftmaxRegs>();
+        softmax_role<D, C>(p, sbase, tmem, items, vflags, ctl, warp, lane);
+    } else {
+        regs_down<kOtherRegs>();
+        if (warp == kLoadWarp) {
+            // ------------------------------------------------------------ items, Q, K, V
+            const uint32_t n_items = p.hdr->n_items;
+            int count = 0, G = 0, e[2] = {0, 0};
+            bool ok = true;
+            while (ok) {
+                const int slot = count & 1;
+                Item it{};
+                it.b = -1;
+                for (;;) {
+                    uint32_t id = 0u;
+                    if (lane == 0) id = atomicAdd(&p.hdr->next, 1u);
+                    id = __shfl_sync(0xFFFFFFFFu, id, 0);
+                    if (id >= n_items) break;
+                    const Entry *first = p.entries + id / p.s.Hk;
+                    const int seq0 = first->seq0, seq_n = first->seq_n;
+                    const int rest = static_cast<int>(id) - seq0 * p.s.Hk;
+                    const Entry en = p.entries[seq0 + rest % seq_n];
+                    if (en.t0 < 0) continue;
+                    it.b = en.b, it.t0 = en.t0, it.lo = en.lo, it.hi = en.hi, it.kh = rest / seq_n;
+                    it.slot = en.slot < 0 ? -1 : en.slot + it.kh;
+                    break;
+                }
+                if (it.b >= 0) {
+                    const Seq q = seq_of(p.s, it.b, p.err);
+                    it.n_q = q.n_q, it.n_k = q.n_k, it.q0 = q.q0, it.k0 = q.k0;
+                }
+                if (count >= 2 && !warp_wait_all(bar(C::B_TEMPTY + slot), ((count >> 1) - 1) & 1, ctl)) break;
+                if (lane == 0) {
+                    volatile int *w = items + slot * C::kItemWords;
+                    w[0] = it.b, w[1] = it.t0, w[2] = it.n_q, w[3] = it.n_k, w[4] = it.q0, w[5] = it.k0, w[6] = it.kh, w[7] = it.lo,
+                    w[8] = it.hi, w[9] = it.slot;
+                    vflags[slot] = 0u;
+                    mbar_arrive(bar(C::B_TFULL + slot));
+                }
+                __syncwarp();
+                ++count;
+                if (it.b < 0) break;
+                if (p.stall) continue;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (tile_steps(p, it, x) == 0) continue;
+                    if (e[x] >= 1 && !warp_wait_all(bar(C::B_QEMPTY + x), (e[x] - 1) & 1, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar(C::B_QFULL + x), static_cast<uint32_t>(p.s.g * p.s.tpt * D * 2));
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(sbase + C::Q_OFF + x * C::kQBytes + c * C::kSlab, &tmQ, c * 64, it.kh * p.s.g,
+                                        it.q0 + it.t0 + x * p.s.tpt, bar(C::B_QFULL + x));
+                    }
+                    __syncwarp();
+                    ++e[x];
+                }
+                for (int i = it.lo; ok && i < it.hi; ++i, ++G) {
+                    const int ks = G % C::NK, vs = G % C::NV;
+                    if (G >= C::NK && !warp_wait_all(bar(C::B_KEMPTY + ks), ((G / C::NK) - 1) & 1, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar(C::B_KFULL + ks), C::kKVBytes);
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(sbase + C::K_OFF + ks * C::kKVBytes + c * C::kSlab, &tmK, c * 64, it.k0 + i * kStep, it.kh,
+                                        bar(C::B_KFULL + ks));
+                    }
+                    __syncwarp();
+                    if (G >= C::NV && !warp_wait_all(bar(C::B_VEMPTY + vs), ((G / C::NV) - 1) & 1, ctl)) {
+                        // the K load of this step is in flight and no later one will be: count it below
+                        ++G;
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar(C::B_VFULL + vs), C::kKVBytes);
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(sbase + C::V_OFF + vs * C::kKVBytes + c * C::kSlab, &tmV, c * 64, it.k0 + i * kStep, it.kh,
+                                        bar(C::B_VFULL + vs));
+                    }
+                    __syncwarp();
+                }
+            }
+            // after an abort: no copy of this warp is in flight when the CTA ends (a phase that has completed, or one
+            // that no copy fills, ends a wait too: at its limit)
+            if (lane == 0 && *ctl.abort_flag) {
+                for (int x = 0; x < 2; ++x)
+                    if (e[x] > 0) wait_bar_drain(bar(C::B_QFULL + x), (e[x] - 1) & 1);
+                for (int g = max(0, G - C::NK); g < G; ++g)
+                    wait_bar_drain(bar(C::B_KFULL + g % C::NK), (g / C::NK) & 1);
+                for (int g = max(0, G - C::NV); g < G; ++g)
+                    wait_bar_drain(bar(C::B_VFULL + g % C::NV), (g / C::NV) & 1);
+            }
+            __syncwarp();
+        } else if (warp == kFixWarp) {
+            // ------------------------------------------------------------ V where a mask ends
+            int count = 0, G = 0;
+            bool ok = true;
+            Item it;
+            while (ok && fetch<C>(sbase, items, ctl, lane, count, it)) {
+                const int from = visible(p.s.causal, it.n_q, it.n_k, it.t0) / kStep;  // first step that some row sees in part
+                for (int i = it.lo; i < it.hi; ++i, ++G) {
+                    const int s = G % C::NV;
+                    if (!warp_wait_all(bar(C::B_VFULL + s), (G / C::NV) & 1, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    if (i >= from) {
+                        const int rows = min(kStep, it.n_k - i * kStep);  // rows of the block that are the sequence's
+                        uint8_t *v = smem + C::V_OFF + s * C::kKVBytes;
+                        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                        uint32_t big = 0u;  // largest magnitude of either half
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            uint4 *slab = reinterpret_cast<uint4 *>(v + c * C::kSlab);
+                            for (int k = lane; k < rows * 8; k += 32) {
+                                const uint4 w = slab[k];
+                                big = __vmaxu2(big, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                                             __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+                            }
+                            for (int k = rows * 8 + lane; k < kStep * 8; k += 32) slab[k] = zero;
+                        }
+                        const bool bad = (big & 0xFFFFu) >= 0x7F80u || (big >> 16) >= 0x7F80u;
+                        if (__any_sync(0xFFFFFFFFu, bad)) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 64; ++c) {
+                                uint16_t *slab = reinterpret_cast<uint16_t *>(v + c * C::kSlab);
+                                for (int k = lane; k < rows * 64; k += 32)
+                                    if ((slab[k] & 0x7F80u) == 0x7F80u) slab[k] = 0;
+                            }
+                            if (lane == 0) {
+                                vflags[(count - 1) & 1] = 1u;
+                                __threadfence_block();
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_VFIXED + s));
+                }
+                done_with<C>(sbase, lane, count);
+            }
+        } else {
+            // ------------------------------------------------------------ products of one tile
+            const int x = warp - kIssueWarp;
+            const uint32_t tS = tmem + C::T_S + x * kStep, tO = tmem + C::T_O + x * D;
+            const uint64_t qdesc = sdesc_sw128(sbase + C::Q_OFF + x * C::kQBytes, 16, 1024);
+            const uint64_t kdesc0 = sdesc_sw128(sbase + C::K_OFF, 16, 1024);
+            const uint64_t vdesc0 = sdesc_sw128(sbase + C::V_OFF, C::kSlab, 1024);
+            int count = 0, G = 0, P = 0, e = 0;  // steps of the ring, steps and items of this tile
+            bool ok = true;
+            Item it;
+            auto issue_qk = [&](int g, bool last) -> bool {
+                const int s = g % C::NK;
+                if (!warp_wait_all(bar(C::B_KFULL + s), (g / C::NK) & 1, ctl)) return false;
+                tc_fence_after();
+                const uint64_t kd = kdesc0 + static_cast<uint64_t>(s * (C::kKVBytes >> 4));
+                __syncwarp();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kSlab + (kk & 3) * 32) >> 4);
+                        mma_ss(tS, qdesc + off, kd + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(bar(C::B_SFULL + x));
+                    tc_commit(bar(C::B_KEMPTY + s));
+                    if (last) tc_commit(bar(C::B_QEMPTY + x));
+                }
+                __syncwarp();
+                return true;
+            };
+            while (ok && !p.stall && fetch<C>(sbase, items, ctl, lane, count, it)) {
+                const int n = tile_steps(p, it, x), all = it.hi - it.lo;
+                done_with<C>(sbase, lane, count);
+                if (n > 0) {
+                    ok = warp_wait_all(bar(C::B_QFULL + x), e & 1, ctl) && issue_qk(G, n == 1);
+                    for (int i = 0; ok && i < n; ++i, ++P) {
+                        const int g = G + i, s = g % C::NV;
+                        if (!warp_wait_all(bar(C::B_VFIXED + s), (g / C::NV) & 1, ctl) ||
+                            !warp_wait_all(bar(C::B_PFULL + x), P & 1, ctl) ||
+                            (i == 0 && e >= 1 && !warp_wait_all(bar(C::B_OEMPTY + x), (e - 1) & 1, ctl))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t vd = vdesc0 + static_cast<uint64_t>(s * (C::kKVBytes >> 4));
+                        __syncwarp();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < kStep / 16; ++kk)
+                                mma_ts(tO, tS + kk * 8, vd + static_cast<uint64_t>(kk * (16 * 128 >> 4)), C::IDESC_PV,
+                                       i == 0 && kk == 0 ? 0u : 1u);
+                            tc_commit(bar(C::B_VEMPTY + s));
+                            if (i == n - 1) tc_commit(bar(C::B_OFULL + x));
+                        }
+                        __syncwarp();
+                        if (i + 1 < n) ok = issue_qk(g + 1, i + 2 == n);
+                    }
+                    ++e;
+                }
+                for (int i = n; ok && i < all; ++i) {  // the other tile's steps: this one is done with their blocks at once
+                    const int g = G + i;
+                    if (!warp_wait_all(bar(C::B_KFULL + g % C::NK), (g / C::NK) & 1, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive(bar(C::B_KEMPTY + g % C::NK));
+                    if (!warp_wait_all(bar(C::B_VFIXED + g % C::NV), (g / C::NV) & 1, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive(bar(C::B_VEMPTY + g % C::NV));
+                    __syncwarp();
+                }
+                G += all;
+            }
+            // all products of the elected lane have completed before TMEM is freed
+            __syncwarp();
+            if (elect_one()) {
+                tc_commit(bar(C::B_DRAIN + x));
+                wait_bar_drain(bar(C::B_DRAIN + x), 0);
+            }
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kIssueWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- joining the parts
+
+struct JoinArgs {
+    Seqs s;
+    PackedView o;
+    float *lse;
+    const PlanHeader *hdr;
+    const Split *splits;
+    const float *part_o;
+    const float4 *part_stats;
+    uint32_t *err;
+};
+
+// A warp per row: O = sum w_k O_k / sum w_k lp_k, LSE = ln2 (M + log2 sum w_k l_k), w_k = 2^(m_k - M)
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const JoinArgs a)
+{
+    constexpr int V = D / 32;  // channels of a lane
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const long long rows = static_cast<long long>(a.hdr->n_splits) * a.s.Hk * 2 * kTileM;
+    const long long step = static_cast<long long>(gridDim.x) * 8;
+    for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows; i += step) {
+        const int row = static_cast<int>(i % (2 * kTileM));
+        const long long rest = i / (2 * kTileM);
+        const int kh = static_cast<int>(rest % a.s.Hk);
+        const Split sp = a.splits[rest / a.s.Hk];
+        const int trow = row % kTileM, rt = trow / a.s.g, rh = trow % a.s.g;
+        const Seq q = seq_of(a.s, sp.b, a.err);
+        const int tok = sp.t0 + (row / kTileM) * a.s.tpt + rt;
+        if (rt >= a.s.tpt || tok >= q.n_q) continue;
+        const size_t first = (static_cast<size_t>(sp.slot + kh) * 2) * kTileM + row, stride = static_cast<size_t>(a.s.Hk) * 2 * kTileM;
+        float4 st = make_float4(-CUDART_INF_F, 0.0f, 0.0f, 0.0f);  // of part `lane`
+        if (lane < sp.chunks) st = __ldcg(a.part_stats + first + lane * stride);
+        float M = st.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+        const float w = st.x == -CUDART_INF_F ? 0.0f : ex2_approx(st.x - M);
+        float L = st.x == -CUDART_INF_F ? 0.0f : w * st.y, LP = st.x == -CUDART_INF_F ? 0.0f : w * st.z;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+            LP += __shfl_xor_sync(0xFFFFFFFFu, LP, o);
+        }
+        float out[V];
+#pragma unroll
+        for (int c = 0; c < V; ++c) out[c] = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < sp.chunks; ++k) {
+            const float wk = __shfl_sync(0xFFFFFFFFu, w, k), mk = __shfl_sync(0xFFFFFFFFu, st.x, k);
+            if (mk == -CUDART_INF_F) continue;
+            const float *src = a.part_o + (first + k * stride) * D + lane * V;
+            if constexpr (V == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                out[0] += wk * v.x, out[1] += wk * v.y, out[2] += wk * v.z, out[3] += wk * v.w;
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                out[0] += wk * v.x, out[1] += wk * v.y;
+            }
+        }
+        const float inv = LP != 0.0f ? 1.0f / LP : 0.0f;
+        const int head = kh * a.s.g + rh;
+        char *dst = a.o.p + static_cast<int64_t>(q.q0 + tok) * a.o.token + head * a.o.head + lane * V * 2;
+        if constexpr (V == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(out[0] * inv, out[1] * inv), pack_bf16x2(out[2] * inv, out[3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(out[0] * inv, out[1] * inv);
+        if (lane == 0 && a.lse)
+            a.lse[static_cast<int64_t>(head) * a.s.Tq + q.q0 + tok] = (M + log2f(L)) * 0.69314718055994530942f;
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+struct Layout {
+    size_t hdr, entries, splits, rank, at, stats, part, total;
+    int max_slots;
+    int64_t max_entries;
+};
+
+int tokens_per_tile(int H, int Hk) { return kTileM / (H / Hk); }
+
+Layout layout_of(int T, int B, int H, int Hk, int d)
+{
+    const int tpt = tokens_per_tile(H, Hk);
+    const int64_t items = T / (2 * tpt) + static_cast<int64_t>(B);
+    Layout l;
+    l.max_slots = static_cast<int>(items * Hk * kMaxChunks < kMaxSlots ? items * Hk * kMaxChunks : kMaxSlots);
+    size_t at = kCacheScratch;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at = align_up(at + bytes, 256);
+        return here;
+    };
+    l.hdr = take(sizeof(PlanHeader));
+    l.max_entries = items + kMaxParts;
+    l.entries = take(sizeof(Entry) * static_cast<size_t>(l.max_entries));
+    l.splits = take(sizeof(Split) * (kMaxSlots / 2 + 1));
+    l.rank = take(sizeof(int32_t) * static_cast<size_t>(B));
+    l.at = take(sizeof(int32_t) * static_cast<size_t>(B));
+    l.stats = take(sizeof(float4) * 2 * kTileM * static_cast<size_t>(l.max_slots));
+    l.part = take(sizeof(float) * 2 * kTileM * static_cast<size_t>(d) * l.max_slots);
+    l.total = at - kCacheScratch;
+    return l;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled find_encode_tiled()
+{
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    return reinterpret_cast<EncodeTiled>(fn);
+}
+
+// {channel, head, token} of Q, or {channel, token, head} of K and V: 64 channels x n1 x n2 boxes, 128-byte swizzle
+bool make_map(CUtensorMap *m, const PackedView &t, int d, uint64_t n1, int64_t s1, uint64_t n2, int64_t s2, uint32_t box1, uint32_t box2)
+{
+    static const EncodeTiled fn = find_encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), n1, n2};
+    const cuuint64_t strides[2] = {n1 > 1 ? static_cast<cuuint64_t>(s1) : static_cast<cuuint64_t>(d) * 2,
+                                   n2 > 1 ? static_cast<cuuint64_t>(s2) : static_cast<cuuint64_t>(d) * 2};
+    const cuuint32_t box[3] = {64u, box1, box2}, es[3] = {1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+bsa_status launch(const PromptArgs &a, cudaStream_t st)
+{
+    using C = Cfg<D>;
+    static_assert(C::SMEM_ALLOC <= 227 * 1024, "shared memory");
+    static_assert(2 * (kStep + D) <= 512, "TMEM columns");
+    int sms = 0;
+    const bsa_status s = current_sm_count(&sms);
+    if (s != BSA_OK) return s;
+    auto kern = prompt_kernel<D>;
+    static std::atomic<uint64_t> ready{0};
+    if (!allow_shared_memory(kern, C::SMEM_ALLOC, ready)) return BSA_ERR_CUDA;
+    // setmaxnreg hands out what the block was launched with: with fewer registers the split would wait for ever
+    static const bool split_fits = [&] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kern) == cudaSuccess &&
+               f.numRegs * kThreads >= kSoftmaxWarps * 32 * kSoftmaxRegs + (kThreads - kSoftmaxWarps * 32) * kOtherRegs;
+    }();
+    if (!split_fits) return BSA_ERR_UNSUPPORTED;
+    const Layout l = layout_of(a.Tq, a.B, a.H, a.Hk, a.d);
+    const int g = a.H / a.Hk, tpt = tokens_per_tile(a.H, a.Hk);
+    CUtensorMap mq, mk, mv;
+    // without keys no step is loaded: any tensor does in their place
+    const bool keys = a.Tk > 0;
+    if (!make_map(&mq, a.q, D, a.H, a.q.head, a.Tq, a.q.token, g, tpt) ||
+        !make_map(&mk, keys ? a.k : a.q, D, keys ? a.Tk : 1, a.k.token, keys ? a.Hk : 1, a.k.head, kStep, 1) ||
+        !make_map(&mv, keys ? a.v : a.q, D, keys ? a.Tk : 1, a.v.token, keys ? a.Hk : 1, a.v.head, kStep, 1))
+        return BSA_ERR_CUDA;
+    const Seqs seqs{a.cu_q, a.cu_k, a.Tq, a.Tk, a.B, a.Hk, g, tpt, a.causal != 0};
+    uint32_t *err = reinterpret_cast<uint32_t *>(a.ws);
+    PlanHeader *hdr = reinterpret_cast<PlanHeader *>(a.ws + l.hdr);
+    const PlanArgs pa{seqs, sms, l.max_slots, l.max_entries, hdr, reinterpret_cast<Entry *>(a.ws + l.entries),
+                      reinterpret_cast<Split *>(a.ws + l.splits), reinterpret_cast<int32_t *>(a.ws + l.rank),
+                      reinterpret_cast<int32_t *>(a.ws + l.at), err};
+    plan_kernel<<<1, kPlanThreads, 0, st>>>(pa);
+    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+    Params p;
+    p.s = seqs;
+    p.scale_log2 = a.scale * 1.44269504088896340736f;
+    p.o = a.o;
+    p.v = a.v;
+    p.lse = a.lse;
+    p.hdr = hdr;
+    p.entries = pa.entries;
+    p.part_o = reinterpret_cast<float *>(a.ws + l.part);
+    p.part_stats = reinterpret_cast<float4 *>(a.ws + l.stats);
+    p.err = err;
+    p.wait_limit_ns = a.wait_limit_ns;
+    p.stall = (a.dbg_flags & kDbgStall) != 0u;
+    if (!pdl_launch(kern, dim3(static_cast<unsigned>(sms)), kThreads, C::SMEM_ALLOC, st, mq, mk, mv, p)) return BSA_ERR_CUDA;
+    const JoinArgs ja{seqs, a.o, a.lse, hdr, pa.splits, p.part_o, p.part_stats, err};
+    if (!pdl_launch(join_kernel<D>, dim3(static_cast<unsigned>(2 * sms)), 256, 0, st, ja)) return BSA_ERR_CUDA;
+    return BSA_OK;
+}
+
+}  // namespace
+
+size_t prompt_workspace(int T, int B, int H, int Hk, int d) { return layout_of(T, B, H, Hk, d).total; }
+
+bsa_status launch_prompt_attention(const PromptArgs &a, cudaStream_t st)
+{
+    return a.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
+}
+
+}  // namespace bsa

@@ -1,0 +1,350 @@
+"""The cache's rows and attention over it (bsa_cache_write, bsa_cache_read, bsa_cache_attention) against their 64-bit forms."""
+import pytest
+import torch
+
+import block_sparse_attention_mean_gb300 as pkg
+from block_sparse_attention_mean_gb300 import binding as bb
+from block_sparse_attention_mean_gb300 import build as bbuild
+from block_sparse_attention_mean_gb300 import cache_binding as cb
+from tests import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    bbuild.build()
+    cb.load()
+
+
+def gen(seed):
+    return torch.Generator(DEV).manual_seed(seed)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def starts(lens):
+    at = [0]
+    for n in lens:
+        at.append(at[-1] + n)
+    return ints(at)
+
+
+def paged(g, held, page, spare=3, width=None):
+    """(table, pages in all): the sequences' pages in random order; entries behind a sequence's last page are not pages"""
+    counts = [-(-n // page) for n in held]
+    order = torch.randperm(sum(counts) + spare, generator=g, device=DEV).to(torch.int32)
+    table = torch.full((len(held), width or max(1, max(counts))), -7, dtype=torch.int32, device=DEV)
+    at = 0
+    for b, n in enumerate(counts):
+        table[b, :n] = order[at:at + n]
+        at += n
+    return table, sum(counts) + spare
+
+
+def draw(g, *shape):
+    return torch.randn(*shape, generator=g, device=DEV)
+
+
+def rows(g, T, H, d):
+    """keys and values [T, H, d] whose rows differ in size"""
+    return tuple((draw(g, T, H, d) * torch.exp(draw(g, T, H, 1))).to(BF16) for _ in range(2))
+
+
+def filled(g, n_pages, page, Hk, d, kind):
+    """a cache of random contents, and its values [pages, Hk, page, d] in 64 bits"""
+    k, v = rows(g, n_pages * Hk * page, 1, d)
+    cache = pkg.kv_cache(n_pages, page, Hk, d, kind, DEV)
+    values = []
+    for x, data, exps in ((k, cache.k, cache.k_exp), (v, cache.v, cache.v_exp)):
+        x = x.view(n_pages, Hk, page, d)
+        if kind == "bf16":
+            data.copy_(x)
+            values.append(x.double())
+        else:
+            held, e = ref.e4m3_rows(x)
+            unit = ((e.long() - 127 + 1023) << 52).view(torch.float64)[..., None]
+            data.copy_((held / unit).float())
+            exps.copy_(e)
+            values.append(held)
+    return cache, values
+
+
+def sequence(values, table, b, n, page):
+    """the first n tokens of sequence b: [n, Hk, d]"""
+    ids = table[b, : -(-n // page)].long()
+    return values[ids].transpose(1, 2).flatten(0, 1)[:n]
+
+
+# ------------------------------------------------------------------ rows
+
+
+ROWS = [
+    # kind, page, Hk, d, tokens held before, new tokens
+    ("bf16", 16, 1, 64, [0], [1]),
+    ("e4m3", 16, 1, 128, [15], [1]),
+    ("bf16", 64, 8, 128, [0, 63, 64, 130], [65, 1, 64, 3]),
+    ("e4m3", 32, 5, 64, [0, 31, 7, 100], [33, 2, 0, 200]),
+    ("e4m3", 128, 24, 128, [0, 500], [300, 129]),
+    ("bf16", 256, 3, 64, [255, 0, 1], [2, 0, 511]),
+    ("e4m3", 64, 2, 128, [10] * 70, [i % 4 for i in range(70)]),
+]
+
+
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("kind,page,Hk,d,past,new", ROWS)
+def test_write_then_read(kind, page, Hk, d, past, new, fused):
+    g = gen(1)
+    held = [a + b for a, b in zip(past, new)]
+    table, n_pages = paged(g, held, page)
+    cache, values = filled(g, n_pages, page, Hk, d, kind)
+    T = sum(new)
+    k, v = rows(g, T, Hk, d)
+    k[T // 2, 0] = 0
+    if fused:
+        k, v = torch.cat((draw(g, T, 2, d).to(BF16), k, v), dim=1).split([2, Hk, Hk], dim=1)[1:]
+    before = [None if x is None else x.clone() for x in cache]
+    pkg.cache_write(cache, k, v, table, ints(held), starts(new))
+    got_k, got_v = pkg.cache_read(cache, table, starts(held), sum(held))
+    at_new = at = 0
+    touched = torch.zeros(n_pages, page, dtype=torch.bool, device=DEV)
+    for b, (p, n) in enumerate(zip(past, new)):
+        for x, old, got in ((k, values[0], got_k), (v, values[1], got_v)):
+            fresh = x[at_new:at_new + n]
+            fresh = fresh.double() if kind == "bf16" else ref.e4m3_rows(fresh)[0]
+            want = torch.cat((sequence(old, table, b, p, page), fresh))
+            assert torch.equal(got[at:at + p + n].double(), want)
+        for t in range(p, p + n):
+            touched[table[b, t // page].long(), t % page] = True
+        at_new, at = at_new + n, at + p + n
+    # the other rows are as they were, exponents too
+    for x, old in zip(cache, before):
+        if x is not None:
+            x, old = x.view(torch.uint8 if x.element_size() == 1 else torch.int16), old.view(torch.uint8 if x.element_size() == 1 else torch.int16)
+            keep = ~touched[:, None, :].expand(n_pages, Hk, page)
+            assert torch.equal(x[keep], old[keep])
+
+
+def test_write_one_token_a_sequence_and_heads_first():
+    g = gen(2)
+    held = [1, 16, 17, 100]
+    table, n_pages = paged(g, held, 16)
+    cache, _ = filled(g, n_pages, 16, 3, 64, "bf16")
+    k, v = (draw(g, 3, 4, 64).to(BF16).transpose(0, 1) for _ in range(2))  # [T, Hk, d] of [Hk, T, d]
+    pkg.cache_write(cache, k, v, table, ints(held))
+    for b, n in enumerate(held):
+        for x, pool in ((k, cache.k), (v, cache.v)):
+            assert torch.equal(pool[table[b, (n - 1) // 16].long(), :, (n - 1) % 16], x[b])
+    out = tuple(torch.empty(3, 118 + 16, 64, dtype=BF16, device=DEV).transpose(0, 1) for _ in range(2))
+    a = pkg.cache_read(cache, table, starts(held), out=out)
+    b = pkg.cache_read(cache, table, starts(held), sum(held))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_quantised_rows_at_their_edges():
+    g = gen(3)
+    d, inf, nan = 64, float("inf"), float("nan")
+    x = draw(g, 16, 1, d)
+    x[0] = 0.0
+    x[1] = 3.3e38
+    x[2] = 0.0
+    x[2, 0, 3] = 448.0
+    x[3] = 0.0
+    x[3, 0, 3] = 450.0          # one step of bf16 above 448
+    x[4] *= 2.0 ** -120         # below the least exponent
+    x[5, 0, 7] = inf
+    x[6, 0, 9] = nan
+    x[7] = -inf
+    x[8, 0, 0], x[8, 0, 1] = 1.0e30, 1.0e-30
+    x[9] = torch.arange(d, device=DEV) * 4.0 + 200.0   # ties between steps
+    x[10] = 1.0e-38
+    x = x.to(BF16)
+    held, e = ref.e4m3_rows(x)
+    cache = pkg.kv_cache(1, 16, 1, d, "e4m3", DEV)
+    table = ints([[0]])
+    pkg.cache_write(cache, x, x, table, ints([16]), ints([0, 16]))
+    k, v = pkg.cache_read(cache, table, ints([0, 16]), 16)
+    assert torch.equal(cache.k_exp[0, 0], e[:, 0]) and torch.equal(cache.v_exp[0, 0], e[:, 0])
+    for got in (k, v):
+        assert torch.equal(got.isnan(), held.isnan())
+        assert torch.equal(torch.nan_to_num(got.double()), torch.nan_to_num(held))
+
+
+def test_rows_of_no_sequence_stay():
+    g = gen(4)
+    cache, values = filled(g, 4, 16, 2, 128, "e4m3")
+    table = ints([[2, 0], [1, 3]])
+    out = tuple(torch.full((40, 2, 128), 7.0, dtype=BF16, device=DEV) for _ in range(2))
+    pkg.cache_read(cache, table, ints([3, 20, 30]), out=out)
+    for o, x in zip(out, values):
+        assert torch.equal(o[3:20].double(), sequence(x, table, 0, 17, 16))
+        assert torch.equal(o[20:30].double(), sequence(x, table, 1, 10, 16))
+        assert (o[:3] == 7).all() and (o[30:] == 7).all()
+    before = [x.clone() for x in cache]
+    k, v = rows(g, 9, 2, 128)
+    pkg.cache_write(cache, k, v, table, ints([5, 8]), ints([2, 3, 6]))  # tokens 0, 1 and 6 .. 8 belong to nobody
+    same = [(x.view(torch.uint8) == y.view(torch.uint8)) for x, y in zip(cache, before)]
+    assert same[2].sum() >= same[2].numel() - 4 * 2
+    assert same[0][2, :, :4].all() and same[0][2, :, 5:].all() and same[0][1, :, 8:].all() and same[0][3].all()
+
+
+def test_no_tokens():
+    cache = pkg.kv_cache(2, 16, 1, 64, "bf16", DEV)
+    empty = torch.empty(0, 1, 64, dtype=BF16, device=DEV)
+    pkg.cache_write(cache, empty, empty, ints([[0]]), ints([0]), ints([0, 0]))
+    k, v = pkg.cache_read(cache, ints([[0]]), ints([0, 0]), 0)
+    assert k.shape == (0, 1, 64)
+
+
+# ------------------------------------------------------------------ attention of one token
+
+
+def check_decode(q, cache, values, table, held, page, kind, scale=None, out=None, lse=None):
+    B, H, d = q.shape
+    Hk = cache.k.shape[1]
+    scale = d ** -0.5 if scale is None else scale
+    o = torch.empty_like(out, dtype=torch.float64) if out is not None else None
+    bound, want, lbound = torch.zeros_like(o), torch.zeros_like(lse, dtype=torch.float64), torch.zeros_like(lse, dtype=torch.float64)
+    for b, n in enumerate(held):
+        k, v = (sequence(x, table, b, n, page) for x in values)
+        for h in range(H):
+            kh = h // (H // Hk)
+            see = torch.ones(1, n, dtype=torch.bool, device=DEV)
+            oo, bo, ll, bl = ref.attention(q[b, h][None], k[:, kh], v[:, kh], see, scale, half_weights=kind == "e4m3")
+            o[b, h], bound[b, h], want[b, h], lbound[b, h] = oo[0], bo[0], ll[0], bl[0]
+    ref.within(out, o, bound, "O")
+    ref.within(lse, want, lbound, "LSE")
+
+
+DECODE = [
+    # kind, page, H, Hk, d, lengths
+    ("bf16", 16, 1, 1, 64, [1]),
+    ("e4m3", 16, 1, 1, 128, [1]),
+    ("bf16", 64, 8, 8, 128, [63, 64, 65, 0, 1]),
+    ("e4m3", 64, 8, 8, 64, [0, 15, 16, 17, 128, 129]),
+    ("bf16", 32, 24, 8, 128, [1000, 33, 2]),
+    ("e4m3", 32, 24, 8, 128, [1000, 33, 2]),
+    ("bf16", 16, 16, 1, 64, [777]),          # 16 heads share a key head
+    ("e4m3", 256, 16, 1, 128, [5000, 1]),
+    ("bf16", 128, 21, 1, 128, [300, 40]),    # 21 of them: two chunks of heads, the second in part
+    ("e4m3", 64, 40, 1, 64, [511]),
+    ("bf16", 64, 7, 7, 64, [9, 0, 0, 200]),
+    ("e4m3", 16, 14, 2, 128, [4097, 31, 16]),
+    ("bf16", 64, 4, 2, 128, [30011]),        # cut over many CTAs, joined in two steps
+    ("e4m3", 64, 2, 1, 64, [60001, 3]),
+    ("bf16", 16, 2, 1, 64, [i * 13 % 90 for i in range(300)]),
+]
+
+
+@pytest.mark.parametrize("kind,page,H,Hk,d,held", DECODE)
+def test_cache_attention(kind, page, H, Hk, d, held):
+    g = gen(5)
+    table, n_pages = paged(g, held, page)
+    cache, values = filled(g, n_pages, page, Hk, d, kind)
+    q = draw(g, len(held), H, d).to(BF16)
+    out, lse = pkg.cache_attention(q, cache, table, ints(held))
+    check_decode(q, cache, values, table, held, page, kind, out=out, lse=lse)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_cache_attention_views_scale_and_spread_scores(kind):
+    g = gen(6)
+    held, page, H, Hk, d = [200, 77, 500], 16, 12, 4, 128
+    table, n_pages = paged(g, held, page, width=64)
+    cache, values = filled(g, n_pages, page, Hk, d, kind)
+    q = (draw(g, 3, H + 8, d) * 4).to(BF16)[:, 3:3 + H]     # scores of some tens: the maximum is raised often
+    out = torch.empty(3, 2, H, d, dtype=BF16, device=DEV)[:, 1]
+    out, lse = pkg.cache_attention(q, cache, table, ints(held), 0.2, out=out)
+    check_decode(q, cache, values, table, held, page, kind, scale=0.2, out=out, lse=lse)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_cache_attention_is_blind_behind_the_end(kind):
+    """NaN in the rows behind a sequence's last token, and in pages that are not its own, does not reach it"""
+    g = gen(7)
+    held, page, H, Hk, d = [70, 1, 16, 0], 64, 8, 2, 128
+    table, n_pages = paged(g, held, page)
+    cache, values = filled(g, n_pages, page, Hk, d, kind)
+    q = draw(g, 4, H, d).to(BF16)
+    a, la = pkg.cache_attention(q, cache, table, ints(held))
+    own = torch.zeros(n_pages, page, dtype=torch.bool, device=DEV)
+    for b, n in enumerate(held):
+        for t in range(n):
+            own[table[b, t // page].long(), t % page] = True
+    other = ~own[:, None, :].expand(n_pages, Hk, page)
+    for x in cache[:2]:
+        x.view(torch.int16 if kind == "bf16" else torch.uint8)[other] = 0x7FC0 if kind == "bf16" else 0x7F
+    for x in cache[2:]:
+        if x is not None:
+            x[other] = 255
+    b, lb = pkg.cache_attention(q, cache, table, ints(held))
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    assert (a[3] == 0).all() and (la[3] == float("-inf")).all()
+
+
+def test_cache_attention_values_of_very_different_size():
+    """8-bit rows whose exponents differ by 40: weights are rounded relative to the largest product"""
+    g = gen(8)
+    held, page, H, Hk, d = [300], 16, 4, 1, 64
+    table, n_pages = paged(g, held, page)
+    cache, values = filled(g, n_pages, page, Hk, d, "e4m3")
+    shift = torch.randint(-20, 21, cache.v_exp.shape, generator=g, device=DEV)
+    cache.v_exp.copy_((cache.v_exp.long() + shift).to(torch.uint8))
+    values[1] *= torch.pow(2.0, shift.double())[..., None]
+    q = draw(g, 1, H, d).to(BF16)
+    out, lse = pkg.cache_attention(q, cache, table, ints(held))
+    check_decode(q, cache, values, table, held, page, "e4m3", out=out, lse=lse)
+
+
+def test_a_result_does_not_depend_on_the_other_sequences_order():
+    """the same call twice, bit for bit, and with the workspace of other calls before it"""
+    g = gen(9)
+    held, page = [4000, 1, 999, 2500], 64
+    table, n_pages = paged(g, held, page)
+    cache, _ = filled(g, n_pages, page, 4, 128, "e4m3")
+    q = draw(g, 4, 8, 128).to(BF16)
+    ws = pkg.cache_workspace(4, 4, 8, 4, 128, DEV)
+    a = pkg.cache_attention(q, cache, table, ints(held), ws=ws)
+    for _ in range(3):
+        b = pkg.cache_attention(q, cache, table, ints(held), ws=ws)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        pkg.cache_attention(q[:1], cache, table[:1], ints(held[:1]), ws=ws)
+
+
+# ------------------------------------------------------------------ what only the device sees
+
+
+def test_bad_pages_and_lengths_are_reported():
+    g = gen(10)
+    cache, _ = filled(g, 4, 16, 2, 64, "bf16")
+    q = draw(g, 2, 2, 64).to(BF16)
+    k, v = rows(g, 2, 2, 64)
+    for table, held in (([[0, 4], [1, 1]], [17, 5]), ([[0, 1], [-1, 2]], [17, 5]), ([[0, 1], [2, 3]], [33, 5]),
+                        ([[0, 1], [2, 3]], [17, -1])):
+        ws = pkg.cache_workspace(2, 2, 2, 2, 64, DEV)
+        for call in (lambda: pkg.cache_attention(q, cache, ints(table), ints(held), ws=ws),
+                     lambda: pkg.cache_write(cache, k, v, ints(table), ints(held), ws=ws)):
+            with pytest.raises(bb.BsaError) as e:
+                call()
+            assert e.value.code == bb.ERR_INVALID_ARG
+            pkg.cache_check(ws)  # cleared
+    with pytest.raises(bb.BsaError):
+        pkg.cache_read(cache, ints([[0, 9]]), ints([0, 20]), 20)
+    with pytest.raises(bb.BsaError):
+        pkg.cache_read(cache, ints([[0, 1]]), ints([0, 40]), 40)     # longer than its table
+    with pytest.raises(bb.BsaError):
+        pkg.cache_read(cache, ints([[0, 1]]), ints([0, 40]), 20)     # leaves its tensor
+    # a sequence that is well formed beside one that is not gets its result
+    table, held = ints([[0, 1], [2, 3]]), [20, -3]
+    ws = pkg.cache_workspace(2, 2, 2, 2, 64, DEV)
+    out, lse = pkg.cache_attention(q, cache, table, ints(held), ws=ws, check=False)
+    check_decode(q[:1], cache, [x.double() for x in cache[:2]], table, [20], 16, "bf16", out=out[:1], lse=lse[:1])
+    assert (out[1] == 0).all() and (lse[1] == float("-inf")).all()
+    with pytest.raises(bb.BsaError):
+        pkg.cache_check(ws)
