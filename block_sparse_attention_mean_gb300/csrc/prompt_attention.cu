@@ -4,16 +4,17 @@
 // 128 x 128 block of one head takes 2 x 512 cycles of an SM (d = 128) and its 16384 exponentials about 550.
 //
 //   * A tile is 128 rows of S = Q K^T: floor(128 / g) tokens of a sequence with the g query heads of one key head, loaded
-//     by one TMA box, so that grouped heads share each K and V block that is fetched. A CTA holds two tiles of
-//     consecutive tokens (one CTA per SM) and both use each block: half the shared-memory fills per product.
-//   * 8 softmax warps, 4 per tile, a thread per row; a warp that issues each tile's products, a warp that loads, and one
-//     that looks after V where a mask ends in a block. The two tiles take turns on the tensor cores: while one's
-//     softmax runs, the other's P V and next Q K^T do. P (bf16) overwrites S in TMEM: 2 x (128 + d) columns.
-//   * The order of one tile's products is PV(i), QK(i + 1), from one thread: they execute in that order, so a
-//     QK(i + 1) may overwrite the P that PV(i) reads, and a full S(i + 1) says that O holds PV(i).
-//   * Online softmax in log2: the running maximum is raised only when a row's step sum passes 2^8 (then the step is
-//     done again and O rescaled). fp32 sums; O is divided by the sum of the weights as rounded to bf16.
-//   * A plan in one CTA cuts the work: items are (sequence, key head, two tiles), a sequence's heads one after another
+//     by one TMA box, so that grouped heads share each K and V block that is fetched. One persistent CTA per SM.
+//   * Two groups of four softmax warps, a thread per row, take a tile's steps in turn: a step's chain (load S, 128
+//     exponentials and sums, store P) is twice as long as its products take on the tensor cores. One warp issues the
+//     Q K^T, up to three steps ahead (three S / P buffers in TMEM), one the P V; one loads, and one looks after V
+//     where a mask ends in a block.
+//   * Online softmax in log2, P in bf16 over S in TMEM: the running maximum of a row is raised only when a step's sum
+//     passes 2^8 (the step is then done again and O rescaled). The groups share it: a step is computed with the
+//     maximum as last seen; before its P is stored, the warp waits for the decision of the step before (the other group's
+//     warp of the same rows) and does the step again if that raised it. Each group sums its own steps; the one of the
+//     last step adds them up. fp32 sums; O is divided by the sum of the weights as rounded to bf16.
+//   * A plan in one CTA cuts the work: items are (sequence, key head, tile), a sequence's heads one after another
 //     so that its K and V stay in L2, longest sequences and longest ranges first; an item well above the average of a
 //     CTA is split by key range, and a second launch joins the parts in order.
 //   * 0 * NaN: a masked weight of zero still multiplies V. In blocks where a mask ends, rows of V behind the sequence
@@ -34,7 +35,7 @@ namespace {
 constexpr int kTileM = 128;
 constexpr int kStep = 128;  // keys of a step
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarp = 8, kIssueWarp = 9, kFixWarp = 11;  // issuers: one per tile
+constexpr int kLoadWarp = 8, kQkWarp = 9, kPvWarp = 10, kFixWarp = 11;
 constexpr int kThreads = 12 * 32;
 // registers a thread after the split: 256 * 216 + 128 * 72 = 384 * 168, what the block is launched with
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
@@ -44,14 +45,14 @@ constexpr unsigned long long kDrainNs = 1000000000ull;  // copies and products i
 
 // Parts: an item of more than 1.5 shares (a CTA's average of steps, rounded up) becomes ceil(steps / share) parts, so
 // all split items together at most 1.67 per CTA.
-constexpr int kMaxSlots = 320;   // partial results (two tiles each): 1.67 * 152 and some
+constexpr int kMaxSlots = 320;   // partial results (a tile each): 1.67 * 152 and some
 constexpr int kMaxParts = 1088;  // entries that parts add: 1.67 * 640
 constexpr int kMaxChunks = 32;   // parts of one item
 constexpr int kPlanThreads = 1024;
 
 // Work of one CTA at a time; expanded by the key heads
 struct __align__(16) Entry {
-    int b, t0;       // sequence, first token of the first tile
+    int b, t0;       // sequence, first token
     int lo, hi;      // steps of 128 keys
     int slot, seq0;  // first partial slot (of key head 0) or -1; first entry of the sequence
     int seq_n, pad;  // entries of the sequence
@@ -102,7 +103,7 @@ __device__ __forceinline__ int steps_of(int causal, int n_q, int n_k, int t0, in
 }
 __device__ __forceinline__ int item_steps(const Seqs &s, const Seq &q, int t0)
 {
-    return max(steps_of(s.causal, q.n_q, q.n_k, t0, s.tpt), steps_of(s.causal, q.n_q, q.n_k, t0 + s.tpt, s.tpt));
+    return steps_of(s.causal, q.n_q, q.n_k, t0, s.tpt);
 }
 
 // ---------------------------------------------------------------- plan
@@ -184,9 +185,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     int most = 0;
     for (int b = warp; b < s.B; b += 32) {
         const Seq q = seq_of(s, b, a.err);
-        const int items = (q.n_q + 2 * s.tpt - 1) / (2 * s.tpt);
+        const int items = (q.n_q + s.tpt - 1) / s.tpt;
         for (int i = lane; i < items; i += 32) {
-            const int n = item_steps(s, q, i * 2 * s.tpt);
+            const int n = item_steps(s, q, i * s.tpt);
             mine += n;
             most = max(most, n);
         }
@@ -198,11 +199,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     // entries of each sequence, in order of rank, and their places
     for (int r = warp; r < s.B; r += 32) {
         const Seq q = seq_of(s, a.rank[r], a.err);
-        const int items = (q.n_q + 2 * s.tpt - 1) / (2 * s.tpt);
+        const int items = (q.n_q + s.tpt - 1) / s.tpt;
         int n = items;
         if (split) {
             n = 0;
-            for (int i = lane; i < items; i += 32) n += chunks_of(item_steps(s, q, i * 2 * s.tpt), share);
+            for (int i = lane; i < items; i += 32) n += chunks_of(item_steps(s, q, i * s.tpt), share);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
         }
@@ -231,12 +232,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     for (int r = warp; r < s.B; r += 32) {
         const int b = a.rank[r];
         const Seq q = seq_of(s, b, a.err);
-        const int items = (q.n_q + 2 * s.tpt - 1) / (2 * s.tpt);
+        const int items = (q.n_q + s.tpt - 1) / s.tpt;
         const int seq0 = a.at[r], seq_n = (r + 1 < s.B ? a.at[r + 1] : entries) - seq0;
         int base = seq0;
         for (int i0 = 0; i0 < items; i0 += 32) {
             const int i = items - 1 - (i0 + lane);  // longest first
-            const int t0 = i * 2 * s.tpt;
+            const int t0 = i * s.tpt;
             const int steps = i >= 0 ? item_steps(s, q, t0) : 0;
             const int c = i >= 0 ? (split ? chunks_of(steps, share) : 1) : 0;
             int incl = c;
@@ -286,8 +287,8 @@ struct Params {
     float *lse;
     PlanHeader *hdr;
     const Entry *entries;
-    float *part_o;       // [slot][2][128][D]
-    float4 *part_stats;  // [slot][2][128] (max in log2, sum, sum of the rounded weights, 0)
+    float *part_o;       // [slot][128][D]
+    float4 *part_stats;  // [slot][128] (max in log2, sum, sum of the rounded weights, 0)
     uint32_t *err;
     unsigned long long wait_limit_ns;
     int stall;  // load and multiply nothing: the first waits run out
@@ -299,22 +300,24 @@ struct Item {
 
 template <int D>
 struct Cfg {
-    static constexpr int NK = D == 128 ? 2 : 4, NV = D == 128 ? 3 : 4;
+    static constexpr int QS = 2, NK = D == 128 ? 2 : 4, NV = D == 128 ? 2 : 4, NSB = 3;  // Q, K, V slots; S / P buffers
     static constexpr int kQBytes = kTileM * D * 2, kKVBytes = kStep * D * 2;
     static constexpr int kSlab = 128 * 128;  // bytes of 64 columns of 128 rows
-    static constexpr int Q_OFF = 0, K_OFF = 2 * kQBytes, V_OFF = K_OFF + NK * kKVBytes, BAR_OFF = V_OFF + NV * kKVBytes;
-    static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_KFULL = 4, B_KEMPTY = B_KFULL + NK, B_VFULL = B_KEMPTY + NK,
-                         B_VEMPTY = B_VFULL + NV, B_VFIXED = B_VEMPTY + NV, B_SFULL = B_VFIXED + NV, B_PFULL = B_SFULL + 2,
-                         B_OFULL = B_PFULL + 2, B_OEMPTY = B_OFULL + 2, B_TFULL = B_OEMPTY + 2, B_TEMPTY = B_TFULL + 2,
-                         B_DRAIN = B_TEMPTY + 2, NBAR = B_DRAIN + 2;
+    static constexpr int Q_OFF = 0, K_OFF = QS * kQBytes, V_OFF = K_OFF + NK * kKVBytes, BAR_OFF = V_OFF + NV * kKVBytes;
+    static constexpr int B_QFULL = 0, B_QEMPTY = B_QFULL + QS, B_KFULL = B_QEMPTY + QS, B_KEMPTY = B_KFULL + NK,
+                         B_VFULL = B_KEMPTY + NK, B_VEMPTY = B_VFULL + NV, B_VFIXED = B_VEMPTY + NV, B_SFULL = B_VFIXED + NV,
+                         B_PFULL = B_SFULL + NSB, B_PVDONE = B_PFULL + NSB, B_OEMPTY = B_PVDONE + NSB, B_TFULL = B_OEMPTY + 1,
+                         B_TEMPTY = B_TFULL + 2, B_MAX = B_TEMPTY + 2, B_SUMS = B_MAX + 8, B_DRAIN = B_SUMS + 4,
+                         NBAR = B_DRAIN + 2;
     static constexpr int MISC_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;
     static constexpr int kItemWords = 12;
     static constexpr int MISC_WORDS = 4 + 2 * kItemWords;  // TMEM base, abort flag, V flags of the two items, the items
-    static constexpr int SMEM = MISC_OFF + 4 * MISC_WORDS;
+    static constexpr int ROWS_OFF = MISC_OFF + 4 * MISC_WORDS;  // running maxima [128], one group's sums [2][128][2]
+    static constexpr int SMEM = ROWS_OFF + 4 * (128 + 2 * 128 * 2);
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(kTileM, kStep, 0, 0);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(kTileM, D, 0, 1);
-    static constexpr int T_S = 0, T_O = 2 * kStep;  // TMEM columns: S / P of both tiles, then O of both
+    static constexpr int T_O = NSB * kStep;  // TMEM columns: the S / P buffers, then O
 };
 
 // ---- bounded waits, inlined: a kernel that moves registers between its warps calls no functions
@@ -362,13 +365,6 @@ __device__ __forceinline__ void regs_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// steps of tile x among the item's
-__device__ __forceinline__ int tile_steps(const Params &p, const Item &it, int x)
-{
-    const int n = steps_of(p.s.causal, it.n_q, it.n_k, it.t0 + x * p.s.tpt, p.s.tpt);
-    return max(0, min(n, it.hi) - it.lo);
-}
-
 // The next item from the ring of two; false at the end or when a wait gave up
 template <class C>
 __device__ __forceinline__ bool fetch(uint32_t sbase, const volatile int *items, const Ctl &ctl, int lane, int &count, Item &it)
@@ -405,29 +401,39 @@ __device__ __forceinline__ void add_not_finite(const char *v, int64_t stride, in
 }
 
 template <int D, class C>
-__device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, uint32_t tmem, const volatile int *items,
+__device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, uint32_t tmem, volatile float *row_max,
+                                             volatile float *row_sums, const volatile int *items,
                                              const volatile uint32_t *vflags, const Ctl &ctl, int warp, int lane)
 {
     auto bar = [&](int idx) -> uint32_t { return sbase + C::BAR_OFF + 8u * idx; };
     constexpr int NC = kStep / 32;
-    const int x = warp >> 2;  // tile
-    const int trow = (warp & 3) * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + C::T_S + x * kStep;
-    const uint32_t tO = tmem + lanes + C::T_O + x * D;
+    const int group = warp >> 2, w4 = warp & 3;
+    const int trow = w4 * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t tO = tmem + lanes + C::T_O;
     const int rt = trow / p.s.g, rh = trow % p.s.g;  // token and head of the row within the tile
-    int G = 0, e = 0, count = 0;
+    int G = 0, count = 0, pairs = 0;  // steps and items so far, items of two steps and more
     Item it;
     while (fetch<C>(sbase, items, ctl, lane, count, it)) {
-        const int n = tile_steps(p, it, x);
-        const int tok = it.t0 + x * p.s.tpt + rt;
+        const int n = it.hi - it.lo;
+        const int tok = it.t0 + rt;
         const bool real = rt < p.s.tpt && tok < it.n_q;
         const int nvis = real ? visible(p.s.causal, it.n_q, it.n_k, tok) : 0;
         float m_run = -CUDART_INF_F;
         uint64_t acc[2] = {0ull, 0ull};
         float accp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int i = 0; i < n; ++i, ++G) {
-            if (!warp_wait_all(bar(C::B_SFULL + x), G & 1, ctl)) return;
+        float m_other = -CUDART_INF_F;  // the maximum that the other group's sums are relative to
+        auto rescale_sums = [&](float alpha) {
+            const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) acc[k] = f2_fma(acc[k], a2, 0ull);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) accp[k] *= alpha;
+        };
+        for (int i = (G ^ group) & 1; i < n; i += 2) {  // this group's steps: every other one, over all items
+            const int g = G + i, b = g % C::NSB;
+            const uint32_t tS = tmem + lanes + b * kStep;
+            if (!warp_wait_all(bar(C::B_SFULL + b), (g / C::NSB) & 1, ctl)) return;
             tc_fence_after();
             const int nv = nvis - (it.lo + i) * kStep;  // columns that the row sees
             const bool masked = __any_sync(0xFFFFFFFFu, nv < kStep);
@@ -459,7 +465,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
             const uint64_t c2x = f2_pack(p.scale_log2, p.scale_log2);
             uint64_t sacc[2];
             float sap[4];
-            uint32_t pk[NC][16];  // P, stored over S when the step's sum has passed
+            uint32_t pk[NC][16];  // P, stored over S when the step's maximum is settled
             auto exps = [&](float m) {
                 const float base = m == -CUDART_INF_F ? 0.0f : m;  // a row that has seen no key yet: every weight 0
                 const uint64_t nm2 = f2_pack(-base, -base);
@@ -484,48 +490,68 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                     }
                 }
             };
-            if (__any_sync(0xFFFFFFFFu, m_run == -CUDART_INF_F)) {
-                const float m_step = step_max();
-                if (m_run == -CUDART_INF_F) m_run = m_step;
+            // the other group's warp of these rows has settled the maximum of the step before
+            auto wait_settled = [&]() -> bool {
+                return g == 0 || warp_wait_all(bar(C::B_MAX + (1 - group) * 4 + w4), ((g - 1) >> 1) & 1, ctl);
+            };
+            auto settle = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_MAX + group * 4 + w4));
+            };
+            bool settled = false;  // the step before is known
+            if (i == 0) {  // a new tile: its first step's maximum, known before the exponentials are
+                m_run = step_max();
+                if (!wait_settled()) return;
+                row_max[trow] = m_run;
+                settle();
+            } else if (i == 1) {
+                if (!wait_settled()) return;
+                m_run = m_other = row_max[trow];
+                settled = true;
             }
-            // a step sum of at most 2^8 bounds every weight: only a larger one (or NaN) raises the running maximum
-            float alpha = 1.0f;
-            bool again = false;
+            bool raised = false;
             for (;;) {
                 exps(m_run);
-                if (again) break;
-                float s0, s1;
-                f2_unpack(f2_add(sacc[0], sacc[1]), s0, s1);
-                const bool raise = !(s0 + s1 <= kRescaleSum);
-                if (!__any_sync(0xFFFFFFFFu, raise)) break;
-                again = true;  // the whole warp: TMEM accesses are the warp's
-                const float m_step = fmaxf(m_run, step_max());
-                if (raise) {
-                    alpha = ex2_approx(m_run - m_step);
-                    m_run = m_step;
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < NC; ++c) tmem_st16(tS + c * 16, pk[c]);
-            if (again) {
-                const uint64_t a2 = f2_pack(alpha, alpha);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) acc[k] = f2_fma(acc[k], a2, 0ull);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) accp[k] *= alpha;
-                if (i > 0) {  // O holds the steps before this one (see the order of the products)
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t ov[32];
-                        tmem_ld32(tO + c * 32, ov);
-                        tmem_wait_ld();
-                        reg_fence32(ov);
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alpha);
-                        tmem_st32(tO + c * 32, ov);
+                if (i == 0) break;
+                if (!settled) {
+                    if (!wait_settled()) return;
+                    settled = true;
+                    const float m_now = m_other = row_max[trow];
+                    if (__any_sync(0xFFFFFFFFu, m_now != m_run)) {
+                        rescale_sums(m_now != m_run ? ex2_approx(m_run - m_now) : 1.0f);
+                        m_run = m_now;
+                        continue;
                     }
                 }
+                if (raised) break;
+                // a step sum of at most 2^8 bounds every weight: only a larger one (or NaN) raises the maximum
+                float s0, s1;
+                f2_unpack(f2_add(sacc[0], sacc[1]), s0, s1);
+                const bool raise = !(s0 + s1 <= kRescaleSum) || (m_run == -CUDART_INF_F && s0 + s1 > 0.0f);
+                if (!__any_sync(0xFFFFFFFFu, raise)) break;
+                raised = true;  // the whole warp: TMEM accesses are the warp's
+                const float m_all = step_max();
+                const float m_step = raise ? fmaxf(m_run, m_all) : m_run;
+                const float alpha = m_step != m_run ? ex2_approx(m_run - m_step) : 1.0f;
+                m_run = m_step;
+                row_max[trow] = m_run;
+                rescale_sums(alpha);
+                if (!warp_wait_all(bar(C::B_PVDONE + (g - 1) % C::NSB), ((g - 1) / C::NSB) & 1, ctl)) return;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t ov[32];
+                    tmem_ld32(tO + c * 32, ov);
+                    tmem_wait_ld();
+                    reg_fence32(ov);
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alpha);
+                    tmem_st32(tO + c * 32, ov);
+                }
             }
+            if (i > 0) settle();
+#pragma unroll
+            for (int c = 0; c < NC; ++c) tmem_st16(tS + c * 16, pk[c]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) acc[k] = f2_add(acc[k], sacc[k]);
 #pragma unroll
@@ -533,71 +559,92 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::B_PFULL + x));
+            if (lane == 0) mbar_arrive(bar(C::B_PFULL + b));
         }
         float e0, e1;
         f2_unpack(f2_add(acc[0], acc[1]), e0, e1);
-        const float l = e0 + e1, lp = (accp[0] + accp[1]) + (accp[2] + accp[3]);
-        const bool part = it.slot >= 0;
-        const int head = it.kh * p.s.g + rh;
-        char *orow = p.o.p + static_cast<int64_t>(it.q0 + tok) * p.o.token + head * p.o.head;
-        const size_t prow = part ? static_cast<size_t>(it.slot * 2 + x) * kTileM + trow : 0;
-        bool dirty = false;
-        if (n > 0) {
-            if (!warp_wait_all(bar(C::B_OFULL + x), e & 1, ctl)) return;
-            tc_fence_after();
-            ++e;
-            dirty = vflags[(count - 1) & 1] != 0u;
+        float l = e0 + e1, lp = (accp[0] + accp[1]) + (accp[2] + accp[3]);
+        // The group of the last step finishes the tile; the other one leaves its sums. Two buffers, used in turn: it may be
+        // one such tile ahead, not two, since each has a step of both groups and they wait for one another's.
+        const bool finishes = n > 0 ? ((G + n - 1) & 1) == group : group == 0;
+        volatile float *sums = row_sums + (pairs & 1) * 256 + trow * 2;
+        if (n >= 2 && !finishes) {
+            sums[0] = l;
+            sums[1] = lp;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_SUMS + w4));
         }
-        const float inv = part ? 1.0f : lp != 0.0f ? 1.0f / lp : 0.0f;
-#pragma unroll
-        for (int c0 = 0; c0 < D / 32; c0 += 2) {
-            uint32_t ov[2][32];
-            if (n > 0) {
-                tmem_ld32(tO + c0 * 32, ov[0]);
-                tmem_ld32(tO + (c0 + 1) * 32, ov[1]);
-                tmem_wait_ld();
-                reg_fence32(ov[0]);
-                reg_fence32(ov[1]);
-                if (c0 + 2 == D / 32) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + x));
-                }
+        if (finishes) {
+            if (n >= 2) {
+                if (!warp_wait_all(bar(C::B_SUMS + w4), pairs & 1, ctl)) return;
+                // its sums are relative to the maximum after the last step but one
+                const float a = m_other == m_run ? 1.0f : ex2_approx(m_other - m_run);
+                l += a * sums[0];
+                lp += a * sums[1];
             }
+            const bool part = it.slot >= 0;
+            const int head = it.kh * p.s.g + rh;
+            char *orow = p.o.p + static_cast<int64_t>(it.q0 + tok) * p.o.token + head * p.o.head;
+            const size_t prow = part ? static_cast<size_t>(it.slot) * kTileM + trow : 0;
+            bool dirty = false;
+            if (n > 0) {
+                const int t = G + n - 1;
+                if (!warp_wait_all(bar(C::B_PVDONE + t % C::NSB), (t / C::NSB) & 1, ctl)) return;
+                tc_fence_after();
+                dirty = vflags[(count - 1) & 1] != 0u;
+            }
+            const float inv = part ? 1.0f : lp != 0.0f ? 1.0f / lp : 0.0f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = c0 + h;
+            for (int c0 = 0; c0 < D / 32; c0 += 2) {
+                uint32_t ov[2][32];
+                if (n > 0) {
+                    tmem_ld32(tO + c0 * 32, ov[0]);
+                    tmem_ld32(tO + (c0 + 1) * 32, ov[1]);
+                    tmem_wait_ld();
+                    reg_fence32(ov[0]);
+                    reg_fence32(ov[1]);
+                    if (c0 + 2 == D / 32) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::B_OEMPTY));
+                    }
+                }
 #pragma unroll
-                for (int q = 0; q < 32; ++q) ov[h][q] = n > 0 ? __float_as_uint(__uint_as_float(ov[h][q]) * inv) : 0u;
-                if (part) {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + c * 32);
+                for (int h = 0; h < 2; ++h) {
+                    const int c = c0 + h;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        dst[q] = make_float4(__uint_as_float(ov[h][4 * q]), __uint_as_float(ov[h][4 * q + 1]),
-                                             __uint_as_float(ov[h][4 * q + 2]), __uint_as_float(ov[h][4 * q + 3]));
-                } else if (real) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 64);
+                    for (int q = 0; q < 32; ++q) ov[h][q] = n > 0 ? __float_as_uint(__uint_as_float(ov[h][q]) * inv) : 0u;
+                    if (part) {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + c * 32);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint4 w;
-                        w.x = pack_bf16x2(__uint_as_float(ov[h][8 * q]), __uint_as_float(ov[h][8 * q + 1]));
-                        w.y = pack_bf16x2(__uint_as_float(ov[h][8 * q + 2]), __uint_as_float(ov[h][8 * q + 3]));
-                        w.z = pack_bf16x2(__uint_as_float(ov[h][8 * q + 4]), __uint_as_float(ov[h][8 * q + 5]));
-                        w.w = pack_bf16x2(__uint_as_float(ov[h][8 * q + 6]), __uint_as_float(ov[h][8 * q + 7]));
-                        dst[q] = w;
+                        for (int q = 0; q < 8; ++q)
+                            dst[q] = make_float4(__uint_as_float(ov[h][4 * q]), __uint_as_float(ov[h][4 * q + 1]),
+                                                 __uint_as_float(ov[h][4 * q + 2]), __uint_as_float(ov[h][4 * q + 3]));
+                    } else if (real) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 64);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint4 w;
+                            w.x = pack_bf16x2(__uint_as_float(ov[h][8 * q]), __uint_as_float(ov[h][8 * q + 1]));
+                            w.y = pack_bf16x2(__uint_as_float(ov[h][8 * q + 2]), __uint_as_float(ov[h][8 * q + 3]));
+                            w.z = pack_bf16x2(__uint_as_float(ov[h][8 * q + 4]), __uint_as_float(ov[h][8 * q + 5]));
+                            w.w = pack_bf16x2(__uint_as_float(ov[h][8 * q + 6]), __uint_as_float(ov[h][8 * q + 7]));
+                            dst[q] = w;
+                        }
                     }
                 }
             }
+            if (dirty && real) {
+                const int from = max(it.lo, visible(p.s.causal, it.n_q, it.n_k, it.t0) / kStep) * kStep;
+                add_not_finite<D>(p.v.p + static_cast<int64_t>(it.k0) * p.v.token + it.kh * p.v.head, p.v.token, from,
+                                  min(nvis, it.hi * kStep), part ? reinterpret_cast<char *>(p.part_o + prow * D) : orow, part);
+            }
+            if (part) p.part_stats[prow] = make_float4(m_run, l, lp, 0.0f);
+            else if (real && p.lse)
+                p.lse[static_cast<int64_t>(head) * p.s.Tq + it.q0 + tok] = (m_run + log2f(l)) * 0.69314718055994530942f;
         }
-        if (dirty && real) {
-            const int from = max(it.lo, visible(p.s.causal, it.n_q, it.n_k, it.t0) / kStep) * kStep;
-            add_not_finite<D>(p.v.p + static_cast<int64_t>(it.k0) * p.v.token + it.kh * p.v.head, p.v.token, from,
-                              min(nvis, it.hi * kStep), part ? reinterpret_cast<char *>(p.part_o + prow * D) : orow, part);
-        }
-        if (part) p.part_stats[prow] = make_float4(m_run, l, lp, 0.0f);
-        else if (real && p.lse)
-            p.lse[static_cast<int64_t>(head) * p.s.Tq + it.q0 + tok] = (m_run + log2f(l)) * 0.69314718055994530942f;
+        if (n >= 2) ++pairs;
+        G += n;
         done_with<C>(sbase, lane, count);
     }
 }
@@ -615,34 +662,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile uint32_t *vflags = misc + 2;
     volatile int *items = reinterpret_cast<volatile int *>(misc + 4);
+    volatile float *row_max = reinterpret_cast<volatile float *>(smem + C::ROWS_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
+        for (int s = 0; s < C::QS; ++s) {
+            mbar_init(bar(C::B_QFULL + s), 1);
+            mbar_init(bar(C::B_QEMPTY + s), 1);
+        }
+        for (int s = 0; s < C::NK; ++s) {
+            mbar_init(bar(C::B_KFULL + s), 1);
+            mbar_init(bar(C::B_KEMPTY + s), 1);
+        }
+        for (int s = 0; s < C::NV; ++s) {
+            mbar_init(bar(C::B_VFULL + s), 1);
+            mbar_init(bar(C::B_VEMPTY + s), 1);
+            mbar_init(bar(C::B_VFIXED + s), 1);
+        }
+        for (int b = 0; b < C::NSB; ++b) {
+            mbar_init(bar(C::B_SFULL + b), 1);
+            mbar_init(bar(C::B_PFULL + b), 4);
+            mbar_init(bar(C::B_PVDONE + b), 1);
+        }
+        mbar_init(bar(C::B_OEMPTY), 4);
         for (int x = 0; x < 2; ++x) {
-            mbar_init(bar(C::B_QFULL + x), 1);
-            mbar_init(bar(C::B_QEMPTY + x), 1);
-            mbar_init(bar(C::B_SFULL + x), 1);
-            mbar_init(bar(C::B_PFULL + x), 4);
-            mbar_init(bar(C::B_OFULL + x), 1);
-            mbar_init(bar(C::B_OEMPTY + x), 4);
             mbar_init(bar(C::B_TFULL + x), 1);
             mbar_init(bar(C::B_TEMPTY + x), kSoftmaxWarps + 3);
             mbar_init(bar(C::B_DRAIN + x), 1);
         }
-        for (int s = 0; s < C::NK; ++s) {
-            mbar_init(bar(C::B_KFULL + s), 1);
-            mbar_init(bar(C::B_KEMPTY + s), 2);  // both tiles' issuers
-        }
-        for (int s = 0; s < C::NV; ++s) {
-            mbar_init(bar(C::B_VFULL + s), 1);
-            mbar_init(bar(C::B_VEMPTY + s), 2);
-            mbar_init(bar(C::B_VFIXED + s), 1);
-        }
+        for (int w = 0; w < 8; ++w) mbar_init(bar(C::B_MAX + w), 1);
+        for (int w = 0; w < 4; ++w) mbar_init(bar(C::B_SUMS + w), 1);
         misc[1] = 0u;
         misc[2] = misc[3] = 0u;
         fence_mbar_init();
     }
-    if (warp == kIssueWarp) {
+    if (warp == kPvWarp) {
         tmem_alloc(smem_u32(misc), 512);
         tmem_relinquish();
     }
@@ -660,23 +714,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kSoftmaxWarps) {
         regs_up<kSoftmaxRegs>();
-        softmax_role<D, C>(p, sbase, tmem, items, vflags, ctl, warp, lane);
+        softmax_role<D, C>(p, sbase, tmem, row_max, row_max + 128, items, vflags, ctl, warp, lane);
     } else {
         regs_down<kOtherRegs>();
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ items, Q, K, V
+            // Order: K of a step, then V of the step before it. A V slot is free when a P V completes, a K slot, long
+            // before, when a Q K^T does: a V that waits for its slot must not hold back the K that the softmax needs
+            // next. The item after this one is fetched while the first steps run.
             const uint32_t n_items = p.hdr->n_items;
-            int count = 0, G = 0, e[2] = {0, 0};
-            bool ok = true;
-            while (ok) {
-                const int slot = count & 1;
+            int count = 0, GK = 0, GV = 0, e = 0;
+            int v_row = 0, v_head = 0;  // the V that is due, if GV < GK
+            auto get = [&]() -> Item {
                 Item it{};
                 it.b = -1;
                 for (;;) {
                     uint32_t id = 0u;
                     if (lane == 0) id = atomicAdd(&p.hdr->next, 1u);
                     id = __shfl_sync(0xFFFFFFFFu, id, 0);
-                    if (id >= n_items) break;
+                    if (id >= n_items) return it;
                     const Entry *first = p.entries + id / p.s.Hk;
                     const int seq0 = first->seq0, seq_n = first->seq_n;
                     const int rest = static_cast<int>(id) - seq0 * p.s.Hk;
@@ -684,13 +740,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (en.t0 < 0) continue;
                     it.b = en.b, it.t0 = en.t0, it.lo = en.lo, it.hi = en.hi, it.kh = rest / seq_n;
                     it.slot = en.slot < 0 ? -1 : en.slot + it.kh;
-                    break;
-                }
-                if (it.b >= 0) {
                     const Seq q = seq_of(p.s, it.b, p.err);
                     it.n_q = q.n_q, it.n_k = q.n_k, it.q0 = q.q0, it.k0 = q.k0;
+                    return it;
                 }
-                if (count >= 2 && !warp_wait_all(bar(C::B_TEMPTY + slot), ((count >> 1) - 1) & 1, ctl)) break;
+            };
+            auto publish = [&](const Item &it) -> bool {
+                const int slot = count & 1;
+                if (count >= 2 && !warp_wait_all(bar(C::B_TEMPTY + slot), ((count >> 1) - 1) & 1, ctl)) return false;
                 if (lane == 0) {
                     volatile int *w = items + slot * C::kItemWords;
                     w[0] = it.b, w[1] = it.t0, w[2] = it.n_q, w[3] = it.n_k, w[4] = it.q0, w[5] = it.k0, w[6] = it.kh, w[7] = it.lo,
@@ -700,64 +757,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 ++count;
-                if (it.b < 0) break;
-                if (p.stall) continue;
+                return true;
+            };
+            auto load_v = [&]() -> bool {
+                const int s = GV % C::NV;
+                if (GV >= C::NV && !warp_wait_all(bar(C::B_VEMPTY + s), ((GV / C::NV) - 1) & 1, ctl)) return false;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar(C::B_VFULL + s), C::kKVBytes);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (tile_steps(p, it, x) == 0) continue;
-                    if (e[x] >= 1 && !warp_wait_all(bar(C::B_QEMPTY + x), (e[x] - 1) & 1, ctl)) {
-                        ok = false;
-                        break;
-                    }
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(bar(C::B_QFULL + x), static_cast<uint32_t>(p.s.g * p.s.tpt * D * 2));
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load_3d(sbase + C::Q_OFF + x * C::kQBytes + c * C::kSlab, &tmQ, c * 64, it.kh * p.s.g,
-                                        it.q0 + it.t0 + x * p.s.tpt, bar(C::B_QFULL + x));
-                    }
-                    __syncwarp();
-                    ++e[x];
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(sbase + C::V_OFF + s * C::kKVBytes + c * C::kSlab, &tmV, c * 64, v_row, v_head, bar(C::B_VFULL + s));
                 }
-                for (int i = it.lo; ok && i < it.hi; ++i, ++G) {
-                    const int ks = G % C::NK, vs = G % C::NV;
-                    if (G >= C::NK && !warp_wait_all(bar(C::B_KEMPTY + ks), ((G / C::NK) - 1) & 1, ctl)) {
-                        ok = false;
-                        break;
-                    }
+                __syncwarp();
+                ++GV;
+                return true;
+            };
+            Item it = get();
+            bool ok = publish(it);
+            while (ok && it.b >= 0) {
+                Item next{};
+                bool fetched = false;
+                if (!p.stall && it.hi > it.lo) {
+                    const int qs = e % C::QS;
+                    if (e >= C::QS && !warp_wait_all(bar(C::B_QEMPTY + qs), ((e / C::QS) - 1) & 1, ctl)) break;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(bar(C::B_KFULL + ks), C::kKVBytes);
+                        mbar_arrive_expect_tx(bar(C::B_QFULL + qs), static_cast<uint32_t>(p.s.g * p.s.tpt * D * 2));
 #pragma unroll
                         for (int c = 0; c < D / 64; ++c)
-                            tma_load_3d(sbase + C::K_OFF + ks * C::kKVBytes + c * C::kSlab, &tmK, c * 64, it.k0 + i * kStep, it.kh,
-                                        bar(C::B_KFULL + ks));
+                            tma_load_3d(sbase + C::Q_OFF + qs * C::kQBytes + c * C::kSlab, &tmQ, c * 64, it.kh * p.s.g, it.q0 + it.t0,
+                                        bar(C::B_QFULL + qs));
                     }
                     __syncwarp();
-                    if (G >= C::NV && !warp_wait_all(bar(C::B_VEMPTY + vs), ((G / C::NV) - 1) & 1, ctl)) {
-                        // the K load of this step is in flight and no later one will be: count it below
-                        ++G;
-                        ok = false;
-                        break;
-                    }
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(bar(C::B_VFULL + vs), C::kKVBytes);
+                    ++e;
+                    for (int i = it.lo; i < it.hi; ++i) {
+                        const int s = GK % C::NK;
+                        if (GK >= C::NK && !warp_wait_all(bar(C::B_KEMPTY + s), ((GK / C::NK) - 1) & 1, ctl)) {
+                            ok = false;
+                            break;
+                        }
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(bar(C::B_KFULL + s), C::kKVBytes);
 #pragma unroll
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load_3d(sbase + C::V_OFF + vs * C::kKVBytes + c * C::kSlab, &tmV, c * 64, it.k0 + i * kStep, it.kh,
-                                        bar(C::B_VFULL + vs));
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_3d(sbase + C::K_OFF + s * C::kKVBytes + c * C::kSlab, &tmK, c * 64, it.k0 + i * kStep, it.kh,
+                                            bar(C::B_KFULL + s));
+                        }
+                        __syncwarp();
+                        ++GK;
+                        if (GV + 1 < GK && !load_v()) {
+                            ok = false;
+                            break;
+                        }
+                        v_row = it.k0 + i * kStep;
+                        v_head = it.kh;
+                        if (!fetched && (i == it.lo + 1 || i + 1 == it.hi)) {
+                            next = get();
+                            fetched = true;
+                            if (!publish(next)) {
+                                ok = false;
+                                break;
+                            }
+                        }
                     }
-                    __syncwarp();
                 }
+                if (ok && !fetched) {  // an item without steps: what is due comes before a wait for the tile it belongs to
+                    next = get();
+                    ok = (GV == GK || load_v()) && publish(next);
+                }
+                it = next;
             }
+            if (ok && GV < GK) load_v();
             // after an abort: no copy of this warp is in flight when the CTA ends (a phase that has completed, or one
             // that no copy fills, ends a wait too: at its limit)
             if (lane == 0 && *ctl.abort_flag) {
-                for (int x = 0; x < 2; ++x)
-                    if (e[x] > 0) wait_bar_drain(bar(C::B_QFULL + x), (e[x] - 1) & 1);
-                for (int g = max(0, G - C::NK); g < G; ++g)
-                    wait_bar_drain(bar(C::B_KFULL + g % C::NK), (g / C::NK) & 1);
-                for (int g = max(0, G - C::NV); g < G; ++g)
-                    wait_bar_drain(bar(C::B_VFULL + g % C::NV), (g / C::NV) & 1);
+                for (int q = max(0, e - C::QS); q < e; ++q) wait_bar_drain(bar(C::B_QFULL + q % C::QS), (q / C::QS) & 1);
+                for (int g = max(0, GK - C::NK); g < GK; ++g) wait_bar_drain(bar(C::B_KFULL + g % C::NK), (g / C::NK) & 1);
+                for (int g = max(0, GV - C::NV); g < GV; ++g) wait_bar_drain(bar(C::B_VFULL + g % C::NV), (g / C::NV) & 1);
             }
             __syncwarp();
         } else if (warp == kFixWarp) {
@@ -808,92 +883,94 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 done_with<C>(sbase, lane, count);
             }
-        } else {
-            // ------------------------------------------------------------ products of one tile
-            const int x = warp - kIssueWarp;
-            const uint32_t tS = tmem + C::T_S + x * kStep, tO = tmem + C::T_O + x * D;
-            const uint64_t qdesc = sdesc_sw128(sbase + C::Q_OFF + x * C::kQBytes, 16, 1024);
-            const uint64_t kdesc0 = sdesc_sw128(sbase + C::K_OFF, 16, 1024);
-            const uint64_t vdesc0 = sdesc_sw128(sbase + C::V_OFF, C::kSlab, 1024);
-            int count = 0, G = 0, P = 0, e = 0;  // steps of the ring, steps and items of this tile
+        } else if (warp == kQkWarp) {
+            // ------------------------------------------------------------ S = Q K^T
+            const uint64_t qdesc0 = sdesc_sw128(sbase + C::Q_OFF, 16, 1024), kdesc0 = sdesc_sw128(sbase + C::K_OFF, 16, 1024);
+            int count = 0, G = 0, e = 0;
             bool ok = true;
             Item it;
-            auto issue_qk = [&](int g, bool last) -> bool {
-                const int s = g % C::NK;
-                if (!warp_wait_all(bar(C::B_KFULL + s), (g / C::NK) & 1, ctl)) return false;
-                tc_fence_after();
-                const uint64_t kd = kdesc0 + static_cast<uint64_t>(s * (C::kKVBytes >> 4));
-                __syncwarp();
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kSlab + (kk & 3) * 32) >> 4);
-                        mma_ss(tS, qdesc + off, kd + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
-                    }
-                    tc_commit(bar(C::B_SFULL + x));
-                    tc_commit(bar(C::B_KEMPTY + s));
-                    if (last) tc_commit(bar(C::B_QEMPTY + x));
-                }
-                __syncwarp();
-                return true;
-            };
             while (ok && !p.stall && fetch<C>(sbase, items, ctl, lane, count, it)) {
-                const int n = tile_steps(p, it, x), all = it.hi - it.lo;
+                const int n = it.hi - it.lo;
                 done_with<C>(sbase, lane, count);
-                if (n > 0) {
-                    ok = warp_wait_all(bar(C::B_QFULL + x), e & 1, ctl) && issue_qk(G, n == 1);
-                    for (int i = 0; ok && i < n; ++i, ++P) {
-                        const int g = G + i, s = g % C::NV;
-                        if (!warp_wait_all(bar(C::B_VFIXED + s), (g / C::NV) & 1, ctl) ||
-                            !warp_wait_all(bar(C::B_PFULL + x), P & 1, ctl) ||
-                            (i == 0 && e >= 1 && !warp_wait_all(bar(C::B_OEMPTY + x), (e - 1) & 1, ctl))) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint64_t vd = vdesc0 + static_cast<uint64_t>(s * (C::kKVBytes >> 4));
-                        __syncwarp();
-                        if (elect_one()) {
+                if (n == 0) continue;
+                const int qs = e % C::QS;
+                if (!warp_wait_all(bar(C::B_QFULL + qs), (e / C::QS) & 1, ctl)) break;
+                const uint64_t qd = qdesc0 + static_cast<uint64_t>(qs * (C::kQBytes >> 4));
+                for (int i = 0; i < n; ++i, ++G) {
+                    const int s = G % C::NK, b = G % C::NSB;
+                    if (!warp_wait_all(bar(C::B_KFULL + s), (G / C::NK) & 1, ctl) ||
+                        (G >= C::NSB && !warp_wait_all(bar(C::B_PVDONE + b), ((G / C::NSB) - 1) & 1, ctl))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t kd = kdesc0 + static_cast<uint64_t>(s * (C::kKVBytes >> 4));
+                    __syncwarp();
+                    if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < kStep / 16; ++kk)
-                                mma_ts(tO, tS + kk * 8, vd + static_cast<uint64_t>(kk * (16 * 128 >> 4)), C::IDESC_PV,
-                                       i == 0 && kk == 0 ? 0u : 1u);
-                            tc_commit(bar(C::B_VEMPTY + s));
-                            if (i == n - 1) tc_commit(bar(C::B_OFULL + x));
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::kSlab + (kk & 3) * 32) >> 4);
+                            mma_ss(tmem + b * kStep, qd + off, kd + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
                         }
-                        __syncwarp();
-                        if (i + 1 < n) ok = issue_qk(g + 1, i + 2 == n);
+                        tc_commit(bar(C::B_SFULL + b));
+                        tc_commit(bar(C::B_KEMPTY + s));
+                        if (i + 1 == n) tc_commit(bar(C::B_QEMPTY + qs));
                     }
-                    ++e;
-                }
-                for (int i = n; ok && i < all; ++i) {  // the other tile's steps: this one is done with their blocks at once
-                    const int g = G + i;
-                    if (!warp_wait_all(bar(C::B_KFULL + g % C::NK), (g / C::NK) & 1, ctl)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive(bar(C::B_KEMPTY + g % C::NK));
-                    if (!warp_wait_all(bar(C::B_VFIXED + g % C::NV), (g / C::NV) & 1, ctl)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive(bar(C::B_VEMPTY + g % C::NV));
                     __syncwarp();
                 }
-                G += all;
+                ++e;
             }
             // all products of the elected lane have completed before TMEM is freed
             __syncwarp();
             if (elect_one()) {
-                tc_commit(bar(C::B_DRAIN + x));
-                wait_bar_drain(bar(C::B_DRAIN + x), 0);
+                tc_commit(bar(C::B_DRAIN));
+                wait_bar_drain(bar(C::B_DRAIN), 0);
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ O += P V
+            const uint64_t vdesc0 = sdesc_sw128(sbase + C::V_OFF, C::kSlab, 1024);
+            int count = 0, G = 0, e = 0;
+            bool ok = true;
+            Item it;
+            while (ok && !p.stall && fetch<C>(sbase, items, ctl, lane, count, it)) {
+                const int n = it.hi - it.lo;
+                done_with<C>(sbase, lane, count);
+                for (int i = 0; i < n; ++i, ++G) {
+                    const int s = G % C::NV, b = G % C::NSB;
+                    // the first product of a tile overwrites O: the tile before has been read
+                    if (!warp_wait_all(bar(C::B_VFIXED + s), (G / C::NV) & 1, ctl) ||
+                        (i == 0 && e >= 1 && !warp_wait_all(bar(C::B_OEMPTY), (e - 1) & 1, ctl)) ||
+                        !warp_wait_all(bar(C::B_PFULL + b), (G / C::NSB) & 1, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t vd = vdesc0 + static_cast<uint64_t>(s * (C::kKVBytes >> 4));
+                    __syncwarp();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < kStep / 16; ++kk)
+                            mma_ts(tmem + C::T_O, tmem + b * kStep + kk * 8, vd + static_cast<uint64_t>(kk * (16 * 128 >> 4)),
+                                   C::IDESC_PV, i == 0 && kk == 0 ? 0u : 1u);
+                        tc_commit(bar(C::B_PVDONE + b));
+                        tc_commit(bar(C::B_VEMPTY + s));
+                    }
+                    __syncwarp();
+                }
+                if (n > 0) ++e;
+            }
+            __syncwarp();
+            if (elect_one()) {
+                tc_commit(bar(C::B_DRAIN + 1));
+                wait_bar_drain(bar(C::B_DRAIN + 1), 0);
             }
             __syncwarp();
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kIssueWarp) {
+    if (warp == kPvWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -919,18 +996,18 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinArgs a)
     constexpr int V = D / 32;  // channels of a lane
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    const long long rows = static_cast<long long>(a.hdr->n_splits) * a.s.Hk * 2 * kTileM;
+    const long long rows = static_cast<long long>(a.hdr->n_splits) * a.s.Hk * kTileM;
     const long long step = static_cast<long long>(gridDim.x) * 8;
     for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows; i += step) {
-        const int row = static_cast<int>(i % (2 * kTileM));
-        const long long rest = i / (2 * kTileM);
+        const int trow = static_cast<int>(i % kTileM);
+        const long long rest = i / kTileM;
         const int kh = static_cast<int>(rest % a.s.Hk);
         const Split sp = a.splits[rest / a.s.Hk];
-        const int trow = row % kTileM, rt = trow / a.s.g, rh = trow % a.s.g;
+        const int rt = trow / a.s.g, rh = trow % a.s.g;
         const Seq q = seq_of(a.s, sp.b, a.err);
-        const int tok = sp.t0 + (row / kTileM) * a.s.tpt + rt;
+        const int tok = sp.t0 + rt;
         if (rt >= a.s.tpt || tok >= q.n_q) continue;
-        const size_t first = (static_cast<size_t>(sp.slot + kh) * 2) * kTileM + row, stride = static_cast<size_t>(a.s.Hk) * 2 * kTileM;
+        const size_t first = static_cast<size_t>(sp.slot + kh) * kTileM + trow, stride = static_cast<size_t>(a.s.Hk) * kTileM;
         float4 st = make_float4(-CUDART_INF_F, 0.0f, 0.0f, 0.0f);  // of part `lane`
         if (lane < sp.chunks) st = __ldcg(a.part_stats + first + lane * stride);
         float M = st.x;
@@ -984,7 +1061,7 @@ int tokens_per_tile(int H, int Hk) { return kTileM / (H / Hk); }
 Layout layout_of(int T, int B, int H, int Hk, int d)
 {
     const int tpt = tokens_per_tile(H, Hk);
-    const int64_t items = T / (2 * tpt) + static_cast<int64_t>(B);
+    const int64_t items = T / tpt + static_cast<int64_t>(B);
     Layout l;
     l.max_slots = static_cast<int>(items * Hk * kMaxChunks < kMaxSlots ? items * Hk * kMaxChunks : kMaxSlots);
     size_t at = kCacheScratch;
@@ -999,8 +1076,8 @@ Layout layout_of(int T, int B, int H, int Hk, int d)
     l.splits = take(sizeof(Split) * (kMaxSlots / 2 + 1));
     l.rank = take(sizeof(int32_t) * static_cast<size_t>(B));
     l.at = take(sizeof(int32_t) * static_cast<size_t>(B));
-    l.stats = take(sizeof(float4) * 2 * kTileM * static_cast<size_t>(l.max_slots));
-    l.part = take(sizeof(float) * 2 * kTileM * static_cast<size_t>(d) * l.max_slots);
+    l.stats = take(sizeof(float4) * kTileM * static_cast<size_t>(l.max_slots));
+    l.part = take(sizeof(float) * kTileM * static_cast<size_t>(d) * l.max_slots);
     l.total = at - kCacheScratch;
     return l;
 }
@@ -1037,7 +1114,7 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
 {
     using C = Cfg<D>;
     static_assert(C::SMEM_ALLOC <= 227 * 1024, "shared memory");
-    static_assert(2 * (kStep + D) <= 512, "TMEM columns");
+    static_assert(C::T_O + D <= 512, "TMEM columns");
     int sms = 0;
     const bsa_status s = current_sm_count(&sms);
     if (s != BSA_OK) return s;
