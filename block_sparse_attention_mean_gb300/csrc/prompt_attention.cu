@@ -6,13 +6,13 @@
 //   * A tile is 128 rows of S = Q K^T: floor(128 / g) tokens of a sequence with the g query heads of one key head, loaded
 //     by one TMA box, so that grouped heads share each K and V block that is fetched. One persistent CTA per SM.
 //   * Two groups of four softmax warps, a thread per row, take a tile's steps in turn: a step's chain (load S, 128
-//     exponentials and sums, store P) is twice as long as its products take on the tensor cores. One warp issues the
-//     Q K^T, up to three steps ahead (three S / P buffers in TMEM), one the P V; one loads, and one looks after V
-//     where a mask ends in a block.
+//     exponentials and sums, store P) is twice as long as its products take on the tensor cores. Of the other four
+//     warps one issues the Q K^T, up to three steps ahead (three S / P buffers in TMEM), one the P V; one hands out the
+//     items and loads Q and K, and one loads V and looks after it where a mask ends in a block.
 //   * Online softmax in log2, P in bf16 over S in TMEM: the running maximum of a row is raised only when a step's sum
 //     passes 2^8 (the step is then done again and O rescaled). The groups share it: a step is computed with the
-//     maximum as last seen; before its P is stored, the warp waits for the decision of the step before (the other group's
-//     warp of the same rows) and does the step again if that raised it. Each group sums its own steps; the one of the
+//     maximum as last seen; before its P is stored, each row looks at what the step before settled on (shared memory, with
+//     the step's number) and the warp does the step again if that raised it. Each group sums its own steps; the one of the
 //     last step adds them up. fp32 sums; O is divided by the sum of the weights as rounded to bf16.
 //   * A plan in one CTA cuts the work: items are (sequence, key head, tile), a sequence's heads one after another
 //     so that its K and V stay in L2, longest sequences and longest ranges first; an item well above the average of a
@@ -35,7 +35,8 @@ namespace {
 constexpr int kTileM = 128;
 constexpr int kStep = 128;  // keys of a step
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarp = 8, kQkWarp = 9, kPvWarp = 10, kFixWarp = 11;
+constexpr int kLoadWarp = 8, kQkWarp = 9, kPvWarp = 10, kValueWarp = 11;
+constexpr int kRing = 4;  // items in flight
 constexpr int kThreads = 12 * 32;
 // registers a thread after the split: 256 * 216 + 128 * 72 = 384 * 168, what the block is launched with
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
@@ -307,13 +308,12 @@ struct Cfg {
     static constexpr int B_QFULL = 0, B_QEMPTY = B_QFULL + QS, B_KFULL = B_QEMPTY + QS, B_KEMPTY = B_KFULL + NK,
                          B_VFULL = B_KEMPTY + NK, B_VEMPTY = B_VFULL + NV, B_VFIXED = B_VEMPTY + NV, B_SFULL = B_VFIXED + NV,
                          B_PFULL = B_SFULL + NSB, B_PVDONE = B_PFULL + NSB, B_OEMPTY = B_PVDONE + NSB, B_TFULL = B_OEMPTY + 1,
-                         B_TEMPTY = B_TFULL + 2, B_MAX = B_TEMPTY + 2, B_SUMS = B_MAX + 8, B_DRAIN = B_SUMS + 4,
-                         NBAR = B_DRAIN + 2;
+                         B_TEMPTY = B_TFULL + kRing, B_SUMS = B_TEMPTY + kRing, B_DRAIN = B_SUMS + 4, NBAR = B_DRAIN + 2;
     static constexpr int MISC_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;
     static constexpr int kItemWords = 12;
-    static constexpr int MISC_WORDS = 4 + 2 * kItemWords;  // TMEM base, abort flag, V flags of the two items, the items
-    static constexpr int ROWS_OFF = MISC_OFF + 4 * MISC_WORDS;  // running maxima [128], one group's sums [2][128][2]
-    static constexpr int SMEM = ROWS_OFF + 4 * (128 + 2 * 128 * 2);
+    static constexpr int MISC_WORDS = 2 + kRing + kRing * kItemWords;  // TMEM base, abort flag, V flags of the items, the items
+    static constexpr int ROWS_OFF = (MISC_OFF + 4 * MISC_WORDS + 15) / 16 * 16;  // settled maxima [128][2], sums [2][128][2]
+    static constexpr int SMEM = ROWS_OFF + 4 * (128 * 2 + 2 * 128 * 2);
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(kTileM, kStep, 0, 0);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(kTileM, D, 0, 1);
@@ -365,12 +365,12 @@ __device__ __forceinline__ void regs_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The next item from the ring of two; false at the end or when a wait gave up
+// The next item from the ring; false at the end or when a wait gave up
 template <class C>
 __device__ __forceinline__ bool fetch(uint32_t sbase, const volatile int *items, const Ctl &ctl, int lane, int &count, Item &it)
 {
-    const int slot = count & 1;
-    if (!warp_wait_all(sbase + C::BAR_OFF + 8u * (C::B_TFULL + slot), (count >> 1) & 1, ctl)) return false;
+    const int slot = count % kRing;
+    if (!warp_wait_all(sbase + C::BAR_OFF + 8u * (C::B_TFULL + slot), (count / kRing) & 1, ctl)) return false;
     const volatile int *w = items + slot * C::kItemWords;
     it.b = w[0], it.t0 = w[1], it.n_q = w[2], it.n_k = w[3], it.q0 = w[4], it.k0 = w[5], it.kh = w[6], it.lo = w[7], it.hi = w[8],
     it.slot = w[9];
@@ -382,7 +382,13 @@ template <class C>
 __device__ __forceinline__ void done_with(uint32_t sbase, int lane, int count)
 {
     __syncwarp();
-    if (lane == 0) mbar_arrive(sbase + C::BAR_OFF + 8u * (C::B_TEMPTY + ((count - 1) & 1)));
+    if (lane == 0) mbar_arrive(sbase + C::BAR_OFF + 8u * (C::B_TEMPTY + (count - 1) % kRing));
+}
+
+// first step of the item in which some row of the tile does not see all keys
+__device__ __forceinline__ int first_masked(const Params &p, const Item &it)
+{
+    return max(it.lo, visible(p.s.causal, it.n_q, it.n_k, it.t0) / kStep);
 }
 
 // Adds what is not finite among the rows [j_lo, j_hi) of V to a row of D results (fp32 or bf16) in global memory
@@ -401,7 +407,7 @@ __device__ __forceinline__ void add_not_finite(const char *v, int64_t stride, in
 }
 
 template <int D, class C>
-__device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, uint32_t tmem, volatile float *row_max,
+__device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, uint32_t tmem, uint32_t settled_at,
                                              volatile float *row_sums, const volatile int *items,
                                              const volatile uint32_t *vflags, const Ctl &ctl, int warp, int lane)
 {
@@ -490,23 +496,35 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                     }
                 }
             };
-            // the other group's warp of these rows has settled the maximum of the step before
-            auto wait_settled = [&]() -> bool {
-                return g == 0 || warp_wait_all(bar(C::B_MAX + (1 - group) * 4 + w4), ((g - 1) >> 1) & 1, ctl);
+            // What the step before settled on for this row. Each step writes (maximum, its number plus one) in one access:
+            // the number says whose it is. False where the other group's warp gave up.
+            auto wait_settled = [&](float &m) -> bool {
+                uint32_t tag;
+                uint64_t t0 = 0ull;
+                for (;;) {
+                    asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];" : "=f"(m), "=r"(tag) : "r"(settled_at + trow * 8) : "memory");
+                    if (__all_sync(0xFFFFFFFFu, tag == static_cast<uint32_t>(g))) return true;
+                    if (t0 == 0ull) t0 = globaltimer_ns();
+                    else if (__any_sync(0xFFFFFFFFu, *ctl.abort_flag != 0u || globaltimer_ns() - t0 > ctl.limit)) break;
+                }
+                if (lane == 0 && !*ctl.abort_flag) {
+                    *ctl.abort_flag = 1u;
+                    raise_error(ctl.err, BSA_ERR_TIMEOUT);
+                }
+                return false;
             };
-            auto settle = [&]() {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_MAX + group * 4 + w4));
+            auto settle = [&](float m) {
+                asm volatile("st.volatile.shared.v2.b32 [%0], {%1, %2};" ::"r"(settled_at + trow * 8), "f"(m), "r"(g + 1) : "memory");
             };
             bool settled = false;  // the step before is known
             if (i == 0) {  // a new tile: its first step's maximum, known before the exponentials are
                 m_run = step_max();
-                if (!wait_settled()) return;
-                row_max[trow] = m_run;
-                settle();
+                float before;
+                if (!wait_settled(before)) return;
+                settle(m_run);
             } else if (i == 1) {
-                if (!wait_settled()) return;
-                m_run = m_other = row_max[trow];
+                if (!wait_settled(m_run)) return;
+                m_other = m_run;
                 settled = true;
             }
             bool raised = false;
@@ -514,9 +532,10 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 exps(m_run);
                 if (i == 0) break;
                 if (!settled) {
-                    if (!wait_settled()) return;
+                    float m_now;
+                    if (!wait_settled(m_now)) return;
                     settled = true;
-                    const float m_now = m_other = row_max[trow];
+                    m_other = m_now;
                     if (__any_sync(0xFFFFFFFFu, m_now != m_run)) {
                         rescale_sums(m_now != m_run ? ex2_approx(m_run - m_now) : 1.0f);
                         m_run = m_now;
@@ -534,7 +553,6 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 const float m_step = raise ? fmaxf(m_run, m_all) : m_run;
                 const float alpha = m_step != m_run ? ex2_approx(m_run - m_step) : 1.0f;
                 m_run = m_step;
-                row_max[trow] = m_run;
                 rescale_sums(alpha);
                 if (!warp_wait_all(bar(C::B_PVDONE + (g - 1) % C::NSB), ((g - 1) / C::NSB) & 1, ctl)) return;
                 tc_fence_after();
@@ -549,7 +567,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                     tmem_st32(tO + c * 32, ov);
                 }
             }
-            if (i > 0) settle();
+            if (i > 0) settle(m_run);
 #pragma unroll
             for (int c = 0; c < NC; ++c) tmem_st16(tS + c * 16, pk[c]);
 #pragma unroll
@@ -591,7 +609,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 const int t = G + n - 1;
                 if (!warp_wait_all(bar(C::B_PVDONE + t % C::NSB), (t / C::NSB) & 1, ctl)) return;
                 tc_fence_after();
-                dirty = vflags[(count - 1) & 1] != 0u;
+                dirty = vflags[(count - 1) % kRing] != 0u;
             }
             const float inv = part ? 1.0f : lp != 0.0f ? 1.0f / lp : 0.0f;
 #pragma unroll
@@ -635,7 +653,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 }
             }
             if (dirty && real) {
-                const int from = max(it.lo, visible(p.s.causal, it.n_q, it.n_k, it.t0) / kStep) * kStep;
+                const int from = first_masked(p, it) * kStep;
                 add_not_finite<D>(p.v.p + static_cast<int64_t>(it.k0) * p.v.token + it.kh * p.v.head, p.v.token, from,
                                   min(nvis, it.hi * kStep), part ? reinterpret_cast<char *>(p.part_o + prow * D) : orow, part);
             }
@@ -661,8 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int idx) -> uint32_t { return sbase + C::BAR_OFF + 8u * idx; };
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
     volatile uint32_t *vflags = misc + 2;
-    volatile int *items = reinterpret_cast<volatile int *>(misc + 4);
-    volatile float *row_max = reinterpret_cast<volatile float *>(smem + C::ROWS_OFF);
+    volatile int *items = reinterpret_cast<volatile int *>(misc + 2 + kRing);
+    volatile float *row_sums = reinterpret_cast<volatile float *>(smem + C::ROWS_OFF + 128 * 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -685,17 +703,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(C::B_PVDONE + b), 1);
         }
         mbar_init(bar(C::B_OEMPTY), 4);
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kRing; ++x) {
             mbar_init(bar(C::B_TFULL + x), 1);
-            mbar_init(bar(C::B_TEMPTY + x), kSoftmaxWarps + 3);
-            mbar_init(bar(C::B_DRAIN + x), 1);
+            mbar_init(bar(C::B_TEMPTY + x), kSoftmaxWarps + 3);  // softmax, Q K^T, P V, V
         }
-        for (int w = 0; w < 8; ++w) mbar_init(bar(C::B_MAX + w), 1);
+        mbar_init(bar(C::B_DRAIN), 1);
+        mbar_init(bar(C::B_DRAIN + 1), 1);
         for (int w = 0; w < 4; ++w) mbar_init(bar(C::B_SUMS + w), 1);
         misc[1] = 0u;
-        misc[2] = misc[3] = 0u;
         fence_mbar_init();
     }
+    // no step has settled on anything: step 0 looks for the number 0
+    if (threadIdx.x < 256) reinterpret_cast<uint32_t *>(smem + C::ROWS_OFF)[threadIdx.x] = 0u;
     if (warp == kPvWarp) {
         tmem_alloc(smem_u32(misc), 512);
         tmem_relinquish();
@@ -714,25 +733,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kSoftmaxWarps) {
         regs_up<kSoftmaxRegs>();
-        softmax_role<D, C>(p, sbase, tmem, row_max, row_max + 128, items, vflags, ctl, warp, lane);
+        softmax_role<D, C>(p, sbase, tmem, sbase + C::ROWS_OFF, row_sums, items, vflags, ctl, warp, lane);
     } else {
         regs_down<kOtherRegs>();
         if (warp == kLoadWarp) {
-            // ------------------------------------------------------------ items, Q, K, V
-            // Order: K of a step, then V of the step before it. A V slot is free when a P V completes, a K slot, long
-            // before, when a Q K^T does: a V that waits for its slot must not hold back the K that the softmax needs
-            // next. The item after this one is fetched while the first steps run.
+            // ------------------------------------------------------------ items, Q, K
+            // The item after the one at hand is fetched while its first steps run.
             const uint32_t n_items = p.hdr->n_items;
-            int count = 0, GK = 0, GV = 0, e = 0;
-            int v_row = 0, v_head = 0;  // the V that is due, if GV < GK
-            auto get = [&]() -> Item {
-                Item it{};
+            int count = 0, G = 0, e = 0;
+            auto hand_out = [&](Item &it) -> bool {
                 it.b = -1;
                 for (;;) {
                     uint32_t id = 0u;
                     if (lane == 0) id = atomicAdd(&p.hdr->next, 1u);
                     id = __shfl_sync(0xFFFFFFFFu, id, 0);
-                    if (id >= n_items) return it;
+                    if (id >= n_items) break;
                     const Entry *first = p.entries + id / p.s.Hk;
                     const int seq0 = first->seq0, seq_n = first->seq_n;
                     const int rest = static_cast<int>(id) - seq0 * p.s.Hk;
@@ -742,12 +757,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     it.slot = en.slot < 0 ? -1 : en.slot + it.kh;
                     const Seq q = seq_of(p.s, it.b, p.err);
                     it.n_q = q.n_q, it.n_k = q.n_k, it.q0 = q.q0, it.k0 = q.k0;
-                    return it;
+                    break;
                 }
-            };
-            auto publish = [&](const Item &it) -> bool {
-                const int slot = count & 1;
-                if (count >= 2 && !warp_wait_all(bar(C::B_TEMPTY + slot), ((count >> 1) - 1) & 1, ctl)) return false;
+                const int slot = count % kRing;
+                if (count >= kRing && !warp_wait_all(bar(C::B_TEMPTY + slot), ((count / kRing) - 1) & 1, ctl)) return false;
                 if (lane == 0) {
                     volatile int *w = items + slot * C::kItemWords;
                     w[0] = it.b, w[1] = it.t0, w[2] = it.n_q, w[3] = it.n_k, w[4] = it.q0, w[5] = it.k0, w[6] = it.kh, w[7] = it.lo,
@@ -759,25 +772,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++count;
                 return true;
             };
-            auto load_v = [&]() -> bool {
-                const int s = GV % C::NV;
-                if (GV >= C::NV && !warp_wait_all(bar(C::B_VEMPTY + s), ((GV / C::NV) - 1) & 1, ctl)) return false;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(bar(C::B_VFULL + s), C::kKVBytes);
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_3d(sbase + C::V_OFF + s * C::kKVBytes + c * C::kSlab, &tmV, c * 64, v_row, v_head, bar(C::B_VFULL + s));
-                }
-                __syncwarp();
-                ++GV;
-                return true;
-            };
-            Item it = get();
-            bool ok = publish(it);
+            Item it{}, next{};
+            bool ok = hand_out(it);
             while (ok && it.b >= 0) {
-                Item next{};
                 bool fetched = false;
-                if (!p.stall && it.hi > it.lo) {
+                if (it.hi > it.lo && !p.stall) {
                     const int qs = e % C::QS;
                     if (e >= C::QS && !warp_wait_all(bar(C::B_QEMPTY + qs), ((e / C::QS) - 1) & 1, ctl)) break;
                     if (elect_one()) {
@@ -789,9 +788,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                     ++e;
-                    for (int i = it.lo; i < it.hi; ++i) {
-                        const int s = GK % C::NK;
-                        if (GK >= C::NK && !warp_wait_all(bar(C::B_KEMPTY + s), ((GK / C::NK) - 1) & 1, ctl)) {
+                    for (int i = it.lo; i < it.hi; ++i, ++G) {
+                        const int s = G % C::NK;
+                        if (G >= C::NK && !warp_wait_all(bar(C::B_KEMPTY + s), ((G / C::NK) - 1) & 1, ctl)) {
                             ok = false;
                             break;
                         }
@@ -803,52 +802,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             bar(C::B_KFULL + s));
                         }
                         __syncwarp();
-                        ++GK;
-                        if (GV + 1 < GK && !load_v()) {
-                            ok = false;
-                            break;
-                        }
-                        v_row = it.k0 + i * kStep;
-                        v_head = it.kh;
                         if (!fetched && (i == it.lo + 1 || i + 1 == it.hi)) {
-                            next = get();
                             fetched = true;
-                            if (!publish(next)) {
+                            if (!hand_out(next)) {
+                                ++G;  // its copy is in flight
                                 ok = false;
                                 break;
                             }
                         }
                     }
                 }
-                if (ok && !fetched) {  // an item without steps: what is due comes before a wait for the tile it belongs to
-                    next = get();
-                    ok = (GV == GK || load_v()) && publish(next);
-                }
+                if (ok && !fetched) ok = hand_out(next);
                 it = next;
             }
-            if (ok && GV < GK) load_v();
-            // after an abort: no copy of this warp is in flight when the CTA ends (a phase that has completed, or one
-            // that no copy fills, ends a wait too: at its limit)
+            // after an abort: no copy of this warp is in flight when the CTA ends
             if (lane == 0 && *ctl.abort_flag) {
                 for (int q = max(0, e - C::QS); q < e; ++q) wait_bar_drain(bar(C::B_QFULL + q % C::QS), (q / C::QS) & 1);
-                for (int g = max(0, GK - C::NK); g < GK; ++g) wait_bar_drain(bar(C::B_KFULL + g % C::NK), (g / C::NK) & 1);
-                for (int g = max(0, GV - C::NV); g < GV; ++g) wait_bar_drain(bar(C::B_VFULL + g % C::NV), (g / C::NV) & 1);
+                for (int g = max(0, G - C::NK); g < G; ++g) wait_bar_drain(bar(C::B_KFULL + g % C::NK), (g / C::NK) & 1);
             }
             __syncwarp();
-        } else if (warp == kFixWarp) {
-            // ------------------------------------------------------------ V where a mask ends
+        } else if (warp == kValueWarp) {
+            // ------------------------------------------------------------ V, and V where a mask ends
             int count = 0, G = 0;
-            bool ok = true;
+            bool ok = !p.stall;
             Item it;
             while (ok && fetch<C>(sbase, items, ctl, lane, count, it)) {
-                const int from = visible(p.s.causal, it.n_q, it.n_k, it.t0) / kStep;  // first step that some row sees in part
+                const int from = first_masked(p, it);
                 for (int i = it.lo; i < it.hi; ++i, ++G) {
                     const int s = G % C::NV;
-                    if (!warp_wait_all(bar(C::B_VFULL + s), (G / C::NV) & 1, ctl)) {
+                    if (G >= C::NV && !warp_wait_all(bar(C::B_VEMPTY + s), ((G / C::NV) - 1) & 1, ctl)) {
                         ok = false;
                         break;
                     }
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar(C::B_VFULL + s), C::kKVBytes);
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(sbase + C::V_OFF + s * C::kKVBytes + c * C::kSlab, &tmV, c * 64, it.k0 + i * kStep, it.kh,
+                                        bar(C::B_VFULL + s));
+                    }
+                    __syncwarp();
                     if (i >= from) {
+                        if (!warp_wait_all(bar(C::B_VFULL + s), (G / C::NV) & 1, ctl)) {
+                            ++G;  // its copy is in flight
+                            ok = false;
+                            break;
+                        }
                         const int rows = min(kStep, it.n_k - i * kStep);  // rows of the block that are the sequence's
                         uint8_t *v = smem + C::V_OFF + s * C::kKVBytes;
                         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -872,17 +871,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     if ((slab[k] & 0x7F80u) == 0x7F80u) slab[k] = 0;
                             }
                             if (lane == 0) {
-                                vflags[(count - 1) & 1] = 1u;
+                                vflags[(count - 1) % kRing] = 1u;
                                 __threadfence_block();
                             }
                         }
                         fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_VFIXED + s));
+                    if (lane == 0) mbar_arrive(bar(C::B_VFIXED + s));  // nobody waits for it where no mask ends
                 }
                 done_with<C>(sbase, lane, count);
             }
+            if (lane == 0 && *ctl.abort_flag)
+                for (int g = max(0, G - C::NV); g < G; ++g) wait_bar_drain(bar(C::B_VFULL + g % C::NV), (g / C::NV) & 1);
+            __syncwarp();
         } else if (warp == kQkWarp) {
             // ------------------------------------------------------------ S = Q K^T
             const uint64_t qdesc0 = sdesc_sw128(sbase + C::Q_OFF, 16, 1024), kdesc0 = sdesc_sw128(sbase + C::K_OFF, 16, 1024);
@@ -934,12 +936,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             Item it;
             while (ok && !p.stall && fetch<C>(sbase, items, ctl, lane, count, it)) {
-                const int n = it.hi - it.lo;
+                const int n = it.hi - it.lo, from = first_masked(p, it) - it.lo;
                 done_with<C>(sbase, lane, count);
                 for (int i = 0; i < n; ++i, ++G) {
                     const int s = G % C::NV, b = G % C::NSB;
                     // the first product of a tile overwrites O: the tile before has been read
-                    if (!warp_wait_all(bar(C::B_VFIXED + s), (G / C::NV) & 1, ctl) ||
+                    if (!warp_wait_all(bar((i >= from ? C::B_VFIXED : C::B_VFULL) + s), (G / C::NV) & 1, ctl) ||
                         (i == 0 && e >= 1 && !warp_wait_all(bar(C::B_OEMPTY), (e - 1) & 1, ctl)) ||
                         !warp_wait_all(bar(C::B_PFULL + b), (G / C::NSB) & 1, ctl)) {
                         ok = false;
