@@ -183,8 +183,8 @@ bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, i
 static bsa_status check_prompt_shape(int T, int B, int H, int Hk, int d)
 {
     if ((d != 64 && d != 128) || T < 0 || B < 1 || !valid_heads(H, Hk) || H / Hk > 128) return BSA_ERR_SHAPE;
-    // items (tiles of floor(128 / g) tokens) of all key heads, parts included, are counted in 31 bits
-    const int64_t items = T / (128 / (H / Hk)) + static_cast<int64_t>(B) + 2048;
+    // items (tiles of floor(128 / g) tokens) of all key heads are counted in 31 bits
+    const int64_t items = T / (128 / (H / Hk)) + static_cast<int64_t>(B);
     return items * Hk <= INT32_MAX ? BSA_OK : BSA_ERR_SHAPE;
 }
 

@@ -13,10 +13,15 @@
 //     passes 2^8 (the step is then done again and O rescaled). The groups share it: a step is computed with the
 //     maximum as last seen; before its P is stored, each row looks at what the step before settled on (shared memory, with
 //     the step's number) and the warp does the step again if that raised it. Each group sums its own steps; the one of the
-//     last step adds them up. fp32 sums; O is divided by the sum of the weights as rounded to bf16.
-//   * A plan in one CTA cuts the work: items are (sequence, key head, tile), a sequence's heads one after another
-//     so that its K and V stay in L2, longest sequences and longest ranges first; an item well above the average of a
-//     CTA is split by key range, and a second launch joins the parts in order.
+//     last step adds them up. fp32 sums. P is
+//     rounded to bf16, each weight by at most half a step (2^-8 of it), and O is divided by the sum of the weights before.
+//   * Items are (sequence, key head, tile); a launch of one CTA looks at the lengths first. With many items, CTAs take them
+//     from a counter: longest sequences first, a sequence's heads one after another, so that K and V of the one or two in
+//     use stay in L2 (32768 tokens, 16 heads of 128: five heads in use cost a quarter of the rate, two heads a sixth), and
+//     of each head the longest items first. The last heads, two rounds of items of all CTAs, go together, longest items
+//     first, so that the work ends with short ones. Where that would leave CTAs idle (few items, or
+//     one far above a CTA's average), all steps in a row are cut evenly over the CTAs instead, and a third launch joins
+//     the parts of an item that a cut runs through, in order.
 //   * 0 * NaN: a masked weight of zero still multiplies V. In blocks where a mask ends, rows of V behind the sequence
 //     are zeroed in shared memory, and other values that are not finite too; these are then added in the epilogue to
 //     the rows that see them. Blocks that every row sees whole are not looked at.
@@ -44,26 +49,26 @@ constexpr float kRescaleSum = 256.0f;
 constexpr uint32_t kDbgStall = 1u;  // of bsa_debug_config
 constexpr unsigned long long kDrainNs = 1000000000ull;  // copies and products in flight are waited for this long
 
-// Parts: an item of more than 1.5 shares (a CTA's average of steps, rounded up) becomes ceil(steps / share) parts, so
-// all split items together at most 1.67 per CTA.
-constexpr int kMaxSlots = 320;   // partial results (a tile each): 1.67 * 152 and some
-constexpr int kMaxParts = 1088;  // entries that parts add: 1.67 * 640
-constexpr int kMaxChunks = 32;   // parts of one item
+constexpr int kMaxSlots = 320;       // partial results (a tile each): two per CTA
+constexpr int kMaxCutItems = 65536;  // items (of all key heads) up to which the steps are cut evenly
 constexpr int kPlanThreads = 1024;
 
-// Work of one CTA at a time; expanded by the key heads
+// A part of an item (or all of it) where the steps are cut evenly
 struct __align__(16) Entry {
-    int b, t0;       // sequence, first token
-    int lo, hi;      // steps of 128 keys
-    int slot, seq0;  // first partial slot (of key head 0) or -1; first entry of the sequence
-    int seq_n, pad;  // entries of the sequence
+    int b, t0, kh;  // sequence, first token, key head
+    int lo, hi;     // steps of 128 keys
+    int slot;       // of its partial result, or -1: it is whole
+    int pad[2];
 };
+// An item in parts: the first is the last of CTA c0, the others the first of the CTAs after it
 struct __align__(16) Split {
-    int b, t0, chunks, slot;
+    int b, t0, kh, c0, parts, pad[3];
 };
+__host__ __device__ constexpr int slot_of(int c0, int part) { return part == 0 ? 2 * c0 + 1 : 2 * (c0 + part); }
 
 struct PlanHeader {  // in the workspace, behind the tickets
-    uint32_t next, n_items, n_splits, n_slots;
+    uint32_t next, n_items, n_splits;
+    int cut;  // CTAs that the steps are cut over; 0: items come from the counter
 };
 
 struct Seqs {
@@ -111,13 +116,16 @@ __device__ __forceinline__ int item_steps(const Seqs &s, const Seq &q, int t0)
 
 struct PlanArgs {
     Seqs s;
-    int ctas, max_slots;
-    long long max_entries;
+    int ctas;
+    long long max_items, max_entries;
     PlanHeader *hdr;
+    int32_t *rank;         // [B] sequences, longest first
+    int32_t *item0;        // [B + 1] items of the ranks before
+    long long *step0;      // [B] steps of all heads of the ranks before
+    int32_t *item_step0;   // [items] steps of the items before in the sequence (only where the steps are cut)
+    int32_t *first;        // [CTAs + 1] first entry of a CTA
     Entry *entries;
     Split *splits;
-    int32_t *rank;    // [B] sequences, longest first
-    int32_t *at;      // [B] scratch: entries of the sequence of that rank
     uint32_t *err;
 };
 
@@ -149,11 +157,73 @@ __device__ __forceinline__ long long block_prefix(long long v, long long &total,
     return excl;
 }
 
-__device__ __forceinline__ int chunks_of(int steps, int share)
+// The steps [from, to) of all items in a row, as entries of CTA c; their number, and written where `out` is given. Items
+// without steps belong to the CTA that they lie in front of, or to the last one.
+__device__ int walk_cut(const PlanArgs &a, int c, int ctas, long long from, long long to, long long total, Entry *out)
 {
-    if (steps <= share + share / 2) return 1;
-    const int n = (steps + share - 1) / share;
-    return n < kMaxChunks ? n : kMaxChunks;
+    const Seqs &s = a.s;
+    // the rank and head where the range begins: the first rank at `from`, else the one that `from` is inside of
+    int lo = 0, hi = s.B;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.step0[mid] >= from) hi = mid;
+        else lo = mid + 1;
+    }
+    int r = lo, kh = 0, i = 0;
+    long long at = from;  // steps in front of item i of head kh of rank r
+    int skip = 0;         // steps of it that belong to the CTA before
+    if (r == s.B || a.step0[r] > from) {
+        --r;
+        const long long head = ((r + 1 < s.B ? a.step0[r + 1] : total) - a.step0[r]) / s.Hk;  // > 0: `from` is inside
+        kh = static_cast<int>((from - a.step0[r]) / head);
+        const int off = static_cast<int>((from - a.step0[r]) % head);
+        const int base = a.item0[r], n = a.item0[r + 1] - base;
+        int l = 0, h = n;
+        while (l < h) {
+            const int mid = (l + h) >> 1;
+            if (a.item_step0[base + mid] >= off) h = mid;
+            else l = mid + 1;
+        }
+        i = l;
+        if (i == n || a.item_step0[base + i] > off) {
+            --i;
+            skip = off - a.item_step0[base + i];
+            at = from - skip;
+        }
+    }
+    int count = 0;
+    for (; r < s.B; ++r, kh = 0) {
+        const int b = a.rank[r];
+        const Seq q = seq_of(s, b, a.err);
+        const int n = a.item0[r + 1] - a.item0[r];
+        for (; n > 0 && kh < s.Hk; ++kh, i = 0)
+            for (; i < n; ++i) {
+                if (at >= to && c + 1 < ctas) return count;
+                const int steps = item_steps(s, q, i * s.tpt);
+                const long long end = at + steps;
+                const bool more = end > to;  // it goes on in the next CTA
+                if (out) {
+                    Entry e{};
+                    e.b = b;
+                    e.t0 = i * s.tpt;
+                    e.kh = kh;
+                    e.lo = skip;
+                    e.hi = more ? static_cast<int>(to - at) : steps;
+                    e.slot = skip > 0 ? 2 * c : more ? 2 * c + 1 : -1;
+                    out[count] = e;
+                    if (skip == 0 && more) {
+                        const int last = static_cast<int>((end * ctas + total - 1) / total) - 1;  // CTA of its last step
+                        a.splits[atomicAdd(&a.hdr->n_splits, 1u)] = Split{b, e.t0, kh, c, last - c + 1, {0, 0, 0}};
+                    }
+                }
+                ++count;
+                if (more) return count;
+                skip = 0;
+                at = end;
+            }
+        i = 0;
+    }
+    return count;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
@@ -162,11 +232,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     __shared__ long long warp_sums[32];
     __shared__ int bucket[kPlanThreads];
     __shared__ int longest;
-    __shared__ uint32_t n_splits, n_slots;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Seqs &s = a.s;
     bucket[tid] = 0;
-    if (tid == 0) longest = 0, n_splits = 0u, n_slots = 0u;
+    if (tid == 0) longest = 0;
     __syncthreads();
     // sequences by their last item's steps, longest first (counting sort; 1023 steps and more count as equal)
     auto key = [&](const Seq &q) -> int {
@@ -181,102 +250,85 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     bucket[tid] = start;
     __syncthreads();
     for (int b = tid; b < s.B; b += kPlanThreads) a.rank[atomicAdd(&bucket[key(seq_of(s, b, a.err))], 1)] = b;
-    // steps of all items, and of the longest
-    long long mine = 0;
+    __syncthreads();
+    // items and steps of each, and the longest item
     int most = 0;
-    for (int b = warp; b < s.B; b += 32) {
-        const Seq q = seq_of(s, b, a.err);
-        const int items = (q.n_q + s.tpt - 1) / s.tpt;
-        for (int i = lane; i < items; i += 32) {
-            const int n = item_steps(s, q, i * s.tpt);
-            mine += n;
-            most = max(most, n);
-        }
-    }
-    atomicMax(&longest, most);
-    block_prefix(mine, total, warp_sums);
-    const int share = static_cast<int>(max(1ll, min(1ll << 29, (total * s.Hk + a.ctas - 1) / a.ctas)));
-    const bool split = chunks_of(longest, share) > 1;
-    // entries of each sequence, in order of rank, and their places
     for (int r = warp; r < s.B; r += 32) {
         const Seq q = seq_of(s, a.rank[r], a.err);
         const int items = (q.n_q + s.tpt - 1) / s.tpt;
-        int n = items;
-        if (split) {
-            n = 0;
-            for (int i = lane; i < items; i += 32) n += chunks_of(item_steps(s, q, i * s.tpt), share);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+        long long sum = 0;
+        for (int i = lane; i < items; i += 32) {
+            const int n = item_steps(s, q, i * s.tpt);
+            sum += n;
+            most = max(most, n);
         }
-        if (lane == 0) a.at[r] = n;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == 0) {
+            a.item0[r] = items;
+            a.step0[r] = sum * s.Hk;
+        }
     }
+    atomicMax(&longest, most);
     __syncthreads();
+    // exclusive sums over the ranks
     const int run = (s.B + kPlanThreads - 1) / kPlanThreads;
     const int lo = min(s.B, tid * run), hi = min(s.B, lo + run);
-    long long n = 0;
-    for (int r = lo; r < hi; ++r) n += a.at[r];
-    long long before = block_prefix(n, total, warp_sums);
-    if (total > a.max_entries) {  // sequences that overlap: more tokens than there are
-        if (tid == 0) {
-            raise_error(a.err, BSA_ERR_INVALID_ARG);
-            a.hdr->next = a.hdr->n_items = a.hdr->n_splits = 0u;
-        }
-        return;
-    }
+    long long items = 0, steps = 0, all_items, all_steps;
+    for (int r = lo; r < hi; ++r) items += a.item0[r], steps += a.step0[r];
+    items = block_prefix(items, all_items, warp_sums);
+    steps = block_prefix(steps, all_steps, warp_sums);
     for (int r = lo; r < hi; ++r) {
-        const int c = a.at[r];
-        a.at[r] = static_cast<int>(before);
-        before += c;
+        const int n = a.item0[r];
+        const long long m = a.step0[r];
+        a.item0[r] = static_cast<int>(items);
+        a.step0[r] = steps;
+        items += n;
+        steps += m;
     }
+    const bool sound = all_items <= a.max_items;  // else sequences overlap: more tokens than there are
+    if (!sound) raise_error(a.err, BSA_ERR_INVALID_ARG);
+    // The steps of the CTA that works longest when items come from the counter: whole rounds where all are as long, else about
+    // the share and what is left of an item at the end. Cutting costs about eight steps (partial results, the join), and spreads
+    // the CTAs over all heads, whose K and V then share L2: it has to gain an eighth of the share besides.
+    const long long n_items = all_items * s.Hk, share = max(1ll, (all_steps + a.ctas - 1) / a.ctas);
+    const long long rounds = (n_items + a.ctas - 1) / a.ctas;
+    const long long uncut = all_steps == n_items * longest || rounds == 1 ? rounds * longest
+                                                                          : max(static_cast<long long>(longest), share + longest / 8);
+    const bool cut = sound && n_items <= kMaxCutItems && 2 * a.ctas <= kMaxSlots && uncut > share + share / 8 + 8;
+    const int ctas = static_cast<int>(max(1ll, min(static_cast<long long>(a.ctas), all_steps)));
+    if (tid == 0) {
+        a.item0[s.B] = sound ? static_cast<int>(all_items) : 0;
+        a.hdr->next = 0u;
+        a.hdr->n_items = sound ? static_cast<uint32_t>(all_items) * static_cast<uint32_t>(s.Hk) : 0u;
+        a.hdr->n_splits = 0u;
+        a.hdr->cut = cut ? ctas : 0;
+    }
+    if (!cut) return;
     __syncthreads();
-    const int entries = static_cast<int>(total);
     for (int r = warp; r < s.B; r += 32) {
-        const int b = a.rank[r];
-        const Seq q = seq_of(s, b, a.err);
-        const int items = (q.n_q + s.tpt - 1) / s.tpt;
-        const int seq0 = a.at[r], seq_n = (r + 1 < s.B ? a.at[r + 1] : entries) - seq0;
-        int base = seq0;
-        for (int i0 = 0; i0 < items; i0 += 32) {
-            const int i = items - 1 - (i0 + lane);  // longest first
-            const int t0 = i * s.tpt;
-            const int steps = i >= 0 ? item_steps(s, q, t0) : 0;
-            const int c = i >= 0 ? (split ? chunks_of(steps, share) : 1) : 0;
-            int incl = c;
+        const Seq q = seq_of(s, a.rank[r], a.err);
+        const int base = a.item0[r], n = a.item0[r + 1] - base;
+        int before = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane;
+            const int m = i < n ? item_steps(s, q, i * s.tpt) : 0;
+            int incl = m;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
                 if (lane >= o) incl += y;
             }
-            const int at = base + incl - c;
-            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
-            if (c == 0) continue;
-            // parts where there is room for their results; else the first entry takes the whole range
-            int slot = -1;
-            if (c > 1) {
-                slot = static_cast<int>(atomicAdd(&n_slots, static_cast<uint32_t>(c * s.Hk)));
-                if (slot + c * s.Hk > a.max_slots) slot = -1;
-                else a.splits[atomicAdd(&n_splits, 1u)] = Split{b, t0, c, slot};
-            }
-            for (int k = 0; k < c; ++k) {
-                Entry e;
-                e.b = b;
-                e.t0 = slot < 0 && k > 0 ? -1 : t0;  // -1: nothing to do
-                e.lo = slot < 0 ? 0 : static_cast<int>(static_cast<long long>(k) * steps / c);
-                e.hi = slot < 0 ? steps : static_cast<int>(static_cast<long long>(k + 1) * steps / c);
-                e.slot = slot < 0 ? -1 : slot + k * s.Hk;
-                e.seq0 = seq0;
-                e.seq_n = seq_n;
-                e.pad = 0;
-                a.entries[at + k] = e;
-            }
+            if (i < n) a.item_step0[base + i] = before + incl - m;
+            before += __shfl_sync(0xFFFFFFFFu, incl, 31);
         }
     }
     __syncthreads();
-    if (tid == 0) {
-        a.hdr->next = 0u;
-        a.hdr->n_items = static_cast<uint32_t>(entries) * static_cast<uint32_t>(s.Hk);
-        a.hdr->n_splits = n_splits;
-    }
+    const long long from = tid < ctas ? tid * all_steps / ctas : 0, to = tid < ctas ? (tid + 1) * all_steps / ctas : 0;
+    const int mine = tid < ctas ? walk_cut(a, tid, ctas, from, to, all_steps, nullptr) : 0;
+    const int at = static_cast<int>(block_prefix(mine, total, warp_sums));
+    if (tid <= ctas) a.first[tid] = at;
+    if (tid < ctas) walk_cut(a, tid, ctas, from, to, all_steps, a.entries + at);
 }
 
 // ---------------------------------------------------------------- the attention
@@ -287,9 +339,10 @@ struct Params {
     PackedView o, v;
     float *lse;
     PlanHeader *hdr;
+    const int32_t *rank, *item0, *first;
     const Entry *entries;
     float *part_o;       // [slot][128][D]
-    float4 *part_stats;  // [slot][128] (max in log2, sum, sum of the rounded weights, 0)
+    float2 *part_stats;  // [slot][128] (max in log2, sum)
     uint32_t *err;
     unsigned long long wait_limit_ns;
     int stall;  // load and multiply nothing: the first waits run out
@@ -308,12 +361,12 @@ struct Cfg {
     static constexpr int B_QFULL = 0, B_QEMPTY = B_QFULL + QS, B_KFULL = B_QEMPTY + QS, B_KEMPTY = B_KFULL + NK,
                          B_VFULL = B_KEMPTY + NK, B_VEMPTY = B_VFULL + NV, B_VFIXED = B_VEMPTY + NV, B_SFULL = B_VFIXED + NV,
                          B_PFULL = B_SFULL + NSB, B_PVDONE = B_PFULL + NSB, B_OEMPTY = B_PVDONE + NSB, B_TFULL = B_OEMPTY + 1,
-                         B_TEMPTY = B_TFULL + kRing, B_SUMS = B_TEMPTY + kRing, B_DRAIN = B_SUMS + 4, NBAR = B_DRAIN + 2;
+                         B_TEMPTY = B_TFULL + kRing, B_SUMS = B_TEMPTY + kRing, B_DRAIN = B_SUMS + 8, NBAR = B_DRAIN + 2;
     static constexpr int MISC_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;
     static constexpr int kItemWords = 12;
     static constexpr int MISC_WORDS = 2 + kRing + kRing * kItemWords;  // TMEM base, abort flag, V flags of the items, the items
-    static constexpr int ROWS_OFF = (MISC_OFF + 4 * MISC_WORDS + 15) / 16 * 16;  // settled maxima [128][2], sums [2][128][2]
-    static constexpr int SMEM = ROWS_OFF + 4 * (128 * 2 + 2 * 128 * 2);
+    static constexpr int ROWS_OFF = (MISC_OFF + 4 * MISC_WORDS + 15) / 16 * 16;  // settled maxima [128][2], sums [2][128]
+    static constexpr int SMEM = ROWS_OFF + 4 * (128 * 2 + 2 * 128);
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(kTileM, kStep, 0, 0);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(kTileM, D, 0, 1);
@@ -427,14 +480,11 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
         const int nvis = real ? visible(p.s.causal, it.n_q, it.n_k, tok) : 0;
         float m_run = -CUDART_INF_F;
         uint64_t acc[2] = {0ull, 0ull};
-        float accp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         float m_other = -CUDART_INF_F;  // the maximum that the other group's sums are relative to
         auto rescale_sums = [&](float alpha) {
             const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll
             for (int k = 0; k < 2; ++k) acc[k] = f2_fma(acc[k], a2, 0ull);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) accp[k] *= alpha;
         };
         for (int i = (G ^ group) & 1; i < n; i += 2) {  // this group's steps: every other one, over all items
             const int g = G + i, b = g % C::NSB;
@@ -442,24 +492,29 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
             if (!warp_wait_all(bar(C::B_SFULL + b), (g / C::NSB) & 1, ctl)) return;
             tc_fence_after();
             const int nv = nvis - (it.lo + i) * kStep;  // columns that the row sees
-            const bool masked = __any_sync(0xFFFFFFFFu, nv < kStep);
-            // chunk c of S, columns that the row does not see as -inf; the loads that are under way complete here
-            auto ready = [&](int c, uint32_t (&sv)[32]) {
-                tmem_wait_ld();
-                reg_fence32(sv);
-                if (masked) {
+            if (__any_sync(0xFFFFFFFFu, nv < kStep)) {
+                // a mask ends in this step: S is masked in place, so that the loop below (the code that counts) is short
+#pragma unroll 1
+                for (int c = 0; c < NC; ++c) {
+                    uint32_t sv[32];
+                    tmem_ld32(tS + c * 32, sv);
+                    tmem_wait_ld();
+                    reg_fence32(sv);
 #pragma unroll
                     for (int t = 0; t < 32; ++t)
                         if (c * 32 + t >= nv) sv[t] = 0xFF800000u;
+                    tmem_st32(tS + c * 32, sv);
                 }
-            };
+                tmem_wait_st();
+            }
             auto step_max = [&]() -> float {
                 float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll 1
                 for (int c = 0; c < NC; ++c) {
                     uint32_t sv[32];
                     tmem_ld32(tS + c * 32, sv);
-                    ready(c, sv);
+                    tmem_wait_ld();
+                    reg_fence32(sv);
 #pragma unroll
                     for (int t = 0; t < 32; t += 8)
 #pragma unroll
@@ -470,19 +525,17 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
             };
             const uint64_t c2x = f2_pack(p.scale_log2, p.scale_log2);
             uint64_t sacc[2];
-            float sap[4];
             uint32_t pk[NC][16];  // P, stored over S when the step's maximum is settled
             auto exps = [&](float m) {
                 const float base = m == -CUDART_INF_F ? 0.0f : m;  // a row that has seen no key yet: every weight 0
                 const uint64_t nm2 = f2_pack(-base, -base);
                 sacc[0] = sacc[1] = 0ull;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sap[k] = 0.0f;
                 uint32_t sv[2][32];
                 tmem_ld32(tS, sv[0]);
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    ready(c, sv[c & 1]);
+                    tmem_wait_ld();
+                    reg_fence32(sv[c & 1]);
                     if (c + 1 < NC) tmem_ld32(tS + (c + 1) * 32, sv[(c + 1) & 1]);
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
@@ -492,7 +545,6 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                         const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                         sacc[q & 1] = f2_add(sacc[q & 1], f2_pack(p0, p1));
                         pk[c][q] = pack_bf16x2(p0, p1);
-                        add_bf16x2_to_f32(sap[2 * (q & 1)], sap[2 * (q & 1) + 1], pk[c][q]);
                     }
                 }
             };
@@ -572,8 +624,6 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
             for (int c = 0; c < NC; ++c) tmem_st16(tS + c * 16, pk[c]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) acc[k] = f2_add(acc[k], sacc[k]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) accp[k] += sap[k];
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -581,24 +631,22 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
         }
         float e0, e1;
         f2_unpack(f2_add(acc[0], acc[1]), e0, e1);
-        float l = e0 + e1, lp = (accp[0] + accp[1]) + (accp[2] + accp[3]);
-        // The group of the last step finishes the tile; the other one leaves its sums. Two buffers, used in turn: it may be
-        // one such tile ahead, not two, since each has a step of both groups and they wait for one another's.
+        float l = e0 + e1;
+        // The group of the last step finishes the tile; the other one leaves its sums. Two buffers with a barrier each, used
+        // in turn: it may be one such tile ahead, not two, since each has a step of both groups and they wait for one
+        // another's. (With one barrier it could be two phases ahead of a wait, which then never ends.)
         const bool finishes = n > 0 ? ((G + n - 1) & 1) == group : group == 0;
-        volatile float *sums = row_sums + (pairs & 1) * 256 + trow * 2;
+        volatile float *sum = row_sums + (pairs & 1) * 128 + trow;
         if (n >= 2 && !finishes) {
-            sums[0] = l;
-            sums[1] = lp;
+            *sum = l;
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::B_SUMS + w4));
+            if (lane == 0) mbar_arrive(bar(C::B_SUMS + (pairs & 1) * 4 + w4));
         }
         if (finishes) {
             if (n >= 2) {
-                if (!warp_wait_all(bar(C::B_SUMS + w4), pairs & 1, ctl)) return;
+                if (!warp_wait_all(bar(C::B_SUMS + (pairs & 1) * 4 + w4), (pairs >> 1) & 1, ctl)) return;
                 // its sums are relative to the maximum after the last step but one
-                const float a = m_other == m_run ? 1.0f : ex2_approx(m_other - m_run);
-                l += a * sums[0];
-                lp += a * sums[1];
+                l += (m_other == m_run ? 1.0f : ex2_approx(m_other - m_run)) * *sum;
             }
             const bool part = it.slot >= 0;
             const int head = it.kh * p.s.g + rh;
@@ -611,7 +659,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 tc_fence_after();
                 dirty = vflags[(count - 1) % kRing] != 0u;
             }
-            const float inv = part ? 1.0f : lp != 0.0f ? 1.0f / lp : 0.0f;
+            const float inv = part ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
             for (int c0 = 0; c0 < D / 32; c0 += 2) {
                 uint32_t ov[2][32];
@@ -657,7 +705,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 add_not_finite<D>(p.v.p + static_cast<int64_t>(it.k0) * p.v.token + it.kh * p.v.head, p.v.token, from,
                                   min(nvis, it.hi * kStep), part ? reinterpret_cast<char *>(p.part_o + prow * D) : orow, part);
             }
-            if (part) p.part_stats[prow] = make_float4(m_run, l, lp, 0.0f);
+            if (part) p.part_stats[prow] = make_float2(m_run, l);
             else if (real && p.lse)
                 p.lse[static_cast<int64_t>(head) * p.s.Tq + it.q0 + tok] = (m_run + log2f(l)) * 0.69314718055994530942f;
         }
@@ -709,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(bar(C::B_DRAIN), 1);
         mbar_init(bar(C::B_DRAIN + 1), 1);
-        for (int w = 0; w < 4; ++w) mbar_init(bar(C::B_SUMS + w), 1);
+        for (int w = 0; w < 8; ++w) mbar_init(bar(C::B_SUMS + w), 1);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -739,25 +787,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ items, Q, K
             // The item after the one at hand is fetched while its first steps run.
-            const uint32_t n_items = p.hdr->n_items;
+            // (past L1: the plan was written while this kernel was on its way)
+            const uint32_t n_items = __ldcg(&p.hdr->n_items);
+            const int cut = __ldcg(&p.hdr->cut);
+            int due = 0, due_end = 0;  // where the steps are cut: this CTA's entries
+            if (static_cast<int>(blockIdx.x) < cut) due = __ldcg(p.first + blockIdx.x), due_end = __ldcg(p.first + blockIdx.x + 1);
             int count = 0, G = 0, e = 0;
             auto hand_out = [&](Item &it) -> bool {
                 it.b = -1;
-                for (;;) {
+                if (cut) {
+                    if (due < due_end) {
+                        const int4 *en = reinterpret_cast<const int4 *>(p.entries + due++);
+                        const int4 x = __ldcg(en), y = __ldcg(en + 1);
+                        it.b = x.x, it.t0 = x.y, it.kh = x.z, it.lo = x.w, it.hi = y.x, it.slot = y.y;
+                    }
+                } else {
                     uint32_t id = 0u;
                     if (lane == 0) id = atomicAdd(&p.hdr->next, 1u);
                     id = __shfl_sync(0xFFFFFFFFu, id, 0);
-                    if (id >= n_items) break;
-                    const Entry *first = p.entries + id / p.s.Hk;
-                    const int seq0 = first->seq0, seq_n = first->seq_n;
-                    const int rest = static_cast<int>(id) - seq0 * p.s.Hk;
-                    const Entry en = p.entries[seq0 + rest % seq_n];
-                    if (en.t0 < 0) continue;
-                    it.b = en.b, it.t0 = en.t0, it.lo = en.lo, it.hi = en.hi, it.kh = rest / seq_n;
-                    it.slot = en.slot < 0 ? -1 : en.slot + it.kh;
+                    if (id < n_items) {
+                        // the rank: the last r with item0[r] <= id / Hk, 32 places looked at together
+                        const int item = static_cast<int>(id / static_cast<uint32_t>(p.s.Hk));
+                        int r = 0;
+                        for (int n = p.s.B; n > 1;) {
+                            const int step = (n + 31) / 32, k = r + lane * step;
+                            const bool below = lane * step < n && __ldcg(p.item0 + k) <= item;
+                            const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, below));
+                            r += last * step;
+                            n = min(step, n - last * step);
+                        }
+                        const int base = __ldcg(p.item0 + r), n = __ldcg(p.item0 + r + 1) - base;
+                        const int rest = static_cast<int>(id) - base * p.s.Hk;
+                        // the last `mixed` heads of the sequence, tile by tile; the others head by head
+                        const int mixed = min(p.s.Hk, (2 * static_cast<int>(gridDim.x) + n - 1) / n);
+                        const int in_order = (p.s.Hk - mixed) * n, tail = rest - in_order;
+                        it.b = __ldcg(p.rank + r);
+                        it.kh = tail < 0 ? rest / n : p.s.Hk - mixed + tail % mixed;
+                        it.t0 = (n - 1 - (tail < 0 ? rest % n : tail / mixed)) * p.s.tpt;
+                        it.lo = 0;
+                        it.slot = -1;
+                    }
+                }
+                if (it.b >= 0) {
                     const Seq q = seq_of(p.s, it.b, p.err);
                     it.n_q = q.n_q, it.n_k = q.n_k, it.q0 = q.q0, it.k0 = q.k0;
-                    break;
+                    if (!cut) it.hi = item_steps(p.s, q, it.t0);
                 }
                 const int slot = count % kRing;
                 if (count >= kRing && !warp_wait_all(bar(C::B_TEMPTY + slot), ((count / kRing) - 1) & 1, ctl)) return false;
@@ -987,59 +1061,50 @@ struct JoinArgs {
     const PlanHeader *hdr;
     const Split *splits;
     const float *part_o;
-    const float4 *part_stats;
+    const float2 *part_stats;
     uint32_t *err;
 };
 
-// A warp per row: O = sum w_k O_k / sum w_k lp_k, LSE = ln2 (M + log2 sum w_k l_k), w_k = 2^(m_k - M)
+// A warp per row: O = sum w_k O_k / sum w_k l_k, LSE = ln2 (M + log2 sum w_k l_k), w_k = 2^(m_k - M)
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const JoinArgs a)
 {
     constexpr int V = D / 32;  // channels of a lane
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    const long long rows = static_cast<long long>(a.hdr->n_splits) * a.s.Hk * kTileM;
+    const long long rows = static_cast<long long>(__ldcg(&a.hdr->n_splits)) * kTileM;
     const long long step = static_cast<long long>(gridDim.x) * 8;
     for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows; i += step) {
         const int trow = static_cast<int>(i % kTileM);
-        const long long rest = i / kTileM;
-        const int kh = static_cast<int>(rest % a.s.Hk);
-        const Split sp = a.splits[rest / a.s.Hk];
+        const Split sp = a.splits[i / kTileM];
         const int rt = trow / a.s.g, rh = trow % a.s.g;
         const Seq q = seq_of(a.s, sp.b, a.err);
         const int tok = sp.t0 + rt;
         if (rt >= a.s.tpt || tok >= q.n_q) continue;
-        const size_t first = static_cast<size_t>(sp.slot + kh) * kTileM + trow, stride = static_cast<size_t>(a.s.Hk) * kTileM;
-        float4 st = make_float4(-CUDART_INF_F, 0.0f, 0.0f, 0.0f);  // of part `lane`
-        if (lane < sp.chunks) st = __ldcg(a.part_stats + first + lane * stride);
-        float M = st.x;
+        auto row_of = [&](int part) { return static_cast<size_t>(slot_of(sp.c0, part)) * kTileM + trow; };
+        float M = -CUDART_INF_F;
+        for (int k = lane; k < sp.parts; k += 32) M = fmaxf(M, __ldcg(a.part_stats + row_of(k)).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-        const float w = st.x == -CUDART_INF_F ? 0.0f : ex2_approx(st.x - M);
-        float L = st.x == -CUDART_INF_F ? 0.0f : w * st.y, LP = st.x == -CUDART_INF_F ? 0.0f : w * st.z;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
-            LP += __shfl_xor_sync(0xFFFFFFFFu, LP, o);
-        }
-        float out[V];
+        float L = 0.0f, out[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) out[c] = 0.0f;
 #pragma unroll 4
-        for (int k = 0; k < sp.chunks; ++k) {
-            const float wk = __shfl_sync(0xFFFFFFFFu, w, k), mk = __shfl_sync(0xFFFFFFFFu, st.x, k);
-            if (mk == -CUDART_INF_F) continue;
-            const float *src = a.part_o + (first + k * stride) * D + lane * V;
+        for (int k = 0; k < sp.parts; ++k) {
+            const float2 st = __ldcg(a.part_stats + row_of(k));
+            const float w = st.x == M ? 1.0f : ex2_approx(st.x - M);
+            L += w * st.y;
+            const float *src = a.part_o + row_of(k) * D + lane * V;
             if constexpr (V == 4) {
                 const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                out[0] += wk * v.x, out[1] += wk * v.y, out[2] += wk * v.z, out[3] += wk * v.w;
+                out[0] += w * v.x, out[1] += w * v.y, out[2] += w * v.z, out[3] += w * v.w;
             } else {
                 const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                out[0] += wk * v.x, out[1] += wk * v.y;
+                out[0] += w * v.x, out[1] += w * v.y;
             }
         }
-        const float inv = LP != 0.0f ? 1.0f / LP : 0.0f;
-        const int head = kh * a.s.g + rh;
+        const float inv = L != 0.0f ? 1.0f / L : 0.0f;
+        const int head = sp.kh * a.s.g + rh;
         char *dst = a.o.p + static_cast<int64_t>(q.q0 + tok) * a.o.token + head * a.o.head + lane * V * 2;
         if constexpr (V == 4)
             *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(out[0] * inv, out[1] * inv), pack_bf16x2(out[2] * inv, out[3] * inv));
@@ -1053,19 +1118,18 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinArgs a)
 // ---------------------------------------------------------------- host
 
 struct Layout {
-    size_t hdr, entries, splits, rank, at, stats, part, total;
-    int max_slots;
-    int64_t max_entries;
+    size_t hdr, rank, item0, step0, item_step0, first, entries, splits, stats, part, total;
+    int64_t max_items, max_entries;
 };
 
 int tokens_per_tile(int H, int Hk) { return kTileM / (H / Hk); }
 
 Layout layout_of(int T, int B, int H, int Hk, int d)
 {
-    const int tpt = tokens_per_tile(H, Hk);
-    const int64_t items = T / tpt + static_cast<int64_t>(B);
     Layout l;
-    l.max_slots = static_cast<int>(items * Hk * kMaxChunks < kMaxSlots ? items * Hk * kMaxChunks : kMaxSlots);
+    l.max_items = T / tokens_per_tile(H, Hk) + static_cast<int64_t>(B);
+    const int64_t cut_items = l.max_items * Hk < kMaxCutItems ? l.max_items * Hk : kMaxCutItems;
+    l.max_entries = cut_items + kMaxSlots;
     size_t at = kCacheScratch;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -1073,13 +1137,15 @@ Layout layout_of(int T, int B, int H, int Hk, int d)
         return here;
     };
     l.hdr = take(sizeof(PlanHeader));
-    l.max_entries = items + kMaxParts;
-    l.entries = take(sizeof(Entry) * static_cast<size_t>(l.max_entries));
-    l.splits = take(sizeof(Split) * (kMaxSlots / 2 + 1));
     l.rank = take(sizeof(int32_t) * static_cast<size_t>(B));
-    l.at = take(sizeof(int32_t) * static_cast<size_t>(B));
-    l.stats = take(sizeof(float4) * kTileM * static_cast<size_t>(l.max_slots));
-    l.part = take(sizeof(float) * kTileM * static_cast<size_t>(d) * l.max_slots);
+    l.item0 = take(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
+    l.step0 = take(sizeof(long long) * static_cast<size_t>(B));
+    l.item_step0 = take(sizeof(int32_t) * static_cast<size_t>(cut_items));
+    l.first = take(sizeof(int32_t) * (kMaxSlots / 2 + 1));
+    l.entries = take(sizeof(Entry) * static_cast<size_t>(l.max_entries));
+    l.splits = take(sizeof(Split) * (kMaxSlots / 2));
+    l.stats = take(sizeof(float2) * kTileM * kMaxSlots);
+    l.part = take(sizeof(float) * kTileM * static_cast<size_t>(d) * kMaxSlots);
     l.total = at - kCacheScratch;
     return l;
 }
@@ -1142,9 +1208,20 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
     const Seqs seqs{a.cu_q, a.cu_k, a.Tq, a.Tk, a.B, a.Hk, g, tpt, a.causal != 0};
     uint32_t *err = reinterpret_cast<uint32_t *>(a.ws);
     PlanHeader *hdr = reinterpret_cast<PlanHeader *>(a.ws + l.hdr);
-    const PlanArgs pa{seqs, sms, l.max_slots, l.max_entries, hdr, reinterpret_cast<Entry *>(a.ws + l.entries),
-                      reinterpret_cast<Split *>(a.ws + l.splits), reinterpret_cast<int32_t *>(a.ws + l.rank),
-                      reinterpret_cast<int32_t *>(a.ws + l.at), err};
+    PlanArgs pa;
+    pa.s = seqs;
+    pa.ctas = sms;
+    pa.max_items = l.max_items;
+    pa.max_entries = l.max_entries;
+    pa.hdr = hdr;
+    pa.rank = reinterpret_cast<int32_t *>(a.ws + l.rank);
+    pa.item0 = reinterpret_cast<int32_t *>(a.ws + l.item0);
+    pa.step0 = reinterpret_cast<long long *>(a.ws + l.step0);
+    pa.item_step0 = reinterpret_cast<int32_t *>(a.ws + l.item_step0);
+    pa.first = reinterpret_cast<int32_t *>(a.ws + l.first);
+    pa.entries = reinterpret_cast<Entry *>(a.ws + l.entries);
+    pa.splits = reinterpret_cast<Split *>(a.ws + l.splits);
+    pa.err = err;
     plan_kernel<<<1, kPlanThreads, 0, st>>>(pa);
     if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     Params p;
@@ -1154,9 +1231,12 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
     p.v = a.v;
     p.lse = a.lse;
     p.hdr = hdr;
+    p.rank = pa.rank;
+    p.item0 = pa.item0;
+    p.first = pa.first;
     p.entries = pa.entries;
     p.part_o = reinterpret_cast<float *>(a.ws + l.part);
-    p.part_stats = reinterpret_cast<float4 *>(a.ws + l.stats);
+    p.part_stats = reinterpret_cast<float2 *>(a.ws + l.stats);
     p.err = err;
     p.wait_limit_ns = a.wait_limit_ns;
     p.stall = (a.dbg_flags & kDbgStall) != 0u;
