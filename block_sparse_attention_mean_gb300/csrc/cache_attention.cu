@@ -4,11 +4,11 @@
 // bounds the call (2 * d multiplications per byte-pair and head are far below the tensor cores' rate), so the
 // kernel is built around keeping loads in flight everywhere at once.
 //
-//   * The tokens of all sequences and key heads form one row of units of 64 tokens, which is cut evenly over the
+//   * The tokens of all sequences and key heads form one row of units of 64 or 128 tokens, which is cut evenly over the
 //     resident CTAs, whatever the lengths. Where a cut falls inside a (sequence, key head), its pieces leave partial
 //     results (O, max, sums) in the workspace and the CTA that finishes last joins them in the order of the tokens:
 //     in groups of kGroup, then over the groups, so that no CTA reads many.
-//   * Each of a CTA's four warps takes 16 tokens of a unit through a ring of its own in shared memory, filled with
+//   * Each of a CTA's four warps takes 16 or 32 tokens of a unit through a ring of its own in shared memory, filled with
 //     16-byte cp.async far ahead and across the ends of sequences. Warps meet only at the end of a (sequence, head).
 //   * The products run on mma.sync.m16n8k16 with the 16 tokens (then 16 channels) as rows and 8 query heads as
 //     columns, S^T = K Q^T and O^T = V^T P^T: 8 heads fill the narrow side, as many as share a key head in practice, and the
@@ -32,9 +32,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;              // tokens of a warp at a time
-constexpr int kUnit = kWarps * kTile;  // tokens of a unit
-constexpr int kGroup = 16;             // partial results that one CTA joins at a time
+constexpr int kGroup = 8;              // partial results that one CTA joins at a time
+constexpr int kMaxJoin = (kCacheMaxCtas + kGroup - 1) / kGroup;  // groups of one (sequence, key head), at most
+static_assert(kMaxJoin >= kGroup, "room for a group's weights");
 constexpr int kSlotHeads = 16;         // query heads of a partial result
 constexpr float kRaise = 8.0f;         // log2 of how far a score may pass the running maximum
 
@@ -56,13 +56,17 @@ template <int D, bool E4M3>
 struct Ring {
     static constexpr int kRow = E4M3 ? D : 2 * D;  // bytes of a row
     static constexpr int kChunks = kRow / 16;
+    // Tokens of a warp at a time: 32 where two rings of three stages fit an SM. The chain of one tile (page, loads, products,
+    // maxima) costs about the same for 16.
+    static constexpr int kTile = kRow <= 128 ? 32 : 16;
+    static constexpr int kUnit = kWarps * kTile;   // tokens of a unit
     static constexpr int kData = kTile * kRow;     // K of a tile, or V
-    static constexpr int kStage = 2 * kData + (E4M3 ? 32 : 0);
-    static constexpr int kStages = 24576 / (2 * kData) > 8 ? 8 : 24576 / (2 * kData);
+    static constexpr int kStage = 2 * kData + (E4M3 ? 2 * kTile : 0);
+    static constexpr int kStages = 24576 / (2 * kData) > 6 ? 6 : 24576 / (2 * kData);
     static constexpr int kWarpBytes = kStages * kStage;
     static constexpr int kPad = D + 4;             // floats between heads where warps join
     static constexpr int kJoin = kWarps * kWarpBytes;
-    static constexpr int kBytes = kJoin + 8 * kPad * 4;
+    static constexpr int kBytes = kJoin + 2 * 8 * kPad * 4;
     // 16-byte chunk ch of row r lies at chunk swizzle(ch, r): without it the readers' rows share banks
     static __device__ __forceinline__ int k_swizzle(int ch, int r) { return E4M3 ? (D == 128 ? ch ^ ((r & 1) << 2) : ch) : ch ^ (r & 7); }
     static __device__ __forceinline__ int v_swizzle(int ch, int r)
@@ -148,6 +152,7 @@ __device__ __forceinline__ int valid_len(const Params &p, int b)
 }
 
 // A place among the units: unit `tile` of (sequence b, chunk of heads hu)
+template <int kUnit>
 struct Place {
     int b, hu, tile, len;
     __device__ __forceinline__ int tiles() const { return (len + kUnit - 1) / kUnit; }
@@ -179,29 +184,74 @@ struct Joined {
     float m, l, lp;
 };
 
-// The partial results 0, step, 2 step, ... (count of them) of the parts that begin at CTA c0, for one head and 8 channels
+// Weights and sums of the partial results 0, step, 2 step, ... (count of them) of the parts that begin at CTA c0, left in
+// shared memory for join_parts. All threads.
+struct Weights {
+    float w[kMaxJoin][kSlotHeads];
+    float m[kSlotHeads], l[kSlotHeads], lp[kSlotHeads];
+};
+__device__ __forceinline__ void weigh_parts(const Params &p, Weights &ws, int c0, int first, int step, int count, int heads)
+{
+    // eight threads a head, which take every eighth part
+    static_assert(kThreads == 8 * kSlotHeads, "a thread's head and parts");
+    constexpr int kEach = (kMaxJoin + 7) / 8;
+    const int head = threadIdx.x / 8, j = threadIdx.x % 8;
+    float4 s[kEach];
+    float m = -CUDART_INF_F, l = 0.0f, lp = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int i = k * 8 + j;
+        s[k] = make_float4(-CUDART_INF_F, 0.0f, 0.0f, 0.0f);
+        if (i < count && head < heads) s[k] = __ldcg(p.part_s + slot_of(c0, first + i * step) * kSlotHeads + head);
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) m = fmaxf(m, s[k].x);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float base = m == -CUDART_INF_F ? 0.0f : m;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int i = k * 8 + j;
+        if (i >= count || head >= heads) continue;
+        const float w = ex2_approx(s[k].x - base);
+        ws.w[i][head] = w;
+        l += w * s[k].y;
+        lp += w * s[k].z;
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        lp += __shfl_xor_sync(0xFFFFFFFFu, lp, o);
+    }
+    if (j == 0) ws.m[head] = m, ws.l[head] = l, ws.lp[head] = lp;
+    __syncthreads();
+}
+
+// ... and their sum for one head and 8 channels
 template <int D>
-__device__ __forceinline__ Joined join_parts(const Params &p, int c0, int first, int step, int count, int head, int ch)
+__device__ __forceinline__ Joined join_parts(const Params &p, const Weights &ws, int c0, int first, int step, int count, int head, int ch)
 {
     Joined r;
-    r.m = -CUDART_INF_F;
-    for (int i = 0; i < count; ++i)
-        r.m = fmaxf(r.m, __ldcg(p.part_s + slot_of(c0, first + i * step) * kSlotHeads + head).x);
-    r.l = r.lp = 0.0f;
+    r.m = ws.m[head], r.l = ws.l[head], r.lp = ws.lp[head];
 #pragma unroll
     for (int k = 0; k < 8; ++k) r.o[k] = 0.0f;
-    const float base = r.m == -CUDART_INF_F ? 0.0f : r.m;
-#pragma unroll 4
-    for (int i = 0; i < count; ++i) {
-        const size_t row = slot_of(c0, first + i * step) * kSlotHeads + head;
-        const float4 s = __ldcg(p.part_s + row);
-        const float4 *src = reinterpret_cast<const float4 *>(p.part_o + row * D + ch);
-        const float4 a = __ldcg(src), b = __ldcg(src + 1);
-        const float w = ex2_approx(s.x - base);
-        r.l += w * s.y;
-        r.lp += w * s.z;
-        r.o[0] += w * a.x, r.o[1] += w * a.y, r.o[2] += w * a.z, r.o[3] += w * a.w;
-        r.o[4] += w * b.x, r.o[5] += w * b.y, r.o[6] += w * b.z, r.o[7] += w * b.w;
+    for (int i0 = 0; i0 < count; i0 += 8) {
+        float4 a[8], b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            a[k] = b[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i0 + k >= count) continue;
+            const float4 *src = reinterpret_cast<const float4 *>(
+                p.part_o + (slot_of(c0, first + (i0 + k) * step) * kSlotHeads + head) * D + ch);
+            a[k] = __ldcg(src), b[k] = __ldcg(src + 1);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (i0 + k >= count) continue;
+            const float w = ws.w[i0 + k][head];
+            r.o[0] += w * a[k].x, r.o[1] += w * a[k].y, r.o[2] += w * a[k].z, r.o[3] += w * a[k].w;
+            r.o[4] += w * b[k].x, r.o[5] += w * b[k].y, r.o[6] += w * b[k].z, r.o[7] += w * b[k].w;
+        }
     }
     return r;
 }
@@ -224,12 +274,14 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
 {
     using R = Ring<D, E4M3>;
     constexpr int KS = D / 16;  // steps of 16 channels
+    constexpr int kTile = R::kTile, kUnit = R::kUnit, kHalves = kTile / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scan[kWarps];
     __shared__ int64_t found_rel;
     __shared__ int found_b;
     __shared__ float st_m[kWarps][8 * NH], st_l[kWarps][8 * NH], st_lp[kWarps][8 * NH];
     __shared__ uint32_t arrived;
+    __shared__ Weights weights;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, j = lane & 3;
     const int cta = blockIdx.x;
@@ -281,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
         }
     }
     __syncthreads();
-    Place here;
+    Place<kUnit> here;
     here.b = found_b;
     here.len = valid_len(p, here.b);
     here.hu = static_cast<int>(found_rel / here.tiles());
@@ -289,39 +341,45 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
 
     // ---- the warp's ring: `ahead` runs kStages - 1 units in front of `here`
     const uint32_t ring = smem_u32(smem) + warp * R::kWarpBytes;
-    Place ahead = here;
+    Place<kUnit> ahead = here;
     int64_t issued = u_lo;  // next unit to load
     const int page_mask = (1 << p.cache.page_shift) - 1;
-    auto page_of = [&](const Place &w) -> int {
-        const int tok = w.tile * kUnit + warp * kTile;
-        if (tok >= w.len) return 0;
+    auto page_of = [&](const Place<kUnit> &w, int half) -> int {
+        const int tok = w.tile * kUnit + warp * kTile + half * 16;
+        if (tok >= w.len) return 0;  // no page is looked up; its rows become zeros
         return __ldg(p.table.pages + w.b * p.table.stride + (tok >> p.cache.page_shift));
     };
-    int page = page_of(ahead);
+    int page[kHalves];  // a tile of 32 tokens may lie in two pages of 16
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) page[h] = page_of(ahead, h);
     auto load = [&](int stage) {
         if (issued < u_hi) {
             const int tok = ahead.tile * kUnit + warp * kTile;
             const int left = ahead.len - tok;  // tokens of the tile that exist
-            if (left > 0) {
-                bool ok = page >= 0 && page < p.cache.n_pages;
+            const int kh = ahead.hu / p.chunks;
+            const uint32_t at = ring + stage * R::kStage;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                const bool ok = page[h] >= 0 && page[h] < p.cache.n_pages;
                 if (!ok) raise_error(p.err, BSA_ERR_INVALID_ARG);
-                const int kh = ahead.hu / p.chunks;
-                const int64_t row = ok ? ((static_cast<int64_t>(page) * p.cache.heads + kh) << p.cache.page_shift) + (tok & page_mask) : 0;
+                const int64_t row =
+                    ok ? ((static_cast<int64_t>(page[h]) * p.cache.heads + kh) << p.cache.page_shift) + ((tok + h * 16) & page_mask) : 0;
                 const char *ks = p.cache.k + row * R::kRow, *vs = p.cache.v + row * R::kRow;
-                const uint32_t at = ring + stage * R::kStage;
 #pragma unroll
                 for (int i = 0; i < R::kChunks / 2; ++i) {
-                    const int idx = i * 32 + lane, rr = idx / R::kChunks, ch = idx % R::kChunks;
+                    const int idx = i * 32 + lane, rr = idx / R::kChunks + h * 16, ch = idx % R::kChunks;
                     const uint32_t bytes = ok && rr < left ? 16u : 0u;  // rows that do not exist become zeros
                     cp_async16(at + rr * R::kRow + R::k_swizzle(ch, rr) * 16, ks + idx * 16, bytes);
                     cp_async16(at + R::kData + rr * R::kRow + R::v_swizzle(ch, rr) * 16, vs + idx * 16, bytes);
                 }
                 if constexpr (E4M3)
-                    if (lane < 2) cp_async16(at + 2 * R::kData + lane * 16, (lane ? p.cache.v_exp : p.cache.k_exp) + row, ok ? 16u : 0u);
+                    if (lane < 2)
+                        cp_async16(at + 2 * R::kData + lane * kTile + h * 16, (lane ? p.cache.v_exp : p.cache.k_exp) + row, ok ? 16u : 0u);
             }
             if (++issued < u_hi) {
                 ahead.next(p);
-                page = page_of(ahead);
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) page[h] = page_of(ahead, h);
             }
         }
         cp_async_commit();
@@ -399,129 +457,150 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
             const int left = here.len - tile * kUnit - warp * kTile;
             if (left > 0) {
                 const uint32_t ka = ring + stage * R::kStage, va = ka + R::kData;
-                float s[NH][2][4];  // S^T, two sums of every other step: rows are tokens, columns heads
+                float s[kHalves][NH][4];  // S^T: rows are tokens, columns heads
 #pragma unroll
-                for (int n = 0; n < NH; ++n)
+                for (int h = 0; h < kHalves; ++h) {
+                    float s2[NH][2][4];  // two sums, of every other step
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) s[n][0][k] = s[n][1][k] = 0.0f;
-                if constexpr (E4M3) {
+                    for (int n = 0; n < NH; ++n)
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        const uint4 lo = lds128(ka + r * R::kRow + R::k_swizzle(j + 4 * c, r) * 16);
-                        const uint4 hi = lds128(ka + (r + 8) * R::kRow + R::k_swizzle(j + 4 * c, r + 8) * 16);
-                        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+                        for (int k = 0; k < 4; ++k) s2[n][0][k] = s2[n][1][k] = 0.0f;
+                    if constexpr (E4M3) {
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const uint32_t a[4] = {half2_lo(wl[t]), half2_lo(wh[t]), half2_hi(wl[t]), half2_hi(wh[t])};
+                        for (int c = 0; c < D / 64; ++c) {
+                            const int r0 = h * 16 + r;
+                            const uint4 lo = lds128(ka + r0 * R::kRow + R::k_swizzle(j + 4 * c, r0) * 16);
+                            const uint4 hi = lds128(ka + (r0 + 8) * R::kRow + R::k_swizzle(j + 4 * c, r0 + 8) * 16);
+                            const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-                            for (int n = 0; n < NH; ++n) mma16816<true>(s[n][t & 1], a, qf[n][4 * c + t][0], qf[n][4 * c + t][1]);
+                            for (int t = 0; t < 4; ++t) {
+                                const uint32_t a[4] = {half2_lo(wl[t]), half2_lo(wh[t]), half2_hi(wl[t]), half2_hi(wh[t])};
+#pragma unroll
+                                for (int n = 0; n < NH; ++n) mma16816<true>(s2[n][t & 1], a, qf[n][4 * c + t][0], qf[n][4 * c + t][1]);
+                            }
+                        }
+                    } else {
+                        const int row = h * 16 + (lane & 15);
+#pragma unroll
+                        for (int t = 0; t < KS; ++t) {
+                            uint32_t a[4];
+                            ldmatrix4(a, ka + row * R::kRow + R::k_swizzle(2 * t + (lane >> 4), row) * 16);
+#pragma unroll
+                            for (int n = 0; n < NH; ++n) mma16816<false>(s2[n][t & 1], a, qf[n][t][0], qf[n][t][1]);
                         }
                     }
-                } else {
 #pragma unroll
-                    for (int t = 0; t < KS; ++t) {
-                        uint32_t a[4];
-                        ldmatrix4(a, ka + (lane & 15) * R::kRow + R::k_swizzle(2 * t + (lane >> 4), lane & 15) * 16);
+                    for (int n = 0; n < NH; ++n)
 #pragma unroll
-                        for (int n = 0; n < NH; ++n) mma16816<false>(s[n][t & 1], a, qf[n][t][0], qf[n][t][1]);
-                    }
+                        for (int k = 0; k < 4; ++k) s[h][n][k] = s2[n][0][k] + s2[n][1][k];
                 }
-                // weights: log2 of them in x, of tokens r and r + 8
-                const bool in0 = r < left, in1 = r + 8 < left;
-                float k0 = 1.0f, k1 = 1.0f, e0 = 0.0f, e1 = 0.0f, d0 = 1.0f, d1 = 1.0f;
-                if constexpr (E4M3) {
-                    const uint32_t ea = ka + 2 * R::kData;
-                    const uint32_t b0 = lds8(ea + r), b1 = lds8(ea + r + 8), c0 = lds8(ea + 16 + r), c1 = lds8(ea + 24 + r);
-                    k0 = __uint_as_float(b0 << 23), k1 = __uint_as_float(b1 << 23);
-                    e0 = static_cast<float>(static_cast<int>(c0) - 127), e1 = static_cast<float>(static_cast<int>(c1) - 127);
-                    d0 = __uint_as_float((254u - min(c0, 253u)) << 23), d1 = __uint_as_float((254u - min(c1, 253u)) << 23);
-                }
+                // log2 of the weights, of tokens r and r + 8 of each half
+                float d[kHalves][2];  // 2^-e of the values
                 bool pass = false;
 #pragma unroll
-                for (int n = 0; n < NH; ++n)
+                for (int h = 0; h < kHalves; ++h) {
+                    const bool in[2] = {h * 16 + r < left, h * 16 + r + 8 < left};
+                    float ke[2] = {1.0f, 1.0f}, ve[2] = {0.0f, 0.0f};
+                    if constexpr (E4M3) {
+                        const uint32_t ea = ka + 2 * R::kData + h * 16 + r;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float x = s[n][0][k] + s[n][1][k];
-                        if constexpr (E4M3) x = fmaf(x, qs[n][k & 1] * (k < 2 ? k0 : k1), k < 2 ? e0 : e1);
-                        else x *= qs[n][k & 1];
-                        x = (k < 2 ? in0 : in1) ? x : -CUDART_INF_F;
-                        s[n][0][k] = x;
-                        pass |= x > m[n][k & 1] + kRaise;
+                        for (int t = 0; t < 2; ++t) {
+                            const uint32_t kb = lds8(ea + 8 * t), vb = lds8(ea + kTile + 8 * t);
+                            ke[t] = __uint_as_float(kb << 23);
+                            ve[t] = static_cast<float>(static_cast<int>(vb) - 127);
+                            d[h][t] = __uint_as_float((254u - min(vb, 253u)) << 23);
+                        }
                     }
+#pragma unroll
+                    for (int n = 0; n < NH; ++n)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float x = s[h][n][k];
+                            if constexpr (E4M3) x = fmaf(x, qs[n][k & 1] * ke[k >> 1], ve[k >> 1]);
+                            else x *= qs[n][k & 1];
+                            x = in[k >> 1] ? x : -CUDART_INF_F;
+                            s[h][n][k] = x;
+                            pass |= x > m[n][k & 1] + kRaise;
+                        }
+                }
                 if (__any_sync(0xFFFFFFFFu, pass)) {
 #pragma unroll
                     for (int n = 0; n < NH; ++n)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float x = fmaxf(s[n][0][h], s[n][0][2 + h]);
+                        for (int c = 0; c < 2; ++c) {
+                            float x = m[n][c];
+#pragma unroll
+                            for (int h = 0; h < kHalves; ++h) x = fmax3(x, s[h][n][c], s[h][n][2 + c]);
 #pragma unroll
                             for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
-                            x = fmaxf(x, m[n][h]);
-                            const float a = x == -CUDART_INF_F ? 1.0f : ex2_approx(m[n][h] - x);
-                            m[n][h] = x;
-                            l[n][h] *= a;
-                            lp[n][h] *= a;
+                            const float a = x == m[n][c] ? 1.0f : ex2_approx(m[n][c] - x);
+                            m[n][c] = x;
+                            l[n][c] *= a;
+                            lp[n][c] *= a;
 #pragma unroll
-                            for (int t = 0; t < KS; ++t) o[t][n][h] *= a, o[t][n][2 + h] *= a;
+                            for (int t = 0; t < KS; ++t) o[t][n][c] *= a, o[t][n][2 + c] *= a;
                         }
                 }
-                uint32_t pf[NH][2];
 #pragma unroll
-                for (int n = 0; n < NH; ++n) {
-                    float w[4];
+                for (int h = 0; h < kHalves; ++h) {
+                    uint32_t pf[NH][2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float base = m[n][k & 1] == -CUDART_INF_F ? 0.0f : m[n][k & 1];
-                        w[k] = ex2_approx(s[n][0][k] - base);
-                        if constexpr (E4M3) l[n][k & 1] = fmaf(w[k], k < 2 ? d0 : d1, l[n][k & 1]);
-                        else l[n][k & 1] += w[k];
+                    for (int n = 0; n < NH; ++n) {
+                        float w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float base = m[n][k & 1] == -CUDART_INF_F ? 0.0f : m[n][k & 1];
+                            w[k] = ex2_approx(s[h][n][k] - base);
+                            if constexpr (E4M3) l[n][k & 1] = fmaf(w[k], d[h][k >> 1], l[n][k & 1]);
+                            else l[n][k & 1] += w[k];
+                        }
+                        if constexpr (E4M3) {
+                            pf[n][0] = pack_half2(w[0], w[1]);
+                            pf[n][1] = pack_half2(w[2], w[3]);
+                        } else {
+                            pf[n][0] = pack_bf16x2(w[0], w[1]);
+                            pf[n][1] = pack_bf16x2(w[2], w[3]);
+                            add_bf16x2_to_f32(lp[n][0], lp[n][1], pf[n][0]);
+                            add_bf16x2_to_f32(lp[n][0], lp[n][1], pf[n][1]);
+                        }
+                        pf[n][0] = transpose8x8(pf[n][0]);
+                        pf[n][1] = transpose8x8(pf[n][1]);
                     }
                     if constexpr (E4M3) {
-                        pf[n][0] = pack_half2(w[0], w[1]);
-                        pf[n][1] = pack_half2(w[2], w[3]);
+                        // thread r has channels [r * D / 8, (r + 1) * D / 8) of tokens 2j, 2j + 1, 2j + 8, 2j + 9
+                        uint32_t w[4][D / 32];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int row = h * 16 + 2 * j + (k & 1) + 8 * (k >> 1);
+                            if constexpr (D == 128) {
+                                const uint4 v = lds128(va + row * R::kRow + R::v_swizzle(r, row) * 16);
+                                w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
+                            } else {
+                                const uint2 v = lds64(va + row * R::kRow + R::v_swizzle(r >> 1, row) * 16 + (r & 1) * 8);
+                                w[k][0] = v.x, w[k][1] = v.y;
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < D / 32; ++q) {
+                            const uint32_t a01 = __byte_perm(w[0][q], w[1][q], 0x5140), a23 = __byte_perm(w[0][q], w[1][q], 0x7362);
+                            const uint32_t b01 = __byte_perm(w[2][q], w[3][q], 0x5140), b23 = __byte_perm(w[2][q], w[3][q], 0x7362);
+                            const uint32_t t0[4] = {half2_lo(a01), half2_hi(a01), half2_lo(b01), half2_hi(b01)};
+                            const uint32_t t1[4] = {half2_lo(a23), half2_hi(a23), half2_lo(b23), half2_hi(b23)};
+#pragma unroll
+                            for (int n = 0; n < NH; ++n) {
+                                mma16816<true>(o[2 * q][n], t0, pf[n][0], pf[n][1]);
+                                mma16816<true>(o[2 * q + 1][n], t1, pf[n][0], pf[n][1]);
+                            }
+                        }
                     } else {
-                        pf[n][0] = pack_bf16x2(w[0], w[1]);
-                        pf[n][1] = pack_bf16x2(w[2], w[3]);
-                        add_bf16x2_to_f32(lp[n][0], lp[n][1], pf[n][0]);
-                        add_bf16x2_to_f32(lp[n][0], lp[n][1], pf[n][1]);
-                    }
-                    pf[n][0] = transpose8x8(pf[n][0]);
-                    pf[n][1] = transpose8x8(pf[n][1]);
-                }
-                if constexpr (E4M3) {
-                    // thread r has channels [r * D / 8, (r + 1) * D / 8) of tokens 2j, 2j + 1, 2j + 8, 2j + 9
-                    uint32_t w[4][D / 32];
+                        const int row = h * 16 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int row = 2 * j + (k & 1) + 8 * (k >> 1);
-                        if constexpr (D == 128) {
-                            const uint4 v = lds128(va + row * R::kRow + R::v_swizzle(r, row) * 16);
-                            w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
-                        } else {
-                            const uint2 v = lds64(va + row * R::kRow + R::v_swizzle(r >> 1, row) * 16 + (r & 1) * 8);
-                            w[k][0] = v.x, w[k][1] = v.y;
+                        for (int t = 0; t < KS; ++t) {
+                            uint32_t a[4];
+                            ldmatrix4_trans(a, va + row * R::kRow + R::v_swizzle(2 * t + ((lane >> 3) & 1), row) * 16);
+#pragma unroll
+                            for (int n = 0; n < NH; ++n) mma16816<false>(o[t][n], a, pf[n][0], pf[n][1]);
                         }
-                    }
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        const uint32_t a01 = __byte_perm(w[0][q], w[1][q], 0x5140), a23 = __byte_perm(w[0][q], w[1][q], 0x7362);
-                        const uint32_t b01 = __byte_perm(w[2][q], w[3][q], 0x5140), b23 = __byte_perm(w[2][q], w[3][q], 0x7362);
-                        const uint32_t t0[4] = {half2_lo(a01), half2_hi(a01), half2_lo(b01), half2_hi(b01)};
-                        const uint32_t t1[4] = {half2_lo(a23), half2_hi(a23), half2_lo(b23), half2_hi(b23)};
-#pragma unroll
-                        for (int n = 0; n < NH; ++n) {
-                            mma16816<true>(o[2 * q][n], t0, pf[n][0], pf[n][1]);
-                            mma16816<true>(o[2 * q + 1][n], t1, pf[n][0], pf[n][1]);
-                        }
-                    }
-                } else {
-                    const int row = (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-                    for (int t = 0; t < KS; ++t) {
-                        uint32_t a[4];
-                        ldmatrix4_trans(a, va + row * R::kRow + R::v_swizzle(2 * t + ((lane >> 3) & 1), row) * 16);
-#pragma unroll
-                        for (int n = 0; n < NH; ++n) mma16816<false>(o[t][n], a, pf[n][0], pf[n][1]);
                     }
                 }
             }
@@ -560,14 +639,14 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                 const float M = fmaxf(fmaxf(st_m[0][c], st_m[1][c]), fmaxf(st_m[2][c], st_m[3][c]));
                 wt[h] = M == -CUDART_INF_F ? 0.0f : ex2_approx(m[n][h] - M);
             }
-            for (int w = 0; w < kWarps; ++w) {  // in turn, so that the sum has one order
-                if (w == warp) {
+            for (int w = 0; w < 2; ++w) {  // warps 0 and 1, then 2 and 3 into their buffers: the sum has one order
+                if (w == warp >> 1) {
 #pragma unroll
                     for (int t = 0; t < KS; ++t)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int ch = E4M3 ? r * (D / 8) + 2 * t + (k >> 1) : 16 * t + r + 8 * (k >> 1);
-                            float *at = join + (2 * j + (k & 1)) * R::kPad + ch;
+                            float *at = join + ((warp & 1) * 8 + 2 * j + (k & 1)) * R::kPad + ch;
                             const float x = o[t][n][k] * wt[k & 1];
                             *at = w == 0 ? x : *at + x;
                         }
@@ -587,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                     res.lp += a * st_lp[w][c];
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) res.o[k] = join[hd * R::kPad + ch + k];
+                for (int k = 0; k < 8; ++k) res.o[k] = join[hd * R::kPad + ch + k] + join[(8 + hd) * R::kPad + ch + k];
                 if (is_whole) {
                     write_result(p, here.b, kh * p.g + head0 + c, ch, res);
                 } else {
@@ -607,27 +686,28 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
             const int group = part / kGroup, groups = (parts + kGroup - 1) / kGroup;
             const int members = min(kGroup, parts - group * kGroup);
             auto last_of = [&](uint32_t *ticket, int count) -> bool {
-                __threadfence();
-                __syncthreads();
+                __syncthreads();  // the CTA's results are written; one thread's fences stand for all
                 if (tid == 0) {
+                    __threadfence();
                     const uint32_t before_me = atomicAdd(ticket, 1u);
                     if (before_me == static_cast<uint32_t>(count - 1)) *ticket = 0u;  // for the next call
+                    __threadfence();
                     arrived = before_me;
                 }
                 __syncthreads();
                 const bool last = arrived == static_cast<uint32_t>(count - 1);
-                __threadfence();
                 __syncthreads();  // `arrived` may be written again
                 return last;
             };
             const int heads = min(8 * NH, p.g - head0);
             if (last_of(p.tickets + (group == 0 ? 0 : kCacheMaxCtas) + c0 + group * kGroup, members)) {
-                bool final_join = groups == 1;
+                const bool final_join = groups == 1;
+                weigh_parts(p, weights, c0, group * kGroup, 1, members, heads);
                 for (int i0 = 0; i0 < heads * (D / 8); i0 += kThreads) {
                     const int i = i0 + tid, hd = i / (D / 8), ch = (i % (D / 8)) * 8;
                     const bool on = hd < heads;
                     Joined res;
-                    if (on) res = join_parts<D>(p, c0, group * kGroup, 1, members, hd, ch);
+                    if (on) res = join_parts<D>(p, weights, c0, group * kGroup, 1, members, hd, ch);
                     if (final_join) {
                         if (on) write_result(p, here.b, kh * p.g + head0 + hd, ch, res);
                         continue;
@@ -642,9 +722,10 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                     }
                 }
                 if (!final_join && last_of(p.tickets + 2 * kCacheMaxCtas + c0, groups)) {
+                    weigh_parts(p, weights, c0, 0, kGroup, groups, heads);
                     for (int i = tid; i < heads * (D / 8); i += kThreads) {
                         const int hd = i / (D / 8), ch = (i % (D / 8)) * 8;
-                        write_result(p, here.b, kh * p.g + head0 + hd, ch, join_parts<D>(p, c0, 0, kGroup, groups, hd, ch));
+                        write_result(p, here.b, kh * p.g + head0 + hd, ch, join_parts<D>(p, weights, c0, 0, kGroup, groups, hd, ch));
                     }
                 }
             }
@@ -662,7 +743,7 @@ bsa_status launch(const CacheAttentionArgs &a, cudaStream_t st)
 {
     using R = Ring<D, E4M3>;
     auto kern = cache_attention_kernel<D, E4M3, NH>;
-    static_assert(2 * (R::kBytes + 2048) <= 233472, "two CTAs per SM");
+    static_assert(2 * (R::kBytes + 1024 + 6400) <= 233472, "two CTAs per SM");
     static std::atomic<uint64_t> ready{0};
     if (!allow_shared_memory(kern, R::kBytes, ready)) return BSA_ERR_CUDA;
     int sms = 0;
