@@ -18,7 +18,8 @@ import torch
 
 from . import binding
 from .binding import BF16, ERR_DTYPE, ERR_INVALID_ARG, ERR_SHAPE, BsaError, _check, _ptr, _stream
-from .block_binding import _cuda_device, _elsewhere, _run, _view, _workspace_bytes
+from .block_binding import _current_stream as _block_current_stream
+from .block_binding import _cuda_device, _elsewhere, _view
 
 CACHE_BF16 = 0
 CACHE_E4M3 = 1
@@ -113,21 +114,29 @@ def bsa_cache_workspace_size(T: int, B: int, H: int, Hk: int, d: int) -> int:
 
 # ------------------------------------------------------------------ helpers
 #
-# As in block_binding, descriptors go as bytes in the structures' layout, and messages wait for a failure.
+# As in block_binding, descriptors go as bytes in the structures' layout, and messages wait for a failure: a tensor is
+# looked at in as few calls as tell that it is right, and _view says what is wrong with it if it is not. A KvCache keeps
+# its descriptor from call to call.
 
 _CACHE = struct.Struct("4P5i4x")
 _TABLE = struct.Struct("Pq2i")
 _PACKED = struct.Struct("Pqq")
-_BF16, _INT = torch.bfloat16, torch.int32
+_BF16, _INT, _FP32 = torch.bfloat16, torch.int32, torch.float32
+_grad_enabled = torch.is_grad_enabled
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _block_current_stream
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-class KvCache(NamedTuple):
-    """Pages of keys and values: k, v [pages, key heads, page size, d], bf16, or float8_e4m3fn with the bytes k_exp, v_exp
-    [pages, key heads, page size] of their exponents: a row is data * 2 ** (exp - 127)."""
+class _KvCacheFields(NamedTuple):
     k: torch.Tensor
     v: torch.Tensor
     k_exp: Optional[torch.Tensor] = None
     v_exp: Optional[torch.Tensor] = None
+
+
+class KvCache(_KvCacheFields):
+    """Pages of keys and values: k, v [pages, key heads, page size, d], bf16, or float8_e4m3fn with the bytes k_exp, v_exp
+    [pages, key heads, page size] of their exponents: a row is data * 2 ** (exp - 127)."""
 
 
 def kv_cache(n_pages: int, page_size: int, kv_heads: int, d: int, kind: str = "bf16", device="cuda") -> KvCache:
@@ -162,20 +171,29 @@ def cache_check(ws: torch.Tensor, stream=None) -> None:
 
 
 def _contiguous(t: torch.Tensor, shape, dtype, device, what: str, name: str) -> int:
-    at, _ = _view(t, shape, dtype, device, what, name)
-    if not t.is_contiguous():
+    """Address of a contiguous tensor of this shape, dtype and device."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
+        _view(t, shape, dtype, device, what, name)
         raise BsaError(ERR_INVALID_ARG, f"{what}: {name} must be contiguous")
-    return at
+    return t.data_ptr()
 
 
 def _packed(t: torch.Tensor, shape, device, what: str, name: str) -> bytes:
+    """bsa_packed of a bf16 tensor of this shape and device, channels contiguous."""
+    s = t.stride()
+    if t.dtype is _BF16 and t.shape == shape and s[2] == 1 and t.device == device and not (t.requires_grad and _grad_enabled()):
+        return _PACKED.pack(t.data_ptr(), s[0], s[1])
     at, s = _view(t, shape, _BF16, device, what, name)
     return _PACKED.pack(at, s[0], s[1])
 
 
 def _cache_args(cache: KvCache, what: str):
-    """(descriptor, device, key heads, d)"""
+    """(descriptor, device, key heads, d), kept with the cache while its tensors stay where they are"""
+    kept = getattr(cache, "_kept", None)
     k, v, k_exp, v_exp = cache
+    if (kept is not None and kept[4] == k.data_ptr() and kept[5] == v.data_ptr() and
+            not ((k.requires_grad or v.requires_grad) and _grad_enabled())):
+        return kept
     device = _cuda_device(k, what)
     if k.dim() != 4:
         raise BsaError(ERR_SHAPE, f"{what}: a cache of {k.dim()} dimensions, expected 4")
@@ -193,23 +211,40 @@ def _cache_args(cache: KvCache, what: str):
     else:
         raise BsaError(ERR_DTYPE, f"{what}: cache dtype {dtype}")
     n_pages, heads, page_size, d = shape
-    return (_CACHE.pack(_contiguous(k, shape, dtype, device, what, "cache k"),
-                        _contiguous(v, shape, dtype, device, what, "cache v"), ke, ve, kind, n_pages, page_size, heads, d),
-            device, heads, d)
+    for t, name in ((k, "cache k"), (v, "cache v")):
+        _view(t, shape, dtype, device, what, name)
+    at = _contiguous(k, shape, dtype, device, what, "cache k"), _contiguous(v, shape, dtype, device, what, "cache v")
+    kept = (_CACHE.pack(*at, ke, ve, kind, n_pages, page_size, heads, d), device, heads, d, *at)
+    if isinstance(cache, KvCache):
+        cache._kept = kept
+    return kept
 
 
 def _table_args(table: torch.Tensor, device, what: str):
     """(descriptor, B)"""
-    if table.dim() != 2:
-        raise BsaError(ERR_SHAPE, f"{what}: a page table of {table.dim()} dimensions, expected 2")
-    at, s = _view(table, table.shape, _INT, device, what, "table")
-    B, width = table.shape
-    return _TABLE.pack(at, s[0], B, width), B
+    shape = table.shape
+    if len(shape) != 2:
+        raise BsaError(ERR_SHAPE, f"{what}: a page table of {len(shape)} dimensions, expected 2")
+    s = table.stride()
+    if not (table.dtype is _INT and s[1] == 1 and table.device == device):
+        _view(table, shape, _INT, device, what, "table")
+    return _TABLE.pack(table.data_ptr(), s[0], *shape), shape[0]
 
 
-def _finish(ws: torch.Tensor, check: bool, what: str) -> None:
+def _call(what: str, fn, device: torch.device, ws: torch.Tensor, check: bool, *args) -> None:
+    """fn(*args, the workspace and its bytes, the device's current stream) with `device` current."""
+    if not (ws.device == device and ws.is_contiguous()):
+        raise BsaError(ERR_INVALID_ARG, f"{what}: the workspace must be contiguous and on {device}")
+    index = device.index
+    stream = _current_stream(index)
+    if index == _current_device():
+        code = fn(*args, ws.data_ptr(), ws.nbytes, stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, ws.data_ptr(), ws.nbytes, stream)
+    _check(code, what)
     if check:
-        with torch.cuda.device(ws.device):
+        with torch.cuda.device(device):
             _check(binding.bsa_check_device_error(ws), what + " (device)")
 
 
@@ -222,17 +257,15 @@ def cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     if stream is not None and (there := _elsewhere(stream, k, what)):
         with there:
             return cache_write(cache, k, v, table, kv_lens, cu, ws=ws, check=check)
-    desc, device, heads, d = _cache_args(cache, what)
+    desc, device, heads, d, _, _ = _cache_args(cache, what)
     pages, B = _table_args(table, device, what)
     shape = (k.shape[0], heads, d)
     if ws is None:
         ws = _rows_workspace(device)
-    _run("bsa_cache_write", load().bsa_cache_write, device, desc, _packed(k, shape, device, what, "k"),
-         _packed(v, shape, device, what, "v"), BF16, shape[0], pages,
-         _contiguous(kv_lens, (B,), _INT, device, what, "kv_lens"),
-         _contiguous(cu, (B + 1,), _INT, device, what, "cu") if cu is not None else None, ws.data_ptr(),
-         _workspace_bytes(ws, device, what))
-    _finish(ws, check, what)
+    _call("bsa_cache_write", load().bsa_cache_write, device, ws, check, desc, _packed(k, shape, device, what, "k"),
+          _packed(v, shape, device, what, "v"), BF16, shape[0], pages,
+          _contiguous(kv_lens, (B,), _INT, device, what, "kv_lens"),
+          _contiguous(cu, (B + 1,), _INT, device, what, "cu") if cu is not None else None)
 
 
 def cache_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, tokens: Optional[int] = None, *,
@@ -244,7 +277,7 @@ def cache_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, tokens: Op
     if stream is not None and (there := _elsewhere(stream, cache.k, what)):
         with there:
             return cache_read(cache, table, cu, tokens, out=out, ws=ws, check=check)
-    desc, device, heads, d = _cache_args(cache, what)
+    desc, device, heads, d, _, _ = _cache_args(cache, what)
     pages, B = _table_args(table, device, what)
     if out is None:
         if tokens is None:
@@ -254,10 +287,9 @@ def cache_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, tokens: Op
     shape = (k.shape[0] if tokens is None else tokens, heads, d)
     if ws is None:
         ws = _rows_workspace(device)
-    _run("bsa_cache_read", load().bsa_cache_read, device, desc, pages,
-         _contiguous(cu, (B + 1,), _INT, device, what, "cu"), _packed(k, shape, device, what, "out k"),
-         _packed(v, shape, device, what, "out v"), BF16, shape[0], ws.data_ptr(), _workspace_bytes(ws, device, what))
-    _finish(ws, check, what)
+    _call("bsa_cache_read", load().bsa_cache_read, device, ws, check, desc, pages,
+          _contiguous(cu, (B + 1,), _INT, device, what, "cu"), _packed(k, shape, device, what, "out k"),
+          _packed(v, shape, device, what, "out v"), BF16, shape[0])
     return k, v
 
 
@@ -270,7 +302,7 @@ def cache_attention(q: torch.Tensor, cache: KvCache, table: torch.Tensor, kv_len
     if stream is not None and (there := _elsewhere(stream, q, what)):
         with there:
             return cache_attention(q, cache, table, kv_lens, scale, out=out, lse=lse, ws=ws, check=check)
-    desc, device, heads, d = _cache_args(cache, what)
+    desc, device, heads, d, _, _ = _cache_args(cache, what)
     pages, B = _table_args(table, device, what)
     if q.dim() != 3:
         raise BsaError(ERR_SHAPE, f"{what}: q has {q.dim()} dimensions, expected 3")
@@ -279,13 +311,12 @@ def cache_attention(q: torch.Tensor, cache: KvCache, table: torch.Tensor, kv_len
     if out is None:
         out = torch.empty(shape, dtype=_BF16, device=device)
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=device)
+        lse = torch.empty((B, H), dtype=_FP32, device=device)
     if ws is None:
         ws = cache_workspace(1, 1, heads, heads, d, device)
-    _run("bsa_cache_attention", load().bsa_cache_attention, device, desc, _packed(q, shape, device, what, "q"), BF16, H,
-         pages, _contiguous(kv_lens, (B,), _INT, device, what, "kv_lens"), scale, _packed(out, shape, device, what, "out"),
-         _contiguous(lse, (B, H), torch.float32, device, what, "lse"), ws.data_ptr(), _workspace_bytes(ws, device, what))
-    _finish(ws, check, what)
+    _call("bsa_cache_attention", load().bsa_cache_attention, device, ws, check, desc, _packed(q, shape, device, what, "q"), BF16,
+          H, pages, _contiguous(kv_lens, (B,), _INT, device, what, "kv_lens"), scale, _packed(out, shape, device, what, "out"),
+          _contiguous(lse, (B, H), _FP32, device, what, "lse"))
     return out, lse
 
 
@@ -312,13 +343,11 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     if out is None:
         out = torch.empty(shape, dtype=_BF16, device=device)
     if lse is None:
-        lse = torch.empty((H, T), dtype=torch.float32, device=device)
+        lse = torch.empty((H, T), dtype=_FP32, device=device)
     if ws is None:
         ws = cache_workspace(T, B, H, Hk, d, device)
-    _run("bsa_prompt_attention", load().bsa_prompt_attention, device, _packed(q, shape, device, what, "q"),
-         _packed(k, kv_shape, device, what, "k"), _packed(v, kv_shape, device, what, "v"), BF16, T, Tk, B, H, Hk, d,
-         _contiguous(cu_q, (B + 1,), _INT, device, what, "cu_q"), _contiguous(cu_k, (B + 1,), _INT, device, what, "cu_k"),
-         int(causal), scale, _packed(out, shape, device, what, "out"),
-         _contiguous(lse, (H, T), torch.float32, device, what, "lse"), ws.data_ptr(), _workspace_bytes(ws, device, what))
-    _finish(ws, check, what)
+    _call("bsa_prompt_attention", load().bsa_prompt_attention, device, ws, check, _packed(q, shape, device, what, "q"),
+          _packed(k, kv_shape, device, what, "k"), _packed(v, kv_shape, device, what, "v"), BF16, T, Tk, B, H, Hk, d,
+          _contiguous(cu_q, (B + 1,), _INT, device, what, "cu_q"), _contiguous(cu_k, (B + 1,), _INT, device, what, "cu_k"),
+          int(causal), scale, _packed(out, shape, device, what, "out"), _contiguous(lse, (H, T), _FP32, device, what, "lse"))
     return out, lse

@@ -51,6 +51,10 @@ constexpr unsigned long long kDrainNs = 1000000000ull;  // copies and products i
 
 constexpr int kMaxSlots = 320;       // partial results (a tile each): two per CTA
 constexpr int kMaxCutItems = 65536;  // items (of all key heads) up to which the steps are cut evenly
+constexpr int kCutSteps = 8;          // what a cut has to save, in steps
+// No item longer than that: the steps are never cut. With at most 32 sequences besides, the loading warps plan for themselves,
+// a lane a sequence, and the call is one launch (four sequences of 12 to 128 tokens, 24 heads of 64: MEASURED).
+constexpr int kShortKeys = kCutSteps * kStep;
 constexpr int kPlanThreads = 1024;
 
 // A part of an item (or all of it) where the steps are cut evenly
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     const long long rounds = (n_items + a.ctas - 1) / a.ctas;
     const long long uncut = all_steps == n_items * longest || rounds == 1 ? rounds * longest
                                                                           : max(static_cast<long long>(longest), share + longest / 8);
-    const bool cut = sound && n_items <= kMaxCutItems && 2 * a.ctas <= kMaxSlots && uncut > share + share / 8 + 8;
+    const bool cut = sound && n_items <= kMaxCutItems && 2 * a.ctas <= kMaxSlots && uncut > share + share / 8 + kCutSteps;
     const int ctas = static_cast<int>(max(1ll, min(static_cast<long long>(a.ctas), all_steps)));
     if (tid == 0) {
         a.item0[s.B] = sound ? static_cast<int>(all_items) : 0;
@@ -338,6 +342,7 @@ struct Params {
     float scale_log2;
     PackedView o, v;
     float *lse;
+    long long max_items;
     PlanHeader *hdr;
     const int32_t *rank, *item0, *first;
     const Entry *entries;
@@ -459,6 +464,15 @@ __device__ __forceinline__ void add_not_finite(const char *v, int64_t stride, in
         }
 }
 
+// 32 lanes x 16 columns of TMEM, as tmem_ld32
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+
 template <int D, class C>
 __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, uint32_t tmem, uint32_t settled_at,
                                              volatile float *row_sums, const volatile int *items,
@@ -530,21 +544,21 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 const float base = m == -CUDART_INF_F ? 0.0f : m;  // a row that has seen no key yet: every weight 0
                 const uint64_t nm2 = f2_pack(-base, -base);
                 sacc[0] = sacc[1] = 0ull;
-                uint32_t sv[2][32];
-                tmem_ld32(tS, sv[0]);
+                uint32_t sv[2][16];  // 16 columns at a time: with 32 the registers did not suffice
+                tmem_ld16(tS, sv[0]);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
+                for (int c = 0; c < 2 * NC; ++c) {
                     tmem_wait_ld();
-                    reg_fence32(sv[c & 1]);
-                    if (c + 1 < NC) tmem_ld32(tS + (c + 1) * 32, sv[(c + 1) & 1]);
+                    reg_fence(sv[c & 1]);
+                    if (c + 1 < 2 * NC) tmem_ld16(tS + (c + 1) * 16, sv[(c + 1) & 1]);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
+                    for (int q = 0; q < 8; ++q) {
                         float x0, x1;
                         f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c & 1][2 * q]), __uint_as_float(sv[c & 1][2 * q + 1])), c2x, nm2),
                                   x0, x1);
                         const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                         sacc[q & 1] = f2_add(sacc[q & 1], f2_pack(p0, p1));
-                        pk[c][q] = pack_bf16x2(p0, p1);
+                        pk[c >> 1][(c & 1) * 8 + q] = pack_bf16x2(p0, p1);
                     }
                 }
             };
@@ -715,7 +729,8 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
     }
 }
 
-template <int D>
+// PLANNED: after plan_kernel; else at most 32 sequences of at most kShortKeys keys
+template <int D, bool PLANNED>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const Params p)
@@ -787,15 +802,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ items, Q, K
             // The item after the one at hand is fetched while its first steps run.
-            // (past L1: the plan was written while this kernel was on its way)
-            const uint32_t n_items = __ldcg(&p.hdr->n_items);
-            const int cut = __ldcg(&p.hdr->cut);
-            int due = 0, due_end = 0;  // where the steps are cut: this CTA's entries
-            if (static_cast<int>(blockIdx.x) < cut) due = __ldcg(p.first + blockIdx.x), due_end = __ldcg(p.first + blockIdx.x + 1);
+            uint32_t n_items;
+            int cut = 0, due = 0, due_end = 0;  // where the steps are cut: this CTA's entries
+            int seq_items = 0, seq_end = 0;     // without a plan: items of sequence `lane`, and of those up to it
+            if constexpr (PLANNED) {  // (past L1: the plan was written while this kernel was on its way)
+                n_items = __ldcg(&p.hdr->n_items);
+                cut = __ldcg(&p.hdr->cut);
+                if (static_cast<int>(blockIdx.x) < cut) due = __ldcg(p.first + blockIdx.x), due_end = __ldcg(p.first + blockIdx.x + 1);
+            } else {
+                if (lane < p.s.B) seq_items = (seq_of(p.s, lane, p.err).n_q + p.s.tpt - 1) / p.s.tpt;
+                seq_end = seq_items;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xFFFFFFFFu, seq_end, o);
+                    if (lane >= o) seq_end += y;
+                }
+                const int all = __shfl_sync(0xFFFFFFFFu, seq_end, 31);
+                if (all > p.max_items) raise_error(p.err, BSA_ERR_INVALID_ARG);  // sequences overlap
+                n_items = all > p.max_items ? 0u : static_cast<uint32_t>(all) * static_cast<uint32_t>(p.s.Hk);
+            }
             int count = 0, G = 0, e = 0;
             auto hand_out = [&](Item &it) -> bool {
                 it.b = -1;
-                if (cut) {
+                if constexpr (!PLANNED) {
+                    const uint32_t id = blockIdx.x + static_cast<uint32_t>(count) * gridDim.x;
+                    if (id < n_items) {
+                        const int item = static_cast<int>(id / static_cast<uint32_t>(p.s.Hk));
+                        const int b = __popc(__ballot_sync(0xFFFFFFFFu, seq_end <= item));  // the first that ends behind it
+                        it.b = b;
+                        it.kh = static_cast<int>(id) - item * p.s.Hk;
+                        it.t0 = (__shfl_sync(0xFFFFFFFFu, seq_end, b) - 1 - item) * p.s.tpt;  // its last tile first
+                        it.lo = 0;
+                        it.slot = -1;
+                    }
+                } else if (cut) {
                     if (due < due_end) {
                         const int4 *en = reinterpret_cast<const int4 *>(p.entries + due++);
                         const int4 x = __ldcg(en), y = __ldcg(en + 1);
@@ -1177,7 +1217,7 @@ bool make_map(CUtensorMap *m, const PackedView &t, int d, uint64_t n1, int64_t s
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool PLANNED>
 bsa_status launch(const PromptArgs &a, cudaStream_t st)
 {
     using C = Cfg<D>;
@@ -1186,7 +1226,7 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
     int sms = 0;
     const bsa_status s = current_sm_count(&sms);
     if (s != BSA_OK) return s;
-    auto kern = prompt_kernel<D>;
+    auto kern = prompt_kernel<D, PLANNED>;
     static std::atomic<uint64_t> ready{0};
     if (!allow_shared_memory(kern, C::SMEM_ALLOC, ready)) return BSA_ERR_CUDA;
     // setmaxnreg hands out what the block was launched with: with fewer registers the split would wait for ever
@@ -1222,14 +1262,13 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
     pa.entries = reinterpret_cast<Entry *>(a.ws + l.entries);
     pa.splits = reinterpret_cast<Split *>(a.ws + l.splits);
     pa.err = err;
-    plan_kernel<<<1, kPlanThreads, 0, st>>>(pa);
-    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     Params p;
     p.s = seqs;
     p.scale_log2 = a.scale * 1.44269504088896340736f;
     p.o = a.o;
     p.v = a.v;
     p.lse = a.lse;
+    p.max_items = l.max_items;
     p.hdr = hdr;
     p.rank = pa.rank;
     p.item0 = pa.item0;
@@ -1240,7 +1279,15 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
     p.err = err;
     p.wait_limit_ns = a.wait_limit_ns;
     p.stall = (a.dbg_flags & kDbgStall) != 0u;
+    if constexpr (!PLANNED) {
+        const int64_t items = l.max_items * a.Hk;
+        kern<<<static_cast<unsigned>(items < sms ? items : sms), kThreads, C::SMEM_ALLOC, st>>>(mq, mk, mv, p);
+        return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+    }
+    plan_kernel<<<1, kPlanThreads, 0, st>>>(pa);
+    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     if (!pdl_launch(kern, dim3(static_cast<unsigned>(sms)), kThreads, C::SMEM_ALLOC, st, mq, mk, mv, p)) return BSA_ERR_CUDA;
+    if (a.Tk <= kShortKeys) return BSA_OK;  // nothing is cut
     const JoinArgs ja{seqs, a.o, a.lse, hdr, pa.splits, p.part_o, p.part_stats, err};
     if (!pdl_launch(join_kernel<D>, dim3(static_cast<unsigned>(2 * sms)), 256, 0, st, ja)) return BSA_ERR_CUDA;
     return BSA_OK;
@@ -1252,7 +1299,9 @@ size_t prompt_workspace(int T, int B, int H, int Hk, int d) { return layout_of(T
 
 bsa_status launch_prompt_attention(const PromptArgs &a, cudaStream_t st)
 {
-    return a.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
+    const bool planned = a.B > 32 || a.Tk > kShortKeys;
+    if (a.d == 128) return planned ? launch<128, true>(a, st) : launch<128, false>(a, st);
+    return planned ? launch<64, true>(a, st) : launch<64, false>(a, st);
 }
 
 }  // namespace bsa

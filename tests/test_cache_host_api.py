@@ -275,7 +275,7 @@ def on_any_device(monkeypatch):
     def not_reached(*args):
         raise AssertionError("the library was called")
 
-    monkeypatch.setattr(cb, "_run", not_reached)
+    monkeypatch.setattr(cb, "_call", not_reached)
 
 
 def test_helpers_refuse_tensors_that_do_not_go_together(monkeypatch):
