@@ -8,7 +8,7 @@
 //   * Two groups of four softmax warps, a thread per row, take a tile's steps in turn: a step's chain (load S, 128
 //     exponentials and sums, store P) is twice as long as its products take on the tensor cores. Of the other four
 //     warps one issues the Q K^T, up to three steps ahead (three S / P buffers in TMEM), one the P V; one hands out the
-//     items and loads Q and K, and one loads V and looks after it where a mask ends in a block.
+//     items and loads Q and K, and one loads V.
 //   * Online softmax in log2, P in bf16 over S in TMEM: the running maximum of a row is raised only when a step's sum
 //     passes 2^8 (the step is then done again and O rescaled). The groups share it: a step is computed with the
 //     maximum as last seen; before its P is stored, each row looks at what the step before settled on (shared memory, with
@@ -22,9 +22,10 @@
 //     first, so that the work ends with short ones. Where that would leave CTAs idle (few items, or
 //     one far above a CTA's average), all steps in a row are cut evenly over the CTAs instead, and a third launch joins
 //     the parts of an item that a cut runs through, in order.
-//   * 0 * NaN: a masked weight of zero still multiplies V. In blocks where a mask ends, rows of V behind the sequence
-//     are zeroed in shared memory, and other values that are not finite too; these are then added in the epilogue to
-//     the rows that see them. Blocks that every row sees whole are not looked at.
+//   * 0 * NaN: a masked weight of zero still multiplies V. In steps where a mask ends, the softmax warps look through V before
+//     they hand P over, a quarter of the rows each: rows behind the sequence are zeroed in shared memory, and other
+//     values that are not finite too; these are then added in the epilogue to the rows that see them. Steps that every row
+//     sees whole are not looked at.
 //   * Every wait is bounded (BSA_ERR_TIMEOUT in the workspace, clean exit).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,8 +44,8 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kLoadWarp = 8, kQkWarp = 9, kPvWarp = 10, kValueWarp = 11;
 constexpr int kRing = 4;  // items in flight
 constexpr int kThreads = 12 * 32;
-// registers a thread after the split: 256 * 216 + 128 * 72 = 384 * 168, what the block is launched with
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+// registers a thread after the split: 256 * 192 + 128 * 120 = 384 * 168, what the block is launched with
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 constexpr float kRescaleSum = 256.0f;
 constexpr uint32_t kDbgStall = 1u;  // of bsa_debug_config
 constexpr unsigned long long kDrainNs = 1000000000ull;  // copies and products in flight are waited for this long
@@ -56,6 +57,7 @@ constexpr int kCutSteps = 8;          // what a cut has to save, in steps
 // a lane a sequence, and the call is one launch (four sequences of 12 to 128 tokens, 24 heads of 64: MEASURED).
 constexpr int kShortKeys = kCutSteps * kStep;
 constexpr int kPlanThreads = 1024;
+constexpr int kSmallPlan = 256, kSmallItems = 2048;  // sequences and items that a plan holds in shared memory
 
 // A part of an item (or all of it) where the steps are cut evenly
 struct __align__(16) Entry {
@@ -66,7 +68,8 @@ struct __align__(16) Entry {
 };
 // An item in parts: the first is the last of CTA c0, the others the first of the CTAs after it
 struct __align__(16) Split {
-    int b, t0, kh, c0, parts, pad[3];
+    int q0, tokens, kh, c0, parts;  // first query (packed) and how many there are of the tile
+    int pad[3];
 };
 __host__ __device__ constexpr int slot_of(int c0, int part) { return part == 0 ? 2 * c0 + 1 : 2 * (c0 + part); }
 
@@ -217,7 +220,7 @@ __device__ int walk_cut(const PlanArgs &a, int c, int ctas, long long from, long
                     out[count] = e;
                     if (skip == 0 && more) {
                         const int last = static_cast<int>((end * ctas + total - 1) / total) - 1;  // CTA of its last step
-                        a.splits[atomicAdd(&a.hdr->n_splits, 1u)] = Split{b, e.t0, kh, c, last - c + 1, {0, 0, 0}};
+                        a.splits[atomicAdd(&a.hdr->n_splits, 1u)] = Split{q.q0 + e.t0, min(s.tpt, q.n_q - e.t0), kh, c, last - c + 1, {0, 0, 0}};
                     }
                 }
                 ++count;
@@ -236,6 +239,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     __shared__ long long warp_sums[32];
     __shared__ int bucket[kPlanThreads];
     __shared__ int longest;
+    // small plans are made in shared memory (the attention reads rank and item0 in the workspace)
+    __shared__ int s_rank[kSmallPlan], s_item0[kSmallPlan + 1], s_item_step0[kSmallItems];
+    __shared__ long long s_step0[kSmallPlan];
+    PlanArgs pl = a;
+    if (a.s.B <= kSmallPlan) pl.rank = s_rank, pl.item0 = s_item0, pl.step0 = s_step0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Seqs &s = a.s;
     bucket[tid] = 0;
@@ -253,12 +261,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     const int start = static_cast<int>(block_prefix(bucket[tid], total, warp_sums));
     bucket[tid] = start;
     __syncthreads();
-    for (int b = tid; b < s.B; b += kPlanThreads) a.rank[atomicAdd(&bucket[key(seq_of(s, b, a.err))], 1)] = b;
+    for (int b = tid; b < s.B; b += kPlanThreads) pl.rank[atomicAdd(&bucket[key(seq_of(s, b, a.err))], 1)] = b;
     __syncthreads();
     // items and steps of each, and the longest item
     int most = 0;
     for (int r = warp; r < s.B; r += 32) {
-        const Seq q = seq_of(s, a.rank[r], a.err);
+        const Seq q = seq_of(s, pl.rank[r], a.err);
         const int items = (q.n_q + s.tpt - 1) / s.tpt;
         long long sum = 0;
         for (int i = lane; i < items; i += 32) {
@@ -269,8 +277,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (lane == 0) {
-            a.item0[r] = items;
-            a.step0[r] = sum * s.Hk;
+            pl.item0[r] = items;
+            pl.step0[r] = sum * s.Hk;
         }
     }
     atomicMax(&longest, most);
@@ -279,14 +287,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     const int run = (s.B + kPlanThreads - 1) / kPlanThreads;
     const int lo = min(s.B, tid * run), hi = min(s.B, lo + run);
     long long items = 0, steps = 0, all_items, all_steps;
-    for (int r = lo; r < hi; ++r) items += a.item0[r], steps += a.step0[r];
+    for (int r = lo; r < hi; ++r) items += pl.item0[r], steps += pl.step0[r];
     items = block_prefix(items, all_items, warp_sums);
     steps = block_prefix(steps, all_steps, warp_sums);
     for (int r = lo; r < hi; ++r) {
-        const int n = a.item0[r];
-        const long long m = a.step0[r];
-        a.item0[r] = static_cast<int>(items);
-        a.step0[r] = steps;
+        const int n = pl.item0[r];
+        const long long m = pl.step0[r];
+        pl.item0[r] = static_cast<int>(items);
+        pl.step0[r] = steps;
         items += n;
         steps += m;
     }
@@ -301,8 +309,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
                                                                           : max(static_cast<long long>(longest), share + longest / 8);
     const bool cut = sound && n_items <= kMaxCutItems && 2 * a.ctas <= kMaxSlots && uncut > share + share / 8 + kCutSteps;
     const int ctas = static_cast<int>(max(1ll, min(static_cast<long long>(a.ctas), all_steps)));
+    if (pl.rank != a.rank)
+        for (int r = lo; r < hi; ++r) a.rank[r] = pl.rank[r], a.item0[r] = pl.item0[r];
+    if (all_items <= kSmallItems) pl.item_step0 = s_item_step0;
     if (tid == 0) {
-        a.item0[s.B] = sound ? static_cast<int>(all_items) : 0;
+        a.item0[s.B] = pl.item0[s.B] = sound ? static_cast<int>(all_items) : 0;
         a.hdr->next = 0u;
         a.hdr->n_items = sound ? static_cast<uint32_t>(all_items) * static_cast<uint32_t>(s.Hk) : 0u;
         a.hdr->n_splits = 0u;
@@ -311,8 +322,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     if (!cut) return;
     __syncthreads();
     for (int r = warp; r < s.B; r += 32) {
-        const Seq q = seq_of(s, a.rank[r], a.err);
-        const int base = a.item0[r], n = a.item0[r + 1] - base;
+        const Seq q = seq_of(s, pl.rank[r], a.err);
+        const int base = pl.item0[r], n = pl.item0[r + 1] - base;
         int before = 0;
         for (int i0 = 0; i0 < n; i0 += 32) {
             const int i = i0 + lane;
@@ -323,16 +334,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
                 const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
                 if (lane >= o) incl += y;
             }
-            if (i < n) a.item_step0[base + i] = before + incl - m;
+            if (i < n) pl.item_step0[base + i] = before + incl - m;
             before += __shfl_sync(0xFFFFFFFFu, incl, 31);
         }
     }
     __syncthreads();
     const long long from = tid < ctas ? tid * all_steps / ctas : 0, to = tid < ctas ? (tid + 1) * all_steps / ctas : 0;
-    const int mine = tid < ctas ? walk_cut(a, tid, ctas, from, to, all_steps, nullptr) : 0;
+    const int mine = tid < ctas ? walk_cut(pl, tid, ctas, from, to, all_steps, nullptr) : 0;
     const int at = static_cast<int>(block_prefix(mine, total, warp_sums));
     if (tid <= ctas) a.first[tid] = at;
-    if (tid < ctas) walk_cut(a, tid, ctas, from, to, all_steps, a.entries + at);
+    if (tid < ctas) walk_cut(pl, tid, ctas, from, to, all_steps, a.entries + at);
 }
 
 // ---------------------------------------------------------------- the attention
@@ -364,14 +375,15 @@ struct Cfg {
     static constexpr int kSlab = 128 * 128;  // bytes of 64 columns of 128 rows
     static constexpr int Q_OFF = 0, K_OFF = QS * kQBytes, V_OFF = K_OFF + NK * kKVBytes, BAR_OFF = V_OFF + NV * kKVBytes;
     static constexpr int B_QFULL = 0, B_QEMPTY = B_QFULL + QS, B_KFULL = B_QEMPTY + QS, B_KEMPTY = B_KFULL + NK,
-                         B_VFULL = B_KEMPTY + NK, B_VEMPTY = B_VFULL + NV, B_VFIXED = B_VEMPTY + NV, B_SFULL = B_VFIXED + NV,
+                         B_VFULL = B_KEMPTY + NK, B_VEMPTY = B_VFULL + NV, B_SFULL = B_VEMPTY + NV,
                          B_PFULL = B_SFULL + NSB, B_PVDONE = B_PFULL + NSB, B_OEMPTY = B_PVDONE + NSB, B_TFULL = B_OEMPTY + 1,
                          B_TEMPTY = B_TFULL + kRing, B_SUMS = B_TEMPTY + kRing, B_DRAIN = B_SUMS + 8, NBAR = B_DRAIN + 2;
     static constexpr int MISC_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;
     static constexpr int kItemWords = 12;
     static constexpr int MISC_WORDS = 2 + kRing + kRing * kItemWords;  // TMEM base, abort flag, V flags of the items, the items
     static constexpr int ROWS_OFF = (MISC_OFF + 4 * MISC_WORDS + 15) / 16 * 16;  // settled maxima [128][2], sums [2][128]
-    static constexpr int SMEM = ROWS_OFF + 4 * (128 * 2 + 2 * 128);
+    static constexpr int OUT_OFF = ROWS_OFF + 4 * (128 * 2 + 2 * 128);  // 64 bytes of each of a warp's 32 rows on their way out
+    static constexpr int SMEM = OUT_OFF + kSoftmaxWarps * 2048;
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(kTileM, kStep, 0, 0);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(kTileM, D, 0, 1);
@@ -475,8 +487,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 
 template <int D, class C>
 __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, uint32_t tmem, uint32_t settled_at,
-                                             volatile float *row_sums, const volatile int *items,
-                                             const volatile uint32_t *vflags, const Ctl &ctl, int warp, int lane)
+                                             volatile float *row_sums, uint4 *out, uint8_t *values, const volatile int *items,
+                                             volatile uint32_t *vflags, const Ctl &ctl, int warp, int lane)
 {
     auto bar = [&](int idx) -> uint32_t { return sbase + C::BAR_OFF + 8u * idx; };
     constexpr int NC = kStep / 32;
@@ -488,7 +500,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
     int G = 0, count = 0, pairs = 0;  // steps and items so far, items of two steps and more
     Item it;
     while (fetch<C>(sbase, items, ctl, lane, count, it)) {
-        const int n = it.hi - it.lo;
+        const int n = it.hi - it.lo, from = first_masked(p, it);
         const int tok = it.t0 + rt;
         const bool real = rt < p.s.tpt && tok < it.n_q;
         const int nvis = real ? visible(p.s.causal, it.n_q, it.n_k, tok) : 0;
@@ -634,6 +646,39 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 }
             }
             if (i > 0) settle(m_run);
+            if (it.lo + i >= from) {
+                // V: this warp's rows of the block
+                const int s = g % C::NV;
+                if (!warp_wait_all(bar(C::B_VFULL + s), (g / C::NV) & 1, ctl)) return;
+                const int rows = it.n_k - (it.lo + i) * kStep - w4 * 32;  // of the 32 that are the sequence's
+                uint32_t big = 0u;  // largest magnitude of either half
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    uint4 *slab = reinterpret_cast<uint4 *>(values + s * C::kKVBytes + c * C::kSlab + w4 * 32 * 128);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int at = k * 32 + lane;  // 16 bytes of row at / 8
+                        if ((at >> 3) >= rows) slab[at] = make_uint4(0u, 0u, 0u, 0u);
+                        const uint4 w = slab[at];
+                        big = __vmaxu2(big, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                                     __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+                    }
+                }
+                if (__any_sync(0xFFFFFFFFu, (big & 0xFFFFu) >= 0x7F80u || (big >> 16) >= 0x7F80u)) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint16_t *slab = reinterpret_cast<uint16_t *>(values + s * C::kKVBytes + c * C::kSlab + w4 * 32 * 128);
+#pragma unroll 1
+                        for (int k = lane; k < 32 * 64; k += 32)
+                            if ((slab[k] & 0x7F80u) == 0x7F80u) slab[k] = 0;
+                    }
+                    if (lane == 0) {
+                        vflags[(count - 1) % kRing] = 1u;
+                        __threadfence_block();
+                    }
+                }
+                fence_proxy_async_smem();
+            }
 #pragma unroll
             for (int c = 0; c < NC; ++c) tmem_st16(tS + c * 16, pk[c]);
 #pragma unroll
@@ -664,8 +709,30 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
             }
             const bool part = it.slot >= 0;
             const int head = it.kh * p.s.g + rh;
-            char *orow = p.o.p + static_cast<int64_t>(it.q0 + tok) * p.o.token + head * p.o.head;
-            const size_t prow = part ? static_cast<size_t>(it.slot) * kTileM + trow : 0;
+            // Rows go out through shared memory, 64 bytes of 32 rows at a time: four lanes write a row's, in place of each lane
+            // 16 bytes of a row of its own (half a sector; an epilogue took 8000 to 11000 cycles). A lane has rows
+            // lane / 4, + 8, + 16, + 24 of the warp's; `to` is where they begin, nullptr where they do not exist.
+            char *const own = part ? reinterpret_cast<char *>(p.part_o + (static_cast<size_t>(it.slot) * kTileM + trow) * D)
+                                   : p.o.p + static_cast<int64_t>(it.q0 + tok) * p.o.token + head * p.o.head;
+            char *to[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const unsigned long long at =
+                    __shfl_sync(0xFFFFFFFFu, part || real ? reinterpret_cast<unsigned long long>(own) : 0ull, k * 8 + (lane >> 2));
+                to[k] = at ? reinterpret_cast<char *>(at) + (lane & 3) * 16 : nullptr;
+            }
+            auto put = [&](const uint4 (&v)[4], int at) {  // this row's bytes [at, at + 64)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) out[lane * 4 + (k ^ ((lane >> 1) & 3))] = v[k];
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = k * 8 + (lane >> 2);
+                    const uint4 w = out[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
+                    if (to[k]) *reinterpret_cast<uint4 *>(to[k] + at) = w;
+                }
+                __syncwarp();
+            };
             bool dirty = false;
             if (n > 0) {
                 const int t = G + n - 1;
@@ -673,53 +740,45 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 tc_fence_after();
                 dirty = vflags[(count - 1) % kRing] != 0u;
             }
-            const float inv = part ? 1.0f : l != 0.0f ? 1.0f / l : 0.0f;
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
 #pragma unroll
-            for (int c0 = 0; c0 < D / 32; c0 += 2) {
-                uint32_t ov[2][32];
+                for (int q = 0; q < 32; ++q) ov[q] = 0u;
                 if (n > 0) {
-                    tmem_ld32(tO + c0 * 32, ov[0]);
-                    tmem_ld32(tO + (c0 + 1) * 32, ov[1]);
+                    tmem_ld32(tO + c * 32, ov);
                     tmem_wait_ld();
-                    reg_fence32(ov[0]);
-                    reg_fence32(ov[1]);
-                    if (c0 + 2 == D / 32) {
+                    reg_fence32(ov);
+                    if (c + 1 == D / 32) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::B_OEMPTY));
                     }
                 }
+                auto of = [&](int q) { return __uint_as_float(ov[q]) * inv; };
+                uint4 w[4];
+                if (part) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int c = c0 + h;
+                    for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) ov[h][q] = n > 0 ? __float_as_uint(__uint_as_float(ov[h][q]) * inv) : 0u;
-                    if (part) {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + c * 32);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            dst[q] = make_float4(__uint_as_float(ov[h][4 * q]), __uint_as_float(ov[h][4 * q + 1]),
-                                                 __uint_as_float(ov[h][4 * q + 2]), __uint_as_float(ov[h][4 * q + 3]));
-                    } else if (real) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(orow + c * 64);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint4 w;
-                            w.x = pack_bf16x2(__uint_as_float(ov[h][8 * q]), __uint_as_float(ov[h][8 * q + 1]));
-                            w.y = pack_bf16x2(__uint_as_float(ov[h][8 * q + 2]), __uint_as_float(ov[h][8 * q + 3]));
-                            w.z = pack_bf16x2(__uint_as_float(ov[h][8 * q + 4]), __uint_as_float(ov[h][8 * q + 5]));
-                            w.w = pack_bf16x2(__uint_as_float(ov[h][8 * q + 6]), __uint_as_float(ov[h][8 * q + 7]));
-                            dst[q] = w;
-                        }
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = make_uint4(ov[16 * x + 4 * q], ov[16 * x + 4 * q + 1], ov[16 * x + 4 * q + 2], ov[16 * x + 4 * q + 3]);
+                        put(w, c * 128 + x * 64);
                     }
+                } else {
+                    auto two = [&](int q) { return pack_bf16x2(of(q), of(q + 1)); };
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) w[q] = make_uint4(two(8 * q), two(8 * q + 2), two(8 * q + 4), two(8 * q + 6));
+                    put(w, c * 64);
                 }
             }
+            if (__any_sync(0xFFFFFFFFu, dirty && real)) __threadfence_block();  // the row is read back
             if (dirty && real) {
-                const int from = first_masked(p, it) * kStep;
-                add_not_finite<D>(p.v.p + static_cast<int64_t>(it.k0) * p.v.token + it.kh * p.v.head, p.v.token, from,
-                                  min(nvis, it.hi * kStep), part ? reinterpret_cast<char *>(p.part_o + prow * D) : orow, part);
+                add_not_finite<D>(p.v.p + static_cast<int64_t>(it.k0) * p.v.token + it.kh * p.v.head, p.v.token, from * kStep,
+                                  min(nvis, it.hi * kStep), own, part);
             }
-            if (part) p.part_stats[prow] = make_float2(m_run, l);
+            if (part) p.part_stats[static_cast<size_t>(it.slot) * kTileM + trow] = make_float2(m_run, l);
             else if (real && p.lse)
                 p.lse[static_cast<int64_t>(head) * p.s.Tq + it.q0 + tok] = (m_run + log2f(l)) * 0.69314718055994530942f;
         }
@@ -758,7 +817,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < C::NV; ++s) {
             mbar_init(bar(C::B_VFULL + s), 1);
             mbar_init(bar(C::B_VEMPTY + s), 1);
-            mbar_init(bar(C::B_VFIXED + s), 1);
         }
         for (int b = 0; b < C::NSB; ++b) {
             mbar_init(bar(C::B_SFULL + b), 1);
@@ -796,7 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kSoftmaxWarps) {
         regs_up<kSoftmaxRegs>();
-        softmax_role<D, C>(p, sbase, tmem, sbase + C::ROWS_OFF, row_sums, items, vflags, ctl, warp, lane);
+        softmax_role<D, C>(p, sbase, tmem, sbase + C::ROWS_OFF, row_sums,
+                           reinterpret_cast<uint4 *>(smem + C::OUT_OFF + warp * 2048), smem + C::V_OFF, items, vflags, ctl, warp, lane);
     } else {
         regs_down<kOtherRegs>();
         if (warp == kLoadWarp) {
@@ -936,12 +995,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         } else if (warp == kValueWarp) {
-            // ------------------------------------------------------------ V, and V where a mask ends
+            // ------------------------------------------------------------ V
             int count = 0, G = 0;
             bool ok = !p.stall;
             Item it;
             while (ok && fetch<C>(sbase, items, ctl, lane, count, it)) {
-                const int from = first_masked(p, it);
+                done_with<C>(sbase, lane, count);
                 for (int i = it.lo; i < it.hi; ++i, ++G) {
                     const int s = G % C::NV;
                     if (G >= C::NV && !warp_wait_all(bar(C::B_VEMPTY + s), ((G / C::NV) - 1) & 1, ctl)) {
@@ -956,45 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         bar(C::B_VFULL + s));
                     }
                     __syncwarp();
-                    if (i >= from) {
-                        if (!warp_wait_all(bar(C::B_VFULL + s), (G / C::NV) & 1, ctl)) {
-                            ++G;  // its copy is in flight
-                            ok = false;
-                            break;
-                        }
-                        const int rows = min(kStep, it.n_k - i * kStep);  // rows of the block that are the sequence's
-                        uint8_t *v = smem + C::V_OFF + s * C::kKVBytes;
-                        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                        uint32_t big = 0u;  // largest magnitude of either half
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c) {
-                            uint4 *slab = reinterpret_cast<uint4 *>(v + c * C::kSlab);
-                            for (int k = lane; k < rows * 8; k += 32) {
-                                const uint4 w = slab[k];
-                                big = __vmaxu2(big, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                                             __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
-                            }
-                            for (int k = rows * 8 + lane; k < kStep * 8; k += 32) slab[k] = zero;
-                        }
-                        const bool bad = (big & 0xFFFFu) >= 0x7F80u || (big >> 16) >= 0x7F80u;
-                        if (__any_sync(0xFFFFFFFFu, bad)) {
-#pragma unroll 1
-                            for (int c = 0; c < D / 64; ++c) {
-                                uint16_t *slab = reinterpret_cast<uint16_t *>(v + c * C::kSlab);
-                                for (int k = lane; k < rows * 64; k += 32)
-                                    if ((slab[k] & 0x7F80u) == 0x7F80u) slab[k] = 0;
-                            }
-                            if (lane == 0) {
-                                vflags[(count - 1) % kRing] = 1u;
-                                __threadfence_block();
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (lane == 0) mbar_arrive(bar(C::B_VFIXED + s));  // nobody waits for it where no mask ends
                 }
-                done_with<C>(sbase, lane, count);
             }
             if (lane == 0 && *ctl.abort_flag)
                 for (int g = max(0, G - C::NV); g < G; ++g) wait_bar_drain(bar(C::B_VFULL + g % C::NV), (g / C::NV) & 1);
@@ -1050,12 +1071,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             Item it;
             while (ok && !p.stall && fetch<C>(sbase, items, ctl, lane, count, it)) {
-                const int n = it.hi - it.lo, from = first_masked(p, it) - it.lo;
+                const int n = it.hi - it.lo;
                 done_with<C>(sbase, lane, count);
                 for (int i = 0; i < n; ++i, ++G) {
                     const int s = G % C::NV, b = G % C::NSB;
                     // the first product of a tile overwrites O: the tile before has been read
-                    if (!warp_wait_all(bar((i >= from ? C::B_VFIXED : C::B_VFULL) + s), (G / C::NV) & 1, ctl) ||
+                    if (!warp_wait_all(bar(C::B_VFULL + s), (G / C::NV) & 1, ctl) ||
                         (i == 0 && e >= 1 && !warp_wait_all(bar(C::B_OEMPTY), (e - 1) & 1, ctl)) ||
                         !warp_wait_all(bar(C::B_PFULL + b), (G / C::NSB) & 1, ctl)) {
                         ok = false;
@@ -1112,46 +1133,66 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinArgs a)
     constexpr int V = D / 32;  // channels of a lane
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    const long long rows = static_cast<long long>(__ldcg(&a.hdr->n_splits)) * kTileM;
-    const long long step = static_cast<long long>(gridDim.x) * 8;
-    for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < rows; i += step) {
-        const int trow = static_cast<int>(i % kTileM);
-        const Split sp = a.splits[i / kTileM];
+    const int rows = static_cast<int>(__ldcg(&a.hdr->n_splits)) * kTileM;
+    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += gridDim.x * 8) {
+        const int trow = i % kTileM;
+        const int4 *record = reinterpret_cast<const int4 *>(a.splits + i / kTileM);
+        const int4 sp = __ldcg(record);  // q0, tokens, kh, c0
+        const int parts = __ldcg(record + 1).x;
         const int rt = trow / a.s.g, rh = trow % a.s.g;
-        const Seq q = seq_of(a.s, sp.b, a.err);
-        const int tok = sp.t0 + rt;
-        if (rt >= a.s.tpt || tok >= q.n_q) continue;
-        auto row_of = [&](int part) { return static_cast<size_t>(slot_of(sp.c0, part)) * kTileM + trow; };
-        float M = -CUDART_INF_F;
-        for (int k = lane; k < sp.parts; k += 32) M = fmaxf(M, __ldcg(a.part_stats + row_of(k)).x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-        float L = 0.0f, out[V];
+        if (rt >= sp.y) continue;
+        auto row_of = [&](int part) { return static_cast<size_t>(slot_of(sp.w, part)) * kTileM + trow; };
+        float M = -CUDART_INF_F, L = 0.0f, out[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) out[c] = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < sp.parts; ++k) {
-            const float2 st = __ldcg(a.part_stats + row_of(k));
-            const float w = st.x == M ? 1.0f : ex2_approx(st.x - M);
-            L += w * st.y;
-            const float *src = a.part_o + row_of(k) * D + lane * V;
-            if constexpr (V == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                out[0] += w * v.x, out[1] += w * v.y, out[2] += w * v.z, out[3] += w * v.w;
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                out[0] += w * v.x, out[1] += w * v.y;
+        for (int k0 = 0; k0 < parts; k0 += 32) {
+            // 32 parts' statistics at a time, a lane each; then their rows, eight loads in flight
+            float2 st = make_float2(-CUDART_INF_F, 0.0f);
+            if (k0 + lane < parts) st = __ldcg(a.part_stats + row_of(k0 + lane));
+            float m = st.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            m = fmaxf(m, M);
+            const float old = m == M ? 1.0f : ex2_approx(M - m), w = st.x == m ? 1.0f : ex2_approx(st.x - m);
+            M = m;
+            float l = k0 + lane < parts ? w * st.y : 0.0f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+            L = L * old + l;
+#pragma unroll
+            for (int c = 0; c < V; ++c) out[c] *= old;
+            const int n = min(32, parts - k0);
+            for (int j0 = 0; j0 < n; j0 += 8) {
+                float v[8][V];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float *src = a.part_o + row_of(k0 + min(j0 + j, n - 1)) * D + lane * V;
+                    if constexpr (V == 4) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                        v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+                    } else {
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                        v[j][0] = x.x, v[j][1] = x.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float wj = __shfl_sync(0xFFFFFFFFu, w, min(j0 + j, 31));
+                    if (j0 + j >= n) break;
+#pragma unroll
+                    for (int c = 0; c < V; ++c) out[c] = fmaf(wj, v[j][c], out[c]);
+                }
             }
         }
         const float inv = L != 0.0f ? 1.0f / L : 0.0f;
-        const int head = sp.kh * a.s.g + rh;
-        char *dst = a.o.p + static_cast<int64_t>(q.q0 + tok) * a.o.token + head * a.o.head + lane * V * 2;
+        const int head = sp.z * a.s.g + rh;
+        char *dst = a.o.p + static_cast<int64_t>(sp.x + rt) * a.o.token + head * a.o.head + lane * V * 2;
         if constexpr (V == 4)
             *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(out[0] * inv, out[1] * inv), pack_bf16x2(out[2] * inv, out[3] * inv));
         else
             *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(out[0] * inv, out[1] * inv);
         if (lane == 0 && a.lse)
-            a.lse[static_cast<int64_t>(head) * a.s.Tq + q.q0 + tok] = (M + log2f(L)) * 0.69314718055994530942f;
+            a.lse[static_cast<int64_t>(head) * a.s.Tq + sp.x + rt] = (M + log2f(L)) * 0.69314718055994530942f;
     }
 }
 
@@ -1289,7 +1330,7 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
     if (!pdl_launch(kern, dim3(static_cast<unsigned>(sms)), kThreads, C::SMEM_ALLOC, st, mq, mk, mv, p)) return BSA_ERR_CUDA;
     if (a.Tk <= kShortKeys) return BSA_OK;  // nothing is cut
     const JoinArgs ja{seqs, a.o, a.lse, hdr, pa.splits, p.part_o, p.part_stats, err};
-    if (!pdl_launch(join_kernel<D>, dim3(static_cast<unsigned>(2 * sms)), 256, 0, st, ja)) return BSA_ERR_CUDA;
+    if (!pdl_launch(join_kernel<D>, dim3(static_cast<unsigned>(4 * sms)), 256, 0, st, ja)) return BSA_ERR_CUDA;
     return BSA_OK;
 }
 
