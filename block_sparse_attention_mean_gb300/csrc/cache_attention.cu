@@ -64,7 +64,11 @@ struct Ring {
     static constexpr int kStage = 2 * kData + (E4M3 ? 2 * kTile : 0);
     static constexpr int kStages = 24576 / (2 * kData) > 6 ? 6 : 24576 / (2 * kData);
     static constexpr int kWarpBytes = kStages * kStage;
-    static constexpr int kPad = D + 4;             // floats between heads where warps join
+    // Floats between heads where warps join, and between a thread's runs of channels there (8-bit rows: a thread has D / 8
+    // channels next to each other): no two of the threads that write together share a bank more than twice
+    static constexpr int kRun = E4M3 ? D / 8 + 2 : 8;
+    static constexpr int kPad = 8 * kRun * (E4M3 ? 1 : D / 64) + 4;
+    static __device__ __forceinline__ int channel_at(int ch) { return E4M3 ? ch / (D / 8) * kRun + ch % (D / 8) : ch; }
     static constexpr int kJoin = kWarps * kWarpBytes;
     static constexpr int kBytes = kJoin + 2 * 8 * kPad * 4;
     // 16-byte chunk ch of row r lies at chunk swizzle(ch, r): without it the readers' rows share banks
@@ -170,11 +174,17 @@ struct Place {
     }
 };
 
-// CTA that has unit u when `units` are cut over `ctas`: CTA c has [c * units / ctas, (c + 1) * units / ctas)
-__device__ __forceinline__ int cta_of(int64_t u, int64_t units, int ctas)
-{
-    return static_cast<int>(((u + 1) * ctas + units - 1) / units) - 1;
-}
+// `units` cut over `ctas`: the first units % ctas of them have one more
+struct Cut {
+    int base, rem;
+    __device__ __forceinline__ Cut(int units, int ctas) : base(units / ctas), rem(units % ctas) {}
+    __device__ __forceinline__ int begin(int cta) const { return cta * base + min(cta, rem); }
+    __device__ __forceinline__ int cta_of(int u) const
+    {
+        const int longer = rem * (base + 1);
+        return u < longer ? u / (base + 1) : rem + (u - longer) / base;
+    }
+};
 
 __device__ __forceinline__ size_t slot_of(int c0, int part) { return part == 0 ? 2 * c0 + 1 : 2 * (c0 + part); }
 
@@ -276,9 +286,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
     constexpr int KS = D / 16;  // steps of 16 channels
     constexpr int kTile = R::kTile, kUnit = R::kUnit, kHalves = kTile / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t scan[kWarps];
-    __shared__ int64_t found_rel;
-    __shared__ int found_b;
+    __shared__ int scan[kWarps];
+    __shared__ int found[3];  // sequence, unit within it, length
     __shared__ float st_m[kWarps][8 * NH], st_l[kWarps][8 * NH], st_lp[kWarps][8 * NH];
     __shared__ uint32_t arrived;
     __shared__ Weights weights;
@@ -286,29 +295,24 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
     const int r = lane >> 2, j = lane & 3;
     const int cta = blockIdx.x;
 
-    // sequences without tokens
-    for (int b = cta; b < p.table.B; b += gridDim.x) {
-        if (valid_len(p, b) != 0) continue;
-        for (int i = tid; i < p.H * (D / 8); i += kThreads)
-            *reinterpret_cast<uint4 *>(p.o.p + b * p.o.token + (i / (D / 8)) * p.o.head + (i % (D / 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        if (p.lse)
-            for (int h = tid; h < p.H; h += kThreads) p.lse[static_cast<int64_t>(b) * p.H + h] = -CUDART_INF_F;
-    }
-
-    // units in front of each thread's run of sequences, and of all
+    // units in front of each thread's run of sequences, and of all (the host keeps them below 2^31)
     const int run = (p.table.B + kThreads - 1) / kThreads;
     const int b_lo = min(p.table.B, tid * run), b_hi = min(p.table.B, b_lo + run);
-    int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += (valid_len(p, b) + kUnit - 1) / kUnit;
-    int64_t incl = mine;
+    const int own_len = cta < p.table.B ? valid_len(p, cta) : 1;  // see the end: started with the other loads
+    int mine = 0, len = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        len = valid_len(p, b);
+        mine += (len + kUnit - 1) / kUnit;
+    }
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += y;
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    int64_t units = 0, before = incl - mine;
+    int units = 0, before = incl - mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += scan[w];
@@ -316,17 +320,26 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
     }
     units *= p.HH;
     before *= p.HH;
+    // sequences without tokens
+    for (int b = cta; b < p.table.B; b += gridDim.x) {
+        if ((b == cta ? own_len : valid_len(p, b)) != 0) continue;
+        for (int i = tid; i < p.H * (D / 8); i += kThreads)
+            *reinterpret_cast<uint4 *>(p.o.p + b * p.o.token + (i / (D / 8)) * p.o.head + (i % (D / 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse)
+            for (int h = tid; h < p.H; h += kThreads) p.lse[static_cast<int64_t>(b) * p.H + h] = -CUDART_INF_F;
+    }
     // every CTA that takes part has a unit, so that the parts of a (sequence, head) belong to consecutive ones
-    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), units));
+    const int ctas = min(static_cast<int>(gridDim.x), units);
     if (cta >= ctas) return;
-    const int64_t u_lo = cta * units / ctas, u_hi = (cta + 1) * units / ctas;
+    const Cut cut(units, ctas);
+    const int u_lo = cut.begin(cta), u_hi = cut.begin(cta + 1);
     if (u_lo >= before && u_lo < before + mine * p.HH) {
-        int64_t at = before;
+        int at = before;
         for (int b = b_lo; b < b_hi; ++b) {
-            const int64_t n = static_cast<int64_t>((valid_len(p, b) + kUnit - 1) / kUnit) * p.HH;
+            if (run > 1) len = valid_len(p, b);
+            const int n = (len + kUnit - 1) / kUnit * p.HH;
             if (u_lo < at + n) {
-                found_b = b;
-                found_rel = u_lo - at;
+                found[0] = b, found[1] = u_lo - at, found[2] = len;
                 break;
             }
             at += n;
@@ -334,29 +347,85 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
     }
     __syncthreads();
     Place<kUnit> here;
-    here.b = found_b;
-    here.len = valid_len(p, here.b);
-    here.hu = static_cast<int>(found_rel / here.tiles());
-    here.tile = static_cast<int>(found_rel - static_cast<int64_t>(here.hu) * here.tiles());
+    here.b = found[0];
+    here.len = found[2];
+    here.hu = found[1] / here.tiles();
+    here.tile = found[1] - here.hu * here.tiles();
+
+    // ---- Q of a (sequence, chunk of heads): loads first, the rest when they are needed
+    uint32_t qf[NH][KS][2];
+    float qs[NH][2];  // scale of the scores of heads 2j and 2j + 1
+    auto load_q = [&](const Place<kUnit> &w) {
+        const int kh = w.hu / p.chunks, head0 = (w.hu % p.chunks) * 8 * NH;  // of the group
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const int head = head0 + n * 8 + r;
+            const bool real = head < p.g;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                p.q.p + w.b * p.q.token + static_cast<int64_t>(kh * p.g + (real ? head : 0)) * p.q.head);
+#pragma unroll
+            for (int t = 0; t < KS; ++t) {
+                qf[n][t][0] = qf[n][t][1] = 0u;
+                if (!real) continue;
+                if constexpr (E4M3) {  // channels c .. c + 3, as the thread reads them from K's rows
+                    const int c = D == 128 ? (j + 4 * (t >> 2)) * 16 + 4 * (t & 3) : j * 16 + 4 * t;
+                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src + c / 2));
+                    qf[n][t][0] = x.x, qf[n][t][1] = x.y;
+                } else {
+                    qf[n][t][0] = __ldg(src + t * 8 + j), qf[n][t][1] = __ldg(src + t * 8 + j + 4);
+                }
+            }
+        }
+    };
+    auto ready_q = [&]() {
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            qs[n][0] = qs[n][1] = p.scale;
+            if constexpr (E4M3) {
+                uint32_t big = 0u;
+#pragma unroll
+                for (int t = 0; t < KS; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) big = max(big, max((qf[n][t][k] << 16) & 0x7FFFFFFFu, qf[n][t][k] & 0x7FFF0000u));
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+                // |q| < 2 after division by 2^E; a row below 2^-126 keeps its values (they are zero in fp16)
+                const int E = max(-126, min(126, static_cast<int>(big >> 23) - 127));
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
+                const float up = p.scale * __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
+#pragma unroll
+                for (int t = 0; t < KS; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        qf[n][t][k] = pack_half2(__uint_as_float(qf[n][t][k] << 16) * down,
+                                                 __uint_as_float(qf[n][t][k] & 0xFFFF0000u) * down);
+                qs[n][0] = __shfl_sync(0xFFFFFFFFu, up, 8 * j);
+                qs[n][1] = __shfl_sync(0xFFFFFFFFu, up, 8 * j + 4);
+            }
+        }
+    };
+    load_q(here);
 
     // ---- the warp's ring: `ahead` runs kStages - 1 units in front of `here`
     const uint32_t ring = smem_u32(smem) + warp * R::kWarpBytes;
     Place<kUnit> ahead = here;
-    int64_t issued = u_lo;  // next unit to load
+    int issued = u_lo;  // next unit to load
     const int page_mask = (1 << p.cache.page_shift) - 1;
     auto page_of = [&](const Place<kUnit> &w, int half) -> int {
         const int tok = w.tile * kUnit + warp * kTile + half * 16;
         if (tok >= w.len) return 0;  // no page is looked up; its rows become zeros
         return __ldg(p.table.pages + w.b * p.table.stride + (tok >> p.cache.page_shift));
     };
-    int page[kHalves];  // a tile of 32 tokens may lie in two pages of 16
+    // a tile of 32 tokens may lie in two pages of 16
+    auto pages_of = [&](const Place<kUnit> &w, int (&page)[kHalves]) {
 #pragma unroll
-    for (int h = 0; h < kHalves; ++h) page[h] = page_of(ahead, h);
-    auto load = [&](int stage) {
-        if (issued < u_hi) {
-            const int tok = ahead.tile * kUnit + warp * kTile;
-            const int left = ahead.len - tok;  // tokens of the tile that exist
-            const int kh = ahead.hu / p.chunks;
+        for (int h = 0; h < kHalves; ++h) page[h] = page_of(w, h);
+    };
+    auto copy = [&](int stage, const Place<kUnit> &w, const int (&page)[kHalves]) {
+        const int tok = w.tile * kUnit + warp * kTile;
+        const int left = w.len - tok;  // tokens of the tile that exist
+        if (left > 0) {
+            const int kh = w.hu / p.chunks;
             const uint32_t at = ring + stage * R::kStage;
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
@@ -376,72 +445,51 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                     if (lane < 2)
                         cp_async16(at + 2 * R::kData + lane * kTile + h * 16, (lane ? p.cache.v_exp : p.cache.k_exp) + row, ok ? 16u : 0u);
             }
+        }
+    };
+    int page[kHalves];  // of `ahead`
+    auto load = [&](int stage) {
+        if (issued < u_hi) {
+            copy(stage, ahead, page);
             if (++issued < u_hi) {
                 ahead.next(p);
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h) page[h] = page_of(ahead, h);
+                pages_of(ahead, page);
             }
         }
         cp_async_commit();
     };
+    {  // the first stages: all page numbers are on their way before the first is needed
+        Place<kUnit> first[R::kStages - 1];
+        int first_page[R::kStages - 1][kHalves];
 #pragma unroll
-    for (int s = 0; s < R::kStages - 1; ++s) load(s);
+        for (int s = 0; s < R::kStages - 1; ++s) {
+            first[s] = ahead;
+            if (issued < u_hi) {
+                pages_of(ahead, first_page[s]);
+                if (++issued < u_hi) ahead.next(p);
+            }
+        }
+        if (issued < u_hi) pages_of(ahead, page);
+#pragma unroll
+        for (int s = 0; s < R::kStages - 1; ++s) {
+            if (u_lo + s < u_hi) copy(s, first[s], first_page[s]);
+            cp_async_commit();
+        }
+    }
 
-    uint32_t qf[NH][KS][2];
-    float qs[NH][2];           // scale of the scores of heads 2j and 2j + 1
     float m[NH][2], l[NH][2], lp[NH][2];
     float o[KS][NH][4];        // O^T: rows are channels, columns heads 2j and 2j + 1
     int stage = 0;
-    int64_t u = u_lo;
+    int u = u_lo;
     while (u < u_hi) {
         // ---- a (sequence, chunk of heads): its units in this CTA are [here.tile, end)
         const int tiles = here.tiles(), first = here.tile;
-        const int64_t whole = u - first;  // its first unit
-        const int end = static_cast<int>(min(static_cast<int64_t>(tiles), u_hi - whole));
-        const int kh = here.hu / p.chunks, head0 = (here.hu % p.chunks) * 8 * NH;  // of the group
+        const int whole = u - first;  // its first unit
+        const int end = min(tiles, u_hi - whole);
+        const int b = here.b, kh = here.hu / p.chunks, head0 = (here.hu % p.chunks) * 8 * NH;  // of the group
+        ready_q();
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-            const int head = head0 + n * 8 + r;
-            const bool real = head < p.g;
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(
-                p.q.p + here.b * p.q.token + static_cast<int64_t>(kh * p.g + (real ? head : 0)) * p.q.head);
-            uint32_t big = 0u;
-#pragma unroll
-            for (int t = 0; t < KS; ++t) {
-                if constexpr (E4M3) {  // channels c .. c + 3, as the thread reads them from K's rows
-                    const int c = D == 128 ? (j + 4 * (t >> 2)) * 16 + 4 * (t & 3) : j * 16 + 4 * t;
-                    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(src + c / 2));
-                    qf[n][t][0] = real ? w.x : 0u;
-                    qf[n][t][1] = real ? w.y : 0u;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        big = max(big, (qf[n][t][k] << 16) & 0x7FFFFFFFu);
-                        big = max(big, qf[n][t][k] & 0x7FFF0000u);
-                    }
-                } else {
-                    const uint32_t lo = __ldg(src + t * 8 + j), hi = __ldg(src + t * 8 + j + 4);
-                    qf[n][t][0] = real ? lo : 0u;
-                    qf[n][t][1] = real ? hi : 0u;
-                }
-            }
-            if constexpr (E4M3) {
-                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-                // |q| < 2 after division by 2^E; a row below 2^-126 keeps its values (they are zero in fp16)
-                const int E = max(-126, min(126, static_cast<int>(big >> 23) - 127));
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
-                const float up = p.scale * __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
-#pragma unroll
-                for (int t = 0; t < KS; ++t)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        qf[n][t][k] = pack_half2(__uint_as_float(qf[n][t][k] << 16) * down,
-                                                 __uint_as_float(qf[n][t][k] & 0xFFFF0000u) * down);
-                qs[n][0] = __shfl_sync(0xFFFFFFFFu, up, 8 * j);
-                qs[n][1] = __shfl_sync(0xFFFFFFFFu, up, 8 * j + 4);
-            } else {
-                qs[n][0] = qs[n][1] = p.scale;
-            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) m[n][k] = -CUDART_INF_F, l[n][k] = lp[n][k] = 0.0f;
 #pragma unroll
@@ -608,6 +656,12 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
             stage = stage + 1 == R::kStages ? 0 : stage + 1;
         }
 
+        if (u < u_hi) {  // the next one's Q is on its way while this one's results are put together
+            here.tile = tiles - 1;
+            here.next(p);
+            load_q(here);
+        }
+
         // ---- the four warps' results become one
 #pragma unroll
         for (int n = 0; n < NH; ++n)
@@ -626,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
             }
         __syncthreads();
         const bool is_whole = first == 0 && end == tiles;
-        const int c0 = cta_of(whole, units, ctas), c1 = cta_of(whole + tiles - 1, units, ctas);
+        const int c0 = cut.cta_of(whole), c1 = cut.cta_of(whole + tiles - 1);
         const int parts = c1 - c0 + 1, part = cta - c0;
         float *join = reinterpret_cast<float *>(smem + R::kJoin);
 #pragma unroll
@@ -641,14 +695,21 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
             }
             for (int w = 0; w < 2; ++w) {  // warps 0 and 1, then 2 and 3 into their buffers: the sum has one order
                 if (w == warp >> 1) {
+                    float *to = join + ((warp & 1) * 8 + 2 * j) * R::kPad;
 #pragma unroll
                     for (int t = 0; t < KS; ++t)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int ch = E4M3 ? r * (D / 8) + 2 * t + (k >> 1) : 16 * t + r + 8 * (k >> 1);
-                            float *at = join + ((warp & 1) * 8 + 2 * j + (k & 1)) * R::kPad + ch;
-                            const float x = o[t][n][k] * wt[k & 1];
-                            *at = w == 0 ? x : *at + x;
+                        for (int c = 0; c < 2; ++c) {  // heads 2j and 2j + 1
+                            const float x = o[t][n][c] * wt[c], y = o[t][n][2 + c] * wt[c];
+                            if constexpr (E4M3) {
+                                float2 *at = reinterpret_cast<float2 *>(to + c * R::kPad + r * R::kRun + 2 * t);
+                                const float2 old = w == 0 ? make_float2(0.0f, 0.0f) : *at;
+                                *at = make_float2(old.x + x, old.y + y);
+                            } else {
+                                float *at = to + c * R::kPad + 16 * t + r;
+                                at[0] = w == 0 ? x : at[0] + x;
+                                at[8] = w == 0 ? y : at[8] + y;
+                            }
                         }
                 }
                 __syncthreads();
@@ -666,9 +727,12 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                     res.lp += a * st_lp[w][c];
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) res.o[k] = join[hd * R::kPad + ch + k] + join[(8 + hd) * R::kPad + ch + k];
+                for (int k = 0; k < 8; ++k) {
+                    const int at = hd * R::kPad + R::channel_at(ch + k);
+                    res.o[k] = join[at] + join[8 * R::kPad + at];
+                }
                 if (is_whole) {
-                    write_result(p, here.b, kh * p.g + head0 + c, ch, res);
+                    write_result(p, b, kh * p.g + head0 + c, ch, res);
                 } else {
                     const size_t row = slot_of(c0, part) * kSlotHeads + c;
                     float4 *dst = reinterpret_cast<float4 *>(p.part_o + row * D + ch);
@@ -709,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                     Joined res;
                     if (on) res = join_parts<D>(p, weights, c0, group * kGroup, 1, members, hd, ch);
                     if (final_join) {
-                        if (on) write_result(p, here.b, kh * p.g + head0 + hd, ch, res);
+                        if (on) write_result(p, b, kh * p.g + head0 + hd, ch, res);
                         continue;
                     }
                     __syncthreads();  // this round's heads are read: their first part's slot takes the group's result
@@ -725,14 +789,10 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                     weigh_parts(p, weights, c0, 0, kGroup, groups, heads);
                     for (int i = tid; i < heads * (D / 8); i += kThreads) {
                         const int hd = i / (D / 8), ch = (i % (D / 8)) * 8;
-                        write_result(p, here.b, kh * p.g + head0 + hd, ch, join_parts<D>(p, weights, c0, 0, kGroup, groups, hd, ch));
+                        write_result(p, b, kh * p.g + head0 + hd, ch, join_parts<D>(p, weights, c0, 0, kGroup, groups, hd, ch));
                     }
                 }
             }
-        }
-        if (u < u_hi) {
-            here.tile = tiles - 1;
-            here.next(p);
         }
     }
     cp_async_wait_group<0>();
