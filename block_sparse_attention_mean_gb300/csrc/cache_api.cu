@@ -174,7 +174,7 @@ bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, i
     // units of 64 tokens of all key heads and chunks of query heads are counted in 31 bits
     const int64_t chunks = static_cast<int64_t>(cache->heads) * ((H / cache->heads + 7) / 8);
     const double tokens = static_cast<double>(table->B) * table->width * cache->page_size;
-    if ((tokens / 64 + table->B) * chunks > INT32_MAX) return BSA_ERR_SHAPE;
+    if ((tokens / 64 + 3.0 * table->B) * chunks > INT32_MAX) return BSA_ERR_SHAPE;
     a.kv_lens = kv_lens;
     a.lse = LSE;
     a.H = H;

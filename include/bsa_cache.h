@@ -19,7 +19,8 @@
  *     not looked at): views of a fused projection do, and [heads][T][d]. Tokens and heads of an
  *     output must not overlap.
  *   - Sequence b of B owns tokens [cu[b], cu[b + 1]) of a packed tensor, cu int32 [B + 1], cu[0] >= 0.
- *     Tokens in front of cu[0] and from cu[B] on belong to no sequence: they are neither read nor written.
+ *     Tokens in front of cu[0] and from cu[B] on belong to no sequence: nothing depends on them, and as results
+ *     they are left as they were.
  *   - Query heads share keys in groups: H a multiple of Hk, head h uses key head h / (H / Hk).
  *   - What only the device can see goes to the workspace's first word, which bsa_check_device_error
  *     returns and clears: BSA_ERR_INVALID_ARG for a page outside the cache, a length below zero or
