@@ -1,8 +1,10 @@
 // cache_rows.cu -- rows of keys and values into the pages of a cache (bsa_cache_write) and back (bsa_cache_read).
 //
 // Both move each row once and compute next to nothing: memory bounds them. A row of d channels belongs to d / 8
-// lanes, 16 bytes of bf16 each; a unit of work is kHeads rows (heads) of one token, of K or of V, all loaded before
-// the first is used, so that a thread has 64 bytes in flight and finds its token's sequence and page once for them.
+// lanes, 16 bytes of bf16 each; a unit of work is HEADS rows (heads) of one token, of K or of V, all loaded before
+// the first is used, so that a thread has 64 bytes in flight and finds its token's sequence and page once for them: four
+// rows, and eight of a large 8-bit call, whose arithmetic weighs more (65536 tokens, 16 heads of 128: 173 us written
+// with four, 163 us with eight; bf16 loses 6% with eight, and a call of 64 tokens 0.5 us).
 //
 // 8-bit rows: the exponent of a row is that of its largest magnitude a, found with log2(d / 8) shuffles on the bits of
 // |x| (the order of floats of one sign is that of their bits), two channels in a word (15717 tokens, 8 heads of 128: 25.4 us
@@ -20,7 +22,6 @@ namespace bsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;  // rows of one token that a thread has in flight
 
 // Sequence of packed token t: the last b with cu[b] <= t. False for a token of no sequence, and (with the error
 // raised) of a malformed one. [t - cu[b], cu[b + 1] - cu[b]) is returned as (at, n).
@@ -71,7 +72,7 @@ __device__ __forceinline__ int row_exp(uint32_t a)
 }
 
 // The unit (token, K or V, group of heads) of a thread, and its lane within a row
-template <int D>
+template <int D, int HEADS>
 struct Unit {
     int t, kv, h0, lane;
     bool any;
@@ -82,7 +83,7 @@ struct Unit {
         lane = threadIdx.x % LPR;
         any = u < T * 2 * groups;
         const int64_t r = u / groups;
-        h0 = static_cast<int>(u - r * groups) * kHeads;
+        h0 = static_cast<int>(u - r * groups) * HEADS;
         t = static_cast<int>(r >> 1);
         kv = static_cast<int>(r & 1);
     }
@@ -94,17 +95,17 @@ __device__ __forceinline__ int64_t row_of(const CacheView &c, int page, int head
     return ((static_cast<int64_t>(page) * c.heads + head) << c.page_shift) + row;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int HEADS>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheRowsArgs a, int groups)
 {
     constexpr int LPR = D / 8;
-    const Unit<D> u(a.T, groups);
+    const Unit<D, HEADS> u(a.T, groups);
     // the rows are on their way while their place is looked up: the tensor has them, whether a sequence does or not
     const PackedView &src = u.kv ? a.v : a.k;
-    int heads = u.any ? min(kHeads, a.cache.heads - u.h0) : 0;
-    uint4 x[kHeads];
+    int heads = u.any ? min(HEADS, a.cache.heads - u.h0) : 0;
+    uint4 x[HEADS];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
+    for (int i = 0; i < HEADS; ++i) {
         x[i] = make_uint4(0u, 0u, 0u, 0u);
         if (i < heads)
             x[i] = __ldg(reinterpret_cast<const uint4 *>(src.p + u.t * src.token + (u.h0 + i) * src.head) + u.lane);
@@ -130,12 +131,12 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheRowsAr
     char *data = u.kv ? a.cache.v : a.cache.k;
     if constexpr (!E4M3) {
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i)
+        for (int i = 0; i < HEADS; ++i)
             if (i < heads) reinterpret_cast<uint4 *>(data)[row_of(a.cache, page, u.h0 + i, row) * LPR + u.lane] = x[i];
     } else {
         uint8_t *exps = u.kv ? a.cache.v_exp : a.cache.k_exp;
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
+        for (int i = 0; i < HEADS; ++i) {
             uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             // magnitudes by their bits, two channels at a time; what is not finite counts as zero
             uint32_t big = 0u, odd = 0u;
@@ -155,7 +156,11 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheRowsAr
             }
             uint32_t q[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) q[k] = to_e4m3x2(bf16_lo(w[k]) * unit, bf16_hi(w[k]) * unit);
+            for (int k = 0; k < 4; ++k) {
+                float lo, hi;  // subnormals as zeros: at most 2^-26 after the product, far below the least step
+                f2_unpack(f2_fma(f2_pack(bf16_lo(w[k]), bf16_hi(w[k])), f2_pack(unit, unit), 0ull), lo, hi);
+                q[k] = to_e4m3x2(lo, hi);
+            }
             if (i < heads) {
                 const int64_t r = row_of(a.cache, page, u.h0 + i, row);
                 reinterpret_cast<uint2 *>(data)[r * LPR + u.lane] = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
@@ -177,11 +182,11 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w, float unit)
     return pack_bf16x2(lo * unit, hi * unit);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int HEADS>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArgs a, int groups)
 {
     constexpr int LPR = D / 8;
-    const Unit<D> u(a.T, groups);
+    const Unit<D, HEADS> u(a.T, groups);
     if (!u.any) return;
     int b = 0, at = 0, n = 0, page = 0, row = 0;
     if (!find_sequence(a.cu, a.table.B, a.T, u.t, b, at, n, a.err)) return;
@@ -196,12 +201,12 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArg
     const PackedView &dst = u.kv ? a.v : a.k;
     const char *data = u.kv ? a.cache.v : a.cache.k;
     const uint8_t *exps = u.kv ? a.cache.v_exp : a.cache.k_exp;
-    const int heads = min(kHeads, a.cache.heads - u.h0);
-    uint4 x[kHeads];
-    uint2 w[kHeads];
-    int e[kHeads];
+    const int heads = min(HEADS, a.cache.heads - u.h0);
+    uint4 x[HEADS];
+    uint2 w[HEADS];
+    int e[HEADS];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
+    for (int i = 0; i < HEADS; ++i) {
         x[i] = make_uint4(0u, 0u, 0u, 0u);
         w[i] = make_uint2(0u, 0u);
         e[i] = 127;
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArg
         }
     }
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
+    for (int i = 0; i < HEADS; ++i) {
         if (i >= heads) continue;
         if constexpr (E4M3) {
             // bytes of 0, 255 and others that no row written by this library has are taken as they stand
@@ -228,10 +233,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArg
     }
 }
 
-template <typename Kernel>
+template <int HEADS, typename Kernel>
 bsa_status launch_rows(Kernel kern, const CacheRowsArgs &a, cudaStream_t st)
 {
-    const int groups = (a.cache.heads + kHeads - 1) / kHeads;
+    const int groups = (a.cache.heads + HEADS - 1) / HEADS;
     const int64_t threads = static_cast<int64_t>(a.T) * 2 * groups * (a.d / 8);
     const int64_t ctas = (threads + kThreads - 1) / kThreads;
     if (ctas > INT32_MAX) return BSA_ERR_SHAPE;
@@ -240,18 +245,30 @@ bsa_status launch_rows(Kernel kern, const CacheRowsArgs &a, cudaStream_t st)
     return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
+// eight rows a thread: 8-bit rows, enough of them to fill the device (152 SMs of 1024 threads) all the same
+bool eight(const CacheRowsArgs &a)
+{
+    return a.cache.e4m3 && static_cast<int64_t>(a.T) * 2 * ((a.cache.heads + 7) / 8) * (a.d / 8) >= 152 * 1024;
+}
+
+template <int D>
+bsa_status launch_write(const CacheRowsArgs &a, cudaStream_t st)
+{
+    if (eight(a)) return launch_rows<8>(cache_write_kernel<D, true, 8>, a, st);
+    return a.cache.e4m3 ? launch_rows<4>(cache_write_kernel<D, true, 4>, a, st) : launch_rows<4>(cache_write_kernel<D, false, 4>, a, st);
+}
+
+template <int D>
+bsa_status launch_read(const CacheRowsArgs &a, cudaStream_t st)
+{
+    if (eight(a)) return launch_rows<8>(cache_read_kernel<D, true, 8>, a, st);
+    return a.cache.e4m3 ? launch_rows<4>(cache_read_kernel<D, true, 4>, a, st) : launch_rows<4>(cache_read_kernel<D, false, 4>, a, st);
+}
+
 }  // namespace
 
-bsa_status launch_cache_write(const CacheRowsArgs &a, cudaStream_t st)
-{
-    if (a.d == 128) return a.cache.e4m3 ? launch_rows(cache_write_kernel<128, true>, a, st) : launch_rows(cache_write_kernel<128, false>, a, st);
-    return a.cache.e4m3 ? launch_rows(cache_write_kernel<64, true>, a, st) : launch_rows(cache_write_kernel<64, false>, a, st);
-}
+bsa_status launch_cache_write(const CacheRowsArgs &a, cudaStream_t st) { return a.d == 128 ? launch_write<128>(a, st) : launch_write<64>(a, st); }
 
-bsa_status launch_cache_read(const CacheRowsArgs &a, cudaStream_t st)
-{
-    if (a.d == 128) return a.cache.e4m3 ? launch_rows(cache_read_kernel<128, true>, a, st) : launch_rows(cache_read_kernel<128, false>, a, st);
-    return a.cache.e4m3 ? launch_rows(cache_read_kernel<64, true>, a, st) : launch_rows(cache_read_kernel<64, false>, a, st);
-}
+bsa_status launch_cache_read(const CacheRowsArgs &a, cudaStream_t st) { return a.d == 128 ? launch_read<128>(a, st) : launch_read<64>(a, st); }
 
 }  // namespace bsa
