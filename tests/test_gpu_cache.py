@@ -348,3 +348,65 @@ def test_bad_pages_and_lengths_are_reported():
     assert (out[1] == 0).all() and (lse[1] == float("-inf")).all()
     with pytest.raises(bb.BsaError):
         pkg.cache_check(ws)
+
+
+# ------------------------------------------------------------------ large
+
+
+def test_large_calls_take_eight_rows_a_thread():
+    """8-bit calls of many rows, written and read with eight heads a thread, heads that are no multiple of it"""
+    g = gen(11)
+    for Hk, d, n in ((12, 128, 5000), (9, 64, 9000)):
+        table, n_pages = paged(g, [n, 7], 64)
+        cache = pkg.kv_cache(n_pages, 64, Hk, d, "e4m3", DEV)
+        k, v = rows(g, n + 7, Hk, d)
+        pkg.cache_write(cache, k, v, table, ints([n, 7]), starts([n, 7]))
+        for got, x in zip(pkg.cache_read(cache, table, starts([n, 7]), n + 7), (k, v)):
+            assert torch.equal(got.double(), ref.e4m3_rows(x)[0])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(kind):
+    """a cache of more than 2^32 bytes a tensor, the sequences' pages at its end"""
+    g = gen(12)
+    Hk, d, page = 8, 128, 256
+    row = Hk * page * d * (2 if kind == "bf16" else 1)
+    n_pages = (1 << 32) // row + 40
+    cache = pkg.kv_cache(n_pages, page, Hk, d, kind, DEV)
+    held = [1000, 300]
+    table = torch.zeros(2, 4, dtype=torch.int32, device=DEV)
+    table[0, :4] = torch.arange(n_pages - 4, n_pages, device=DEV)
+    table[1, :2] = torch.tensor([n_pages - 9, 3], device=DEV)
+    k, v = rows(g, sum(held), Hk, d)
+    pkg.cache_write(cache, k, v, table, ints(held), starts(held))
+    got = pkg.cache_read(cache, table, starts(held), sum(held))
+    held_values = [x.double() if kind == "bf16" else ref.e4m3_rows(x)[0] for x in (k, v)]
+    assert all(torch.equal(a.double(), b) for a, b in zip(got, held_values))
+    q = draw(g, 2, Hk, d).to(BF16)
+    out, lse = pkg.cache_attention(q, cache, table, ints(held))
+    at = 0
+    for b, n in enumerate(held):
+        for h in range(Hk):
+            see = torch.ones(1, n, dtype=torch.bool, device=DEV)
+            o, bo, l, bl = ref.attention(q[b, h][None], held_values[0][at:at + n, h], held_values[1][at:at + n, h], see, d ** -0.5,
+                                         half_weights=kind == "e4m3")
+            ref.within(out[b, h][None], o, bo, "O")
+            ref.within(lse[b, h][None], l, bl, "LSE")
+        at += n
+
+
+def test_cache_attention_keeps_infinities_and_nan_of_its_own_keys():
+    g = gen(13)
+    held, page, H, Hk, d = [90, 90], 16, 4, 2, 64
+    table, n_pages = paged(g, held, page)
+    cache, values = filled(g, n_pages, page, Hk, d, "bf16")
+    q = draw(g, 2, H, d).to(BF16)
+    p, r = table[0, 70 // page].long(), 70 % page
+    cache.v[p, 0, r, 5] = float("inf")
+    cache.v[p, 1, r, 9] = float("nan")
+    out, lse = pkg.cache_attention(q, cache, table, ints(held))
+    check_decode(q[1:], cache, values, table[1:], held[1:], page, "bf16", out=out[1:], lse=lse[1:])
+    assert (out[0, :2, 5] == float("inf")).all() and out[0, 2:, 9].isnan().all()
+    keep = torch.ones(H, d, dtype=torch.bool, device=DEV)
+    keep[:2, 5] = keep[2:, 9] = False
+    assert out[0][keep].isfinite().all() and lse.isfinite().all()

@@ -216,3 +216,219 @@ def test_a_wait_that_runs_out_is_reported():
         bb.bsa_debug_config(0, 0)
     b = pkg.prompt_attention(q, k, v, ints(cu), ws=ws)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_cut_sequences_of_equal_length_give_the_same_bits():
+    """few items, cut evenly over the CTAs: where the cuts fall does not vary from call to call"""
+    g = gen(10)
+    cu_q, cu_k = starts([64] * 5), starts([4000] * 5)
+    q, k, v = draw(g, cu_q[-1], 4, 64), draw(g, cu_k[-1], 2, 64), draw(g, cu_k[-1], 2, 64)
+    a = check(q, k, v, cu_q, cu_k, False)
+    for _ in range(10):
+        b = pkg.prompt_attention(q, k, v, ints(cu_q), ints(cu_k), causal=False)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+LONG = [
+    # many items, taken from the counter; more sequences than a plan holds in shared memory; mixed heads
+    (4, 4, 128, [2500, 1, 900, 2500, 130], None, True),
+    (2, 1, 64, [5 + i * 37 % 90 for i in range(300)], [i * 11 % 700 for i in range(300)], True),
+    (6, 2, 128, [1200, 64], [300, 5000], True),
+    (8, 8, 64, [1500, 1500], None, False),
+]
+
+
+@pytest.mark.parametrize("H,Hk,d,new,past,causal", LONG)
+def test_longer_prompts(H, Hk, d, new, past, causal):
+    g = gen(11)
+    cu_q = starts(new)
+    cu_k = cu_q if past is None else starts([a + b for a, b in zip(new, past)])
+    q, k, v = draw(g, cu_q[-1], H, d), draw(g, cu_k[-1], Hk, d), draw(g, cu_k[-1], Hk, d)
+    check(q, k, v, cu_q, cu_k, causal)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_short_items_of_every_kind(seed):
+    """hundreds of tiles of one to three steps, one after another in a CTA, empty ones among them"""
+    g = gen(20 + seed)
+    r = torch.Generator().manual_seed(seed)
+    n = 60
+    new = torch.randint(0, 300, (n,), generator=r).tolist()
+    keys = [max(0, a + int(x)) for a, x in zip(new, torch.randint(-200, 200, (n,), generator=r))]
+    cu_q, cu_k = starts(new), starts(keys)
+    H, Hk, d = [(6, 2, 128), (4, 4, 64), (8, 1, 128), (3, 3, 128), (16, 8, 64), (5, 1, 64)][seed]
+    q, k, v = draw(g, cu_q[-1], H, d), draw(g, cu_k[-1], Hk, d), draw(g, cu_k[-1], Hk, d)
+    check(q, k, v, cu_q, cu_k, seed % 2 == 0)
+
+
+# ------------------------------------------------------------------ the four calls together
+
+
+def new_tokens(g, n, H, Hk, d):
+    x = draw(g, n, H + 2 * Hk, d)
+    return x.split([H, Hk, Hk], dim=1)
+
+
+@pytest.mark.parametrize("kind,H,Hk,d,page", [("bf16", 6, 2, 128, 16), ("e4m3", 8, 8, 64, 64), ("e4m3", 12, 4, 128, 32)])
+def test_prompts_then_a_later_chunk_then_tokens_one_by_one(kind, H, Hk, d, page):
+    """as a model that answers uses them: prompts attend to themselves and go into the cache; a later chunk of each reads the
+    cache back and attends to all of it; then tokens come one by one. Every result against the 64-bit form over what
+    the cache holds."""
+    g = gen(30)
+    prompts, chunks, steps = [100, 1, 333], [20, 65, 7], 5
+    B, most = 3, 512
+    table = torch.randperm(B * (most // page), generator=g, device=DEV).to(torch.int32).view(B, most // page)
+    cache = pkg.kv_cache(B * (most // page), page, Hk, d, kind, DEV)
+    ws = pkg.cache_workspace(sum(prompts), B, H, Hk, d, DEV)
+    held = [0] * B
+    keys, values = ([torch.empty(0, Hk, d, dtype=BF16, device=DEV) for _ in range(B)] for _ in range(2))
+
+    def append(new, k, v):
+        at = 0
+        for b, n in enumerate(new):
+            for x, seen in ((k, keys), (v, values)):
+                fresh = x[at:at + n]
+                seen[b] = torch.cat((seen[b], fresh if kind == "bf16" else ref.e4m3_rows(fresh)[0].to(BF16)))
+            at += n
+            held[b] += n
+
+    q, k, v = new_tokens(g, sum(prompts), H, Hk, d)
+    check(q, k, v, starts(prompts), starts(prompts), True, ws=ws)
+    append(prompts, k, v)
+    pkg.cache_write(cache, k, v, table, ints(held), ints(starts(prompts)), ws=ws)
+
+    q, k, v = new_tokens(g, sum(chunks), H, Hk, d)
+    append(chunks, k, v)
+    pkg.cache_write(cache, k, v, table, ints(held), ints(starts(chunks)), ws=ws)
+    all_k, all_v = pkg.cache_read(cache, table, ints(starts(held)), sum(held), ws=ws)
+    assert torch.equal(all_k, torch.cat(keys)) and torch.equal(all_v, torch.cat(values))
+    check(q, all_k, all_v, starts(chunks), starts(held), True, ws=ws)
+
+    for _ in range(steps):
+        q, k, v = new_tokens(g, B, H, Hk, d)
+        append([1] * B, k, v)
+        pkg.cache_write(cache, k, v, table, ints(held), ws=ws)
+        out, lse = pkg.cache_attention(q, cache, table, ints(held), ws=ws)
+        for b in range(B):
+            for h in range(H):
+                kh = h // (H // Hk)
+                see = torch.ones(1, held[b], dtype=torch.bool, device=DEV)
+                o, bo, l, bl = ref.attention(q[b, h][None], keys[b][:, kh], values[b][:, kh], see, d ** -0.5, half_weights=kind == "e4m3")
+                ref.within(out[b, h][None], o, bo, "O")
+                ref.within(lse[b, h][None], l, bl, "LSE")
+
+
+def test_rotary_outputs_are_inputs():
+    """bsa_rotary's q, k, v [1, H, T, d] as packed views, and the block-sparse forward with every block over the same tokens"""
+    g = gen(31)
+    T, H, d = 512, 4, 128
+    plan = pkg.rotary_plan(d, axis_dims=[d])
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)[:, None]
+    q, k, v = pkg.rotary(plan, *(draw(g, 1, T, H, d) for _ in range(3)), positions=pos)
+    pq, pk, pv = (x[0].transpose(0, 1) for x in (q, k, v))
+    out, lse = check(pq, pk, pv, [0, T], [0, T], False)
+    nb = T // 128
+    ones = torch.full((nb,), -1, dtype=torch.int32, device=DEV)
+    full = bb.build_mask(None, None, block=128, spec=bb.explicit_spec(ones, broadcast_bh=True), shape=q.shape)
+    O, L = bb.forward(q, k, v, full)
+    o, bo, l, bl = expected(pq, pk, pv, [0, T], [0, T], False, d ** -0.5)
+    ref.within(O[0].transpose(0, 1), o, bo, "block-sparse O")
+    ref.within(L[0], l, bl, "block-sparse LSE")
+
+
+class Loop:
+    """one sequence of tokens through the cache, with everything allocated: what a captured decoding step holds"""
+
+    def __init__(self, g, kind="e4m3", B=4, H=8, Hk=2, d=128, page=32, most=256):
+        self.q, self.k, self.v = new_tokens(g, B, H, Hk, d)
+        self.table = torch.randperm(B * (most // page), generator=g, device=DEV).to(torch.int32).view(B, most // page)
+        self.cache = pkg.kv_cache(B * (most // page), page, Hk, d, kind, DEV)
+        self.held = ints([100, 1, 37, 200])
+        past_k, past_v = draw(g, 338, Hk, d), draw(g, 338, Hk, d)
+        pkg.cache_write(self.cache, past_k, past_v, self.table, self.held, ints(starts([100, 1, 37, 200])))
+        self.out, self.lse = torch.empty(B, H, d, dtype=BF16, device=DEV), torch.empty(B, H, device=DEV)
+        self.args = dict(H=H, Hk=Hk, d=d)
+
+    def step(self, ws, stream=None):
+        self.held += 1
+        pkg.cache_write(self.cache, self.k, self.v, self.table, self.held, ws=ws, check=False)
+        pkg.cache_attention(self.q, self.cache, self.table, self.held, out=self.out, lse=self.lse, ws=ws, check=False)
+
+    def expected(self):
+        fresh = pkg.cache_workspace(4, 4, self.args["H"], self.args["Hk"], self.args["d"], DEV)
+        return pkg.cache_attention(self.q, self.cache, self.table, self.held, ws=fresh)
+
+
+def test_a_captured_step_replayed_and_two_graphs_with_one_workspace():
+    g = gen(32)
+    a, b = Loop(g), Loop(g, kind="bf16")
+    ws = pkg.cache_workspace(4, 4, 8, 2, 128, DEV)
+    graphs = []
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        for x in (a, b):
+            x.step(ws)  # a first call outside
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                x.step(ws)
+            graphs.append(graph)
+        for _ in range(3):
+            for graph in graphs:
+                graph.replay()
+        stream.synchronize()
+    pkg.cache_check(ws)
+    for x in (a, b):
+        assert x.held.tolist() == [104, 5, 41, 204]
+        o, l = x.expected()
+        assert torch.equal(x.out, o) and torch.equal(x.lse, l)
+
+
+def test_captured_prompts_replayed_with_other_lengths():
+    """the lengths live on the device: a captured call follows them"""
+    g = gen(33)
+    T, H, Hk, d = 900, 4, 2, 64
+    q, k, v = new_tokens(g, T, H, Hk, d)
+    cu = ints([0, 300, 300, 900])
+    out, lse = torch.empty(T, H, d, dtype=BF16, device=DEV), torch.empty(H, T, device=DEV)
+    ws = pkg.cache_workspace(T, 3, H, Hk, d, DEV)
+    pkg.prompt_attention(q, k, v, cu, out=out, lse=lse, ws=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkg.prompt_attention(q, k, v, cu, out=out, lse=lse, ws=ws, check=False)
+    for lens in ([0, 1, 450, 900], [0, 900, 900, 900], [0, 128, 640, 900]):
+        cu.copy_(ints(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        o, bo, l, bl = expected(q, k, v, lens, lens, True, d ** -0.5)
+        ref.within(out, o, bo, "O")
+        ref.within(lse, l, bl, "LSE")
+
+
+def test_two_streams_with_a_workspace_each():
+    g = gen(34)
+    loops = [Loop(g), Loop(g, kind="bf16")]
+    streams = [torch.cuda.Stream() for _ in loops]
+    torch.cuda.synchronize()
+    spaces = [pkg.cache_workspace(4, 4, 8, 2, 128, DEV) for _ in loops]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, s, ws in zip(loops, streams, spaces):
+            with torch.cuda.stream(s):
+                x.step(ws)
+    torch.cuda.synchronize()
+    for x, ws in zip(loops, spaces):
+        pkg.cache_check(ws)
+        o, l = x.expected()
+        assert torch.equal(x.out, o) and torch.equal(x.lse, l)
+
+
+def test_the_stream_argument_orders_the_calls():
+    g = gen(35)
+    q, k, v = new_tokens(g, 500, 4, 2, 128)
+    cu = ints([0, 500])
+    want = pkg.prompt_attention(q, k, v, cu)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = pkg.prompt_attention(q, k, v, cu, stream=s)
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
