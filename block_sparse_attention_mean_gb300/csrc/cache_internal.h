@@ -15,6 +15,7 @@ namespace bsa {
 // Workspace of the four calls: the header of internal.h (its first word is the error word), then the tickets of
 // bsa_cache_attention, which every call leaves zero, then whatever the call at hand keeps there.
 constexpr int kCacheMaxCtas = 640;  // CTAs of a bsa_cache_attention launch
+constexpr size_t kCacheCounter = kWsHeader - 2 * sizeof(uint32_t);  // two words of bsa_prompt_attention, zero between calls too
 constexpr size_t kCacheTickets = kWsHeader;
 constexpr size_t kCacheScratch = BSA_CACHE_ROWS_WORKSPACE;
 static_assert(kCacheTickets + sizeof(uint32_t) * 3 * kCacheMaxCtas <= kCacheScratch, "room for the tickets");

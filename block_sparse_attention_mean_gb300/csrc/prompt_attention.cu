@@ -59,10 +59,11 @@ constexpr unsigned long long kDrainNs = 1000000000ull;  // copies and products i
 constexpr int kMaxSlots = 320;       // partial results (a tile each): two per CTA
 constexpr int kMaxCutItems = 65536;  // items (of all key heads) up to which the steps are cut evenly
 constexpr int kCutSteps = 8;          // what a cut has to save, in steps
-// No item longer than that: the steps are never cut. With at most 32 sequences besides, the loading warps plan for themselves,
-// a lane a sequence, and the call is one launch (four sequences of 12 to 128 tokens, 24 heads of 64: 8 us on the device, 15 us
-// with a plan).
-constexpr int kShortKeys = kCutSteps * kStep;
+constexpr int kShortKeys = kCutSteps * kStep;  // no item longer than that: the steps are never cut
+// At most so many sequences and tiles: each CTA's loading warp makes the plan for itself, a lane a sequence, while the
+// others set up. (A launch of its own took 6 to 11 us; two launches of the call are left, one without long sequences.
+// Four sequences of 12 to 128 tokens, 24 heads of 64: 8 us on the device, 15 us with a plan's launch.)
+constexpr int kWarpPlan = 32, kWarpItems = 4096;
 constexpr int kPlanThreads = 1024;
 constexpr int kSmallPlan = 256, kSmallItems = 2048;  // sequences and items that a plan holds in shared memory
 
@@ -73,7 +74,8 @@ struct __align__(16) Entry {
     int slot;       // of its partial result, or -1: it is whole
     int pad[2];
 };
-// An item in parts: the first is the last of CTA c0, the others the first of the CTAs after it
+// An item in parts, in the record of the CTA c0 whose last one is the first of them (the others are the first of the CTAs
+// after it). parts 0: none.
 struct __align__(16) Split {
     int q0, tokens, kh, c0, parts;  // first query (packed) and how many there are of the tile
     int pad[3];
@@ -81,8 +83,9 @@ struct __align__(16) Split {
 __host__ __device__ constexpr int slot_of(int c0, int part) { return part == 0 ? 2 * c0 + 1 : 2 * (c0 + part); }
 
 struct PlanHeader {  // in the workspace, behind the tickets
-    uint32_t next, n_items, n_splits;
+    uint32_t next, n_items;
     int cut;  // CTAs that the steps are cut over; 0: items come from the counter
+    int pad;
 };
 
 struct Seqs {
@@ -142,6 +145,33 @@ struct PlanArgs {
     Split *splits;
     uint32_t *err;
 };
+
+// CTAs that the steps are cut over, or 0: with items from a counter no CTA works much longer than the average. That one
+// would have whole rounds of items where all are as long, else about its share and what is left of an item at the
+// end. Cutting costs about eight steps (partial results, the join), and spreads the CTAs over all heads, whose K and V then
+// share L2: it has to gain an eighth of the share besides.
+__device__ __forceinline__ int cut_over(long long n_items, long long steps, int longest, int ctas)
+{
+    const long long share = max(1ll, (steps + ctas - 1) / ctas), rounds = (n_items + ctas - 1) / ctas;
+    const long long uncut = steps == n_items * longest || rounds == 1 ? rounds * longest
+                                                                      : max(static_cast<long long>(longest), share + longest / 8);
+    if (n_items > kMaxCutItems || 2 * ctas > kMaxSlots || uncut <= share + share / 8 + kCutSteps) return 0;
+    return static_cast<int>(max(1ll, min(static_cast<long long>(ctas), steps)));
+}
+// The record of an item of which CTA c has the first part; `end`: the steps up to its last one
+__device__ __forceinline__ Split split_of(const Seqs &s, const Seq &q, int t0, int kh, int c, long long end, long long total, int ctas)
+{
+    const int last = static_cast<int>((end * ctas + total - 1) / total) - 1;  // CTA of its last step
+    return Split{q.q0 + t0, min(s.tpt, q.n_q - t0), kh, c, last - c + 1, {0, 0, 0}};
+}
+
+// Item `rest` of a sequence of n tiles: the last `mixed` heads tile by tile, the others head by head; last tiles first
+__device__ __forceinline__ void item_of(int rest, int n, int Hk, int ctas, int tpt, int &kh, int &t0)
+{
+    const int mixed = min(Hk, (2 * ctas + n - 1) / n), in_order = (Hk - mixed) * n, tail = rest - in_order;
+    kh = tail < 0 ? rest / n : Hk - mixed + tail % mixed;
+    t0 = (n - 1 - (tail < 0 ? rest % n : tail / mixed)) * tpt;
+}
 
 // Exclusive prefix over the block's threads, and the total
 __device__ __forceinline__ long long block_prefix(long long v, long long &total, long long *warp_sums)
@@ -225,10 +255,7 @@ __device__ int walk_cut(const PlanArgs &a, int c, int ctas, long long from, long
                     e.hi = more ? static_cast<int>(to - at) : steps;
                     e.slot = skip > 0 ? 2 * c : more ? 2 * c + 1 : -1;
                     out[count] = e;
-                    if (skip == 0 && more) {
-                        const int last = static_cast<int>((end * ctas + total - 1) / total) - 1;  // CTA of its last step
-                        a.splits[atomicAdd(&a.hdr->n_splits, 1u)] = Split{q.q0 + e.t0, min(s.tpt, q.n_q - e.t0), kh, c, last - c + 1, {0, 0, 0}};
-                    }
+                    if (skip == 0 && more) a.splits[c] = split_of(s, q, e.t0, kh, c, end, total, ctas);
                 }
                 ++count;
                 if (more) return count;
@@ -317,15 +344,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
     }
     const bool sound = all_items <= a.max_items;  // else sequences overlap: more tokens than there are
     if (!sound) raise_error(a.err, BSA_ERR_INVALID_ARG);
-    // The steps of the CTA that works longest when items come from the counter: whole rounds where all are as long, else about
-    // the share and what is left of an item at the end. Cutting costs about eight steps (partial results, the join), and spreads
-    // the CTAs over all heads, whose K and V then share L2: it has to gain an eighth of the share besides.
-    const long long n_items = all_items * s.Hk, share = max(1ll, (all_steps + a.ctas - 1) / a.ctas);
-    const long long rounds = (n_items + a.ctas - 1) / a.ctas;
-    const long long uncut = all_steps == n_items * longest || rounds == 1 ? rounds * longest
-                                                                          : max(static_cast<long long>(longest), share + longest / 8);
-    const bool cut = sound && n_items <= kMaxCutItems && 2 * a.ctas <= kMaxSlots && uncut > share + share / 8 + kCutSteps;
-    const int ctas = static_cast<int>(max(1ll, min(static_cast<long long>(a.ctas), all_steps)));
+    const int ctas = sound ? cut_over(all_items * s.Hk, all_steps, longest, a.ctas) : 0;
     if (pl.rank != a.rank)
         for (int r = lo; r < hi; ++r) a.rank[r] = pl.rank[r], a.item0[r] = pl.item0[r];
     if (all_items <= kSmallItems) pl.item_step0 = s_item_step0;
@@ -333,10 +352,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a)
         a.item0[s.B] = pl.item0[s.B] = sound ? static_cast<int>(all_items) : 0;
         a.hdr->next = 0u;
         a.hdr->n_items = sound ? static_cast<uint32_t>(all_items) * static_cast<uint32_t>(s.Hk) : 0u;
-        a.hdr->n_splits = 0u;
-        a.hdr->cut = cut ? ctas : 0;
+        a.hdr->cut = ctas;
     }
-    if (!cut) return;
+    if (!ctas) return;
+    if (tid < ctas) a.splits[tid].parts = 0;
     __syncthreads();
     for (int r = warp; r < s.B; r += 32) {
         const Seq q = seq_of(s, pl.rank[r], a.err);
@@ -374,6 +393,8 @@ struct Params {
     PlanHeader *hdr;
     const int32_t *rank, *item0, *first;
     const Entry *entries;
+    Split *splits;
+    uint32_t *counter;  // without a plan: the next item, and CTAs that are done (both zero between calls)
     float *part_o;       // [slot][128][D]
     float2 *part_stats;  // [slot][128] (max in log2, sum)
     uint32_t *err;
@@ -471,6 +492,166 @@ __device__ __forceinline__ void done_with(uint32_t sbase, int lane, int count)
     __syncwarp();
     if (lane == 0) mbar_arrive(sbase + C::BAR_OFF + 8u * (C::B_TEMPTY + (count - 1) % kRing));
 }
+
+// The plan of a warp for itself: lane r has the r-th longest sequence
+struct WarpPlan {
+    int b, items, n_q, n_k;     // the lane's sequence
+    int item_end;               // items of the ranks up to the lane's
+    long long step0, head;      // steps of all heads of the ranks before, steps of one head of this one
+    uint32_t n_items;
+    int cut;
+    // where the steps are cut: this CTA's range, and where it is in it
+    long long total, at, to;
+    int r, kh, i, skip;
+
+    __device__ __forceinline__ void make(const Params &p, int lane)
+    {
+        const Seqs &s = p.s;
+        Seq q{0, 0, 0, 0};
+        if (lane < s.B) q = seq_of(s, lane, p.err);
+        const int key = q.n_q > 0 ? visible(s.causal, q.n_q, q.n_k, q.n_q - 1) : -1;
+        int rank = 0, from = lane;  // lanes without a sequence come last, in order
+        for (int j = 0; j < s.B; ++j) {
+            const int other = __shfl_sync(0xFFFFFFFFu, key, j);
+            rank += other > key || (other == key && j < lane);
+        }
+        for (int j = 0; j < s.B; ++j)
+            if (__shfl_sync(0xFFFFFFFFu, rank, j) == lane && lane < s.B) from = j;
+        b = from;
+        n_q = __shfl_sync(0xFFFFFFFFu, q.n_q, from);
+        n_k = __shfl_sync(0xFFFFFFFFu, q.n_k, from);
+        items = (n_q + s.tpt - 1) / s.tpt;
+        item_end = items;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, item_end, o);
+            if (lane >= o) item_end += y;
+        }
+        const int all = __shfl_sync(0xFFFFFFFFu, item_end, 31);
+        const bool sound = all <= p.max_items;  // else sequences overlap
+        if (!sound) raise_error(p.err, BSA_ERR_INVALID_ARG);
+        n_items = sound ? static_cast<uint32_t>(all) * static_cast<uint32_t>(s.Hk) : 0u;
+        cut = 0;
+        head = 0;
+        if (s.Tk > kShortKeys && sound) {
+            int longest = 0;
+            for (int j = 0; j < s.B; ++j) {
+                const int nq = __shfl_sync(0xFFFFFFFFu, n_q, j), nk = __shfl_sync(0xFFFFFFFFu, n_k, j), n = __shfl_sync(0xFFFFFFFFu, items, j);
+                long long wide = 0;
+                for (int t = lane; t < n; t += 32) {
+                    const int m = steps_of(s.causal, nq, nk, t * s.tpt, s.tpt);
+                    wide += m;
+                    longest = max(longest, m);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xFFFFFFFFu, wide, o);
+                if (lane == j) head = wide;
+            }
+            longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+            long long end = head * s.Hk;
+            step0 = end;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, end, o);
+                if (lane >= o) end += y;
+            }
+            step0 = end - step0;
+            total = __shfl_sync(0xFFFFFFFFu, end, 31);
+            cut = cut_over(n_items, total, longest, gridDim.x);
+        }
+        if (blockIdx.x == 0 && lane == 0) p.hdr->cut = cut;  // for the join
+        if (cut) begin_parts(p, lane);
+    }
+
+    // item `id` where they come from the counter
+    __device__ __forceinline__ void item(const Params &p, int id, Item &it) const
+    {
+        const int of = id / p.s.Hk, j = __popc(__ballot_sync(0xFFFFFFFFu, item_end <= of));  // the first that ends behind it
+        const int n = __shfl_sync(0xFFFFFFFFu, items, j), base = __shfl_sync(0xFFFFFFFFu, item_end, j) - n;
+        it.b = __shfl_sync(0xFFFFFFFFu, b, j);
+        it.lo = 0;
+        item_of(id - base * p.s.Hk, n, p.s.Hk, gridDim.x, p.s.tpt, it.kh, it.t0);
+    }
+
+    // this CTA's range of the steps, and the item that it begins in (as walk_cut)
+    __device__ __forceinline__ void begin_parts(const Params &p, int lane)
+    {
+        const Seqs &s = p.s;
+        const int c = blockIdx.x;
+        r = s.B;
+        if (c >= cut) return;
+        if (lane == 0) p.splits[c].parts = 0;
+        const long long from = c * total / cut;
+        to = (c + 1) * total / cut;
+        at = from;
+        kh = i = skip = 0;
+        r = __popc(__ballot_sync(0xFFFFFFFFu, lane < s.B && step0 < from));  // the first rank at or behind `from`
+        const long long next = __shfl_sync(0xFFFFFFFFu, step0, min(r, 31));
+        if (r < s.B && next == from) return;
+        --r;
+        const long long off = from - __shfl_sync(0xFFFFFFFFu, step0, r), one = __shfl_sync(0xFFFFFFFFu, head, r);
+        const int nq = __shfl_sync(0xFFFFFFFFu, n_q, r), nk = __shfl_sync(0xFFFFFFFFu, n_k, r), n = __shfl_sync(0xFFFFFFFFu, items, r);
+        kh = static_cast<int>(off / one);
+        const long long in = off - kh * one;  // steps of this head in front of `from`
+        long long before = 0;
+        i = n;
+        for (int t0 = 0; t0 < n; t0 += 32) {
+            const int m = t0 + lane < n ? steps_of(s.causal, nq, nk, (t0 + lane) * s.tpt, s.tpt) : 0;
+            long long incl = m;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const unsigned reached = __ballot_sync(0xFFFFFFFFu, t0 + lane < n && before + incl - m >= in);
+            if (reached) {
+                i = t0 + __ffs(reached) - 1;
+                before += __shfl_sync(0xFFFFFFFFu, incl - m, __ffs(reached) - 1);
+                break;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+        if (i == n || before > in) {  // `from` is inside the one before
+            --i;
+            before -= steps_of(s.causal, nq, nk, i * s.tpt, s.tpt);
+            skip = static_cast<int>(in - before);
+            at = from - skip;
+        }
+    }
+
+    // the next part or item of this CTA, or it.b = -1
+    __device__ __forceinline__ void next_part(const Params &p, int lane, Item &it)
+    {
+        const Seqs &s = p.s;
+        const int c = blockIdx.x;
+        for (;;) {
+            if (r >= s.B) return;
+            const int n = __shfl_sync(0xFFFFFFFFu, items, r);
+            if (i < n) break;
+            i = 0;
+            if (n == 0 || ++kh >= s.Hk) kh = 0, ++r;
+        }
+        if (at >= to && c + 1 < cut) {
+            r = s.B;
+            return;
+        }
+        it.b = __shfl_sync(0xFFFFFFFFu, b, r);
+        it.kh = kh;
+        it.t0 = i * s.tpt;
+        const Seq q = seq_of(s, it.b, p.err);
+        const int steps = item_steps(s, q, it.t0);
+        const long long end = at + steps;
+        const bool more = end > to;
+        it.lo = skip;
+        it.hi = more ? static_cast<int>(to - at) : steps;
+        it.slot = skip > 0 ? 2 * c : more ? 2 * c + 1 : -1;
+        if (skip == 0 && more && lane == 0) p.splits[c] = split_of(s, q, it.t0, kh, c, end, total, cut);
+        skip = 0;
+        at = end;
+        ++i;
+        if (more) r = s.B;
+    }
+};
 
 // first step of the item in which some row of the tile does not see all keys
 __device__ __forceinline__ int first_masked(const Params &p, const Item &it)
@@ -805,7 +986,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
     }
 }
 
-// PLANNED: after plan_kernel; else at most 32 sequences of at most kShortKeys keys
+// PLANNED: after plan_kernel; else the loading warps plan for themselves
 template <int D, bool PLANNED>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -880,43 +1061,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The item after the one at hand is fetched while its first steps run.
             uint32_t n_items;
             int cut = 0, due = 0, due_end = 0;  // where the steps are cut: this CTA's entries
-            int seq_items = 0, seq_end = 0;     // without a plan: items of sequence `lane`, and of those up to it
+            WarpPlan plan;
             if constexpr (PLANNED) {  // (past L1: the plan was written while this kernel was on its way)
                 n_items = __ldcg(&p.hdr->n_items);
                 cut = __ldcg(&p.hdr->cut);
                 if (static_cast<int>(blockIdx.x) < cut) due = __ldcg(p.first + blockIdx.x), due_end = __ldcg(p.first + blockIdx.x + 1);
             } else {
-                if (lane < p.s.B) seq_items = (seq_of(p.s, lane, p.err).n_q + p.s.tpt - 1) / p.s.tpt;
-                seq_end = seq_items;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xFFFFFFFFu, seq_end, o);
-                    if (lane >= o) seq_end += y;
-                }
-                const int all = __shfl_sync(0xFFFFFFFFu, seq_end, 31);
-                if (all > p.max_items) raise_error(p.err, BSA_ERR_INVALID_ARG);  // sequences overlap
-                n_items = all > p.max_items ? 0u : static_cast<uint32_t>(all) * static_cast<uint32_t>(p.s.Hk);
+                plan.make(p, lane);
+                n_items = plan.n_items;
+                cut = plan.cut;
             }
             int count = 0, G = 0, e = 0;
             auto hand_out = [&](Item &it) -> bool {
                 it.b = -1;
-                if constexpr (!PLANNED) {
-                    const uint32_t id = blockIdx.x + static_cast<uint32_t>(count) * gridDim.x;
-                    if (id < n_items) {
-                        const int item = static_cast<int>(id / static_cast<uint32_t>(p.s.Hk));
-                        const int b = __popc(__ballot_sync(0xFFFFFFFFu, seq_end <= item));  // the first that ends behind it
-                        it.b = b;
-                        it.kh = static_cast<int>(id) - item * p.s.Hk;
-                        it.t0 = (__shfl_sync(0xFFFFFFFFu, seq_end, b) - 1 - item) * p.s.tpt;  // its last tile first
-                        it.lo = 0;
-                        it.slot = -1;
-                    }
+                it.slot = -1;
+                if (cut && !PLANNED) {
+                    plan.next_part(p, lane, it);
                 } else if (cut) {
                     if (due < due_end) {
                         const int4 *en = reinterpret_cast<const int4 *>(p.entries + due++);
                         const int4 x = __ldcg(en), y = __ldcg(en + 1);
                         it.b = x.x, it.t0 = x.y, it.kh = x.z, it.lo = x.w, it.hi = y.x, it.slot = y.y;
                     }
+                } else if constexpr (!PLANNED) {
+                    uint32_t id = blockIdx.x;  // the first is the CTA's own
+                    if (count > 0) {
+                        if (lane == 0) id = gridDim.x + atomicAdd(p.counter, 1u);
+                        id = __shfl_sync(0xFFFFFFFFu, id, 0);
+                    }
+                    if (id < n_items) plan.item(p, static_cast<int>(id), it);
                 } else {
                     uint32_t id = 0u;
                     if (lane == 0) id = atomicAdd(&p.hdr->next, 1u);
@@ -933,15 +1106,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             n = min(step, n - last * step);
                         }
                         const int base = __ldcg(p.item0 + r), n = __ldcg(p.item0 + r + 1) - base;
-                        const int rest = static_cast<int>(id) - base * p.s.Hk;
-                        // the last `mixed` heads of the sequence, tile by tile; the others head by head
-                        const int mixed = min(p.s.Hk, (2 * static_cast<int>(gridDim.x) + n - 1) / n);
-                        const int in_order = (p.s.Hk - mixed) * n, tail = rest - in_order;
                         it.b = __ldcg(p.rank + r);
-                        it.kh = tail < 0 ? rest / n : p.s.Hk - mixed + tail % mixed;
-                        it.t0 = (n - 1 - (tail < 0 ? rest % n : tail / mixed)) * p.s.tpt;
                         it.lo = 0;
-                        it.slot = -1;
+                        item_of(static_cast<int>(id) - base * p.s.Hk, n, p.s.Hk, gridDim.x, p.s.tpt, it.kh, it.t0);
                     }
                 }
                 if (it.b >= 0) {
@@ -1005,6 +1172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok && !fetched) ok = hand_out(next);
                 it = next;
             }
+            if (!PLANNED && !cut && lane == 0 && atomicAdd(p.counter + 1, 1u) == gridDim.x - 1)
+                p.counter[0] = p.counter[1] = 0u;  // the last CTA; for the next call
             // after an abort: no copy of this warp is in flight when the CTA ends
             if (lane == 0 && *ctl.abort_flag) {
                 for (int q = max(0, e - C::QS); q < e; ++q) wait_bar_drain(bar(C::B_QFULL + q % C::QS), (q / C::QS) & 1);
@@ -1143,17 +1312,40 @@ struct JoinArgs {
     uint32_t *err;
 };
 
-// A warp per row: O = sum w_k O_k / sum w_k l_k, LSE = ln2 (M + log2 sum w_k l_k), w_k = 2^(m_k - M)
+// A warp per row, or, where there are no more rows than CTAs, a CTA: its warps take a share of the
+// parts each, as the loads' latency is all there is then (16 queries over 31,760 keys in parts of
+// 38 CTAs: 35 -> 24.5 us for the call).  O = sum w_k O_k / sum w_k l_k, LSE = ln2 (M + log2 sum w_k l_k), w_k = 2^(m_k - M)
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const JoinArgs a)
 {
     constexpr int V = D / 32;  // channels of a lane
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int rows = static_cast<int>(__ldcg(&a.hdr->n_splits)) * kTileM;
-    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < rows; i += gridDim.x * 8) {
+    __shared__ float share[8][32][V + 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the CTAs' records that hold an item in parts, as bits
+    const int ctas = __ldcg(&a.hdr->cut);
+    unsigned held[kMaxSlots / 2 / 32];
+    int rows = 0;
+#pragma unroll
+    for (int w = 0; w < kMaxSlots / 2 / 32; ++w) {
+        const int c = w * 32 + lane;
+        held[w] = __ballot_sync(0xFFFFFFFFu, c < ctas && __ldcg(&a.splits[c].parts) > 0);
+        rows += __popc(held[w]) * kTileM;
+    }
+    const bool wide = rows <= static_cast<int>(gridDim.x);
+    const int stride = static_cast<int>(gridDim.x) * (wide ? 1 : 8);
+    for (int i = wide ? blockIdx.x : blockIdx.x * 8 + warp; i < rows; i += stride) {
         const int trow = i % kTileM;
-        const int4 *record = reinterpret_cast<const int4 *>(a.splits + i / kTileM);
+        int nth = i / kTileM, c = 0;
+#pragma unroll
+        for (int w = 0; w < kMaxSlots / 2 / 32; ++w) {
+            // the lane whose bit is the nth of this word, where the word has so many
+            const unsigned bit = 1u << lane;
+            const unsigned here = __ballot_sync(0xFFFFFFFFu, (held[w] & bit) && __popc(held[w] & (bit - 1)) == nth);
+            if (here) c = w * 32 + __ffs(here) - 1;
+            nth -= __popc(held[w]);
+        }
+        const int4 *record = reinterpret_cast<const int4 *>(a.splits + c);
         const int4 sp = __ldcg(record);  // q0, tokens, kh, c0
         const int parts = __ldcg(record + 1).x;
         const int rt = trow / a.s.g, rh = trow % a.s.g;
@@ -1162,27 +1354,29 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinArgs a)
         float M = -CUDART_INF_F, L = 0.0f, out[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) out[c] = 0.0f;
-        for (int k0 = 0; k0 < parts; k0 += 32) {
-            // 32 parts' statistics at a time, a lane each; then their rows, eight loads in flight
+        const int each = wide ? (parts + 7) / 8 : parts, begin = wide ? warp * each : 0;
+        const int end = min(begin + each, parts);
+        for (int k0 = begin; k0 < end; k0 += 32) {
+            // 32 parts' statistics at a time, a lane each; then their rows, 16 loads in flight
             float2 st = make_float2(-CUDART_INF_F, 0.0f);
-            if (k0 + lane < parts) st = __ldcg(a.part_stats + row_of(k0 + lane));
+            if (k0 + lane < end) st = __ldcg(a.part_stats + row_of(k0 + lane));
             float m = st.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             m = fmaxf(m, M);
             const float old = m == M ? 1.0f : ex2_approx(M - m), w = st.x == m ? 1.0f : ex2_approx(st.x - m);
             M = m;
-            float l = k0 + lane < parts ? w * st.y : 0.0f;
+            float l = k0 + lane < end ? w * st.y : 0.0f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
             L = L * old + l;
 #pragma unroll
             for (int c = 0; c < V; ++c) out[c] *= old;
-            const int n = min(32, parts - k0);
-            for (int j0 = 0; j0 < n; j0 += 8) {
-                float v[8][V];
+            const int n = min(32, end - k0);
+            for (int j0 = 0; j0 < n; j0 += 16) {
+                float v[16][V];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 16; ++j) {
                     const float *src = a.part_o + row_of(k0 + min(j0 + j, n - 1)) * D + lane * V;
                     if constexpr (V == 4) {
                         const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
@@ -1193,12 +1387,29 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinArgs a)
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 16; ++j) {
                     const float wj = __shfl_sync(0xFFFFFFFFu, w, min(j0 + j, 31));
                     if (j0 + j >= n) break;
 #pragma unroll
                     for (int c = 0; c < V; ++c) out[c] = fmaf(wj, v[j][c], out[c]);
                 }
+            }
+        }
+        if (wide) {
+            share[warp][lane][0] = M, share[warp][lane][1] = L;
+#pragma unroll
+            for (int c = 0; c < V; ++c) share[warp][lane][2 + c] = out[c];
+            __syncthreads();
+            if (warp != 0) return;  // a CTA has one row
+            for (int k = 0; k < 8; ++k) M = fmaxf(M, share[k][lane][0]);
+            L = 0.0f;
+#pragma unroll
+            for (int c = 0; c < V; ++c) out[c] = 0.0f;
+            for (int k = 0; k < 8; ++k) {
+                const float m = share[k][lane][0], w = m == M ? 1.0f : ex2_approx(m - M);
+                L += w * share[k][lane][1];
+#pragma unroll
+                for (int c = 0; c < V; ++c) out[c] = fmaf(w, share[k][lane][2 + c], out[c]);
             }
         }
         const float inv = L != 0.0f ? 1.0f / L : 0.0f;
@@ -1332,19 +1543,24 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
     p.item0 = pa.item0;
     p.first = pa.first;
     p.entries = pa.entries;
+    p.splits = pa.splits;
+    p.counter = reinterpret_cast<uint32_t *>(a.ws + kCacheCounter);
     p.part_o = reinterpret_cast<float *>(a.ws + l.part);
     p.part_stats = reinterpret_cast<float2 *>(a.ws + l.stats);
     p.err = err;
     p.wait_limit_ns = a.wait_limit_ns;
     p.stall = (a.dbg_flags & kDbgStall) != 0u;
-    if constexpr (!PLANNED) {
+    if constexpr (PLANNED) {
+        plan_kernel<<<1, kPlanThreads, 0, st>>>(pa);
+        if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
+        if (!pdl_launch(kern, dim3(static_cast<unsigned>(sms)), kThreads, C::SMEM_ALLOC, st, mq, mk, mv, p)) return BSA_ERR_CUDA;
+    } else {
+        // all SMs where steps may be cut, else no more than there can be items
         const int64_t items = l.max_items * a.Hk;
-        kern<<<static_cast<unsigned>(items < sms ? items : sms), kThreads, C::SMEM_ALLOC, st>>>(mq, mk, mv, p);
-        return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+        const int ctas = a.Tk > kShortKeys || items > sms ? sms : static_cast<int>(items);
+        kern<<<static_cast<unsigned>(ctas), kThreads, C::SMEM_ALLOC, st>>>(mq, mk, mv, p);
+        if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     }
-    plan_kernel<<<1, kPlanThreads, 0, st>>>(pa);
-    if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
-    if (!pdl_launch(kern, dim3(static_cast<unsigned>(sms)), kThreads, C::SMEM_ALLOC, st, mq, mk, mv, p)) return BSA_ERR_CUDA;
     if (a.Tk <= kShortKeys) return BSA_OK;  // nothing is cut
     const JoinArgs ja{seqs, a.o, a.lse, hdr, pa.splits, p.part_o, p.part_stats, err};
     if (!pdl_launch(join_kernel<D>, dim3(static_cast<unsigned>(4 * sms)), 256, 0, st, ja)) return BSA_ERR_CUDA;
@@ -1357,7 +1573,7 @@ size_t prompt_workspace(int T, int B, int H, int Hk, int d) { return layout_of(T
 
 bsa_status launch_prompt_attention(const PromptArgs &a, cudaStream_t st)
 {
-    const bool planned = a.B > 32 || a.Tk > kShortKeys;
+    const bool planned = a.B > kWarpPlan || layout_of(a.Tq, a.B, a.H, a.Hk, a.d).max_items > kWarpItems;
     if (a.d == 128) return planned ? launch<128, true>(a, st) : launch<128, false>(a, st);
     return planned ? launch<64, true>(a, st) : launch<64, false>(a, st);
 }

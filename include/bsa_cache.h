@@ -133,8 +133,8 @@ bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, i
  * What a query does not see does not reach it, NaN and infinities included. O must not overlap an
  * input. T_q may be 0.
  * Scores, sums and accumulators are fp32; weights are rounded to bf16, and O is divided by their sum
- * before the rounding. One launch for at most 32 sequences and T_k <= 1024, else up to three. Errors: as
- * bsa_cache_write.
+ * before the rounding. One to three launches (one for few sequences with T_k <= 1024).
+ * Errors: as bsa_cache_write.
  */
 bsa_status bsa_prompt_attention(const bsa_packed *q, const bsa_packed *k, const bsa_packed *v, int dt, int T_q,
                                 int T_k, int B, int H, int Hk, int d, const int32_t *cu_q, const int32_t *cu_k,
