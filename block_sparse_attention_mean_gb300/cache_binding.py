@@ -115,28 +115,24 @@ def bsa_cache_workspace_size(T: int, B: int, H: int, Hk: int, d: int) -> int:
 # ------------------------------------------------------------------ helpers
 #
 # As in block_binding, descriptors go as bytes in the structures' layout, and messages wait for a failure: a tensor is
-# looked at in as few calls as tell that it is right, and _view says what is wrong with it if it is not. A KvCache keeps
-# its descriptor from call to call.
+# looked at in as few calls as tell that it is right, and _view says what is wrong with it if it is not.
 
 _CACHE = struct.Struct("4P5i4x")
 _TABLE = struct.Struct("Pq2i")
 _PACKED = struct.Struct("Pqq")
-_BF16, _INT, _FP32 = torch.bfloat16, torch.int32, torch.float32
+_BF16, _E4M3, _INT, _FP32, _UINT8 = torch.bfloat16, torch.float8_e4m3fn, torch.int32, torch.float32, torch.uint8
 _grad_enabled = torch.is_grad_enabled
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _block_current_stream
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-class _KvCacheFields(NamedTuple):
+class KvCache(NamedTuple):
+    """Pages of keys and values: k, v [pages, key heads, page size, d], bf16, or float8_e4m3fn with the bytes k_exp, v_exp
+    [pages, key heads, page size] of their exponents: a row is data * 2 ** (exp - 127)."""
     k: torch.Tensor
     v: torch.Tensor
     k_exp: Optional[torch.Tensor] = None
     v_exp: Optional[torch.Tensor] = None
-
-
-class KvCache(_KvCacheFields):
-    """Pages of keys and values: k, v [pages, key heads, page size, d], bf16, or float8_e4m3fn with the bytes k_exp, v_exp
-    [pages, key heads, page size] of their exponents: a row is data * 2 ** (exp - 127)."""
 
 
 def kv_cache(n_pages: int, page_size: int, kv_heads: int, d: int, kind: str = "bf16", device="cuda") -> KvCache:
@@ -172,7 +168,8 @@ def cache_check(ws: torch.Tensor, stream=None) -> None:
 
 def _contiguous(t: torch.Tensor, shape, dtype, device, what: str, name: str) -> int:
     """Address of a contiguous tensor of this shape, dtype and device."""
-    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device and
+            (dtype is _INT or not (t.requires_grad and _grad_enabled()))):
         _view(t, shape, dtype, device, what, name)
         raise BsaError(ERR_INVALID_ARG, f"{what}: {name} must be contiguous")
     return t.data_ptr()
@@ -188,36 +185,27 @@ def _packed(t: torch.Tensor, shape, device, what: str, name: str) -> bytes:
 
 
 def _cache_args(cache: KvCache, what: str):
-    """(descriptor, device, key heads, d), kept with the cache while its tensors stay where they are"""
-    kept = getattr(cache, "_kept", None)
+    """(descriptor, device, key heads, d)"""
     k, v, k_exp, v_exp = cache
-    if (kept is not None and kept[4] == k.data_ptr() and kept[5] == v.data_ptr() and
-            not ((k.requires_grad or v.requires_grad) and _grad_enabled())):
-        return kept
     device = _cuda_device(k, what)
-    if k.dim() != 4:
-        raise BsaError(ERR_SHAPE, f"{what}: a cache of {k.dim()} dimensions, expected 4")
     shape, dtype = k.shape, k.dtype
-    if dtype == _BF16:
+    if len(shape) != 4:
+        raise BsaError(ERR_SHAPE, f"{what}: a cache of {len(shape)} dimensions, expected 4")
+    if dtype is _BF16:
         kind, ke, ve = CACHE_BF16, 0, 0
         if k_exp is not None or v_exp is not None:
             raise BsaError(ERR_INVALID_ARG, f"{what}: a bf16 cache has no exponents")
-    elif dtype == torch.float8_e4m3fn:
+    elif dtype is _E4M3:
         if k_exp is None or v_exp is None:
             raise BsaError(ERR_INVALID_ARG, f"{what}: an e4m3 cache needs its exponents")
-        kind = CACHE_E4M3
-        ke = _contiguous(k_exp, shape[:3], torch.uint8, device, what, "k_exp")
-        ve = _contiguous(v_exp, shape[:3], torch.uint8, device, what, "v_exp")
+        kind, rows = CACHE_E4M3, shape[:3]
+        ke = _contiguous(k_exp, rows, _UINT8, device, what, "k_exp")
+        ve = _contiguous(v_exp, rows, _UINT8, device, what, "v_exp")
     else:
         raise BsaError(ERR_DTYPE, f"{what}: cache dtype {dtype}")
-    n_pages, heads, page_size, d = shape
-    for t, name in ((k, "cache k"), (v, "cache v")):
-        _view(t, shape, dtype, device, what, name)
     at = _contiguous(k, shape, dtype, device, what, "cache k"), _contiguous(v, shape, dtype, device, what, "cache v")
-    kept = (_CACHE.pack(*at, ke, ve, kind, n_pages, page_size, heads, d), device, heads, d, *at)
-    if isinstance(cache, KvCache):
-        cache._kept = kept
-    return kept
+    n_pages, heads, page_size, d = shape
+    return _CACHE.pack(*at, ke, ve, kind, n_pages, page_size, heads, d), device, heads, d
 
 
 def _table_args(table: torch.Tensor, device, what: str):
@@ -257,7 +245,7 @@ def cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     if stream is not None and (there := _elsewhere(stream, k, what)):
         with there:
             return cache_write(cache, k, v, table, kv_lens, cu, ws=ws, check=check)
-    desc, device, heads, d, _, _ = _cache_args(cache, what)
+    desc, device, heads, d = _cache_args(cache, what)
     pages, B = _table_args(table, device, what)
     shape = (k.shape[0], heads, d)
     if ws is None:
@@ -277,7 +265,7 @@ def cache_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, tokens: Op
     if stream is not None and (there := _elsewhere(stream, cache.k, what)):
         with there:
             return cache_read(cache, table, cu, tokens, out=out, ws=ws, check=check)
-    desc, device, heads, d, _, _ = _cache_args(cache, what)
+    desc, device, heads, d = _cache_args(cache, what)
     pages, B = _table_args(table, device, what)
     if out is None:
         if tokens is None:
@@ -302,7 +290,7 @@ def cache_attention(q: torch.Tensor, cache: KvCache, table: torch.Tensor, kv_len
     if stream is not None and (there := _elsewhere(stream, q, what)):
         with there:
             return cache_attention(q, cache, table, kv_lens, scale, out=out, lse=lse, ws=ws, check=check)
-    desc, device, heads, d, _, _ = _cache_args(cache, what)
+    desc, device, heads, d = _cache_args(cache, what)
     pages, B = _table_args(table, device, what)
     if q.dim() != 3:
         raise BsaError(ERR_SHAPE, f"{what}: q has {q.dim()} dimensions, expected 3")

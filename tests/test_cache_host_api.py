@@ -4,6 +4,7 @@ import ctypes
 import os
 import re
 import shutil
+import struct
 import subprocess
 
 import pytest
@@ -328,3 +329,38 @@ def test_helpers_refuse_tensors_that_do_not_go_together(monkeypatch):
         args = dict(q=p, k=k, v=k, cu_q=cu, cu_k=cu, ws=ws, check=False)
         args.update(bad)
         refused(code, pkg.prompt_attention, **args)
+
+
+def test_a_cache_is_looked_at_in_every_call(monkeypatch):
+    monkeypatch.setattr(cb, "_cuda_device", lambda t, what: t.device)
+    seen = []
+    monkeypatch.setattr(cb, "_call", lambda what, fn, device, ws, check, *args: seen.append(args[0]))
+    cache = pkg.kv_cache(3, 16, 4, 64, "e4m3", "cpu")
+    t, n, k, ws = host(2, 3, dtype=torch.int32), host(2, dtype=torch.int32), host(2, 4, 64), host(1 << 14, dtype=torch.uint8)
+
+    def write():
+        pkg.cache_write(cache, k, k, t, n, ws=ws, check=False)
+        return struct.unpack("4P5i4x", seen[-1])
+
+    assert write() == (*(x.data_ptr() for x in cache), 1, 3, 16, 4, 64)
+    other = torch.empty_like(cache.k_exp)
+    cache.k_exp.set_(other)  # its keys and values stay where they are
+    assert write() == (cache.k.data_ptr(), cache.v.data_ptr(), other.data_ptr(), cache.v_exp.data_ptr(), 1, 3, 16, 4, 64)
+    for x in cache:
+        x.set_(x[:2])
+    assert write()[5] == 2
+    cache.k.set_(cache.k[:1])
+    refused(bb.ERR_SHAPE, write)
+
+
+def test_helpers_refuse_gradients_of_caches_and_sums(monkeypatch):
+    on_any_device(monkeypatch)
+    cache = pkg.kv_cache(3, 16, 4, 64, "bf16", "cpu")
+    t, n, ws = host(2, 3, dtype=torch.int32), host(2, dtype=torch.int32), host(1 << 14, dtype=torch.uint8)
+    lse = host(2, 8, dtype=torch.float32).requires_grad_()
+    refused(bb.ERR_INVALID_ARG, pkg.cache_attention, host(2, 8, 64), cache, t, n, lse=lse, ws=ws, check=False)
+    learned = cache._replace(v=cache.v.clone().requires_grad_())
+    refused(bb.ERR_INVALID_ARG, pkg.cache_attention, host(2, 8, 64), learned, t, n, ws=ws, check=False)
+    refused(bb.ERR_INVALID_ARG, pkg.cache_write, learned, host(2, 4, 64), host(2, 4, 64), t, n, ws=ws, check=False)
+    with torch.no_grad(), pytest.raises(AssertionError, match="library was called"):
+        pkg.cache_attention(host(2, 8, 64), learned, t, n, lse=lse, ws=ws, check=False)
