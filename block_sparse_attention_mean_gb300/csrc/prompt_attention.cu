@@ -26,8 +26,8 @@
 //     that a cut runs through, in order.
 //   * What bounds it: shared memory. A 128 x 128 step moves 64 KB of K and V in, 64 KB of Q and K and 32 KB of V to the
 //     tensor cores, 1250 cycles at 128 bytes a cycle, beside 1024 cycles of products; measured 1550. 32768 causal tokens,
-//     16 heads of 128: 2.65 ms, 1660 TFLOP/s, 87% of the library's rate; six packed sequences of 513 to 4224 tokens, 24
-//     heads over 8: 304 us, 1105 TFLOP/s.
+//     16 heads of 128: 2.57 ms, 1710 TFLOP/s, 90% of the library's rate; six packed sequences of 513 to 4224 tokens, 24
+//     heads over 8: 286 us, 1175 TFLOP/s.
 //   * 0 * NaN: a masked weight of zero still multiplies V. In steps where a mask ends, the softmax warps look through V before
 //     they hand P over, a quarter of the rows each: rows behind the sequence are zeroed in shared memory, and other
 //     values that are not finite too; these are then added in the epilogue to the rows that see them. Steps that every row
@@ -36,6 +36,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math_constants.h>
 
 #include "cache_internal.h"
@@ -701,7 +702,11 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
         const int n = it.hi - it.lo, from = first_masked(p, it);
         const int tok = it.t0 + rt;
         const bool real = rt < p.s.tpt && tok < it.n_q;
-        const int nvis = real ? visible(p.s.causal, it.n_q, it.n_k, tok) : 0;
+        // Rows without a query hold anything and go nowhere: they are never masked (a warp with one would mask every step:
+        // six packed sequences of three heads to a key head 327 us, 286 us so), their scores count as zero and so does
+        // their maximum.
+        const int nvis = real ? visible(p.s.causal, it.n_q, it.n_k, tok) : INT_MAX;
+        const float scale = real ? p.scale_log2 : 0.0f;
         float m_run = -CUDART_INF_F;
         uint64_t acc[2] = {0ull, 0ull};
         float m_other = -CUDART_INF_F;  // the maximum that the other group's sums are relative to
@@ -747,7 +752,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 }
                 return fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.scale_log2;
             };
-            const uint64_t c2x = f2_pack(p.scale_log2, p.scale_log2);
+            const uint64_t c2x = f2_pack(scale, scale);
             uint64_t sacc[2];
             uint32_t pk[NC][16];  // P, stored over S when the step's maximum is settled
             auto exps = [&](float m) {
@@ -795,6 +800,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
             bool settled = false;  // the step before is known
             if (i == 0) {  // a new tile: its first step's maximum, known before the exponentials are
                 m_run = step_max();
+                if (!real) m_run = 0.0f;
                 float before;
                 if (!wait_settled(before)) return;
                 settle(m_run);
@@ -819,10 +825,10 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                     }
                 }
                 if (raised) break;
-                // a step sum of at most 2^8 bounds every weight: only a larger one (or NaN) raises the maximum
+                // a step sum of at most 2^8 bounds every weight: only a larger one raises the maximum (NaN stays NaN either way)
                 float s0, s1;
                 f2_unpack(f2_add(sacc[0], sacc[1]), s0, s1);
-                const bool raise = !(s0 + s1 <= kRescaleSum) || (m_run == -CUDART_INF_F && s0 + s1 > 0.0f);
+                const bool raise = s0 + s1 > kRescaleSum || (m_run == -CUDART_INF_F && s0 + s1 > 0.0f);
                 if (!__any_sync(0xFFFFFFFFu, raise)) break;
                 raised = true;  // the whole warp: TMEM accesses are the warp's
                 const float m_all = step_max();
@@ -938,36 +944,50 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 tc_fence_after();
                 dirty = vflags[(count - 1) % kRing] != 0u;
             }
-            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            auto o_is_read = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_OEMPTY));
+            };
+            if (part) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t ov[32];
-#pragma unroll
-                for (int q = 0; q < 32; ++q) ov[q] = 0u;
-                if (n > 0) {
-                    tmem_ld32(tO + c * 32, ov);
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t ov[16];  // (a part has steps)
+                    tmem_ld16(tO + c * 16, ov);
                     tmem_wait_ld();
-                    reg_fence32(ov);
-                    if (c + 1 == D / 32) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(C::B_OEMPTY));
+                    reg_fence(ov);
+                    if (c + 1 == D / 16) o_is_read();
+                    uint4 w[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) w[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+                    put(w, c * 64);
+                }
+            } else {
+                // all of O first: the next tile's first product waits for it, and these warps are missed by the next tile's
+                // steps (32768 tokens: 2666 us with loads and stores in turn, 2571 us so)
+                const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+                uint32_t o2[D / 2], ov[2][16];
+#pragma unroll
+                for (int q = 0; q < D / 2; ++q) o2[q] = 0u;
+                if (n > 0) {
+                    tmem_ld16(tO, ov[0]);
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        tmem_wait_ld();
+                        reg_fence(ov[c & 1]);
+                        if (c + 1 < D / 16) tmem_ld16(tO + (c + 1) * 16, ov[(c + 1) & 1]);
+                        else o_is_read();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            o2[c * 8 + q] = pack_bf16x2(__uint_as_float(ov[c & 1][2 * q]) * inv, __uint_as_float(ov[c & 1][2 * q + 1]) * inv);
                     }
                 }
-                auto of = [&](int q) { return __uint_as_float(ov[q]) * inv; };
-                uint4 w[4];
-                if (part) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                for (int c = 0; c < D / 32; ++c) {
+                    uint4 w[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w[q] = make_uint4(ov[16 * x + 4 * q], ov[16 * x + 4 * q + 1], ov[16 * x + 4 * q + 2], ov[16 * x + 4 * q + 3]);
-                        put(w, c * 128 + x * 64);
-                    }
-                } else {
-                    auto two = [&](int q) { return pack_bf16x2(of(q), of(q + 1)); };
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) w[q] = make_uint4(two(8 * q), two(8 * q + 2), two(8 * q + 4), two(8 * q + 6));
+                    for (int q = 0; q < 4; ++q)
+                        w[q] = make_uint4(o2[c * 16 + 4 * q], o2[c * 16 + 4 * q + 1], o2[c * 16 + 4 * q + 2], o2[c * 16 + 4 * q + 3]);
                     put(w, c * 64);
                 }
             }
