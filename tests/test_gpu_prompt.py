@@ -432,3 +432,41 @@ def test_the_stream_argument_orders_the_calls():
     got = pkg.prompt_attention(q, k, v, cu, stream=s)
     s.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("H,Hk,d", [(4, 4, 64), (6, 2, 128), (5, 1, 128)])
+@pytest.mark.parametrize("bad", [INF, float("nan"), 1e30])
+def test_queries_of_others_in_the_same_tile_do_not_reach(H, Hk, d, bad):
+    """a tile's rows behind its sequence hold the next one's queries, which may be anything; cut and whole tiles"""
+    g = gen(12)
+    cu_q, cu_k = starts([50, 60, 200]), starts([50, 5000, 200])
+    q, k, v = draw(g, 310, H, d), draw(g, cu_k[-1], Hk, d), draw(g, cu_k[-1], Hk, d)
+    clean = pkg.prompt_attention(q, k, v, ints(cu_q), ints(cu_k))
+    q[110:] = bad
+    out, lse = pkg.prompt_attention(q, k, v, ints(cu_q), ints(cu_k))
+    assert torch.equal(out[:110], clean[0][:110]) and torch.equal(lse[:, :110], clean[1][:, :110])
+    assert clean[0].isfinite().all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_infinite_scores(causal):
+    """a score of +inf is NaN in the results as in the formula, one of -inf is a weight of zero, in any step"""
+    g = gen(13)
+    cu = starts([600])
+    q, k, v = (draw(g, 600, 2, 128).abs() for _ in range(3))
+    k[400, 0, 7] = -INF
+    k[500, 1, 7] = INF
+    out, lse = pkg.prompt_attention(q, k, v, ints(cu), causal=causal)
+    first = 500 if causal else 0
+    assert out[first:, 1].isnan().all() and lse[1, first:].isnan().all()
+    keep = torch.arange(600, device=DEV) != 400
+    k2, v2 = k[keep][:, :1].contiguous(), v[keep][:, :1].contiguous()
+    # without key 400: rows behind it see the same keys but that one
+    if causal:
+        o, bo, l, bl = expected(q[:400, :1].contiguous(), k[:400, :1].contiguous(), v[:400, :1].contiguous(), starts([400]), starts([400]), True, 128 ** -0.5)
+        ref.within(out[:400, :1], o, bo, "O")
+        o, bo, l, bl = expected(q[401:, :1].contiguous(), k2, v2, starts([199]), starts([599]), True, 128 ** -0.5)
+        ref.within(out[401:, :1], o, bo, "O")
+    else:
+        o, bo, l, bl = expected(q[:, :1].contiguous(), k2, v2, starts([600]), starts([599]), False, 128 ** -0.5)
+        ref.within(out[:, :1], o, bo, "O")
