@@ -39,6 +39,7 @@ static_assert(kMaxJoin >= kGroup, "room for a group's weights");
 // (64 sequences of 100 to 8192 tokens, 8 key heads: 57 us without, 46 us with one to three of them)
 constexpr int kEnd = 2;
 constexpr int kSlotHeads = 16;         // query heads of a partial result
+constexpr float kFarApart = 90.0f;      // log2 of a running maximum over a value's unit from which fp32 may lose a weight
 constexpr float kRaise = 8.0f;         // log2 of how far a score may pass the running maximum
 
 struct Params {
@@ -192,6 +193,16 @@ struct Cut {
 
 __device__ __forceinline__ size_t slot_of(int c0, int part) { return part == 0 ? 2 * c0 + 1 : 2 * (c0 + part); }
 
+// x 2^e in two steps: 2^e alone may vanish where the product does not (sums relative to the maximum of the weights times
+// their values' units, with an 8-bit cache)
+__device__ __forceinline__ float scaled(float x, float e)
+{
+    const float h = ex2_approx(0.5f * e);
+    return x * h * h;
+}
+// log2 of a power of two; -127 of zero
+__device__ __forceinline__ float log2_of(float x) { return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127); }
+
 // One thread's share of a joined result: 8 channels of a head
 struct Joined {
     float o[8];
@@ -229,8 +240,8 @@ __device__ __forceinline__ void weigh_parts(const Params &p, Weights &ws, int c0
         if (i >= count || head >= heads) continue;
         const float w = ex2_approx(s[k].x - base);
         ws.w[i][head] = w;
-        l += w * s[k].y;
-        lp += w * s[k].z;
+        l += scaled(s[k].y, s[k].x - base);
+        lp += scaled(s[k].z, s[k].x - base);
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
@@ -598,12 +609,38 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
 #pragma unroll
                             for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
                             const float a = x == m[n][c] ? 1.0f : ex2_approx(m[n][c] - x);
+                            if constexpr (E4M3) l[n][c] = x == m[n][c] ? l[n][c] : scaled(l[n][c], m[n][c] - x);
+                            else l[n][c] *= a;
                             m[n][c] = x;
-                            l[n][c] *= a;
                             lp[n][c] *= a;
 #pragma unroll
                             for (int t = 0; t < KS; ++t) o[t][n][c] *= a, o[t][n][2 + c] *= a;
                         }
+                }
+                if constexpr (E4M3) {
+                    // a weight times its value's unit may vanish beside the largest one where the weight does not (zeros have
+                    // the least exponent there is): such tiles' weights are summed by themselves
+                    float hi = -CUDART_INF_F, most = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < NH; ++n) hi = fmax3(hi, m[n][0], m[n][1]);
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            if (h * 16 + r + 8 * t < left) most = fmaxf(most, d[h][t]);
+                    if (__any_sync(0xFFFFFFFFu, hi + log2_of(most) > kFarApart)) {
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h) {
+#pragma unroll
+                            for (int n = 0; n < NH; ++n)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float base = m[n][k & 1] == -CUDART_INF_F ? 0.0f : m[n][k & 1];
+                                    l[n][k & 1] += ex2_approx(s[h][n][k] - base + log2_of(d[h][k >> 1]));
+                                }
+                            d[h][0] = d[h][1] = 0.0f;
+                        }
+                    }
                 }
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
@@ -739,9 +776,9 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                 res.l = res.lp = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float a = res.m == -CUDART_INF_F ? 0.0f : ex2_approx(st_m[w][c] - res.m);
-                    res.l += a * st_l[w][c];
-                    res.lp += a * st_lp[w][c];
+                    const float off = res.m == -CUDART_INF_F ? -CUDART_INF_F : st_m[w][c] - res.m;
+                    res.l += scaled(st_l[w][c], off);
+                    res.lp += scaled(st_lp[w][c], off);
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {

@@ -113,7 +113,9 @@ bsa_status bsa_cache_read(const bsa_kv_cache *cache, const bsa_page_table *table
  * A sequence of length 0 has O = 0 and LSE = -inf; so has a malformed one. Tokens of a page outside
  * the cache count as zeros. With an 8-bit cache the products are those of the values held; scores,
  * sums and accumulators are fp32, weights are rounded to 11 bits (bf16 cache: 8 bits, and O is
- * divided by the sum of the rounded weights).
+ * divided by the sum of the rounded weights). A weight of an 8-bit cache is rounded together with its
+ * row's power of two, so its product is off by up to 2^-24 of the largest one; beside values above 2^90
+ * the sum misses weights below 2^-30.
  * One launch. Errors: as bsa_cache_write.
  */
 bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, int dt, int H,

@@ -410,3 +410,24 @@ def test_cache_attention_keeps_infinities_and_nan_of_its_own_keys():
     keep = torch.ones(H, d, dtype=torch.bool, device=DEV)
     keep[:2, 5] = keep[2:, 9] = False
     assert out[0][keep].isfinite().all() and lse.isfinite().all()
+
+
+@pytest.mark.parametrize("d,H,held", [(64, 4, [300]), (128, 16, [5000, 17]), (128, 3, [40000])])
+@pytest.mark.parametrize("large", [20, 60, 80])
+def test_weights_of_zeros_and_of_tiny_values_count(d, H, held, large):
+    """8-bit rows of zeros and of the least exponent among large ones: their weights are part of the sum all the same"""
+    g = gen(14)
+    page = 32
+    table, n_pages = paged(g, held, page)
+    cache, values = filled(g, n_pages, page, 1, d, "e4m3")
+    kind = torch.randint(0, 3, cache.v_exp.shape, generator=g, device=DEV)
+    kind[:, :, page // 2:] = torch.where(kind[:, :, page // 2:] == 2, 0, kind[:, :, page // 2:])  # tiles without a large one
+    data = values[1] * torch.pow(2.0, -(cache.v_exp.double() - 127))[..., None]
+    data = torch.where((kind == 0)[..., None], 0.0, data)
+    exps = torch.where(kind == 2, cache.v_exp.long() + large, 27)
+    cache.v.copy_(data.float())
+    cache.v_exp.copy_(exps.to(torch.uint8))
+    values[1] = data * torch.pow(2.0, (exps - 127).double())[..., None]
+    q = draw(g, len(held), H, d).to(BF16)
+    out, lse = pkg.cache_attention(q, cache, table, ints(held))
+    check_decode(q, cache, values, table, held, page, "e4m3", out=out, lse=lse)
