@@ -1,4 +1,9 @@
 """bsa_prompt_attention against its 64-bit form, and the four calls together."""
+import concurrent.futures
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -470,3 +475,75 @@ def test_infinite_scores(causal):
     else:
         o, bo, l, bl = expected(q[:, :1].contiguous(), k2, v2, starts([600]), starts([599]), False, 128 ** -0.5)
         ref.within(out[:, :1], o, bo, "O")
+
+
+def test_one_workspace_for_calls_of_every_kind():
+    """planned by a launch of its own or not, cut or not, and tokens between: each call leaves the workspace as the next needs it"""
+    g = gen(36)
+    calls = []
+    for H, Hk, d, new, past in ((4, 2, 128, [40] * 40, [900] + [0] * 39), (4, 4, 64, [300, 20], None), (8, 2, 128, [16], [9000]),
+                                (2, 1, 64, [5] * 50, None), (6, 2, 128, [700, 1, 64], [2000, 0, 5])):
+        cu_q, cu_k = starts(new), starts([n + p for n, p in zip(new, past or [0] * len(new))])
+        q, k, v = draw(g, cu_q[-1], H, d), draw(g, cu_k[-1], Hk, d), draw(g, cu_k[-1], Hk, d)
+        calls.append((q, k, v, ints(cu_q), ints(cu_k)))
+    loop = Loop(g)
+    ws = pkg.cache_workspace(2000, 50, 8, 8, 128, DEV)
+    want = [pkg.prompt_attention(*c) for c in calls]
+    for order in (range(5), (3, 1, 4, 0, 2), (2, 2, 1, 3, 4)):
+        for i in order:
+            got = pkg.prompt_attention(*calls[i], ws=ws)
+            assert torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1])
+            loop.step(ws)
+            o, l = loop.expected()
+            assert torch.equal(loop.out, o) and torch.equal(loop.lse, l)
+    pkg.cache_check(ws)
+
+
+def test_two_threads_at_once():
+    g = gen(37)
+    calls = []
+    for H, Hk, d, new in ((4, 2, 128, [700, 60]), (4, 4, 64, [1500])):
+        cu = starts(new)
+        calls.append((draw(g, cu[-1], H, d), draw(g, cu[-1], Hk, d), draw(g, cu[-1], Hk, d), ints(cu)))
+    want = [pkg.prompt_attention(*c) for c in calls]
+    torch.cuda.synchronize()
+
+    def work(i):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            runs = [pkg.prompt_attention(*calls[i]) for _ in range(20)]
+        side.synchronize()
+        return all(torch.equal(a, b) for run in runs for a, b in zip(run, want[i]))
+
+    with concurrent.futures.ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(work, range(2)))
+
+
+FIRST_CALL = """
+import torch
+import block_sparse_attention_mean_gb300 as pkg
+g = torch.Generator("cuda").manual_seed(1)
+def draw(*s): return torch.randn(*s, generator=g, device="cuda").bfloat16()
+def ints(x): return torch.tensor(x, dtype=torch.int32, device="cuda")
+q, k, v, cu, held, table = draw(300, 4, 64), draw(300, 2, 64), draw(300, 2, 64), ints([0, 100, 300]), ints([100, 200]), ints([list(range(4)), list(range(4, 8))])
+ws, cache, q1 = pkg.cache_workspace(300, 2, 4, 2, 64), pkg.kv_cache(8, 64, 2, 64, "e4m3"), draw(2, 4, 64)
+def step():
+    pkg.cache_write(cache, k, v, table, held, cu, ws=ws, check=False)
+    return (*pkg.prompt_attention(q, k, v, cu, ws=ws, check=False), *pkg.cache_attention(q1, cache, table, held, ws=ws, check=False),
+            *pkg.cache_read(cache, table, cu, 300, ws=ws, check=False))
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+pkg.cache_check(ws)
+print("same")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.split() == ["same"], r.stdout + r.stderr
