@@ -27,7 +27,7 @@
 //   * What bounds it: shared memory. A 128 x 128 step moves 64 KB of K and V in, 64 KB of Q and K and 32 KB of V to the
 //     tensor cores, 1250 cycles at 128 bytes a cycle, beside 1024 cycles of products; measured 1550. 32768 causal tokens,
 //     16 heads of 128: 2.57 ms, 1710 TFLOP/s, 90% of the library's rate; six packed sequences of 513 to 4224 tokens, 24
-//     heads over 8: 286 us, 1175 TFLOP/s.
+//     heads over 8: 275 us, 1220 TFLOP/s.
 //   * 0 * NaN: a masked weight of zero still multiplies V. In steps where a mask ends, the softmax warps look through V before
 //     they hand P over, a quarter of the rows each: rows behind the sequence are zeroed in shared memory, and other
 //     values that are not finite too; these are then added in the epilogue to the rows that see them. Steps that every row
@@ -51,8 +51,8 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kLoadWarp = 8, kQkWarp = 9, kPvWarp = 10, kValueWarp = 11;
 constexpr int kRing = 4;  // items in flight
 constexpr int kThreads = 12 * 32;
-// registers a thread after the split: 256 * 192 + 128 * 120 = 384 * 168, what the block is launched with
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
+// registers a thread after the split: 256 * 184 + 128 * 136 = 384 * 168, what the block is launched with
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 136;
 constexpr float kRescaleSum = 256.0f;
 constexpr uint32_t kDbgStall = 1u;  // of bsa_debug_config
 constexpr unsigned long long kDrainNs = 1000000000ull;  // copies and products in flight are waited for this long
@@ -409,7 +409,7 @@ struct Item {
 
 template <int D>
 struct Cfg {
-    static constexpr int QS = 2, NK = D == 128 ? 2 : 4, NV = D == 128 ? 2 : 4, NSB = 3;  // Q, K, V slots; S / P buffers
+    static constexpr int QS = D == 128 ? 2 : 3, NK = D == 128 ? 2 : 4, NV = D == 128 ? 2 : 4, NSB = 3;  // Q, K, V slots; S / P buffers
     static constexpr int kQBytes = kTileM * D * 2, kKVBytes = kStep * D * 2;
     static constexpr int kSlab = 128 * 128;  // bytes of 64 columns of 128 rows
     static constexpr int Q_OFF = 0, K_OFF = QS * kQBytes, V_OFF = K_OFF + NK * kKVBytes, BAR_OFF = V_OFF + NV * kKVBytes;
@@ -421,8 +421,7 @@ struct Cfg {
     static constexpr int kItemWords = 12;
     static constexpr int MISC_WORDS = 2 + kRing + kRing * kItemWords;  // TMEM base, abort flag, V flags of the items, the items
     static constexpr int ROWS_OFF = (MISC_OFF + 4 * MISC_WORDS + 15) / 16 * 16;  // settled maxima [128][2], sums [2][128]
-    static constexpr int OUT_OFF = ROWS_OFF + 4 * (128 * 2 + 2 * 128);  // 64 bytes of each of a warp's 32 rows on their way out
-    static constexpr int SMEM = OUT_OFF + kSoftmaxWarps * 2048;
+    static constexpr int SMEM = ROWS_OFF + 4 * (128 * 2 + 2 * 128);
     static constexpr int SMEM_ALLOC = SMEM + 1024;
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(kTileM, kStep, 0, 0);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(kTileM, D, 0, 1);
@@ -686,7 +685,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
 
 template <int D, class C>
 __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, uint32_t tmem, uint32_t settled_at,
-                                             volatile float *row_sums, uint4 *out, uint8_t *values, const volatile int *items,
+                                             volatile float *row_sums, uint8_t *queries, uint8_t *values, const volatile int *items,
                                              volatile uint32_t *vflags, const Ctl &ctl, int warp, int lane)
 {
     auto bar = [&](int idx) -> uint32_t { return sbase + C::BAR_OFF + 8u * idx; };
@@ -696,7 +695,8 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
     const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
     const uint32_t tO = tmem + lanes + C::T_O;
     const int rt = trow / p.s.g, rh = trow % p.s.g;  // token and head of the row within the tile
-    int G = 0, count = 0, pairs = 0;  // steps and items so far, items of two steps and more
+    int G = 0, count = 0, pairs = 0, e = 0;  // steps and items so far, items of three steps and more, of any steps
+    bool lead = group == 0;  // has a tile's first step
     Item it;
     while (fetch<C>(sbase, items, ctl, lane, count, it)) {
         const int n = it.hi - it.lo, from = first_masked(p, it);
@@ -715,7 +715,9 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
 #pragma unroll
             for (int k = 0; k < 2; ++k) acc[k] = f2_fma(acc[k], a2, 0ull);
         };
-        for (int i = (G ^ group) & 1; i < n; i += 2) {  // this group's steps: every other one, over all items
+        // The group that writes the tile before out is late: the other one has the first two steps, then they take turns.
+        // (With the results' way out, below: six packed sequences 287 us with steps in strict turn, 275 us so.)
+        for (int i = lead ? 0 : 2; i < n; i += lead && i == 0 ? 1 : 2) {
             const int g = G + i, b = g % C::NSB;
             const uint32_t tS = tmem + lanes + b * kStep;
             if (!warp_wait_all(bar(C::B_SFULL + b), (g / C::NSB) & 1, ctl)) return;
@@ -804,7 +806,7 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 float before;
                 if (!wait_settled(before)) return;
                 settle(m_run);
-            } else if (i == 1) {
+            } else if (i <= 2) {  // the group's second or first step
                 if (!wait_settled(m_run)) return;
                 m_other = m_run;
                 settled = true;
@@ -895,45 +897,48 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
         float e0, e1;
         f2_unpack(f2_add(acc[0], acc[1]), e0, e1);
         float l = e0 + e1;
-        // The group of the last step finishes the tile; the other one leaves its sums. Two buffers with a barrier each, used
-        // in turn: it may be one such tile ahead, not two, since each has a step of both groups and they wait for one
-        // another's. (With one barrier it could be two phases ahead of a wait, which then never ends.)
-        const bool finishes = n > 0 ? ((G + n - 1) & 1) == group : group == 0;
+        // The group of the last step finishes the tile; the other one, which has steps where there are three or more, leaves
+        // its sums. Two buffers with a barrier each, used in turn: it may be one such tile ahead, not two, since both have
+        // steps in each and every step waits until the one before is settled. (With one barrier it could be two phases
+        // ahead of a wait, which then never ends.)
+        const bool finishes = n > 0 ? lead == (n == 1 || n % 2 == 0) : group == 0;
         volatile float *sum = row_sums + (pairs & 1) * 128 + trow;
-        if (n >= 2 && !finishes) {
+        if (n >= 3 && !finishes) {
             *sum = l;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_SUMS + (pairs & 1) * 4 + w4));
         }
         if (finishes) {
-            if (n >= 2) {
+            if (n >= 3) {
                 if (!warp_wait_all(bar(C::B_SUMS + (pairs & 1) * 4 + w4), (pairs >> 1) & 1, ctl)) return;
                 // its sums are relative to the maximum after the last step but one
                 l += (m_other == m_run ? 1.0f : ex2_approx(m_other - m_run)) * *sum;
             }
             const bool part = it.slot >= 0;
             const int head = it.kh * p.s.g + rh;
-            // Rows go out through shared memory, 64 bytes of 32 rows at a time: four lanes write a row's, in place of each lane
-            // 16 bytes of a row of its own (half a sector; an epilogue took 8000 to 11000 cycles). A lane has rows
-            // lane / 4, + 8, + 16, + 24 of the warp's; `to` is where they begin, nullptr where they do not exist.
-            char *const own = part ? reinterpret_cast<char *>(p.part_o + (static_cast<size_t>(it.slot) * kTileM + trow) * D)
-                                   : p.o.p + static_cast<int64_t>(it.q0 + tok) * p.o.token + head * p.o.head;
-            char *to[4];
+            // Rows go out through the tile's Q, which nothing reads any more: 16 bytes a lane in, a row's 128 bytes by eight
+            // lanes out. (Each lane 16 bytes of a row of its own, half a sector: an epilogue took 8000 to 11000 cycles.)
+            // A quarter of a warp has the rows lane / 8, + 4, ... of the warp's; addresses are 0 for rows that do not exist.
+            const unsigned long long own =
+                part ? reinterpret_cast<unsigned long long>(p.part_o + (static_cast<size_t>(it.slot) * kTileM + trow) * D)
+                     : real ? reinterpret_cast<unsigned long long>(p.o.p + static_cast<int64_t>(it.q0 + tok) * p.o.token + head * p.o.head)
+                            : 0ull;
+            uint8_t *const stage = queries + (e % C::QS) * C::kQBytes + w4 * 32 * 128;
+            auto put = [&](const uint32_t (&v)[D / 2], int at) {  // this row's bytes [at, at + 2 D)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const unsigned long long at =
-                    __shfl_sync(0xFFFFFFFFu, part || real ? reinterpret_cast<unsigned long long>(own) : 0ull, k * 8 + (lane >> 2));
-                to[k] = at ? reinterpret_cast<char *>(at) + (lane & 3) * 16 : nullptr;
-            }
-            auto put = [&](const uint4 (&v)[4], int at) {  // this row's bytes [at, at + 64)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) out[lane * 4 + (k ^ ((lane >> 1) & 3))] = v[k];
+                for (int x = 0; x < D / 8; ++x)
+                    *reinterpret_cast<uint4 *>(stage + (x >> 3) * C::kSlab + lane * 128 + ((x ^ lane) & 7) * 16) =
+                        make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
                 __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = k * 8 + (lane >> 2);
-                    const uint4 w = out[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
-                    if (to[k]) *reinterpret_cast<uint4 *>(to[k] + at) = w;
+                for (int k = 0; k < 8; ++k) {
+                    const int r = k * 4 + (lane >> 3);
+                    char *to = reinterpret_cast<char *>(__shfl_sync(0xFFFFFFFFu, own, r));
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(stage + x * C::kSlab + r * 128 + ((lane ^ r) & 7) * 16);
+                        if (to) *reinterpret_cast<uint4 *>(to + at + x * 128 + (lane & 7) * 16) = w;
+                    }
                 }
                 __syncwarp();
             };
@@ -949,58 +954,62 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_OEMPTY));
             };
-            if (part) {
-#pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t ov[16];  // (a part has steps)
-                    tmem_ld16(tO + c * 16, ov);
-                    tmem_wait_ld();
-                    reg_fence(ov);
-                    if (c + 1 == D / 16) o_is_read();
-                    uint4 w[4];
+            if (n == 0) {
+                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) w[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
-                    put(w, c * 64);
+                for (int x = 0; x < D / 8; ++x)
+                    if (real) *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(own) + x * 16) = none;
+            } else if (part) {
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t o[D / 2];
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t ov[16];
+                        tmem_ld16(tO + half * (D / 2) + c * 16, ov);
+                        tmem_wait_ld();
+                        reg_fence(ov);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) o[c * 16 + q] = ov[q];
+                    }
+                    if (half == 1) o_is_read();
+                    put(o, half * D * 2);
                 }
             } else {
                 // all of O first: the next tile's first product waits for it, and these warps are missed by the next tile's
                 // steps (32768 tokens: 2666 us with loads and stores in turn, 2571 us so)
                 const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-                uint32_t o2[D / 2], ov[2][16];
+                uint32_t o[D / 2], ov[2][16];
+                tmem_ld16(tO, ov[0]);
 #pragma unroll
-                for (int q = 0; q < D / 2; ++q) o2[q] = 0u;
-                if (n > 0) {
-                    tmem_ld16(tO, ov[0]);
+                for (int c = 0; c < D / 16; ++c) {
+                    tmem_wait_ld();
+                    reg_fence(ov[c & 1]);
+                    if (c + 1 < D / 16) tmem_ld16(tO + (c + 1) * 16, ov[(c + 1) & 1]);
+                    else o_is_read();
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        tmem_wait_ld();
-                        reg_fence(ov[c & 1]);
-                        if (c + 1 < D / 16) tmem_ld16(tO + (c + 1) * 16, ov[(c + 1) & 1]);
-                        else o_is_read();
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            o2[c * 8 + q] = pack_bf16x2(__uint_as_float(ov[c & 1][2 * q]) * inv, __uint_as_float(ov[c & 1][2 * q + 1]) * inv);
-                    }
+                    for (int q = 0; q < 8; ++q)
+                        o[c * 8 + q] = pack_bf16x2(__uint_as_float(ov[c & 1][2 * q]) * inv, __uint_as_float(ov[c & 1][2 * q + 1]) * inv);
                 }
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint4 w[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        w[q] = make_uint4(o2[c * 16 + 4 * q], o2[c * 16 + 4 * q + 1], o2[c * 16 + 4 * q + 2], o2[c * 16 + 4 * q + 3]);
-                    put(w, c * 64);
-                }
+                put(o, 0);
+            }
+            if (n > 0) {  // the slot is the next Q's but one
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_QEMPTY + e % C::QS));
             }
             if (__any_sync(0xFFFFFFFFu, dirty && real)) __threadfence_block();  // the row is read back
             if (dirty && real) {
                 add_not_finite<D>(p.v.p + static_cast<int64_t>(it.k0) * p.v.token + it.kh * p.v.head, p.v.token, from * kStep,
-                                  min(nvis, it.hi * kStep), own, part);
+                                  min(nvis, it.hi * kStep), reinterpret_cast<char *>(own), part);
             }
             if (part) p.part_stats[static_cast<size_t>(it.slot) * kTileM + trow] = make_float2(m_run, l);
             else if (real && p.lse)
                 p.lse[static_cast<int64_t>(head) * p.s.Tq + it.q0 + tok] = (m_run + log2f(l)) * 0.69314718055994530942f;
         }
-        if (n >= 2) ++pairs;
+        if (n >= 3) ++pairs;
+        if (n > 0) lead = !finishes;
+        if (n > 0) ++e;
         G += n;
         done_with<C>(sbase, lane, count);
     }
@@ -1026,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::QS; ++s) {
             mbar_init(bar(C::B_QFULL + s), 1);
-            mbar_init(bar(C::B_QEMPTY + s), 1);
+            mbar_init(bar(C::B_QEMPTY + s), 4);  // the warps that finish a tile
         }
         for (int s = 0; s < C::NK; ++s) {
             mbar_init(bar(C::B_KFULL + s), 1);
@@ -1073,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kSoftmaxWarps) {
         regs_up<kSoftmaxRegs>();
         softmax_role<D, C>(p, sbase, tmem, sbase + C::ROWS_OFF, row_sums,
-                           reinterpret_cast<uint4 *>(smem + C::OUT_OFF + warp * 2048), smem + C::V_OFF, items, vflags, ctl, warp, lane);
+                           smem + C::Q_OFF, smem + C::V_OFF, items, vflags, ctl, warp, lane);
     } else {
         regs_down<kOtherRegs>();
         if (warp == kLoadWarp) {
@@ -1257,7 +1266,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc_commit(bar(C::B_SFULL + b));
                         tc_commit(bar(C::B_KEMPTY + s));
-                        if (i + 1 == n) tc_commit(bar(C::B_QEMPTY + qs));
                     }
                     __syncwarp();
                 }
