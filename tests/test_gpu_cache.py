@@ -431,3 +431,20 @@ def test_weights_of_zeros_and_of_tiny_values_count(d, H, held, large):
     q = draw(g, len(held), H, d).to(BF16)
     out, lse = pkg.cache_attention(q, cache, table, ints(held))
     check_decode(q, cache, values, table, held, page, "e4m3", out=out, lse=lse)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_thousands_of_sequences(kind):
+    """more than the CTAs, most of them empty or of few tokens"""
+    g = gen(15)
+    B, H, Hk, d, page = 5000, 2, 1, 64, 16
+    held = torch.randint(-20, 40, (B,), generator=g, device=DEV).clamp(min=0).tolist()
+    held[4990] = 700
+    table, n_pages = paged(g, held, page)
+    cache, values = filled(g, n_pages, page, Hk, d, kind)
+    q = draw(g, B, H, d).to(BF16)
+    out, lse = pkg.cache_attention(q, cache, table, ints(held))
+    some = torch.randperm(B, generator=g, device=DEV)[:150].tolist() + [0, 4990, B - 1]
+    check_decode(q[some].contiguous(), cache, values, table[some], [held[b] for b in some], page, kind, out=out[some], lse=lse[some])
+    empty = torch.tensor(held, device=DEV) == 0
+    assert (out[empty] == 0).all() and (lse[empty] == float("-inf")).all()

@@ -547,3 +547,38 @@ def test_first_call_of_a_process_inside_a_capture():
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and r.stdout.split() == ["same"], r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("H,Hk,d,B,most,past", [(2, 1, 64, 3000, 9, 0), (2, 2, 128, 1100, 3, 40), (3, 1, 64, 33, 200, 2000)])
+def test_many_sequences(H, Hk, d, B, most, past):
+    """more than a plan's threads, and a few more than a warp's lanes; some without queries, some without keys"""
+    g = gen(38)
+    new = torch.randint(0, most, (B,), generator=g, device=DEV).tolist()
+    old = torch.randint(0, past + 1, (B,), generator=g, device=DEV).tolist()
+    old[1::7] = [-n for n in new[1::7]]  # no keys
+    cu_q, cu_k = starts(new), starts([n + p for n, p in zip(new, old)])
+    q, k, v = draw(g, cu_q[-1], H, d), draw(g, cu_k[-1], Hk, d), draw(g, cu_k[-1], Hk, d)
+    out, lse = pkg.prompt_attention(q, k, v, ints(cu_q), ints(cu_k))
+    some = torch.randperm(B, generator=g, device=DEV)[:200].tolist() + [0, 1, B - 1]
+    for b in some:
+        rows, keys = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        o, bo, l, bl = expected(q[rows], k[keys], v[keys], [0, new[b]], [0, new[b] + old[b]], True, d ** -0.5)
+        ref.within(out[rows], o, bo, "O")
+        ref.within(lse[:, rows], l, bl, "LSE")
+
+
+@pytest.mark.parametrize("H,Hk,d,new", [(128, 1, 64, [3, 1, 260]), (64, 1, 128, [5, 130]), (100, 2, 64, [70])])
+def test_many_heads_share_a_key_head(H, Hk, d, new):
+    g = gen(39)
+    cu = starts(new)
+    check(draw(g, cu[-1], H, d), draw(g, cu[-1], Hk, d), draw(g, cu[-1], Hk, d), cu, cu, True)
+
+
+@pytest.mark.parametrize("H,Hk,d,causal", [(48, 16, 128, True), (40, 40, 64, True), (64, 8, 64, False), (21, 7, 128, False)])
+def test_short_items_of_few_sequences(H, Hk, d, causal):
+    """as above where each CTA plans for itself: up to 32 sequences, ten tiles of one to four steps a CTA"""
+    g = gen(40)
+    new = torch.randint(0, 500, (32,), generator=g, device=DEV).tolist()
+    keys = [max(0, a + x) for a, x in zip(new, torch.randint(-300, 100, (32,), generator=g, device=DEV).tolist())]
+    cu_q, cu_k = starts(new), starts(keys)
+    check(draw(g, cu_q[-1], H, d), draw(g, cu_k[-1], Hk, d), draw(g, cu_k[-1], Hk, d), cu_q, cu_k, causal)
