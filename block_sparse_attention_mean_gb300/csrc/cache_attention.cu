@@ -5,9 +5,10 @@
 // kernel is built around keeping loads in flight everywhere at once.
 //
 //   * The tokens of all sequences and key heads form one row of units of 64 or 128 tokens, which is cut evenly over the
-//     resident CTAs, whatever the lengths; the end of each (sequence, key head) counts as kEnd units more. Where a cut falls inside a (sequence, key head), its pieces leave partial
-//     results (O, max, sums) in the workspace and the CTA that finishes last joins them in the order of the tokens:
-//     in groups of kGroup, then over the groups, so that no CTA reads many.
+//     resident CTAs, whatever the lengths; the end of each (sequence, key head) counts as kEnd units more. Where a cut
+//     falls inside a (sequence, key head), its pieces leave partial results (O, max, sums) in the workspace and the CTA
+//     that finishes last joins them in the order of the tokens: in groups of kGroup, then over the groups, so that no
+//     CTA reads many.
 //   * Each of a CTA's four warps takes 16 or 32 tokens of a unit through a ring of its own in shared memory, filled with
 //     16-byte cp.async far ahead and across the ends of sequences. Warps meet only at the end of a (sequence, head).
 //   * The products run on mma.sync.m16n8k16 with the 16 tokens (then 16 channels) as rows and 8 query heads as

@@ -28,8 +28,9 @@
  *     is left out (see each call); nothing outside the buffers is read or written. BSA_ERR_TIMEOUT:
  *     a bounded wait gave up.
  *   - Workspaces are 256-byte aligned; the first BSA_CACHE_ROWS_WORKSPACE bytes of a new one are
- *     zero-filled once before its first call. Calls that share one must not overlap on the GPU. One workspace of sufficient size serves all four calls in
- *     turn, captured into graphs or not. Its size does not depend on lengths or on the cache.
+ *     zero-filled once before its first call. Calls that share one must not overlap on the GPU. One
+ *     workspace of sufficient size serves all four calls in turn, captured into graphs or not. Its size
+ *     does not depend on lengths or on the cache.
  *   - A result depends on the call's inputs and the device alone: sums run in an order fixed by the
  *     lengths, without atomics on values.
  */
