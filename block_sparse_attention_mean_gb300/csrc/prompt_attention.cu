@@ -19,15 +19,15 @@
 //     but in rows of one large weight, where it doubles that of O's own rounding.
 //   * Items are (sequence, key head, tile); each CTA looks at the lengths itself, or, of many sequences, a launch of one
 //     CTA before does. With many items, CTAs take them from a counter: longest sequences first, a sequence's heads one
-//     after another, so that K and V of the one or two in use stay in L2 (32768 tokens, 16 heads of 128: five heads in use cost a quarter of the rate, two heads a sixth), and
-//     of each head the longest items first. The last heads, two rounds of items of all CTAs, go together, longest items
-//     first, so that the work ends with short ones. Where that would leave CTAs idle (few items, or one far above a CTA's
-//     average), all steps in a row are cut evenly over the CTAs instead, and a last launch joins the parts of an item
-//     that a cut runs through, in order.
+//     after another, so that K and V of the one or two in use stay in L2 (32768 tokens, 16 heads of 128: five heads in
+//     use cost a quarter of the rate, two heads a sixth), and of each head the longest items first. The last heads, two
+//     rounds of items of all CTAs, go together, longest items first, so that the work ends with short ones. Where that
+//     would leave CTAs idle (few items, or one far above a CTA's average), all steps in a row are cut evenly over the
+//     CTAs instead, and a last launch joins the parts of an item that a cut runs through, in order.
 //   * What bounds it: shared memory. A 128 x 128 step moves 64 KB of K and V in, 64 KB of Q and K and 32 KB of V to the
-//     tensor cores, 1250 cycles at 128 bytes a cycle, beside 1024 cycles of products; measured 0.74 us, about
-//     1490, with its share of the tiles' ends. 32768 causal tokens, 16 heads of 128: 2.57 ms, 1710 TFLOP/s, 90% of the library's rate; six packed sequences of 513 to 4224 tokens, 24
-//     heads over 8: 275 us, 1220 TFLOP/s.
+//     tensor cores, 1250 cycles at 128 bytes a cycle, beside 1024 cycles of products; measured 0.74 us, about 1490, with
+//     its share of the tiles' ends. 32768 causal tokens, 16 heads of 128: 2.57 ms, 1710 TFLOP/s, 90% of the library's
+//     rate; six packed sequences of 513 to 4224 tokens, 24 heads over 8: 275 us, 1220 TFLOP/s.
 //   * 0 * NaN: a masked weight of zero still multiplies V. In steps where a mask ends, the softmax warps look through V before
 //     they hand P over, a quarter of the rows each: rows behind the sequence are zeroed in shared memory, and other
 //     values that are not finite too; these are then added in the epilogue to the rows that see them. Steps that every row
