@@ -19,7 +19,8 @@
 //   * 8-bit rows become fp16 (exact: e4m3 has 4 bits and fp16 its range). Q is scaled by a power of two to below 2
 //     and rounded to fp16 (exact for all of its 8 bits down to 2^-17 of the largest); the key's exponent multiplies
 //     the fp32 score, the value's is added to it in log2, so that P 2^e is what is rounded, to 11 bits, with a maximum
-//     of its own near one; the softmax's sum takes 2^-e out again.
+//     of its own near one. The softmax's sum is that of the scores alone, with a running maximum of its own: beside a value
+//     of 2^40 the product of a weight and a row of zeros vanishes, the weight does not.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -40,8 +41,8 @@ static_assert(kMaxJoin >= kGroup, "room for a group's weights");
 // (64 sequences of 100 to 8192 tokens, 8 key heads: 57 us without, 46 us with one to three of them)
 constexpr int kEnd = 2;
 constexpr int kSlotHeads = 16;         // query heads of a partial result
-constexpr float kFarApart = 90.0f;      // log2 of a running maximum over a value's unit from which fp32 may lose a weight
 constexpr float kRaise = 8.0f;         // log2 of how far a score may pass the running maximum
+constexpr float kRaiseSum = 256.0f;    // and of an 8-bit cache's weights, a thread's sum over a tile
 
 struct Params {
     CacheView cache;
@@ -54,7 +55,7 @@ struct Params {
     uint32_t *err;
     uint32_t *tickets;  // [3][kCacheMaxCtas]
     float *part_o;      // [slot][kSlotHeads][D]
-    float4 *part_s;     // [slot][kSlotHeads] (max in log2, sum, sum of the rounded weights, 0)
+    float4 *part_s;     // [slot][kSlotHeads]: Stats
 };
 
 template <int D, bool E4M3>
@@ -194,62 +195,88 @@ struct Cut {
 
 __device__ __forceinline__ size_t slot_of(int c0, int part) { return part == 0 ? 2 * c0 + 1 : 2 * (c0 + part); }
 
-// x 2^e in two steps: 2^e alone may vanish where the product does not (sums relative to the maximum of the weights times
-// their values' units, with an 8-bit cache)
+// x 2^e in two steps: 2^e alone may vanish, or be infinite, where the product is neither
 __device__ __forceinline__ float scaled(float x, float e)
 {
     const float h = ex2_approx(0.5f * e);
     return x * h * h;
 }
-// log2 of a power of two; -127 of zero
-__device__ __forceinline__ float log2_of(float x) { return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127); }
+// 2^(x - m), one where both are the same infinity
+__device__ __forceinline__ float rescale(float x, float m) { return x == m ? 1.0f : ex2_approx(x - m); }
+
+// What a partial result O (fp32, relative to 2^m) is divided by. bf16 cache: l the sum of the weights, lp of the rounded
+// ones, both relative to 2^m. 8-bit cache: l the sum of the weights relative to 2^lm, the maximum of the scores alone, where
+// m is that of the scores with their values' exponents.
+struct Stats {
+    float m, l, lp, lm;
+};
+__device__ __forceinline__ Stats load_stats(const float4 *p)
+{
+    const float4 v = __ldcg(p);
+    return Stats{v.x, v.y, v.z, v.w};
+}
+// nothing
+__device__ __forceinline__ Stats no_stats() { return Stats{-CUDART_INF_F, 0.0f, 0.0f, -CUDART_INF_F}; }
+// the maxima of both
+template <bool E4M3>
+__device__ __forceinline__ void raise_stats(Stats &a, float m, float lm)
+{
+    a.m = fmaxf(a.m, m);
+    if constexpr (E4M3) a.lm = fmaxf(a.lm, lm);
+}
+// adds b's sums to a's, whose maxima are b's at least
+template <bool E4M3>
+__device__ __forceinline__ void add_stats(Stats &a, const Stats &b)
+{
+    const float from = E4M3 ? b.lm : b.m, to = E4M3 ? a.lm : a.m, e = from == to ? 0.0f : from - to;
+    a.l += scaled(b.l, e);
+    if constexpr (!E4M3) a.lp += scaled(b.lp, e);
+}
 
 // One thread's share of a joined result: 8 channels of a head
 struct Joined {
     float o[8];
-    float m, l, lp;
+    Stats s;
 };
 
 // Weights and sums of the partial results 0, step, 2 step, ... (count of them) of the parts that begin at CTA c0, left in
 // shared memory for join_parts. All threads.
 struct Weights {
     float w[kMaxJoin][kSlotHeads];
-    float m[kSlotHeads], l[kSlotHeads], lp[kSlotHeads];
+    Stats s[kSlotHeads];
 };
+template <bool E4M3>
 __device__ __forceinline__ void weigh_parts(const Params &p, Weights &ws, int c0, int first, int step, int count, int heads)
 {
     // eight threads a head, which take every eighth part
     static_assert(kThreads == 8 * kSlotHeads, "a thread's head and parts");
     constexpr int kEach = (kMaxJoin + 7) / 8;
     const int head = threadIdx.x / 8, j = threadIdx.x % 8;
-    float4 s[kEach];
-    float m = -CUDART_INF_F, l = 0.0f, lp = 0.0f;
+    Stats s[kEach], all = no_stats();
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
         const int i = k * 8 + j;
-        s[k] = make_float4(-CUDART_INF_F, 0.0f, 0.0f, 0.0f);
-        if (i < count && head < heads) s[k] = __ldcg(p.part_s + slot_of(c0, first + i * step) * kSlotHeads + head);
+        s[k] = no_stats();
+        if (i < count && head < heads) s[k] = load_stats(p.part_s + slot_of(c0, first + i * step) * kSlotHeads + head);
     }
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) m = fmaxf(m, s[k].x);
+    for (int k = 0; k < kEach; ++k) raise_stats<E4M3>(all, s[k].m, s[k].lm);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const float base = m == -CUDART_INF_F ? 0.0f : m;
+    for (int o = 1; o < 8; o <<= 1)
+        raise_stats<E4M3>(all, __shfl_xor_sync(0xFFFFFFFFu, all.m, o), __shfl_xor_sync(0xFFFFFFFFu, all.lm, o));
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
         const int i = k * 8 + j;
         if (i >= count || head >= heads) continue;
-        const float w = ex2_approx(s[k].x - base);
-        ws.w[i][head] = w;
-        l += scaled(s[k].y, s[k].x - base);
-        lp += scaled(s[k].z, s[k].x - base);
+        ws.w[i][head] = rescale(s[k].m, all.m);
+        add_stats<E4M3>(all, s[k]);
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-        lp += __shfl_xor_sync(0xFFFFFFFFu, lp, o);
+        all.l += __shfl_xor_sync(0xFFFFFFFFu, all.l, o);
+        if constexpr (!E4M3) all.lp += __shfl_xor_sync(0xFFFFFFFFu, all.lp, o);
     }
-    if (j == 0) ws.m[head] = m, ws.l[head] = l, ws.lp[head] = lp;
+    if (j == 0) ws.s[head] = all;
     __syncthreads();
 }
 
@@ -258,7 +285,7 @@ template <int D>
 __device__ __forceinline__ Joined join_parts(const Params &p, const Weights &ws, int c0, int first, int step, int count, int head, int ch)
 {
     Joined r;
-    r.m = ws.m[head], r.l = ws.l[head], r.lp = ws.lp[head];
+    r.s = ws.s[head];
 #pragma unroll
     for (int k = 0; k < 8; ++k) r.o[k] = 0.0f;
     for (int i0 = 0; i0 < count; i0 += 8) {
@@ -282,17 +309,21 @@ __device__ __forceinline__ Joined join_parts(const Params &p, const Weights &ws,
     return r;
 }
 
+template <bool E4M3>
 __device__ __forceinline__ void write_result(const Params &p, int b, int h, int ch, const Joined &r)
 {
-    const float inv = r.lp != 0.0f ? 1.0f / r.lp : 0.0f;
-    uint4 v;
-    v.x = pack_bf16x2(r.o[0] * inv, r.o[1] * inv);
-    v.y = pack_bf16x2(r.o[2] * inv, r.o[3] * inv);
-    v.z = pack_bf16x2(r.o[4] * inv, r.o[5] * inv);
-    v.w = pack_bf16x2(r.o[6] * inv, r.o[7] * inv);
-    *reinterpret_cast<uint4 *>(p.o.p + b * p.o.token + h * p.o.head + ch * 2) = v;
+    const Stats &s = r.s;
+    const float sum = E4M3 ? s.l : s.lp, inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    float o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        o[k] = r.o[k] * inv;
+        if constexpr (E4M3) o[k] = scaled(o[k], s.m == s.lm ? 0.0f : s.m - s.lm);  // (equal: also without a score)
+    }
+    *reinterpret_cast<uint4 *>(p.o.p + b * p.o.token + h * p.o.head + ch * 2) =
+        make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
     if (ch == 0 && p.lse)
-        p.lse[static_cast<int64_t>(b) * p.H + h] = (r.m + log2f(r.l)) * 0.69314718055994530942f;
+        p.lse[static_cast<int64_t>(b) * p.H + h] = ((E4M3 ? s.lm : s.m) + log2f(s.l)) * 0.69314718055994530942f;
 }
 
 template <int D, bool E4M3, int NH>
@@ -304,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int scan[kWarps];
     __shared__ int found[3];  // sequence, unit within it, length
-    __shared__ float st_m[kWarps][8 * NH], st_l[kWarps][8 * NH], st_lp[kWarps][8 * NH];
+    __shared__ Stats st[kWarps][8 * NH];
     __shared__ uint32_t arrived;
     __shared__ Weights weights;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -506,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
         }
     }
 
-    float m[NH][2], l[NH][2], lp[NH][2];
+    float m[NH][2], l[NH][2], lp[NH][2], lm[NH][2];  // as in Stats
     float o[KS][NH][4];        // O^T: rows are channels, columns heads 2j and 2j + 1
     int stage = 0;
     while (u < u_hi) {
@@ -519,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) m[n][k] = -CUDART_INF_F, l[n][k] = lp[n][k] = 0.0f;
+            for (int k = 0; k < 2; ++k) m[n][k] = lm[n][k] = -CUDART_INF_F, l[n][k] = lp[n][k] = 0.0f;
 #pragma unroll
             for (int t = 0; t < KS; ++t)
 #pragma unroll
@@ -570,35 +601,47 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
 #pragma unroll
                         for (int k = 0; k < 4; ++k) s[h][n][k] = s2[n][0][k] + s2[n][1][k];
                 }
-                // log2 of the weights, of tokens r and r + 8 of each half
-                float d[kHalves][2];  // 2^-e of the values
+                // scores in log2, of tokens r and r + 8 of each half
+                float ve[kHalves][2];  // exponents of the values
+                auto product = [&](int h, int n, int k) { return E4M3 ? s[h][n][k] + ve[h][k >> 1] : s[h][n][k]; };
                 bool pass = false;
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
                     const bool in[2] = {h * 16 + r < left, h * 16 + r + 8 < left};
-                    float ke[2] = {1.0f, 1.0f}, ve[2] = {0.0f, 0.0f};
+                    float ke[2] = {1.0f, 1.0f};
                     if constexpr (E4M3) {
                         const uint32_t ea = ka + 2 * R::kData + h * 16 + r;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            const uint32_t kb = lds8(ea + 8 * t), vb = lds8(ea + kTile + 8 * t);
-                            ke[t] = __uint_as_float(kb << 23);
-                            ve[t] = static_cast<float>(static_cast<int>(vb) - 127);
-                            d[h][t] = __uint_as_float((254u - min(vb, 253u)) << 23);
+                            ke[t] = __uint_as_float(lds8(ea + 8 * t) << 23);
+                            ve[h][t] = static_cast<float>(static_cast<int>(lds8(ea + kTile + 8 * t)) - 127);
                         }
                     }
 #pragma unroll
                     for (int n = 0; n < NH; ++n)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            float x = s[h][n][k];
-                            if constexpr (E4M3) x = fmaf(x, qs[n][k & 1] * ke[k >> 1], ve[k >> 1]);
-                            else x *= qs[n][k & 1];
+                            float x = s[h][n][k] * (E4M3 ? qs[n][k & 1] * ke[k >> 1] : qs[n][k & 1]);
                             x = in[k >> 1] ? x : -CUDART_INF_F;
                             s[h][n][k] = x;
-                            pass |= x > m[n][k & 1] + kRaise;
+                            pass |= product(h, n, k) > m[n][k & 1] + kRaise;
                         }
                 }
+                // the maximum of the scores alone, and the sum relative to it
+                auto raise_sums = [&]() {
+#pragma unroll
+                    for (int n = 0; n < NH; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float x = lm[n][c];
+#pragma unroll
+                            for (int h = 0; h < kHalves; ++h) x = fmax3(x, s[h][n][c], s[h][n][2 + c]);
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
+                            l[n][c] *= rescale(lm[n][c], x);
+                            lm[n][c] = x;
+                        }
+                };
                 if (__any_sync(0xFFFFFFFFu, pass)) {
 #pragma unroll
                     for (int n = 0; n < NH; ++n)
@@ -606,42 +649,42 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                         for (int c = 0; c < 2; ++c) {
                             float x = m[n][c];
 #pragma unroll
-                            for (int h = 0; h < kHalves; ++h) x = fmax3(x, s[h][n][c], s[h][n][2 + c]);
+                            for (int h = 0; h < kHalves; ++h) x = fmax3(x, product(h, n, c), product(h, n, 2 + c));
 #pragma unroll
                             for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
-                            const float a = x == m[n][c] ? 1.0f : ex2_approx(m[n][c] - x);
-                            if constexpr (E4M3) l[n][c] = x == m[n][c] ? l[n][c] : scaled(l[n][c], m[n][c] - x);
-                            else l[n][c] *= a;
+                            const float a = rescale(m[n][c], x);
                             m[n][c] = x;
-                            lp[n][c] *= a;
+                            if constexpr (!E4M3) l[n][c] *= a, lp[n][c] *= a;
 #pragma unroll
                             for (int t = 0; t < KS; ++t) o[t][n][c] *= a, o[t][n][2 + c] *= a;
                         }
+                    if constexpr (E4M3) raise_sums();
                 }
                 if constexpr (E4M3) {
-                    // a weight times its value's unit may vanish beside the largest one where the weight does not (zeros have
-                    // the least exponent there is): such tiles' weights are summed by themselves
-                    float hi = -CUDART_INF_F, most = 0.0f;
+                    float sum[NH][2];
+                    auto weights = [&]() -> bool {  // false: some are far above the maximum that they are relative to
+                        bool small = true;
 #pragma unroll
-                    for (int n = 0; n < NH; ++n) hi = fmax3(hi, m[n][0], m[n][1]);
+                        for (int n = 0; n < NH; ++n)
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h)
+                            for (int c = 0; c < 2; ++c) {
+                                const float base = lm[n][c] == -CUDART_INF_F ? 0.0f : lm[n][c];
+                                sum[n][c] = 0.0f;
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            if (h * 16 + r + 8 * t < left) most = fmaxf(most, d[h][t]);
-                    if (__any_sync(0xFFFFFFFFu, hi + log2_of(most) > kFarApart)) {
-#pragma unroll
-                        for (int h = 0; h < kHalves; ++h) {
-#pragma unroll
-                            for (int n = 0; n < NH; ++n)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const float base = m[n][k & 1] == -CUDART_INF_F ? 0.0f : m[n][k & 1];
-                                    l[n][k & 1] += ex2_approx(s[h][n][k] - base + log2_of(d[h][k >> 1]));
-                                }
-                            d[h][0] = d[h][1] = 0.0f;
-                        }
+                                for (int h = 0; h < kHalves; ++h)
+                                    sum[n][c] += ex2_approx(s[h][n][c] - base) + ex2_approx(s[h][n][2 + c] - base);
+                                small &= !(sum[n][c] > kRaiseSum);  // NaN stays
+                            }
+                        return __all_sync(0xFFFFFFFFu, small);
+                    };
+                    if (!weights()) {  // the scores rise while the values' exponents fall
+                        raise_sums();
+                        weights();
                     }
+#pragma unroll
+                    for (int n = 0; n < NH; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) l[n][c] += sum[n][c];
                 }
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
@@ -652,9 +695,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float base = m[n][k & 1] == -CUDART_INF_F ? 0.0f : m[n][k & 1];
-                            w[k] = ex2_approx(s[h][n][k] - base);
-                            if constexpr (E4M3) l[n][k & 1] = fmaf(w[k], d[h][k >> 1], l[n][k & 1]);
-                            else l[n][k & 1] += w[k];
+                            w[k] = ex2_approx(product(h, n, k) - base);
+                            if constexpr (!E4M3) l[n][k & 1] += w[k];
                         }
                         if constexpr (E4M3) {
                             pf[n][0] = pack_half2(w[0], w[1]);
@@ -727,11 +769,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                     l[n][h] += __shfl_xor_sync(0xFFFFFFFFu, l[n][h], w);
                     lp[n][h] += __shfl_xor_sync(0xFFFFFFFFu, lp[n][h], w);
                 }
-                if (r == 0) {
-                    st_m[warp][n * 8 + 2 * j + h] = m[n][h];
-                    st_l[warp][n * 8 + 2 * j + h] = l[n][h];
-                    st_lp[warp][n * 8 + 2 * j + h] = E4M3 ? l[n][h] : lp[n][h];
-                }
+                if (r == 0) st[warp][n * 8 + 2 * j + h] = Stats{m[n][h], l[n][h], lp[n][h], lm[n][h]};
             }
         __syncthreads();
         const bool is_whole = first == 0 && end == tiles;
@@ -745,8 +783,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int c = n * 8 + 2 * j + h;
-                const float M = fmaxf(fmaxf(st_m[0][c], st_m[1][c]), fmaxf(st_m[2][c], st_m[3][c]));
-                wt[h] = M == -CUDART_INF_F ? 0.0f : ex2_approx(m[n][h] - M);
+                const float M = fmaxf(fmaxf(st[0][c].m, st[1][c].m), fmaxf(st[2][c].m, st[3][c].m));
+                wt[h] = rescale(m[n][h], M);
             }
             for (int w = 0; w < 2; ++w) {  // warps 0 and 1, then 2 and 3 into their buffers: the sum has one order
                 if (w == warp >> 1) {
@@ -773,27 +811,24 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                 const int hd = i / (D / 8), ch = (i % (D / 8)) * 8, c = n * 8 + hd;
                 if (head0 + c >= p.g) continue;
                 Joined res;
-                res.m = fmaxf(fmaxf(st_m[0][c], st_m[1][c]), fmaxf(st_m[2][c], st_m[3][c]));
-                res.l = res.lp = 0.0f;
+                res.s = no_stats();
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float off = res.m == -CUDART_INF_F ? -CUDART_INF_F : st_m[w][c] - res.m;
-                    res.l += scaled(st_l[w][c], off);
-                    res.lp += scaled(st_lp[w][c], off);
-                }
+                for (int w = 0; w < kWarps; ++w) raise_stats<E4M3>(res.s, st[w][c].m, st[w][c].lm);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) add_stats<E4M3>(res.s, st[w][c]);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int at = hd * R::kPad + R::channel_at(ch + k);
                     res.o[k] = join[at] + join[8 * R::kPad + at];
                 }
                 if (is_whole) {
-                    write_result(p, b, kh * p.g + head0 + c, ch, res);
+                    write_result<E4M3>(p, b, kh * p.g + head0 + c, ch, res);
                 } else {
                     const size_t row = slot_of(c0, part) * kSlotHeads + c;
                     float4 *dst = reinterpret_cast<float4 *>(p.part_o + row * D + ch);
                     dst[0] = make_float4(res.o[0], res.o[1], res.o[2], res.o[3]);
                     dst[1] = make_float4(res.o[4], res.o[5], res.o[6], res.o[7]);
-                    if (ch == 0) p.part_s[row] = make_float4(res.m, res.l, res.lp, 0.0f);
+                    if (ch == 0) p.part_s[row] = make_float4(res.s.m, res.s.l, res.s.lp, res.s.lm);
                 }
             }
             __syncthreads();
@@ -820,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
             const int heads = min(8 * NH, p.g - head0);
             if (last_of(p.tickets + (group == 0 ? 0 : kCacheMaxCtas) + c0 + group * kGroup, members)) {
                 const bool final_join = groups == 1;
-                weigh_parts(p, weights, c0, group * kGroup, 1, members, heads);
+                weigh_parts<E4M3>(p, weights, c0, group * kGroup, 1, members, heads);
                 constexpr int kRounds = 8 * NH * (D / 8) / kThreads > 0 ? 8 * NH * (D / 8) / kThreads : 1;
                 Joined res[kRounds];
 #pragma unroll
@@ -835,20 +870,20 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attention_kernel(const Para
                     const int i = k * kThreads + tid, hd = i / (D / 8), ch = (i % (D / 8)) * 8;
                     if (hd >= heads) continue;
                     if (final_join) {
-                        write_result(p, b, kh * p.g + head0 + hd, ch, res[k]);
+                        write_result<E4M3>(p, b, kh * p.g + head0 + hd, ch, res[k]);
                         continue;
                     }
                     const size_t row = slot_of(c0, group * kGroup) * kSlotHeads + hd;
                     float4 *dst = reinterpret_cast<float4 *>(p.part_o + row * D + ch);
                     dst[0] = make_float4(res[k].o[0], res[k].o[1], res[k].o[2], res[k].o[3]);
                     dst[1] = make_float4(res[k].o[4], res[k].o[5], res[k].o[6], res[k].o[7]);
-                    if (ch == 0) p.part_s[row] = make_float4(res[k].m, res[k].l, res[k].lp, 0.0f);
+                    if (ch == 0) p.part_s[row] = make_float4(res[k].s.m, res[k].s.l, res[k].s.lp, res[k].s.lm);
                 }
                 if (!final_join && last_of(p.tickets + 2 * kCacheMaxCtas + c0, groups)) {
-                    weigh_parts(p, weights, c0, 0, kGroup, groups, heads);
+                    weigh_parts<E4M3>(p, weights, c0, 0, kGroup, groups, heads);
                     for (int i = tid; i < heads * (D / 8); i += kThreads) {
                         const int hd = i / (D / 8), ch = (i % (D / 8)) * 8;
-                        write_result(p, b, kh * p.g + head0 + hd, ch, join_parts<D>(p, weights, c0, 0, kGroup, groups, hd, ch));
+                        write_result<E4M3>(p, b, kh * p.g + head0 + hd, ch, join_parts<D>(p, weights, c0, 0, kGroup, groups, hd, ch));
                     }
                 }
             }
@@ -862,7 +897,7 @@ bsa_status launch(const CacheAttentionArgs &a, cudaStream_t st)
 {
     using R = Ring<D, E4M3>;
     auto kern = cache_attention_kernel<D, E4M3, NH>;
-    static_assert(2 * (R::kBytes + 1024 + 6400) <= 233472, "two CTAs per SM");
+    static_assert(2 * (R::kBytes + 1024 + 6528) <= 233472, "two CTAs per SM");
     static std::atomic<uint64_t> ready{0};
     if (!allow_shared_memory(kern, R::kBytes, ready)) return BSA_ERR_CUDA;
     int sms = 0;

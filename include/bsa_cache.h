@@ -115,8 +115,8 @@ bsa_status bsa_cache_read(const bsa_kv_cache *cache, const bsa_page_table *table
  * the cache count as zeros. With an 8-bit cache the products are those of the values held; scores,
  * sums and accumulators are fp32, weights are rounded to 11 bits (bf16 cache: 8 bits, and O is
  * divided by the sum of the rounded weights). A weight of an 8-bit cache is rounded together with its
- * row's power of two, so its product is off by up to 2^-24 of the largest one; beside values above 2^90
- * the sum misses weights below 2^-30.
+ * row's power of two, so its product is off by up to 2^-24 of the largest one; the sum, of unrounded
+ * weights, has every one of them at fp32's precision, whatever the values beside it.
  * One launch. Errors: as bsa_cache_write.
  */
 bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, int dt, int H,

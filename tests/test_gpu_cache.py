@@ -11,6 +11,7 @@ from tests import cache_ref as ref
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 BF16 = torch.bfloat16
+INF = float("inf")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -448,3 +449,63 @@ def test_thousands_of_sequences(kind):
     check_decode(q[some].contiguous(), cache, values, table[some], [held[b] for b in some], page, kind, out=out[some], lse=lse[some])
     empty = torch.tensor(held, device=DEV) == 0
     assert (out[empty] == 0).all() and (lse[empty] == float("-inf")).all()
+
+
+@pytest.mark.parametrize("d,H,held", [(64, 4, [300]), (128, 16, [5000, 17]), (128, 3, [40000])])
+@pytest.mark.parametrize("large", [24, 45, 84, 118])
+@pytest.mark.parametrize("level,lift", [(-30, 0), (-40, 5), (-60, 0), (-60, 9), (-200, 5), (0, 9), (60, 0), (200, 5)])
+def test_weights_count_at_any_level_of_the_scores(d, H, held, large, level, lift):
+    """8-bit rows: zeros and the least exponent, and one in fifty of them large. Every score is moved by `level`, and the large
+    rows' by `lift` more: a row's weight is part of the sum wherever the scores lie and however small its value is beside
+    another's (of up to 2^127)"""
+    g = gen(16)
+    page = 32
+    table, n_pages = paged(g, held, page)
+    cache, values = filled(g, n_pages, page, 1, d, "e4m3")
+    kind = torch.randint(0, 50, cache.v_exp.shape, generator=g, device=DEV)
+    big = kind == 49
+    k = draw(g, *values[0].shape)
+    k[..., 0], k[..., 1] = -8.0, torch.where(big, 1.0, 0.0)
+    k, e = ref.e4m3_rows(k.to(BF16))
+    cache.k.copy_((k / ((e.long() - 127 + 1023) << 52).view(torch.float64)[..., None]).float())
+    cache.k_exp.copy_(e)
+    data = values[1] * torch.pow(2.0, -(cache.v_exp.double() - 127))[..., None]
+    data = torch.where((kind < 25)[..., None], 0.0, data)
+    exps = torch.where(big, cache.v_exp.long() + large, 27).clamp(max=246)
+    cache.v.copy_(data.float())
+    cache.v_exp.copy_(exps.to(torch.uint8))
+    values = [k, data * torch.pow(2.0, (exps - 127).double())[..., None]]
+    q = draw(g, len(held), H, d)
+    q[..., 0], q[..., 1] = -level * d ** 0.5 / 8, lift * d ** 0.5
+    q = q.to(BF16)
+    out, lse = pkg.cache_attention(q, cache, table, ints(held))
+    check_decode(q, cache, values, table, held, page, "e4m3", out=out, lse=lse)
+
+
+def test_scores_rise_while_the_values_become_smaller():
+    """the running maximum of scores and values together stays, that of the scores alone rises by a hundred, within one CTA's
+    share too; and a key that is not finite"""
+    g = gen(17)
+    B, n, page, H, d = 150, 1200, 64, 2, 64
+    at = torch.arange(n, device=DEV)
+    k, v = draw(g, n, 1, d), draw(g, n, 1, d) * torch.pow(2.0, 60 - at * 0.125)[:, None, None]
+    k[:, 0, 0] = at * (8.0 / n)                   # scores of up to 100, 144 as powers of two
+    k, v = k.to(BF16), v.to(BF16)
+    table, n_pages = paged(g, [n, n], page)
+    cache = pkg.kv_cache(n_pages, page, 1, d, "e4m3", DEV)
+    other = k.clone()
+    other[700, 0, 3] = INF
+    pkg.cache_write(cache, torch.cat((k, other)), torch.cat((v, v)), table, ints([n, n]), ints([0, n, 2 * n]))
+    table = torch.cat((table, table[:1].expand(B - 2, -1)))  # all but one read the same pages
+    q = draw(g, B, H, d)
+    q[..., 0] = 100.0
+    q = q.to(BF16)
+    out, lse = pkg.cache_attention(q, cache, table, ints([n] * B))
+    assert out[1].isnan().all() and lse[1].isnan().all()
+    keep = torch.arange(B, device=DEV) != 1
+    k, v = (ref.e4m3_rows(x)[0][:, 0] for x in (k, v))
+    see = torch.ones(1, n, dtype=torch.bool, device=DEV).expand(B - 1, n)
+    for h in range(H):
+        o, bo, l, bl = ref.attention(q[keep, h], k, v, see, d ** -0.5, half_weights=True)
+        ref.within(out[keep, h], o, bo, "O")
+        ref.within(lse[keep, h], l, bl, "LSE")
