@@ -132,7 +132,7 @@ bsa_status bsa_cache_write(const bsa_kv_cache *cache, const bsa_packed *k, const
     if (!all.check()) return BSA_ERR_INVALID_ARG;
     a.kv_lens = kv_lens;
     a.cu = cu;
-    return T == 0 ? BSA_OK : bsa::launch_cache_write(a, static_cast<cudaStream_t>(stream));
+    return bsa::launch_cache_write(a, static_cast<cudaStream_t>(stream));
 }
 
 bsa_status bsa_cache_read(const bsa_kv_cache *cache, const bsa_page_table *table, const int32_t *cu, const bsa_packed *k,
@@ -145,7 +145,7 @@ bsa_status bsa_cache_read(const bsa_kv_cache *cache, const bsa_page_table *table
     if (!reads_ints(cu, static_cast<int64_t>(table->B) + 1, &all)) return BSA_ERR_INVALID_ARG;
     if (!all.check()) return BSA_ERR_INVALID_ARG;
     a.cu = cu;
-    return T == 0 ? BSA_OK : bsa::launch_cache_read(a, static_cast<cudaStream_t>(stream));
+    return bsa::launch_cache_read(a, static_cast<cudaStream_t>(stream));
 }
 
 bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, int dt, int H, const bsa_page_table *table,

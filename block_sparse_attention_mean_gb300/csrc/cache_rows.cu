@@ -15,6 +15,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "cache_internal.h"
 #include "ptx.cuh"
 
@@ -22,17 +24,32 @@ namespace bsa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCheckCtas = 64;  // that look at the sequences, at most
 
-// Sequence of packed token t: the last b with cu[b] <= t. False for a token of no sequence, and (with the error
-// raised) of a malformed one. [t - cu[b], cu[b + 1] - cu[b]) is returned as (at, n).
-__device__ __forceinline__ bool find_sequence(const int32_t *cu, int B, int T, int t, int &b, int &at, int &n, uint32_t *err)
+// tokens that a sequence's row of the table has room for
+__device__ __forceinline__ int64_t room(const CacheRowsArgs &a) { return static_cast<int64_t>(a.table.width) << a.cache.page_shift; }
+
+// Reports sequences that are malformed: a token finds one sequence, and what is wrong with others (those between that decrease,
+// those that no token falls in) shows nowhere else. The first `ctas` of the launch do nothing else, so that short calls do not
+// wait for it. WRITE: the lengths too.
+template <bool WRITE>
+__device__ __forceinline__ void check_sequences(const CacheRowsArgs &a, int ctas)
+{
+    for (int64_t b = blockIdx.x * kThreads + threadIdx.x; b < a.table.B; b += ctas * kThreads) {
+        const int begin = a.cu ? __ldg(a.cu + b) : 0, end = a.cu ? __ldg(a.cu + b + 1) : 1;
+        bool ok = begin >= 0 && end >= begin && end <= a.T;
+        const int64_t n = static_cast<int64_t>(end) - begin, len = WRITE ? __ldg(a.kv_lens + b) : n;
+        ok = ok && len >= n && len <= room(a);
+        if (!ok) raise_error(a.err, BSA_ERR_INVALID_ARG);
+    }
+}
+
+// Sequence of packed token t: the last b with cu[b] <= t (of an ordered cu). False for a token of no sequence, and of a
+// malformed one. [t - cu[b], cu[b + 1] - cu[b]) is returned as (at, n).
+__device__ __forceinline__ bool find_sequence(const int32_t *cu, int B, int T, int t, int &b, int &at, int &n)
 {
     int lo = 0, hi = B;  // cu[lo] <= t < cu[hi], if at all
-    if (t < __ldg(cu)) {
-        if (__ldg(cu) > T) raise_error(err, BSA_ERR_INVALID_ARG);
-        return false;
-    }
-    if (t >= __ldg(cu + B)) return false;
+    if (t < __ldg(cu) || t >= __ldg(cu + B)) return false;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (__ldg(cu + mid) <= t) lo = mid;
@@ -42,11 +59,7 @@ __device__ __forceinline__ bool find_sequence(const int32_t *cu, int B, int T, i
     b = lo;
     at = t - begin;
     n = end - begin;
-    if (begin < 0 || end > T || begin > t || end <= t) {
-        raise_error(err, BSA_ERR_INVALID_ARG);
-        return false;
-    }
-    return true;
+    return begin >= 0 && end <= T && begin <= t && end > t;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -76,10 +89,10 @@ template <int D, int HEADS>
 struct Unit {
     int t, kv, h0, lane;
     bool any;
-    __device__ __forceinline__ Unit(int64_t T, int groups)
+    __device__ __forceinline__ Unit(unsigned cta, int64_t T, int groups)
     {
         constexpr int LPR = D / 8;
-        const int64_t u = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LPR;
+        const int64_t u = (static_cast<int64_t>(cta) * kThreads + threadIdx.x) / LPR;
         lane = threadIdx.x % LPR;
         any = u < T * 2 * groups;
         const int64_t r = u / groups;
@@ -96,10 +109,14 @@ __device__ __forceinline__ int64_t row_of(const CacheView &c, int page, int head
 }
 
 template <int D, bool E4M3, int HEADS>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheRowsArgs a, int groups)
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheRowsArgs a, int groups, int check_ctas)
 {
+    if (static_cast<int>(blockIdx.x) < check_ctas) {
+        check_sequences<true>(a, check_ctas);
+        return;
+    }
     constexpr int LPR = D / 8;
-    const Unit<D, HEADS> u(a.T, groups);
+    const Unit<D, HEADS> u(blockIdx.x - check_ctas, a.T, groups);
     // the rows are on their way while their place is looked up: the tensor has them, whether a sequence does or not
     const PackedView &src = u.kv ? a.v : a.k;
     int heads = u.any ? min(HEADS, a.cache.heads - u.h0) : 0;
@@ -113,19 +130,19 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheRowsAr
     bool ok = u.any;
     int b = 0, at = 0, n = 1, page = 0, row = 0;
     if (ok) {
-        if (a.cu) ok = find_sequence(a.cu, a.table.B, a.T, u.t, b, at, n, a.err);
+        if (a.cu) ok = find_sequence(a.cu, a.table.B, a.T, u.t, b, at, n);
         else b = u.t;
     }
     if (ok) {
         const int len = __ldg(a.kv_lens + b);
         const int64_t place = static_cast<int64_t>(len) - n + at;
-        ok = len >= n && len <= (static_cast<int64_t>(a.table.width) << a.cache.page_shift);
+        ok = len >= n && len <= room(a);
         if (ok) {
             page = __ldg(a.table.pages + b * a.table.stride + (place >> a.cache.page_shift));
             row = static_cast<int>(place & ((1 << a.cache.page_shift) - 1));
             ok = page >= 0 && page < a.cache.n_pages;
+            if (!ok) raise_error(a.err, BSA_ERR_INVALID_ARG);
         }
-        if (!ok) raise_error(a.err, BSA_ERR_INVALID_ARG);
     }
     if (!ok) heads = 0;
     char *data = u.kv ? a.cache.v : a.cache.k;
@@ -183,17 +200,17 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w, float unit)
 }
 
 template <int D, bool E4M3, int HEADS>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArgs a, int groups)
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheRowsArgs a, int groups, int check_ctas)
 {
-    constexpr int LPR = D / 8;
-    const Unit<D, HEADS> u(a.T, groups);
-    if (!u.any) return;
-    int b = 0, at = 0, n = 0, page = 0, row = 0;
-    if (!find_sequence(a.cu, a.table.B, a.T, u.t, b, at, n, a.err)) return;
-    if (n > (static_cast<int64_t>(a.table.width) << a.cache.page_shift)) {
-        raise_error(a.err, BSA_ERR_INVALID_ARG);
+    if (static_cast<int>(blockIdx.x) < check_ctas) {
+        check_sequences<false>(a, check_ctas);
         return;
     }
+    constexpr int LPR = D / 8;
+    const Unit<D, HEADS> u(blockIdx.x - check_ctas, a.T, groups);
+    if (!u.any) return;
+    int b = 0, at = 0, n = 0, page = 0, row = 0;
+    if (!find_sequence(a.cu, a.table.B, a.T, u.t, b, at, n) || n > room(a)) return;
     page = __ldg(a.table.pages + b * a.table.stride + (at >> a.cache.page_shift));
     row = at & ((1 << a.cache.page_shift) - 1);
     const bool there = page >= 0 && page < a.cache.n_pages;
@@ -238,10 +255,10 @@ bsa_status launch_rows(Kernel kern, const CacheRowsArgs &a, cudaStream_t st)
 {
     const int groups = (a.cache.heads + HEADS - 1) / HEADS;
     const int64_t threads = static_cast<int64_t>(a.T) * 2 * groups * (a.d / 8);
-    const int64_t ctas = (threads + kThreads - 1) / kThreads;
+    const int check = std::min((a.table.B - 1) / kThreads + 1, kCheckCtas);
+    const int64_t ctas = (threads + kThreads - 1) / kThreads + check;
     if (ctas > INT32_MAX) return BSA_ERR_SHAPE;
-    if (ctas == 0) return BSA_OK;
-    kern<<<static_cast<unsigned>(ctas), kThreads, 0, st>>>(a, groups);
+    kern<<<static_cast<unsigned>(ctas), kThreads, 0, st>>>(a, groups, check);
     return cudaGetLastError() == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 

@@ -25,8 +25,9 @@
  *   - What only the device can see goes to the workspace's first word, which bsa_check_device_error
  *     returns and clears: BSA_ERR_INVALID_ARG for a page outside the cache, a length below zero or
  *     beyond its page table, and a cu that decreases or leaves its tensor. Such a token or sequence
- *     is left out (see each call); nothing outside the buffers is read or written. BSA_ERR_TIMEOUT:
- *     a bounded wait gave up.
+ *     is left out (see each call); nothing outside the buffers is read or written. Where a cu
+ *     decreases, which tokens of the other sequences bsa_cache_write and bsa_cache_read move is
+ *     unspecified, as are results of sequences that overlap. BSA_ERR_TIMEOUT: a bounded wait gave up.
  *   - Workspaces are 256-byte aligned; the first BSA_CACHE_ROWS_WORKSPACE bytes of a new one are
  *     zero-filled once before its first call. Calls that share one must not overlap on the GPU. One
  *     workspace of sufficient size serves all four calls in turn, captured into graphs or not. Its size
@@ -85,7 +86,8 @@ typedef struct {
  *   cu          device int32 [B + 1], or NULL: one token per sequence (T == B)
  * No other row of the cache changes. Places that two tokens of one call share (sequences that
  * share a page and both write to it) have unspecified contents. T may be 0.
- * A token whose sequence is malformed, or whose page is outside the cache, is not written.
+ * A token whose sequence is malformed, or whose page is outside the cache, is not written. Malformed
+ * sequences are reported with new tokens or without.
  * One launch. Errors: BSA_ERR_SHAPE, BSA_ERR_DTYPE, BSA_ERR_INVALID_ARG (null or misaligned
  * pointers, strides, kind, page size, k or v overlapping the cache), BSA_ERR_WORKSPACE, BSA_ERR_CUDA.
  */
@@ -134,7 +136,7 @@ bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, i
  * A query that sees no key (no keys, or causal with n_q > n_k) has O = 0 and LSE = -inf. Rows of O
  * and LSE that belong to no sequence, and those of a malformed sequence, are left as they were.
  * What a query does not see does not reach it, NaN and infinities included. O must not overlap an
- * input. T_q may be 0.
+ * input. T_q may be 0: nothing is enqueued, and nothing reported.
  * Scores, sums and accumulators are fp32; weights are rounded to bf16, and O is divided by their sum
  * before the rounding. One to three launches (one for few sequences with T_k <= 1024).
  * Errors: as bsa_cache_write.

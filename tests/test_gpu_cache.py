@@ -509,3 +509,54 @@ def test_scores_rise_while_the_values_become_smaller():
         o, bo, l, bl = ref.attention(q[keep, h], k, v, see, d ** -0.5, half_weights=True)
         ref.within(out[keep, h], o, bo, "O")
         ref.within(lse[keep, h], l, bl, "LSE")
+
+
+MALFORMED = [
+    # tokens, cu, well-formed sequences where cu nowhere decreases (else it is unspecified what is moved)
+    (50, [0, 50, 40], []), (8, [0, 5, 3, 8], []), (8, [0, 8, 12], [0]), (12, [0, 8, 4, 12], []), (8, [-3, 0, 8], [1]), (8, [9, 9], []),
+    (8, [3, 2, 2], []), (8, [0, 8, 3], []), (3, [0] * 299 + [-1] + [0] * 300 + [3], []), (0, [0, 4], []), (0, [-1, 0], []),
+]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,cu,sound", MALFORMED)
+def test_malformed_sequences_are_reported_wherever_they_are(T, cu, sound, kind):
+    """also those that no token falls in"""
+    g = gen(18)
+    B = len(cu) - 1
+    cache, values = filled(g, B * 4, 16, 2, 64, kind)
+    table = torch.randperm(B * 4, generator=g, device=DEV).to(torch.int32).view(B, 4)
+    ws = pkg.cache_workspace(T, B, 2, 2, 64, DEV)
+    k, v = rows(g, T, 2, 64)
+
+    def reported(call):
+        with pytest.raises(bb.BsaError) as e:
+            call()
+        assert e.value.code == bb.ERR_INVALID_ARG
+        pkg.cache_check(ws)
+
+    out = tuple(torch.full((T, 2, 64), 7.0, dtype=BF16, device=DEV) for _ in range(2))
+    reported(lambda: pkg.cache_read(cache, table, ints(cu), out=out, ws=ws))
+    for b in sound:
+        for o, x in zip(out, values):
+            assert torch.equal(o[cu[b]:cu[b + 1]].double(), sequence(x, table, b, cu[b + 1] - cu[b], 16))
+    reported(lambda: pkg.cache_write(cache, k, v, table, ints([60] * B), ints(cu), ws=ws))
+    for b in sound:
+        n = cu[b + 1] - cu[b]
+        got = pkg.cache_read(cache, table[b:b + 1], ints([0, 60]), 60, ws=ws)
+        for o, x in zip(got, (k, v)):
+            want = x[cu[b]:cu[b + 1]]
+            assert torch.equal(o[60 - n:].double(), want.double() if kind == "bf16" else ref.e4m3_rows(want)[0])
+
+
+@pytest.mark.parametrize("lens,cu", [([-1, 8], [0, 0, 8]), ([65, 8], [0, 0, 8]), ([8, 7], [0, 0, 8]), ([8, -2 ** 31], [0, 8, 8]),
+                                     ([2 ** 31 - 1, 64], [0, 0, 8]), ([-5], [0, 0]), ([5, 65], None), ([0, 5], None)])
+def test_lengths_of_sequences_without_new_tokens_are_looked_at(lens, cu):
+    g = gen(19)
+    cache, _ = filled(g, 8, 16, 2, 64, "bf16")
+    table = torch.arange(8, dtype=torch.int32, device=DEV).view(2, 4)[:len(lens)]
+    T = len(lens) if cu is None else cu[-1]
+    k, v = rows(g, T, 2, 64)
+    with pytest.raises(bb.BsaError) as e:
+        pkg.cache_write(cache, k, v, table, ints(lens), None if cu is None else ints(cu))
+    assert e.value.code == bb.ERR_INVALID_ARG
