@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheRowsAr
             for (int o = 1; o < LPR; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
             const int e = row_exp(max(big & 0xFFFFu, big >> 16));
             const float unit = exp2_int(-e);
+            const uint64_t none = f2_pack(-0.0f, -0.0f);  // the addend that keeps a zero's sign
             if (odd) {  // infinities to NaN: the conversion would make them 448
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w[k] |= __vcmpgeu2(w[k] & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheRowsAr
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float lo, hi;  // subnormals as zeros: at most 2^-26 after the product, far below the least step
-                f2_unpack(f2_fma(f2_pack(bf16_lo(w[k]), bf16_hi(w[k])), f2_pack(unit, unit), 0ull), lo, hi);
+                f2_unpack(f2_fma(f2_pack(bf16_lo(w[k]), bf16_hi(w[k])), f2_pack(unit, unit), none), lo, hi);
                 q[k] = to_e4m3x2(lo, hi);
             }
             if (i < heads) {

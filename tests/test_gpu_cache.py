@@ -560,3 +560,21 @@ def test_lengths_of_sequences_without_new_tokens_are_looked_at(lens, cu):
     with pytest.raises(bb.BsaError) as e:
         pkg.cache_write(cache, k, v, table, ints(lens), None if cu is None else ints(cu))
     assert e.value.code == bb.ERR_INVALID_ARG
+
+
+def test_zeros_keep_their_sign():
+    """and what is rounded to zero keeps its own, in either form of the 8-bit kernels"""
+    g = gen(20)
+    for T, Hk, d in ((40, 3, 64), (5000, 12, 128)):
+        x = draw(g, T, Hk, d)
+        x[..., ::3] = -0.0
+        x[..., 1::3] *= 2.0 ** -30
+        x[..., 4::9] *= 2.0 ** -100   # subnormal
+        x[T // 2] = -0.0
+        x = x.to(BF16)
+        table, n_pages = paged(g, [T], 64)
+        cache = pkg.kv_cache(n_pages, 64, Hk, d, "e4m3", DEV)
+        pkg.cache_write(cache, x, x, table, ints([T]), ints([0, T]))
+        want = ref.e4m3_rows(x)[0]
+        for got in pkg.cache_read(cache, table, ints([0, T]), T):
+            assert torch.equal(got.double(), want) and torch.equal(got.signbit(), want.signbit())
