@@ -827,10 +827,11 @@ __device__ __forceinline__ void softmax_role(const Params &p, uint32_t sbase, ui
                     }
                 }
                 if (raised) break;
-                // a step sum of at most 2^8 bounds every weight: only a larger one raises the maximum (NaN stays NaN either way)
+                // a step sum of at most 2^8 bounds every weight: only a larger one raises the maximum (NaN stays NaN either way);
+                // and, of a row that has seen nothing but scores of -inf, any: its weights may all vanish beside the base of zero
                 float s0, s1;
                 f2_unpack(f2_add(sacc[0], sacc[1]), s0, s1);
-                const bool raise = s0 + s1 > kRescaleSum || (m_run == -CUDART_INF_F && s0 + s1 > 0.0f);
+                const bool raise = s0 + s1 > (m_run == -CUDART_INF_F ? -1.0f : kRescaleSum);
                 if (!__any_sync(0xFFFFFFFFu, raise)) break;
                 raised = true;  // the whole warp: TMEM accesses are the warp's
                 const float m_all = step_max();

@@ -113,12 +113,13 @@ bsa_status bsa_cache_read(const bsa_kv_cache *cache, const bsa_page_table *table
  *   scale       > 0, finite; 0 means 1 / sqrt(d)
  *   O           [B][H][d] (written)
  *   LSE         device fp32 [B][H], contiguous (written), or NULL
- * A sequence of length 0 has O = 0 and LSE = -inf; so has a malformed one. Tokens of a page outside
- * the cache count as zeros. With an 8-bit cache the products are those of the values held; scores,
- * sums and accumulators are fp32, weights are rounded to 11 bits (bf16 cache: 8 bits, and O is
- * divided by the sum of the rounded weights). A weight of an 8-bit cache is rounded together with its
- * row's power of two, so its product is off by up to 2^-24 of the largest one; the sum, of unrounded
- * weights, has every one of them at fp32's precision, whatever the values beside it.
+ * A sequence of length 0, or with no scores but -inf (over finite values), has O = 0 and LSE = -inf;
+ * so has a malformed one. Tokens of a page outside the cache count as zeros. With an 8-bit cache the
+ * products are those of the values held; scores, sums and accumulators are fp32, weights are rounded
+ * to 11 bits (bf16 cache: 8 bits, and O is divided by the sum of the rounded weights). A weight of an
+ * 8-bit cache is rounded together with its row's power of two, so its product is off by up to 2^-24 of
+ * the largest one; the sum, of unrounded weights, has every one of them at fp32's precision, whatever
+ * the values beside it.
  * One launch. Errors: as bsa_cache_write.
  */
 bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, int dt, int H,
@@ -133,10 +134,11 @@ bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, i
  *   cu_q, cu_k  device int32 [B + 1]
  *   scale       as bsa_cache_attention
  *   LSE         device fp32 [H][T_q], contiguous (written), or NULL
- * A query that sees no key (no keys, or causal with n_q > n_k) has O = 0 and LSE = -inf. Rows of O
- * and LSE that belong to no sequence, and those of a malformed sequence, are left as they were.
- * What a query does not see does not reach it, NaN and infinities included. O must not overlap an
- * input. T_q may be 0: nothing is enqueued, and nothing reported.
+ * A query that sees no key (no keys, or causal with n_q > n_k), or none but with scores of -inf and
+ * finite values, has O = 0 and LSE = -inf. Rows of O and LSE that belong to no sequence, and those of
+ * a malformed sequence, are left as they were. What a query does not see does not reach it, NaN and
+ * infinities included. O must not overlap an input. T_q may be 0: nothing is enqueued, and nothing
+ * reported.
  * Scores, sums and accumulators are fp32; weights are rounded to bf16, and O is divided by their sum
  * before the rounding. One to three launches (one for few sequences with T_k <= 1024).
  * Errors: as bsa_cache_write.

@@ -582,3 +582,25 @@ def test_short_items_of_few_sequences(H, Hk, d, causal):
     keys = [max(0, a + x) for a, x in zip(new, torch.randint(-300, 100, (32,), generator=g, device=DEV).tolist())]
     cu_q, cu_k = starts(new), starts(keys)
     check(draw(g, cu_q[-1], H, d), draw(g, cu_k[-1], Hk, d), draw(g, cu_k[-1], Hk, d), cu_q, cu_k, causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,first", [(64, 140), (128, 128), (128, 300), (64, 1)])
+def test_low_scores_behind_infinite_ones(d, first, causal):
+    """the first keys have scores of -inf, the others' lie far below zero: their weights count all the same"""
+    g = gen(14)
+    n = 600
+    q, k, v = (draw(g, n, 2, d) for _ in range(3))
+    q[..., 0], k[..., 0] = 16.0, -100.0     # scores of about -140 and -200
+    k[:first, 0, 0] = -INF
+    out, lse = pkg.prompt_attention(q, k, v, ints([0, n]), causal=causal)
+    rest = n - first
+    from_row = first if causal else 0
+    o, bo, l, bl = expected(q[from_row:, :1], k[first:, :1], v[first:, :1], [0, n - from_row], [0, rest], causal, d ** -0.5)
+    ref.within(out[from_row:, :1], o, bo, "O")
+    ref.within(lse[:1, from_row:], l, bl, "LSE")
+    o, bo, l, bl = expected(q[:, 1:], k[:, 1:], v[:, 1:], [0, n], [0, n], causal, d ** -0.5)
+    ref.within(out[:, 1:], o, bo, "O")
+    ref.within(lse[1:], l, bl, "LSE")
+    if causal:  # they see nothing else
+        assert (out[:first, 0] == 0).all() and (lse[0, :first] == -INF).all()
