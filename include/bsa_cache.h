@@ -119,7 +119,8 @@ bsa_status bsa_cache_read(const bsa_kv_cache *cache, const bsa_page_table *table
  * to 11 bits (bf16 cache: 8 bits, and O is divided by the sum of the rounded weights). A weight of an
  * 8-bit cache is rounded together with its row's power of two, so its product is off by up to 2^-24 of
  * the largest one; the sum, of unrounded weights, has every one of them at fp32's precision, whatever
- * the values beside it.
+ * the values beside it. Beside an 8-bit cache q is fp16, relative to the row's largest channel: a
+ * channel below 2^-17 of that is off by up to 2^-25 of it, and a score by that times scale sum |k|.
  * One launch. Errors: as bsa_cache_write.
  */
 bsa_status bsa_cache_attention(const bsa_kv_cache *cache, const bsa_packed *q, int dt, int H,
