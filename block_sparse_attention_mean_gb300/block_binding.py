@@ -6,7 +6,8 @@ As in ``binding`` there is no fallback: if libbsa.so cannot be loaded every call
 run on the tensors' device and on ``stream`` (that device's current stream by default), as under
 torch.cuda.stream(stream): what they allocate, results and workspace, belongs to that stream. They record
 nothing for autograd, and refuse a tensor that requires a gradient while gradients are recorded: call them
-under torch.no_grad() or inside a torch.autograd.Function, whose backward calls the backward helper.
+under torch.no_grad() or inside a torch.autograd.Function, whose backward calls the backward helper. A tensor
+that carries a tangent (forward-mode differentiation) is refused too.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import struct
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import binding
 from .binding import BF16, ERR_DTYPE, ERR_INVALID_ARG, ERR_SHAPE, FP32, OK, BsaError, _check, _ptr, _stream
@@ -205,6 +207,20 @@ def _view(t: torch.Tensor, shape, dtype: torch.dtype, device, what: str, name: s
                                     "torch.no_grad() or in a torch.autograd.Function")
 
 
+def _no_tangents(what: str, *tensors) -> None:
+    """Within a level of forward-mode differentiation: refuses tensors whose tangent would not reach the results."""
+    if not torch._C._is_fwd_grad_enabled():  # in a torch.autograd.Function's forward
+        return
+    for t in tensors:
+        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+            raise BsaError(ERR_INVALID_ARG, f"{what}: a tensor carries a tangent, which this call does not compute: call "
+                                            "it in a torch.autograd.Function with a jvp")
+
+
+def _of_norms(*norms):
+    return [t for n in norms if n is not None for t in (n.weight, n.bias)]
+
+
 def _cuda_device(t: torch.Tensor, what: str) -> torch.device:
     if not t.is_cuda:
         raise BsaError(ERR_INVALID_ARG, f"{what}: not a CUDA tensor")
@@ -356,6 +372,8 @@ def rotary(plan: RotaryPlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor
         with there:
             return rotary(plan, q, k, v, positions=positions, norm_eps=norm_eps, q_weight=q_weight, k_weight=k_weight,
                           out=out)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(what, q, k, v, q_weight, k_weight, *(out or ()))
     device, dtype, code, B, N, pos, pos_batch, weights = _rotary_args(
         plan, first, positions, q is not None or k is not None, norm_eps is not None, q_weight, k_weight, 1, what)
     d = plan.d
@@ -398,6 +416,8 @@ def rotary_backward(plan: RotaryPlan, dq: Optional[torch.Tensor], dk: Optional[t
         with there:
             return rotary_backward(plan, dq, dk, dv, positions=positions, q=q, k=k, norm_eps=norm_eps,
                                    q_weight=q_weight, k_weight=k_weight, out=out, ws=ws)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(what, dq, dk, dv, q, k, q_weight, k_weight, *(out or ()))
     device, dtype, code, B, N, pos, pos_batch, weights = _rotary_args(
         plan, first, positions, dq is not None or dk is not None, norm_eps is not None, q_weight, k_weight, 2, what)
     norm, d = norm_eps is not None, plan.d
@@ -499,6 +519,8 @@ def gated_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, gate: Optio
         with there:
             return gated_norm(x, y, gate=gate, alpha=alpha, post=post, pre=pre, scale=scale, shift=shift, out=out,
                               branch_dtype=branch_dtype)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(what, x, y, gate, scale, shift, *_of_norms(post, pre), *(out or ()))
     device = _cuda_device(x, what)
     if x.dim() != 3:
         raise BsaError(ERR_SHAPE, f"gated_norm: x has {x.dim()} dimensions, expected 3")
@@ -552,6 +574,8 @@ def gated_norm_backward(dh: Optional[torch.Tensor], dz: Optional[torch.Tensor], 
         with there:
             return gated_norm_backward(dh, dz, h, y, gate=gate, alpha=alpha, post=post, pre=pre, scale=scale,
                                        shift=shift, out=out, ws=ws)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(what, dh, dz, h, y, gate, scale, shift, *_of_norms(post, pre), *(out or ()))
     device = _cuda_device(first, what)
     if first.dim() != 3:
         raise BsaError(ERR_SHAPE, f"{what}: {first.dim()} dimensions, expected 3")

@@ -6,7 +6,7 @@ As in ``binding`` there is no fallback, and the helpers read the device error wo
 false: a loop of calls, or one captured into a graph, passes check=False and a workspace, and looks at it with
 ``cache_check`` when it likes. As in ``block_binding`` they run on the tensors' device and on ``stream`` (that device's
 current stream by default), record nothing for autograd, and refuse a tensor that requires a gradient while gradients
-are recorded.
+are recorded, or carries a tangent.
 """
 from __future__ import annotations
 
@@ -15,11 +15,12 @@ import struct
 from typing import NamedTuple, Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import binding
 from .binding import BF16, ERR_DTYPE, ERR_INVALID_ARG, ERR_SHAPE, BsaError, _check, _ptr, _stream
 from .block_binding import _current_stream as _block_current_stream
-from .block_binding import _cuda_device, _elsewhere, _view
+from .block_binding import _cuda_device, _elsewhere, _no_tangents, _view
 
 CACHE_BF16 = 0
 CACHE_E4M3 = 1
@@ -245,6 +246,8 @@ def cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     if stream is not None and (there := _elsewhere(stream, k, what)):
         with there:
             return cache_write(cache, k, v, table, kv_lens, cu, ws=ws, check=check)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(what, k, v, *cache[:2])
     desc, device, heads, d = _cache_args(cache, what)
     pages, B = _table_args(table, device, what)
     shape = (k.shape[0], heads, d)
@@ -265,6 +268,8 @@ def cache_read(cache: KvCache, table: torch.Tensor, cu: torch.Tensor, tokens: Op
     if stream is not None and (there := _elsewhere(stream, cache.k, what)):
         with there:
             return cache_read(cache, table, cu, tokens, out=out, ws=ws, check=check)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(what, *cache[:2], *(out or ()))
     desc, device, heads, d = _cache_args(cache, what)
     pages, B = _table_args(table, device, what)
     if out is None:
@@ -290,6 +295,8 @@ def cache_attention(q: torch.Tensor, cache: KvCache, table: torch.Tensor, kv_len
     if stream is not None and (there := _elsewhere(stream, q, what)):
         with there:
             return cache_attention(q, cache, table, kv_lens, scale, out=out, lse=lse, ws=ws, check=check)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(what, q, *cache[:2], out, lse)
     desc, device, heads, d = _cache_args(cache, what)
     pages, B = _table_args(table, device, what)
     if q.dim() != 3:
@@ -319,6 +326,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     if stream is not None and (there := _elsewhere(stream, q, what)):
         with there:
             return prompt_attention(q, k, v, cu_q, cu_k, causal=causal, scale=scale, out=out, lse=lse, ws=ws, check=check)
+    if _forward_ad._current_level >= 0:
+        _no_tangents(what, q, k, v, out, lse)
     device = _cuda_device(q, what)
     if q.dim() != 3 or k.dim() != 3:
         raise BsaError(ERR_SHAPE, f"{what}: q and k have {q.dim()} and {k.dim()} dimensions, expected 3")

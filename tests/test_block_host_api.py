@@ -632,3 +632,34 @@ def test_gradients_that_would_vanish_are_refused(monkeypatch):
             assert e.value.code == bb.ERR_INVALID_ARG, name
             with torch.no_grad(), pytest.raises(Reached):
                 fn(**wanted)
+
+
+def test_tangents_are_refused(monkeypatch):
+    """forward-mode differentiation: a tensor that carries a tangent, each operand in turn"""
+    monkeypatch.setattr(ob, "_cuda_device", lambda t, what: t.device)
+    monkeypatch.setattr(ob, "_run", lambda *args: None)
+    heads, rows, mod, w64, plan = torch.zeros(1, 4, 2, 64), torch.zeros(1, 4, 64), torch.zeros(1, 64), torch.ones(64), _plan()
+    pos, dy = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(1, 2, 4, 64)
+    turn = dict(positions=pos, norm_eps=1e-6, q_weight=w64, k_weight=w64)
+
+    def outs(fn, *args):
+        return lambda out0, out1, norm_w=w64, **t: fn(*args, **t, out=(out0, out1), pre=ob.NormSpec("rms", norm_w))
+
+    calls = [
+        (lambda out0, **t: pkg.rotary(plan, out=(out0, None, None), **t), dict(turn, q=heads, k=heads, v=heads, out0=dy)),
+        (lambda out0, **t: pkg.rotary_backward(plan, out=(out0, None, None), **t),
+         dict(turn, dq=dy, dk=dy, dv=dy, q=heads, k=heads, out0=heads)),
+        (outs(pkg.gated_norm), dict(x=rows, y=rows, gate=mod, scale=mod, shift=mod, norm_w=w64, out0=rows, out1=rows)),
+        (outs(pkg.gated_norm_backward),
+         dict(dh=rows, dz=rows, h=rows, y=rows, gate=mod, scale=mod, shift=mod, norm_w=w64, out0=rows, out1=rows)),
+    ]
+    ad = torch.autograd.forward_ad
+    with ad.dual_level():
+        for fn, tensors in calls:
+            fn(**tensors)
+            for name, t in tensors.items():
+                if not isinstance(t, torch.Tensor) or not t.is_floating_point():
+                    continue
+                with pytest.raises(bb.BsaError, match="tangent") as e:
+                    fn(**dict(tensors, **{name: ad.make_dual(t.clone(), torch.ones_like(t))}))
+                assert e.value.code == bb.ERR_INVALID_ARG, name

@@ -364,3 +364,44 @@ def test_helpers_refuse_gradients_of_caches_and_sums(monkeypatch):
     refused(bb.ERR_INVALID_ARG, pkg.cache_write, learned, host(2, 4, 64), host(2, 4, 64), t, n, ws=ws, check=False)
     with torch.no_grad(), pytest.raises(AssertionError, match="library was called"):
         pkg.cache_attention(host(2, 8, 64), learned, t, n, lse=lse, ws=ws, check=False)
+
+
+def test_helpers_refuse_tangents(monkeypatch):
+    """each operand in turn; what carries none passes, and so does everything in a torch.autograd.Function's forward"""
+    monkeypatch.setattr(cb, "_cuda_device", lambda t, what: t.device)
+    reached = []
+    monkeypatch.setattr(cb, "_call", lambda what, *args: reached.append(what))
+    cache, q8 = pkg.kv_cache(3, 16, 4, 64, "bf16", "cpu"), pkg.kv_cache(3, 16, 4, 64, "e4m3", "cpu")
+    t, n, cu, ws = host(2, 3, dtype=torch.int32), host(2, dtype=torch.int32), host(3, dtype=torch.int32), host(1 << 14, dtype=torch.uint8)
+    q, kv = host(2, 8, 64), host(2, 4, 64)
+    more = dict(ws=ws, check=False)
+    calls = [
+        (lambda k, v, ck, cv: pkg.cache_write(cb.KvCache(ck, cv), k, v, t, n, **more), dict(k=kv, v=kv, ck=cache.k, cv=cache.v)),
+        (lambda ck, cv, ok, ov: pkg.cache_read(cb.KvCache(ck, cv), t, cu, out=(ok, ov), **more), dict(ck=cache.k, cv=cache.v, ok=kv, ov=kv)),
+        (lambda q, ck, cv, out, lse: pkg.cache_attention(q, cb.KvCache(ck, cv), t, n, out=out, lse=lse, **more),
+         dict(q=q, ck=cache.k, cv=cache.v, out=q, lse=host(2, 8, dtype=torch.float32))),
+        (lambda q, k, v, out, lse: pkg.prompt_attention(q, k, v, cu, out=out, lse=lse, **more),
+         dict(q=q, k=kv, v=kv, out=q, lse=host(8, 2, dtype=torch.float32))),
+    ]
+    ad = torch.autograd.forward_ad
+    for fn, tensors in calls:
+        with ad.dual_level():
+            fn(**tensors)
+            for name, x in tensors.items():
+                before = len(reached)
+                refused(bb.ERR_INVALID_ARG, fn, **dict(tensors, **{name: ad.make_dual(x.clone(), torch.ones_like(x))}))
+                assert len(reached) == before
+    with ad.dual_level():
+        pkg.cache_write(q8, kv, kv, t, n, **more)
+
+        class Wrapped(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x):
+                return pkg.prompt_attention(x, kv, kv, cu, lse=host(8, 2, dtype=torch.float32), **more)[0]
+
+            @staticmethod
+            def jvp(ctx, dx):
+                return dx
+
+        out = Wrapped.apply(ad.make_dual(q.clone(), torch.ones_like(q)))
+        assert (ad.unpack_dual(out).tangent == 1).all()
