@@ -135,7 +135,7 @@ __device__ __forceinline__ int item_steps(const Seqs &s, const Seq &q, int t0)
 struct PlanArgs {
     Seqs s;
     int ctas;
-    long long max_items, max_entries;
+    long long max_items;
     PlanHeader *hdr;
     int32_t *rank;         // [B] sequences, longest first
     int32_t *item0;        // [B + 1] items of the ranks before
@@ -1338,7 +1338,6 @@ struct JoinArgs {
     const Split *splits;
     const float *part_o;
     const float2 *part_stats;
-    uint32_t *err;
 };
 
 // A warp per row, or, where there are no more rows than CTAs, a CTA: its warps take a share of the
@@ -1457,7 +1456,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinArgs a)
 
 struct Layout {
     size_t hdr, rank, item0, step0, item_step0, first, entries, splits, stats, part, total;
-    int64_t max_items, max_entries;
+    int64_t max_items;
 };
 
 int tokens_per_tile(int H, int Hk) { return kTileM / (H / Hk); }
@@ -1467,7 +1466,7 @@ Layout layout_of(int T, int B, int H, int Hk, int d)
     Layout l;
     l.max_items = T / tokens_per_tile(H, Hk) + static_cast<int64_t>(B);
     const int64_t cut_items = l.max_items * Hk < kMaxCutItems ? l.max_items * Hk : kMaxCutItems;
-    l.max_entries = cut_items + kMaxSlots;
+    const int64_t max_entries = cut_items + kMaxSlots;  // an item has an entry in each CTA that it is part of: one more per cut
     size_t at = kCacheScratch;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -1480,7 +1479,7 @@ Layout layout_of(int T, int B, int H, int Hk, int d)
     l.step0 = take(sizeof(long long) * static_cast<size_t>(B));
     l.item_step0 = take(sizeof(int32_t) * static_cast<size_t>(cut_items));
     l.first = take(sizeof(int32_t) * (kMaxSlots / 2 + 1));
-    l.entries = take(sizeof(Entry) * static_cast<size_t>(l.max_entries));
+    l.entries = take(sizeof(Entry) * static_cast<size_t>(max_entries));
     l.splits = take(sizeof(Split) * (kMaxSlots / 2));
     l.stats = take(sizeof(float2) * kTileM * kMaxSlots);
     l.part = take(sizeof(float) * kTileM * static_cast<size_t>(d) * kMaxSlots);
@@ -1550,7 +1549,6 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
     pa.s = seqs;
     pa.ctas = sms;
     pa.max_items = l.max_items;
-    pa.max_entries = l.max_entries;
     pa.hdr = hdr;
     pa.rank = reinterpret_cast<int32_t *>(a.ws + l.rank);
     pa.item0 = reinterpret_cast<int32_t *>(a.ws + l.item0);
@@ -1591,7 +1589,7 @@ bsa_status launch(const PromptArgs &a, cudaStream_t st)
         if (cudaGetLastError() != cudaSuccess) return BSA_ERR_CUDA;
     }
     if (a.Tk <= kShortKeys) return BSA_OK;  // nothing is cut
-    const JoinArgs ja{seqs, a.o, a.lse, hdr, pa.splits, p.part_o, p.part_stats, err};
+    const JoinArgs ja{seqs, a.o, a.lse, hdr, pa.splits, p.part_o, p.part_stats};
     if (!pdl_launch(join_kernel<D>, dim3(static_cast<unsigned>(4 * sms)), 256, 0, st, ja)) return BSA_ERR_CUDA;
     return BSA_OK;
 }
