@@ -24,10 +24,14 @@
 //     rounds of items of all CTAs, go together, longest items first, so that the work ends with short ones. Where that
 //     would leave CTAs idle (few items, or one far above a CTA's average), all steps in a row are cut evenly over the
 //     CTAs instead, and a last launch joins the parts of an item that a cut runs through, in order.
-//   * What bounds it: shared memory. A 128 x 128 step moves 64 KB of K and V in, 64 KB of Q and K and 32 KB of V to the
-//     tensor cores, 1250 cycles at 128 bytes a cycle, beside 1024 cycles of products; measured 0.74 us, about 1490, with
-//     its share of the tiles' ends. 32768 causal tokens, 16 heads of 128: 2.57 ms, 1710 TFLOP/s, 90% of the library's
-//     rate; six packed sequences of 513 to 4224 tokens, 24 heads over 8: 275 us, 1220 TFLOP/s.
+//   * What bounds it: no unit by itself. Of a 128 x 128 step's 1550 cycles (8192 causal tokens, 16 heads of 128, the tiles'
+//     ends among them) the tensor cores work 66%; the path from shared memory to them, 64 KB of Q and K and 32 KB of V, is
+//     taken 49% (768 cycles, as counted), beside 64 KB of K and V that come in. If both shared 128 bytes a cycle they
+//     would take 1250 cycles; the counters do not show that. The rest is the chain of a step and the ends of tiles.
+//     32768 causal tokens, 16 heads of 128: 2.58 to 2.62 ms in a few calls after a pause (1710 to 1680 TFLOP/s, 89% of the
+//     library's rate), 2.75 to 3.1 ms in long loops of calls (1600 to 1430: the power cap); 8192: 198 us (1390). Six packed
+//     sequences of 513 to 4224 tokens, 24 heads over 8: 274 to 295 us (1220 to 1140). 16384 tokens, 16 heads of 64: 490 us
+//     (1120), 1070 cycles a step, of which 512 are products.
 //   * 0 * NaN: a masked weight of zero still multiplies V. In steps where a mask ends, the softmax warps look through V before
 //     they hand P over, a quarter of the rows each: rows behind the sequence are zeroed in shared memory, and other
 //     values that are not finite too; these are then added in the epilogue to the rows that see them. Steps that every row
