@@ -34,6 +34,8 @@
  *     does not depend on lengths or on the cache.
  *   - A result depends on the call's inputs and the device alone: sums run in an order fixed by the
  *     lengths, without atomics on values.
+ *   - NaN and infinities among what a query sees go where the formulas take them, but for an infinite
+ *     value whose weight lies below fp32's range: NaN, as zero times infinity, or the infinity.
  */
 #ifndef BSA_CACHE_H_
 #define BSA_CACHE_H_
